@@ -42,6 +42,17 @@ FP8G_ACT_RELU = 1
 FP8G_ACT_GELU = 2
 FP8G_MAX_EXPERTS = 64
 FP8G_QUANT_FUSED = 1
+FP8G_MAX_ROUTED_EXPERTS = 256
+FP8G_MAX_TOP_K = 16
+FP8G_MAX_ROUTED_TOKENS = 262144
+FP8G_MOE_MAX_TOKENS = 512
+FP8G_SCORE_SOFTMAX = 0
+FP8G_SCORE_SOFTMAX_TOPK = 1
+FP8G_SCORE_SIGMOID = 2
+FP8G_SCORE_SIGMOID_NORM = 3
+FP8G_GATE_SILU = 0
+FP8G_GATE_GELU = 1
+FP8G_GATE_RELU = 2
 
 # Every symbol include/fp8gemm.h declares.
 EXPORTS = (
@@ -55,6 +66,7 @@ EXPORTS = (
     "fp8g_kernel_timing_begin", "fp8g_kernel_timing_end",
     "fp8_gemm_status", "fp8g_status_string",
     "fp8g_set_wait_timeout_ms", "fp8g_shutdown", "fp8g_version",
+    "fp8g_packed_scale_bytes", "fp8g_pack_scales", "fp8g_moe_route", "fp8_moe_layer",
 )
 
 
@@ -146,6 +158,16 @@ def load():
         lib.fp8_grouped_gemm_fmt.restype = st
         lib.fp8_grouped_gemm_fmt.argtypes = [P, P, P, P, P, ctypes.c_int, i32, i32, P, i32, i64,
                                              i64, i64, P, P, P]
+        lib.fp8g_packed_scale_bytes.restype = i64
+        lib.fp8g_packed_scale_bytes.argtypes = [i64, i64, i64]
+        lib.fp8g_pack_scales.restype = st
+        lib.fp8g_pack_scales.argtypes = [P, i64, i64, i64, P, P]
+        lib.fp8g_moe_route.restype = st
+        lib.fp8g_moe_route.argtypes = [P, i32, i64, i64, i32, i32, i32, ctypes.c_float, P, P, P, P,
+                                       P, P]
+        lib.fp8_moe_layer.restype = st
+        lib.fp8_moe_layer.argtypes = [P, i32, P, P, P, P, P, P, P, ctypes.c_int, i32, i32, i64,
+                                      i32, i32, i64, i64, P]
         lib.fp8_gemm_status.restype = st
         lib.fp8_gemm_status.argtypes = [P, P]
         lib.fp8g_status_string.restype = ctypes.c_char_p
@@ -360,6 +382,30 @@ def fp8g_quantize_rows(x, in_dtype: int, x_rows: int, cols: int, rows, n_rows: i
                                      _stream(stream)), "fp8g_quantize_rows")
 
 
+def fp8g_packed_scale_bytes(matrices: int, rows: int, K: int) -> int:
+    return int(load().fp8g_packed_scale_bytes(matrices, rows, K))
+
+
+def fp8g_pack_scales(sf, matrices: int, rows: int, K: int, packed, stream=None):
+    _check(load().fp8g_pack_scales(_ptr(sf), matrices, rows, K, _ptr(packed), _stream(stream)),
+           "fp8g_pack_scales")
+
+
+def fp8g_moe_route(logits, in_dtype: int, ld: int, T: int, E: int, k: int, score: int,
+                   scale: float, ids, weights, counts=None, rows=None, slots=None, stream=None):
+    _check(load().fp8g_moe_route(_ptr(logits), int(in_dtype), ld, T, int(E), int(k), int(score),
+                                 float(scale), _ptr(ids), _ptr(weights), _ptr(counts), _ptr(rows),
+                                 _ptr(slots), _stream(stream)), "fp8g_moe_route")
+
+
+def fp8_moe_layer(x, x_dtype: int, ids, weights, W13, sf13, W2, sf2, out, out_dtype: int,
+                  w_fmt: int, gate: int, T: int, k: int, E: int, H: int, F: int, stream=None):
+    _check(load().fp8_moe_layer(_ptr(x), int(x_dtype), _ptr(ids), _ptr(weights), _ptr(W13),
+                                _ptr(sf13), _ptr(W2), _ptr(sf2), _ptr(out), int(out_dtype),
+                                int(w_fmt), int(gate), T, int(k), int(E), H, F, _stream(stream)),
+           "fp8_moe_layer")
+
+
 def fp8g_kernel_timing_begin(n: int):
     _check(load().fp8g_kernel_timing_begin(int(n)), "fp8g_kernel_timing_begin")
 
@@ -439,3 +485,70 @@ def gemm(A, B, sa, sb, out: str = "bf16", block: bool = True, stream=None):
     else:
         fp8_gemm(A, B, sa, sb, C, o, M, N, K, stream)
     return C
+
+
+def pack_scales(sf, stream=None):
+    """Block scales fp32 [rows, K/32] or [matrices, rows, K/32] -> the packed
+    uint8 [(matrices,) ceil(K/128), ceil(rows/128), 512] that moe_layer and
+    gemm_lora take (once per weight)."""
+    import torch
+    assert sf.is_cuda and sf.dtype == torch.float32 and sf.dim() in (2, 3)
+    sf = sf.contiguous()
+    rows, kb = sf.shape[-2:]
+    lead = tuple(sf.shape[:-2])
+    out = torch.empty(lead + (-(-kb // 4), -(-rows // 128), 512), dtype=torch.uint8,
+                      device=sf.device)
+    fp8g_pack_scales(sf, lead[0] if lead else 1, rows, 32 * kb, out, stream)
+    return out
+
+
+def moe_route(logits, k: int, score: int = FP8G_SCORE_SOFTMAX_TOPK, scale: float = 1.0,
+              ordered: bool = False, stream=None):
+    """fp32 or bf16 logits [T, E] -> (ids int32 [T, k], weights fp32 [T, k]), and
+    with `ordered` also (counts [E], rows [T k], slots [T k]), the row order of the
+    grouped GEMM (its counts, rows and c_row_of)."""
+    import torch
+    assert logits.is_cuda and logits.dim() == 2
+    assert logits.dtype in (torch.float32, torch.bfloat16)
+    T, E = logits.shape
+    if E > 1 and logits.stride(1) != 1 or T > 1 and logits.stride(0) < E:
+        logits = logits.contiguous()
+    ld = logits.stride(0) if T > 1 else E
+    dev = logits.device
+    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    w = torch.empty((T, k), dtype=torch.float32, device=dev)
+    order = ()
+    if ordered:
+        order = (torch.empty((E,), dtype=torch.int32, device=dev),
+                 torch.empty((T * k,), dtype=torch.int32, device=dev),
+                 torch.empty((T * k,), dtype=torch.int32, device=dev))
+    dt = FP8G_IN_BF16 if logits.dtype == torch.bfloat16 else FP8G_IN_F32
+    fp8g_moe_route(logits, dt, ld, T, E, k, score, scale, ids, w, *order, stream=stream)
+    return (ids, w) + order
+
+
+def moe_layer(x, ids, weights, W13, sf13, W2, sf2, w_fmt: int = FP8G_E4M3,
+              gate: int = FP8G_GATE_SILU, out: str = "bf16", stream=None):
+    """Mixture-of-experts layer of a few tokens: x fp32 or bf16 [T, H], ids and
+    weights [T, k] from moe_route, W13 [E, 2F, H] and W2 [E, H, F] codes of w_fmt,
+    sf13 / sf2 from pack_scales (sf13 of W13's scales viewed as [2E, F, H/32]).
+    Allocates the output [T, H]."""
+    import torch
+    assert x.is_cuda and x.dim() == 2 and x.dtype in (torch.float32, torch.bfloat16)
+    assert ids.dtype == torch.int32 and weights.dtype == torch.float32
+    assert ids.shape == weights.shape and ids.dim() == 2 and ids.shape[0] == x.shape[0]
+    assert W13.dim() == 3 and W2.dim() == 3 and W13.is_contiguous() and W2.is_contiguous()
+    T, H = x.shape
+    k = ids.shape[1]
+    E, F = W13.shape[0], W13.shape[1] // 2
+    assert W13.shape == (E, 2 * F, packed_cols(H, w_fmt))
+    assert W2.shape == (E, H, packed_cols(F, w_fmt))
+    assert sf13.numel() == fp8g_packed_scale_bytes(2 * E, F, H)
+    assert sf2.numel() == fp8g_packed_scale_bytes(E, H, F)
+    x, ids, weights = x.contiguous(), ids.contiguous(), weights.contiguous()
+    o = torch.empty((T, H), dtype=torch.bfloat16 if out == "bf16" else torch.float32,
+                    device=x.device)
+    fp8_moe_layer(x, FP8G_IN_BF16 if x.dtype == torch.bfloat16 else FP8G_IN_F32, ids, weights, W13,
+                  sf13, W2, sf2, o, FP8G_OUT_BF16 if out == "bf16" else FP8G_OUT_F32, w_fmt, gate,
+                  T, k, E, H, F, stream)
+    return o

@@ -648,6 +648,34 @@ fp8g_status device_ready() {
     return device_info(di);
 }
 
+fp8g_status host_device(HostDevice &d) {
+    DevInfo di;
+    const fp8g_status st = device_info(di);
+    if (st != FP8G_OK) return st;
+    d.dev = di.dev;
+    d.num_sms = di.num_sms;
+    d.status = di.status;
+    d.timeout_ns = timeout_ns();
+    return FP8G_OK;
+}
+
+fp8g_status host_pool(int dev, cudaMemPool_t &pool) { return scale_pool(dev, pool); }
+
+fp8g_status host_operand_map(const void *ptr, int fmt, int rank, const uint64_t *dims,
+                             const uint32_t *box, int dev, CUtensorMap &out) {
+    return tmap_operand(ptr, fmt, rank, dims, box, dev, out);
+}
+
+fp8g_status host_bf16_map(const void *ptr, int rank, const uint64_t *dims, const uint32_t *box,
+                          int dev, CUtensorMap &out) {
+    return tmap_encode(ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 16, rank, dims, box,
+                       CU_TENSOR_MAP_SWIZZLE_128B, dev, out);
+}
+
+uint32_t host_mma_type(int fmt) { return mma_type(fmt); }
+
+int32_t host_gap8(int fmt) { return gap8(fmt); }
+
 }  // namespace fp8g
 
 using namespace fp8g;

@@ -147,13 +147,14 @@ fp8g_status device_ready();
 // Launch with programmatic stream serialization: the kernel may begin while
 // the previous one on the stream finishes; it calls grid_dep_wait before any
 // global memory access.
+// (_smem: with `smem` bytes of dynamic shared memory.)
 template <typename... KArgs, typename... Args>
-cudaError_t launch_programmatic(void (*kern)(KArgs...), dim3 grid, dim3 block, cudaStream_t s,
-                                Args... args) {
+cudaError_t launch_programmatic_smem(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                     cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
-    cfg.dynamicSmemBytes = 0;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -161,6 +162,11 @@ cudaError_t launch_programmatic(void (*kern)(KArgs...), dim3 grid, dim3 block, c
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+template <typename... KArgs, typename... Args>
+cudaError_t launch_programmatic(void (*kern)(KArgs...), dim3 grid, dim3 block, cudaStream_t s,
+                                Args... args) {
+    return launch_programmatic_smem(kern, grid, block, 0, s, static_cast<KArgs>(args)...);
 }
 
 struct PackArgs {
@@ -201,5 +207,33 @@ cudaError_t launch_quantize_rows(const void *x, int in_bf16, int64_t x_rows, int
                                  const int32_t *rows, int64_t n_rows, int32_t block, int fmt,
                                  uint8_t *q, float *scales, unsigned int *status, int num_sms,
                                  cudaStream_t s);
+
+// api.cu: what the entry points of other translation units need of the
+// current device, the library pool and the tensor-map cache.
+struct HostDevice {
+    int dev, num_sms;
+    unsigned int *status;
+    uint64_t timeout_ns;
+};
+fp8g_status host_device(HostDevice &d);
+fp8g_status host_pool(int dev, cudaMemPool_t &pool);
+// Operand tile map (128-byte swizzle) of format fmt over dims / box elements,
+// innermost first.
+fp8g_status host_operand_map(const void *ptr, int fmt, int rank, const uint64_t *dims,
+                             const uint32_t *box, int dev, CUtensorMap &out);
+// The same for bf16 elements (64 of them are one swizzle span).
+fp8g_status host_bf16_map(const void *ptr, int rank, const uint64_t *dims, const uint32_t *box,
+                          int dev, CUtensorMap &out);
+uint32_t host_mma_type(int fmt);  // the MMA instruction descriptor's type field
+int32_t host_gap8(int fmt);       // eighths of a tile that a packed load does not deliver
+
+// route.cu: logits [T, E] (rows ld elements apart) -> ids, weights [T, k];
+// rows != null: counts [E], rows, slots [T k] too, with hist a temporary of
+// route_blocks(T) * E int32 (unused when route_blocks(T) is 1).
+int route_blocks(int64_t T);
+cudaError_t launch_moe_route(const void *logits, int bf16, int64_t ld, int32_t T, int32_t E, int32_t k,
+                             int32_t score, float scale, int32_t *ids, float *weights,
+                             int32_t *counts, int32_t *rows, int32_t *slots, int32_t *hist,
+                             cudaStream_t s);
 
 }  // namespace fp8g

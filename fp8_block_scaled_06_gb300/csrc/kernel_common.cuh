@@ -32,15 +32,18 @@ __device__ __forceinline__ uint32_t ue8m0_code(uint32_t bits, bool &bad) {
     return ex;
 }
 
-__device__ __forceinline__ void record_error(const GemmParams &p, unsigned code, unsigned detail) {
+// (P: a parameter struct with `status` and `timeout_ns`, as GemmParams has.)
+template <typename P>
+__device__ __forceinline__ void record_error(const P &p, unsigned code, unsigned detail) {
     if (atomicCAS(&p.status[0], 0u, code) == 0u) atomicExch(&p.status[1], detail);
 }
 
 // Bounded wait on an mbarrier phase.  Returns false when this CTA is aborting
 // (another role timed out) or when this wait itself exceeded the limit.
 // sleep_ns > 0 backs off between polls (for roles that wait a whole tile).
+template <typename P>
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                         const GemmParams &p, unsigned detail,
+                                         const P &p, unsigned detail,
                                          uint32_t sleep_ns = 0) {
     if (ptx::mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = ptx::globaltimer();
@@ -75,8 +78,9 @@ __device__ __forceinline__ bool wait_bar_landed(uint32_t bar, uint32_t parity,
 
 // Warp-uniform bounded wait: lane 0 waits, the outcome is broadcast, and the
 // warp re-converges before any .sync.aligned tcgen05 instruction follows.
+template <typename P>
 __device__ __forceinline__ bool wait_bar_warp(uint32_t bar, uint32_t parity,
-                                              volatile int *abort_flag, const GemmParams &p,
+                                              volatile int *abort_flag, const P &p,
                                               unsigned detail, uint32_t sleep_ns = 0) {
     int ok = 0;
     if ((threadIdx.x & 31) == 0) ok = wait_bar(bar, parity, abort_flag, p, detail, sleep_ns) ? 1 : 0;

@@ -1,0 +1,66 @@
+// The streaming GEMM kernel (stream.cu): few tokens against block-scaled
+// weights that are read once.  Declarations shared by its users.
+#pragma once
+#include "internal.h"
+
+namespace fp8g {
+
+// One group: up to nb token rows against one weight matrix.
+struct StreamGroup {
+    int32_t mat;    // weight matrix (expert)
+    int32_t row0;   // first token row of the operand
+    int32_t n;      // token rows
+    int32_t unit0;  // work units of the groups before it
+};
+
+constexpr int kStreamMaxGroups = 352;
+constexpr int kStreamMaxTokens = 128;  // token rows of a group
+constexpr int kStreamMinUnits = 4;     // work units a CTA takes at least
+
+enum StreamEpi : int {
+    kStreamGated = 0,  // act(gate) * up, quantised to E4M3 with 1x32 scales
+    kStreamRows = 1,   // fp32 rows
+    kStreamOut = 2,    // output rows with bias; low-rank steps
+};
+
+struct StreamParams {
+    int32_t mt;      // weight-row tiles per group
+    int32_t ks;      // 128-wide K steps
+    int32_t rows;    // rows of a weight matrix (gated: of each half)
+    int32_t n_rt;    // 128-row tiles of packed scales per matrix
+    int32_t nb;      // token columns per accumulator (a multiple of 16)
+    int32_t nacc;    // accumulators (2: a tile's epilogue overlaps the next tile)
+    int32_t stages, stage_bytes, x_bytes;  // shared-memory ring
+    uint32_t w_fmt;  // weight format as MMA instruction-descriptor bits
+    int32_t gap8;    // eighths of a weight tile a packed load does not deliver
+    const uint8_t *sfw;      // packed weight scales [matrix][ks][n_rt][512]
+    const uint8_t *sfx;      // packed token scales [group][ks][512]
+    const int32_t *head;     // [0] groups, [1] work units
+    const StreamGroup *groups;
+    int32_t *tile_cnt;       // [group][mt] units done of split tiles, zero at the start
+    float *part;             // partial tiles [2 grid][2][nb][128]
+    unsigned int *status;
+    uint64_t timeout_ns;
+    // gated
+    int32_t gate;
+    uint8_t *hq;             // codes [rows of tokens][rows]
+    uint8_t *hsf;            // packed scales [group][mt][512]
+    // rows
+    float *y;                // [rows of tokens][rows]
+    // out
+    void *c;                 // [tokens][rows]
+    int32_t out_f32;
+    const float *bias;
+    int32_t rank, kr, slot_cap;      // low-rank: rank, 64-wide steps per slot, slots per group
+    const int32_t *slot_cnt;         // [group]
+    const int32_t *slot_adapter;     // [group][slot_cap]
+};
+
+// Ring and accumulator sizes for nb token columns; lora: V's two halves share
+// the token region of a stage.
+void stream_sizes(StreamParams &p, int nb, bool lora);
+size_t stream_part_bytes(const StreamParams &p, int grid);
+cudaError_t launch_stream(int epi, const CUtensorMap &w, const CUtensorMap &x, const CUtensorMap &lb,
+                          const CUtensorMap &v, const StreamParams &p, int grid, cudaStream_t s);
+
+}  // namespace fp8g

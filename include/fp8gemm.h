@@ -481,6 +481,94 @@ FP8G_API fp8g_status fp8_grouped_gemm_quant(const void *X, int32_t x_dtype, int6
                                            cudaStream_t stream);
 
 /*
+ * Weight scales laid out once, for the entry points that take packed scales
+ * (fp8_moe_layer, fp8_gemm_lora; the source pages have no counterpart).
+ * sf: device fp32 [matrices, rows, K/32], positive powers of two (others record
+ * FP8G_ERR_SCALE_FORMAT in the status word, as fp8_gemm_blockscaled does;
+ * NaN stays NaN).  packed: uint8 [matrices, ceil(K/128), ceil(rows/128), 512]:
+ * in the 512 bytes of K group g and row tile t of a matrix, byte 16 d + 4 w + j
+ * is the 8-bit exponent code (value 2^(code - 127)) of row 128 t + 32 w + d, K
+ * block 4 g + j; rows and blocks past the matrix hold 127.  K % 32 == 0 and at
+ * most 65535 matrices and row tiles, else FP8G_ERR_UNSUPPORTED_SHAPE; sf and
+ * packed 16-byte aligned.  fp8g_packed_scale_bytes gives the size (0 for sizes
+ * out of range).
+ */
+FP8G_API int64_t fp8g_packed_scale_bytes(int64_t matrices, int64_t rows, int64_t K);
+FP8G_API fp8g_status fp8g_pack_scales(const float *sf, int64_t matrices, int64_t rows, int64_t K,
+                                      uint8_t *packed, cudaStream_t stream);
+
+/* Limits of the router and of fp8_moe_layer. */
+#define FP8G_MAX_ROUTED_EXPERTS 256
+#define FP8G_MAX_TOP_K 16
+#define FP8G_MAX_ROUTED_TOKENS 262144
+#define FP8G_MOE_MAX_TOKENS 512
+
+/*
+ * Weight of a chosen expert from its logit: softmax over every expert of the
+ * token, softmax over the chosen ones, the sigmoid, the sigmoid divided by the
+ * sum of the chosen ones' sigmoids.
+ */
+typedef enum {
+    FP8G_SCORE_SOFTMAX = 0,
+    FP8G_SCORE_SOFTMAX_TOPK = 1,
+    FP8G_SCORE_SIGMOID = 2,
+    FP8G_SCORE_SIGMOID_NORM = 3
+} fp8g_score;
+
+/*
+ * MoE router [JAX-BW MoE paragraph: tokens routed to experts; the pages print
+ * no router, the reading taken is this].  Row t of logits (fp32 or bf16 per
+ * in_dtype, rows ld elements apart, ld >= E) chooses its k largest logits,
+ * largest first, equal ones by lower index; a logit that is NaN or -inf is
+ * never chosen.  ids int32 [T, k]: the chosen experts, -1 where fewer than k
+ * can be chosen; weights fp32 [T, k]: scale times the score (fp8g_score, in
+ * fp32; several +inf logits share the softmax equally), 0 for -1.
+ * counts, rows, slots (all or none): the order the grouped GEMM takes.
+ * counts int32 [E]; rows and slots int32 [T k]: the pairs (t, j) by expert,
+ * then by t k + j, rows = t (`rows` of fp8_grouped_gemm_quant) and slots =
+ * t k + j (`c_row_of` of the grouped GEMMs over a C of T k rows); entries past
+ * the sum of counts, which is T k unless some id is -1, are -1.  The order is
+ * the same in every run.  One kernel; with the order and more than 256 tokens
+ * two, and a temporary of 4 E ceil(T / 256) bytes from the library's pool.
+ * k <= E, else FP8G_ERR_INVALID_ARG; E <= FP8G_MAX_ROUTED_EXPERTS, k <=
+ * FP8G_MAX_TOP_K, T <= FP8G_MAX_ROUTED_TOKENS, else FP8G_ERR_UNSUPPORTED_SHAPE;
+ * T may be 0.  Pointers aligned to their elements.
+ */
+FP8G_API fp8g_status fp8g_moe_route(const void *logits, int32_t in_dtype, int64_t ld, int64_t T,
+                                    int32_t E, int32_t k, int32_t score, float scale, int32_t *ids,
+                                    float *weights, int32_t *counts, int32_t *rows, int32_t *slots,
+                                    cudaStream_t stream);
+
+/* Activation of the gate of fp8_moe_layer: g / (1 + exp(-g)), the erf GELU, ReLU. */
+typedef enum { FP8G_GATE_SILU = 0, FP8G_GATE_GELU = 1, FP8G_GATE_RELU = 2 } fp8g_gate;
+
+/*
+ * A whole mixture-of-experts feed-forward layer for a few tokens [JAX-BW MoE
+ * paragraph; its fine-grained (1x32) quantisation advice].  With Q the E4M3
+ * quantisation of fp8g_quantize (block 32) and e = ids[t, j]:
+ *   g = Q(x[t]) . W13[e][0..F)^T,  u = Q(x[t]) . W13[e][F..2F)^T   (fp32)
+ *   h = act(g) u                                                   (fp32)
+ *   out[t] = out( sum_j weights[t, j] ( Q(h) . W2[e]^T ) )         (fp32, j in order)
+ * x: fp32 or bf16 (x_dtype) [T, H], 16-byte aligned; ids int32 [T, k] (negative:
+ * skipped; >= E: skipped and recorded as FP8G_ERR_INVALID_ARG, detail t k + j),
+ * weights fp32 [T, k]: as fp8g_moe_route gives them.  W13 [E, 2F, H] (gate rows,
+ * then up rows) and W2 [E, H, F]: codes of format w_fmt (packed formats as in
+ * fp8g_format); sf13, sf2: their scales from fp8g_pack_scales, W13's as 2E
+ * matrices of F rows.  out [T, H] bf16 or fp32 (out_dtype), 16-byte aligned;
+ * a token without an expert gets zeros.  H % 32 == 0, F % 32 == 0 (packed
+ * formats 128), T <= FP8G_MOE_MAX_TOKENS, k <= FP8G_MAX_TOP_K, E <=
+ * FP8G_MAX_ROUTED_EXPERTS, else FP8G_ERR_UNSUPPORTED_SHAPE; T may be 0.  The
+ * weights of experts without tokens are not read.  For more tokens route with
+ * fp8g_moe_route and use the grouped GEMMs.  Results do not vary between runs.
+ * Four kernels and one temporary from the library's pool.
+ */
+FP8G_API fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t *ids,
+                                   const float *weights, const void *W13, const uint8_t *sf13,
+                                   const void *W2, const uint8_t *sf2, void *out, int out_dtype,
+                                   int32_t w_fmt, int32_t gate, int64_t T, int32_t k, int32_t E,
+                                   int64_t H, int64_t F, cudaStream_t stream);
+
+/*
  * Synchronises `stream`, then returns and clears the current device's status
  * word (FP8G_OK if no kernel recorded an error since the last call).
  * `detail` (nullable) receives a kernel-specific code for the first error
