@@ -46,6 +46,8 @@ FP8G_MAX_ROUTED_EXPERTS = 256
 FP8G_MAX_TOP_K = 16
 FP8G_MAX_ROUTED_TOKENS = 262144
 FP8G_MOE_MAX_TOKENS = 512
+FP8G_MAX_ADAPTERS = 1024
+FP8G_MAX_LORA_RANK = 256
 FP8G_SCORE_SOFTMAX = 0
 FP8G_SCORE_SOFTMAX_TOPK = 1
 FP8G_SCORE_SIGMOID = 2
@@ -67,6 +69,7 @@ EXPORTS = (
     "fp8_gemm_status", "fp8g_status_string",
     "fp8g_set_wait_timeout_ms", "fp8g_shutdown", "fp8g_version",
     "fp8g_packed_scale_bytes", "fp8g_pack_scales", "fp8g_moe_route", "fp8_moe_layer",
+    "fp8_gemm_lora",
 )
 
 
@@ -168,6 +171,9 @@ def load():
         lib.fp8_moe_layer.restype = st
         lib.fp8_moe_layer.argtypes = [P, i32, P, P, P, P, P, P, P, ctypes.c_int, i32, i32, i64,
                                       i32, i32, i64, i64, P]
+        lib.fp8_gemm_lora.restype = st
+        lib.fp8_gemm_lora.argtypes = [P, i32, P, P, i32, P, P, P, P, i32, i32, P, P, ctypes.c_int,
+                                      i64, i64, i64, P]
         lib.fp8_gemm_status.restype = st
         lib.fp8_gemm_status.argtypes = [P, P]
         lib.fp8g_status_string.restype = ctypes.c_char_p
@@ -406,6 +412,14 @@ def fp8_moe_layer(x, x_dtype: int, ids, weights, W13, sf13, W2, sf2, out, out_dt
            "fp8_moe_layer")
 
 
+def fp8_gemm_lora(x, x_dtype: int, W, sfw, w_fmt: int, lora_a, lora_b, alpha, adapter, L: int,
+                  r: int, bias, C, out: int, M: int, N: int, K: int, stream=None):
+    _check(load().fp8_gemm_lora(_ptr(x), int(x_dtype), _ptr(W), _ptr(sfw), int(w_fmt),
+                                _ptr(lora_a), _ptr(lora_b), _ptr(alpha), _ptr(adapter), int(L),
+                                int(r), _ptr(bias), _ptr(C), int(out), M, N, K, _stream(stream)),
+           "fp8_gemm_lora")
+
+
 def fp8g_kernel_timing_begin(n: int):
     _check(load().fp8g_kernel_timing_begin(int(n)), "fp8g_kernel_timing_begin")
 
@@ -552,3 +566,28 @@ def moe_layer(x, ids, weights, W13, sf13, W2, sf2, w_fmt: int = FP8G_E4M3,
                   sf13, W2, sf2, o, FP8G_OUT_BF16 if out == "bf16" else FP8G_OUT_F32, w_fmt, gate,
                   T, k, E, H, F, stream)
     return o
+
+
+def gemm_lora(x, W, sfw, lora_a, lora_b, alpha, adapter, bias=None, w_fmt: int = FP8G_E4M3,
+              out: str = "bf16", stream=None):
+    """Projection with low-rank adapters: x fp32 or bf16 [M, K], W codes [N, K] of
+    w_fmt, sfw from pack_scales, lora_a bf16 [L, r, K], lora_b bf16 [L, N, r],
+    alpha fp32 [L] or None, adapter int32 [M] (negative: none).  Allocates C [M, N]."""
+    import torch
+    assert x.is_cuda and x.dim() == 2 and x.dtype in (torch.float32, torch.bfloat16)
+    assert W.dim() == 2 and W.is_contiguous() and adapter.dtype == torch.int32
+    assert lora_a.dtype == torch.bfloat16 and lora_b.dtype == torch.bfloat16
+    M, K = x.shape
+    N = W.shape[0]
+    L, r = lora_a.shape[:2]
+    assert W.shape[1] == packed_cols(K, w_fmt) and adapter.shape == (M,)
+    assert lora_a.shape == (L, r, K) and lora_b.shape == (L, N, r)
+    assert sfw.numel() == fp8g_packed_scale_bytes(1, N, K)
+    x, adapter = x.contiguous(), adapter.contiguous()
+    lora_a, lora_b = lora_a.contiguous(), lora_b.contiguous()
+    C = torch.empty((M, N), dtype=torch.bfloat16 if out == "bf16" else torch.float32,
+                    device=x.device)
+    fp8_gemm_lora(x, FP8G_IN_BF16 if x.dtype == torch.bfloat16 else FP8G_IN_F32, W, sfw, w_fmt,
+                  lora_a, lora_b, alpha, adapter, L, r, bias, C,
+                  FP8G_OUT_BF16 if out == "bf16" else FP8G_OUT_F32, M, N, K, stream)
+    return C

@@ -527,6 +527,57 @@ fp8g_status run_gemm(int mode, const void *A, const void *B, const float *sa, co
     return (e == cudaSuccess && ef == cudaSuccess) ? FP8G_OK : FP8G_ERR_CUDA;
 }
 
+fp8g_status run_pair_packed(const void *A, const uint8_t *sfa, const void *B, const uint8_t *sfb,
+                            int b_fmt, const float *bias, void *C, int out, int64_t M, int64_t N,
+                            int64_t K, const PairLora *lora, cudaStream_t stream) {
+    DevInfo di;
+    fp8g_status st = device_info(di);
+    if (st != FP8G_OK) return st;
+    GemmParams p{};
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.num_kb = (int32_t)((K + kBK - 1) / kBK);
+    p.npm = (int32_t)((M + 255) / 256);
+    p.npn = (int32_t)((N + 255) / 256);
+    p.T = (int64_t)p.npm * p.npn;
+    p.split = 1;
+    p.kb_per_split = p.num_kb;
+    p.sfc = K / 32;
+    p.C = C;
+    p.c_rows = M;
+    p.status = di.status;
+    p.timeout_ns = timeout_ns();
+    p.ab_fmt = mma_type(b_fmt) << 10;
+    p.b_gap8 = gap8(b_fmt);
+    p.bias = bias;
+    p.st32 = aligned(C, 32) && (N * (out == FP8G_OUT_F32 ? 4 : 2)) % 32 == 0;
+    p.sfa_pk = sfa;
+    p.sfb_pk = sfb;
+    p.n_rtA = (int32_t)((M + kBM - 1) / kBM);
+    // (an odd count: the last tile's second chunk is another K group's, for
+    // columns past N)
+    p.n_rtB = (int32_t)((N + kBM - 1) / kBM);
+    GemmMaps maps;
+    const uint64_t dA[2] = {(uint64_t)K, (uint64_t)M}, dB[2] = {(uint64_t)K, (uint64_t)N};
+    const uint32_t box[2] = {(uint32_t)kBK, (uint32_t)kBM};
+    const uint64_t dSA[2] = {128u, (uint64_t)p.num_kb * (uint64_t)p.n_rtA};
+    const uint64_t dSB[2] = {128u, (uint64_t)p.num_kb * (uint64_t)p.n_rtB};
+    const uint32_t bSA[2] = {128u, 1u}, bSB[2] = {128u, 2u};
+    if ((st = tmap_operand(A, FP8G_E4M3, 2, dA, box, di.dev, maps.A)) != FP8G_OK ||
+        (st = tmap_operand(B, b_fmt, 2, dB, box, di.dev, maps.B)) != FP8G_OK ||
+        (st = tmap_encode(sfa, CU_TENSOR_MAP_DATA_TYPE_UINT32, 32, 2, dSA, bSA,
+                          CU_TENSOR_MAP_SWIZZLE_NONE, di.dev, maps.SA)) != FP8G_OK ||
+        (st = tmap_encode(sfb, CU_TENSOR_MAP_DATA_TYPE_UINT32, 32, 2, dSB, bSB,
+                          CU_TENSOR_MAP_SWIZZLE_NONE, di.dev, maps.SB)) != FP8G_OK)
+        return st;
+    const int64_t clusters = p.T < di.num_sms / 2 ? p.T : di.num_sms / 2;
+    const cudaError_t e = timed_launch(stream, [&] {
+        return launch_gemm_pair(kModeBlock, out == FP8G_OUT_F32, maps, p, (int)(2 * clusters), stream, lora);
+    });
+    return e == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+}
+
 // NVFP4 on CTA pairs (kind::mxf4nvf4 is issued with cta_group::2) whatever
 // the shape: pack the E4M3 scale codes into the pair kernel's chunks (a
 // stream-ordered temporary from the library pool), run the GEMM, return the

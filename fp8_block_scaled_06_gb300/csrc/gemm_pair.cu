@@ -174,12 +174,28 @@ __device__ __forceinline__ PairTile pair_tile(int32_t t, const GemmParams &p, co
     return ti;
 }
 
-template <int MODE, bool OUT_F32, int F4>
+// The low-rank steps of kernels that have them (LORA), nothing for the others.
+template <bool LORA>
+struct LoraArg {};
+template <>
+struct LoraArg<true> {
+    PairLora p;
+};
+
+template <int MODE, bool OUT_F32, int F4, bool LORA>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmSA,
-                     const __grid_constant__ CUtensorMap tmSB, const GemmParams p) {
+                     const __grid_constant__ CUtensorMap tmSB, const GemmParams p,
+                     const __grid_constant__ LoraArg<LORA> la) {
     using PC = PairCfg<MODE, F4>;
+    static_assert(!LORA || (MODE == kModeBlock && F4 == 0), "low-rank steps: block-scaled FP8-rate");
+    // Low-rank steps of a tile, after its num_kb FP8 steps: step ls is 64-wide
+    // step ls / 2 % kr of slot ls / (2 kr), first half of V, then second
+    auto lora_steps = [&](const int32_t pm) -> int {
+        if constexpr (LORA) return 2 * la.p.kr * __ldcg(la.p.slots + pm);
+        return 0;
+    };
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = ptx::smem_addr(smem_raw);
     uint8_t *smem = smem_raw + ((1024u - (raw_base & 1023u)) & 1023u);
@@ -283,10 +299,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                         *reinterpret_cast<int4 *>(p.tile_map_out + 4 * (int64_t)t) =
                             make_int4(ti.e, ti.pm, ti.pn, 0);
                 }
-                for (int kb = 0; kb < p.num_kb; ++kb) {
+                const int n_steps = p.num_kb + lora_steps(ti.pm);
+                for (int kb = 0; kb < n_steps; ++kb) {
                     if (!wait_bar(bar_empty(stage), phase ^ 1u, abort_flag, p, 0 * 256 + stage))
                         goto roles_done;
                     const uint32_t fb = leader ? bar_full(stage) : ptx::map_shared(bar_full(stage), 0);
+                    if constexpr (LORA) {
+                        if (kb >= p.num_kb) {
+                            const int ls = kb - p.num_kb, sl = ls / (2 * la.p.kr);
+                            const int c = (ls / 2 - sl * la.p.kr) * 64;
+                            const int slot = ti.pm * la.p.cap + sl;
+                            if (leader) ptx::mbar_arrive_expect_tx(fb, 2 * (kA + kB));
+                            ptx::tma_load_2d_pair(sbase + PC::OFF_A + stage * kA, &la.p.V, fb, c,
+                                                  (2 * slot + (ls & 1)) * 256 + (int32_t)rank * kBM);
+                            ptx::tma_load_3d_pair(sbase + PC::OFF_B + stage * kB, &la.p.B, fb, c, nb0,
+                                                  __ldcg(la.p.adapters + slot));
+                            if (++stage == PC::STAGES) {
+                                stage = 0;
+                                phase ^= 1u;
+                            }
+                            continue;
+                        }
+                    }
                     if (leader) ptx::mbar_arrive_expect_tx(fb, 2 * tx_bytes);
                     // first K element of the stage: a 128-byte row holds 128 one-byte
                     // elements, or 32 fp32 ones (TF32)
@@ -345,7 +379,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       1 * 256 + 64))
                     goto roles_done;
                 ptx::tc_fence_after();
-                for (int kb = 0; kb < p.num_kb; ++kb) {
+                const int n_steps =
+                    p.num_kb + (LORA ? lora_steps(pair_tile<MODE>(t, p, row_off, tile_off, rt_off).pm) : 0);
+                for (int kb = 0; kb < n_steps; ++kb) {
                     // block modes: data and scale factors in place (the
                     // scale-copy thread waited for "full" and committed its copies)
                     const uint32_t rb = PC::kBlock ? bar_sfr(stage) : bar_full(stage);
@@ -353,7 +389,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tc_fence_after();
                     const uint32_t a0 = sbase + PC::OFF_A + stage * kA;
                     const uint32_t b0 = sbase + PC::OFF_B + stage * kB;
-                    if constexpr (F4 == 2) {
+                    if (LORA && kb >= p.num_kb) {
+                        if constexpr (LORA) {
+                            const int c = (kb - p.num_kb) / 2 % la.p.kr * 64;
+                            const int nk = (min(64, la.p.rank - c) + 15) / 16;
+                            for (int k = 0; k < nk; ++k)
+                                ptx::mma_bf16_pair(d_tmem, ptx::desc_kmajor_sw128(a0 + k * 32),
+                                                   ptx::desc_kmajor_sw128(b0 + k * 32),
+                                                   ptx::idesc_bf16(2 * kBM, kPairBN), 1u);
+                        }
+                    } else if constexpr (F4 == 2) {
                         // MMA k: K elements 64k .. 64k + 63 = K group k's four
                         // 16-wide scale blocks (the whole word, sf_id 0)
                         const uint32_t sf = tmem_base + 256 + stage * PC::SF_COLS;
@@ -418,10 +463,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             uint32_t stage = 0, phase = 0;
             for (int32_t t = t_first; t < T; t += t_step) {
-                for (int kb = 0; kb < p.num_kb; ++kb) {
+                const int n_steps =
+                    p.num_kb + (LORA ? lora_steps(pair_tile<MODE>(t, p, row_off, tile_off, rt_off).pm) : 0);
+                for (int kb = 0; kb < n_steps; ++kb) {
                     if (!wait_bar(bar_full(stage), phase, abort_flag, p, 2 * 256 + stage))
                         goto roles_done;
                     ptx::tc_fence_after();
+                    if (LORA && kb >= p.num_kb) {  // no scales: pass the stage on
+                        ptx::tc_commit_pair_mc(bar_sfr(stage), 0x1);
+                        if (++stage == PC::STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                        continue;
+                    }
                     const uint32_t sf = tmem_base + 256 + stage * PC::SF_COLS;
                     const uint32_t cs = sbase + PC::OFF_SF + stage * PC::CHUNK;
                     constexpr int G = PC::G;
@@ -533,10 +588,11 @@ roles_done:
     }
 }
 
-template <int MODE, bool OUT_F32, int F4 = 0>
-cudaError_t launch_pair(const GemmMaps &maps, const GemmParams &p, int grid, cudaStream_t stream) {
+template <int MODE, bool OUT_F32, int F4 = 0, bool LORA = false>
+cudaError_t launch_pair(const GemmMaps &maps, const GemmParams &p, int grid, cudaStream_t stream,
+                        const LoraArg<LORA> &la = {}) {
     using PC = PairCfg<MODE, F4>;
-    auto kern = gemm_pair_kernel<MODE, OUT_F32, F4>;
+    auto kern = gemm_pair_kernel<MODE, OUT_F32, F4, LORA>;
     static unsigned long long attr_done = 0ull;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -561,13 +617,19 @@ cudaError_t launch_pair(const GemmMaps &maps, const GemmParams &p, int grid, cud
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, maps.A, maps.B, maps.SA, maps.SB, p);
+    return cudaLaunchKernelEx(&cfg, kern, maps.A, maps.B, maps.SA, maps.SB, p, la);
 }
 
 }  // namespace
 
 cudaError_t launch_gemm_pair(int mode, bool out_f32, const GemmMaps &maps, const GemmParams &p,
-                             int grid, cudaStream_t stream) {
+                             int grid, cudaStream_t stream, const PairLora *lora) {
+    if (lora != nullptr) {
+        if (mode != kModeBlock || p.f4) return cudaErrorInvalidValue;
+        const LoraArg<true> la{*lora};
+        return out_f32 ? launch_pair<kModeBlock, true, 0, true>(maps, p, grid, stream, la)
+                       : launch_pair<kModeBlock, false, 0, true>(maps, p, grid, stream, la);
+    }
     if (p.f4 == 2 && mode == kModeBlock)
         return out_f32 ? launch_pair<kModeBlock, true, 2>(maps, p, grid, stream)
                        : launch_pair<kModeBlock, false, 2>(maps, p, grid, stream);

@@ -104,9 +104,27 @@ cudaError_t launch_wait_selftest(unsigned int *status, uint64_t timeout_ns, cuda
 cudaError_t launch_gemm_promote(bool out_f32, const GemmMaps &maps, const GemmParams &p, int grid,
                                 cudaStream_t stream);
 
-// gemm_pair.cu (per-tensor and block-scaled, CTA pairs)
+// Low-rank steps of the block-scaled CTA-pair kernel: after a tile's FP8 steps,
+// 2 kr bf16 steps per slot of its 256 rows (V's two halves against the
+// adapter's rows; lora.cu).
+struct PairLora {
+    CUtensorMap V;  // bf16 rows: half h of row i of slot s of row tile t at ((t cap + s) 2 + h) 256 + i
+    CUtensorMap B;  // bf16 [adapter][N][rank]
+    const int32_t *slots;     // [row tile]
+    const int32_t *adapters;  // [row tile][cap]
+    int32_t cap, rank, kr;
+};
+
+// gemm_pair.cu (per-tensor and block-scaled, CTA pairs); lora: block-scaled only
 cudaError_t launch_gemm_pair(int mode, bool out_f32, const GemmMaps &maps, const GemmParams &p,
-                             int grid, cudaStream_t stream);
+                             int grid, cudaStream_t stream, const PairLora *lora = nullptr);
+
+// api.cu: block-scaled GEMM on CTA pairs from scales that are packed already
+// (A's as [ceil(K/128)][ceil(M/128)][512], B's as fp8g_pack_scales gives them),
+// A in E4M3; lora may be null.
+fp8g_status run_pair_packed(const void *A, const uint8_t *sfa, const void *B, const uint8_t *sfb,
+                            int b_fmt, const float *bias, void *C, int out, int64_t M, int64_t N,
+                            int64_t K, const PairLora *lora, cudaStream_t stream);
 
 
 // api.cu: checks done by the caller; scratch == nullptr takes the packed

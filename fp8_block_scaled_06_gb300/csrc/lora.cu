@@ -1,0 +1,436 @@
+// A block-scaled projection with low-rank adapters of many requests.
+//
+//   C[i] = out( Q(x_i) W^T + bias + alpha_l B_l (A_l x_i) ),  l = adapter[i]
+//
+// Two launches.  The first quantises x and forms V = alpha A x; the second is
+// the product, with V against the adapters' B rows as further K steps into
+// the same fp32 accumulator, so the sum is rounded once: for few rows the
+// streaming kernel (stream.cu), else the CTA-pair kernel (gemm_pair.cu).
+//
+// V.  Rows are taken in tiles of `tile` (a group of the streaming kernel, or
+// the 256 rows of a pair).  The adapters among a tile's rows, in rising order,
+// are its slots; a slot holds V of all the tile's rows, zero for those of
+// other adapters, as two bf16 halves (V = hi + lo to 16 bits): the product
+// then needs no gather, and an adapter costs rank / 128 of a K step's weights.
+#include <cuda_bf16.h>
+
+#include "internal.h"
+#include "kernel_common.cuh"
+#include "quant_math.cuh"
+#include "stream.h"
+
+namespace fp8g {
+
+namespace {
+
+constexpr int kLThreads = 512;
+constexpr int kLWarps = kLThreads / 32;
+constexpr int kMaxTile = 256;
+
+struct LoraPrep {
+    const void *x;
+    int32_t M, K;
+    uint8_t *xq;        // [M][K] codes
+    uint8_t *xsf;       // chunk of (row tile rt of sf_rows rows, K group kg) at kg sf_k + rt sf_t
+    int32_t sf_rows;
+    int64_t sf_k, sf_t;
+    int32_t ks;
+    int32_t *cnt;       // counters to zero
+    int32_t n_cnt;
+    // low-rank part
+    const __nv_bfloat16 *a;   // [L][r][K]
+    const float *alpha;       // [L] or null
+    const int32_t *adapter;   // [M]
+    int32_t L, r, r64;        // r64: V's row length, r rounded up to 64
+    int32_t tile, cap, tiles;
+    __nv_bfloat16 *v;         // [tiles][cap][2][tile][r64]
+    int32_t *slot_cnt, *slot_adapter;  // tables of the pair kernel, or null
+    int32_t items;            // blocks per tile and rank block of the low-rank part
+    unsigned int *status;
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&b);
+}
+
+__device__ __forceinline__ float bf16_round(float v) { return __bfloat162float(__float2bfloat16_rn(v)); }
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 8 consecutive values of x as bf16 pairs; HALF 0: x rounded to bf16, 1: what
+// that leaves, rounded (fp32 x: 16 significant bits in two halves).
+template <bool BF16, int HALF>
+__device__ __forceinline__ uint4 x_pairs(const void *x, int64_t off, bool in) {
+    if (!in) return make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (BF16) {
+        return __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(x) + off));
+    } else {
+        float4 a, b;
+        load8<false>(x, off, a, b);
+        float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        if constexpr (HALF == 1) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] -= bf16_round(v[i]);
+        }
+        return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                          pack_bf16(v[6], v[7]));
+    }
+}
+
+// Blocks [0, M): quantise row blockIdx.x.  The rest: the low-rank part, block
+// (tile, rank block of 16, item): items are the pairs (slot, 16 of the slot's
+// rows) in order.  The K range goes over the block's warps (bound by the
+// latency of its loads: 16 warps with their loads of up to 128 K each in
+// flight), each a 16 x 16 product by mma.sync, joined in shared memory in warp
+// order.  A lane's 16-byte load covers 8 consecutive K of a row; the same K
+// permutation on both operands leaves the product unchanged.
+template <bool BF16>
+__global__ void __launch_bounds__(kLThreads) lora_prep_kernel(LoraPrep p) {
+    __shared__ int32_t ad[kMaxTile];
+    __shared__ int32_t cnt[kMaxAdapters];
+    __shared__ int32_t pick[3];  // adapter, slot, first of its rows
+    __shared__ int32_t rows[16];
+    __shared__ float acc[kLWarps][16][17];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int blk = blockIdx.x;
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    if (blk < p.M) {
+        for (int i = blk * kLThreads + tid; i < p.n_cnt; i += p.M * kLThreads) p.cnt[i] = 0;
+        const int rt = blk / p.sf_rows, in_t = blk - rt * p.sf_rows;
+        const int groups = p.ks * 16;
+        for (int c0 = 0; c0 < groups; c0 += kLThreads) {
+            const int c = c0 + tid;
+            float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
+            const bool in = c * 8 < p.K;
+            if (in) load8<BF16>(p.x, (int64_t)blk * p.K + c * 8, v0, v1);
+            float am = absmax8(v0, v1);
+            am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+            am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+            const float s = pow2_scale<0>(am);
+            if (in)
+                *reinterpret_cast<uint2 *>(p.xq + (int64_t)blk * p.K + c * 8) = quant8_pow2<0>(v0, v1, s);
+            if (c < groups && (c & 3) == 0)
+                p.xsf[(c >> 4) * p.sf_k + rt * p.sf_t + 16 * (in_t & 31) + 4 * (in_t >> 5) + ((c >> 2) & 3)] =
+                    (uint8_t)(__float_as_uint(s) >> 23);
+        }
+        return;
+    }
+    // ------------------------------------------------------- low-rank part
+    const int rblocks = (p.r + 15) / 16;
+    int w = blk - p.M;
+    const int item = w % p.items;
+    w /= p.items;
+    const int rb = w % rblocks, tile = w / rblocks;
+    const int row0 = tile * p.tile, n = min(p.tile, p.M - row0);
+    for (int i = tid; i < p.L; i += kLThreads) cnt[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < p.tile; i += kLThreads) {
+        int l = i < n ? __ldg(p.adapter + row0 + i) : -1;
+        if (l >= p.L) {
+            if (item == 0 && rb == 0 && atomicCAS(&p.status[0], 0u, (unsigned)FP8G_ERR_INVALID_ARG) == 0u)
+                atomicExch(&p.status[1], (unsigned)(row0 + i));
+            l = -1;
+        }
+        ad[i] = l < 0 ? -1 : l;
+        if (l >= 0) atomicAdd(&cnt[l], 1);
+    }
+    if (tid == 0) pick[0] = -1;
+    if (tid < 16) rows[tid] = -1;
+    __syncthreads();
+    if (warp == 0) {
+        int slots = 0, items = 0;  // of the adapters before this step's
+        for (int l0 = 0; l0 < p.L; l0 += 32) {
+            const int l = l0 + lane;
+            const int c = l < p.L ? cnt[l] : 0, it = (c + 15) / 16, has = c > 0;
+            int s_it = it, s_sl = has;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int vi = __shfl_up_sync(0xffffffffu, s_it, o), vs = __shfl_up_sync(0xffffffffu, s_sl, o);
+                if (lane >= o) {
+                    s_it += vi;
+                    s_sl += vs;
+                }
+            }
+            const int first = items + s_it - it, slot = slots + s_sl - has;
+            if (has && item >= first && item < first + it) {
+                pick[0] = l;
+                pick[1] = slot;
+                pick[2] = 16 * (item - first);
+            }
+            if (has && p.slot_cnt != nullptr && item == 0 && rb == 0) p.slot_adapter[tile * p.cap + slot] = l;
+            items += __shfl_sync(0xffffffffu, s_it, 31);
+            slots += __shfl_sync(0xffffffffu, s_sl, 31);
+        }
+        if (lane == 0 && p.slot_cnt != nullptr && item == 0 && rb == 0) p.slot_cnt[tile] = slots;
+        __syncwarp();
+        const int l = pick[0];
+        if (l >= 0) {  // this item's rows: those of adapter l, from the pick[2]-th on
+            int seen = 0;
+            for (int i0 = 0; i0 < p.tile; i0 += 32) {
+                const bool m = i0 + lane < p.tile && ad[i0 + lane] == l;
+                const uint32_t b = __ballot_sync(0xffffffffu, m);
+                const int at = seen + __popc(b & ((1u << lane) - 1u)) - pick[2];
+                if (m && at >= 0 && at < 16) rows[at] = i0 + lane;
+                seen += __popc(b);
+            }
+        }
+    }
+    __syncthreads();
+    const int l = pick[0];
+    if (l < 0) return;
+    __nv_bfloat16 *hi = p.v + ((int64_t)(tile * p.cap + pick[1]) * 2 * p.tile) * p.r64 + rb * 16;
+    const int64_t half = (int64_t)p.tile * p.r64;
+    // zero rows of the other adapters (the slot's first item), and the columns
+    // past the rank up to r64 (its first rank block)
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    if (pick[2] == 0)
+        for (int i = tid; i < p.tile; i += kLThreads) {
+            uint4 *d = reinterpret_cast<uint4 *>(hi + (int64_t)i * p.r64);
+            uint4 *e = reinterpret_cast<uint4 *>(hi + half + (int64_t)i * p.r64);
+            if (ad[i] != l) d[0] = d[1] = e[0] = e[1] = z;
+            if (rb == 0)
+                for (int c = 2 * rblocks; c < p.r64 / 8; ++c) d[c] = e[c] = z;
+        }
+    // this lane's x rows (g, g + 8) and adapter rows (ranks g, g + 8 of the block)
+    const int g = lane >> 2, c8 = 8 * (lane & 3);
+    const int i0 = rows[g], i1 = rows[g + 8];
+    const int64_t x0 = (int64_t)(row0 + max(i0, 0)) * p.K + c8, x1 = (int64_t)(row0 + max(i1, 0)) * p.K + c8;
+    const int r0 = rb * 16 + g, r1 = r0 + 8;
+    const __nv_bfloat16 *a0 = p.a + ((int64_t)l * p.r + min(r0, p.r - 1)) * p.K + c8;
+    const __nv_bfloat16 *a1 = p.a + ((int64_t)l * p.r + min(r1, p.r - 1)) * p.K + c8;
+    float d0[4] = {}, d1[4] = {};
+    const int steps = p.K / 32;  // K is a multiple of 32
+    constexpr int kU = 4;
+    for (int s0 = warp * kU; s0 < steps; s0 += kLWarps * kU) {
+        uint4 xa[kU], xb[kU], wa[kU], wb[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const bool in = s0 + u < steps;
+            const int64_t k = in ? (int64_t)(s0 + u) * 32 : 0;
+            xa[u] = x_pairs<BF16, 0>(p.x, x0 + k, in && i0 >= 0);
+            xb[u] = x_pairs<BF16, 0>(p.x, x1 + k, in && i1 >= 0);
+            wa[u] = in && r0 < p.r ? __ldg(reinterpret_cast<const uint4 *>(a0 + k)) : z;
+            wb[u] = in && r1 < p.r ? __ldg(reinterpret_cast<const uint4 *>(a1 + k)) : z;
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const uint32_t f0[4] = {xa[u].x, xb[u].x, xa[u].y, xb[u].y};
+            const uint32_t f1[4] = {xa[u].z, xb[u].z, xa[u].w, xb[u].w};
+            mma_16816(d0, f0, wa[u].x, wa[u].y);
+            mma_16816(d1, f0, wb[u].x, wb[u].y);
+            mma_16816(d0, f1, wa[u].z, wa[u].w);
+            mma_16816(d1, f1, wb[u].z, wb[u].w);
+            if constexpr (!BF16) {
+                const bool in = s0 + u < steps;
+                const int64_t k = in ? (int64_t)(s0 + u) * 32 : 0;
+                const uint4 ya = x_pairs<false, 1>(p.x, x0 + k, in && i0 >= 0);
+                const uint4 yb = x_pairs<false, 1>(p.x, x1 + k, in && i1 >= 0);
+                const uint32_t h0[4] = {ya.x, yb.x, ya.y, yb.y}, h1[4] = {ya.z, yb.z, ya.w, yb.w};
+                mma_16816(d0, h0, wa[u].x, wa[u].y);
+                mma_16816(d1, h0, wb[u].x, wb[u].y);
+                mma_16816(d0, h1, wa[u].z, wa[u].w);
+                mma_16816(d1, h1, wb[u].z, wb[u].w);
+            }
+        }
+    }
+    {
+        const int c = 2 * (lane & 3);
+        acc[warp][g][c] = d0[0];
+        acc[warp][g][c + 1] = d0[1];
+        acc[warp][g + 8][c] = d0[2];
+        acc[warp][g + 8][c + 1] = d0[3];
+        acc[warp][g][8 + c] = d1[0];
+        acc[warp][g][8 + c + 1] = d1[1];
+        acc[warp][g + 8][8 + c] = d1[2];
+        acc[warp][g + 8][8 + c + 1] = d1[3];
+    }
+    __syncthreads();
+    if (tid < 256) {
+        const int i = tid >> 4, c = tid & 15, row = rows[i];
+        float v = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kLWarps; ++q) v += acc[q][i][c];
+        if (p.alpha != nullptr) v *= __ldg(p.alpha + l);
+        if (row >= 0) {
+            if (rb * 16 + c >= p.r) v = 0.0f;
+            const __nv_bfloat16 h = __float2bfloat16_rn(v);
+            // (an infinite or NaN V has no second half)
+            const float rest = v - __bfloat162float(h);
+            hi[(int64_t)row * p.r64 + c] = h;
+            hi[half + (int64_t)row * p.r64 + c] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
+        }
+    }
+}
+
+bool is_aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+bool packed(int f) { return f == FP8G_E2M1 || f == FP8G_E2M3 || f == FP8G_E3M2; }
+constexpr int64_t kMaxDim = (int64_t)1 << 31;
+
+}  // namespace
+
+}  // namespace fp8g
+
+using namespace fp8g;
+
+extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void *W, const uint8_t *sfw,
+                                     int32_t w_fmt, const void *lora_a, const void *lora_b,
+                                     const float *alpha, const int32_t *adapter, int32_t L, int32_t r,
+                                     const float *bias, void *C, int out, int64_t M, int64_t N, int64_t K,
+                                     cudaStream_t stream) {
+    if (x_dtype != FP8G_IN_F32 && x_dtype != FP8G_IN_BF16) return FP8G_ERR_INVALID_ARG;
+    if (out != FP8G_OUT_BF16 && out != FP8G_OUT_F32) return FP8G_ERR_INVALID_ARG;
+    if (w_fmt < FP8G_E4M3 || w_fmt > FP8G_E3M2) return FP8G_ERR_INVALID_ARG;
+    if (M < 0 || N < 1 || K < 1 || L < 0 || (L > 0 && r < 1)) return FP8G_ERR_INVALID_ARG;
+    if (W == nullptr || sfw == nullptr) return FP8G_ERR_INVALID_ARG;
+    if (M > 0 && (x == nullptr || C == nullptr)) return FP8G_ERR_INVALID_ARG;
+    const bool lora = L > 0;
+    if (lora && (lora_a == nullptr || lora_b == nullptr || (M > 0 && adapter == nullptr)))
+        return FP8G_ERR_INVALID_ARG;
+    if (K % (packed(w_fmt) ? 128 : 32) != 0 || (lora && r % 8 != 0)) return FP8G_ERR_UNSUPPORTED_SHAPE;
+    if (L > FP8G_MAX_ADAPTERS || (lora && r > FP8G_MAX_LORA_RANK) || M >= (1 << 24) || N >= (1 << 24) ||
+        K >= (1 << 24))
+        return FP8G_ERR_UNSUPPORTED_SHAPE;
+    if (!is_aligned(x, 16) || !is_aligned(C, 16) || !is_aligned(W, packed(w_fmt) ? 32 : 16) ||
+        !is_aligned(sfw, 16) || !is_aligned(bias, 4) || (N * (out == FP8G_OUT_F32 ? 4 : 2)) % 16 != 0)
+        return FP8G_ERR_ALIGNMENT;
+    if (lora && (!is_aligned(lora_a, 16) || !is_aligned(lora_b, 16) || !is_aligned(alpha, 4) ||
+                 !is_aligned(adapter, 4)))
+        return FP8G_ERR_ALIGNMENT;
+    HostDevice d;
+    fp8g_status st = host_device(d);
+    if (st != FP8G_OK) return st;
+    if (M == 0) return FP8G_OK;
+
+    const bool pair = M > kStreamMaxLoraRows;
+    const int nb = pair ? 256 : (int)(M < kStreamMaxTokens ? (M + 15) / 16 * 16 : kStreamMaxTokens);
+    const int tiles = (int)((M + nb - 1) / nb);
+    const int32_t ks = (int32_t)((K + 127) / 128), n_rt = (int32_t)((N + 127) / 128);
+    const int cap = L < nb ? L : nb, r64 = lora ? (r + 63) / 64 * 64 : 64;
+    const int32_t n_rtA = (int32_t)((M + 127) / 128);
+    StreamParams sp{};
+    if (!pair) {
+        stream_sizes(sp, nb, lora);
+        sp.mt = (int32_t)((N + 255) / 256);
+        sp.ks = ks;
+        sp.rows = (int32_t)N;
+        sp.n_rt = n_rt;
+        sp.kr = lora ? r64 / 64 : 0;
+        if ((int64_t)tiles * sp.mt * (ks + (int64_t)cap * sp.kr) >= INT32_MAX)
+            return FP8G_ERR_UNSUPPORTED_SHAPE;
+    }
+    if ((int64_t)tiles * cap * 2 * nb >= kMaxDim || (int64_t)ks * n_rtA >= kMaxDim)
+        return FP8G_ERR_UNSUPPORTED_SHAPE;  // rows of V and of the scales: 32-bit TMA coordinates
+    size_t at = 0;
+    auto take = [&at](size_t bytes) {
+        const size_t o = at;
+        at += (bytes + 1023) / 1024 * 1024;
+        return o;
+    };
+    const size_t o_xq = take((size_t)M * K), o_xsf = take((size_t)(pair ? n_rtA : tiles) * ks * 512);
+    const size_t o_v = take((size_t)tiles * cap * 2 * nb * r64 * 2);
+    const int n_cnt = pair ? 0 : tiles * sp.mt;
+    const size_t o_cnt = take((size_t)n_cnt * 4);
+    const size_t o_part = take(pair ? 0 : stream_part_bytes(sp, d.num_sms));
+    const size_t o_sc = take((size_t)tiles * 4), o_sa = take((size_t)tiles * cap * 4);
+    cudaMemPool_t pool;
+    if ((st = host_pool(d.dev, pool)) != FP8G_OK) return st;
+    void *wsv = nullptr;
+    if (cudaMallocFromPoolAsync(&wsv, at, pool, stream) != cudaSuccess) return FP8G_ERR_CUDA;
+    uint8_t *ws = static_cast<uint8_t *>(wsv);
+
+    LoraPrep a{};
+    a.x = x;
+    a.M = (int32_t)M;
+    a.K = (int32_t)K;
+    a.xq = ws + o_xq;
+    a.xsf = ws + o_xsf;
+    a.sf_rows = pair ? 128 : nb;
+    a.sf_k = pair ? (int64_t)n_rtA * 512 : 512;
+    a.sf_t = pair ? 512 : (int64_t)ks * 512;
+    a.ks = ks;
+    a.cnt = reinterpret_cast<int32_t *>(ws + o_cnt);
+    a.n_cnt = n_cnt;
+    a.a = static_cast<const __nv_bfloat16 *>(lora_a);
+    a.alpha = alpha;
+    a.adapter = adapter;
+    a.L = L;
+    a.r = r;
+    a.r64 = r64;
+    a.tile = nb;
+    a.cap = cap;
+    a.tiles = tiles;
+    a.v = reinterpret_cast<__nv_bfloat16 *>(ws + o_v);
+    if (pair) {
+        a.slot_cnt = reinterpret_cast<int32_t *>(ws + o_sc);
+        a.slot_adapter = reinterpret_cast<int32_t *>(ws + o_sa);
+    }
+    // at most one partly filled item per slot beside the whole ones
+    a.items = nb / 16 + cap;
+    a.status = d.status;
+    const int64_t blocks = M + (lora ? (int64_t)tiles * ((r + 15) / 16) * a.items : 0);
+    cudaError_t e = blocks >= INT32_MAX ? cudaErrorInvalidValue
+                    : x_dtype == FP8G_IN_BF16
+                        ? launch_programmatic(lora_prep_kernel<true>, dim3((unsigned)blocks), dim3(kLThreads),
+                                              stream, a)
+                        : launch_programmatic(lora_prep_kernel<false>, dim3((unsigned)blocks),
+                                              dim3(kLThreads), stream, a);
+    CUtensorMap mb{}, mv{};
+    if (e == cudaSuccess && lora) {
+        const uint64_t db[3] = {(uint64_t)r, (uint64_t)N, (uint64_t)L};
+        const uint32_t bb[3] = {64u, 128u, 1u};
+        const uint64_t dv[2] = {(uint64_t)r64, (uint64_t)tiles * cap * 2 * nb};
+        const uint32_t bv[2] = {64u, pair ? 128u : 16u};
+        st = host_bf16_map(lora_b, 3, db, bb, d.dev, mb);
+        if (st == FP8G_OK) st = host_bf16_map(a.v, 2, dv, bv, d.dev, mv);
+    }
+    if (e == cudaSuccess && st == FP8G_OK && !pair) {
+        CUtensorMap mw, mx;
+        const uint64_t dw[3] = {(uint64_t)K, (uint64_t)N, 1u};
+        const uint32_t bw[3] = {(uint32_t)kBK, 128u, 1u};
+        const uint64_t dx[2] = {(uint64_t)K, (uint64_t)M};
+        const uint32_t bx[2] = {(uint32_t)kBK, 16u};
+        st = host_operand_map(W, w_fmt, 3, dw, bw, d.dev, mw);
+        if (st == FP8G_OK) st = host_operand_map(a.xq, FP8G_E4M3, 2, dx, bx, d.dev, mx);
+        if (!lora) mb = mv = mx;
+        sp.w_fmt = host_mma_type(w_fmt) << 7;
+        sp.gap8 = host_gap8(w_fmt);
+        sp.sfw = sfw;
+        sp.sfx = a.xsf;
+        sp.idx = adapter;
+        sp.n_idx = (int32_t)M;
+        sp.n_mat = L;
+        sp.tile_cnt = a.cnt;
+        sp.part = reinterpret_cast<float *>(ws + o_part);
+        sp.status = d.status;
+        sp.timeout_ns = d.timeout_ns;
+        sp.c = C;
+        sp.out_f32 = out == FP8G_OUT_F32;
+        sp.bias = bias;
+        sp.rank = r;
+        sp.slot_cap = cap;
+        if (st == FP8G_OK) e = launch_stream(kStreamOut, mw, mx, mb, mv, sp, d.num_sms, stream);
+    } else if (e == cudaSuccess && st == FP8G_OK) {
+        PairLora pl{};
+        if (lora) {
+            pl.V = mv;
+            pl.B = mb;
+            pl.slots = a.slot_cnt;
+            pl.adapters = a.slot_adapter;
+            pl.cap = cap;
+            pl.rank = r;
+            pl.kr = r64 / 64;
+        }
+        st = run_pair_packed(a.xq, a.xsf, W, sfw, w_fmt, bias, C, out, M, N, K, lora ? &pl : nullptr, stream);
+    }
+    const cudaError_t ef = cudaFreeAsync(wsv, stream);
+    if (st != FP8G_OK) return st;
+    return e == cudaSuccess && ef == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+}

@@ -31,24 +31,21 @@ struct PrepArgs {
     int32_t T, k, E, H;
     int32_t nb;        // tokens per group
     int32_t ks;        // 128-wide K steps of x
-    int32_t units1, units2;  // work units per group of the two products
     uint8_t *xq;       // [T k][H] codes, expert order
     uint8_t *xsf;      // [group][ks][512]
     int32_t *pos;      // [T k] row in expert order, -1: not routed
-    int32_t *head1, *head2;  // groups, units
-    StreamGroup *g1, *g2;
     int32_t *cnt;      // counters of both products
     int32_t n_cnt;
     unsigned int *status;
 };
 
 // Block t: token t.  Every block derives the routing tables it needs from the
-// ids itself (a few thousand integers at most); block 0 stores them.
+// ids itself (a few thousand integers at most), as the products' CTAs do.
 template <bool BF16>
 __global__ void __launch_bounds__(kPrepThreads) moe_prep_kernel(PrepArgs a) {
     __shared__ int16_t id[kMaxPairs];
     __shared__ int32_t cnt[kMaxExperts], off[kMaxExperts], goff[kMaxExperts];
-    __shared__ int32_t my_row[16], my_tile[16], my_in[16], sum_g;
+    __shared__ int32_t my_row[16], my_tile[16], my_in[16];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int R = a.T * a.k, t = blockIdx.x;
     for (int e = tid; e < a.E; e += kPrepThreads) cnt[e] = 0;
@@ -90,22 +87,8 @@ __global__ void __launch_bounds__(kPrepThreads) moe_prep_kernel(PrepArgs a) {
             rr += __shfl_sync(0xffffffffu, s, 31);
             gg += __shfl_sync(0xffffffffu, sg, 31);
         }
-        if (lane == 0) sum_g = gg;
     }
     __syncthreads();
-    if (t == 0) {
-        if (tid == 0) {
-            a.head1[0] = a.head2[0] = sum_g;
-            a.head1[1] = sum_g * a.units1;
-            a.head2[1] = sum_g * a.units2;
-        }
-        for (int e = tid; e < a.E; e += kPrepThreads)
-            for (int i = 0; i * a.nb < cnt[e]; ++i) {
-                const int g = goff[e] + i, n = min(a.nb, cnt[e] - i * a.nb);
-                a.g1[g] = StreamGroup{e, off[e] + i * a.nb, n, g * a.units1};
-                a.g2[g] = StreamGroup{e, off[e] + i * a.nb, n, g * a.units2};
-            }
-    }
     // this token's places: the pairs before it with the same expert
     for (int j = warp; j < a.k; j += kPrepThreads / 32) {
         const int i = t * a.k + j, e = id[i];
@@ -310,8 +293,6 @@ fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t *ids, co
     const size_t o_y = take((size_t)R * H * 4), o_part = take(stream_part_bytes(p1, d.num_sms));
     const int n_cnt = max_groups * (p1.mt + p2.mt);
     const size_t o_cnt = take((size_t)n_cnt * 4), o_pos = take((size_t)R * 4);
-    const size_t o_g1 = take(sizeof(StreamGroup) * (size_t)max_groups);
-    const size_t o_g2 = take(sizeof(StreamGroup) * (size_t)max_groups), o_head = take(16);
     cudaMemPool_t pool;
     if ((st = host_pool(d.dev, pool)) != FP8G_OK) return st;
     void *wsv = nullptr;
@@ -330,7 +311,6 @@ fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t *ids, co
         if (st == FP8G_OK) st = host_operand_map(ws + o_hq, FP8G_E4M3, 2, dh, bx, d.dev, mh);
     }
     cudaError_t e = st == FP8G_OK ? cudaSuccess : cudaErrorInvalidValue;
-    int32_t *head = reinterpret_cast<int32_t *>(ws + o_head);
     int32_t *cnt = reinterpret_cast<int32_t *>(ws + o_cnt);
     int32_t *pos = reinterpret_cast<int32_t *>(ws + o_pos);
     if (e == cudaSuccess) {
@@ -343,15 +323,9 @@ fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t *ids, co
         a.H = (int32_t)H;
         a.nb = nb;
         a.ks = p1.ks;
-        a.units1 = (int32_t)units1;
-        a.units2 = (int32_t)units2;
         a.xq = ws + o_xq;
         a.xsf = ws + o_xsf;
         a.pos = pos;
-        a.head1 = head;
-        a.head2 = head + 2;
-        a.g1 = reinterpret_cast<StreamGroup *>(ws + o_g1);
-        a.g2 = reinterpret_cast<StreamGroup *>(ws + o_g2);
         a.cnt = cnt;
         a.n_cnt = n_cnt;
         a.status = d.status;
@@ -363,22 +337,21 @@ fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t *ids, co
     for (StreamParams *p : {&p1, &p2}) {
         p->w_fmt = host_mma_type(w_fmt) << 7;
         p->gap8 = host_gap8(w_fmt);
+        p->idx = ids;
+        p->n_idx = R;
+        p->n_mat = E;
         p->part = reinterpret_cast<float *>(ws + o_part);
         p->status = d.status;
         p->timeout_ns = d.timeout_ns;
     }
     p1.sfw = sf13;
     p1.sfx = ws + o_xsf;
-    p1.head = head;
-    p1.groups = reinterpret_cast<StreamGroup *>(ws + o_g1);
     p1.tile_cnt = cnt;
     p1.gate = gate;
     p1.hq = ws + o_hq;
     p1.hsf = ws + o_hsf;
     p2.sfw = sf2;
     p2.sfx = ws + o_hsf;
-    p2.head = head + 2;
-    p2.groups = reinterpret_cast<StreamGroup *>(ws + o_g2);
     p2.tile_cnt = cnt + (size_t)max_groups * p1.mt;
     p2.y = reinterpret_cast<float *>(ws + o_y);
     if (e == cudaSuccess) e = launch_stream(kStreamGated, m13, mx, mx, mx, p1, d.num_sms, stream);

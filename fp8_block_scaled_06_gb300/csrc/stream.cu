@@ -42,16 +42,28 @@ constexpr int kMaxStages = 16;
 constexpr int kSfSlot = 16;        // tensor-memory columns of a stage's scales
 constexpr int kSmemMax = 232448;
 
+constexpr int kLoraGroups = kStreamMaxLoraRows / kStreamMaxTokens;
+
 // Shared memory after the ring: barriers, table of groups.
 struct StreamTail {
     uint64_t full[kMaxStages], empty[kMaxStages], accf[2], acce[2], drain;
     uint32_t tmem;
     int abort_flag;
     int last;
-    int n_groups, units;
+    int units;
     StreamGroup g[kStreamMaxGroups + 1];
-    int32_t slots[kStreamMaxGroups];
+    union {
+        int32_t cnt[FP8G_MAX_ROUTED_EXPERTS];  // rows per expert
+        struct {
+            uint32_t bits[kLoraGroups][kMaxAdapters / 32];      // adapters of a group's rows
+            int32_t n[kLoraGroups];                             // slots: how many of them
+            int16_t adapter[kLoraGroups][kStreamMaxTokens];     // in rising order
+        } lora;
+    };
 };
+
+static_assert(kSmemMax - 1024 - (int)sizeof(StreamTail) >= 6 * (2 * kWTile + 16 * 128 + 2048),
+              "six stages with 16 token columns");
 
 // A CTA's part of one tile.
 struct StreamTile {
@@ -73,7 +85,7 @@ __device__ __forceinline__ bool stream_next(const StreamParams &p, const StreamT
     while (t.g[w.g + 1].unit0 <= w.u) ++w.g;
     const StreamGroup gr = t.g[w.g];
     o.g = w.g;
-    o.upt = p.ks + (EPI == kStreamOut ? t.slots[w.g] * p.kr : 0);
+    o.upt = p.ks + (EPI == kStreamOut ? t.lora.n[w.g] * p.kr : 0);
     const int32_t rel = w.u - gr.unit0;
     o.mt = rel / o.upt;
     o.k0 = rel - o.mt * o.upt;
@@ -124,6 +136,82 @@ __device__ __forceinline__ float gate_act(float g, int gate) {
     return g < 0.0f ? 0.0f : g;
 }
 
+// The groups and the number of units.  Call with all threads.
+template <int EPI>
+__device__ __forceinline__ void stream_tables(const StreamParams &p, StreamTail &t) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if constexpr (EPI == kStreamOut) {
+        const int ng = (p.n_idx + p.nb - 1) / p.nb;
+        for (int i = threadIdx.x; i < kLoraGroups * kMaxAdapters / 32; i += kSThreads)
+            t.lora.bits[0][i] = 0;
+        __syncthreads();
+        if (p.kr > 0)
+            for (int i = threadIdx.x; i < p.n_idx; i += kSThreads) {
+                const int l = __ldcg(p.idx + i);
+                if (l >= 0 && l < p.n_mat) atomicOr(&t.lora.bits[i / p.nb][l >> 5], 1u << (l & 31));
+            }
+        __syncthreads();
+        if (warp < ng) {  // lane i: adapters 32 i .. 32 i + 31 (at most 12 groups)
+            const uint32_t w = t.lora.bits[warp][lane];
+            int at = __popc(w), sum = at;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            at = sum - at;
+            for (uint32_t m = w; m != 0; m &= m - 1)
+                t.lora.adapter[warp][at++] = (int16_t)(32 * lane + __ffs((int)m) - 1);
+            if (lane == 31) t.lora.n[warp] = sum;
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            int u = 0;
+            for (int g = 0; g < ng; ++g) {
+                t.g[g] = StreamGroup{0, g * p.nb, min(p.nb, p.n_idx - g * p.nb), u};
+                u += p.mt * (p.ks + t.lora.n[g] * p.kr);
+            }
+            t.units = u;
+            t.g[ng].unit0 = 0x7FFFFFFF;
+        }
+    } else {
+        for (int e = threadIdx.x; e < p.n_mat; e += kSThreads) t.cnt[e] = 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < p.n_idx; i += kSThreads) {
+            const int e = __ldcg(p.idx + i);
+            if (e >= 0 && e < p.n_mat) atomicAdd(&t.cnt[e], 1);
+        }
+        __syncthreads();
+        if (warp == 0) {
+            const int per = p.mt * p.ks;
+            int rr = 0, gg = 0;
+            for (int e0 = 0; e0 < p.n_mat; e0 += 32) {
+                const int e = e0 + lane;
+                const int c = e < p.n_mat ? t.cnt[e] : 0, ng = (c + p.nb - 1) / p.nb;
+                int s = c, sg = ng;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, s, o), vg = __shfl_up_sync(0xffffffffu, sg, o);
+                    if (lane >= o) {
+                        s += v;
+                        sg += vg;
+                    }
+                }
+                for (int i = 0; i < ng; ++i) {
+                    const int g = gg + sg - ng + i;
+                    t.g[g] = StreamGroup{e, rr + s - c + i * p.nb, min(p.nb, c - i * p.nb), g * per};
+                }
+                rr += __shfl_sync(0xffffffffu, s, 31);
+                gg += __shfl_sync(0xffffffffu, sg, 31);
+            }
+            if (lane == 0) {
+                t.units = gg * per;
+                t.g[gg].unit0 = 0x7FFFFFFF;
+            }
+        }
+    }
+}
+
 template <int EPI>
 __global__ void __launch_bounds__(kSThreads, 1)
     stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
@@ -159,21 +247,12 @@ __global__ void __launch_bounds__(kSThreads, 1)
         ptx::tmem_alloc(ptx::smem_addr(&t.tmem), 512);
         ptx::tmem_relinquish();
     }
-    ptx::grid_dep_wait();  // global memory only after the previous kernel
-    ptx::grid_dep_launch();
-    {
-        const int ng = min(__ldcg(p.head), kStreamMaxGroups);
-        for (int i = threadIdx.x; i < ng; i += kSThreads) {
-            const int4 v = __ldcg(reinterpret_cast<const int4 *>(p.groups) + i);
-            t.g[i] = StreamGroup{v.x, v.y, v.z, v.w};
-            if constexpr (EPI == kStreamOut) t.slots[i] = __ldcg(p.slot_cnt + i);
-        }
-        if (threadIdx.x == 0) {
-            t.n_groups = ng;
-            t.units = __ldcg(p.head + 1);
-            t.g[ng].unit0 = 0x7FFFFFFF;
-        }
-    }
+    // Launched programmatically: the previous kernel, which writes the tokens'
+    // codes, may still run.  What was complete before that kernel began (it
+    // lets this one start only after its own wait), the weights and the
+    // indices, is read right away: the first stages' weights are on their way
+    // while the tokens are prepared.
+    stream_tables<EPI>(p, t);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -192,42 +271,65 @@ __global__ void __launch_bounds__(kSThreads, 1)
         // ===== TMA producer =====
         if (lane == 0) {
             const uint32_t w_tx = kWTile - kWTile / 8 * p.gap8;
-            int stage = 0;
+            // the two halves of a step's loads: weights and their scales (or an
+            // adapter's rows), tokens and theirs (or V)
+            auto weights = [&](const StreamTile &o, int k, int stage) {
+                const uint32_t fb = ptx::smem_addr(&t.full[stage]);
+                const uint32_t s0 = sbase + stage * p.stage_bytes;
+                const uint32_t nw = o.has1 ? 2 : 1;
+                if (EPI != kStreamOut || k < p.ks) {
+                    ptx::mbar_arrive_expect_tx(fb, nw * (w_tx + 512u) + o.n16 * 128u + 512u);
+                    const int64_t c0 = ((int64_t)o.mat0 * p.ks + k) * p.n_rt + o.w0 / 128;
+                    ptx::tma_load_3d(s0, &tmW, fb, k * kBK, o.w0, o.mat0);
+                    ptx::bulk_load(s0 + off_sf, p.sfw + c0 * 512, 512, fb);
+                    if (o.has1) {
+                        const int64_t c1 = ((int64_t)o.mat1 * p.ks + k) * p.n_rt + o.w1 / 128;
+                        ptx::tma_load_3d(s0 + kWTile, &tmW, fb, k * kBK, o.w1, o.mat1);
+                        ptx::bulk_load(s0 + off_sf + 512, p.sfw + c1 * 512, 512, fb);
+                    }
+                } else {
+                    const int ls = k - p.ks, sl = ls / p.kr, c = (ls - sl * p.kr) * 64;
+                    const int l = t.lora.adapter[o.g][sl];
+                    ptx::mbar_arrive_expect_tx(fb, nw * kWTile + 2 * o.n16 * 128u);
+                    ptx::tma_load_3d(s0, &tmB, fb, c, o.w0, l);
+                    if (o.has1) ptx::tma_load_3d(s0 + kWTile, &tmB, fb, c, o.w1, l);
+                }
+            };
+            auto tokens = [&](const StreamTile &o, int k, int stage) {
+                const uint32_t fb = ptx::smem_addr(&t.full[stage]);
+                const uint32_t s0 = sbase + stage * p.stage_bytes;
+                if (EPI != kStreamOut || k < p.ks) {
+                    ptx::bulk_load(s0 + off_sf + 1024, p.sfx + ((int64_t)o.g * p.ks + k) * 512, 512, fb);
+                    for (int i = 0; i < o.n16; i += 16)
+                        ptx::tma_load_2d(s0 + off_x + i * 128, &tmX, fb, k * kBK, o.row0 + i);
+                } else {
+                    const int ls = k - p.ks, sl = ls / p.kr, c = (ls - sl * p.kr) * 64;
+                    const int v0 = (o.g * p.slot_cap + sl) * 2 * p.nb;
+                    for (int i = 0; i < o.n16; i += 16) {
+                        ptx::tma_load_2d(s0 + off_x + i * 128, &tmV, fb, c, v0 + i);
+                        ptx::tma_load_2d(s0 + off_x + (p.nb + i) * 128, &tmV, fb, c, v0 + p.nb + i);
+                    }
+                }
+            };
+            // the ring's first fill: weights before the wait, tokens after it
+            int ahead = 0;
+            {
+                StreamWalk w2 = walk;
+                while (ahead < p.stages && stream_next<EPI>(p, t, w2, ti))
+                    for (int k = ti.k0; k < ti.k1 && ahead < p.stages; ++k) weights(ti, k, ahead++);
+            }
+            ptx::grid_dep_wait();
+            ptx::grid_dep_launch();
+            int stage = 0, done = 0;
             uint32_t phase = 0;
             while (stream_next<EPI>(p, t, walk, ti)) {
-                for (int k = ti.k0; k < ti.k1; ++k) {
-                    if (!wait_bar(ptx::smem_addr(&t.empty[stage]), phase ^ 1u, abort_flag, p, stage))
-                        goto roles_done;
-                    const uint32_t fb = ptx::smem_addr(&t.full[stage]);
-                    const uint32_t s0 = sbase + stage * p.stage_bytes;
-                    const uint32_t nw = ti.has1 ? 2 : 1;
-                    if (EPI != kStreamOut || k < p.ks) {
-                        ptx::mbar_arrive_expect_tx(fb, nw * (w_tx + 512u) + ti.n16 * 128u + 512u);
-                        const int64_t c0 = ((int64_t)ti.mat0 * p.ks + k) * p.n_rt + ti.w0 / 128;
-                        ptx::tma_load_3d(s0, &tmW, fb, k * kBK, ti.w0, ti.mat0);
-                        ptx::bulk_load(s0 + off_sf, p.sfw + c0 * 512, 512, fb);
-                        if (ti.has1) {
-                            const int64_t c1 = ((int64_t)ti.mat1 * p.ks + k) * p.n_rt + ti.w1 / 128;
-                            ptx::tma_load_3d(s0 + kWTile, &tmW, fb, k * kBK, ti.w1, ti.mat1);
-                            ptx::bulk_load(s0 + off_sf + 512, p.sfw + c1 * 512, 512, fb);
-                        }
-                        ptx::bulk_load(s0 + off_sf + 1024, p.sfx + ((int64_t)ti.g * p.ks + k) * 512, 512,
-                                       fb);
-                        for (int i = 0; i < ti.n16; i += 16)
-                            ptx::tma_load_2d(s0 + off_x + i * 128, &tmX, fb, k * kBK, ti.row0 + i);
-                    } else {
-                        const int ls = k - p.ks, sl = ls / p.kr, c = (ls - sl * p.kr) * 64;
-                        const int slot = ti.g * p.slot_cap + sl;
-                        const int l = __ldcg(p.slot_adapter + slot);
-                        const int v0 = slot * 2 * p.nb;
-                        ptx::mbar_arrive_expect_tx(fb, nw * kWTile + 2 * ti.n16 * 128u);
-                        ptx::tma_load_3d(s0, &tmB, fb, c, ti.w0, l);
-                        if (ti.has1) ptx::tma_load_3d(s0 + kWTile, &tmB, fb, c, ti.w1, l);
-                        for (int i = 0; i < ti.n16; i += 16) {
-                            ptx::tma_load_2d(s0 + off_x + i * 128, &tmV, fb, c, v0 + i);
-                            ptx::tma_load_2d(s0 + off_x + (p.nb + i) * 128, &tmV, fb, c, v0 + p.nb + i);
-                        }
+                for (int k = ti.k0; k < ti.k1; ++k, ++done) {
+                    if (done >= ahead) {
+                        if (!wait_bar(ptx::smem_addr(&t.empty[stage]), phase ^ 1u, abort_flag, p, stage))
+                            goto roles_done;
+                        weights(ti, k, stage);
                     }
+                    tokens(ti, k, stage);
                     if (++stage == p.stages) {
                         stage = 0;
                         phase ^= 1u;
@@ -297,6 +399,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
         }
     } else if (warp >= kSEpiWarp0) {
         // ===== epilogue =====
+        ptx::grid_dep_wait();  // counters, partials and outputs: after the previous kernel
         const int q = warp & 3, half = (warp - kSEpiWarp0) >> 2;
         const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16);
         const int row_l = q * 32 + lane;  // weight row within a tile

@@ -13,7 +13,9 @@ struct StreamGroup {
     int32_t unit0;  // work units of the groups before it
 };
 
-constexpr int kStreamMaxGroups = 352;
+constexpr int kStreamMaxGroups = 320;
+constexpr int kStreamMaxLoraRows = 512;  // token rows of a call with low-rank steps
+constexpr int kMaxAdapters = 1024;
 constexpr int kStreamMaxTokens = 128;  // token rows of a group
 constexpr int kStreamMinUnits = 4;     // work units a CTA takes at least
 
@@ -35,8 +37,11 @@ struct StreamParams {
     int32_t gap8;    // eighths of a weight tile a packed load does not deliver
     const uint8_t *sfw;      // packed weight scales [matrix][ks][n_rt][512]
     const uint8_t *sfx;      // packed token scales [group][ks][512]
-    const int32_t *head;     // [0] groups, [1] work units
-    const StreamGroup *groups;
+    // the groups, which every CTA derives from its call's routing: `n_idx`
+    // indices idx[]: expert of each pair (negative or >= n_mat: none), or
+    // (kStreamOut) adapter of each token row
+    const int32_t *idx;
+    int32_t n_idx, n_mat;
     int32_t *tile_cnt;       // [group][mt] units done of split tiles, zero at the start
     float *part;             // partial tiles [2 grid][2][nb][128]
     unsigned int *status;
@@ -51,9 +56,9 @@ struct StreamParams {
     void *c;                 // [tokens][rows]
     int32_t out_f32;
     const float *bias;
-    int32_t rank, kr, slot_cap;      // low-rank: rank, 64-wide steps per slot, slots per group
-    const int32_t *slot_cnt;         // [group]
-    const int32_t *slot_adapter;     // [group][slot_cap]
+    // low-rank: rank, 64-wide steps per slot (0: none), slots per group (V's
+    // rows of slot s of group g begin at (g slot_cap + s) 2 nb); n_mat adapters
+    int32_t rank, kr, slot_cap;
 };
 
 // Ring and accumulator sizes for nb token columns; lora: V's two halves share

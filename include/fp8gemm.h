@@ -568,6 +568,39 @@ FP8G_API fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t
                                    int32_t w_fmt, int32_t gate, int64_t T, int32_t k, int32_t E,
                                    int64_t H, int64_t F, cudaStream_t stream);
 
+/* Limits of fp8_gemm_lora: adapters of a call, their rank. */
+#define FP8G_MAX_ADAPTERS 1024
+#define FP8G_MAX_LORA_RANK 256
+
+/*
+ * Block-scaled projection with low-rank adapters of many requests beside it
+ * [JAX-BW microscaling paragraph for the projection; the pages have no
+ * adapters].  With Q the E4M3 quantisation of fp8g_quantize (block 32) and
+ * l = adapter[i]:
+ *   C[i] = out( Q(x_i) . W^T + bias + alpha[l] B_l (A_l x_i) )
+ * one fp32 sum, rounded once; the last term, from the unquantised x_i, is left
+ * out where l < 0 (l >= L too, recorded as FP8G_ERR_INVALID_ARG, detail i).
+ * x: fp32 or bf16 (x_dtype) [M, K]; W [N, K]: codes of format w_fmt (packed
+ * formats as in fp8g_format), sfw their scales from fp8g_pack_scales (one
+ * matrix); lora_a: bf16 [L, r, K]; lora_b: bf16 [L, N, r]; alpha: fp32 [L] or
+ * null (1); adapter: device int32 [M]; bias: fp32 [N] or null; C: [M, N] bf16
+ * or fp32 per `out`.  Adapters of smaller rank are padded with zeros to r.
+ * alpha A x is held to 16 significant bits (two bf16 halves) for the product
+ * with B, an fp32 x to as many for the product with A; sums are fp32.
+ * K % 32 == 0 (packed formats 128), r % 8 == 0, L <= FP8G_MAX_ADAPTERS, r <=
+ * FP8G_MAX_LORA_RANK, else FP8G_ERR_UNSUPPORTED_SHAPE; L = 0: no adapters
+ * (lora_a, lora_b, adapter unused, may be null); M may be 0.  x, W (packed
+ * formats 32), sfw, lora_a, lora_b, C 16-byte aligned, N * sizeof(out element)
+ * % 16 == 0, else FP8G_ERR_ALIGNMENT.  Results do not vary between runs.  Two
+ * kernels and one temporary from the library's pool of about M K + 4 M
+ * min(L, 256) max(r, 64) bytes.
+ */
+FP8G_API fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void *W, const uint8_t *sfw,
+                                   int32_t w_fmt, const void *lora_a, const void *lora_b,
+                                   const float *alpha, const int32_t *adapter, int32_t L, int32_t r,
+                                   const float *bias, void *C, int out, int64_t M, int64_t N,
+                                   int64_t K, cudaStream_t stream);
+
 /*
  * Synchronises `stream`, then returns and clears the current device's status
  * word (FP8G_OK if no kernel recorded an error since the last call).
