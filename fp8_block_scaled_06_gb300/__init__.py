@@ -91,6 +91,8 @@ def build(force: bool = False) -> str:
 def load():
     """Load libfp8g.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -199,6 +201,11 @@ def _ptr(x):
 def _stream(stream):
     if stream is None:
         import torch
+        # the raw handle without a Stream object around it (0.2 against 2.9 us
+        # on the GB300 host, a third of a small call)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None and torch.cuda.is_initialized():
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -501,6 +508,11 @@ def gemm(A, B, sa, sb, out: str = "bf16", block: bool = True, stream=None):
     return C
 
 
+def _packed_bytes(matrices: int, rows: int, K: int) -> int:
+    """fp8g_packed_scale_bytes, without the call."""
+    return matrices * (-(-rows // 128)) * (-(-K // 128)) * 512
+
+
 def pack_scales(sf, stream=None):
     """Block scales fp32 [rows, K/32] or [matrices, rows, K/32] -> the packed
     uint8 [(matrices,) ceil(K/128), ceil(rows/128), 512] that moe_layer and
@@ -522,23 +534,27 @@ def moe_route(logits, k: int, score: int = FP8G_SCORE_SOFTMAX_TOPK, scale: float
     with `ordered` also (counts [E], rows [T k], slots [T k]), the row order of the
     grouped GEMM (its counts, rows and c_row_of)."""
     import torch
-    assert logits.is_cuda and logits.dim() == 2
-    assert logits.dtype in (torch.float32, torch.bfloat16)
+    bf16 = logits.dtype == torch.bfloat16
+    assert logits.is_cuda and (bf16 or logits.dtype == torch.float32)
     T, E = logits.shape
-    if E > 1 and logits.stride(1) != 1 or T > 1 and logits.stride(0) < E:
+    ld, step = logits.stride()
+    if E > 1 and step != 1 or T > 1 and ld < E:
         logits = logits.contiguous()
-    ld = logits.stride(0) if T > 1 else E
-    dev = logits.device
-    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        ld = E
+    elif T <= 1:
+        ld = E
+    dev, i32 = logits.device, torch.int32
+    ids = torch.empty((T, k), dtype=i32, device=dev)
     w = torch.empty((T, k), dtype=torch.float32, device=dev)
-    order = ()
-    if ordered:
-        order = (torch.empty((E,), dtype=torch.int32, device=dev),
-                 torch.empty((T * k,), dtype=torch.int32, device=dev),
-                 torch.empty((T * k,), dtype=torch.int32, device=dev))
-    dt = FP8G_IN_BF16 if logits.dtype == torch.bfloat16 else FP8G_IN_F32
-    fp8g_moe_route(logits, dt, ld, T, E, k, score, scale, ids, w, *order, stream=stream)
-    return (ids, w) + order
+    dt = FP8G_IN_BF16 if bf16 else FP8G_IN_F32
+    if not ordered:
+        fp8g_moe_route(logits, dt, ld, T, E, k, score, scale, ids, w, stream=stream)
+        return ids, w
+    counts = torch.empty(E, dtype=i32, device=dev)
+    rows = torch.empty(T * k, dtype=i32, device=dev)
+    slots = torch.empty(T * k, dtype=i32, device=dev)
+    fp8g_moe_route(logits, dt, ld, T, E, k, score, scale, ids, w, counts, rows, slots, stream)
+    return ids, w, counts, rows, slots
 
 
 def moe_layer(x, ids, weights, W13, sf13, W2, sf2, w_fmt: int = FP8G_E4M3,
@@ -548,23 +564,22 @@ def moe_layer(x, ids, weights, W13, sf13, W2, sf2, w_fmt: int = FP8G_E4M3,
     sf13 / sf2 from pack_scales (sf13 of W13's scales viewed as [2E, F, H/32]).
     Allocates the output [T, H]."""
     import torch
-    assert x.is_cuda and x.dim() == 2 and x.dtype in (torch.float32, torch.bfloat16)
+    bf16 = x.dtype == torch.bfloat16
+    assert x.is_cuda and (bf16 or x.dtype == torch.float32)
     assert ids.dtype == torch.int32 and weights.dtype == torch.float32
-    assert ids.shape == weights.shape and ids.dim() == 2 and ids.shape[0] == x.shape[0]
-    assert W13.dim() == 3 and W2.dim() == 3 and W13.is_contiguous() and W2.is_contiguous()
     T, H = x.shape
     k = ids.shape[1]
     E, F = W13.shape[0], W13.shape[1] // 2
-    assert W13.shape == (E, 2 * F, packed_cols(H, w_fmt))
-    assert W2.shape == (E, H, packed_cols(F, w_fmt))
-    assert sf13.numel() == fp8g_packed_scale_bytes(2 * E, F, H)
-    assert sf2.numel() == fp8g_packed_scale_bytes(E, H, F)
+    assert ids.shape == (T, k) == weights.shape
+    assert W13.shape == (E, 2 * F, packed_cols(H, w_fmt)) and W13.is_contiguous()
+    assert W2.shape == (E, H, packed_cols(F, w_fmt)) and W2.is_contiguous()
+    assert sf13.numel() == _packed_bytes(2 * E, F, H) and sf2.numel() == _packed_bytes(E, H, F)
     x, ids, weights = x.contiguous(), ids.contiguous(), weights.contiguous()
     o = torch.empty((T, H), dtype=torch.bfloat16 if out == "bf16" else torch.float32,
                     device=x.device)
-    fp8_moe_layer(x, FP8G_IN_BF16 if x.dtype == torch.bfloat16 else FP8G_IN_F32, ids, weights, W13,
-                  sf13, W2, sf2, o, FP8G_OUT_BF16 if out == "bf16" else FP8G_OUT_F32, w_fmt, gate,
-                  T, k, E, H, F, stream)
+    fp8_moe_layer(x, FP8G_IN_BF16 if bf16 else FP8G_IN_F32, ids, weights, W13, sf13, W2, sf2, o,
+                  FP8G_OUT_BF16 if out == "bf16" else FP8G_OUT_F32, w_fmt, gate, T, k, E, H, F,
+                  stream)
     return o
 
 
@@ -574,20 +589,21 @@ def gemm_lora(x, W, sfw, lora_a, lora_b, alpha, adapter, bias=None, w_fmt: int =
     w_fmt, sfw from pack_scales, lora_a bf16 [L, r, K], lora_b bf16 [L, N, r],
     alpha fp32 [L] or None, adapter int32 [M] (negative: none).  Allocates C [M, N]."""
     import torch
-    assert x.is_cuda and x.dim() == 2 and x.dtype in (torch.float32, torch.bfloat16)
-    assert W.dim() == 2 and W.is_contiguous() and adapter.dtype == torch.int32
+    bf16 = x.dtype == torch.bfloat16
+    assert x.is_cuda and (bf16 or x.dtype == torch.float32)
     assert lora_a.dtype == torch.bfloat16 and lora_b.dtype == torch.bfloat16
     M, K = x.shape
     N = W.shape[0]
-    L, r = lora_a.shape[:2]
-    assert W.shape[1] == packed_cols(K, w_fmt) and adapter.shape == (M,)
+    L, r, _ = lora_a.shape
+    assert W.shape == (N, packed_cols(K, w_fmt)) and W.is_contiguous()
+    assert adapter.dtype == torch.int32 and adapter.shape == (M,)
     assert lora_a.shape == (L, r, K) and lora_b.shape == (L, N, r)
-    assert sfw.numel() == fp8g_packed_scale_bytes(1, N, K)
+    assert sfw.numel() == _packed_bytes(1, N, K)
     x, adapter = x.contiguous(), adapter.contiguous()
     lora_a, lora_b = lora_a.contiguous(), lora_b.contiguous()
     C = torch.empty((M, N), dtype=torch.bfloat16 if out == "bf16" else torch.float32,
                     device=x.device)
-    fp8_gemm_lora(x, FP8G_IN_BF16 if x.dtype == torch.bfloat16 else FP8G_IN_F32, W, sfw, w_fmt,
-                  lora_a, lora_b, alpha, adapter, L, r, bias, C,
-                  FP8G_OUT_BF16 if out == "bf16" else FP8G_OUT_F32, M, N, K, stream)
+    fp8_gemm_lora(x, FP8G_IN_BF16 if bf16 else FP8G_IN_F32, W, sfw, w_fmt, lora_a, lora_b, alpha,
+                  adapter, L, r, bias, C, FP8G_OUT_BF16 if out == "bf16" else FP8G_OUT_F32, M, N, K,
+                  stream)
     return C

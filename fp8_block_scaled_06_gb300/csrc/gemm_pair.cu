@@ -190,10 +190,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ LoraArg<LORA> la) {
     using PC = PairCfg<MODE, F4>;
     static_assert(!LORA || (MODE == kModeBlock && F4 == 0), "low-rank steps: block-scaled FP8-rate");
-    // Low-rank steps of a tile, after its num_kb FP8 steps: step ls is 64-wide
-    // step ls / 2 % kr of slot ls / (2 kr), first half of V, then second
+    // Low-rank steps of a tile, after its num_kb FP8 steps: halves * kr per
+    // slot; of a 64-wide step's two halves of V (halves 2) the hi one first
     auto lora_steps = [&](const int32_t pm) -> int {
-        if constexpr (LORA) return 2 * la.p.kr * __ldcg(la.p.slots + pm);
+        if constexpr (LORA) return la.p.halves * la.p.kr * __ldcg(la.p.slots + pm);
         return 0;
     };
     extern __shared__ uint8_t smem_raw[];
@@ -306,12 +306,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t fb = leader ? bar_full(stage) : ptx::map_shared(bar_full(stage), 0);
                     if constexpr (LORA) {
                         if (kb >= p.num_kb) {
-                            const int ls = kb - p.num_kb, sl = ls / (2 * la.p.kr);
-                            const int c = (ls / 2 - sl * la.p.kr) * 64;
+                            const int hv = la.p.halves, ls = kb - p.num_kb, sl = ls / (hv * la.p.kr);
+                            const int c = (ls / hv - sl * la.p.kr) * 64;
                             const int slot = ti.pm * la.p.cap + sl;
                             if (leader) ptx::mbar_arrive_expect_tx(fb, 2 * (kA + kB));
                             ptx::tma_load_2d_pair(sbase + PC::OFF_A + stage * kA, &la.p.V, fb, c,
-                                                  (2 * slot + (ls & 1)) * 256 + (int32_t)rank * kBM);
+                                                  (hv * slot + ls % hv) * 256 + (int32_t)rank * kBM);
                             ptx::tma_load_3d_pair(sbase + PC::OFF_B + stage * kB, &la.p.B, fb, c, nb0,
                                                   __ldcg(la.p.adapters + slot));
                             if (++stage == PC::STAGES) {
@@ -391,12 +391,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t b0 = sbase + PC::OFF_B + stage * kB;
                     if (LORA && kb >= p.num_kb) {
                         if constexpr (LORA) {
-                            const int c = (kb - p.num_kb) / 2 % la.p.kr * 64;
+                            const int hv = la.p.halves, c = (kb - p.num_kb) / hv % la.p.kr * 64;
                             const int nk = (min(64, la.p.rank - c) + 15) / 16;
-                            for (int k = 0; k < nk; ++k)
-                                ptx::mma_bf16_pair(d_tmem, ptx::desc_kmajor_sw128(a0 + k * 32),
-                                                   ptx::desc_kmajor_sw128(b0 + k * 32),
-                                                   ptx::idesc_bf16(2 * kBM, kPairBN), 1u);
+                            // both halves in a row: the lo one 64 bytes on, against the same rows
+                            for (int h = hv; h < 3; ++h)
+                                for (int k = 0; k < nk; ++k)
+                                    ptx::mma_bf16_pair(d_tmem,
+                                                       ptx::desc_kmajor_sw128(a0 + (h - hv) * 64 + k * 32),
+                                                       ptx::desc_kmajor_sw128(b0 + k * 32),
+                                                       ptx::idesc_bf16(2 * kBM, kPairBN), 1u);
                         }
                     } else if constexpr (F4 == 2) {
                         // MMA k: K elements 64k .. 64k + 63 = K group k's four

@@ -105,14 +105,14 @@ cudaError_t launch_gemm_promote(bool out_f32, const GemmMaps &maps, const GemmPa
                                 cudaStream_t stream);
 
 // Low-rank steps of the block-scaled CTA-pair kernel: after a tile's FP8 steps,
-// 2 kr bf16 steps per slot of its 256 rows (V's two halves against the
-// adapter's rows; lora.cu).
+// halves * kr bf16 steps per slot of its 256 rows (V against the adapter's
+// rows; lora.cu).  halves 1: both halves of V in a row (LoraV in stream.h).
 struct PairLora {
-    CUtensorMap V;  // bf16 rows: half h of row i of slot s of row tile t at ((t cap + s) 2 + h) 256 + i
+    CUtensorMap V;  // bf16 rows: block h of row i of slot s of row tile t at ((t cap + s) halves + h) 256 + i
     CUtensorMap B;  // bf16 [adapter][N][rank]
     const int32_t *slots;     // [row tile]
     const int32_t *adapters;  // [row tile][cap]
-    int32_t cap, rank, kr;
+    int32_t cap, rank, kr, halves;
 };
 
 // gemm_pair.cu (per-tensor and block-scaled, CTA pairs); lora: block-scaled only

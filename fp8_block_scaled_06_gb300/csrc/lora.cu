@@ -41,11 +41,12 @@ struct LoraPrep {
     const __nv_bfloat16 *a;   // [L][r][K]
     const float *alpha;       // [L] or null
     const int32_t *adapter;   // [M]
-    int32_t L, r, r64;        // r64: V's row length, r rounded up to 64
+    int32_t L, r, r64, wide;  // LoraV: V's row length, halves in rows of their own
     int32_t tile, cap, tiles;
-    __nv_bfloat16 *v;         // [tiles][cap][2][tile][r64]
+    __nv_bfloat16 *v;         // [tiles][cap][halves][tile][r64]
     int32_t *slot_cnt, *slot_adapter;  // tables of the pair kernel, or null
     int32_t items;            // blocks per tile and rank block of the low-rank part
+    int32_t low_blocks;       // blocks of the low-rank part
     unsigned int *status;
 };
 
@@ -84,15 +85,47 @@ __device__ __forceinline__ uint4 x_pairs(const void *x, int64_t off, bool in) {
     }
 }
 
-// Blocks [0, M): quantise row blockIdx.x.  The rest: the low-rank part, block
-// (tile, rank block of 16, item): items are the pairs (slot, 16 of the slot's
-// rows) in order.  The K range goes over the block's warps (bound by the
+// Row blk of x: codes, scale bytes; with the counters to zero shared out.
+template <bool BF16>
+__device__ __forceinline__ void quantise_row(const LoraPrep &p, int blk) {
+    const int tid = threadIdx.x, nt = blockDim.x;
+    for (int i = blk * nt + tid; i < p.n_cnt; i += p.M * nt) p.cnt[i] = 0;
+    const int rt = blk / p.sf_rows, in_t = blk - rt * p.sf_rows;
+    const int groups = p.ks * 16;
+    for (int c0 = 0; c0 < groups; c0 += nt) {
+        const int c = c0 + tid;
+        float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
+        const bool in = c * 8 < p.K;
+        if (in) load8<BF16>(p.x, (int64_t)blk * p.K + c * 8, v0, v1);
+        float am = absmax8(v0, v1);
+        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+        const float s = pow2_scale<0>(am);
+        if (in)
+            *reinterpret_cast<uint2 *>(p.xq + (int64_t)blk * p.K + c * 8) = quant8_pow2<0>(v0, v1, s);
+        if (c < groups && (c & 3) == 0)
+            p.xsf[(c >> 4) * p.sf_k + rt * p.sf_t + 16 * (in_t & 31) + 4 * (in_t >> 5) + ((c >> 2) & 3)] =
+                (uint8_t)(__float_as_uint(s) >> 23);
+    }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(256) lora_quant_kernel(const __grid_constant__ LoraPrep p) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    quantise_row<BF16>(p, blockIdx.x);
+}
+
+// Blocks below p.low_blocks: the low-rank part, block (tile, rank block of 16,
+// item): items are the pairs (slot, 16 of the slot's rows) in order.  The
+// blocks after them quantise a row each (the low-rank blocks take longer, so
+// they come first).  The K range goes over the block's warps (bound by the
 // latency of its loads: 16 warps with their loads of up to 128 K each in
 // flight), each a 16 x 16 product by mma.sync, joined in shared memory in warp
 // order.  A lane's 16-byte load covers 8 consecutive K of a row; the same K
 // permutation on both operands leaves the product unchanged.
 template <bool BF16>
-__global__ void __launch_bounds__(kLThreads) lora_prep_kernel(LoraPrep p) {
+__global__ void __launch_bounds__(kLThreads) lora_prep_kernel(const __grid_constant__ LoraPrep p) {
     __shared__ int32_t ad[kMaxTile];
     __shared__ int32_t cnt[kMaxAdapters];
     __shared__ int32_t pick[3];  // adapter, slot, first of its rows
@@ -102,30 +135,13 @@ __global__ void __launch_bounds__(kLThreads) lora_prep_kernel(LoraPrep p) {
     const int blk = blockIdx.x;
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    if (blk < p.M) {
-        for (int i = blk * kLThreads + tid; i < p.n_cnt; i += p.M * kLThreads) p.cnt[i] = 0;
-        const int rt = blk / p.sf_rows, in_t = blk - rt * p.sf_rows;
-        const int groups = p.ks * 16;
-        for (int c0 = 0; c0 < groups; c0 += kLThreads) {
-            const int c = c0 + tid;
-            float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
-            const bool in = c * 8 < p.K;
-            if (in) load8<BF16>(p.x, (int64_t)blk * p.K + c * 8, v0, v1);
-            float am = absmax8(v0, v1);
-            am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
-            am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-            const float s = pow2_scale<0>(am);
-            if (in)
-                *reinterpret_cast<uint2 *>(p.xq + (int64_t)blk * p.K + c * 8) = quant8_pow2<0>(v0, v1, s);
-            if (c < groups && (c & 3) == 0)
-                p.xsf[(c >> 4) * p.sf_k + rt * p.sf_t + 16 * (in_t & 31) + 4 * (in_t >> 5) + ((c >> 2) & 3)] =
-                    (uint8_t)(__float_as_uint(s) >> 23);
-        }
+    if (blk >= p.low_blocks) {
+        quantise_row<BF16>(p, blk - p.low_blocks);
         return;
     }
     // ------------------------------------------------------- low-rank part
     const int rblocks = (p.r + 15) / 16;
-    int w = blk - p.M;
+    int w = blk;
     const int item = w % p.items;
     w /= p.items;
     const int rb = w % rblocks, tile = w / rblocks;
@@ -186,10 +202,11 @@ __global__ void __launch_bounds__(kLThreads) lora_prep_kernel(LoraPrep p) {
     __syncthreads();
     const int l = pick[0];
     if (l < 0) return;
-    __nv_bfloat16 *hi = p.v + ((int64_t)(tile * p.cap + pick[1]) * 2 * p.tile) * p.r64 + rb * 16;
-    const int64_t half = (int64_t)p.tile * p.r64;
+    __nv_bfloat16 *hi =
+        p.v + ((int64_t)(tile * p.cap + pick[1]) * (p.wide ? 2 : 1) * p.tile) * p.r64 + rb * 16;
+    const int64_t half = p.wide ? (int64_t)p.tile * p.r64 : 32;
     // zero rows of the other adapters (the slot's first item), and the columns
-    // past the rank up to r64 (its first rank block)
+    // past the rank (its first rank block)
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
     if (pick[2] == 0)
         for (int i = tid; i < p.tile; i += kLThreads) {
@@ -197,7 +214,7 @@ __global__ void __launch_bounds__(kLThreads) lora_prep_kernel(LoraPrep p) {
             uint4 *e = reinterpret_cast<uint4 *>(hi + half + (int64_t)i * p.r64);
             if (ad[i] != l) d[0] = d[1] = e[0] = e[1] = z;
             if (rb == 0)
-                for (int c = 2 * rblocks; c < p.r64 / 8; ++c) d[c] = e[c] = z;
+                for (int c = 2 * rblocks; c < (p.wide ? p.r64 : 32) / 8; ++c) d[c] = e[c] = z;
         }
     // this lane's x rows (g, g + 8) and adapter rows (ranks g, g + 8 of the block)
     const int g = lane >> 2, c8 = 8 * (lane & 3);
@@ -313,16 +330,17 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
     const int nb = pair ? 256 : (int)(M < kStreamMaxTokens ? (M + 15) / 16 * 16 : kStreamMaxTokens);
     const int tiles = (int)((M + nb - 1) / nb);
     const int32_t ks = (int32_t)((K + 127) / 128), n_rt = (int32_t)((N + 127) / 128);
-    const int cap = L < nb ? L : nb, r64 = lora ? (r + 63) / 64 * 64 : 64;
+    const int cap = L < nb ? L : nb;
+    const LoraV lv(lora ? r : 1);
     const int32_t n_rtA = (int32_t)((M + 127) / 128);
     StreamParams sp{};
     if (!pair) {
-        stream_sizes(sp, nb, lora);
+        stream_sizes(sp, nb, lv.halves);
         sp.mt = (int32_t)((N + 255) / 256);
         sp.ks = ks;
         sp.rows = (int32_t)N;
         sp.n_rt = n_rt;
-        sp.kr = lora ? r64 / 64 : 0;
+        sp.kr = lora ? lv.kr : 0;
         if ((int64_t)tiles * sp.mt * (ks + (int64_t)cap * sp.kr) >= INT32_MAX)
             return FP8G_ERR_UNSUPPORTED_SHAPE;
     }
@@ -335,7 +353,7 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
         return o;
     };
     const size_t o_xq = take((size_t)M * K), o_xsf = take((size_t)(pair ? n_rtA : tiles) * ks * 512);
-    const size_t o_v = take((size_t)tiles * cap * 2 * nb * r64 * 2);
+    const size_t o_v = take((size_t)tiles * cap * lv.halves * nb * lv.r64 * 2);
     const int n_cnt = pair ? 0 : tiles * sp.mt;
     const size_t o_cnt = take((size_t)n_cnt * 4);
     const size_t o_part = take(pair ? 0 : stream_part_bytes(sp, d.num_sms));
@@ -363,7 +381,8 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
     a.adapter = adapter;
     a.L = L;
     a.r = r;
-    a.r64 = r64;
+    a.r64 = lv.r64;
+    a.wide = lv.wide;
     a.tile = nb;
     a.cap = cap;
     a.tiles = tiles;
@@ -375,18 +394,26 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
     // at most one partly filled item per slot beside the whole ones
     a.items = nb / 16 + cap;
     a.status = d.status;
-    const int64_t blocks = M + (lora ? (int64_t)tiles * ((r + 15) / 16) * a.items : 0);
-    cudaError_t e = blocks >= INT32_MAX ? cudaErrorInvalidValue
-                    : x_dtype == FP8G_IN_BF16
-                        ? launch_programmatic(lora_prep_kernel<true>, dim3((unsigned)blocks), dim3(kLThreads),
-                                              stream, a)
-                        : launch_programmatic(lora_prep_kernel<false>, dim3((unsigned)blocks),
-                                              dim3(kLThreads), stream, a);
+    const int64_t low = lora ? (int64_t)tiles * ((r + 15) / 16) * a.items : 0;
+    a.low_blocks = (int32_t)low;
+    cudaError_t e = low + M >= INT32_MAX ? cudaErrorInvalidValue : cudaSuccess;
+    const bool bf16 = x_dtype == FP8G_IN_BF16;
+    // Many rows: the rows in blocks of their own, with few registers (beside
+    // the low-rank part's, one block of 512 threads fills an SM).
+    const bool apart = pair || !lora;
+    if (e == cudaSuccess && apart)
+        e = bf16 ? launch_programmatic(lora_quant_kernel<true>, dim3((unsigned)M), dim3(256), stream, a)
+                 : launch_programmatic(lora_quant_kernel<false>, dim3((unsigned)M), dim3(256), stream, a);
+    if (e == cudaSuccess && lora) {
+        const unsigned blocks = (unsigned)(low + (apart ? 0 : M));
+        e = bf16 ? launch_programmatic(lora_prep_kernel<true>, dim3(blocks), dim3(kLThreads), stream, a)
+                 : launch_programmatic(lora_prep_kernel<false>, dim3(blocks), dim3(kLThreads), stream, a);
+    }
     CUtensorMap mb{}, mv{};
     if (e == cudaSuccess && lora) {
         const uint64_t db[3] = {(uint64_t)r, (uint64_t)N, (uint64_t)L};
         const uint32_t bb[3] = {64u, 128u, 1u};
-        const uint64_t dv[2] = {(uint64_t)r64, (uint64_t)tiles * cap * 2 * nb};
+        const uint64_t dv[2] = {(uint64_t)lv.r64, (uint64_t)tiles * cap * lv.halves * nb};
         const uint32_t bv[2] = {64u, pair ? 128u : 16u};
         st = host_bf16_map(lora_b, 3, db, bb, d.dev, mb);
         if (st == FP8G_OK) st = host_bf16_map(a.v, 2, dv, bv, d.dev, mv);
@@ -416,6 +443,7 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
         sp.bias = bias;
         sp.rank = r;
         sp.slot_cap = cap;
+        sp.v_rows = lv.halves * nb;
         if (st == FP8G_OK) e = launch_stream(kStreamOut, mw, mx, mb, mv, sp, d.num_sms, stream);
     } else if (e == cudaSuccess && st == FP8G_OK) {
         PairLora pl{};
@@ -426,7 +454,8 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
             pl.adapters = a.slot_adapter;
             pl.cap = cap;
             pl.rank = r;
-            pl.kr = r64 / 64;
+            pl.kr = lv.kr;
+            pl.halves = lv.halves;
         }
         st = run_pair_packed(a.xq, a.xsf, W, sfw, w_fmt, bias, C, out, M, N, K, lora ? &pl : nullptr, stream);
     }

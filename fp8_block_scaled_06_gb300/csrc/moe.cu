@@ -266,8 +266,8 @@ fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t *ids, co
     // groups: each expert's rows in tiles of nb
     const int max_groups = (int)((E < R ? E : R) + R / nb);
     StreamParams p1{}, p2{};
-    stream_sizes(p1, nb, false);
-    stream_sizes(p2, nb, false);
+    stream_sizes(p1, nb, 1);
+    stream_sizes(p2, nb, 1);
     p1.mt = (int32_t)((F + 127) / 128);
     p1.ks = (int32_t)((H + 127) / 128);
     p1.rows = (int32_t)F;

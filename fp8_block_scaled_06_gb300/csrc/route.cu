@@ -30,6 +30,7 @@ namespace {
 
 constexpr int kWarps = 32;
 constexpr int kTokensPerBlock = 256;
+constexpr int kQuadTokens = 32;  // more tokens than this: four lanes a token
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float((int)0xFF800000u); }
 
@@ -137,6 +138,90 @@ __device__ __forceinline__ int route_token(const RouteArgs &a, int t, int lane) 
     return mine;
 }
 
+__device__ __forceinline__ uint64_t umax64(uint64_t a, uint64_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint64_t umin64(uint64_t a, uint64_t b) { return a > b ? b : a; }
+
+// Four lanes take a token: lane q the experts q, q + 4, ...  Each keeps its
+// K best as a descending list of (key, ~expert) words, a new one passing down
+// the list by compare-exchange; two rounds of bitonic merges over the lanes
+// give all four the token's list.  Returns it in `best`; t < 0: no token (the
+// lane takes part in the shuffles only).
+template <int NE, int K, bool BF16>
+__device__ __forceinline__ void route_quad(const RouteArgs &a, int t, int q, uint64_t (&best)[K]) {
+    uint32_t key[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        const int e = q + 4 * i;
+        key[i] = 0u;
+        if (t >= 0 && e < a.E) {
+            const int64_t off = (int64_t)t * a.ld + e;
+            if constexpr (BF16)
+                key[i] = route_key(__bfloat162float(static_cast<const __nv_bfloat16 *>(a.logits)[off]));
+            else
+                key[i] = route_key(static_cast<const float *>(a.logits)[off]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < K; ++j) best[j] = 0;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        uint64_t w = key[i] == 0u ? 0 : (uint64_t)key[i] << 32 | (uint32_t)~(q + 4 * i);
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const uint64_t lo = umin64(best[j], w);
+            best[j] = umax64(best[j], w);
+            w = lo;
+        }
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        uint64_t c[K];
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+            c[j] = umax64(best[j], __shfl_xor_sync(0xffffffffu, best[K - 1 - j], o));
+#pragma unroll
+        for (int h = K / 2; h > 0; h >>= 1)
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                if ((j & h) == 0) {
+                    const uint64_t hi = umax64(c[j], c[j + h]);
+                    c[j + h] = umin64(c[j], c[j + h]);
+                    c[j] = hi;
+                }
+#pragma unroll
+        for (int j = 0; j < K; ++j) best[j] = c[j];
+    }
+    // the scores, in the order of the choices (the same on all four lanes)
+    const float top = key_value((uint32_t)(best[0] >> 32));
+    float sum = 0.0f;
+    if (a.score == FP8G_SCORE_SOFTMAX) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            if (key[i] != 0u) sum += rel_exp(key_value(key[i]), top);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    }
+    float w[K];
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        const uint32_t kj = (uint32_t)(best[j] >> 32);
+        w[j] = 0.0f;
+        if (j < a.k && kj != 0u)
+            w[j] = a.score <= FP8G_SCORE_SOFTMAX_TOPK ? rel_exp(key_value(kj), top)
+                                                      : 1.0f / (1.0f + expf(-key_value(kj)));
+        if (a.score == FP8G_SCORE_SOFTMAX_TOPK || a.score == FP8G_SCORE_SIGMOID_NORM) sum += w[j];
+    }
+    if (t < 0) return;
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+        if ((j & 3) == q && j < a.k) {
+            const bool on = (best[j] >> 32) != 0;
+            const float v = a.score == FP8G_SCORE_SIGMOID ? w[j] : __fdiv_rn(w[j], sum);
+            a.ids[(int64_t)t * a.k + j] = on ? (int)~(uint32_t)best[j] : -1;
+            a.weights[(int64_t)t * a.k + j] = on ? v * a.scale : 0.0f;
+        }
+}
+
 // The pairs [i0, i0 + n) of the ids, ranked among themselves by expert, to
 // their places: base[e] is the first place of this block's pairs of expert e.
 // wh [kWarps][E] counts per warp.  Call with all threads.
@@ -207,7 +292,9 @@ __device__ __forceinline__ void expert_prefix(const int32_t *cnt, int32_t *base,
     __syncthreads();
 }
 
-template <int NV, bool BF16>
+// K 0: a warp takes a token, NV = ceil(E / 32); else four lanes take one, NV =
+// ceil(E / 4), K at least a.k.
+template <int NV, int K, bool BF16>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a) {
     extern __shared__ int32_t sm[];  // cnt [E], base [E], total, warp counts [kWarps][E]
     int32_t *cnt = sm, *base = sm + a.E, *total = sm + 2 * a.E, *wh = sm + 2 * a.E + 1;
@@ -218,9 +305,20 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a) {
     __syncthreads();
     ptx::grid_dep_wait();  // launched programmatically: global memory from here on
     const int t0 = blockIdx.x * kTokensPerBlock, t1 = min(a.T, t0 + kTokensPerBlock);
-    for (int t = t0 + warp; t < t1; t += blockDim.x >> 5) {
-        const int e = route_token<NV, BF16>(a, t, lane);
-        if (ordered && e >= 0) atomicAdd(&cnt[e], 1);
+    if constexpr (K == 0) {
+        for (int t = t0 + warp; t < t1; t += blockDim.x >> 5) {
+            const int e = route_token<NV, BF16>(a, t, lane);
+            if (ordered && e >= 0) atomicAdd(&cnt[e], 1);
+        }
+    } else {
+        const int t = t0 + (int)(threadIdx.x >> 2), q = threadIdx.x & 3;
+        uint64_t best[K];
+        route_quad<NV, K, BF16>(a, t < t1 ? t : -1, q, best);
+        if (ordered && t < t1) {
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                if ((j & 3) == q && j < a.k && (best[j] >> 32) != 0) atomicAdd(&cnt[~(uint32_t)best[j]], 1);
+        }
     }
     if (!ordered) {
         ptx::grid_dep_launch();
@@ -270,11 +368,11 @@ __global__ void __launch_bounds__(kWarps * 32) route_order_kernel(RouteArgs a, i
     place_pairs(a, a.ids, (int64_t)t0 * a.k, (t1 - t0) * a.k, base, wh, *total);
 }
 
-template <int NV>
+template <int NV, int K>
 cudaError_t launch_nv(const RouteArgs &a, bool bf16, int blocks, int threads, size_t smem,
                       cudaStream_t s) {
-    return bf16 ? launch_programmatic_smem(route_kernel<NV, true>, dim3(blocks), dim3(threads), smem, s, a)
-                : launch_programmatic_smem(route_kernel<NV, false>, dim3(blocks), dim3(threads), smem, s, a);
+    return bf16 ? launch_programmatic_smem(route_kernel<NV, K, true>, dim3(blocks), dim3(threads), smem, s, a)
+                : launch_programmatic_smem(route_kernel<NV, K, false>, dim3(blocks), dim3(threads), smem, s, a);
 }
 
 }  // namespace
@@ -287,17 +385,27 @@ cudaError_t launch_moe_route(const void *logits, int bf16, int64_t ld, int32_t T
                              cudaStream_t s) {
     const RouteArgs a{logits, ld, T, E, k, score, scale, ids, weights, counts, rows, slots, hist};
     const int blocks = route_blocks(T);
-    const int warps = T < kWarps ? T : kWarps;
     const size_t smem = (size_t)(2 * E + 1 + kWarps * E) * 4;  // E <= 256: 34 KB
     cudaError_t e;
-    if (E <= 32)
-        e = launch_nv<1>(a, bf16 != 0, blocks, 32 * warps, smem, s);
-    else if (E <= 64)
-        e = launch_nv<2>(a, bf16 != 0, blocks, 32 * warps, smem, s);
-    else if (E <= 128)
-        e = launch_nv<4>(a, bf16 != 0, blocks, 32 * warps, smem, s);
-    else
-        e = launch_nv<8>(a, bf16 != 0, blocks, 32 * warps, smem, s);
+    if (T > kQuadTokens && E <= 64) {
+        const int threads = (int)((T < kTokensPerBlock ? T : kTokensPerBlock) * 4 + 31) / 32 * 32;
+        if (E <= 32)
+            e = k <= 8 ? launch_nv<8, 8>(a, bf16 != 0, blocks, threads, smem, s)
+                       : launch_nv<8, 16>(a, bf16 != 0, blocks, threads, smem, s);
+        else
+            e = k <= 8 ? launch_nv<16, 8>(a, bf16 != 0, blocks, threads, smem, s)
+                       : launch_nv<16, 16>(a, bf16 != 0, blocks, threads, smem, s);
+    } else {
+        const int threads = 32 * (T < kWarps ? T : kWarps);
+        if (E <= 32)
+            e = launch_nv<1, 0>(a, bf16 != 0, blocks, threads, smem, s);
+        else if (E <= 64)
+            e = launch_nv<2, 0>(a, bf16 != 0, blocks, threads, smem, s);
+        else if (E <= 128)
+            e = launch_nv<4, 0>(a, bf16 != 0, blocks, threads, smem, s);
+        else
+            e = launch_nv<8, 0>(a, bf16 != 0, blocks, threads, smem, s);
+    }
     if (e != cudaSuccess || rows == nullptr || blocks == 1) return e;
     return launch_programmatic_smem(route_order_kernel, dim3(blocks), dim3(kWarps * 32),
                                     smem + (size_t)E * 4, s, a, blocks);

@@ -16,8 +16,8 @@
 // order (the result does not depend on who that is).  No CTA waits for another.
 //
 // Roles: warp 0 TMA producer (a ring of stages: two weight tiles, the tokens'
-// K slice, the three packed scale chunks), warp 1 copies a stage's scales to
-// tensor memory and issues its MMAs, warps 4-11 epilogue.
+// K slice, the three packed scale chunks), warp 2 copies a stage's scales to
+// tensor memory, warp 1 issues its MMAs, warps 4-11 epilogue.
 //
 // Low-rank steps (kStreamOut): after the FP8 steps a tile takes, per adapter
 // among the group's tokens, 64-wide bf16 steps (kind::f16) of the adapter's B
@@ -39,6 +39,7 @@ constexpr int kSEpiWarp0 = 4;
 constexpr int kSEpiWarps = 8;
 constexpr int kWTile = 128 * 128;  // bytes of a weight tile in shared memory
 constexpr int kMaxStages = 16;
+constexpr int kJoin = 4;           // partial tiles read at a time
 constexpr int kSfSlot = 16;        // tensor-memory columns of a stage's scales
 constexpr int kSmemMax = 232448;
 
@@ -46,7 +47,7 @@ constexpr int kLoraGroups = kStreamMaxLoraRows / kStreamMaxTokens;
 
 // Shared memory after the ring: barriers, table of groups.
 struct StreamTail {
-    uint64_t full[kMaxStages], empty[kMaxStages], accf[2], acce[2], drain;
+    uint64_t full[kMaxStages], empty[kMaxStages], sfr[kMaxStages], accf[2], acce[2], drain, drain_sf;
     uint32_t tmem;
     int abort_flag;
     int last;
@@ -100,9 +101,9 @@ __device__ __forceinline__ bool stream_next(const StreamParams &p, const StreamT
         o.has1 = true;
     } else {
         o.mat0 = o.mat1 = gr.mat;
-        o.w0 = o.mt * 256;
+        o.w0 = o.mt * 128 * p.sub;
         o.w1 = o.w0 + 128;
-        o.has1 = o.w1 < p.rows;
+        o.has1 = p.sub == 2 && o.w1 < p.rows;
     }
     w.u += o.k1 - o.k0;
     return true;
@@ -230,12 +231,14 @@ __global__ void __launch_bounds__(kSThreads, 1)
         for (int s = 0; s < p.stages; ++s) {
             ptx::mbar_init(ptx::smem_addr(&t.full[s]), 1);
             ptx::mbar_init(ptx::smem_addr(&t.empty[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&t.sfr[s]), 1);
         }
         for (int a = 0; a < 2; ++a) {
             ptx::mbar_init(ptx::smem_addr(&t.accf[a]), 1);
             ptx::mbar_init(ptx::smem_addr(&t.acce[a]), kSEpiWarps);
         }
         ptx::mbar_init(ptx::smem_addr(&t.drain), 1);
+        ptx::mbar_init(ptx::smem_addr(&t.drain_sf), 1);
         t.abort_flag = 0;
         ptx::fence_mbar_init();
     }
@@ -271,6 +274,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
         // ===== TMA producer =====
         if (lane == 0) {
             const uint32_t w_tx = kWTile - kWTile / 8 * p.gap8;
+            const bool two_v = p.v_rows > p.nb;
             // the two halves of a step's loads: weights and their scales (or an
             // adapter's rows), tokens and theirs (or V)
             auto weights = [&](const StreamTile &o, int k, int stage) {
@@ -290,7 +294,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
                 } else {
                     const int ls = k - p.ks, sl = ls / p.kr, c = (ls - sl * p.kr) * 64;
                     const int l = t.lora.adapter[o.g][sl];
-                    ptx::mbar_arrive_expect_tx(fb, nw * kWTile + 2 * o.n16 * 128u);
+                    ptx::mbar_arrive_expect_tx(fb, nw * kWTile + (two_v ? 2 : 1) * o.n16 * 128u);
                     ptx::tma_load_3d(s0, &tmB, fb, c, o.w0, l);
                     if (o.has1) ptx::tma_load_3d(s0 + kWTile, &tmB, fb, c, o.w1, l);
                 }
@@ -304,10 +308,11 @@ __global__ void __launch_bounds__(kSThreads, 1)
                         ptx::tma_load_2d(s0 + off_x + i * 128, &tmX, fb, k * kBK, o.row0 + i);
                 } else {
                     const int ls = k - p.ks, sl = ls / p.kr, c = (ls - sl * p.kr) * 64;
-                    const int v0 = (o.g * p.slot_cap + sl) * 2 * p.nb;
+                    const int v0 = (o.g * p.slot_cap + sl) * p.v_rows;
                     for (int i = 0; i < o.n16; i += 16) {
                         ptx::tma_load_2d(s0 + off_x + i * 128, &tmV, fb, c, v0 + i);
-                        ptx::tma_load_2d(s0 + off_x + (p.nb + i) * 128, &tmV, fb, c, v0 + p.nb + i);
+                        if (two_v)
+                            ptx::tma_load_2d(s0 + off_x + (p.nb + i) * 128, &tmV, fb, c, v0 + p.nb + i);
                     }
                 }
             };
@@ -338,7 +343,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
             }
         }
     } else if (warp == 1) {
-        // ===== scales to tensor memory, MMAs =====
+        // ===== MMAs =====
         if (lane == 0) {
             int stage = 0, lt = 0;
             uint32_t phase = 0;
@@ -352,16 +357,13 @@ __global__ void __launch_bounds__(kSThreads, 1)
                 const uint32_t id8 = ptx::idesc_mxf8(128, 0, 0) | ((uint32_t)(ti.n16 >> 3) << 17) | p.w_fmt;
                 const uint32_t id16 = ptx::idesc_bf16(128, 0) | ((uint32_t)(ti.n16 >> 3) << 17);
                 for (int k = ti.k0; k < ti.k1; ++k) {
-                    if (!wait_bar(ptx::smem_addr(&t.full[stage]), phase, abort_flag, p, 256 + stage))
+                    if (!wait_bar(ptx::smem_addr(&t.sfr[stage]), phase, abort_flag, p, 256 + stage))
                         goto roles_done;
                     ptx::tc_fence_after();
                     const uint32_t s0 = sbase + stage * p.stage_bytes;
                     const uint32_t x0 = s0 + off_x;
                     if (EPI != kStreamOut || k < p.ks) {
-                        const uint32_t sf = sf_tmem0 + stage * kSfSlot, cs = s0 + off_sf;
-                        ptx::tc_cp_32x128b_warpx4(sf, ptx::desc_sf_chunk(cs));
-                        if (ti.has1) ptx::tc_cp_32x128b_warpx4(sf + 4, ptx::desc_sf_chunk(cs + 512));
-                        ptx::tc_cp_32x128b_warpx4(sf + 8, ptx::desc_sf_chunk(cs + 1024));
+                        const uint32_t sf = sf_tmem0 + stage * kSfSlot;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const uint32_t id = id8 | ((uint32_t)j << 4) | ((uint32_t)j << 29);
@@ -377,7 +379,9 @@ __global__ void __launch_bounds__(kSThreads, 1)
                         const int nk = (min(64, p.rank - c) + 15) / 16;
                         for (int j = 0; j < nk; ++j) {
                             const uint64_t dh = ptx::desc_kmajor_sw128(x0 + 32 * j);
-                            const uint64_t dl = ptx::desc_kmajor_sw128(x0 + p.nb * 128 + 32 * j);
+                            // the lo half: rows of its own, or columns 32-63
+                            const uint64_t dl = ptx::desc_kmajor_sw128(
+                                x0 + (p.v_rows > p.nb ? p.nb * 128 : 64) + 32 * j);
                             const uint64_t w0 = ptx::desc_kmajor_sw128(s0 + 32 * j);
                             ptx::mma_bf16(d0, w0, dh, id16, (k != ti.k0 || j != 0) ? 1u : 0u);
                             ptx::mma_bf16(d0, w0, dl, id16, 1u);
@@ -397,16 +401,46 @@ __global__ void __launch_bounds__(kSThreads, 1)
                 ptx::tc_commit(ptx::smem_addr(&t.accf[acc]));
             }
         }
+    } else if (warp == 2) {
+        // ===== scales to tensor memory =====
+        // From a thread of their own: issued by the MMA thread each copy holds
+        // up the MMAs behind it.  A stage's columns are rewritten only after
+        // its next "full", when the MMAs that read them are complete.
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            while (stream_next<EPI>(p, t, walk, ti)) {
+                for (int k = ti.k0; k < ti.k1; ++k) {
+                    if (!wait_bar(ptx::smem_addr(&t.full[stage]), phase, abort_flag, p, 2 * 256 + stage))
+                        goto roles_done;
+                    ptx::tc_fence_after();
+                    if (EPI != kStreamOut || k < p.ks) {
+                        const uint32_t sf = sf_tmem0 + stage * kSfSlot;
+                        const uint32_t cs = sbase + stage * p.stage_bytes + off_sf;
+                        ptx::tc_cp_32x128b_warpx4(sf, ptx::desc_sf_chunk(cs));
+                        if (ti.has1) ptx::tc_cp_32x128b_warpx4(sf + 4, ptx::desc_sf_chunk(cs + 512));
+                        ptx::tc_cp_32x128b_warpx4(sf + 8, ptx::desc_sf_chunk(cs + 1024));
+                    }
+                    ptx::tc_commit(ptx::smem_addr(&t.sfr[stage]));
+                    if (++stage == p.stages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        }
     } else if (warp >= kSEpiWarp0) {
         // ===== epilogue =====
         ptx::grid_dep_wait();  // counters, partials and outputs: after the previous kernel
         const int q = warp & 3, half = (warp - kSEpiWarp0) >> 2;
         const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16);
         const int row_l = q * 32 + lane;  // weight row within a tile
-        // gated: both weight tiles, every other 16 columns; else: weight tile `half`
+        // two weight tiles: this warp takes tile `half`; gated, or one tile:
+        // every other 16 columns (of both tiles, gated)
         constexpr int kSubs = EPI == kStreamGated ? 2 : 1;
-        const int c_first = EPI == kStreamGated ? half * 16 : 0;
-        constexpr int kStep = EPI == kStreamGated ? 32 : 16;
+        const bool by_cols = EPI == kStreamGated || p.sub == 1;
+        const int c_first = by_cols ? half * 16 : 0, c_step = by_cols ? 32 : 16;
+        const int my_sub = by_cols ? 0 : half;
         int lt = 0;
         for (; stream_next<EPI>(p, t, walk, ti); ++lt) {
             const int acc = p.nacc == 2 ? (lt & 1) : 0;
@@ -415,7 +449,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
             if (!epi_all(ok)) break;
             ptx::tc_fence_after();
             const bool whole = ti.k0 == 0 && ti.k1 == ti.upt;
-            const bool live = EPI == kStreamGated || half == 0 || ti.has1;  // this warp has a weight tile
+            const bool live = my_sub == 0 || ti.has1;  // this warp has a weight tile
             const uint32_t ta = tq + acc * acc_cols;
             bool finish = whole;
             int c_lo = 0, c_hi = 0;  // CTAs that share the tile
@@ -425,10 +459,10 @@ __global__ void __launch_bounds__(kSThreads, 1)
                 c_hi = span_owner(U, G, tu + ti.upt - 1);
                 float *part = p.part + (int64_t)(2 * cta + (u0 > tu ? 0 : 1)) * 2 * p.nb * 128;
                 if (live)
-                    for (int c = c_first; c < ti.n; c += kStep) {
+                    for (int c = c_first; c < ti.n; c += c_step) {
 #pragma unroll
                         for (int s = 0; s < kSubs; ++s) {
-                            const int sub = EPI == kStreamGated ? s : half;
+                            const int sub = EPI == kStreamGated ? s : my_sub;
                             uint32_t r[16];
                             ptx::tmem_ld_32x32b_x16(ta + sub * p.nb + c, r);
                             ptx::tmem_ld_wait();
@@ -453,11 +487,11 @@ __global__ void __launch_bounds__(kSThreads, 1)
                 finish = t.last != 0;
             }
             if (finish && live) {
-                for (int c = c_first; c < ti.n; c += kStep) {
+                for (int c = c_first; c < ti.n; c += c_step) {
                     float v[kSubs][16];
 #pragma unroll
                     for (int s = 0; s < kSubs; ++s) {
-                        const int sub = EPI == kStreamGated ? s : half;
+                        const int sub = EPI == kStreamGated ? s : my_sub;
                         if (whole) {
                             uint32_t r[16];
                             ptx::tmem_ld_32x32b_x16(ta + sub * p.nb + c, r);
@@ -468,17 +502,27 @@ __global__ void __launch_bounds__(kSThreads, 1)
                             const int64_t tu = (int64_t)t.g[ti.g].unit0 + (int64_t)ti.mt * ti.upt;
 #pragma unroll
                             for (int i = 0; i < 16; ++i) v[s][i] = 0.0f;
-                            for (int o = c_lo; o <= c_hi; ++o) {
-                                const int side = span_begin(U, G, o) > tu ? 0 : 1;
-                                const float *src = p.part + (int64_t)(2 * o + side) * 2 * p.nb * 128 +
-                                                   ((int64_t)sub * p.nb + c) * 128 + row_l;
+                            // in unit order; several CTAs' loads in flight at a time
+                            for (int o = c_lo; o <= c_hi; o += kJoin) {
+                                float x[kJoin][16];
 #pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    if (c + i < ti.n) v[s][i] += __ldcg(src + i * 128);
+                                for (int j = 0; j < kJoin; ++j) {
+                                    const int side = span_begin(U, G, o + j) > tu ? 0 : 1;
+                                    const float *src = p.part + (int64_t)(2 * (o + j) + side) * 2 * p.nb * 128 +
+                                                       ((int64_t)sub * p.nb + c) * 128 + row_l;
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i)
+                                        x[j][i] = o + j <= c_hi && c + i < ti.n ? __ldcg(src + i * 128) : 0.0f;
+                                }
+#pragma unroll
+                                for (int j = 0; j < kJoin; ++j)
+                                    if (o + j <= c_hi)
+#pragma unroll
+                                        for (int i = 0; i < 16; ++i) v[s][i] += x[j][i];
                             }
                         }
                     }
-                    const int f = (EPI == kStreamGated ? ti.w0 : (half ? ti.w1 : ti.w0)) + row_l;
+                    const int f = (my_sub ? ti.w1 : ti.w0) + row_l;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int col = c + i;
@@ -529,10 +573,11 @@ roles_done:
     if (*abort_flag) {
         // wait (bounded) for this CTA's MMAs, then give copies in flight a
         // bounded time before shared memory is released
-        if (warp == 1 && lane == 0) {
-            ptx::tc_commit(ptx::smem_addr(&t.drain));
+        if ((warp == 1 || warp == 2) && lane == 0) {
+            const uint32_t db = ptx::smem_addr(warp == 1 ? &t.drain : &t.drain_sf);
+            ptx::tc_commit(db);
             const uint64_t t0 = ptx::globaltimer();
-            while (!ptx::mbar_try_wait(ptx::smem_addr(&t.drain), 0) &&
+            while (!ptx::mbar_try_wait(db, 0) &&
                    ptx::globaltimer() - t0 < p.timeout_ns) {
             }
         }
@@ -567,11 +612,12 @@ cudaError_t launch_epi(const CUtensorMap &w, const CUtensorMap &x, const CUtenso
 
 }  // namespace
 
-void stream_sizes(StreamParams &p, int nb, bool lora) {
+void stream_sizes(StreamParams &p, int nb, int v_halves) {
     p.nb = nb;
+    p.sub = 2;
     // two accumulators of two tiles each beside the scales, where they fit
     p.nacc = nb <= 64 ? 2 : 1;
-    p.x_bytes = nb * 128 * (lora ? 2 : 1);
+    p.x_bytes = nb * 128 * v_halves;
     p.stage_bytes = 2 * kWTile + p.x_bytes + 2048;  // 1536 bytes of scales; 1024-byte multiples
     const int room = kSmemMax - 1024 - (int)sizeof(StreamTail);
     p.stages = room / p.stage_bytes;

@@ -26,7 +26,8 @@ enum StreamEpi : int {
 };
 
 struct StreamParams {
-    int32_t mt;      // weight-row tiles per group
+    int32_t sub;     // 128-row weight tiles of a work unit (2, or 1; gated: 2)
+    int32_t mt;      // weight-row tiles (of sub 128 rows; gated: 128 features) per group
     int32_t ks;      // 128-wide K steps
     int32_t rows;    // rows of a weight matrix (gated: of each half)
     int32_t n_rt;    // 128-row tiles of packed scales per matrix
@@ -56,14 +57,24 @@ struct StreamParams {
     void *c;                 // [tokens][rows]
     int32_t out_f32;
     const float *bias;
-    // low-rank: rank, 64-wide steps per slot (0: none), slots per group (V's
-    // rows of slot s of group g begin at (g slot_cap + s) 2 nb); n_mat adapters
-    int32_t rank, kr, slot_cap;
+    // low-rank: rank, steps per slot (0: none), slots per group, rows of V a
+    // slot has (LoraV); n_mat adapters
+    int32_t rank, kr, slot_cap, v_rows;
 };
 
-// Ring and accumulator sizes for nb token columns; lora: V's two halves share
-// the token region of a stage.
-void stream_sizes(StreamParams &p, int nb, bool lora);
+// V of a slot.  Rank up to 32: a row of 64 values holds both halves, hi in
+// columns 0-31 and lo in 32-63, one 64-wide step.  More: rows of r64 = rank
+// rounded up to 64, the hi rows first, then the lo rows, r64 / 64 steps.
+struct LoraV {
+    bool wide;  // halves in rows of their own
+    int r64, kr, halves;  // row length, steps per slot, blocks of rows
+    explicit LoraV(int rank)
+        : wide(rank > 32), r64(wide ? (rank + 63) / 64 * 64 : 64), kr(r64 / 64), halves(wide ? 2 : 1) {}
+};
+
+// Ring and accumulator sizes for nb token columns; v_halves 2: V's two halves
+// share the token region of a stage.
+void stream_sizes(StreamParams &p, int nb, int v_halves);
 size_t stream_part_bytes(const StreamParams &p, int grid);
 cudaError_t launch_stream(int epi, const CUtensorMap &w, const CUtensorMap &x, const CUtensorMap &lb,
                           const CUtensorMap &v, const StreamParams &p, int grid, cudaStream_t s);

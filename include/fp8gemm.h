@@ -591,7 +591,7 @@ FP8G_API fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t
  * FP8G_MAX_LORA_RANK, else FP8G_ERR_UNSUPPORTED_SHAPE; L = 0: no adapters
  * (lora_a, lora_b, adapter unused, may be null); M may be 0.  x, W (packed
  * formats 32), sfw, lora_a, lora_b, C 16-byte aligned, N * sizeof(out element)
- * % 16 == 0, else FP8G_ERR_ALIGNMENT.  Results do not vary between runs.  Two
+ * % 16 == 0, else FP8G_ERR_ALIGNMENT.  Results do not vary between runs.  Two or three
  * kernels and one temporary from the library's pool of about M K + 4 M
  * min(L, 256) max(r, 64) bytes.
  */
