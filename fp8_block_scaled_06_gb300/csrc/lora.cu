@@ -2,13 +2,13 @@
 //
 //   C[i] = out( Q(x_i) W^T + bias + alpha_l B_l (A_l x_i) ),  l = adapter[i]
 //
-// Two launches.  The first quantises x and forms V = alpha A x; the second is
-// the product, with V against the adapters' B rows as further K steps into
-// the same fp32 accumulator, so the sum is rounded once: for few rows the
-// streaming kernel (stream.cu), else the CTA-pair kernel (gemm_pair.cu).
+// Few rows: one launch of the streaming kernel (stream.cu).  Many: the rows
+// quantised, V = alpha A x, then the CTA-pair product (gemm_pair.cu).  In both V
+// is taken against the adapters' B rows as further K steps into the product's
+// fp32 accumulator, so the sum is rounded once.
 //
-// V.  Rows are taken in tiles of `tile` (a group of the streaming kernel, or
-// the 256 rows of a pair).  The adapters among a tile's rows, in rising order,
+// V.  Rows are taken in tiles (a group of the streaming kernel, or the 256 rows
+// of a pair).  The adapters among a tile's rows, in rising order,
 // are its slots; a slot holds V of all the tile's rows, zero for those of
 // other adapters, as two bf16 halves (V = hi + lo to 16 bits): the product
 // then needs no gather, and an adapter costs rank / 128 of a K step's weights.
@@ -31,12 +31,8 @@ struct LoraPrep {
     const void *x;
     int32_t M, K;
     uint8_t *xq;        // [M][K] codes
-    uint8_t *xsf;       // chunk of (row tile rt of sf_rows rows, K group kg) at kg sf_k + rt sf_t
-    int32_t sf_rows;
-    int64_t sf_k, sf_t;
-    int32_t ks;
-    int32_t *cnt;       // counters to zero
-    int32_t n_cnt;
+    uint8_t *xsf;       // packed scales [ks][n_rt][512]
+    int32_t ks, n_rt;
     // low-rank part
     const __nv_bfloat16 *a;   // [L][r][K]
     const float *alpha;       // [L] or null
@@ -44,9 +40,8 @@ struct LoraPrep {
     int32_t L, r, r64, wide;  // LoraV: V's row length, halves in rows of their own
     int32_t tile, cap, tiles;
     __nv_bfloat16 *v;         // [tiles][cap][halves][tile][r64]
-    int32_t *slot_cnt, *slot_adapter;  // tables of the pair kernel, or null
+    int32_t *slot_cnt, *slot_adapter;  // the pair kernel's tables
     int32_t items;            // blocks per tile and rank block of the low-rank part
-    int32_t low_blocks;       // blocks of the low-rank part
     unsigned int *status;
 };
 
@@ -85,12 +80,13 @@ __device__ __forceinline__ uint4 x_pairs(const void *x, int64_t off, bool in) {
     }
 }
 
-// Row blk of x: codes, scale bytes; with the counters to zero shared out.
+// Row blockIdx.x of x: codes, scale bytes.
 template <bool BF16>
-__device__ __forceinline__ void quantise_row(const LoraPrep &p, int blk) {
-    const int tid = threadIdx.x, nt = blockDim.x;
-    for (int i = blk * nt + tid; i < p.n_cnt; i += p.M * nt) p.cnt[i] = 0;
-    const int rt = blk / p.sf_rows, in_t = blk - rt * p.sf_rows;
+__global__ void __launch_bounds__(256) lora_quant_kernel(const __grid_constant__ LoraPrep p) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    const int tid = threadIdx.x, nt = blockDim.x, blk = blockIdx.x;
+    const int rt = blk / 128, in_t = blk - rt * 128;
     const int groups = p.ks * 16;
     for (int c0 = 0; c0 < groups; c0 += nt) {
         const int c = c0 + tid;
@@ -104,30 +100,21 @@ __device__ __forceinline__ void quantise_row(const LoraPrep &p, int blk) {
         if (in)
             *reinterpret_cast<uint2 *>(p.xq + (int64_t)blk * p.K + c * 8) = quant8_pow2<0>(v0, v1, s);
         if (c < groups && (c & 3) == 0)
-            p.xsf[(c >> 4) * p.sf_k + rt * p.sf_t + 16 * (in_t & 31) + 4 * (in_t >> 5) + ((c >> 2) & 3)] =
+            p.xsf[((int64_t)(c >> 4) * p.n_rt + rt) * 512 + 16 * (in_t & 31) + 4 * (in_t >> 5) + ((c >> 2) & 3)] =
                 (uint8_t)(__float_as_uint(s) >> 23);
     }
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(256) lora_quant_kernel(const __grid_constant__ LoraPrep p) {
-    ptx::grid_dep_wait();
-    ptx::grid_dep_launch();
-    quantise_row<BF16>(p, blockIdx.x);
-}
-
-// Blocks below p.low_blocks: the low-rank part, block (tile, rank block of 16,
-// item): items are the pairs (slot, 16 of the slot's rows) in order.  The
-// blocks after them quantise a row each (the low-rank blocks take longer, so
-// they come first).  The K range goes over the block's warps (bound by the
+// V.  A block takes an item of a tile and 16 ranks: items are the pairs (slot,
+// 16 of the slot's rows) in order; blocks past the last one leave.  The K range goes over the block's warps (bound by the
 // latency of its loads: 16 warps with their loads of up to 128 K each in
 // flight), each a 16 x 16 product by mma.sync, joined in shared memory in warp
 // order.  A lane's 16-byte load covers 8 consecutive K of a row; the same K
 // permutation on both operands leaves the product unchanged.
 template <bool BF16>
-__global__ void __launch_bounds__(kLThreads) lora_prep_kernel(const __grid_constant__ LoraPrep p) {
+__global__ void __launch_bounds__(kLThreads) lora_v_kernel(const __grid_constant__ LoraPrep p) {
     __shared__ int32_t ad[kMaxTile];
-    __shared__ int32_t cnt[kMaxAdapters];
+    __shared__ int32_t cnt[FP8G_MAX_ADAPTERS];
     __shared__ int32_t pick[3];  // adapter, slot, first of its rows
     __shared__ int32_t rows[16];
     __shared__ float acc[kLWarps][16][17];
@@ -135,10 +122,6 @@ __global__ void __launch_bounds__(kLThreads) lora_prep_kernel(const __grid_const
     const int blk = blockIdx.x;
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    if (blk >= p.low_blocks) {
-        quantise_row<BF16>(p, blk - p.low_blocks);
-        return;
-    }
     // ------------------------------------------------------- low-rank part
     const int rblocks = (p.r + 15) / 16;
     int w = blk;
@@ -181,11 +164,11 @@ __global__ void __launch_bounds__(kLThreads) lora_prep_kernel(const __grid_const
                 pick[1] = slot;
                 pick[2] = 16 * (item - first);
             }
-            if (has && p.slot_cnt != nullptr && item == 0 && rb == 0) p.slot_adapter[tile * p.cap + slot] = l;
+            if (has && item == 0 && rb == 0) p.slot_adapter[tile * p.cap + slot] = l;
             items += __shfl_sync(0xffffffffu, s_it, 31);
             slots += __shfl_sync(0xffffffffu, s_sl, 31);
         }
-        if (lane == 0 && p.slot_cnt != nullptr && item == 0 && rb == 0) p.slot_cnt[tile] = slots;
+        if (lane == 0 && item == 0 && rb == 0) p.slot_cnt[tile] = slots;
         __syncwarp();
         const int l = pick[0];
         if (l >= 0) {  // this item's rows: those of adapter l, from the pick[2]-th on
@@ -326,26 +309,27 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
     if (st != FP8G_OK) return st;
     if (M == 0) return FP8G_OK;
 
-    const bool pair = M > kStreamMaxLoraRows;
-    const int nb = pair ? 256 : (int)(M < kStreamMaxTokens ? (M + 15) / 16 * 16 : kStreamMaxTokens);
-    const int tiles = (int)((M + nb - 1) / nb);
-    const int32_t ks = (int32_t)((K + 127) / 128), n_rt = (int32_t)((N + 127) / 128);
-    const int cap = L < nb ? L : nb;
     const LoraV lv(lora ? r : 1);
+    const bool pair = M > kStreamLoraRows;
+    const int nb = pair ? 256 : (int)(M < kStreamMaxTokens ? (M + 15) / 16 * 16 : kStreamMaxTokens);
+    const int tiles = (int)((M + nb - 1) / nb), cap = L < nb ? L : nb;
+    const int32_t ks = (int32_t)((K + 127) / 128), n_rt = (int32_t)((N + 127) / 128);
     const int32_t n_rtA = (int32_t)((M + 127) / 128);
-    StreamParams sp{};
+    // rows of V and of the scales: 32-bit TMA coordinates
+    if ((int64_t)tiles * cap * lv.halves * nb >= kMaxDim || (int64_t)ks * n_rtA >= kMaxDim)
+        return FP8G_ERR_UNSUPPORTED_SHAPE;
+    StreamParams p{};
+    StreamPhase &h = p.ph[0];
     if (!pair) {
-        stream_sizes(sp, nb, lv.halves);
-        sp.mt = (int32_t)((N + 255) / 256);
-        sp.ks = ks;
-        sp.rows = (int32_t)N;
-        sp.n_rt = n_rt;
-        sp.kr = lora ? lv.kr : 0;
-        if ((int64_t)tiles * sp.mt * (ks + (int64_t)cap * sp.kr) >= INT32_MAX)
-            return FP8G_ERR_UNSUPPORTED_SHAPE;
+        stream_sizes(p, nb, true, lv.halves);
+        h.sub = 2;
+        h.mt = (int32_t)((N + 255) / 256);
+        h.ks = ks;
+        h.rows = (int32_t)N;
+        h.n_rt = n_rt;
+        p.kr = lora ? lv.kr : 0;
+        if ((int64_t)tiles * h.mt * (ks + (int64_t)cap * p.kr) >= INT32_MAX) return FP8G_ERR_UNSUPPORTED_SHAPE;
     }
-    if ((int64_t)tiles * cap * 2 * nb >= kMaxDim || (int64_t)ks * n_rtA >= kMaxDim)
-        return FP8G_ERR_UNSUPPORTED_SHAPE;  // rows of V and of the scales: 32-bit TMA coordinates
     size_t at = 0;
     auto take = [&at](size_t bytes) {
         const size_t o = at;
@@ -354,98 +338,95 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
     };
     const size_t o_xq = take((size_t)M * K), o_xsf = take((size_t)(pair ? n_rtA : tiles) * ks * 512);
     const size_t o_v = take((size_t)tiles * cap * lv.halves * nb * lv.r64 * 2);
-    const int n_cnt = pair ? 0 : tiles * sp.mt;
-    const size_t o_cnt = take((size_t)n_cnt * 4);
-    const size_t o_part = take(pair ? 0 : stream_part_bytes(sp, d.num_sms));
-    const size_t o_sc = take((size_t)tiles * 4), o_sa = take((size_t)tiles * cap * 4);
+    const size_t o_part = take(pair ? (size_t)tiles * 4 : stream_part_bytes(p, d.num_sms));
+    const size_t o_flags = take(pair ? (size_t)tiles * cap * 4 : stream_flag_bytes(d.num_sms));
     cudaMemPool_t pool;
     if ((st = host_pool(d.dev, pool)) != FP8G_OK) return st;
     void *wsv = nullptr;
     if (cudaMallocFromPoolAsync(&wsv, at, pool, stream) != cudaSuccess) return FP8G_ERR_CUDA;
     uint8_t *ws = static_cast<uint8_t *>(wsv);
-
-    LoraPrep a{};
-    a.x = x;
-    a.M = (int32_t)M;
-    a.K = (int32_t)K;
-    a.xq = ws + o_xq;
-    a.xsf = ws + o_xsf;
-    a.sf_rows = pair ? 128 : nb;
-    a.sf_k = pair ? (int64_t)n_rtA * 512 : 512;
-    a.sf_t = pair ? 512 : (int64_t)ks * 512;
-    a.ks = ks;
-    a.cnt = reinterpret_cast<int32_t *>(ws + o_cnt);
-    a.n_cnt = n_cnt;
-    a.a = static_cast<const __nv_bfloat16 *>(lora_a);
-    a.alpha = alpha;
-    a.adapter = adapter;
-    a.L = L;
-    a.r = r;
-    a.r64 = lv.r64;
-    a.wide = lv.wide;
-    a.tile = nb;
-    a.cap = cap;
-    a.tiles = tiles;
-    a.v = reinterpret_cast<__nv_bfloat16 *>(ws + o_v);
-    if (pair) {
-        a.slot_cnt = reinterpret_cast<int32_t *>(ws + o_sc);
-        a.slot_adapter = reinterpret_cast<int32_t *>(ws + o_sa);
-    }
-    // at most one partly filled item per slot beside the whole ones
-    a.items = nb / 16 + cap;
-    a.status = d.status;
-    const int64_t low = lora ? (int64_t)tiles * ((r + 15) / 16) * a.items : 0;
-    a.low_blocks = (int32_t)low;
-    cudaError_t e = low + M >= INT32_MAX ? cudaErrorInvalidValue : cudaSuccess;
-    const bool bf16 = x_dtype == FP8G_IN_BF16;
-    // Many rows: the rows in blocks of their own, with few registers (beside
-    // the low-rank part's, one block of 512 threads fills an SM).
-    const bool apart = pair || !lora;
-    if (e == cudaSuccess && apart)
-        e = bf16 ? launch_programmatic(lora_quant_kernel<true>, dim3((unsigned)M), dim3(256), stream, a)
-                 : launch_programmatic(lora_quant_kernel<false>, dim3((unsigned)M), dim3(256), stream, a);
-    if (e == cudaSuccess && lora) {
-        const unsigned blocks = (unsigned)(low + (apart ? 0 : M));
-        e = bf16 ? launch_programmatic(lora_prep_kernel<true>, dim3(blocks), dim3(kLThreads), stream, a)
-                 : launch_programmatic(lora_prep_kernel<false>, dim3(blocks), dim3(kLThreads), stream, a);
-    }
     CUtensorMap mb{}, mv{};
-    if (e == cudaSuccess && lora) {
+    if (lora) {
         const uint64_t db[3] = {(uint64_t)r, (uint64_t)N, (uint64_t)L};
         const uint32_t bb[3] = {64u, 128u, 1u};
         const uint64_t dv[2] = {(uint64_t)lv.r64, (uint64_t)tiles * cap * lv.halves * nb};
         const uint32_t bv[2] = {64u, pair ? 128u : 16u};
         st = host_bf16_map(lora_b, 3, db, bb, d.dev, mb);
-        if (st == FP8G_OK) st = host_bf16_map(a.v, 2, dv, bv, d.dev, mv);
+        if (st == FP8G_OK) st = host_bf16_map(ws + o_v, 2, dv, bv, d.dev, mv);
     }
-    if (e == cudaSuccess && st == FP8G_OK && !pair) {
-        CUtensorMap mw, mx;
+    const bool bf16 = x_dtype == FP8G_IN_BF16;
+    cudaError_t e = cudaSuccess;
+    if (st == FP8G_OK && !pair) {
         const uint64_t dw[3] = {(uint64_t)K, (uint64_t)N, 1u};
         const uint32_t bw[3] = {(uint32_t)kBK, 128u, 1u};
         const uint64_t dx[2] = {(uint64_t)K, (uint64_t)M};
         const uint32_t bx[2] = {(uint32_t)kBK, 16u};
-        st = host_operand_map(W, w_fmt, 3, dw, bw, d.dev, mw);
-        if (st == FP8G_OK) st = host_operand_map(a.xq, FP8G_E4M3, 2, dx, bx, d.dev, mx);
-        if (!lora) mb = mv = mx;
-        sp.w_fmt = host_mma_type(w_fmt) << 7;
-        sp.gap8 = host_gap8(w_fmt);
-        sp.sfw = sfw;
-        sp.sfx = a.xsf;
-        sp.idx = adapter;
-        sp.n_idx = (int32_t)M;
-        sp.n_mat = L;
-        sp.tile_cnt = a.cnt;
-        sp.part = reinterpret_cast<float *>(ws + o_part);
-        sp.status = d.status;
-        sp.timeout_ns = d.timeout_ns;
-        sp.c = C;
-        sp.out_f32 = out == FP8G_OUT_F32;
-        sp.bias = bias;
-        sp.rank = r;
-        sp.slot_cap = cap;
-        sp.v_rows = lv.halves * nb;
-        if (st == FP8G_OK) e = launch_stream(kStreamOut, mw, mx, mb, mv, sp, d.num_sms, stream);
-    } else if (e == cudaSuccess && st == FP8G_OK) {
+        st = host_operand_map(W, w_fmt, 3, dw, bw, d.dev, h.W);
+        if (st == FP8G_OK) st = host_operand_map(ws + o_xq, FP8G_E4M3, 2, dx, bx, d.dev, h.X);
+        h.sfw = sfw;
+        h.sfx = ws + o_xsf;
+        p.w_fmt = host_mma_type(w_fmt) << 7;
+        p.gap8 = host_gap8(w_fmt);
+        p.x = x;
+        p.x_bf16 = bf16;
+        p.T = (int32_t)M;
+        p.K = (int32_t)K;
+        p.idx = adapter;
+        p.n_idx = (int32_t)M;
+        p.n_mat = L;
+        p.xq = ws + o_xq;
+        p.xsf = ws + o_xsf;
+        p.part = reinterpret_cast<float *>(ws + o_part);
+        p.flags = reinterpret_cast<uint64_t *>(ws + o_flags);
+        p.token = stream_token();
+        p.out = C;
+        p.out_f32 = out == FP8G_OUT_F32;
+        p.status = d.status;
+        p.timeout_ns = d.timeout_ns;
+        p.B = mb;
+        p.V = mv;
+        p.a = lora_a;
+        p.alpha = alpha;
+        p.bias = bias;
+        p.v = ws + o_v;
+        p.rank = r;
+        p.r64 = lv.r64;
+        p.halves = lv.halves;
+        p.slot_cap = cap;
+        if (st == FP8G_OK) e = launch_stream(true, p, d.num_sms, stream);
+    } else if (st == FP8G_OK) {
+        LoraPrep a{};
+        a.x = x;
+        a.M = (int32_t)M;
+        a.K = (int32_t)K;
+        a.xq = ws + o_xq;
+        a.xsf = ws + o_xsf;
+        a.ks = ks;
+        a.n_rt = n_rtA;
+        a.a = static_cast<const __nv_bfloat16 *>(lora_a);
+        a.alpha = alpha;
+        a.adapter = adapter;
+        a.L = L;
+        a.r = r;
+        a.r64 = lv.r64;
+        a.wide = lv.wide;
+        a.tile = nb;
+        a.cap = cap;
+        a.tiles = tiles;
+        a.v = reinterpret_cast<__nv_bfloat16 *>(ws + o_v);
+        a.slot_cnt = reinterpret_cast<int32_t *>(ws + o_part);
+        a.slot_adapter = reinterpret_cast<int32_t *>(ws + o_flags);
+        a.items = nb / 16 + cap;  // at most one partly filled item per slot beside the whole ones
+        a.status = d.status;
+        e = bf16 ? launch_programmatic(lora_quant_kernel<true>, dim3((unsigned)M), dim3(256), stream, a)
+                 : launch_programmatic(lora_quant_kernel<false>, dim3((unsigned)M), dim3(256), stream, a);
+        if (e == cudaSuccess && lora) {
+            const int64_t blocks = (int64_t)tiles * ((r + 15) / 16) * a.items;
+            e = blocks >= INT32_MAX ? cudaErrorInvalidValue
+                : bf16 ? launch_programmatic(lora_v_kernel<true>, dim3((unsigned)blocks), dim3(kLThreads), stream, a)
+                       : launch_programmatic(lora_v_kernel<false>, dim3((unsigned)blocks), dim3(kLThreads), stream,
+                                             a);
+        }
         PairLora pl{};
         if (lora) {
             pl.V = mv;
@@ -457,7 +438,8 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
             pl.kr = lv.kr;
             pl.halves = lv.halves;
         }
-        st = run_pair_packed(a.xq, a.xsf, W, sfw, w_fmt, bias, C, out, M, N, K, lora ? &pl : nullptr, stream);
+        if (e == cudaSuccess)
+            st = run_pair_packed(a.xq, a.xsf, W, sfw, w_fmt, bias, C, out, M, N, K, lora ? &pl : nullptr, stream);
     }
     const cudaError_t ef = cudaFreeAsync(wsv, stream);
     if (st != FP8G_OK) return st;

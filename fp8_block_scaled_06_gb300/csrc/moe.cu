@@ -6,159 +6,13 @@
 //   hq = Q(act(g) u)                 act and product in fp32
 //   out[t] = sum_j w[t, j] hq W2[e]^T   fp32 sum over j in order, one rounding
 //
-// Four launches, each overlapping the start of the next (programmatic
-// launches): prepare (routing tables, tokens quantised in expert order), the
-// two streaming products (stream.cu), combine.  The weights of the chosen
-// experts are read once; everything else is a few hundred kilobytes.
-#include <cuda_bf16.h>
-
-#include "internal.h"
-#include "kernel_common.cuh"
-#include "quant_math.cuh"
+// One launch (stream.cu).  The weights of the chosen experts are read once;
+// everything else is a few hundred kilobytes.
 #include "stream.h"
 
 namespace fp8g {
 
 namespace {
-
-constexpr int kPrepThreads = 512;
-constexpr int kMaxPairs = 8192;  // T k
-constexpr int kMaxExperts = 256;
-
-struct PrepArgs {
-    const void *x;
-    const int32_t *ids;
-    int32_t T, k, E, H;
-    int32_t nb;        // tokens per group
-    int32_t ks;        // 128-wide K steps of x
-    uint8_t *xq;       // [T k][H] codes, expert order
-    uint8_t *xsf;      // [group][ks][512]
-    int32_t *pos;      // [T k] row in expert order, -1: not routed
-    int32_t *cnt;      // counters of both products
-    int32_t n_cnt;
-    unsigned int *status;
-};
-
-// Block t: token t.  Every block derives the routing tables it needs from the
-// ids itself (a few thousand integers at most), as the products' CTAs do.
-template <bool BF16>
-__global__ void __launch_bounds__(kPrepThreads) moe_prep_kernel(PrepArgs a) {
-    __shared__ int16_t id[kMaxPairs];
-    __shared__ int32_t cnt[kMaxExperts], off[kMaxExperts], goff[kMaxExperts];
-    __shared__ int32_t my_row[16], my_tile[16], my_in[16];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int R = a.T * a.k, t = blockIdx.x;
-    for (int e = tid; e < a.E; e += kPrepThreads) cnt[e] = 0;
-    __syncthreads();
-    ptx::grid_dep_wait();
-    ptx::grid_dep_launch();
-    for (int i = tid; i < R; i += kPrepThreads) {
-        int e = __ldg(a.ids + i);
-        if (e >= a.E) {
-            if (t == 0 && atomicCAS(&a.status[0], 0u, (unsigned)FP8G_ERR_INVALID_ARG) == 0u)
-                atomicExch(&a.status[1], (unsigned)i);
-            e = -1;
-        }
-        if (e < 0) e = -1;
-        id[i] = (int16_t)e;
-        if (e >= 0) atomicAdd(&cnt[e], 1);
-    }
-    for (int i = t * kPrepThreads + tid; i < a.n_cnt; i += gridDim.x * kPrepThreads) a.cnt[i] = 0;
-    __syncthreads();
-    if (warp == 0) {  // exclusive prefixes over experts: rows, groups
-        int rr = 0, gg = 0;
-        for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const int e = e0 + lane;
-            const int c = e < a.E ? cnt[e] : 0;
-            const int ng = (c + a.nb - 1) / a.nb;
-            int s = c, sg = ng;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, s, o), vg = __shfl_up_sync(0xffffffffu, sg, o);
-                if (lane >= o) {
-                    s += v;
-                    sg += vg;
-                }
-            }
-            if (e < a.E) {
-                off[e] = rr + s - c;
-                goff[e] = gg + sg - ng;
-            }
-            rr += __shfl_sync(0xffffffffu, s, 31);
-            gg += __shfl_sync(0xffffffffu, sg, 31);
-        }
-    }
-    __syncthreads();
-    // this token's places: the pairs before it with the same expert
-    for (int j = warp; j < a.k; j += kPrepThreads / 32) {
-        const int i = t * a.k + j, e = id[i];
-        int before = 0;
-        if (e >= 0)
-            for (int o = lane; o < i; o += 32) before += id[o] == e;
-        before = __reduce_add_sync(0xffffffffu, before);
-        if (lane == 0) {
-            my_row[j] = e >= 0 ? off[e] + before : -1;
-            my_tile[j] = e >= 0 ? goff[e] + before / a.nb : 0;
-            my_in[j] = before % a.nb;
-            a.pos[i] = my_row[j];
-        }
-    }
-    __syncthreads();
-    // quantise: thread c takes values 8c .. 8c + 7, four threads a block; K
-    // groups past H (the last step's tail) get scale 1
-    const int groups = a.ks * 16;
-    for (int c0 = 0; c0 < groups; c0 += kPrepThreads) {
-        const int c = c0 + tid;
-        float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
-        const bool in = c * 8 < a.H;
-        if (in) load8<BF16>(a.x, (int64_t)t * a.H + c * 8, v0, v1);
-        float am = absmax8(v0, v1);
-        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
-        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-        const float s = pow2_scale<0>(am);
-        const uint2 q = quant8_pow2<0>(v0, v1, s);
-        const int kg = c >> 4, b = (c >> 2) & 3;
-        for (int j = 0; j < a.k; ++j) {
-            const int row = my_row[j];
-            if (row < 0 || c >= groups) continue;
-            if (in) *reinterpret_cast<uint2 *>(a.xq + (int64_t)row * a.H + c * 8) = q;
-            if ((c & 3) == 0)
-                a.xsf[((int64_t)my_tile[j] * a.ks + kg) * 512 + 16 * (my_in[j] & 31) +
-                      4 * (my_in[j] >> 5) + b] = (uint8_t)(__float_as_uint(s) >> 23);
-        }
-    }
-}
-
-// out[t, h] = sum_j w[t, j] y[pos[t, j], h], j in order; four values a thread.
-template <bool F32>
-__global__ void __launch_bounds__(256) moe_combine_kernel(const float *__restrict__ y,
-                                                          const int32_t *__restrict__ pos,
-                                                          const float *__restrict__ w, int32_t k,
-                                                          int32_t H, void *__restrict__ out) {
-    ptx::grid_dep_wait();
-    ptx::grid_dep_launch();
-    const int t = blockIdx.y, h = (blockIdx.x * 256 + threadIdx.x) * 4;
-    if (h >= H) return;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j = 0; j < k; ++j) {
-        const int r = __ldcg(pos + t * k + j);
-        if (r < 0) continue;
-        const float c = __ldg(w + t * k + j);
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(y + (int64_t)r * H + h));
-        s.x = fmaf(c, v.x, s.x);
-        s.y = fmaf(c, v.y, s.y);
-        s.z = fmaf(c, v.z, s.z);
-        s.w = fmaf(c, v.w, s.w);
-    }
-    const int64_t at = (int64_t)t * H + h;
-    if constexpr (F32) {
-        *reinterpret_cast<float4 *>(static_cast<float *>(out) + at) = s;
-    } else {
-        __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(out) + at) =
-            make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
-    }
-}
 
 bool is_aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool packed(int f) { return f == FP8G_E2M1 || f == FP8G_E2M3 || f == FP8G_E3M2; }
@@ -265,105 +119,76 @@ fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t *ids, co
     const int R = (int)(T * k), nb = (int)(T < kStreamMaxTokens ? round_up(T, 16) : kStreamMaxTokens);
     // groups: each expert's rows in tiles of nb
     const int max_groups = (int)((E < R ? E : R) + R / nb);
-    StreamParams p1{}, p2{};
-    stream_sizes(p1, nb, 1);
-    stream_sizes(p2, nb, 1);
-    p1.mt = (int32_t)((F + 127) / 128);
-    p1.ks = (int32_t)((H + 127) / 128);
-    p1.rows = (int32_t)F;
-    p1.n_rt = p1.mt;
-    p2.mt = (int32_t)((H + 255) / 256);
-    p2.ks = p1.mt;
-    p2.rows = (int32_t)H;
-    p2.n_rt = p1.ks;
-    const int64_t units1 = (int64_t)p1.mt * p1.ks, units2 = (int64_t)p2.mt * p2.ks;
-    if (max_groups > kStreamMaxGroups || units1 * max_groups >= INT32_MAX ||
-        units2 * max_groups >= INT32_MAX)
-        return FP8G_ERR_UNSUPPORTED_SHAPE;
+    StreamParams p{};
+    stream_sizes(p, nb, false, 1);
+    StreamPhase &g = p.ph[0], &dn = p.ph[1];
+    g.sub = dn.sub = 2;
+    g.mt = (int32_t)((F + 127) / 128);
+    g.ks = (int32_t)((H + 127) / 128);
+    g.rows = (int32_t)F;
+    g.n_rt = g.mt;
+    dn.mt = (int32_t)((H + 255) / 256);
+    dn.ks = g.mt;
+    dn.rows = (int32_t)H;
+    dn.n_rt = g.ks;
+    if (max_groups > kStreamMaxGroups || (int64_t)g.mt * g.ks >= INT32_MAX) return FP8G_ERR_UNSUPPORTED_SHAPE;
 
-    // one temporary: [codes x][scales x][codes h][scales h][y][partials][tables]
+    // one temporary
     size_t at = 0;
     auto take = [&at](size_t bytes) {
         const size_t o = at;
         at += (bytes + 1023) / 1024 * 1024;
         return o;
     };
-    const size_t o_xq = take((size_t)R * H), o_xsf = take((size_t)max_groups * p1.ks * 512);
-    const size_t o_hq = take((size_t)R * F), o_hsf = take((size_t)max_groups * p1.mt * 512);
-    const size_t o_y = take((size_t)R * H * 4), o_part = take(stream_part_bytes(p1, d.num_sms));
-    const int n_cnt = max_groups * (p1.mt + p2.mt);
-    const size_t o_cnt = take((size_t)n_cnt * 4), o_pos = take((size_t)R * 4);
+    const size_t o_xq = take((size_t)R * H), o_xsf = take((size_t)max_groups * g.ks * 512);
+    const size_t o_hq = take((size_t)R * F), o_hsf = take((size_t)max_groups * g.mt * 512);
+    const size_t o_y = take((size_t)R * H * 4), o_part = take(stream_part_bytes(p, d.num_sms));
+    const size_t o_pos = take((size_t)R * 4), o_flags = take(stream_flag_bytes(d.num_sms));
     cudaMemPool_t pool;
     if ((st = host_pool(d.dev, pool)) != FP8G_OK) return st;
     void *wsv = nullptr;
     if (cudaMallocFromPoolAsync(&wsv, at, pool, stream) != cudaSuccess) return FP8G_ERR_CUDA;
     uint8_t *ws = static_cast<uint8_t *>(wsv);
-
-    CUtensorMap m13, m2, mx, mh;
     {
         const uint32_t bw[3] = {(uint32_t)kBK, 128u, 1u}, bx[2] = {(uint32_t)kBK, 16u};
         const uint64_t d13[3] = {(uint64_t)H, (uint64_t)F, (uint64_t)(2 * E)};
         const uint64_t d2[3] = {(uint64_t)F, (uint64_t)H, (uint64_t)E};
         const uint64_t dx[2] = {(uint64_t)H, (uint64_t)R}, dh[2] = {(uint64_t)F, (uint64_t)R};
-        st = host_operand_map(W13, w_fmt, 3, d13, bw, d.dev, m13);
-        if (st == FP8G_OK) st = host_operand_map(W2, w_fmt, 3, d2, bw, d.dev, m2);
-        if (st == FP8G_OK) st = host_operand_map(ws + o_xq, FP8G_E4M3, 2, dx, bx, d.dev, mx);
-        if (st == FP8G_OK) st = host_operand_map(ws + o_hq, FP8G_E4M3, 2, dh, bx, d.dev, mh);
+        st = host_operand_map(W13, w_fmt, 3, d13, bw, d.dev, g.W);
+        if (st == FP8G_OK) st = host_operand_map(W2, w_fmt, 3, d2, bw, d.dev, dn.W);
+        if (st == FP8G_OK) st = host_operand_map(ws + o_xq, FP8G_E4M3, 2, dx, bx, d.dev, g.X);
+        if (st == FP8G_OK) st = host_operand_map(ws + o_hq, FP8G_E4M3, 2, dh, bx, d.dev, dn.X);
     }
-    cudaError_t e = st == FP8G_OK ? cudaSuccess : cudaErrorInvalidValue;
-    int32_t *cnt = reinterpret_cast<int32_t *>(ws + o_cnt);
-    int32_t *pos = reinterpret_cast<int32_t *>(ws + o_pos);
-    if (e == cudaSuccess) {
-        PrepArgs a{};
-        a.x = x;
-        a.ids = ids;
-        a.T = (int32_t)T;
-        a.k = k;
-        a.E = E;
-        a.H = (int32_t)H;
-        a.nb = nb;
-        a.ks = p1.ks;
-        a.xq = ws + o_xq;
-        a.xsf = ws + o_xsf;
-        a.pos = pos;
-        a.cnt = cnt;
-        a.n_cnt = n_cnt;
-        a.status = d.status;
-        e = x_dtype == FP8G_IN_BF16
-                ? launch_programmatic(moe_prep_kernel<true>, dim3((unsigned)T), dim3(kPrepThreads), stream, a)
-                : launch_programmatic(moe_prep_kernel<false>, dim3((unsigned)T), dim3(kPrepThreads), stream,
-                                      a);
-    }
-    for (StreamParams *p : {&p1, &p2}) {
-        p->w_fmt = host_mma_type(w_fmt) << 7;
-        p->gap8 = host_gap8(w_fmt);
-        p->idx = ids;
-        p->n_idx = R;
-        p->n_mat = E;
-        p->part = reinterpret_cast<float *>(ws + o_part);
-        p->status = d.status;
-        p->timeout_ns = d.timeout_ns;
-    }
-    p1.sfw = sf13;
-    p1.sfx = ws + o_xsf;
-    p1.tile_cnt = cnt;
-    p1.gate = gate;
-    p1.hq = ws + o_hq;
-    p1.hsf = ws + o_hsf;
-    p2.sfw = sf2;
-    p2.sfx = ws + o_hsf;
-    p2.tile_cnt = cnt + (size_t)max_groups * p1.mt;
-    p2.y = reinterpret_cast<float *>(ws + o_y);
-    if (e == cudaSuccess) e = launch_stream(kStreamGated, m13, mx, mx, mx, p1, d.num_sms, stream);
-    if (e == cudaSuccess) e = launch_stream(kStreamRows, m2, mh, mh, mh, p2, d.num_sms, stream);
-    if (e == cudaSuccess) {
-        const dim3 grid((unsigned)((H / 4 + 255) / 256), (unsigned)T);
-        e = out_dtype == FP8G_OUT_F32
-                ? launch_programmatic(moe_combine_kernel<true>, grid, dim3(256), stream, p2.y, pos, weights,
-                                      k, (int32_t)H, out)
-                : launch_programmatic(moe_combine_kernel<false>, grid, dim3(256), stream, p2.y, pos, weights,
-                                      k, (int32_t)H, out);
-    }
+    g.sfw = sf13;
+    g.sfx = ws + o_xsf;
+    dn.sfw = sf2;
+    dn.sfx = ws + o_hsf;
+    p.w_fmt = host_mma_type(w_fmt) << 7;
+    p.gap8 = host_gap8(w_fmt);
+    p.x = x;
+    p.x_bf16 = x_dtype == FP8G_IN_BF16;
+    p.T = (int32_t)T;
+    p.K = (int32_t)H;
+    p.idx = ids;
+    p.n_idx = R;
+    p.n_mat = E;
+    p.xq = ws + o_xq;
+    p.xsf = ws + o_xsf;
+    p.part = reinterpret_cast<float *>(ws + o_part);
+    p.flags = reinterpret_cast<uint64_t *>(ws + o_flags);
+    p.token = stream_token();
+    p.out = out;
+    p.out_f32 = out_dtype == FP8G_OUT_F32;
+    p.status = d.status;
+    p.timeout_ns = d.timeout_ns;
+    p.k = k;
+    p.gate = gate;
+    p.weights = weights;
+    p.pos = reinterpret_cast<int32_t *>(ws + o_pos);
+    p.hq = ws + o_hq;
+    p.hsf = ws + o_hsf;
+    p.y = reinterpret_cast<float *>(ws + o_y);
+    const cudaError_t e = st == FP8G_OK ? launch_stream(false, p, d.num_sms, stream) : cudaErrorInvalidValue;
     const cudaError_t ef = cudaFreeAsync(wsv, stream);
     if (st != FP8G_OK) return st;
     return e == cudaSuccess && ef == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;

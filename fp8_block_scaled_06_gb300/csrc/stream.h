@@ -1,82 +1,79 @@
-// The streaming GEMM kernel (stream.cu): few tokens against block-scaled
-// weights that are read once.  Declarations shared by its users.
+// The streaming kernel (stream.cu): few tokens against block-scaled weights
+// that are read once.  Declarations shared by its users (moe.cu, lora.cu).
 #pragma once
 #include "internal.h"
 
 namespace fp8g {
 
-// One group: up to nb token rows against one weight matrix.
-struct StreamGroup {
-    int32_t mat;    // weight matrix (expert)
-    int32_t row0;   // first token row of the operand
-    int32_t n;      // token rows
-    int32_t unit0;  // work units of the groups before it
-};
-
+constexpr int kStreamMaxTokens = 128;    // token rows of a group
 constexpr int kStreamMaxGroups = 320;
-constexpr int kStreamMaxLoraRows = 512;  // token rows of a call with low-rank steps
-constexpr int kMaxAdapters = 1024;
-constexpr int kStreamMaxTokens = 128;  // token rows of a group
-constexpr int kStreamMinUnits = 4;     // work units a CTA takes at least
+constexpr int kStreamLoraRows = 512;     // token rows of a call with adapters
+constexpr int kStreamLoraGroups = kStreamLoraRows / kStreamMaxTokens;
+constexpr int kStreamFlags = 5;          // flag arrays (stream.cu)
 
-enum StreamEpi : int {
-    kStreamGated = 0,  // act(gate) * up, quantised to E4M3 with 1x32 scales
-    kStreamRows = 1,   // fp32 rows
-    kStreamOut = 2,    // output rows with bias; low-rank steps
-};
-
-struct StreamParams {
-    int32_t sub;     // 128-row weight tiles of a work unit (2, or 1; gated: 2)
-    int32_t mt;      // weight-row tiles (of sub 128 rows; gated: 128 features) per group
-    int32_t ks;      // 128-wide K steps
-    int32_t rows;    // rows of a weight matrix (gated: of each half)
-    int32_t n_rt;    // 128-row tiles of packed scales per matrix
-    int32_t nb;      // token columns per accumulator (a multiple of 16)
-    int32_t nacc;    // accumulators (2: a tile's epilogue overlaps the next tile)
-    int32_t stages, stage_bytes, x_bytes;  // shared-memory ring
-    uint32_t w_fmt;  // weight format as MMA instruction-descriptor bits
-    int32_t gap8;    // eighths of a weight tile a packed load does not deliver
-    const uint8_t *sfw;      // packed weight scales [matrix][ks][n_rt][512]
-    const uint8_t *sfx;      // packed token scales [group][ks][512]
-    // the groups, which every CTA derives from its call's routing: `n_idx`
-    // indices idx[]: expert of each pair (negative or >= n_mat: none), or
-    // (kStreamOut) adapter of each token row
-    const int32_t *idx;
-    int32_t n_idx, n_mat;
-    int32_t *tile_cnt;       // [group][mt] units done of split tiles, zero at the start
-    float *part;             // partial tiles [2 grid][2][nb][128]
-    unsigned int *status;
-    uint64_t timeout_ns;
-    // gated
-    int32_t gate;
-    uint8_t *hq;             // codes [rows of tokens][rows]
-    uint8_t *hsf;            // packed scales [group][mt][512]
-    // rows
-    float *y;                // [rows of tokens][rows]
-    // out
-    void *c;                 // [tokens][rows]
-    int32_t out_f32;
-    const float *bias;
-    // low-rank: rank, steps per slot (0: none), slots per group, rows of V a
-    // slot has (LoraV); n_mat adapters
-    int32_t rank, kr, slot_cap, v_rows;
-};
-
-// V of a slot.  Rank up to 32: a row of 64 values holds both halves, hi in
-// columns 0-31 and lo in 32-63, one 64-wide step.  More: rows of r64 = rank
-// rounded up to 64, the hi rows first, then the lo rows, r64 / 64 steps.
+// V = alpha A x of a slot (an adapter of a row tile) as two bf16 halves, V = hi
+// + lo to 16 bits.  Rank up to 32: a row of 64 values holds both, hi in
+// columns 0-31 and lo in 32-63: one 64-wide step.  More: rows of r64 = rank
+// rounded up to 64, the tile's hi rows first, then its lo rows: r64 / 64 steps.
 struct LoraV {
-    bool wide;  // halves in rows of their own
+    bool wide;            // halves in rows of their own
     int r64, kr, halves;  // row length, steps per slot, blocks of rows
     explicit LoraV(int rank)
         : wide(rank > 32), r64(wide ? (rank + 63) / 64 * 64 : 64), kr(r64 / 64), halves(wide ? 2 : 1) {}
 };
 
-// Ring and accumulator sizes for nb token columns; v_halves 2: V's two halves
-// share the token region of a stage.
-void stream_sizes(StreamParams &p, int nb, int v_halves);
+// One product: weights [n_mat][rows][K] against a group's token rows.
+struct StreamPhase {
+    CUtensorMap W, X;      // weights (box 128 x 128 rows), token codes (box 128 x 16 rows)
+    const uint8_t *sfw;    // packed weight scales [matrix][ks][n_rt][512]
+    const uint8_t *sfx;    // packed token scales [group][ks][512]
+    int32_t sub;           // 128-row weight tiles of a work unit: 2 or 1 (gated: gate and up rows)
+    int32_t mt;            // tiles of sub * 128 rows (gated: of 128 features)
+    int32_t ks;            // 128-wide K steps
+    int32_t rows;          // rows of a weight matrix (gated: of each half)
+    int32_t n_rt;          // 128-row tiles of packed scales per matrix
+};
+
+struct StreamParams {
+    StreamPhase ph[2];     // MoE: gate/up and down products; adapters: ph[0]
+    int32_t nb;            // token columns of an accumulator (a multiple of 16)
+    int32_t nacc;          // accumulators (2: a tile's epilogue overlaps the next tile)
+    int32_t stages, stage_bytes, x_bytes;  // shared-memory ring
+    uint32_t w_fmt;        // weight format as MMA instruction-descriptor bits
+    int32_t gap8;          // eighths of a weight tile a packed load does not deliver
+    const void *x;         // tokens, fp32 or bf16
+    int32_t x_bf16;
+    int32_t T, K;          // token rows, their length
+    const int32_t *idx;    // MoE: expert of each pair [T][k]; adapters: adapter of each row [T]
+    int32_t n_idx, n_mat;  // their number; experts / adapters
+    uint8_t *xq, *xsf;     // token codes (MoE: expert order) and packed scales
+    float *part;           // partial tiles [grid][sub][nb][128]
+    uint64_t *flags;       // [kStreamFlags][grid]
+    uint64_t token;        // this call's, unlike any other call's
+    void *out;
+    int32_t out_f32;
+    unsigned int *status;
+    uint64_t timeout_ns;
+    // MoE
+    int32_t k, gate;
+    const float *weights;  // [T][k]
+    int32_t *pos;          // [T k] row of a pair in expert order, -1: none
+    uint8_t *hq, *hsf;     // h: codes [T k][F] and packed scales
+    float *y;              // [T k][H]
+    // adapters
+    CUtensorMap B, V;
+    const void *a;         // bf16 [L][rank][K]
+    const float *alpha;    // [L] or null
+    const float *bias;     // [N] or null
+    void *v;               // bf16 [group][slot_cap][halves * nb][r64]
+    int32_t rank, kr, r64, halves, slot_cap;  // kr 0: no adapters
+};
+
+// Ring and accumulator sizes for nb token columns.
+void stream_sizes(StreamParams &p, int nb, bool lora, int v_halves);
 size_t stream_part_bytes(const StreamParams &p, int grid);
-cudaError_t launch_stream(int epi, const CUtensorMap &w, const CUtensorMap &x, const CUtensorMap &lb,
-                          const CUtensorMap &v, const StreamParams &p, int grid, cudaStream_t s);
+size_t stream_flag_bytes(int grid);
+uint64_t stream_token();
+cudaError_t launch_stream(bool lora, const StreamParams &p, int grid, cudaStream_t s);
 
 }  // namespace fp8g
