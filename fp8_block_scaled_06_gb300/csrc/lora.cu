@@ -2,7 +2,7 @@
 //
 //   C[i] = out( Q(x_i) W^T + bias + alpha_l B_l (A_l x_i) ),  l = adapter[i]
 //
-// Few rows: one launch of the streaming kernel (stream.cu).  Many: the rows
+// Few rows: the streaming kernels (stream.cu).  Many: the rows
 // quantised, V = alpha A x, then the CTA-pair product (gemm_pair.cu).  In both V
 // is taken against the adapters' B rows as further K steps into the product's
 // fp32 accumulator, so the sum is rounded once.
@@ -311,7 +311,7 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
 
     const LoraV lv(lora ? r : 1);
     const bool pair = M > kStreamLoraRows;
-    const int nb = pair ? 256 : (int)(M < kStreamMaxTokens ? (M + 15) / 16 * 16 : kStreamMaxTokens);
+    const int nb = pair ? 256 : stream_columns(M);
     const int tiles = (int)((M + nb - 1) / nb), cap = L < nb ? L : nb;
     const int32_t ks = (int32_t)((K + 127) / 128), n_rt = (int32_t)((N + 127) / 128);
     const int32_t n_rtA = (int32_t)((M + 127) / 128);
@@ -321,9 +321,10 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
     StreamParams p{};
     StreamPhase &h = p.ph[0];
     if (!pair) {
-        stream_sizes(p, nb, true, lv.halves);
-        h.sub = 2;
-        h.mt = (int32_t)((N + 255) / 256);
+        // one weight tile a unit where pairs of them would be few
+        h.sub = tiles * ((N + 255) / 256) * 8 >= d.num_sms * 5 ? 2 : 1;
+        stream_sizes(p, nb, h.sub, true, lv.halves);
+        h.mt = (int32_t)((N + 128 * h.sub - 1) / (128 * h.sub));
         h.ks = ks;
         h.rows = (int32_t)N;
         h.n_rt = n_rt;
@@ -339,7 +340,8 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
     const size_t o_xq = take((size_t)M * K), o_xsf = take((size_t)(pair ? n_rtA : tiles) * ks * 512);
     const size_t o_v = take((size_t)tiles * cap * lv.halves * nb * lv.r64 * 2);
     const size_t o_part = take(pair ? (size_t)tiles * 4 : stream_part_bytes(p, d.num_sms));
-    const size_t o_flags = take(pair ? (size_t)tiles * cap * 4 : stream_flag_bytes(d.num_sms));
+    p.n_counters = 1 + kStreamSplitTiles;
+    const size_t o_cnt = take(pair ? (size_t)tiles * cap * 4 : (size_t)p.n_counters * 4);
     cudaMemPool_t pool;
     if ((st = host_pool(d.dev, pool)) != FP8G_OK) return st;
     void *wsv = nullptr;
@@ -362,7 +364,9 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
         const uint64_t dx[2] = {(uint64_t)K, (uint64_t)M};
         const uint32_t bx[2] = {(uint32_t)kBK, 16u};
         st = host_operand_map(W, w_fmt, 3, dw, bw, d.dev, h.W);
+        const uint32_t by[2] = {(uint32_t)kBK, 64u};
         if (st == FP8G_OK) st = host_operand_map(ws + o_xq, FP8G_E4M3, 2, dx, bx, d.dev, h.X);
+        if (st == FP8G_OK && nb % 64 == 0) st = host_operand_map(ws + o_xq, FP8G_E4M3, 2, dx, by, d.dev, h.X64);
         h.sfw = sfw;
         h.sfx = ws + o_xsf;
         p.w_fmt = host_mma_type(w_fmt) << 7;
@@ -376,9 +380,9 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
         p.n_mat = L;
         p.xq = ws + o_xq;
         p.xsf = ws + o_xsf;
-        p.part = reinterpret_cast<float *>(ws + o_part);
-        p.flags = reinterpret_cast<uint64_t *>(ws + o_flags);
-        p.token = stream_token();
+        p.counters = reinterpret_cast<int32_t *>(ws + o_cnt);
+        h.part = reinterpret_cast<float *>(ws + o_part);
+        h.part_cnt = p.counters + 1;
         p.out = C;
         p.out_f32 = out == FP8G_OUT_F32;
         p.status = d.status;
@@ -415,7 +419,7 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
         a.tiles = tiles;
         a.v = reinterpret_cast<__nv_bfloat16 *>(ws + o_v);
         a.slot_cnt = reinterpret_cast<int32_t *>(ws + o_part);
-        a.slot_adapter = reinterpret_cast<int32_t *>(ws + o_flags);
+        a.slot_adapter = reinterpret_cast<int32_t *>(ws + o_cnt);
         a.items = nb / 16 + cap;  // at most one partly filled item per slot beside the whole ones
         a.status = d.status;
         e = bf16 ? launch_programmatic(lora_quant_kernel<true>, dim3((unsigned)M), dim3(256), stream, a)

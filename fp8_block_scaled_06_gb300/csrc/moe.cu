@@ -6,7 +6,7 @@
 //   hq = Q(act(g) u)                 act and product in fp32
 //   out[t] = sum_j w[t, j] hq W2[e]^T   fp32 sum over j in order, one rounding
 //
-// One launch (stream.cu).  The weights of the chosen experts are read once;
+// Two launches (stream.cu).  The weights of the chosen experts are read once;
 // everything else is a few hundred kilobytes.
 #include "stream.h"
 
@@ -17,8 +17,6 @@ namespace {
 bool is_aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool packed(int f) { return f == FP8G_E2M1 || f == FP8G_E2M3 || f == FP8G_E3M2; }
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
-
-int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
 }  // namespace
 
@@ -116,11 +114,11 @@ fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t *ids, co
     if (st != FP8G_OK) return st;
     if (T == 0) return FP8G_OK;
 
-    const int R = (int)(T * k), nb = (int)(T < kStreamMaxTokens ? round_up(T, 16) : kStreamMaxTokens);
+    const int R = (int)(T * k), nb = stream_columns(T);
     // groups: each expert's rows in tiles of nb
     const int max_groups = (int)((E < R ? E : R) + R / nb);
     StreamParams p{};
-    stream_sizes(p, nb, false, 1);
+    stream_sizes(p, nb, 2, false, 1);
     StreamPhase &g = p.ph[0], &dn = p.ph[1];
     g.sub = dn.sub = 2;
     g.mt = (int32_t)((F + 127) / 128);
@@ -131,7 +129,9 @@ fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t *ids, co
     dn.ks = g.mt;
     dn.rows = (int32_t)H;
     dn.n_rt = g.ks;
-    if (max_groups > kStreamMaxGroups || (int64_t)g.mt * g.ks >= INT32_MAX) return FP8G_ERR_UNSUPPORTED_SHAPE;
+    if (max_groups > kStreamMaxGroups || (int64_t)max_groups * g.mt * g.ks >= INT32_MAX ||
+        (int64_t)max_groups * dn.mt * dn.ks >= INT32_MAX)
+        return FP8G_ERR_UNSUPPORTED_SHAPE;
 
     // one temporary
     size_t at = 0;
@@ -142,8 +142,10 @@ fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t *ids, co
     };
     const size_t o_xq = take((size_t)R * H), o_xsf = take((size_t)max_groups * g.ks * 512);
     const size_t o_hq = take((size_t)R * F), o_hsf = take((size_t)max_groups * g.mt * 512);
-    const size_t o_y = take((size_t)R * H * 4), o_part = take(stream_part_bytes(p, d.num_sms));
-    const size_t o_pos = take((size_t)R * 4), o_flags = take(stream_flag_bytes(d.num_sms));
+    const size_t o_y = take((size_t)R * H * 4), o_pos = take((size_t)R * 4);
+    const size_t o_part0 = take(stream_part_bytes(p, d.num_sms)), o_part1 = take(stream_part_bytes(p, d.num_sms));
+    p.n_counters = 1 + max_groups + dn.mt + 2 * kStreamSplitTiles;
+    const size_t o_cnt = take((size_t)p.n_counters * 4);
     cudaMemPool_t pool;
     if ((st = host_pool(d.dev, pool)) != FP8G_OK) return st;
     void *wsv = nullptr;
@@ -151,6 +153,7 @@ fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t *ids, co
     uint8_t *ws = static_cast<uint8_t *>(wsv);
     {
         const uint32_t bw[3] = {(uint32_t)kBK, 128u, 1u}, bx[2] = {(uint32_t)kBK, 16u};
+        const uint32_t by[2] = {(uint32_t)kBK, 64u};
         const uint64_t d13[3] = {(uint64_t)H, (uint64_t)F, (uint64_t)(2 * E)};
         const uint64_t d2[3] = {(uint64_t)F, (uint64_t)H, (uint64_t)E};
         const uint64_t dx[2] = {(uint64_t)H, (uint64_t)R}, dh[2] = {(uint64_t)F, (uint64_t)R};
@@ -158,6 +161,10 @@ fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t *ids, co
         if (st == FP8G_OK) st = host_operand_map(W2, w_fmt, 3, d2, bw, d.dev, dn.W);
         if (st == FP8G_OK) st = host_operand_map(ws + o_xq, FP8G_E4M3, 2, dx, bx, d.dev, g.X);
         if (st == FP8G_OK) st = host_operand_map(ws + o_hq, FP8G_E4M3, 2, dh, bx, d.dev, dn.X);
+        if (nb % 64 == 0) {
+            if (st == FP8G_OK) st = host_operand_map(ws + o_xq, FP8G_E4M3, 2, dx, by, d.dev, g.X64);
+            if (st == FP8G_OK) st = host_operand_map(ws + o_hq, FP8G_E4M3, 2, dh, by, d.dev, dn.X64);
+        }
     }
     g.sfw = sf13;
     g.sfx = ws + o_xsf;
@@ -174,9 +181,13 @@ fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t *ids, co
     p.n_mat = E;
     p.xq = ws + o_xq;
     p.xsf = ws + o_xsf;
-    p.part = reinterpret_cast<float *>(ws + o_part);
-    p.flags = reinterpret_cast<uint64_t *>(ws + o_flags);
-    p.token = stream_token();
+    p.counters = reinterpret_cast<int32_t *>(ws + o_cnt);
+    p.done_group = p.counters + 1;
+    p.done_tile = p.done_group + max_groups;
+    g.part = reinterpret_cast<float *>(ws + o_part0);
+    g.part_cnt = p.done_tile + dn.mt;
+    dn.part = reinterpret_cast<float *>(ws + o_part1);
+    dn.part_cnt = g.part_cnt + kStreamSplitTiles;
     p.out = out;
     p.out_f32 = out_dtype == FP8G_OUT_F32;
     p.status = d.status;

@@ -1,5 +1,5 @@
-// The streaming kernel (stream.cu): few tokens against block-scaled weights
-// that are read once.  Declarations shared by its users (moe.cu, lora.cu).
+// The streaming kernels (stream.cu): few tokens against block-scaled weights
+// that are read once.  Declarations shared by their users (moe.cu, lora.cu).
 #pragma once
 #include "internal.h"
 
@@ -9,7 +9,7 @@ constexpr int kStreamMaxTokens = 128;    // token rows of a group
 constexpr int kStreamMaxGroups = 320;
 constexpr int kStreamLoraRows = 512;     // token rows of a call with adapters
 constexpr int kStreamLoraGroups = kStreamLoraRows / kStreamMaxTokens;
-constexpr int kStreamFlags = 5;          // flag arrays (stream.cu)
+constexpr int kStreamSplitTiles = 256;   // a product with as many tiles is not split
 
 // V = alpha A x of a slot (an adapter of a row tile) as two bf16 halves, V = hi
 // + lo to 16 bits.  Rank up to 32: a row of 64 values holds both, hi in
@@ -24,21 +24,23 @@ struct LoraV {
 
 // One product: weights [n_mat][rows][K] against a group's token rows.
 struct StreamPhase {
-    CUtensorMap W, X;      // weights (box 128 x 128 rows), token codes (box 128 x 16 rows)
+    CUtensorMap W, X, X64; // weights (box 128 x 128 rows), token codes (boxes 128 x 16 and 64 rows)
     const uint8_t *sfw;    // packed weight scales [matrix][ks][n_rt][512]
     const uint8_t *sfx;    // packed token scales [group][ks][512]
-    int32_t sub;           // 128-row weight tiles of a work unit: 2 or 1 (gated: gate and up rows)
+    int32_t sub;           // 128-row weight tiles of a step: 2 or 1 (gated: gate and up rows)
     int32_t mt;            // tiles of sub * 128 rows (gated: of 128 features)
     int32_t ks;            // 128-wide K steps
     int32_t rows;          // rows of a weight matrix (gated: of each half)
     int32_t n_rt;          // 128-row tiles of packed scales per matrix
+    float *part;           // partial tiles [tile][part][2][nb][128]
+    int32_t *part_cnt;     // [kStreamSplitTiles] parts done of a tile
 };
 
 struct StreamParams {
     StreamPhase ph[2];     // MoE: gate/up and down products; adapters: ph[0]
     int32_t nb;            // token columns of an accumulator (a multiple of 16)
     int32_t nacc;          // accumulators (2: a tile's epilogue overlaps the next tile)
-    int32_t stages, stage_bytes, x_bytes;  // shared-memory ring
+    int32_t stages, stage_bytes, w_bytes, x_bytes;  // shared-memory ring: a stage, its weights, its tokens
     uint32_t w_fmt;        // weight format as MMA instruction-descriptor bits
     int32_t gap8;          // eighths of a weight tile a packed load does not deliver
     const void *x;         // tokens, fp32 or bf16
@@ -47,9 +49,12 @@ struct StreamParams {
     const int32_t *idx;    // MoE: expert of each pair [T][k]; adapters: adapter of each row [T]
     int32_t n_idx, n_mat;  // their number; experts / adapters
     uint8_t *xq, *xsf;     // token codes (MoE: expert order) and packed scales
-    float *part;           // partial tiles [grid][sub][nb][128]
-    uint64_t *flags;       // [kStreamFlags][grid]
-    uint64_t token;        // this call's, unlike any other call's
+    // counters, zeroed by the preparing kernel: [0] the next ticket, then (MoE)
+    // gated tiles done per group, groups done per tile of the down product,
+    // and the products' part counters
+    int32_t *counters;
+    int32_t n_counters;
+    int32_t *done_group, *done_tile;
     void *out;
     int32_t out_f32;
     unsigned int *status;
@@ -69,11 +74,13 @@ struct StreamParams {
     int32_t rank, kr, r64, halves, slot_cap;  // kr 0: no adapters
 };
 
-// Ring and accumulator sizes for nb token columns.
-void stream_sizes(StreamParams &p, int nb, bool lora, int v_halves);
-size_t stream_part_bytes(const StreamParams &p, int grid);
-size_t stream_flag_bytes(int grid);
-uint64_t stream_token();
-cudaError_t launch_stream(bool lora, const StreamParams &p, int grid, cudaStream_t s);
+// Token columns for groups of up to n rows.
+inline int stream_columns(int64_t n) { return n <= 64 ? (int)((n + 15) / 16 * 16) : kStreamMaxTokens; }
+// Ring and accumulator sizes for nb token columns, sub weight tiles a stage.
+void stream_sizes(StreamParams &p, int nb, int sub, bool lora, int v_halves);
+// Bytes of a product's partial tiles; SMs of the device.
+size_t stream_part_bytes(const StreamParams &p, int num_sms);
+// Prepares the tokens, then runs the products: two launches.
+cudaError_t launch_stream(bool lora, const StreamParams &p, int num_sms, cudaStream_t s);
 
 }  // namespace fp8g
