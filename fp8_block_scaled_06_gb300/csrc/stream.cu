@@ -645,9 +645,12 @@ __device__ __forceinline__ void load_weights(const StreamParams &p, Tail<LORA> &
         ++q.i;
         Tile o;
         if (!decode(p, t, ticket, o)) return;
-        next = atomicAdd(p.counters, 1);  // there by the time this tile's loads are out
         const StreamPhase &h = p.ph[o.ph];
+        const int ask = max(o.k0, o.k1 - 2);
         for (int k = o.k0; k < o.k1; ++k) {
+            // late enough that a CTA does not hold a tile others could start,
+            // early enough that the answer is there when this tile's loads are out
+            if (k == ask) next = atomicAdd(p.counters, 1);
             if (!wait_bar(ptx::smem_addr(&t.empty[r.stage]), r.phase ^ 1u, abort_flag, p, r.stage)) return;
             const uint32_t fb = ptx::smem_addr(&t.full[r.stage]), s0 = sbase + r.stage * p.stage_bytes;
             const Step st = step_of(p, t, o, k);
@@ -757,7 +760,18 @@ __device__ __forceinline__ int acc_of(const StreamParams &p, int lt, uint32_t &p
     return p.nacc == 2 ? (lt & 1) : 0;
 }
 
-// Warp 1.
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// Warp 1.  The whole warp goes through the loop and one lane issues: operands
+// that the compiler knows to be the same in all lanes are in uniform registers
+// already (from a branch for lane 0 alone a step's eight MMAs took 0.4 us to
+// issue, more than 4-bit weights take to load).
 template <bool LORA>
 __device__ __forceinline__ void issue_mmas(const StreamParams &p, Tail<LORA> &t, uint32_t sbase, uint32_t tmem,
                                            uint32_t sf_tmem) {
@@ -765,53 +779,60 @@ __device__ __forceinline__ void issue_mmas(const StreamParams &p, Tail<LORA> &t,
     Ring r;
     Queue q;
     Tile o;
-    for (int lt = 0; take<LORA, false>(p, t, q, o, 1); ++lt) {
+    // matrix descriptors of stage 0; a stage on: stage16 more
+    const uint64_t w_desc = ptx::desc_kmajor_sw128(sbase), x_desc = ptx::desc_kmajor_sw128(sbase + p.w_bytes);
+    const uint32_t stage16 = (uint32_t)p.stage_bytes >> 4, tile16 = kWTile >> 4;
+    for (int lt = 0; take<LORA, true>(p, t, q, o, 1); ++lt) {
         uint32_t par;
         const int acc = acc_of(p, lt, par);
-        if (!wait_bar(ptx::smem_addr(&t.acce[acc]), par ^ 1u, abort_flag, p, 256 + 64 + acc)) return;
+        if (!wait_bar_warp(ptx::smem_addr(&t.acce[acc]), par ^ 1u, abort_flag, p, 256 + 64 + acc)) return;
         ptx::tc_fence_after();
+        const int k0 = uniform(o.k0), k1 = uniform(o.k1), n16 = uniform(o.n16), fp8 = p.ph[0].ks;
+        const bool has1 = uniform(o.has1) != 0;
         const uint32_t d0 = tmem + acc * 2 * p.nb, d1 = d0 + p.nb;
-        const uint32_t id8 = ptx::idesc_mxf8(128, 0, 0) | (uint32_t)(o.n16 >> 3) << 17 | p.w_fmt;
-        for (int k = o.k0; k < o.k1; ++k) {
-            if (!wait_bar(ptx::smem_addr(&t.sfr[r.stage]), r.phase, abort_flag, p, 256 + r.stage)) return;
+        const uint32_t id8 = ptx::idesc_mxf8(128, 0, 0) | (uint32_t)(n16 >> 3) << 17 | p.w_fmt;
+        for (int k = k0; k < k1; ++k) {
+            if (!wait_bar_warp(ptx::smem_addr(&t.sfr[r.stage]), r.phase, abort_flag, p, 256 + r.stage)) return;
             ptx::tc_fence_after();
-            const uint32_t s0 = sbase + r.stage * p.stage_bytes, x0 = s0 + p.w_bytes;
-            const Step st = step_of(p, t, o, k);
-            if (st.fp8) {
+            const uint32_t at = r.stage * stage16;
+            if (!LORA || k < fp8) {
                 const uint32_t sf = sf_tmem + r.stage * kSfSlot;
+                const uint32_t first = k == k0 ? 0u : 1u;
+                if (elect_one()) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t id = id8 | ((uint32_t)j << 4) | ((uint32_t)j << 29);
-                    const uint32_t on = (k != o.k0 || j != 0) ? 1u : 0u;
-                    const uint64_t dx = ptx::desc_kmajor_sw128(x0 + 32 * j);
-                    ptx::mma_mxf8(d0, ptx::desc_kmajor_sw128(s0 + 32 * j), dx, id, sf, sf + 8, on);
-                    if (o.has1)
-                        ptx::mma_mxf8(d1, ptx::desc_kmajor_sw128(s0 + kWTile + 32 * j), dx, id, sf + 4, sf + 8,
-                                      on);
-                }
-            } else {
-                const int nk = (min(64, p.rank - st.c) + 15) / 16;
-                const uint32_t id16 = ptx::idesc_bf16(128, 0) | (uint32_t)(st.n >> 3) << 17;
-                // the lo half: rows of its own, or columns 32-63
-                const uint32_t xh = x0 + st.lo * 128, xl = xh + (p.halves == 2 ? p.nb * 128 : 64);
-                for (int j = 0; j < nk; ++j) {
-                    const uint64_t dh = ptx::desc_kmajor_sw128(xh + 32 * j);
-                    const uint64_t dl = ptx::desc_kmajor_sw128(xl + 32 * j);
-                    const uint64_t w0 = ptx::desc_kmajor_sw128(s0 + 32 * j);
-                    const uint32_t on = (k != o.k0 || j != 0) ? 1u : 0u;
-                    ptx::mma_bf16(d0 + st.lo, w0, dh, id16, on);
-                    ptx::mma_bf16(d0 + st.lo, w0, dl, id16, 1u);
-                    if (o.has1) {
-                        const uint64_t w1 = ptx::desc_kmajor_sw128(s0 + kWTile + 32 * j);
-                        ptx::mma_bf16(d1 + st.lo, w1, dh, id16, on);
-                        ptx::mma_bf16(d1 + st.lo, w1, dl, id16, 1u);
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t id = id8 | ((uint32_t)j << 4) | ((uint32_t)j << 29);
+                        const uint32_t on = j == 0 ? first : 1u;
+                        ptx::mma_mxf8(d0, w_desc + at + 2 * j, x_desc + at + 2 * j, id, sf, sf + 8, on);
+                        if (has1)
+                            ptx::mma_mxf8(d1, w_desc + at + tile16 + 2 * j, x_desc + at + 2 * j, id, sf + 4,
+                                          sf + 8, on);
                     }
                 }
+            } else if constexpr (LORA) {
+                const Step st = step_of(p, t, o, k);
+                const int nk = (min(64, p.rank - st.c) + 15) / 16;
+                const uint32_t id16 = ptx::idesc_bf16(128, 0) | (uint32_t)(st.n >> 3) << 17;
+                // the window's first row; the lo half: rows of its own, or columns 32-63
+                const uint64_t xh = x_desc + at + st.lo * 8, xl = xh + (p.halves == 2 ? p.nb * 8 : 4);
+                if (elect_one())
+                    for (int j = 0; j < nk; ++j) {
+                        const uint32_t on = (k != k0 || j != 0) ? 1u : 0u;
+                        const uint64_t w0 = w_desc + at + 2 * j, w1 = w0 + tile16;
+                        ptx::mma_bf16(d0 + st.lo, w0, xh + 2 * j, id16, on);
+                        ptx::mma_bf16(d0 + st.lo, w0, xl + 2 * j, id16, 1u);
+                        if (has1) {
+                            ptx::mma_bf16(d1 + st.lo, w1, xh + 2 * j, id16, on);
+                            ptx::mma_bf16(d1 + st.lo, w1, xl + 2 * j, id16, 1u);
+                        }
+                    }
             }
-            ptx::tc_commit(ptx::smem_addr(&t.empty[r.stage]));
+            if (elect_one()) ptx::tc_commit(ptx::smem_addr(&t.empty[r.stage]));
+            __syncwarp();
             r.next(p);
         }
-        ptx::tc_commit(ptx::smem_addr(&t.accf[acc]));
+        if (elect_one()) ptx::tc_commit(ptx::smem_addr(&t.accf[acc]));
+        __syncwarp();
     }
 }
 
@@ -1075,7 +1096,7 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const __grid_constant__ 
             load_weights(p, t, sbase);
         }
     } else if (warp == 1) {
-        if (lane == 0) issue_mmas(p, t, sbase, tmem, sf_tmem);
+        issue_mmas(p, t, sbase, tmem, sf_tmem);
     } else if (warp == 2) {
         if (lane == 0) copy_scales(p, t, sbase, sf_tmem);
     } else if (warp == 3) {
