@@ -55,6 +55,7 @@ constexpr int kWTile = 128 * 128;  // bytes of a weight tile in shared memory
 constexpr int kMaxStages = 16;
 constexpr int kSfSlot = 16;        // tensor-memory columns of a stage's scales
 constexpr int kMinSteps = 4;       // steps of a part at least
+constexpr int kPairs = 256;        // pairs (token, expert) of a table of the weighted sum
 constexpr int kTickets = 4;        // tickets in flight in a CTA
 constexpr int kSmemMax = 232448;
 constexpr int kAdWords = FP8G_MAX_ADAPTERS / 32;
@@ -81,7 +82,8 @@ struct LoraTables {
     int16_t row_of[kStreamLoraRows], col_of[kStreamLoraRows];  // column -> row of the call, and back
     uint32_t bits[kStreamLoraGroups][kAdWords];  // adapters of a group's rows
     int16_t word0[kStreamLoraGroups][kAdWords];  // slots before a word's
-    alignas(16) int16_t slot_of[kStreamLoraRows];
+    int16_t slot_of[kStreamLoraRows];
+    uint8_t count[kStreamLoraRows / 32][kStreamMaxTokens + 1];  // a warp's rows of a slot
 };
 
 __device__ __forceinline__ int warp_scan(int v, int lane) {  // inclusive
@@ -144,34 +146,50 @@ __device__ __forceinline__ void make_tables(const StreamParams &p, LoraTables &t
         if (lane == 31) t.n[warp] = s;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < p.T; i += (int)blockDim.x) {
-        const int l = p.kr > 0 ? __ldg(p.idx + i) : -1, g = i / p.nb;
-        t.slot_of[i] = (int16_t)(l < 0 || l >= p.n_mat ? t.n[g]
-                                                       : t.word0[g][l >> 5] +
-                                                             __popc(t.bits[g][l >> 5] & ((1u << (l & 31)) - 1u)));
-    }
-    if ((int)threadIdx.x < ng) {
-        const int g = threadIdx.x;
-        t.first[g][t.n[g]] = (int16_t)(min(p.T, (g + 1) * p.nb) - g * p.nb);
+    // column of a row: the rows of smaller slots, then the earlier ones of its
+    // own; a warp's 32 rows by matching, the warps of a group by their counts
+    const int padded = (p.T + 31) & ~31, last = kStreamMaxTokens;  // slot index of no adapter: n <= 128
+    for (int i = threadIdx.x; i < (padded / 32) * (last + 1); i += (int)blockDim.x) t.count[0][i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < padded; i += (int)blockDim.x) {
+        const int g = i / p.nb;
+        int s = -1;
+        if (i < p.T) {
+            const int l = p.kr > 0 ? __ldg(p.idx + i) : -1;
+            s = l < 0 || l >= p.n_mat
+                    ? t.n[g]
+                    : t.word0[g][l >> 5] + __popc(t.bits[g][l >> 5] & ((1u << (l & 31)) - 1u));
+        }
+        // (rows of two groups in one warp: nb is a multiple of 16)
+        const uint32_t same = __match_any_sync(0xffffffffu, s < 0 ? -1 : s + (g << 8));
+        const int before = __popc(same & ((1u << lane) - 1u));
+        if (s >= 0) {
+            t.slot_of[i] = (int16_t)s;
+            t.col_of[i] = (int16_t)before;
+            if (before == 0) t.count[i / 32][s] += (uint8_t)__popc(same);
+        }
     }
     __syncthreads();
-    // column: the rows of smaller slots, then the earlier ones of its own
-    for (int i = threadIdx.x; i < p.T; i += (int)blockDim.x) {
-        const int g = i / p.nb, lo = g * p.nb, hi = min(p.T, lo + p.nb), s = t.slot_of[i];
-        int less = 0, before = 0;
-        for (int o = lo; o < hi; o += 8) {  // eight slots a load (lo is a multiple of 16)
-            const int4 w = *reinterpret_cast<const int4 *>(&t.slot_of[o]);
-            const int v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int so = (j & 1) ? v[j >> 1] >> 16 : (int)(int16_t)v[j >> 1];
-                less += o + j < hi && so < s;
-                before += o + j < i && so == s;
-            }
+    if (warp < ng) {
+        const int g = warp, w0 = g * p.nb / 32, w1 = (min(p.T, (g + 1) * p.nb) + 31) / 32;
+        int run = 0;
+        for (int s0 = 0; s0 <= t.n[g]; s0 += 32) {
+            const int s = s0 + lane;
+            int c = 0;
+            if (s <= t.n[g])
+                for (int w = w0; w < w1; ++w) c += t.count[w][s];
+            const int incl = warp_scan(c, lane);
+            if (s <= t.n[g]) t.first[g][s] = (int16_t)(run + incl - c);
+            run += __shfl_sync(0xffffffffu, incl, 31);
         }
-        t.col_of[i] = (int16_t)(less + before);
-        t.row_of[lo + less + before] = (int16_t)i;
-        if (before == 0) t.first[g][s] = (int16_t)less;  // s = n: the first without an adapter
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.T; i += (int)blockDim.x) {
+        const int g = i / p.nb, s = t.slot_of[i];
+        int col = t.first[g][s] + t.col_of[i];
+        for (int w = g * p.nb / 32; w < i / 32; ++w) col += t.count[w][s];
+        t.col_of[i] = (int16_t)col;
+        t.row_of[g * p.nb + col] = (int16_t)i;
     }
     if (threadIdx.x == 0) t.n_groups = ng;
     __syncthreads();
@@ -374,7 +392,7 @@ __device__ __forceinline__ void low_rank(const StreamParams &p, LoraTables &t, f
     const __nv_bfloat16 *a1 = A + ((int64_t)l * p.rank + min(r1, p.rank - 1)) * p.K + c8;
     float d0[4] = {}, d1[4] = {};
     const int steps = p.K / 32;  // K is a multiple of 32
-    constexpr int kU = BF16 ? 8 : 4;
+    constexpr int kU = BF16 ? 6 : 2;  // registers: two blocks an SM
     for (int s0 = warp * kU; s0 < steps; s0 += kPrepWarps * kU) {
         uint4 xa[kU], xb[kU], wa[kU], wb[kU], ya[BF16 ? 1 : kU], yb[BF16 ? 1 : kU];
 #pragma unroll
@@ -441,7 +459,7 @@ __device__ __forceinline__ void low_rank(const StreamParams &p, LoraTables &t, f
 
 // Blocks below `items`: V (they take longer, so they come first); the rest
 // quantise a token's segment each.
-__global__ void __launch_bounds__(kPrepThreads) lora_prep_kernel(const __grid_constant__ StreamParams p,
+__global__ void __launch_bounds__(kPrepThreads, 2) lora_prep_kernel(const __grid_constant__ StreamParams p,
                                                                  int32_t items) {
     __shared__ LoraTables t;
     __shared__ float acc[kPrepWarps / 2][16][17];
@@ -492,6 +510,8 @@ struct Tail {
     int abort_flag;
     int last;
     int32_t parts[2], tickets[2];  // parts of a tile, tickets, per product
+    int32_t pair_at[LORA ? 1 : kPairs];
+    float pair_w[LORA ? 1 : kPairs];
     typename TablesOf<LORA>::T tab;
 };
 
@@ -500,11 +520,11 @@ static_assert(kSmemMax - 1024 - (int)(sizeof(Tail<false>) > sizeof(Tail<true>) ?
                   6 * (2 * kWTile + 16 * 128 + 2048),
               "six stages with 16 token columns");
 
-// Parts of the tiles of a product: as many as give the SMs a ticket and a half
-// each, where the tiles alone are fewer than five for eight SMs.
+// Parts of the tiles of a product: as many as give every SM a ticket, where the
+// tiles alone are fewer than five for eight SMs.
 __host__ __device__ inline int parts_of(int tiles, int ks, int num_sms) {
     if (tiles * 8 >= num_sms * 5 || tiles >= kStreamSplitTiles || tiles == 0) return 1;
-    const int want = (3 * num_sms + 2 * tiles - 1) / (2 * tiles), most = ks / kMinSteps;
+    const int want = (num_sms + tiles - 1) / tiles, most = ks / kMinSteps;
     return want < most ? want : most > 1 ? most : 1;
 }
 
@@ -909,38 +929,90 @@ __device__ __forceinline__ void store_cols(const StreamParams &p, const StreamPh
 }
 
 // out[t, h] = sum_j w[t, j] y[pos[t, j], h] of one tile of h, j in order; four
-// values a thread.
-__device__ __forceinline__ void combine(const StreamParams &p, const Tile &o) {
-    const int H = p.ph[1].rows, tid = threadIdx.x - kSEpiWarp0 * 32;
-    const int per = p.ph[1].sub * 32;  // threads for a token's values
-    const int c = o.w0 + tid % per * 4;
-    if (c >= H) return;
-    for (int tok = tid / per; tok < p.T; tok += kEpiThreads / per) {
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int j0 = 0; j0 < p.k; j0 += 4) {
-            float4 v[4];
-            float a[4];
+// values a thread.  y: rows in memory, or where the tiles are split the sums of
+// the tiles' parts (in order).  The pairs' rows and weights go through shared
+// memory a table at a time, so that only the loads of y are on the way, several
+// tokens' at once.
+template <bool LORA>
+__device__ __forceinline__ void combine(const StreamParams &p, Tail<LORA> &t, const Tile &o) {
+    const StreamPhase &h = p.ph[1];
+    const int H = h.rows, tid = threadIdx.x - kSEpiWarp0 * 32, parts = t.parts[1];
+    const int per = h.sub * 32, teams = kEpiThreads / per;  // threads for a token's values
+    const int f = tid % per * 4, c = o.w0 + f, team = tid / per;
+    const int64_t part_size = (int64_t)2 * p.nb * 128;
+    const int step = min(p.T, kPairs / p.k);  // tokens of a table
+    for (int tok0 = 0; tok0 < p.T; tok0 += step) {
+        const int n = min(step, p.T - tok0);
+        (void)epi_all(true);
+        for (int i = tid; i < n * p.k; i += kEpiThreads) {
+            const int pos = __ldcg(p.pos + tok0 * p.k + i);
+            int at = pos;
+            if (parts > 1 && pos >= 0) {
+                // group and column of the row: its partial tiles' first value
+                int g = 0;
+                while (pos >= t.tab.g[g].row0 + t.tab.g[g].n) ++g;
+                at = g << 8 | (pos - t.tab.g[g].row0);
+            }
+            t.pair_at[i] = at;
+            t.pair_w[i] = __ldg(p.weights + tok0 * p.k + i);
+        }
+        (void)epi_all(true);
+        if (c >= H) continue;
+        constexpr int kTok = 4;
+        for (int a = team; a < n; a += teams * kTok) {
+            float4 s[kTok];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = j0 + j < p.k ? __ldcg(p.pos + tok * p.k + j0 + j) : -1;
-                a[j] = r >= 0 ? __ldg(p.weights + tok * p.k + j0 + j) : 0.0f;
-                v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (r >= 0) v[j] = __ldcg(reinterpret_cast<const float4 *>(p.y + (int64_t)r * H + c));
+            for (int u = 0; u < kTok; ++u) s[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int j = 0; j < p.k; ++j) {
+                float4 v[kTok];
+                if (parts == 1) {
+#pragma unroll
+                    for (int u = 0; u < kTok; ++u) {
+                        const int tok = a + u * teams, at = tok < n ? t.pair_at[tok * p.k + j] : -1;
+                        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (at >= 0) v[u] = __ldcg(reinterpret_cast<const float4 *>(p.y + (int64_t)at * H + c));
+                    }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < kTok; ++u) {
+                        const int tok = a + u * teams, at = tok < n ? t.pair_at[tok * p.k + j] : -1;
+                        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (at < 0) continue;
+                        const float *src = h.part + ((int64_t)((at >> 8) * h.mt + o.mt) * parts) * part_size +
+                                           ((int64_t)(f >> 7) * p.nb + (at & 255)) * 128 + (f & 127);
+#pragma unroll 8
+                        for (int q = 0; q < parts; ++q) {
+                            const float4 x = __ldcg(reinterpret_cast<const float4 *>(src + q * part_size));
+                            v[u].x += x.x;
+                            v[u].y += x.y;
+                            v[u].z += x.z;
+                            v[u].w += x.w;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kTok; ++u) {
+                    const int tok = a + u * teams;
+                    if (tok >= n || t.pair_at[tok * p.k + j] < 0) continue;
+                    const float w = t.pair_w[tok * p.k + j];
+                    s[u].x = fmaf(w, v[u].x, s[u].x);
+                    s[u].y = fmaf(w, v[u].y, s[u].y);
+                    s[u].z = fmaf(w, v[u].z, s[u].z);
+                    s[u].w = fmaf(w, v[u].w, s[u].w);
+                }
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                s.x = fmaf(a[j], v[j].x, s.x);
-                s.y = fmaf(a[j], v[j].y, s.y);
-                s.z = fmaf(a[j], v[j].z, s.z);
-                s.w = fmaf(a[j], v[j].w, s.w);
+            for (int u = 0; u < kTok; ++u) {
+                const int tok = a + u * teams;
+                if (tok >= n) continue;
+                const int64_t at = (int64_t)(tok0 + tok) * H + c;
+                if (p.out_f32)
+                    *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = s[u];
+                else
+                    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at) =
+                        make_uint2(pack_bf16(s[u].x, s[u].y), pack_bf16(s[u].z, s[u].w));
             }
         }
-        const int64_t at = (int64_t)tok * H + c;
-        if (p.out_f32)
-            *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = s;
-        else
-            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at) =
-                make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
     }
 }
 
@@ -983,6 +1055,12 @@ __device__ __forceinline__ void finish_tile(const StreamParams &p, Tail<LORA> &t
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&t.acce[acc]));
+        if constexpr (EPI == kRows) {
+            // every part of every group of this tile of h: the weighted sum
+            // reads the parts themselves
+            if (count_in(t, p.done_tile + o.mt, t.tab.n_groups * parts)) combine(p, t, o);
+            return;
+        }
         last = count_in(t, h.part_cnt + o.tile, parts);
     }
     if (last && live)
@@ -1032,7 +1110,7 @@ __device__ __forceinline__ void finish_tile(const StreamParams &p, Tail<LORA> &t
         }
     } else if constexpr (EPI == kRows) {
         // the last group to finish this tile of h sums the tokens' experts
-        if (last && count_in(t, p.done_tile + o.mt, t.tab.n_groups)) combine(p, o);
+        if (count_in(t, p.done_tile + o.mt, t.tab.n_groups)) combine(p, t, o);
     }
 }
 
@@ -1091,6 +1169,16 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const __grid_constant__ 
 
     if (warp == 0) {
         if (lane == 0) {
+            // the weights that some CTA will want first, to L2 while the tokens
+            // are prepared (one-byte formats)
+            Tile o;
+            if (p.gap8 == 0 && decode(p, t, (int)blockIdx.x, o)) {
+                const int k1 = min(min(o.k1, o.k0 + p.stages), p.ph[o.ph].ks);
+                for (int k = o.k0; k < k1; ++k) {
+                    ptx::tma_prefetch_3d(&p.ph[o.ph].W, k * kBK, o.w0, o.mat0);
+                    if (o.has1) ptx::tma_prefetch_3d(&p.ph[o.ph].W, k * kBK, o.w1, o.mat1);
+                }
+            }
             ptx::grid_dep_wait();
             ptx::grid_dep_launch();
             load_weights(p, t, sbase);
@@ -1185,8 +1273,8 @@ void stream_sizes(StreamParams &p, int nb, int sub, bool lora, int v_halves) {
 }
 
 size_t stream_part_bytes(const StreamParams &p, int num_sms) {
-    // tiles * parts_of(tiles) < tiles + 1.5 SMs with tiles < 5/8 SMs
-    return (size_t)(num_sms * 17 / 8 + 2) * 2 * p.nb * 128 * sizeof(float);
+    // tiles * parts_of(tiles) < tiles + SMs with tiles < 5/8 SMs
+    return (size_t)(num_sms * 13 / 8 + 2) * 2 * p.nb * 128 * sizeof(float);
 }
 
 cudaError_t launch_stream(bool lora, const StreamParams &p, int num_sms, cudaStream_t s) {
