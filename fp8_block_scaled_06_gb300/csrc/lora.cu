@@ -340,7 +340,7 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
     const size_t o_xq = take((size_t)M * K), o_xsf = take((size_t)(pair ? n_rtA : tiles) * ks * 512);
     const size_t o_v = take((size_t)tiles * cap * lv.halves * nb * lv.r64 * 2);
     const size_t o_part = take(pair ? (size_t)tiles * 4 : stream_part_bytes(p, d.num_sms));
-    p.n_counters = 1 + kStreamSplitTiles;
+    p.n_counters = 3 + kStreamSplitTiles;
     const size_t o_cnt = take(pair ? (size_t)tiles * cap * 4 : (size_t)p.n_counters * 4);
     cudaMemPool_t pool;
     if ((st = host_pool(d.dev, pool)) != FP8G_OK) return st;
@@ -382,7 +382,7 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
         p.xsf = ws + o_xsf;
         p.counters = reinterpret_cast<int32_t *>(ws + o_cnt);
         h.part = reinterpret_cast<float *>(ws + o_part);
-        h.part_cnt = p.counters + 1;
+        h.part_cnt = p.counters + 3;
         p.out = C;
         p.out_f32 = out == FP8G_OUT_F32;
         p.status = d.status;

@@ -55,6 +55,7 @@ constexpr int kWTile = 128 * 128;  // bytes of a weight tile in shared memory
 constexpr int kMaxStages = 16;
 constexpr int kSfSlot = 16;        // tensor-memory columns of a stage's scales
 constexpr int kMinSteps = 4;       // steps of a part at least
+constexpr int kCols = 8;           // token columns at a time in an epilogue (few: its code runs cold)
 constexpr int kPairs = 256;        // pairs (token, expert) of a table of the weighted sum
 constexpr int kTickets = 4;        // tickets in flight in a CTA
 constexpr int kSmemMax = 232448;
@@ -80,10 +81,15 @@ struct LoraTables {
     // adapter last): a slot's are columns first[s] .. first[s + 1] - 1
     int16_t first[kStreamLoraGroups][kStreamMaxTokens + 1];
     int16_t row_of[kStreamLoraRows], col_of[kStreamLoraRows];  // column -> row of the call, and back
-    uint32_t bits[kStreamLoraGroups][kAdWords];  // adapters of a group's rows
-    int16_t word0[kStreamLoraGroups][kAdWords];  // slots before a word's
-    int16_t slot_of[kStreamLoraRows];
-    uint8_t count[kStreamLoraRows / 32][kStreamMaxTokens + 1];  // a warp's rows of a slot
+    union {
+        struct {  // while the tables are made
+            uint32_t bits[kStreamLoraGroups][kAdWords];  // adapters of a group's rows
+            int16_t word0[kStreamLoraGroups][kAdWords];  // slots before a word's
+            int16_t slot_of[kStreamLoraRows];
+            uint8_t count[kStreamLoraRows / 32][kStreamMaxTokens + 1];  // a warp's rows of a slot
+        };
+        float acc[4][16][17];  // products to join (V)
+    };
 };
 
 __device__ __forceinline__ int warp_scan(int v, int lane) {  // inclusive
@@ -296,194 +302,21 @@ __global__ void __launch_bounds__(kPrepThreads) moe_prep_kernel(const __grid_con
     }
 }
 
-// ------------------------------------------------------------ V = alpha A x
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t *>(&b);
-}
-__device__ __forceinline__ float bf16_rest(float v) { return v - __bfloat162float(__float2bfloat16_rn(v)); }
-
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Eight values of x as bf16 pairs; of fp32 x the rounded values (hi) and what
-// they leave, rounded (lo).
-template <bool BF16>
-__device__ __forceinline__ void x_pairs(const StreamParams &p, int64_t off, bool in, uint4 &hi, uint4 &lo) {
-    hi = make_uint4(0u, 0u, 0u, 0u);
-    if constexpr (BF16) {
-        if (in) hi = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.x) + off));
-        return;
-    }
-    lo = hi;
-    if (!in) return;
-    float4 a, b;
-    load8<false>(p.x, off, a, b);
-    hi = make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
-    lo = make_uint4(pack_bf16(bf16_rest(a.x), bf16_rest(a.y)), pack_bf16(bf16_rest(a.z), bf16_rest(a.w)),
-                    pack_bf16(bf16_rest(b.x), bf16_rest(b.y)), pack_bf16(bf16_rest(b.z), bf16_rest(b.w)));
-}
-
-// An item is 16 rows of a slot against 16 ranks of its
-// adapter; the K range goes over the eight warps, each a 16 x 16 product by
-// mma.sync, joined in warp order.  A lane's 16-byte load covers 8 consecutive K
-// of a row; the same K permutation on both operands leaves the product as it
-// is.  Bound by the latency of its loads (an adapter's 16 ranks are 131 KB at
-// K = 4096): kU K steps of 32 are in flight per warp.
-template <bool BF16>
-__device__ __forceinline__ void low_rank(const StreamParams &p, LoraTables &t, float (*acc_all)[16][17], int32_t *pick, int item) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rblocks = (p.rank + 15) / 16;
-    const __nv_bfloat16 *A = static_cast<const __nv_bfloat16 *>(p.a);
-    if (warp == 0) {
-        // item -> group, slot, 16 rows, rank block
-        int at = 0;
-        if (lane == 0) pick[0] = -1;
-        __syncwarp();
-        for (int g = 0; g < t.n_groups; ++g)
-            for (int s0 = 0; s0 < t.n[g]; s0 += 32) {
-                const int s = s0 + lane;
-                const int c =
-                    s < t.n[g] ? (t.first[g][s + 1] - t.first[g][s] + 15) / 16 * rblocks : 0;
-                const int incl = warp_scan(c, lane), first = at + incl - c;
-                if (item >= first && item < first + c) {
-                    pick[0] = g;
-                    pick[1] = s;
-                    pick[2] = (item - first) / rblocks * 16;
-                    pick[3] = (item - first) % rblocks;
-                }
-                at += __shfl_sync(0xffffffffu, incl, 31);
-            }
-    }
-    __syncthreads();
-    const int g = pick[0];
-    if (g < 0) return;  // past the last item
-    const int slot = pick[1], l = t.adapter[g][slot], rb = pick[3];
-    const int s_lo = t.first[g][slot], s_hi = t.first[g][slot + 1];
-    const int col0 = s_lo + pick[2], n = min(16, s_hi - col0);  // this item's columns
-    __nv_bfloat16 *hi = static_cast<__nv_bfloat16 *>(p.v) +
-                        (int64_t)(g * p.slot_cap + slot) * p.halves * p.nb * p.r64 + rb * 16;
-    const int64_t half = p.halves == 2 ? (int64_t)p.nb * p.r64 : 32;
-    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-    if (pick[2] == 0) {
-        // the slot's first rows: zeros for the tokens of other adapters, and
-        // in the columns past the rank
-        const int cols = (p.halves == 2 ? p.r64 : 32) / 8;
-        for (int i = tid; i < p.nb; i += kPrepThreads) {
-            uint4 *d = reinterpret_cast<uint4 *>(hi + (int64_t)i * p.r64);
-            uint4 *e = reinterpret_cast<uint4 *>(hi + half + (int64_t)i * p.r64);
-            if (i < s_lo || i >= s_hi) d[0] = d[1] = e[0] = e[1] = z;
-            if (rb == 0)
-                for (int c = 2 * rblocks; c < cols; ++c) d[c] = e[c] = z;
-        }
-    }
-    const int gr = lane >> 2, c8 = 8 * (lane & 3);
-    const int64_t lo = (int64_t)g * p.nb + col0;
-    const bool on0 = gr < n, on1 = gr + 8 < n;
-    const int64_t x0 = (int64_t)t.row_of[on0 ? lo + gr : lo] * p.K + c8;
-    const int64_t x1 = (int64_t)t.row_of[on1 ? lo + gr + 8 : lo] * p.K + c8;
-    const int r0 = rb * 16 + gr, r1 = r0 + 8;
-    const __nv_bfloat16 *a0 = A + ((int64_t)l * p.rank + min(r0, p.rank - 1)) * p.K + c8;
-    const __nv_bfloat16 *a1 = A + ((int64_t)l * p.rank + min(r1, p.rank - 1)) * p.K + c8;
-    float d0[4] = {}, d1[4] = {};
-    const int steps = p.K / 32;  // K is a multiple of 32
-    constexpr int kU = BF16 ? 6 : 2;  // registers: two blocks an SM
-    for (int s0 = warp * kU; s0 < steps; s0 += kPrepWarps * kU) {
-        uint4 xa[kU], xb[kU], wa[kU], wb[kU], ya[BF16 ? 1 : kU], yb[BF16 ? 1 : kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const bool in = s0 + u < steps;
-            const int64_t k = in ? (int64_t)(s0 + u) * 32 : 0;
-            x_pairs<BF16>(p, x0 + k, in && on0, xa[u], ya[BF16 ? 0 : u]);
-            x_pairs<BF16>(p, x1 + k, in && on1, xb[u], yb[BF16 ? 0 : u]);
-            wa[u] = in && r0 < p.rank ? __ldg(reinterpret_cast<const uint4 *>(a0 + k)) : z;
-            wb[u] = in && r1 < p.rank ? __ldg(reinterpret_cast<const uint4 *>(a1 + k)) : z;
-        }
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const uint32_t f0[4] = {xa[u].x, xb[u].x, xa[u].y, xb[u].y};
-            const uint32_t f1[4] = {xa[u].z, xb[u].z, xa[u].w, xb[u].w};
-            mma_16816(d0, f0, wa[u].x, wa[u].y);
-            mma_16816(d1, f0, wb[u].x, wb[u].y);
-            mma_16816(d0, f1, wa[u].z, wa[u].w);
-            mma_16816(d1, f1, wb[u].z, wb[u].w);
-            if constexpr (!BF16) {
-                const uint32_t h0[4] = {ya[u].x, yb[u].x, ya[u].y, yb[u].y};
-                const uint32_t h1[4] = {ya[u].z, yb[u].z, ya[u].w, yb[u].w};
-                mma_16816(d0, h0, wa[u].x, wa[u].y);
-                mma_16816(d1, h0, wb[u].x, wb[u].y);
-                mma_16816(d0, h1, wa[u].z, wa[u].w);
-                mma_16816(d1, h1, wb[u].z, wb[u].w);
-            }
-        }
-    }
-    // the warps' products: warp w + 4 to warp w, then the four in order
-    const int c2 = 2 * (lane & 3);
-    float(*acc)[17] = acc_all[warp & 3];
-    if (warp >= 4) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            acc[gr + 8 * (e >> 1)][c2 + (e & 1)] = d0[e];
-            acc[gr + 8 * (e >> 1)][8 + c2 + (e & 1)] = d1[e];
-        }
-    }
-    __syncthreads();
-    if (warp < 4) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            acc[gr + 8 * (e >> 1)][c2 + (e & 1)] += d0[e];
-            acc[gr + 8 * (e >> 1)][8 + c2 + (e & 1)] += d1[e];
-        }
-    }
-    __syncthreads();
-    {
-        const int i = tid >> 4, c = tid & 15;
-        float v = 0.0f;
-#pragma unroll
-        for (int q = 0; q < kPrepWarps / 2; ++q) v += acc_all[q][i][c];
-        if (p.alpha != nullptr) v *= __ldg(p.alpha + l);
-        if (rb * 16 + c >= p.rank) v = 0.0f;
-        if (i < n) {
-            const float rest = bf16_rest(v);  // none for an infinite or NaN V
-            const int64_t at = (int64_t)(col0 + i) * p.r64 + c;
-            hi[at] = __float2bfloat16_rn(v);
-            hi[half + at] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
-        }
-    }
-}
-
-// Blocks below `items`: V (they take longer, so they come first); the rest
-// quantise a token's segment each.
-__global__ void __launch_bounds__(kPrepThreads, 2) lora_prep_kernel(const __grid_constant__ StreamParams p,
-                                                                 int32_t items) {
+// Block (token, segment): the token's codes at its column.
+__global__ void __launch_bounds__(kPrepThreads) lora_prep_kernel(const __grid_constant__ StreamParams p) {
     __shared__ LoraTables t;
-    __shared__ float acc[kPrepWarps / 2][16][17];
-    __shared__ int32_t pick[4];
     const int tid = threadIdx.x;
+    const int ks = p.ph[0].ks, segs = quant_segments(ks);
+    const int tok = blockIdx.x / segs, c = (blockIdx.x - tok * segs) * kPrepThreads + tid;
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    const int ks = p.ph[0].ks, segs = quant_segments(ks);
-    const int it = (int)blockIdx.x - items, tok = it / segs, c = (it - tok * segs) * kPrepThreads + tid;
-    Quant8 q{};
-    if (it >= 0) q = quant_8(p, tok, c);
-    if (it >= 0)
-        for (int i = it * kPrepThreads + tid; i < p.n_counters; i += p.T * segs * kPrepThreads) p.counters[i] = 0;
+    const Quant8 q = quant_8(p, tok, c);
+    for (int i = blockIdx.x * kPrepThreads + tid; i < p.n_counters; i += gridDim.x * kPrepThreads)
+        p.counters[i] = 0;
     if (blockIdx.x == 0 && p.kr > 0)
         for (int i = tid; i < p.T; i += kPrepThreads)
             if (__ldg(p.idx + i) >= p.n_mat) record_error(p, FP8G_ERR_INVALID_ARG, (unsigned)i);
     make_tables(p, t);
-    if (it < 0) {
-        if (p.x_bf16)
-            low_rank<true>(p, t, acc, pick, blockIdx.x);
-        else
-            low_rank<false>(p, t, acc, pick, blockIdx.x);
-        return;
-    }
     if (c >= ks * 16) return;
     const int g = tok / p.nb, col = t.col_of[tok];
     if (q.in) *reinterpret_cast<uint2 *>(p.xq + ((int64_t)g * p.nb + col) * p.K + c * 8) = q.q;
@@ -512,6 +345,7 @@ struct Tail {
     int32_t parts[2], tickets[2];  // parts of a tile, tickets, per product
     int32_t pair_at[LORA ? 1 : kPairs];
     float pair_w[LORA ? 1 : kPairs];
+    int32_t items, item, pick[4];  // items of V, the one at hand
     typename TablesOf<LORA>::T tab;
 };
 
@@ -520,11 +354,11 @@ static_assert(kSmemMax - 1024 - (int)(sizeof(Tail<false>) > sizeof(Tail<true>) ?
                   6 * (2 * kWTile + 16 * 128 + 2048),
               "six stages with 16 token columns");
 
-// Parts of the tiles of a product: as many as give every SM a ticket, where the
-// tiles alone are fewer than five for eight SMs.
+// Parts of the tiles of a product: as many as give every SM two tickets, where
+// the tiles alone are fewer than five for eight SMs.
 __host__ __device__ inline int parts_of(int tiles, int ks, int num_sms) {
     if (tiles * 8 >= num_sms * 5 || tiles >= kStreamSplitTiles || tiles == 0) return 1;
-    const int want = (num_sms + tiles - 1) / tiles, most = ks / kMinSteps;
+    const int want = (2 * num_sms + tiles - 1) / tiles, most = ks / kMinSteps;
     return want < most ? want : most > 1 ? most : 1;
 }
 
@@ -649,6 +483,22 @@ __device__ __forceinline__ int ld_acquire(const int32_t *a) {
 // the counter that orders them).
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
+// Until *counter is n (one thread).  Bounded; false: aborting.
+template <bool LORA>
+__device__ __forceinline__ bool wait_count(const StreamParams &p, Tail<LORA> &t, const int32_t *counter, int n) {
+    volatile int *abort_flag = &t.abort_flag;
+    const uint64_t t0 = ptx::globaltimer();
+    while (ld_acquire(counter) != n) {
+        if (*abort_flag) return false;
+        if (ptx::globaltimer() - t0 > p.timeout_ns) {
+            *abort_flag = 1;
+            record_error(p, FP8G_ERR_TIMEOUT, 4 * 256 + 100);
+            return false;
+        }
+    }
+    return true;
+}
+
 // Warp 0: tickets and weight tiles (or an adapter's rows).
 template <bool LORA>
 __device__ __forceinline__ void load_weights(const StreamParams &p, Tail<LORA> &t, uint32_t sbase) {
@@ -699,18 +549,11 @@ __device__ __forceinline__ void load_tokens(const StreamParams &p, Tail<LORA> &t
     Queue q;
     Tile o;
     int ready = -1;  // groups up to this one are known to be done
+    bool v_done = false;
     while (take<LORA, false>(p, t, q, o, 4)) {
         const StreamPhase &h = p.ph[o.ph];
         if (o.ph == 1 && o.g > ready) {
-            const uint64_t t0 = ptx::globaltimer();
-            while (ld_acquire(p.done_group + o.g) != p.ph[0].mt) {
-                if (*abort_flag) return;
-                if (ptx::globaltimer() - t0 > p.timeout_ns) {
-                    *abort_flag = 1;
-                    record_error(p, FP8G_ERR_TIMEOUT, 4 * 256 + 100);
-                    return;
-                }
-            }
+            if (!wait_count(p, t, p.done_group + o.g, p.ph[0].mt)) return;
             fence_proxy_async_all();
             ready = o.g;
         }
@@ -737,6 +580,11 @@ __device__ __forceinline__ void load_tokens(const StreamParams &p, Tail<LORA> &t
                 ptx::bulk_load(sf + 512, c0 + k * step, pair ? 1024 : 512, fb);
                 if (o.has1 && !pair) ptx::bulk_load(sf + 1024, c1 + k * step, 512, fb);
             } else if constexpr (LORA) {
+                if (!v_done) {  // every item of V
+                    if (!wait_count(p, t, p.counters + 2, t.items)) return;
+                    fence_proxy_async_all();
+                    v_done = true;
+                }
                 const int v0 = (o.g * p.slot_cap + st.slot) * p.halves * p.nb;
                 ptx::mbar_arrive_expect_tx(fb, p.halves * st.n * 128u);
                 for (int b = 0; b < p.halves; ++b)
@@ -882,20 +730,183 @@ __device__ __forceinline__ bool count_in(Tail<LORA> &t, int32_t *counter, int fu
     return t.last != 0;
 }
 
+// ------------------------------------------------------------ V = alpha A x
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&b);
+}
+__device__ __forceinline__ float bf16_rest(float v) { return v - __bfloat162float(__float2bfloat16_rn(v)); }
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Eight values of x as bf16 pairs; of fp32 x the rounded values (hi) and what
+// they leave, rounded (lo).
+template <bool BF16>
+__device__ __forceinline__ void x_pairs(const StreamParams &p, int64_t off, bool in, uint4 &hi, uint4 &lo) {
+    hi = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (BF16) {
+        if (in) hi = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.x) + off));
+        return;
+    }
+    lo = hi;
+    if (!in) return;
+    float4 a, b;
+    load8<false>(p.x, off, a, b);
+    hi = make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
+    lo = make_uint4(pack_bf16(bf16_rest(a.x), bf16_rest(a.y)), pack_bf16(bf16_rest(a.z), bf16_rest(a.w)),
+                    pack_bf16(bf16_rest(b.x), bf16_rest(b.y)), pack_bf16(bf16_rest(b.z), bf16_rest(b.w)));
+}
+
+// An item is 16 rows of a slot against 16 ranks of its
+// adapter; the K range goes over the eight warps, each a 16 x 16 product by
+// mma.sync, joined in warp order.  A lane's 16-byte load covers 8 consecutive K
+// of a row; the same K permutation on both operands leaves the product as it
+// is.  Bound by the latency of its loads (an adapter's 16 ranks are 131 KB at
+// K = 4096): kU K steps of 32 are in flight per warp.
+// False: past the last item.
+template <bool BF16>
+__device__ __forceinline__ bool low_rank(const StreamParams &p, LoraTables &t, int32_t *pick, int item) {
+    const int tid = threadIdx.x - kSEpiWarp0 * 32, warp = tid >> 5, lane = tid & 31;
+    const int rblocks = (p.rank + 15) / 16;
+    const __nv_bfloat16 *A = static_cast<const __nv_bfloat16 *>(p.a);
+    if (warp == 0) {
+        // item -> group, slot, 16 rows, rank block
+        int at = 0;
+        if (lane == 0) pick[0] = -1;
+        __syncwarp();
+        for (int g = 0; g < t.n_groups; ++g)
+            for (int s0 = 0; s0 < t.n[g]; s0 += 32) {
+                const int s = s0 + lane;
+                const int c =
+                    s < t.n[g] ? (t.first[g][s + 1] - t.first[g][s] + 15) / 16 * rblocks : 0;
+                const int incl = warp_scan(c, lane), first = at + incl - c;
+                if (item >= first && item < first + c) {
+                    pick[0] = g;
+                    pick[1] = s;
+                    pick[2] = (item - first) / rblocks * 16;
+                    pick[3] = (item - first) % rblocks;
+                }
+                at += __shfl_sync(0xffffffffu, incl, 31);
+            }
+    }
+    (void)epi_all(true);
+    const int g = pick[0];
+    if (g < 0) return false;
+    const int slot = pick[1], l = t.adapter[g][slot], rb = pick[3];
+    const int s_lo = t.first[g][slot], s_hi = t.first[g][slot + 1];
+    const int col0 = s_lo + pick[2], n = min(16, s_hi - col0);  // this item's columns
+    __nv_bfloat16 *hi = static_cast<__nv_bfloat16 *>(p.v) +
+                        (int64_t)(g * p.slot_cap + slot) * p.halves * p.nb * p.r64 + rb * 16;
+    const int64_t half = p.halves == 2 ? (int64_t)p.nb * p.r64 : 32;
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    if (pick[2] == 0) {
+        // the slot's first rows: zeros for the tokens of other adapters, and
+        // in the columns past the rank
+        const int cols = (p.halves == 2 ? p.r64 : 32) / 8;
+        for (int i = tid; i < p.nb; i += kEpiThreads) {
+            uint4 *d = reinterpret_cast<uint4 *>(hi + (int64_t)i * p.r64);
+            uint4 *e = reinterpret_cast<uint4 *>(hi + half + (int64_t)i * p.r64);
+            if (i < s_lo || i >= s_hi) d[0] = d[1] = e[0] = e[1] = z;
+            if (rb == 0)
+                for (int c = 2 * rblocks; c < cols; ++c) d[c] = e[c] = z;
+        }
+    }
+    const int gr = lane >> 2, c8 = 8 * (lane & 3);
+    const int64_t lo = (int64_t)g * p.nb + col0;
+    const bool on0 = gr < n, on1 = gr + 8 < n;
+    const int64_t x0 = (int64_t)t.row_of[on0 ? lo + gr : lo] * p.K + c8;
+    const int64_t x1 = (int64_t)t.row_of[on1 ? lo + gr + 8 : lo] * p.K + c8;
+    const int r0 = rb * 16 + gr, r1 = r0 + 8;
+    const __nv_bfloat16 *a0 = A + ((int64_t)l * p.rank + min(r0, p.rank - 1)) * p.K + c8;
+    const __nv_bfloat16 *a1 = A + ((int64_t)l * p.rank + min(r1, p.rank - 1)) * p.K + c8;
+    float d0[4] = {}, d1[4] = {};
+    const int steps = p.K / 32;  // K is a multiple of 32
+    constexpr int kU = BF16 ? 4 : 2;
+    for (int s0 = warp * kU; s0 < steps; s0 += kSEpiWarps * kU) {
+        uint4 xa[kU], xb[kU], wa[kU], wb[kU], ya[BF16 ? 1 : kU], yb[BF16 ? 1 : kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const bool in = s0 + u < steps;
+            const int64_t k = in ? (int64_t)(s0 + u) * 32 : 0;
+            x_pairs<BF16>(p, x0 + k, in && on0, xa[u], ya[BF16 ? 0 : u]);
+            x_pairs<BF16>(p, x1 + k, in && on1, xb[u], yb[BF16 ? 0 : u]);
+            wa[u] = in && r0 < p.rank ? __ldg(reinterpret_cast<const uint4 *>(a0 + k)) : z;
+            wb[u] = in && r1 < p.rank ? __ldg(reinterpret_cast<const uint4 *>(a1 + k)) : z;
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const uint32_t f0[4] = {xa[u].x, xb[u].x, xa[u].y, xb[u].y};
+            const uint32_t f1[4] = {xa[u].z, xb[u].z, xa[u].w, xb[u].w};
+            mma_16816(d0, f0, wa[u].x, wa[u].y);
+            mma_16816(d1, f0, wb[u].x, wb[u].y);
+            mma_16816(d0, f1, wa[u].z, wa[u].w);
+            mma_16816(d1, f1, wb[u].z, wb[u].w);
+            if constexpr (!BF16) {
+                const uint32_t h0[4] = {ya[u].x, yb[u].x, ya[u].y, yb[u].y};
+                const uint32_t h1[4] = {ya[u].z, yb[u].z, ya[u].w, yb[u].w};
+                mma_16816(d0, h0, wa[u].x, wa[u].y);
+                mma_16816(d1, h0, wb[u].x, wb[u].y);
+                mma_16816(d0, h1, wa[u].z, wa[u].w);
+                mma_16816(d1, h1, wb[u].z, wb[u].w);
+            }
+        }
+    }
+    // the warps' products: warp w + 4 to warp w, then the four in order
+    const int c2 = 2 * (lane & 3);
+    float(*acc)[17] = t.acc[warp & 3];
+    if (warp >= 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            acc[gr + 8 * (e >> 1)][c2 + (e & 1)] = d0[e];
+            acc[gr + 8 * (e >> 1)][8 + c2 + (e & 1)] = d1[e];
+        }
+    }
+    (void)epi_all(true);
+    if (warp < 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            acc[gr + 8 * (e >> 1)][c2 + (e & 1)] += d0[e];
+            acc[gr + 8 * (e >> 1)][8 + c2 + (e & 1)] += d1[e];
+        }
+    }
+    (void)epi_all(true);
+    {
+        const int i = tid >> 4, c = tid & 15;
+        float v = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kSEpiWarps / 2; ++q) v += t.acc[q][i][c];
+        if (p.alpha != nullptr) v *= __ldg(p.alpha + l);
+        if (rb * 16 + c >= p.rank) v = 0.0f;
+        if (i < n) {
+            const float rest = bf16_rest(v);  // none for an infinite or NaN V
+            const int64_t at = (int64_t)(col0 + i) * p.r64 + c;
+            hi[at] = __float2bfloat16_rn(v);
+            hi[half + at] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
+        }
+    }
+    return true;
+}
+
 __device__ __forceinline__ float gate_act(float g, int gate) {
     if (gate == FP8G_GATE_SILU) return g / (1.0f + expf(-g));
     if (gate == FP8G_GATE_GELU) return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
     return g < 0.0f ? 0.0f : g;
 }
 
-// 16 columns of a finished tile: v[s][i] is this lane's weight row f of weight
+// kCols columns of a finished tile: v[s][i] is this lane's weight row f of weight
 // tile s, token column c + i.
 template <bool LORA, int EPI, int SUBS>
 __device__ __forceinline__ void store_cols(const StreamParams &p, const StreamPhase &h, const Tail<LORA> &t,
                                            const Tile &o, int c, int f, int q, int lane,
-                                           const float (&v)[SUBS][16]) {
+                                           const float (&v)[SUBS][kCols]) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < kCols; ++i) {
         const int col = c + i;
         if (col >= o.n) break;  // warp-uniform
         int row = o.row0 + col;
@@ -1025,11 +1036,11 @@ __device__ __forceinline__ void finish_tile(const StreamParams &p, Tail<LORA> &t
     const int q = warp & 3, half = (warp - kSEpiWarp0) >> 2;
     const int row_l = q * 32 + lane;  // weight row within a tile
     // two weight tiles: this warp takes tile `half`; gated, or one tile: every
-    // other 16 columns (of both tiles, gated)
+    // other kCols columns (of both tiles, gated)
     constexpr int kSubs = EPI == kGated ? 2 : 1;
     constexpr int kJoin = EPI == kGated ? 2 : 4;  // parts read at a time
     const bool by_cols = EPI == kGated || h.sub == 1;
-    const int c_first = by_cols ? half * 16 : 0, c_step = by_cols ? 32 : 16;
+    const int c_first = by_cols ? half * kCols : 0, c_step = by_cols ? 2 * kCols : kCols;
     const int my_sub = by_cols ? 0 : half;
     const bool live = my_sub == 0 || o.has1;  // this warp has a weight tile
     const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + acc * 2 * p.nb;
@@ -1044,12 +1055,12 @@ __device__ __forceinline__ void finish_tile(const StreamParams &p, Tail<LORA> &t
 #pragma unroll
                 for (int s = 0; s < kSubs; ++s) {
                     const int sub = EPI == kGated ? s : my_sub;
-                    uint32_t r[16];
-                    ptx::tmem_ld_32x32b_x16(ta + sub * p.nb + c, r);
+                    uint32_t r[kCols];
+                    ptx::tmem_ld_32x32b_x8(ta + sub * p.nb + c, r);
                     ptx::tmem_ld_wait();
                     float *dst = part + ((int64_t)sub * p.nb + c) * 128 + row_l;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
+                    for (int i = 0; i < kCols; ++i)
                         if (c + i < o.n) __stcg(dst + i * 128, __uint_as_float(r[i]));
                 }
         ptx::tc_fence_before();
@@ -1065,33 +1076,33 @@ __device__ __forceinline__ void finish_tile(const StreamParams &p, Tail<LORA> &t
     }
     if (last && live)
         for (int c = c_first; c < o.n; c += c_step) {
-            float v[kSubs][16];
+            float v[kSubs][kCols];
 #pragma unroll
             for (int s = 0; s < kSubs; ++s) {
                 const int sub = EPI == kGated ? s : my_sub;
                 if (parts == 1) {
-                    uint32_t r[16];
-                    ptx::tmem_ld_32x32b_x16(ta + sub * p.nb + c, r);
+                    uint32_t r[kCols];
+                    ptx::tmem_ld_32x32b_x8(ta + sub * p.nb + c, r);
                     ptx::tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[s][i] = __uint_as_float(r[i]);
+                    for (int i = 0; i < kCols; ++i) v[s][i] = __uint_as_float(r[i]);
                 } else {
                     // in order; several parts' loads in flight at a time
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[s][i] = 0.0f;
+                    for (int i = 0; i < kCols; ++i) v[s][i] = 0.0f;
                     for (int a = 0; a < parts; a += kJoin) {
-                        float x[kJoin][16];
+                        float x[kJoin][kCols];
 #pragma unroll
                         for (int j = 0; j < kJoin; ++j) {
                             const float *src = part0 + (a + j) * part_size + ((int64_t)sub * p.nb + c) * 128 + row_l;
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
+                            for (int i = 0; i < kCols; ++i)
                                 x[j][i] = a + j < parts && c + i < o.n ? __ldcg(src + i * 128) : 0.0f;
                         }
 #pragma unroll
                         for (int j = 0; j < kJoin; ++j)
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) v[s][i] += x[j][i];
+                            for (int i = 0; i < kCols; ++i) v[s][i] += x[j][i];
                     }
                 }
             }
@@ -1161,6 +1172,16 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const __grid_constant__ 
             t.parts[i] = parts_of(tiles, p.ph[i].ks, (int)gridDim.x);
             t.tickets[i] = tiles * t.parts[i];
         }
+    if constexpr (LORA) {
+        if (warp == 1) {
+            int n = 0;
+            for (int g = 0; g < t.tab.n_groups; ++g)
+                for (int s = lane; s < t.tab.n[g]; s += 32)
+                    n += (t.tab.first[g][s + 1] - t.tab.first[g][s] + 15) / 16 * ((p.rank + 15) / 16);
+            n = __reduce_add_sync(0xffffffffu, n);
+            if (lane == 0) t.items = n;
+        }
+    }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -1194,6 +1215,23 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const __grid_constant__ 
         }
     } else if (warp < kSEpiWarp0 + kSEpiWarps) {
         ptx::grid_dep_wait();
+        if constexpr (LORA) {
+            // items of V first, taken off a counter as the tickets are
+            while (true) {
+                (void)epi_all(true);
+                if (threadIdx.x == kSEpiWarp0 * 32) t.item = atomicAdd(p.counters + 1, 1);
+                (void)epi_all(true);
+                const int item = t.item;
+                if (item >= t.items) break;
+                if (p.x_bf16)
+                    (void)low_rank<true>(p, t.tab, t.pick, item);
+                else
+                    (void)low_rank<false>(p, t.tab, t.pick, item);
+                fence_proxy_async_all();
+                (void)epi_all(true);
+                if (threadIdx.x == kSEpiWarp0 * 32) (void)atom_add_acq_rel(p.counters + 2, 1);
+            }
+        }
         Queue q;
         Tile o;
         for (int lt = 0;; ++lt) {
@@ -1273,20 +1311,15 @@ void stream_sizes(StreamParams &p, int nb, int sub, bool lora, int v_halves) {
 }
 
 size_t stream_part_bytes(const StreamParams &p, int num_sms) {
-    // tiles * parts_of(tiles) < tiles + SMs with tiles < 5/8 SMs
-    return (size_t)(num_sms * 13 / 8 + 2) * 2 * p.nb * 128 * sizeof(float);
+    // tiles * parts_of(tiles) < tiles + 2 SMs with tiles < 5/8 SMs
+    return (size_t)(num_sms * 21 / 8 + 2) * 2 * p.nb * 128 * sizeof(float);
 }
 
 cudaError_t launch_stream(bool lora, const StreamParams &p, int num_sms, cudaStream_t s) {
     const int segs = quant_segments(p.ph[0].ks);
     cudaError_t e;
     if (lora) {
-        // items of V: 16 rows of a slot, 16 ranks; a partly filled one per slot at most
-        const int groups = (p.T + p.nb - 1) / p.nb;
-        const int slots = p.T < groups * p.slot_cap ? p.T : groups * p.slot_cap;
-        const int items = p.kr > 0 ? (slots + p.T / 16) * ((p.rank + 15) / 16) : 0;
-        e = launch_programmatic(lora_prep_kernel, dim3((unsigned)(items + p.T * segs)), dim3(kPrepThreads), s, p,
-                                items);
+        e = launch_programmatic(lora_prep_kernel, dim3((unsigned)(p.T * segs)), dim3(kPrepThreads), s, p);
         if (e == cudaSuccess) e = launch_one<true>(p, num_sms, s);
     } else {
         e = launch_programmatic(moe_prep_kernel, dim3((unsigned)(p.T * segs)), dim3(kPrepThreads), s, p);

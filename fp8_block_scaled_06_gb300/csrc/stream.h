@@ -49,9 +49,10 @@ struct StreamParams {
     const int32_t *idx;    // MoE: expert of each pair [T][k]; adapters: adapter of each row [T]
     int32_t n_idx, n_mat;  // their number; experts / adapters
     uint8_t *xq, *xsf;     // token codes (MoE: expert order) and packed scales
-    // counters, zeroed by the preparing kernel: [0] the next ticket, then (MoE)
-    // gated tiles done per group, groups done per tile of the down product,
-    // and the products' part counters
+    // counters, zeroed by the preparing kernel: [0] the next ticket, [1] the
+    // next item of V, [2] items of V done, then (MoE) gated tiles done per group,
+    // groups (of split tiles: parts) done per tile of the down product, and the
+    // products' part counters
     int32_t *counters;
     int32_t n_counters;
     int32_t *done_group, *done_tile;
