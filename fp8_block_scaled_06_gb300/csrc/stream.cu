@@ -54,6 +54,7 @@ constexpr int kPrepWarps = kPrepThreads / 32;
 constexpr int kWTile = 128 * 128;  // bytes of a weight tile in shared memory
 constexpr int kMaxStages = 16;
 constexpr int kSfSlot = 16;        // tensor-memory columns of a stage's scales
+constexpr int kLittle = 16;        // steps an SM, in parts_of
 constexpr int kMinSteps = 4;       // steps of a part at least
 constexpr int kCols = 8;           // token columns at a time in an epilogue (few: its code runs cold)
 constexpr int kPairs = 256;        // pairs (token, expert) of a table of the weighted sum
@@ -76,6 +77,8 @@ struct MoeTables {
 struct LoraTables {
     int32_t n_groups;
     int32_t n[kStreamLoraGroups];  // slots
+    int32_t windows[kStreamLoraGroups];  // windows of a slot's columns (Step)
+    int32_t items;                       // of V, in all groups
     int16_t adapter[kStreamLoraGroups][kStreamMaxTokens];
     // a group's rows are taken in the order of their slots (those without an
     // adapter last): a slot's are columns first[s] .. first[s + 1] - 1
@@ -105,6 +108,30 @@ __device__ __forceinline__ int warp_scan(int v, int lane) {  // inclusive
 // barrier.
 __device__ __forceinline__ void make_tables(const StreamParams &p, MoeTables &t) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (p.n_idx <= 32 && p.n_idx <= p.nb) {
+        // one warp, a pair a lane: a block's barriers and shared-memory sums take
+        // longer than everything else here
+        if (warp == 0) {
+            int e = lane < p.n_idx ? __ldg(p.idx + lane) : -1;
+            if (e >= p.n_mat) e = -1;
+            const uint32_t same = __match_any_sync(0xffffffffu, e);
+            const bool first = e >= 0 && lane == __ffs((int)same) - 1;
+            const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+            int row0 = 0, g = 0;  // rows and groups of smaller experts
+            for (uint32_t m = firsts; m != 0; m &= m - 1) {
+                const int o = __ffs((int)m) - 1;
+                const int eo = __shfl_sync(0xffffffffu, e, o), c = __popc(__shfl_sync(0xffffffffu, same, o));
+                if (eo < e) {
+                    row0 += c;
+                    ++g;
+                }
+            }
+            if (first) t.g[g] = Group{(int16_t)e, (int16_t)row0, (int16_t)__popc(same), 0};
+            if (lane == 0) t.n_groups = __popc(firsts);
+        }
+        __syncthreads();
+        return;
+    }
     for (int e = threadIdx.x; e < p.n_mat; e += blockDim.x) t.cnt[e] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < p.n_idx; i += blockDim.x) {
@@ -129,9 +156,67 @@ __device__ __forceinline__ void make_tables(const StreamParams &p, MoeTables &t)
     __syncthreads();
 }
 
+// Warp 0, after the columns: windows and items.
+__device__ __forceinline__ void lora_windows(const StreamParams &p, LoraTables &t, int lane) {
+    int items = 0;
+    for (int g = 0; g < (p.T + p.nb - 1) / p.nb; ++g) {
+        int most = 0;
+        for (int s = lane; s < t.n[g]; s += 32) {
+            const int lo = t.first[g][s], hi = t.first[g][s + 1];
+            items += (hi - lo + 15) / 16;
+            most = max(most, ((hi + 15) & ~15) - (lo & ~15));
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) t.windows[g] = p.halves == 2 && most > p.v_cols ? 2 : 1;
+    }
+    items = __reduce_add_sync(0xffffffffu, items);
+    if (lane == 0) t.items = items * ((p.rank + 15) / 16);
+    __syncwarp();
+}
+
 __device__ __forceinline__ void make_tables(const StreamParams &p, LoraTables &t) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ng = (p.T + p.nb - 1) / p.nb;
+    if (p.T <= 32) {  // one warp, a row a lane
+        if (warp == 0) {
+            int l = lane < p.T && p.kr > 0 ? __ldg(p.idx + lane) : -1;
+            // rows without an adapter after the others, no rows after those
+            int key = l < 0 || l >= p.n_mat ? FP8G_MAX_ADAPTERS : l;
+            if (lane >= p.T) key = FP8G_MAX_ADAPTERS + 1;
+            const uint32_t same = __match_any_sync(0xffffffffu, key);
+            const bool first = lane == __ffs((int)same) - 1;
+            const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+            int col = __popc(same & ((1u << lane) - 1u)), less = 0, slot = 0;
+            for (uint32_t m = firsts; m != 0; m &= m - 1) {
+                const int o = __ffs((int)m) - 1;
+                const int ko = __shfl_sync(0xffffffffu, key, o), c = __popc(__shfl_sync(0xffffffffu, same, o));
+                if (ko < key) {
+                    less += c;
+                    ++slot;
+                }
+            }
+            col += less;
+            const uint32_t slots = __ballot_sync(0xffffffffu, first && key < FP8G_MAX_ADAPTERS);
+            const uint32_t have = __ballot_sync(0xffffffffu, key < FP8G_MAX_ADAPTERS);
+            if (lane < p.T) {
+                t.col_of[lane] = (int16_t)col;
+                t.row_of[col] = (int16_t)lane;
+                if (first && key < FP8G_MAX_ADAPTERS) {
+                    t.adapter[0][slot] = (int16_t)l;
+                    t.first[0][slot] = (int16_t)less;
+                }
+            }
+            if (lane == 0) {
+                t.n[0] = __popc(slots);
+                t.first[0][__popc(slots)] = (int16_t)__popc(have);
+                t.n_groups = 1;
+            }
+            __syncwarp();
+            lora_windows(p, t, lane);
+        }
+        __syncthreads();
+        return;
+    }
     for (int i = threadIdx.x; i < kStreamLoraGroups * kAdWords; i += (int)blockDim.x) t.bits[0][i] = 0;
     __syncthreads();
     if (p.kr > 0) {
@@ -198,6 +283,7 @@ __device__ __forceinline__ void make_tables(const StreamParams &p, LoraTables &t
         t.row_of[g * p.nb + col] = (int16_t)i;
     }
     if (threadIdx.x == 0) t.n_groups = ng;
+    if (warp == 0) lora_windows(p, t, lane);
     __syncthreads();
 }
 
@@ -345,7 +431,7 @@ struct Tail {
     int32_t parts[2], tickets[2];  // parts of a tile, tickets, per product
     int32_t pair_at[LORA ? 1 : kPairs];
     float pair_w[LORA ? 1 : kPairs];
-    int32_t items, item, pick[4];  // items of V, the one at hand
+    int32_t item, pick[4];  // item of V at hand
     typename TablesOf<LORA>::T tab;
 };
 
@@ -354,11 +440,13 @@ static_assert(kSmemMax - 1024 - (int)(sizeof(Tail<false>) > sizeof(Tail<true>) ?
                   6 * (2 * kWTile + 16 * 128 + 2048),
               "six stages with 16 token columns");
 
-// Parts of the tiles of a product: as many as give every SM two tickets, where
-// the tiles alone are fewer than five for eight SMs.
+// Parts of the tiles of a product, where the tiles alone are fewer than five for
+// eight SMs: as many as give every SM two tickets, or just one where that is
+// little work already (a part costs its sums' way through memory).
 __host__ __device__ inline int parts_of(int tiles, int ks, int num_sms) {
     if (tiles * 8 >= num_sms * 5 || tiles >= kStreamSplitTiles || tiles == 0) return 1;
-    const int want = (2 * num_sms + tiles - 1) / tiles, most = ks / kMinSteps;
+    const bool little = (int64_t)tiles * ks < (int64_t)kLittle * num_sms;
+    const int want = little ? num_sms / tiles : (2 * num_sms + tiles - 1) / tiles, most = ks / kMinSteps;
     return want < most ? want : most > 1 ? most : 1;
 }
 
@@ -384,7 +472,7 @@ __device__ __forceinline__ bool decode(const StreamParams &p, const Tail<LORA> &
     o.mt = o.tile - o.g * h.mt;
     o.upt = h.ks;
     if constexpr (LORA) {
-        o.upt += t.tab.n[o.g] * p.kr;
+        o.upt += t.tab.n[o.g] * p.kr * t.tab.windows[o.g];
         o.row0 = o.g * p.nb;
         o.n = min(p.nb, p.T - o.row0);
         o.mat0 = 0;
@@ -396,6 +484,14 @@ __device__ __forceinline__ bool decode(const StreamParams &p, const Tail<LORA> &
     }
     o.k0 = o.upt * o.part / parts;
     o.k1 = o.upt * (o.part + 1) / parts;
+    if constexpr (LORA) {
+        // a stage without room for V's halves of all columns: the low-rank steps
+        // are the last part's, after an FP8 step at least
+        if (p.halves == 2 && p.v_cols < p.nb) {
+            o.k0 = h.ks * o.part / parts;
+            o.k1 = o.part + 1 == parts ? o.upt : h.ks * (o.part + 1) / parts;
+        }
+    }
     o.n16 = (o.n + 15) & ~15;
     if (!LORA && o.ph == 0) {
         o.mat1 = o.mat0 + 1;
@@ -412,25 +508,36 @@ __device__ __forceinline__ bool decode(const StreamParams &p, const Tail<LORA> &
 
 // Step k of a tile: FP8 steps first, then the low-rank ones.  `lo`, `n`: the
 // token columns it covers, all of them but in low-rank steps: the 16-column
-// windows of the slot's rows (the step that starts an accumulator covers all:
-// V is zero in the others').
+// windows of the slot's rows (of up to v_cols columns where V's halves take rows
+// of their own; the step that starts an accumulator covers all: V is zero in the
+// others').
 struct Step {
     bool fp8;
     int slot, c;  // low-rank: slot of the group, first rank
     int lo, n;
+    bool none;    // low-rank: the slot has no rows in this window
 };
 template <bool LORA>
 __device__ __forceinline__ Step step_of(const StreamParams &p, const Tail<LORA> &t, const Tile &o, int k) {
-    Step s{true, 0, 0, 0, o.n16};
+    Step s{true, 0, 0, 0, o.n16, false};
     if constexpr (LORA) {
         const int l = k - p.ph[0].ks;
         if (l >= 0) {
+            const int nw = t.tab.windows[o.g], per = p.kr * nw;
             s.fp8 = false;
-            s.slot = l / p.kr;
-            s.c = (l - s.slot * p.kr) * 64;
+            s.slot = l / per;
+            const int r = l - s.slot * per;
+            s.c = r / nw * 64;
             if (k != o.k0) {
-                s.lo = t.tab.first[o.g][s.slot] & ~15;
-                s.n = ((t.tab.first[o.g][s.slot + 1] + 15) & ~15) - s.lo;
+                const int lo = t.tab.first[o.g][s.slot] & ~15, hi = (t.tab.first[o.g][s.slot + 1] + 15) & ~15;
+                s.lo = lo;
+                s.n = hi - lo;
+                if (p.halves == 2 && p.v_cols < p.nb) {
+                    const int from = lo + r % nw * p.v_cols;
+                    s.none = from >= hi;
+                    s.lo = s.none ? lo : from;
+                    s.n = s.none ? 16 : min(p.v_cols, hi - from);
+                }
             }
         }
     }
@@ -581,15 +688,15 @@ __device__ __forceinline__ void load_tokens(const StreamParams &p, Tail<LORA> &t
                 if (o.has1 && !pair) ptx::bulk_load(sf + 1024, c1 + k * step, 512, fb);
             } else if constexpr (LORA) {
                 if (!v_done) {  // every item of V
-                    if (!wait_count(p, t, p.counters + 2, t.items)) return;
+                    if (!wait_count(p, t, p.counters + 2, t.tab.items)) return;
                     fence_proxy_async_all();
                     v_done = true;
                 }
                 const int v0 = (o.g * p.slot_cap + st.slot) * p.halves * p.nb;
                 ptx::mbar_arrive_expect_tx(fb, p.halves * st.n * 128u);
-                for (int b = 0; b < p.halves; ++b)
-                    for (int i = st.lo; i < st.lo + st.n; i += 16)
-                        ptx::tma_load_2d(x0 + (b * p.nb + i) * 128, &p.V, fb, st.c, v0 + b * p.nb + i);
+                for (int b = 0; b < p.halves; ++b)  // the window's rows, from the start of the region
+                    for (int i = 0; i < st.n; i += 16)
+                        ptx::tma_load_2d(x0 + (b * st.n + i) * 128, &p.V, fb, st.c, v0 + b * p.nb + st.lo + i);
             }
             r.next(p);
         }
@@ -679,21 +786,24 @@ __device__ __forceinline__ void issue_mmas(const StreamParams &p, Tail<LORA> &t,
                 }
             } else if constexpr (LORA) {
                 const Step st = step_of(p, t, o, k);
-                const int nk = (min(64, p.rank - st.c) + 15) / 16;
-                const uint32_t id16 = ptx::idesc_bf16(128, 0) | (uint32_t)(st.n >> 3) << 17;
-                // the window's first row; the lo half: rows of its own, or columns 32-63
-                const uint64_t xh = x_desc + at + st.lo * 8, xl = xh + (p.halves == 2 ? p.nb * 8 : 4);
-                if (elect_one())
-                    for (int j = 0; j < nk; ++j) {
-                        const uint32_t on = (k != k0 || j != 0) ? 1u : 0u;
+                const int lo = uniform(st.lo), n = uniform(st.n), nk = st.none ? 0 : (uniform(min(64, p.rank - st.c)) + 15) / 16;
+                const uint32_t id16 = ptx::idesc_bf16(128, 0) | (uint32_t)(n >> 3) << 17;
+                const uint32_t first = k == k0 ? 0u : 1u;
+                // the lo half: rows of its own after the hi ones, or columns 32-63
+                const uint64_t xh = x_desc + at, xl = xh + (p.halves == 2 ? n * 8 : 4);
+                if (elect_one()) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (j >= nk) break;
                         const uint64_t w0 = w_desc + at + 2 * j, w1 = w0 + tile16;
-                        ptx::mma_bf16(d0 + st.lo, w0, xh + 2 * j, id16, on);
-                        ptx::mma_bf16(d0 + st.lo, w0, xl + 2 * j, id16, 1u);
+                        ptx::mma_bf16(d0 + lo, w0, xh + 2 * j, id16, j == 0 ? first : 1u);
+                        ptx::mma_bf16(d0 + lo, w0, xl + 2 * j, id16, 1u);
                         if (has1) {
-                            ptx::mma_bf16(d1 + st.lo, w1, xh + 2 * j, id16, on);
-                            ptx::mma_bf16(d1 + st.lo, w1, xl + 2 * j, id16, 1u);
+                            ptx::mma_bf16(d1 + lo, w1, xh + 2 * j, id16, j == 0 ? first : 1u);
+                            ptx::mma_bf16(d1 + lo, w1, xl + 2 * j, id16, 1u);
                         }
                     }
+                }
             }
             if (elect_one()) ptx::tc_commit(ptx::smem_addr(&t.empty[r.stage]));
             __syncwarp();
@@ -769,8 +879,9 @@ __device__ __forceinline__ void x_pairs(const StreamParams &p, int64_t off, bool
 // of a row; the same K permutation on both operands leaves the product as it
 // is.  Bound by the latency of its loads (an adapter's 16 ranks are 131 KB at
 // K = 4096): kU K steps of 32 are in flight per warp.
+// FEW: eight rows at most (the MMA's other eight are zero), more steps in flight.
 // False: past the last item.
-template <bool BF16>
+template <bool BF16, bool FEW>
 __device__ __forceinline__ bool low_rank(const StreamParams &p, LoraTables &t, int32_t *pick, int item) {
     const int tid = threadIdx.x - kSEpiWarp0 * 32, warp = tid >> 5, lane = tid & 31;
     const int rblocks = (p.rank + 15) / 16;
@@ -827,7 +938,7 @@ __device__ __forceinline__ bool low_rank(const StreamParams &p, LoraTables &t, i
     const __nv_bfloat16 *a1 = A + ((int64_t)l * p.rank + min(r1, p.rank - 1)) * p.K + c8;
     float d0[4] = {}, d1[4] = {};
     const int steps = p.K / 32;  // K is a multiple of 32
-    constexpr int kU = BF16 ? 4 : 2;
+    constexpr int kU = BF16 ? (FEW ? 6 : 4) : 2;
     for (int s0 = warp * kU; s0 < steps; s0 += kSEpiWarps * kU) {
         uint4 xa[kU], xb[kU], wa[kU], wb[kU], ya[BF16 ? 1 : kU], yb[BF16 ? 1 : kU];
 #pragma unroll
@@ -835,7 +946,10 @@ __device__ __forceinline__ bool low_rank(const StreamParams &p, LoraTables &t, i
             const bool in = s0 + u < steps;
             const int64_t k = in ? (int64_t)(s0 + u) * 32 : 0;
             x_pairs<BF16>(p, x0 + k, in && on0, xa[u], ya[BF16 ? 0 : u]);
-            x_pairs<BF16>(p, x1 + k, in && on1, xb[u], yb[BF16 ? 0 : u]);
+            if constexpr (FEW)
+                xb[u] = yb[BF16 ? 0 : u] = z;
+            else
+                x_pairs<BF16>(p, x1 + k, in && on1, xb[u], yb[BF16 ? 0 : u]);
             wa[u] = in && r0 < p.rank ? __ldg(reinterpret_cast<const uint4 *>(a0 + k)) : z;
             wb[u] = in && r1 < p.rank ? __ldg(reinterpret_cast<const uint4 *>(a1 + k)) : z;
         }
@@ -1172,16 +1286,6 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const __grid_constant__ 
             t.parts[i] = parts_of(tiles, p.ph[i].ks, (int)gridDim.x);
             t.tickets[i] = tiles * t.parts[i];
         }
-    if constexpr (LORA) {
-        if (warp == 1) {
-            int n = 0;
-            for (int g = 0; g < t.tab.n_groups; ++g)
-                for (int s = lane; s < t.tab.n[g]; s += 32)
-                    n += (t.tab.first[g][s + 1] - t.tab.first[g][s] + 15) / 16 * ((p.rank + 15) / 16);
-            n = __reduce_add_sync(0xffffffffu, n);
-            if (lane == 0) t.items = n;
-        }
-    }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -1222,11 +1326,13 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const __grid_constant__ 
                 if (threadIdx.x == kSEpiWarp0 * 32) t.item = atomicAdd(p.counters + 1, 1);
                 (void)epi_all(true);
                 const int item = t.item;
-                if (item >= t.items) break;
-                if (p.x_bf16)
-                    (void)low_rank<true>(p, t.tab, t.pick, item);
+                if (item >= t.tab.items) break;
+                if (p.x_bf16 && p.T <= 8)
+                    (void)low_rank<true, true>(p, t.tab, t.pick, item);
+                else if (p.x_bf16)
+                    (void)low_rank<true, false>(p, t.tab, t.pick, item);
                 else
-                    (void)low_rank<false>(p, t.tab, t.pick, item);
+                    (void)low_rank<false, false>(p, t.tab, t.pick, item);
                 fence_proxy_async_all();
                 (void)epi_all(true);
                 if (threadIdx.x == kSEpiWarp0 * 32) (void)atom_add_acq_rel(p.counters + 2, 1);
@@ -1300,7 +1406,10 @@ void stream_sizes(StreamParams &p, int nb, int sub, bool lora, int v_halves) {
     // two accumulators of two tiles each beside the scales, where they fit
     p.nacc = nb <= 64 ? 2 : 1;
     p.w_bytes = sub * kWTile;
-    p.x_bytes = nb * 128 * v_halves;
+    // V's halves in rows of their own: room for all columns of both, or of
+    // kStreamMaxTokens for half of them (more stages; the rest takes a second step)
+    p.v_cols = v_halves == 2 && nb == kStreamMaxTokens ? nb / 2 : nb;
+    p.x_bytes = (v_halves == 2 ? 2 * p.v_cols : nb) * 128;
     // the scales' chunks (512 bytes each: tokens, weight tiles), in 1024-byte multiples
     p.stage_bytes = p.w_bytes + p.x_bytes + (sub == 2 ? 2048 : 1024);
     const int room = kSmemMax - 1024 - (int)(lora ? sizeof(Tail<true>) : sizeof(Tail<false>));
