@@ -746,7 +746,9 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, 
 // Warp 1.  The whole warp goes through the loop and one lane issues: operands
 // that the compiler knows to be the same in all lanes are in uniform registers
 // already (from a branch for lane 0 alone a step's eight MMAs took 0.4 us to
-// issue, more than 4-bit weights take to load).
+// issue, more than 4-bit weights take to load).  MMAs into one accumulator follow
+// each other at about 140 cycles however few their columns, so a tile has two
+// where tensor memory allows (chains): MMAs alternate and the epilogue adds them.
 template <bool LORA>
 __device__ __forceinline__ void issue_mmas(const StreamParams &p, Tail<LORA> &t, uint32_t sbase, uint32_t tmem,
                                            uint32_t sf_tmem) {
@@ -757,51 +759,57 @@ __device__ __forceinline__ void issue_mmas(const StreamParams &p, Tail<LORA> &t,
     // matrix descriptors of stage 0; a stage on: stage16 more
     const uint64_t w_desc = ptx::desc_kmajor_sw128(sbase), x_desc = ptx::desc_kmajor_sw128(sbase + p.w_bytes);
     const uint32_t stage16 = (uint32_t)p.stage_bytes >> 4, tile16 = kWTile >> 4;
+    const uint32_t tile_cols = p.chains * p.nb, odd = p.chains == 2 ? p.nb : 0;
+    auto wait = [&](uint64_t *bar, uint32_t phase, unsigned detail) {
+        const uint32_t b = ptx::smem_addr(bar);
+        if (__all_sync(0xffffffffu, ptx::mbar_try_wait(b, phase))) return true;
+        return wait_bar_warp(b, phase, abort_flag, p, detail);
+    };
     for (int lt = 0; take<LORA, true>(p, t, q, o, 1); ++lt) {
         uint32_t par;
         const int acc = acc_of(p, lt, par);
-        if (!wait_bar_warp(ptx::smem_addr(&t.acce[acc]), par ^ 1u, abort_flag, p, 256 + 64 + acc)) return;
+        if (!wait(&t.acce[acc], par ^ 1u, 256 + 64 + acc)) return;
         ptx::tc_fence_after();
         const int k0 = uniform(o.k0), k1 = uniform(o.k1), n16 = uniform(o.n16), fp8 = p.ph[0].ks;
         const bool has1 = uniform(o.has1) != 0;
-        const uint32_t d0 = tmem + acc * 2 * p.nb, d1 = d0 + p.nb;
+        const uint32_t d0 = tmem + acc * p.acc_cols, d1 = d0 + tile_cols;
         const uint32_t id8 = ptx::idesc_mxf8(128, 0, 0) | (uint32_t)(n16 >> 3) << 17 | p.w_fmt;
         for (int k = k0; k < k1; ++k) {
-            if (!wait_bar_warp(ptx::smem_addr(&t.sfr[r.stage]), r.phase, abort_flag, p, 256 + r.stage)) return;
+            if (!wait(&t.sfr[r.stage], r.phase, 256 + r.stage)) return;
             ptx::tc_fence_after();
             const uint32_t at = r.stage * stage16;
+            const uint32_t first = k == k0 ? 0u : 1u;
             if (!LORA || k < fp8) {
                 const uint32_t sf = sf_tmem + r.stage * kSfSlot;
-                const uint32_t first = k == k0 ? 0u : 1u;
                 if (elect_one()) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const uint32_t id = id8 | ((uint32_t)j << 4) | ((uint32_t)j << 29);
-                        const uint32_t on = j == 0 ? first : 1u;
-                        ptx::mma_mxf8(d0, w_desc + at + 2 * j, x_desc + at + 2 * j, id, sf, sf + 8, on);
+                        const uint32_t on = j < p.chains ? first : 1u, c = (j & 1) ? odd : 0;
+                        ptx::mma_mxf8(d0 + c, w_desc + at + 2 * j, x_desc + at + 2 * j, id, sf, sf + 8, on);
                         if (has1)
-                            ptx::mma_mxf8(d1, w_desc + at + tile16 + 2 * j, x_desc + at + 2 * j, id, sf + 4,
+                            ptx::mma_mxf8(d1 + c, w_desc + at + tile16 + 2 * j, x_desc + at + 2 * j, id, sf + 4,
                                           sf + 8, on);
                     }
                 }
             } else if constexpr (LORA) {
                 const Step st = step_of(p, t, o, k);
-                const int lo = uniform(st.lo), n = uniform(st.n), nk = st.none ? 0 : (uniform(min(64, p.rank - st.c)) + 15) / 16;
+                const int lo = uniform(st.lo), n = uniform(st.n);
+                const int nk = uniform(st.none ? 0 : (min(64, p.rank - st.c) + 15) / 16);
                 const uint32_t id16 = ptx::idesc_bf16(128, 0) | (uint32_t)(n >> 3) << 17;
-                const uint32_t first = k == k0 ? 0u : 1u;
-                // the lo half: rows of its own after the hi ones, or columns 32-63
+                // the lo half: rows of its own after the hi ones, or columns 32-63;
+                // into the second accumulator
                 const uint64_t xh = x_desc + at, xl = xh + (p.halves == 2 ? n * 8 : 4);
+                const uint32_t dh = d0 + lo, dl = dh + odd, e = first | (p.chains == 1 ? 1u : 0u);
                 if (elect_one()) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         if (j >= nk) break;
                         const uint64_t w0 = w_desc + at + 2 * j, w1 = w0 + tile16;
-                        ptx::mma_bf16(d0 + lo, w0, xh + 2 * j, id16, j == 0 ? first : 1u);
-                        ptx::mma_bf16(d0 + lo, w0, xl + 2 * j, id16, 1u);
-                        if (has1) {
-                            ptx::mma_bf16(d1 + lo, w1, xh + 2 * j, id16, j == 0 ? first : 1u);
-                            ptx::mma_bf16(d1 + lo, w1, xl + 2 * j, id16, 1u);
-                        }
+                        ptx::mma_bf16(dh, w0, xh + 2 * j, id16, j == 0 ? first : 1u);
+                        if (has1) ptx::mma_bf16(dh + tile_cols, w1, xh + 2 * j, id16, j == 0 ? first : 1u);
+                        ptx::mma_bf16(dl, w0, xl + 2 * j, id16, j == 0 ? e : 1u);
+                        if (has1) ptx::mma_bf16(dl + tile_cols, w1, xl + 2 * j, id16, j == 0 ? e : 1u);
                     }
                 }
             }
@@ -1157,7 +1165,18 @@ __device__ __forceinline__ void finish_tile(const StreamParams &p, Tail<LORA> &t
     const int c_first = by_cols ? half * kCols : 0, c_step = by_cols ? 2 * kCols : kCols;
     const int my_sub = by_cols ? 0 : half;
     const bool live = my_sub == 0 || o.has1;  // this warp has a weight tile
-    const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + acc * 2 * p.nb;
+    const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + acc * p.acc_cols;
+    // kCols columns from c on of weight tile sub, its chains added
+    auto load = [&](int sub, int c, float (&d)[kCols]) {
+        const uint32_t at = ta + sub * p.chains * p.nb + c;
+        uint32_t r[kCols], x[kCols];
+        ptx::tmem_ld_32x32b_x8(at, r);
+        if (p.chains == 2) ptx::tmem_ld_32x32b_x8(at + p.nb, x);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < kCols; ++i)
+            d[i] = p.chains == 2 ? __uint_as_float(r[i]) + __uint_as_float(x[i]) : __uint_as_float(r[i]);
+    };
     const int parts = t.parts[o.ph];
     const int64_t part_size = (int64_t)2 * p.nb * 128;
     float *part0 = h.part + (int64_t)o.tile * parts * part_size;  // the tile's parts
@@ -1169,13 +1188,12 @@ __device__ __forceinline__ void finish_tile(const StreamParams &p, Tail<LORA> &t
 #pragma unroll
                 for (int s = 0; s < kSubs; ++s) {
                     const int sub = EPI == kGated ? s : my_sub;
-                    uint32_t r[kCols];
-                    ptx::tmem_ld_32x32b_x8(ta + sub * p.nb + c, r);
-                    ptx::tmem_ld_wait();
+                    float d[kCols];
+                    load(sub, c, d);
                     float *dst = part + ((int64_t)sub * p.nb + c) * 128 + row_l;
 #pragma unroll
                     for (int i = 0; i < kCols; ++i)
-                        if (c + i < o.n) __stcg(dst + i * 128, __uint_as_float(r[i]));
+                        if (c + i < o.n) __stcg(dst + i * 128, d[i]);
                 }
         ptx::tc_fence_before();
         __syncwarp();
@@ -1195,11 +1213,7 @@ __device__ __forceinline__ void finish_tile(const StreamParams &p, Tail<LORA> &t
             for (int s = 0; s < kSubs; ++s) {
                 const int sub = EPI == kGated ? s : my_sub;
                 if (parts == 1) {
-                    uint32_t r[kCols];
-                    ptx::tmem_ld_32x32b_x8(ta + sub * p.nb + c, r);
-                    ptx::tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < kCols; ++i) v[s][i] = __uint_as_float(r[i]);
+                    load(sub, c, v[s]);
                 } else {
                     // in order; several parts' loads in flight at a time
 #pragma unroll
@@ -1290,7 +1304,7 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const __grid_constant__ 
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = t.tmem;
-    const uint32_t sf_tmem = tmem + p.nacc * 2 * p.nb;
+    const uint32_t sf_tmem = tmem + p.nacc * p.acc_cols;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -1403,8 +1417,13 @@ cudaError_t launch_one(const StreamParams &p, int grid, cudaStream_t s) {
 
 void stream_sizes(StreamParams &p, int nb, int sub, bool lora, int v_halves) {
     p.nb = nb;
-    // two accumulators of two tiles each beside the scales, where they fit
-    p.nacc = nb <= 64 ? 2 : 1;
+    // Tensor memory beside the scales (up to eight stages' 128 columns): two
+    // accumulators, so that a tile's epilogue overlaps the next tile, then two
+    // chains each
+    const int room_cols = 512 - 8 * kSfSlot;
+    p.nacc = 2 * sub * nb <= room_cols ? 2 : 1;
+    p.chains = p.nacc * sub * 2 * nb <= room_cols ? 2 : 1;
+    p.acc_cols = sub * p.chains * nb;
     p.w_bytes = sub * kWTile;
     // V's halves in rows of their own: room for all columns of both, or of
     // kStreamMaxTokens for half of them (more stages; the rest takes a second step)
@@ -1414,7 +1433,7 @@ void stream_sizes(StreamParams &p, int nb, int sub, bool lora, int v_halves) {
     p.stage_bytes = p.w_bytes + p.x_bytes + (sub == 2 ? 2048 : 1024);
     const int room = kSmemMax - 1024 - (int)(lora ? sizeof(Tail<true>) : sizeof(Tail<false>));
     p.stages = room / p.stage_bytes;
-    const int cols = (512 - p.nacc * 2 * nb) / kSfSlot;
+    const int cols = (512 - p.nacc * p.acc_cols) / kSfSlot;
     if (p.stages > cols) p.stages = cols;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
 }

@@ -39,7 +39,7 @@ struct StreamPhase {
 struct StreamParams {
     StreamPhase ph[2];     // MoE: gate/up and down products; adapters: ph[0]
     int32_t nb;            // token columns of an accumulator (a multiple of 16)
-    int32_t nacc;          // accumulators (2: a tile's epilogue overlaps the next tile)
+    int32_t nacc, chains, acc_cols;  // accumulators; chains of MMAs in one, its columns
     int32_t stages, stage_bytes, w_bytes, x_bytes;  // shared-memory ring: a stage, its weights, its tokens
     uint32_t w_fmt;        // weight format as MMA instruction-descriptor bits
     int32_t gap8;          // eighths of a weight tile a packed load does not deliver
