@@ -323,8 +323,8 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
     if (!pair) {
         // one weight tile a unit where pairs of them would be few
         h.sub = tiles * ((N + 255) / 256) * 8 >= d.num_sms * 5 ? 2 : 1;
-        stream_sizes(p, nb, h.sub, true, lv.halves);
         h.mt = (int32_t)((N + 128 * h.sub - 1) / (128 * h.sub));
+        stream_sizes(p, nb, h.sub, true, lv.halves, stream_one_ticket(tiles * h.mt, ks, d.num_sms));
         h.ks = ks;
         h.rows = (int32_t)N;
         h.n_rt = n_rt;
@@ -347,14 +347,18 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
     void *wsv = nullptr;
     if (cudaMallocFromPoolAsync(&wsv, at, pool, stream) != cudaSuccess) return FP8G_ERR_CUDA;
     uint8_t *ws = static_cast<uint8_t *>(wsv);
-    CUtensorMap mb{}, mv{};
+    CUtensorMap mb{}, mv{}, mv1{};
     if (lora) {
         const uint64_t db[3] = {(uint64_t)r, (uint64_t)N, (uint64_t)L};
         const uint32_t bb[3] = {64u, 128u, 1u};
         const uint64_t dv[2] = {(uint64_t)lv.r64, (uint64_t)tiles * cap * lv.halves * nb};
-        const uint32_t bv[2] = {64u, pair ? 128u : 16u};
+        const uint32_t bv[2] = {64u, 128u};
+        const uint64_t dv3[3] = {(uint64_t)lv.r64, (uint64_t)nb, (uint64_t)tiles * cap * lv.halves};
+        const uint32_t bv2[3] = {64u, 16u, (uint32_t)lv.halves}, bv1[3] = {64u, 16u, 1u};
         st = host_bf16_map(lora_b, 3, db, bb, d.dev, mb);
-        if (st == FP8G_OK) st = host_bf16_map(ws + o_v, 2, dv, bv, d.dev, mv);
+        if (st == FP8G_OK)
+            st = pair ? host_bf16_map(ws + o_v, 2, dv, bv, d.dev, mv) : host_bf16_map(ws + o_v, 3, dv3, bv2, d.dev, mv);
+        if (st == FP8G_OK && !pair) st = host_bf16_map(ws + o_v, 3, dv3, bv1, d.dev, mv1);
     }
     const bool bf16 = x_dtype == FP8G_IN_BF16;
     cudaError_t e = cudaSuccess;
@@ -389,6 +393,7 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
         p.timeout_ns = d.timeout_ns;
         p.B = mb;
         p.V = mv;
+        p.V1 = mv1;
         p.a = lora_a;
         p.alpha = alpha;
         p.bias = bias;

@@ -37,6 +37,8 @@
 // 0.08 us to issue a copy, and a step has six.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "kernel_common.cuh"
 #include "quant_math.cuh"
 #include "stream.h"
@@ -432,6 +434,7 @@ struct Tail {
     int32_t pair_at[LORA ? 1 : kPairs];
     float pair_w[LORA ? 1 : kPairs];
     int32_t item, pick[4];  // item of V at hand
+    uint32_t low[LORA ? kMaxStages : 1];  // a stage's low-rank step: first column, columns, MMAs of each half
     typename TablesOf<LORA>::T tab;
 };
 
@@ -517,26 +520,48 @@ struct Step {
     int lo, n;
     bool none;    // low-rank: the slot has no rows in this window
 };
+// A role's way through a tile's low-rank steps: windows in rank blocks in slots.
+struct LowRank {
+    int slot = 0, c = 0, w = 0;
+    template <bool LORA>
+    __device__ __forceinline__ void start(const StreamParams &p, const Tail<LORA> &t, const Tile &o) {
+        if constexpr (LORA) {
+            const int l = o.k0 - p.ph[0].ks;
+            slot = c = w = 0;
+            if (l > 0) {  // (divisions take longer than a step's MMAs: once a tile)
+                const int nw = t.tab.windows[o.g], per = p.kr * nw;
+                slot = l / per;
+                c = (l - slot * per) / nw;
+                w = l - slot * per - c * nw;
+            }
+        }
+    }
+};
 template <bool LORA>
-__device__ __forceinline__ Step step_of(const StreamParams &p, const Tail<LORA> &t, const Tile &o, int k) {
+__device__ __forceinline__ Step step_of(const StreamParams &p, const Tail<LORA> &t, const Tile &o, int k,
+                                        LowRank &q) {
     Step s{true, 0, 0, 0, o.n16, false};
     if constexpr (LORA) {
-        const int l = k - p.ph[0].ks;
-        if (l >= 0) {
-            const int nw = t.tab.windows[o.g], per = p.kr * nw;
+        if (k >= p.ph[0].ks) {
             s.fp8 = false;
-            s.slot = l / per;
-            const int r = l - s.slot * per;
-            s.c = r / nw * 64;
+            s.slot = q.slot;
+            s.c = q.c * 64;
             if (k != o.k0) {
                 const int lo = t.tab.first[o.g][s.slot] & ~15, hi = (t.tab.first[o.g][s.slot + 1] + 15) & ~15;
                 s.lo = lo;
                 s.n = hi - lo;
                 if (p.halves == 2 && p.v_cols < p.nb) {
-                    const int from = lo + r % nw * p.v_cols;
+                    const int from = lo + q.w * p.v_cols;
                     s.none = from >= hi;
                     s.lo = s.none ? lo : from;
                     s.n = s.none ? 16 : min(p.v_cols, hi - from);
+                }
+            }
+            if (++q.w == t.tab.windows[o.g]) {
+                q.w = 0;
+                if (++q.c == p.kr) {
+                    q.c = 0;
+                    ++q.slot;
                 }
             }
         }
@@ -623,6 +648,8 @@ __device__ __forceinline__ void load_weights(const StreamParams &p, Tail<LORA> &
         Tile o;
         if (!decode(p, t, ticket, o)) return;
         const StreamPhase &h = p.ph[o.ph];
+        LowRank low;
+        low.start(p, t, o);
         const int ask = max(o.k0, o.k1 - 2);
         for (int k = o.k0; k < o.k1; ++k) {
             // late enough that a CTA does not hold a tile others could start,
@@ -630,7 +657,7 @@ __device__ __forceinline__ void load_weights(const StreamParams &p, Tail<LORA> &
             if (k == ask) next = atomicAdd(p.counters, 1);
             if (!wait_bar(ptx::smem_addr(&t.empty[r.stage]), r.phase ^ 1u, abort_flag, p, r.stage)) return;
             const uint32_t fb = ptx::smem_addr(&t.full[r.stage]), s0 = sbase + r.stage * p.stage_bytes;
-            const Step st = step_of(p, t, o, k);
+            const Step st = step_of(p, t, o, k, low);
             if (st.fp8) {
                 ptx::mbar_arrive_expect_tx(fb, o.has1 ? 2 * w_tx : w_tx);
                 ptx::tma_load_3d(s0, &h.W, fb, k * kBK, o.w0, o.mat0);
@@ -664,6 +691,8 @@ __device__ __forceinline__ void load_tokens(const StreamParams &p, Tail<LORA> &t
             fence_proxy_async_all();
             ready = o.g;
         }
+        LowRank low;
+        low.start(p, t, o);
         const int64_t step = (int64_t)h.n_rt * 512;
         const uint8_t *c0 = h.sfw + (int64_t)o.mat0 * h.ks * step + o.w0 / 128 * 512;
         const uint8_t *c1 = h.sfw + (int64_t)o.mat1 * h.ks * step + o.w1 / 128 * 512;
@@ -678,7 +707,7 @@ __device__ __forceinline__ void load_tokens(const StreamParams &p, Tail<LORA> &t
                 return;
             const uint32_t fb = ptx::smem_addr(&t.full[r.stage]);
             const uint32_t x0 = sbase + r.stage * p.stage_bytes + p.w_bytes, sf = x0 + p.x_bytes;
-            const Step st = step_of(p, t, o, k);
+            const Step st = step_of(p, t, o, k, low);
             if (st.fp8) {
                 ptx::mbar_arrive_expect_tx(fb, boxes * box * 128u + (o.has1 ? 1536u : 1024u));
                 for (int i = 0; i < boxes; ++i)
@@ -692,11 +721,18 @@ __device__ __forceinline__ void load_tokens(const StreamParams &p, Tail<LORA> &t
                     fence_proxy_async_all();
                     v_done = true;
                 }
-                const int v0 = (o.g * p.slot_cap + st.slot) * p.halves * p.nb;
+                t.low[r.stage] = (uint32_t)(st.lo | st.n << 8 |
+                                            (st.none ? 0 : (min(64, p.rank - st.c) + 15) / 16) << 16);
+                // the window's rows, from the start of the region: the halves in
+                // one copy, or of a wider window each half's 16 rows in turn
+                const int v0 = (o.g * p.slot_cap + st.slot) * p.halves;
                 ptx::mbar_arrive_expect_tx(fb, p.halves * st.n * 128u);
-                for (int b = 0; b < p.halves; ++b)  // the window's rows, from the start of the region
-                    for (int i = 0; i < st.n; i += 16)
-                        ptx::tma_load_2d(x0 + (b * st.n + i) * 128, &p.V, fb, st.c, v0 + b * p.nb + st.lo + i);
+                if (st.n == 16)
+                    ptx::tma_load_3d(x0, &p.V, fb, st.c, st.lo, v0);
+                else
+                    for (int b = 0; b < p.halves; ++b)
+                        for (int i = 0; i < st.n; i += 16)
+                            ptx::tma_load_3d(x0 + (b * st.n + i) * 128, &p.V1, fb, st.c, st.lo + i, v0 + b);
             }
             r.next(p);
         }
@@ -717,7 +753,7 @@ __device__ __forceinline__ void copy_scales(const StreamParams &p, Tail<LORA> &t
             if (!wait_bar(ptx::smem_addr(&t.full[r.stage]), r.phase, &t.abort_flag, p, 2 * 256 + r.stage))
                 return;
             ptx::tc_fence_after();
-            if (step_of(p, t, o, k).fp8) {
+            if (!LORA || k < p.ph[0].ks) {
                 const uint32_t sf = sf_tmem + r.stage * kSfSlot;
                 const uint32_t cs = sbase + r.stage * p.stage_bytes + p.w_bytes + p.x_bytes;
                 ptx::tc_cp_32x128b_warpx4(sf, ptx::desc_sf_chunk(cs + 512));
@@ -793,9 +829,8 @@ __device__ __forceinline__ void issue_mmas(const StreamParams &p, Tail<LORA> &t,
                     }
                 }
             } else if constexpr (LORA) {
-                const Step st = step_of(p, t, o, k);
-                const int lo = uniform(st.lo), n = uniform(st.n);
-                const int nk = uniform(st.none ? 0 : (min(64, p.rank - st.c) + 15) / 16);
+                const int all = uniform((int)t.low[r.stage]);
+                const int lo = all & 255, n = all >> 8 & 255, nk = all >> 16;
                 const uint32_t id16 = ptx::idesc_bf16(128, 0) | (uint32_t)(n >> 3) << 17;
                 // the lo half: rows of its own after the hi ones, or columns 32-63;
                 // into the second accumulator
@@ -853,7 +888,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&b);
 }
-__device__ __forceinline__ float bf16_rest(float v) { return v - __bfloat162float(__float2bfloat16_rn(v)); }
+// What rounding to bf16 leaves of v (of an infinity, or a v rounded to one: nothing).
+__device__ __forceinline__ float bf16_rest(float v) {
+    const float h = __bfloat162float(__float2bfloat16_rn(v));
+    return isinf(h) ? 0.0f : v - h;
+}
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -866,44 +905,132 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
 // Eight values of x as bf16 pairs; of fp32 x the rounded values (hi) and what
 // they leave, rounded (lo).
 template <bool BF16>
-__device__ __forceinline__ void x_pairs(const StreamParams &p, int64_t off, bool in, uint4 &hi, uint4 &lo) {
-    hi = make_uint4(0u, 0u, 0u, 0u);
+__device__ __forceinline__ void x_pairs(const StreamParams &p, int64_t off, uint4 &hi, uint4 &lo) {
     if constexpr (BF16) {
-        if (in) hi = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.x) + off));
-        return;
+        hi = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.x) + off));
+    } else {
+        float4 a, b;
+        load8<false>(p.x, off, a, b);
+        hi = make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
+        lo = make_uint4(pack_bf16(bf16_rest(a.x), bf16_rest(a.y)), pack_bf16(bf16_rest(a.z), bf16_rest(a.w)),
+                        pack_bf16(bf16_rest(b.x), bf16_rest(b.y)), pack_bf16(bf16_rest(b.z), bf16_rest(b.w)));
     }
-    lo = hi;
-    if (!in) return;
-    float4 a, b;
-    load8<false>(p.x, off, a, b);
-    hi = make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
-    lo = make_uint4(pack_bf16(bf16_rest(a.x), bf16_rest(a.y)), pack_bf16(bf16_rest(a.z), bf16_rest(a.w)),
-                    pack_bf16(bf16_rest(b.x), bf16_rest(b.y)), pack_bf16(bf16_rest(b.z), bf16_rest(b.w)));
 }
 
-// An item is 16 rows of a slot against 16 ranks of its
-// adapter; the K range goes over the eight warps, each a 16 x 16 product by
-// mma.sync, joined in warp order.  A lane's 16-byte load covers 8 consecutive K
-// of a row; the same K permutation on both operands leaves the product as it
-// is.  Bound by the latency of its loads (an adapter's 16 ranks are 131 KB at
-// K = 4096): kU K steps of 32 are in flight per warp.
-// FEW: eight rows at most (the MMA's other eight are zero), more steps in flight.
-// False: past the last item.
+// An item is up to 16 rows of a slot against 16 ranks of its adapter; the K range
+// goes over the eight warps, each a 16 x 16 product by mma.sync (ranks x rows),
+// joined in warp order.  A lane's 16-byte load covers 8 consecutive K of a row;
+// the same K permutation on both operands leaves the product as it is.  kU K
+// steps of 32 are on the way in a warp.  With two warps to a scheduler what
+// bounds this, next to the loads' latency (an adapter's 16 ranks are 131 KB at
+// K = 4096), is the number of instructions: rows and ranks past the end read
+// others' values, into products that are not stored, and no load has a condition.
+// FEW: eight rows at most.
 template <bool BF16, bool FEW>
-__device__ __forceinline__ bool low_rank(const StreamParams &p, LoraTables &t, int32_t *pick, int item) {
+__device__ __forceinline__ void low_rank_item(const StreamParams &p, LoraTables &t, const int32_t *pick) {
     const int tid = threadIdx.x - kSEpiWarp0 * 32, warp = tid >> 5, lane = tid & 31;
+    const int g = pick[0], slot = pick[1], l = t.adapter[g][slot], rb = pick[3];
+    const int col0 = t.first[g][slot] + pick[2], n = min(16, t.first[g][slot + 1] - col0);  // this item's columns
+    __nv_bfloat16 *hi = static_cast<__nv_bfloat16 *>(p.v) +
+                        (int64_t)(g * p.slot_cap + slot) * p.halves * p.nb * p.r64 + rb * 16;
+    const int64_t half = p.halves == 2 ? (int64_t)p.nb * p.r64 : 32;
+    if (pick[2] == 0) {
+        // the slot's first rows: zeros for the tokens of other adapters, and
+        // in the columns past the rank
+        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+        const int rblocks = (p.rank + 15) / 16, cols = (p.halves == 2 ? p.r64 : 32) / 8;
+        const int s_lo = t.first[g][slot], s_hi = t.first[g][slot + 1];
+        for (int i = tid; i < p.nb; i += kEpiThreads) {
+            uint4 *d = reinterpret_cast<uint4 *>(hi + (int64_t)i * p.r64);
+            uint4 *e = reinterpret_cast<uint4 *>(hi + half + (int64_t)i * p.r64);
+            if (i < s_lo || i >= s_hi) d[0] = d[1] = e[0] = e[1] = z;
+            if (rb == 0)
+                for (int c = 2 * rblocks; c < cols; ++c) d[c] = e[c] = z;
+        }
+    }
+    const int gr = lane >> 2, c8 = 8 * (lane & 3);
+    const int64_t lo = (int64_t)g * p.nb + col0;
+    const int64_t x0 = (int64_t)t.row_of[lo + min(gr, n - 1)] * p.K + c8;
+    const int64_t x1 = (int64_t)t.row_of[lo + min(gr + 8, n - 1)] * p.K + c8;
+    const int r0 = min(rb * 16 + gr, p.rank - 1), r1 = min(rb * 16 + gr + 8, p.rank - 1);
+    const __nv_bfloat16 *A = static_cast<const __nv_bfloat16 *>(p.a) + (int64_t)l * p.rank * p.K + c8;
+    const __nv_bfloat16 *a0 = A + (int64_t)r0 * p.K, *a1 = A + (int64_t)r1 * p.K;
+    float d0[4] = {}, d1[4] = {};  // rows 0-7, 8-15
+    constexpr int kU = BF16 ? (FEW ? 6 : 4) : 2;
+    auto go = [&](auto count, int s0) {
+        constexpr int U = decltype(count)::value;
+        uint4 xa[U], xb[U], wa[U], wb[U], ya[U], yb[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = (s0 + u) * 32;
+            wa[u] = __ldg(reinterpret_cast<const uint4 *>(a0 + k));
+            wb[u] = __ldg(reinterpret_cast<const uint4 *>(a1 + k));
+            x_pairs<BF16>(p, x0 + k, xa[u], ya[u]);
+            if constexpr (!FEW) x_pairs<BF16>(p, x1 + k, xb[u], yb[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t f0[4] = {wa[u].x, wb[u].x, wa[u].y, wb[u].y};
+            const uint32_t f1[4] = {wa[u].z, wb[u].z, wa[u].w, wb[u].w};
+            mma_16816(d0, f0, xa[u].x, xa[u].y);
+            if constexpr (!FEW) mma_16816(d1, f0, xb[u].x, xb[u].y);
+            mma_16816(d0, f1, xa[u].z, xa[u].w);
+            if constexpr (!FEW) mma_16816(d1, f1, xb[u].z, xb[u].w);
+            if constexpr (!BF16) {
+                mma_16816(d0, f0, ya[u].x, ya[u].y);
+                mma_16816(d1, f0, yb[u].x, yb[u].y);
+                mma_16816(d0, f1, ya[u].z, ya[u].w);
+                mma_16816(d1, f1, yb[u].z, yb[u].w);
+            }
+        }
+    };
+    const int steps = p.K / 32;  // K is a multiple of 32
+    int s0 = warp * kU;
+    for (; s0 + kU <= steps; s0 += kSEpiWarps * kU) go(std::integral_constant<int, kU>{}, s0);
+#pragma unroll 1
+    for (; s0 < steps; ++s0) go(std::integral_constant<int, 1>{}, s0);
+    // the warps' products: warp w + 4 to warp w, then the four in order
+    const int c2 = 2 * (lane & 3);
+    float(*acc)[17] = t.acc[warp & 3];  // [row][rank]
+    if (warp >= 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            acc[c2 + (e & 1)][gr + 8 * (e >> 1)] = d0[e];
+            if constexpr (!FEW) acc[8 + c2 + (e & 1)][gr + 8 * (e >> 1)] = d1[e];
+        }
+    }
+    (void)epi_all(true);
+    if (warp < 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            acc[c2 + (e & 1)][gr + 8 * (e >> 1)] += d0[e];
+            if constexpr (!FEW) acc[8 + c2 + (e & 1)][gr + 8 * (e >> 1)] += d1[e];
+        }
+    }
+    (void)epi_all(true);
+    const int i = tid >> 4, c = tid & 15;
+    float v = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kSEpiWarps / 2; ++q) v += t.acc[q][i][c];
+    if (p.alpha != nullptr) v *= __ldg(p.alpha + l);
+    if (rb * 16 + c >= p.rank) v = 0.0f;
+    if (i < n) {
+        const int64_t at = (int64_t)(col0 + i) * p.r64 + c;
+        hi[at] = __float2bfloat16_rn(v);
+        hi[half + at] = __float2bfloat16_rn(bf16_rest(v));
+    }
+}
+
+__device__ __forceinline__ void low_rank(const StreamParams &p, LoraTables &t, int32_t *pick, int item) {
     const int rblocks = (p.rank + 15) / 16;
-    const __nv_bfloat16 *A = static_cast<const __nv_bfloat16 *>(p.a);
-    if (warp == 0) {
+    if ((threadIdx.x >> 5) == kSEpiWarp0) {
         // item -> group, slot, 16 rows, rank block
+        const int lane = threadIdx.x & 31;
         int at = 0;
-        if (lane == 0) pick[0] = -1;
-        __syncwarp();
         for (int g = 0; g < t.n_groups; ++g)
             for (int s0 = 0; s0 < t.n[g]; s0 += 32) {
                 const int s = s0 + lane;
-                const int c =
-                    s < t.n[g] ? (t.first[g][s + 1] - t.first[g][s] + 15) / 16 * rblocks : 0;
+                const int c = s < t.n[g] ? (t.first[g][s + 1] - t.first[g][s] + 15) / 16 * rblocks : 0;
                 const int incl = warp_scan(c, lane), first = at + incl - c;
                 if (item >= first && item < first + c) {
                     pick[0] = g;
@@ -915,104 +1042,13 @@ __device__ __forceinline__ bool low_rank(const StreamParams &p, LoraTables &t, i
             }
     }
     (void)epi_all(true);
-    const int g = pick[0];
-    if (g < 0) return false;
-    const int slot = pick[1], l = t.adapter[g][slot], rb = pick[3];
-    const int s_lo = t.first[g][slot], s_hi = t.first[g][slot + 1];
-    const int col0 = s_lo + pick[2], n = min(16, s_hi - col0);  // this item's columns
-    __nv_bfloat16 *hi = static_cast<__nv_bfloat16 *>(p.v) +
-                        (int64_t)(g * p.slot_cap + slot) * p.halves * p.nb * p.r64 + rb * 16;
-    const int64_t half = p.halves == 2 ? (int64_t)p.nb * p.r64 : 32;
-    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-    if (pick[2] == 0) {
-        // the slot's first rows: zeros for the tokens of other adapters, and
-        // in the columns past the rank
-        const int cols = (p.halves == 2 ? p.r64 : 32) / 8;
-        for (int i = tid; i < p.nb; i += kEpiThreads) {
-            uint4 *d = reinterpret_cast<uint4 *>(hi + (int64_t)i * p.r64);
-            uint4 *e = reinterpret_cast<uint4 *>(hi + half + (int64_t)i * p.r64);
-            if (i < s_lo || i >= s_hi) d[0] = d[1] = e[0] = e[1] = z;
-            if (rb == 0)
-                for (int c = 2 * rblocks; c < cols; ++c) d[c] = e[c] = z;
-        }
-    }
-    const int gr = lane >> 2, c8 = 8 * (lane & 3);
-    const int64_t lo = (int64_t)g * p.nb + col0;
-    const bool on0 = gr < n, on1 = gr + 8 < n;
-    const int64_t x0 = (int64_t)t.row_of[on0 ? lo + gr : lo] * p.K + c8;
-    const int64_t x1 = (int64_t)t.row_of[on1 ? lo + gr + 8 : lo] * p.K + c8;
-    const int r0 = rb * 16 + gr, r1 = r0 + 8;
-    const __nv_bfloat16 *a0 = A + ((int64_t)l * p.rank + min(r0, p.rank - 1)) * p.K + c8;
-    const __nv_bfloat16 *a1 = A + ((int64_t)l * p.rank + min(r1, p.rank - 1)) * p.K + c8;
-    float d0[4] = {}, d1[4] = {};
-    const int steps = p.K / 32;  // K is a multiple of 32
-    constexpr int kU = BF16 ? (FEW ? 6 : 4) : 2;
-    for (int s0 = warp * kU; s0 < steps; s0 += kSEpiWarps * kU) {
-        uint4 xa[kU], xb[kU], wa[kU], wb[kU], ya[BF16 ? 1 : kU], yb[BF16 ? 1 : kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const bool in = s0 + u < steps;
-            const int64_t k = in ? (int64_t)(s0 + u) * 32 : 0;
-            x_pairs<BF16>(p, x0 + k, in && on0, xa[u], ya[BF16 ? 0 : u]);
-            if constexpr (FEW)
-                xb[u] = yb[BF16 ? 0 : u] = z;
-            else
-                x_pairs<BF16>(p, x1 + k, in && on1, xb[u], yb[BF16 ? 0 : u]);
-            wa[u] = in && r0 < p.rank ? __ldg(reinterpret_cast<const uint4 *>(a0 + k)) : z;
-            wb[u] = in && r1 < p.rank ? __ldg(reinterpret_cast<const uint4 *>(a1 + k)) : z;
-        }
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const uint32_t f0[4] = {xa[u].x, xb[u].x, xa[u].y, xb[u].y};
-            const uint32_t f1[4] = {xa[u].z, xb[u].z, xa[u].w, xb[u].w};
-            mma_16816(d0, f0, wa[u].x, wa[u].y);
-            mma_16816(d1, f0, wb[u].x, wb[u].y);
-            mma_16816(d0, f1, wa[u].z, wa[u].w);
-            mma_16816(d1, f1, wb[u].z, wb[u].w);
-            if constexpr (!BF16) {
-                const uint32_t h0[4] = {ya[u].x, yb[u].x, ya[u].y, yb[u].y};
-                const uint32_t h1[4] = {ya[u].z, yb[u].z, ya[u].w, yb[u].w};
-                mma_16816(d0, h0, wa[u].x, wa[u].y);
-                mma_16816(d1, h0, wb[u].x, wb[u].y);
-                mma_16816(d0, h1, wa[u].z, wa[u].w);
-                mma_16816(d1, h1, wb[u].z, wb[u].w);
-            }
-        }
-    }
-    // the warps' products: warp w + 4 to warp w, then the four in order
-    const int c2 = 2 * (lane & 3);
-    float(*acc)[17] = t.acc[warp & 3];
-    if (warp >= 4) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            acc[gr + 8 * (e >> 1)][c2 + (e & 1)] = d0[e];
-            acc[gr + 8 * (e >> 1)][8 + c2 + (e & 1)] = d1[e];
-        }
-    }
-    (void)epi_all(true);
-    if (warp < 4) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            acc[gr + 8 * (e >> 1)][c2 + (e & 1)] += d0[e];
-            acc[gr + 8 * (e >> 1)][8 + c2 + (e & 1)] += d1[e];
-        }
-    }
-    (void)epi_all(true);
-    {
-        const int i = tid >> 4, c = tid & 15;
-        float v = 0.0f;
-#pragma unroll
-        for (int q = 0; q < kSEpiWarps / 2; ++q) v += t.acc[q][i][c];
-        if (p.alpha != nullptr) v *= __ldg(p.alpha + l);
-        if (rb * 16 + c >= p.rank) v = 0.0f;
-        if (i < n) {
-            const float rest = bf16_rest(v);  // none for an infinite or NaN V
-            const int64_t at = (int64_t)(col0 + i) * p.r64 + c;
-            hi[at] = __float2bfloat16_rn(v);
-            hi[half + at] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
-        }
-    }
-    return true;
+    const int left = t.first[pick[0]][pick[1] + 1] - t.first[pick[0]][pick[1]] - pick[2];
+    if (!p.x_bf16)
+        low_rank_item<false, false>(p, t, pick);
+    else if (left <= 8)
+        low_rank_item<true, true>(p, t, pick);
+    else
+        low_rank_item<true, false>(p, t, pick);
 }
 
 __device__ __forceinline__ float gate_act(float g, int gate) {
@@ -1022,41 +1058,49 @@ __device__ __forceinline__ float gate_act(float g, int gate) {
 }
 
 // kCols columns of a finished tile: v[s][i] is this lane's weight row f of weight
-// tile s, token column c + i.
+// tile s, token column c + i.  (Plain stores go on with all columns and leave out
+// those past the group, so that their latencies overlap; the layer's, mostly of
+// a column or two, end at the last one.)
 template <bool LORA, int EPI, int SUBS>
 __device__ __forceinline__ void store_cols(const StreamParams &p, const StreamPhase &h, const Tail<LORA> &t,
-                                           const Tile &o, int c, int f, int q, int lane,
+                                           const Tile &o, int c, int c_hi, int f, int q, int lane, float bias,
                                            const float (&v)[SUBS][kCols]) {
+    if constexpr (EPI != kOut) {
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) {
-        const int col = c + i;
-        if (col >= o.n) break;  // warp-uniform
-        int row = o.row0 + col;
-        if constexpr (EPI == kOut) row = t.tab.row_of[row];
-        const int64_t at = (int64_t)row * h.rows + f;
-        if constexpr (EPI == kGated) {
-            // this warp's 32 features are one 1x32 block (rows is a multiple of 32)
-            uint32_t code = 127u;  // blocks past the matrix: scale 1
-            if (f < h.rows) {
-                const float x = __fmul_rn(gate_act(v[0][i], p.gate), v[SUBS - 1][i]);
-                const uint32_t mag = isnan(x) ? 0u : __float_as_uint(fabsf(x));
-                const float s = pow2_scale<0>(__uint_as_float(__reduce_max_sync(0xffffffffu, mag)));
-                p.hq[at] = (uint8_t)fp8x2<0>(__fmul_rn(x, __frcp_rn(s)), 0.0f);
-                code = __float_as_uint(s) >> 23;
-            }
-            if (lane == 0)
-                p.hsf[((int64_t)o.g * h.mt + o.mt) * 512 + 16 * (col & 31) + 4 * (col >> 5) + q] =
-                    (uint8_t)code;
-        } else if (f < h.rows) {
-            if constexpr (EPI == kRows) {
+        for (int i = 0; i < kCols; ++i) {
+            const int col = c + i;
+            if (col >= c_hi) break;  // warp-uniform
+            const int64_t at = (int64_t)(o.row0 + col) * h.rows + f;
+            if constexpr (EPI == kGated) {
+                // this warp's 32 features are one 1x32 block (rows is a multiple of 32)
+                uint32_t code = 127u;  // blocks past the matrix: scale 1
+                if (f < h.rows) {
+                    const float x = __fmul_rn(gate_act(v[0][i], p.gate), v[SUBS - 1][i]);
+                    const uint32_t mag = isnan(x) ? 0u : __float_as_uint(fabsf(x));
+                    const float s = pow2_scale<0>(__uint_as_float(__reduce_max_sync(0xffffffffu, mag)));
+                    p.hq[at] = (uint8_t)fp8x2<0>(__fmul_rn(x, __frcp_rn(s)), 0.0f);
+                    code = __float_as_uint(s) >> 23;
+                }
+                if (lane == 0)
+                    p.hsf[((int64_t)o.g * h.mt + o.mt) * 512 + 16 * (col & 31) + 4 * (col >> 5) + q] =
+                        (uint8_t)code;
+            } else if (f < h.rows) {
                 __stcg(p.y + at, v[0][i]);
-            } else {
-                const float x = p.bias != nullptr ? __fadd_rn(v[0][i], __ldg(p.bias + f)) : v[0][i];
-                if (p.out_f32)
-                    static_cast<float *>(p.out)[at] = x;
-                else
-                    static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(x);
             }
+        }
+    } else {
+        int row[kCols];
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) row[i] = c + i < c_hi ? t.tab.row_of[o.row0 + c + i] : 0;
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) {
+            const int64_t at = (int64_t)row[i] * h.rows + f;
+            const float x = p.bias != nullptr ? __fadd_rn(v[0][i], bias) : v[0][i];
+            if (f >= h.rows || c + i >= c_hi) continue;
+            if (p.out_f32)
+                static_cast<float *>(p.out)[at] = x;
+            else
+                static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(x);
         }
     }
 }
@@ -1153,7 +1197,7 @@ __device__ __forceinline__ void combine(const StreamParams &p, Tail<LORA> &t, co
 template <bool LORA, int EPI>
 __device__ __forceinline__ void finish_tile(const StreamParams &p, Tail<LORA> &t, const Tile &o, int acc,
                                             uint32_t tmem) {
-    const StreamPhase &h = p.ph[o.ph];
+    const StreamPhase &h = p.ph[EPI == kRows ? 1 : 0];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int q = warp & 3, half = (warp - kSEpiWarp0) >> 2;
     const int row_l = q * 32 + lane;  // weight row within a tile
@@ -1177,7 +1221,9 @@ __device__ __forceinline__ void finish_tile(const StreamParams &p, Tail<LORA> &t
         for (int i = 0; i < kCols; ++i)
             d[i] = p.chains == 2 ? __uint_as_float(r[i]) + __uint_as_float(x[i]) : __uint_as_float(r[i]);
     };
-    const int parts = t.parts[o.ph];
+    const int parts = t.parts[EPI == kRows ? 1 : 0];
+    const int f = (my_sub ? o.w1 : o.w0) + row_l;
+    const float bias = EPI == kOut && p.bias != nullptr && f < h.rows ? __ldg(p.bias + f) : 0.0f;
     const int64_t part_size = (int64_t)2 * p.nb * 128;
     float *part0 = h.part + (int64_t)o.tile * parts * part_size;  // the tile's parts
     bool last = true;
@@ -1234,7 +1280,7 @@ __device__ __forceinline__ void finish_tile(const StreamParams &p, Tail<LORA> &t
                     }
                 }
             }
-            store_cols<LORA, EPI, kSubs>(p, h, t, o, c, (my_sub ? o.w1 : o.w0) + row_l, q, lane, v);
+            store_cols<LORA, EPI, kSubs>(p, h, t, o, c, o.n, f, q, lane, bias, v);
         }
     if (parts == 1) {
         ptx::tc_fence_before();
@@ -1341,12 +1387,7 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const __grid_constant__ 
                 (void)epi_all(true);
                 const int item = t.item;
                 if (item >= t.tab.items) break;
-                if (p.x_bf16 && p.T <= 8)
-                    (void)low_rank<true, true>(p, t.tab, t.pick, item);
-                else if (p.x_bf16)
-                    (void)low_rank<true, false>(p, t.tab, t.pick, item);
-                else
-                    (void)low_rank<false, false>(p, t.tab, t.pick, item);
+                low_rank(p, t.tab, t.pick, item);
                 fence_proxy_async_all();
                 (void)epi_all(true);
                 if (threadIdx.x == kSEpiWarp0 * 32) (void)atom_add_acq_rel(p.counters + 2, 1);
@@ -1415,13 +1456,14 @@ cudaError_t launch_one(const StreamParams &p, int grid, cudaStream_t s) {
 
 }  // namespace
 
-void stream_sizes(StreamParams &p, int nb, int sub, bool lora, int v_halves) {
+void stream_sizes(StreamParams &p, int nb, int sub, bool lora, int v_halves, bool one) {
     p.nb = nb;
     // Tensor memory beside the scales (up to eight stages' 128 columns): two
     // accumulators, so that a tile's epilogue overlaps the next tile, then two
     // chains each
     const int room_cols = 512 - 8 * kSfSlot;
     p.nacc = 2 * sub * nb <= room_cols ? 2 : 1;
+    if (lora && one && p.nacc * sub * 2 * nb > room_cols && sub * 2 * nb <= room_cols) p.nacc = 1;
     p.chains = p.nacc * sub * 2 * nb <= room_cols ? 2 : 1;
     p.acc_cols = sub * p.chains * nb;
     p.w_bytes = sub * kWTile;
@@ -1436,6 +1478,10 @@ void stream_sizes(StreamParams &p, int nb, int sub, bool lora, int v_halves) {
     const int cols = (512 - p.nacc * p.acc_cols) / kSfSlot;
     if (p.stages > cols) p.stages = cols;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
+}
+
+bool stream_one_ticket(int64_t tiles, int ks, int num_sms) {
+    return tiles <= num_sms && tiles * parts_of((int)tiles, ks, num_sms) <= num_sms;
 }
 
 size_t stream_part_bytes(const StreamParams &p, int num_sms) {

@@ -67,7 +67,7 @@ struct StreamParams {
     uint8_t *hq, *hsf;     // h: codes [T k][F] and packed scales
     float *y;              // [T k][H]
     // adapters
-    CUtensorMap B, V;
+    CUtensorMap B, V, V1;  // V: boxes of 16 rows of all halves, of one
     const void *a;         // bf16 [L][rank][K]
     const float *alpha;    // [L] or null
     const float *bias;     // [N] or null
@@ -79,7 +79,9 @@ struct StreamParams {
 // Token columns for groups of up to n rows.
 inline int stream_columns(int64_t n) { return n <= 64 ? (int)((n + 15) / 16 * 16) : kStreamMaxTokens; }
 // Ring and accumulator sizes for nb token columns, sub weight tiles a stage.
-void stream_sizes(StreamParams &p, int nb, int sub, bool lora, int v_halves);
+void stream_sizes(StreamParams &p, int nb, int sub, bool lora, int v_halves, bool one);
+// Whether no SM takes more than one ticket of a product of so many tiles.
+bool stream_one_ticket(int64_t tiles, int ks, int num_sms);
 // Bytes of a product's partial tiles; SMs of the device.
 size_t stream_part_bytes(const StreamParams &p, int num_sms);
 // Prepares the tokens, then runs the products: two launches.
