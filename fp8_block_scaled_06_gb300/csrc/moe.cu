@@ -27,11 +27,9 @@ using namespace fp8g;
 extern "C" {
 
 int64_t fp8g_packed_scale_bytes(int64_t matrices, int64_t rows, int64_t K) {
-    if (matrices < 1 || rows < 1 || K < 1 || matrices >= kMaxDim || rows >= kMaxDim || K >= kMaxDim)
-        return 0;
-    const int64_t per = ((rows + 127) / 128) * ((K + 127) / 128);
-    if (per > ((int64_t)1 << 50) / matrices) return 0;
-    return matrices * per * 512;
+    if (matrices < 1 || rows < 1 || K < 1 || K % 32 != 0) return 0;
+    if (matrices > 65535 || rows > 65535 * 128 || K >= kMaxDim) return 0;
+    return matrices * ((rows + 127) / 128) * ((K + 127) / 128) * 512;
 }
 
 fp8g_status fp8g_pack_scales(const float *sf, int64_t matrices, int64_t rows, int64_t K,
@@ -61,7 +59,7 @@ fp8g_status fp8g_moe_route(const void *logits, int32_t in_dtype, int64_t ld, int
     if (E > FP8G_MAX_ROUTED_EXPERTS || k > FP8G_MAX_TOP_K || T > FP8G_MAX_ROUTED_TOKENS)
         return FP8G_ERR_UNSUPPORTED_SHAPE;
     const bool ordered = counts != nullptr;
-    if ((rows != nullptr) != ordered || (slots != nullptr) != ordered) return FP8G_ERR_INVALID_ARG;
+    if (T > 0 && ((rows != nullptr) != ordered || (slots != nullptr) != ordered)) return FP8G_ERR_INVALID_ARG;
     if (T > 0 && (logits == nullptr || ids == nullptr || weights == nullptr)) return FP8G_ERR_INVALID_ARG;
     if (!is_aligned(logits, in_dtype == FP8G_IN_BF16 ? 2 : 4) || !is_aligned(ids, 4) ||
         !is_aligned(weights, 4) || !is_aligned(counts, 4) || !is_aligned(rows, 4) || !is_aligned(slots, 4))

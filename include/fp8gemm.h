@@ -490,8 +490,8 @@ FP8G_API fp8g_status fp8_grouped_gemm_quant(const void *X, int32_t x_dtype, int6
  * is the 8-bit exponent code (value 2^(code - 127)) of row 128 t + 32 w + d, K
  * block 4 g + j; rows and blocks past the matrix hold 127.  K % 32 == 0 and at
  * most 65535 matrices and row tiles, else FP8G_ERR_UNSUPPORTED_SHAPE; sf and
- * packed 16-byte aligned.  fp8g_packed_scale_bytes gives the size (0 for sizes
- * out of range).
+ * packed 16-byte aligned.  fp8g_packed_scale_bytes gives the size (0 for what
+ * fp8g_pack_scales refuses).
  */
 FP8G_API int64_t fp8g_packed_scale_bytes(int64_t matrices, int64_t rows, int64_t K);
 FP8G_API fp8g_status fp8g_pack_scales(const float *sf, int64_t matrices, int64_t rows, int64_t K,
@@ -560,7 +560,7 @@ typedef enum { FP8G_GATE_SILU = 0, FP8G_GATE_GELU = 1, FP8G_GATE_RELU = 2 } fp8g
  * FP8G_MAX_ROUTED_EXPERTS, else FP8G_ERR_UNSUPPORTED_SHAPE; T may be 0.  The
  * weights of experts without tokens are not read.  For more tokens route with
  * fp8g_moe_route and use the grouped GEMMs.  Results do not vary between runs.
- * Four kernels and one temporary from the library's pool.
+ * Two kernels and one temporary from the library's pool.
  */
 FP8G_API fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t *ids,
                                    const float *weights, const void *W13, const uint8_t *sf13,
@@ -591,9 +591,11 @@ FP8G_API fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t
  * FP8G_MAX_LORA_RANK, else FP8G_ERR_UNSUPPORTED_SHAPE; L = 0: no adapters
  * (lora_a, lora_b, adapter unused, may be null); M may be 0.  x, W (packed
  * formats 32), sfw, lora_a, lora_b, C 16-byte aligned, N * sizeof(out element)
- * % 16 == 0, else FP8G_ERR_ALIGNMENT.  Results do not vary between runs.  Two or three
- * kernels and one temporary from the library's pool of about M K + 4 M
- * min(L, 256) max(r, 64) bytes.
+ * % 16 == 0, else FP8G_ERR_ALIGNMENT.  Results do not vary between runs.
+ * lora_b is finite: an infinity or NaN in an adapter's B can reach rows of other
+ * adapters as NaN (in W, A, alpha and x they stay with their own column or rows).
+ * Two kernels up to 512 rows, three for more, and one temporary from the library's
+ * pool: M K bytes, 4 M min(L, 256) max(r, 64) for A x, up to 53 MB of partial sums.
  */
 FP8G_API fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void *W, const uint8_t *sfw,
                                    int32_t w_fmt, const void *lora_a, const void *lora_b,
