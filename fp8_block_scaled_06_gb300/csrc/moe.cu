@@ -76,7 +76,9 @@ fp8g_status fp8g_moe_route(const void *logits, int32_t in_dtype, int64_t ld, int
     if (ordered && route_blocks(T) > 1) {
         cudaMemPool_t pool;
         if ((st = host_pool(d.dev, pool)) != FP8G_OK) return st;
-        if (cudaMallocFromPoolAsync(&hist, (size_t)route_blocks(T) * E * 4, pool, stream) != cudaSuccess)
+        // counts of every block of tokens, then ranks of the pairs
+        const size_t bytes = (size_t)route_blocks(T) * E * 4 + (size_t)T * k;
+        if (cudaMallocFromPoolAsync(&hist, bytes, pool, stream) != cudaSuccess)
             return FP8G_ERR_CUDA;
     }
     const cudaError_t e = launch_moe_route(logits, in_dtype == FP8G_IN_BF16, ld, (int32_t)T, E, k, score,

@@ -7,18 +7,7 @@
 //               sigmoid | sigmoid / sum of the chosen sigmoids
 //   order     = the pairs (t, j) by expert, then by t k + j
 //
-// A warp takes a token, its logits in registers as order-preserving integers
-// (lane i: experts i, i + 32, ...).  Each of the k rounds is two warp
-// reductions (redux: the largest key, then the lowest expert that has it), so
-// a token costs about 2 k reductions and one pass over its logits: the kernel
-// reads every logit once and is bound by latency, not by memory (32768 x 64
-// fp32 logits are 8 MB).
-//
-// Order: a stable counting sort.  A block counts its tokens' choices per
-// expert; the second kernel (none when one block holds every token) adds the
-// counts of the blocks before it, ranks each pair among its warp's and its
-// block's, and stores it.  No atomic decides a position, so the order is the
-// same in every run.
+// HEADER
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -42,7 +31,9 @@ struct RouteArgs {
     int32_t *ids;
     float *weights;
     int32_t *counts, *rows, *slots;  // all null: no order wanted
-    int32_t *hist;                   // [blocks][E]
+    int32_t *hist;                   // [blocks][E]: pairs of a block's tokens
+    uint8_t *rank;                   // [T k]: of a pair among its block's of its expert
+    int32_t vec;                     // four logits of a row at a time
 };
 
 // Order-preserving key of a logit, 0 where it cannot be chosen.
@@ -141,132 +132,182 @@ __device__ __forceinline__ int route_token(const RouteArgs &a, int t, int lane) 
 __device__ __forceinline__ uint64_t umax64(uint64_t a, uint64_t b) { return a > b ? a : b; }
 __device__ __forceinline__ uint64_t umin64(uint64_t a, uint64_t b) { return a > b ? b : a; }
 
-// Four lanes take a token: lane q the experts q, q + 4, ...  Each keeps its
-// K best as a descending list of (key, ~expert) words, a new one passing down
-// the list by compare-exchange; two rounds of bitonic merges over the lanes
-// give all four the token's list.  Returns it in `best`; t < 0: no token (the
-// lane takes part in the shuffles only).
+// Larger first.
+__device__ __forceinline__ void order2(uint64_t &a, uint64_t &b) {
+    const uint64_t hi = umax64(a, b);
+    b = umin64(a, b);
+    a = hi;
+}
+// Batcher's odd-even merge sort, largest first (K = 4, 8, 16: 5, 19, 63 pairs).
+template <int K>
+__device__ __forceinline__ void sort_desc(uint64_t (&v)[K]) {
+#pragma unroll
+    for (int p = 1; p < K; p <<= 1)
+#pragma unroll
+        for (int k = p; k >= 1; k >>= 1)
+#pragma unroll
+            for (int i = 0; i < K; ++i)
+                if (i >= k % p && (i - k % p) / k % 2 == 0 && i + k < K && i / (2 * p) == (i + k) / (2 * p))
+                    order2(v[i], v[i + k]);
+}
+// The K largest of two such lists: the larger halves' maxima are bitonic.
+template <int K>
+__device__ __forceinline__ void merge_desc(uint64_t (&v)[K], const uint64_t (&o)[K]) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) v[j] = umax64(v[j], o[K - 1 - j]);
+#pragma unroll
+    for (int h = K / 2; h > 0; h >>= 1)
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+            if ((j & h) == 0) order2(v[j], v[j + h]);
+}
+
+// Four lanes take a token: lane q a quarter of the experts, as (key, ~expert)
+// words, K at a time: sorted, merged into its K best, and those over the lanes
+// in two rounds.  All four end with the token's list `best`; lane q scores and
+// stores choices q, q + 4, ...  t < 0: no token (the lane takes part in the
+// shuffles only).
 template <int NE, int K, bool BF16>
 __device__ __forceinline__ void route_quad(const RouteArgs &a, int t, int q, uint64_t (&best)[K]) {
     uint32_t key[NE];
+    const int64_t row = (int64_t)max(t, 0) * a.ld;
+    const int live = t < 0 ? 0 : a.E;
+    if (a.vec) {  // experts 16 c + 4 q and the next three
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        const int e = q + 4 * i;
-        key[i] = 0u;
-        if (t >= 0 && e < a.E) {
-            const int64_t off = (int64_t)t * a.ld + e;
-            if constexpr (BF16)
-                key[i] = route_key(__bfloat162float(static_cast<const __nv_bfloat16 *>(a.logits)[off]));
-            else
-                key[i] = route_key(static_cast<const float *>(a.logits)[off]);
+        for (int c = 0; c < NE / 4; ++c) {
+            const int e = 16 * c + 4 * q;
+            float l[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+            if (e < live) {
+                if constexpr (BF16) {
+                    const uint2 r = __ldg(reinterpret_cast<const uint2 *>(
+                        static_cast<const __nv_bfloat16 *>(a.logits) + row + e));
+                    l[0] = __uint_as_float(r.x << 16);
+                    l[1] = __uint_as_float(r.x & 0xFFFF0000u);
+                    l[2] = __uint_as_float(r.y << 16);
+                    l[3] = __uint_as_float(r.y & 0xFFFF0000u);
+                } else {
+                    const float4 r =
+                        __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(a.logits) + row + e));
+                    l[0] = r.x;
+                    l[1] = r.y;
+                    l[2] = r.z;
+                    l[3] = r.w;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) key[4 * c + i] = route_key(l[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+            const int e = 16 * (i / 4) + 4 * q + i % 4;
+            float l = neg_inf();
+            if (e < live) {
+                if constexpr (BF16)
+                    l = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.logits)[row + e]);
+                else
+                    l = static_cast<const float *>(a.logits)[row + e];
+            }
+            key[i] = route_key(l);
         }
     }
 #pragma unroll
-    for (int j = 0; j < K; ++j) best[j] = 0;
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        uint64_t w = key[i] == 0u ? 0 : (uint64_t)key[i] << 32 | (uint32_t)~(q + 4 * i);
+    for (int c = 0; c < (NE + K - 1) / K; ++c) {
+        uint64_t v[K];
 #pragma unroll
         for (int j = 0; j < K; ++j) {
-            const uint64_t lo = umin64(best[j], w);
-            best[j] = umax64(best[j], w);
-            w = lo;
+            const int i = c * K + j;
+            v[j] = i < NE && key[i < NE ? i : 0] != 0u
+                       ? (uint64_t)key[i < NE ? i : 0] << 32 | (uint32_t)~(16 * (i / 4) + 4 * q + i % 4)
+                       : 0;
+        }
+        sort_desc<K>(v);
+        if (c == 0) {
+#pragma unroll
+            for (int j = 0; j < K; ++j) best[j] = v[j];
+        } else {
+            merge_desc<K>(best, v);
         }
     }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
-        uint64_t c[K];
+        uint64_t v[K];
 #pragma unroll
-        for (int j = 0; j < K; ++j)
-            c[j] = umax64(best[j], __shfl_xor_sync(0xffffffffu, best[K - 1 - j], o));
-#pragma unroll
-        for (int h = K / 2; h > 0; h >>= 1)
-#pragma unroll
-            for (int j = 0; j < K; ++j)
-                if ((j & h) == 0) {
-                    const uint64_t hi = umax64(c[j], c[j + h]);
-                    c[j + h] = umin64(c[j], c[j + h]);
-                    c[j] = hi;
-                }
-#pragma unroll
-        for (int j = 0; j < K; ++j) best[j] = c[j];
+        for (int j = 0; j < K; ++j) v[j] = __shfl_xor_sync(0xffffffffu, best[j], o);
+        merge_desc<K>(best, v);
     }
-    // the scores, in the order of the choices (the same on all four lanes)
     const float top = key_value((uint32_t)(best[0] >> 32));
     float sum = 0.0f;
     if (a.score == FP8G_SCORE_SOFTMAX) {
 #pragma unroll
         for (int i = 0; i < NE; ++i)
             if (key[i] != 0u) sum += rel_exp(key_value(key[i]), top);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
     }
-    float w[K];
+    float w[K / 4];
+    uint64_t mine[K / 4];
 #pragma unroll
-    for (int j = 0; j < K; ++j) {
-        const uint32_t kj = (uint32_t)(best[j] >> 32);
+    for (int j = 0; j < K / 4; ++j) {
+        const uint64_t lo = q & 1 ? best[4 * j + 1] : best[4 * j], hi = q & 1 ? best[4 * j + 3] : best[4 * j + 2];
+        mine[j] = 4 * j + q < a.k ? (q & 2 ? hi : lo) : 0;
+        const uint32_t kj = (uint32_t)(mine[j] >> 32);
         w[j] = 0.0f;
-        if (j < a.k && kj != 0u)
+        if (kj != 0u)
             w[j] = a.score <= FP8G_SCORE_SOFTMAX_TOPK ? rel_exp(key_value(kj), top)
                                                       : 1.0f / (1.0f + expf(-key_value(kj)));
         if (a.score == FP8G_SCORE_SOFTMAX_TOPK || a.score == FP8G_SCORE_SIGMOID_NORM) sum += w[j];
     }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
     if (t < 0) return;
 #pragma unroll
-    for (int j = 0; j < K; ++j)
-        if ((j & 3) == q && j < a.k) {
-            const bool on = (best[j] >> 32) != 0;
+    for (int j = 0; j < K / 4; ++j)
+        if (4 * j + q < a.k) {
+            const bool on = (mine[j] >> 32) != 0;
             const float v = a.score == FP8G_SCORE_SIGMOID ? w[j] : __fdiv_rn(w[j], sum);
-            a.ids[(int64_t)t * a.k + j] = on ? (int)~(uint32_t)best[j] : -1;
-            a.weights[(int64_t)t * a.k + j] = on ? v * a.scale : 0.0f;
+            a.ids[(int64_t)t * a.k + 4 * j + q] = on ? (int)~(uint32_t)mine[j] : -1;
+            a.weights[(int64_t)t * a.k + 4 * j + q] = on ? v * a.scale : 0.0f;
         }
 }
 
-// The pairs [i0, i0 + n) of the ids, ranked among themselves by expert, to
-// their places: base[e] is the first place of this block's pairs of expert e.
-// wh [kWarps][E] counts per warp.  Call with all threads.
-__device__ __forceinline__ void place_pairs(const RouteArgs &a, const int32_t *ids, int64_t i0, int n,
-                                            const int32_t *base, int32_t *wh, int64_t total) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = blockDim.x >> 5;
-    const int per = ((n + nwarps - 1) / nwarps + 31) & ~31;  // pairs per warp, whole steps
-    for (int i = threadIdx.x; i < nwarps * a.E; i += blockDim.x) wh[i] = 0;
-    __syncthreads();
-    const int lo = warp * per, hi = min(n, lo + per);
-    for (int i = lo + lane; i < hi; i += 32) {
-        const int e = ids[i0 + i];
-        if (e >= 0) atomicAdd(&wh[warp * a.E + e], 1);
+// Shared memory of a block that wants the order.
+struct Order {
+    int32_t *cnt, *base, *total;
+    uint32_t *mask;   // [warps][E / 4]: a byte an expert: which of the warp's (8) tokens chose it
+    uint16_t *start;  // [warps][E]: pairs of the expert in earlier warps
+    int words;        // of a warp's masks
+    __device__ __forceinline__ Order(int32_t *sm, int E) {
+        cnt = sm;
+        base = sm + E;
+        total = sm + 2 * E;
+        words = (E + 3) / 4;
+        mask = reinterpret_cast<uint32_t *>(sm + 2 * E + 1);
+        start = reinterpret_cast<uint16_t *>(mask + kWarps * words);
     }
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-        int run = base[e];
-        for (int w = 0; w < nwarps; ++w) {
-            const int c = wh[w * a.E + e];
-            wh[w * a.E + e] = run;
-            run += c;
-        }
+    __device__ __forceinline__ void note(int warp, int i, int e) {  // the warp's token i chose e
+        atomicOr(mask + warp * words + (e >> 2), 1u << (8 * (e & 3) + i));
     }
-    __syncthreads();
-    for (int i = lo; i < hi; i += 32) {
-        const int f = i + lane;
-        const int e = f < hi ? ids[i0 + f] : -1;
-        const uint32_t same = __match_any_sync(0xffffffffu, e);
-        if (e >= 0) {
-            const int at = wh[warp * a.E + e] + __popc(same & ((1u << lane) - 1u));
-            const int64_t pair = i0 + f;
-            a.rows[at] = (int32_t)(pair / a.k);
-            a.slots[at] = (int32_t)pair;
-        }
-        __syncwarp();
-        if (e >= 0 && lane == 31 - __clz(same)) wh[warp * a.E + e] += __popc(same);
-        __syncwarp();
+    // Rank of that pair among the block's of its expert, after starts().
+    __device__ __forceinline__ int rank(int warp, int i, int e, int E) const {
+        const uint32_t m = mask[warp * words + (e >> 2)] >> (8 * (e & 3));
+        return start[warp * E + e] + __popc(m & ((1u << i) - 1u));
     }
-    // places past the last pair
-    for (int i = threadIdx.x; i < n; i += blockDim.x)
-        if (i0 + i >= total) {
-            a.rows[i0 + i] = -1;
-            a.slots[i0 + i] = -1;
+    // Starts and counts of the block, by all threads, after every note.
+    __device__ __forceinline__ void starts(int E) {
+        __syncthreads();
+        const int warps = (int)blockDim.x >> 5;
+        for (int e = threadIdx.x; e < E; e += blockDim.x) {
+            int run = 0;
+#pragma unroll 8
+            for (int w = 0; w < warps; ++w) {
+                start[w * E + e] = (uint16_t)run;
+                run += __popc(mask[w * words + (e >> 2)] >> (8 * (e & 3)) & 255u);
+            }
+            cnt[e] = run;
         }
-}
+        __syncthreads();
+    }
+};
+size_t order_smem(int E) { return (size_t)(2 * E + 1 + kWarps * ((E + 3) / 4)) * 4 + (size_t)kWarps * E * 2; }
 
 // Exclusive prefix over experts of cnt (in place to base), by warp 0; the sum
 // goes to *total.  Call with all threads.
@@ -292,80 +333,125 @@ __device__ __forceinline__ void expert_prefix(const int32_t *cnt, int32_t *base,
     __syncthreads();
 }
 
-// K 0: a warp takes a token, NV = ceil(E / 32); else four lanes take one, NV =
-// ceil(E / 4), K at least a.k.
+// K 0: a warp takes a token at a time, up to eight in a row, NV = ceil(E / 32);
+// else four lanes take one, NV = ceil(E / 4), K at least a.k.
 template <int NV, int K, bool BF16>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a) {
-    extern __shared__ int32_t sm[];  // cnt [E], base [E], total, warp counts [kWarps][E]
-    int32_t *cnt = sm, *base = sm + a.E, *total = sm + 2 * a.E, *wh = sm + 2 * a.E + 1;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    extern __shared__ int32_t sm[];
+    Order o(sm, a.E);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = (int)blockDim.x >> 5;
     const bool ordered = a.rows != nullptr;
-    if (ordered)
-        for (int e = threadIdx.x; e < a.E; e += blockDim.x) cnt[e] = 0;
-    __syncthreads();
+    if (ordered) {
+        for (int i = threadIdx.x; i < warps * o.words; i += blockDim.x) o.mask[i] = 0u;
+        __syncthreads();
+    }
     ptx::grid_dep_wait();  // launched programmatically: global memory from here on
-    const int t0 = blockIdx.x * kTokensPerBlock, t1 = min(a.T, t0 + kTokensPerBlock);
+    const int t0 = blockIdx.x * kTokensPerBlock, n = min(a.T - t0, kTokensPerBlock);
+    const int per = K == 0 ? (n + warps - 1) / warps : 8;  // tokens of a warp
+    // this lane's choices: (expert, token of the warp), and the pair's number
+    constexpr int kMine = K == 0 ? 8 : K / 4;
+    int mine[kMine];
+    const int q = threadIdx.x & 3, quad = lane >> 2;
     if constexpr (K == 0) {
-        for (int t = t0 + warp; t < t1; t += blockDim.x >> 5) {
-            const int e = route_token<NV, BF16>(a, t, lane);
-            if (ordered && e >= 0) atomicAdd(&cnt[e], 1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            mine[i] = -1;
+            if (i < per && warp * per + i < n) mine[i] = route_token<NV, BF16>(a, t0 + warp * per + i, lane);
         }
     } else {
-        const int t = t0 + (int)(threadIdx.x >> 2), q = threadIdx.x & 3;
+        const int i = (int)(threadIdx.x >> 2);
         uint64_t best[K];
-        route_quad<NV, K, BF16>(a, t < t1 ? t : -1, q, best);
-        if (ordered && t < t1) {
+        route_quad<NV, K, BF16>(a, i < n ? t0 + i : -1, q, best);
 #pragma unroll
-            for (int j = 0; j < K; ++j)
-                if ((j & 3) == q && j < a.k && (best[j] >> 32) != 0) atomicAdd(&cnt[~(uint32_t)best[j]], 1);
+        for (int j = 0; j < K / 4; ++j) {
+            const uint64_t lo = q & 1 ? best[4 * j + 1] : best[4 * j], hi = q & 1 ? best[4 * j + 3] : best[4 * j + 2];
+            const uint64_t b = q & 2 ? hi : lo;
+            mine[j] = i < n && 4 * j + q < a.k && (b >> 32) != 0 ? (int)~(uint32_t)b : -1;
         }
     }
     if (!ordered) {
         ptx::grid_dep_launch();
         return;
     }
-    if (gridDim.x > 1) {
-        __syncthreads();
-        for (int e = threadIdx.x; e < a.E; e += blockDim.x)
-            a.hist[(int64_t)blockIdx.x * a.E + e] = cnt[e];
-        ptx::grid_dep_launch();
-        return;
+#pragma unroll
+    for (int j = 0; j < kMine; ++j)
+        if (mine[j] >= 0) o.note(warp, K == 0 ? j : quad, mine[j]);
+    o.starts(a.E);
+    const bool alone = gridDim.x == 1;
+    if (alone) {
+        expert_prefix(o.cnt, o.base, a.E, o.total);
+        for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.counts[e] = o.cnt[e];
+    } else {
+        for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.hist[(int64_t)blockIdx.x * a.E + e] = o.cnt[e];
     }
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+        if (mine[j] < 0) continue;
+        const int i = K == 0 ? j : quad;
+        const int token = t0 + warp * per + i, pair = token * a.k + (K == 0 ? lane : 4 * j + q);
+        const int r = o.rank(warp, i, mine[j], a.E);
+        if (alone) {
+            a.rows[o.base[mine[j]] + r] = token;
+            a.slots[o.base[mine[j]] + r] = pair;
+        } else {
+            a.rank[pair] = (uint8_t)r;
+        }
+    }
+    if (alone)  // places past the last pair
+        for (int i = *o.total + (int)threadIdx.x; i < n * a.k; i += blockDim.x) a.rows[i] = a.slots[i] = -1;
     ptx::grid_dep_launch();
-    expert_prefix(cnt, base, a.E, total);
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.counts[e] = cnt[e];
-    place_pairs(a, a.ids, 0, a.T * a.k, base, wh, *total);
 }
 
 // More than one block of tokens: the places, from every block's counts.
 __global__ void __launch_bounds__(kWarps * 32) route_order_kernel(RouteArgs a, int blocks) {
     extern __shared__ int32_t sm[];
-    int32_t *cnt = sm, *base = sm + a.E, *total = sm + 2 * a.E, *wh = sm + 2 * a.E + 1;
-    int32_t *before = wh + kWarps * a.E;  // pairs of expert e in earlier blocks
+    int32_t *cnt = sm, *base = sm + a.E, *total = sm + 2 * a.E;
+    int32_t *before = total + 1;  // pairs of expert e in earlier blocks
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) cnt[e] = before[e] = 0;
     __syncthreads();
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
+    const int t0 = blockIdx.x * kTokensPerBlock, n = min(a.T - t0, kTokensPerBlock) * a.k, i0 = t0 * a.k;
+    // this thread's first pairs, on the way while the counts are added
+    constexpr int kFirst = 2;
+    int e[kFirst], r[kFirst];
+#pragma unroll
+    for (int j = 0; j < kFirst; ++j) {
+        const int i = (int)threadIdx.x + j * (int)blockDim.x;
+        e[j] = i < n ? __ldcg(a.ids + i0 + i) : -1;
+        r[j] = i < n ? __ldcg(a.rank + i0 + i) : 0;
+    }
     // whole sums: the order of the additions does not matter
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int e = lane; e < a.E; e += 32) {
+    for (int x = lane; x < a.E; x += 32) {
         int s = 0, p = 0;
+#pragma unroll 4
         for (int b = warp; b < blocks; b += kWarps) {
-            const int c = __ldcg(a.hist + (int64_t)b * a.E + e);
+            const int c = __ldcg(a.hist + (int64_t)b * a.E + x);
             s += c;
             if (b < (int)blockIdx.x) p += c;
         }
-        atomicAdd(&cnt[e], s);
-        atomicAdd(&before[e], p);
+        atomicAdd(&cnt[x], s);
+        atomicAdd(&before[x], p);
     }
     expert_prefix(cnt, base, a.E, total);
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-        if (blockIdx.x == 0) a.counts[e] = cnt[e];
-        base[e] += before[e];
+    for (int x = threadIdx.x; x < a.E; x += blockDim.x) {
+        if (blockIdx.x == 0) a.counts[x] = cnt[x];
+        base[x] += before[x];
     }
     __syncthreads();
-    const int t0 = blockIdx.x * kTokensPerBlock, t1 = min(a.T, t0 + kTokensPerBlock);
-    place_pairs(a, a.ids, (int64_t)t0 * a.k, (t1 - t0) * a.k, base, wh, *total);
+    auto place = [&](int i, int x, int rank) {
+        if (x < 0) return;
+        a.rows[base[x] + rank] = (i0 + i) / a.k;
+        a.slots[base[x] + rank] = i0 + i;
+    };
+#pragma unroll
+    for (int j = 0; j < kFirst; ++j) place((int)threadIdx.x + j * (int)blockDim.x, e[j], r[j]);
+    for (int i = (int)threadIdx.x + kFirst * (int)blockDim.x; i < n; i += (int)blockDim.x)
+        place(i, __ldcg(a.ids + i0 + i), __ldcg(a.rank + i0 + i));
+    // places past the last pair
+    for (int i = (int)threadIdx.x; i < n; i += (int)blockDim.x)
+        if (i0 + i >= *total) a.rows[i0 + i] = a.slots[i0 + i] = -1;
 }
 
 template <int NV, int K>
@@ -383,18 +469,24 @@ cudaError_t launch_moe_route(const void *logits, int bf16, int64_t ld, int32_t T
                              int32_t score, float scale, int32_t *ids, float *weights,
                              int32_t *counts, int32_t *rows, int32_t *slots, int32_t *hist,
                              cudaStream_t s) {
-    const RouteArgs a{logits, ld, T, E, k, score, scale, ids, weights, counts, rows, slots, hist};
     const int blocks = route_blocks(T);
-    const size_t smem = (size_t)(2 * E + 1 + kWarps * E) * 4;  // E <= 256: 34 KB
+    const uintptr_t unit = bf16 ? 8 : 16;  // bytes of four logits
+    const int vec = E % 4 == 0 && ld % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % unit == 0;
+    uint8_t *rank = reinterpret_cast<uint8_t *>(hist + (int64_t)blocks * E);
+    const RouteArgs a{logits, ld, T, E, k, score, scale, ids, weights, counts, rows, slots, hist, rank, vec};
+    const size_t smem = rows == nullptr ? 0 : order_smem(E);  // E <= 256: 27 KB
     cudaError_t e;
     if (T > kQuadTokens && E <= 64) {
         const int threads = (int)((T < kTokensPerBlock ? T : kTokensPerBlock) * 4 + 31) / 32 * 32;
+        const bool b16 = bf16 != 0;
         if (E <= 32)
-            e = k <= 8 ? launch_nv<8, 8>(a, bf16 != 0, blocks, threads, smem, s)
-                       : launch_nv<8, 16>(a, bf16 != 0, blocks, threads, smem, s);
+            e = k <= 4   ? launch_nv<8, 4>(a, b16, blocks, threads, smem, s)
+                : k <= 8 ? launch_nv<8, 8>(a, b16, blocks, threads, smem, s)
+                         : launch_nv<8, 16>(a, b16, blocks, threads, smem, s);
         else
-            e = k <= 8 ? launch_nv<16, 8>(a, bf16 != 0, blocks, threads, smem, s)
-                       : launch_nv<16, 16>(a, bf16 != 0, blocks, threads, smem, s);
+            e = k <= 4   ? launch_nv<16, 4>(a, b16, blocks, threads, smem, s)
+                : k <= 8 ? launch_nv<16, 8>(a, b16, blocks, threads, smem, s)
+                         : launch_nv<16, 16>(a, b16, blocks, threads, smem, s);
     } else {
         const int threads = 32 * (T < kWarps ? T : kWarps);
         if (E <= 32)
@@ -408,7 +500,7 @@ cudaError_t launch_moe_route(const void *logits, int bf16, int64_t ld, int32_t T
     }
     if (e != cudaSuccess || rows == nullptr || blocks == 1) return e;
     return launch_programmatic_smem(route_order_kernel, dim3(blocks), dim3(kWarps * 32),
-                                    smem + (size_t)E * 4, s, a, blocks);
+                                    (size_t)(3 * E + 1) * 4, s, a, blocks);
 }
 
 }  // namespace fp8g
