@@ -539,39 +539,57 @@ def pack_scales(sf, stream=None):
     return out
 
 
+# The three below are called once a layer for a few tokens, where the host's time
+# is what a call costs: torch's names are looked up once, dtypes compared by
+# identity and the library's function called at once (on the GB300 host gemm_lora
+# takes 18.5 us of which the C call 8 to 12, 20.9 before).  A tensor that is not packed is
+# copied on the current stream, so with another `stream` it is refused; the
+# output is the current stream's memory.
+
+_t = None  # torch, its dtypes
+
+
+def _names():
+    global _t
+    import torch
+    _t = (torch.empty, torch.bfloat16, torch.float32, torch.int32)
+    return _t
+
+
+def _packed(x, stream):
+    assert stream is None, "with a stream of its own a call takes packed tensors"
+    return x.contiguous()
+
+
 def moe_route(logits, k: int, score: int = FP8G_SCORE_SOFTMAX_TOPK, scale: float = 1.0,
               ordered: bool = False, stream=None):
     """fp32 or bf16 logits [T, E] -> (ids int32 [T, k], weights fp32 [T, k]), and
     with `ordered` also (counts [E], rows [T k], slots [T k]), the row order of the
     grouped GEMM (its counts, rows and c_row_of)."""
-    import torch
-    bf16 = logits.dtype == torch.bfloat16
-    assert logits.is_cuda and (bf16 or logits.dtype == torch.float32)
+    empty, bf16, f32, i32 = _t or _names()
+    dt, dev = logits.dtype, logits.device
+    assert logits.is_cuda and (dt is f32 or dt is bf16)
     T, E = logits.shape
     ld, step = logits.stride()
-    if E > 1 and step != 1 or T > 1 and ld < E:
-        logits = logits.contiguous()
+    if T <= 1:
         ld = E
-    elif T <= 1:
-        ld = E
-    dev, i32 = logits.device, torch.int32
-    ids = torch.empty((T, k), dtype=i32, device=dev)
-    w = torch.empty((T, k), dtype=torch.float32, device=dev)
-    # (the library function at once: a small call is mostly the host's time)
+    if E > 1 and step != 1 or ld < E:
+        logits, ld = _packed(logits, stream), E
+    ids = empty((T, k), dtype=i32, device=dev)
+    w = empty((T, k), dtype=f32, device=dev)
     if not ordered:
-        st = (_lib or load()).fp8g_moe_route(logits.data_ptr(), FP8G_IN_BF16 if bf16 else FP8G_IN_F32,
-                                             ld, T, E, k, score, scale, ids.data_ptr(),
-                                             w.data_ptr(), None, None, None, _stream(stream))
+        st = (_lib or load()).fp8g_moe_route(
+            logits.data_ptr(), FP8G_IN_BF16 if dt is bf16 else FP8G_IN_F32, ld, T, E, k, score, scale,
+            ids.data_ptr(), w.data_ptr(), None, None, None, _stream(stream))
         if st:
             raise Fp8gError(st, "fp8g_moe_route")
         return ids, w
-    counts = torch.empty(E, dtype=i32, device=dev)
-    rows = torch.empty(T * k, dtype=i32, device=dev)
-    slots = torch.empty(T * k, dtype=i32, device=dev)
-    st = (_lib or load()).fp8g_moe_route(logits.data_ptr(), FP8G_IN_BF16 if bf16 else FP8G_IN_F32, ld,
-                                         T, E, k, score, scale, ids.data_ptr(), w.data_ptr(),
-                                         counts.data_ptr(), rows.data_ptr(), slots.data_ptr(),
-                                         _stream(stream))
+    counts = empty(E, dtype=i32, device=dev)
+    rows = empty(T * k, dtype=i32, device=dev)
+    slots = empty(T * k, dtype=i32, device=dev)
+    st = (_lib or load()).fp8g_moe_route(
+        logits.data_ptr(), FP8G_IN_BF16 if dt is bf16 else FP8G_IN_F32, ld, T, E, k, score, scale,
+        ids.data_ptr(), w.data_ptr(), counts.data_ptr(), rows.data_ptr(), slots.data_ptr(), _stream(stream))
     if st:
         raise Fp8gError(st, "fp8g_moe_route")
     return ids, w, counts, rows, slots
@@ -583,23 +601,28 @@ def moe_layer(x, ids, weights, W13, sf13, W2, sf2, w_fmt: int = FP8G_E4M3,
     weights [T, k] from moe_route, W13 [E, 2F, H] and W2 [E, H, F] codes of w_fmt,
     sf13 / sf2 from pack_scales (sf13 of W13's scales viewed as [2E, F, H/32]).
     Allocates the output [T, H]."""
-    import torch
-    bf16 = x.dtype == torch.bfloat16
-    assert x.is_cuda and (bf16 or x.dtype == torch.float32)
-    assert ids.dtype == torch.int32 and weights.dtype == torch.float32
+    empty, bf16, f32, i32 = _t or _names()
+    dt = x.dtype
+    assert x.is_cuda and (dt is bf16 or dt is f32)
+    assert ids.dtype is i32 and weights.dtype is f32
     T, H = x.shape
-    k = ids.shape[1]
-    E, F = W13.shape[0], W13.shape[1] // 2
-    assert ids.shape == (T, k) == weights.shape
-    assert W13.shape == (E, 2 * F, packed_cols(H, w_fmt)) and W13.is_contiguous()
-    assert W2.shape == (E, H, packed_cols(F, w_fmt)) and W2.is_contiguous()
+    t, k = ids.shape
+    E, F2, c13 = W13.shape
+    F = F2 // 2
+    assert t == T and weights.shape == ids.shape and c13 == packed_cols(H, w_fmt)
+    assert W2.shape == (E, H, packed_cols(F, w_fmt)) and W13.is_contiguous() and W2.is_contiguous()
     assert sf13.numel() == _packed_bytes(2 * E, F, H) and sf2.numel() == _packed_bytes(E, H, F)
-    x, ids, weights = x.contiguous(), ids.contiguous(), weights.contiguous()
-    o = torch.empty((T, H), dtype=torch.bfloat16 if out == "bf16" else torch.float32,
-                    device=x.device)
-    fp8_moe_layer(x, FP8G_IN_BF16 if bf16 else FP8G_IN_F32, ids, weights, W13, sf13, W2, sf2, o,
-                  FP8G_OUT_BF16 if out == "bf16" else FP8G_OUT_F32, w_fmt, gate, T, k, E, H, F,
-                  stream)
+    assert sf13.is_contiguous() and sf2.is_contiguous()
+    if not (x.is_contiguous() and ids.is_contiguous() and weights.is_contiguous()):
+        x, ids, weights = _packed(x, stream), _packed(ids, stream), _packed(weights, stream)
+    wide = out != "bf16"
+    o = empty((T, H), dtype=f32 if wide else bf16, device=x.device)
+    st = (_lib or load()).fp8_moe_layer(
+        x.data_ptr(), FP8G_IN_BF16 if dt is bf16 else FP8G_IN_F32, ids.data_ptr(), weights.data_ptr(),
+        W13.data_ptr(), sf13.data_ptr(), W2.data_ptr(), sf2.data_ptr(), o.data_ptr(),
+        FP8G_OUT_F32 if wide else FP8G_OUT_BF16, w_fmt, gate, T, k, E, H, F, _stream(stream))
+    if st:
+        raise Fp8gError(st, "fp8_moe_layer")
     return o
 
 
@@ -607,23 +630,30 @@ def gemm_lora(x, W, sfw, lora_a, lora_b, alpha, adapter, bias=None, w_fmt: int =
               out: str = "bf16", stream=None):
     """Projection with low-rank adapters: x fp32 or bf16 [M, K], W codes [N, K] of
     w_fmt, sfw from pack_scales, lora_a bf16 [L, r, K], lora_b bf16 [L, N, r],
-    alpha fp32 [L] or None, adapter int32 [M] (negative: none).  Allocates C [M, N]."""
-    import torch
-    bf16 = x.dtype == torch.bfloat16
-    assert x.is_cuda and (bf16 or x.dtype == torch.float32)
-    assert lora_a.dtype == torch.bfloat16 and lora_b.dtype == torch.bfloat16
+    alpha fp32 [L] or None, adapter int32 [M] (negative: none), bias fp32 [N] or
+    None.  Allocates C [M, N]."""
+    empty, bf16, f32, i32 = _t or _names()
+    dt = x.dtype
+    assert x.is_cuda and (dt is bf16 or dt is f32)
+    assert lora_a.dtype is bf16 and lora_b.dtype is bf16 and adapter.dtype is i32
     M, K = x.shape
-    N = W.shape[0]
-    L, r, _ = lora_a.shape
-    assert W.shape == (N, packed_cols(K, w_fmt)) and W.is_contiguous()
-    assert adapter.dtype == torch.int32 and adapter.shape == (M,)
-    assert lora_a.shape == (L, r, K) and lora_b.shape == (L, N, r)
-    assert sfw.numel() == _packed_bytes(1, N, K)
-    x, adapter = x.contiguous(), adapter.contiguous()
-    lora_a, lora_b = lora_a.contiguous(), lora_b.contiguous()
-    C = torch.empty((M, N), dtype=torch.bfloat16 if out == "bf16" else torch.float32,
-                    device=x.device)
-    fp8_gemm_lora(x, FP8G_IN_BF16 if bf16 else FP8G_IN_F32, W, sfw, w_fmt, lora_a, lora_b, alpha,
-                  adapter, L, r, bias, C, FP8G_OUT_BF16 if out == "bf16" else FP8G_OUT_F32, M, N, K,
-                  stream)
+    N, cols = W.shape
+    L, r, ka = lora_a.shape
+    assert cols == packed_cols(K, w_fmt) and ka == K and lora_b.shape == (L, N, r)
+    assert adapter.numel() == M and sfw.numel() == _packed_bytes(1, N, K)
+    assert alpha is None or alpha.dtype is f32 and alpha.numel() == L and alpha.is_contiguous()
+    assert bias is None or bias.dtype is f32 and bias.numel() == N and bias.is_contiguous()
+    assert W.is_contiguous() and sfw.is_contiguous()
+    if not (x.is_contiguous() and adapter.is_contiguous() and lora_a.is_contiguous() and lora_b.is_contiguous()):
+        x, adapter = _packed(x, stream), _packed(adapter, stream)
+        lora_a, lora_b = _packed(lora_a, stream), _packed(lora_b, stream)
+    wide = out != "bf16"
+    C = empty((M, N), dtype=f32 if wide else bf16, device=x.device)
+    st = (_lib or load()).fp8_gemm_lora(
+        x.data_ptr(), FP8G_IN_BF16 if dt is bf16 else FP8G_IN_F32, W.data_ptr(), sfw.data_ptr(), w_fmt,
+        lora_a.data_ptr(), lora_b.data_ptr(), None if alpha is None else alpha.data_ptr(),
+        adapter.data_ptr(), L, r, None if bias is None else bias.data_ptr(), C.data_ptr(),
+        FP8G_OUT_F32 if wide else FP8G_OUT_BF16, M, N, K, _stream(stream))
+    if st:
+        raise Fp8gError(st, "fp8_gemm_lora")
     return C

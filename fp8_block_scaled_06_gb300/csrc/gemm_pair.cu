@@ -190,10 +190,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ LoraArg<LORA> la) {
     using PC = PairCfg<MODE, F4>;
     static_assert(!LORA || (MODE == kModeBlock && F4 == 0), "low-rank steps: block-scaled FP8-rate");
-    // Low-rank steps of a tile, after its num_kb FP8 steps: halves * kr per
-    // slot; of a 64-wide step's two halves of V (halves 2) the hi one first
-    auto lora_steps = [&](const int32_t pm) -> int {
-        if constexpr (LORA) return la.p.halves * la.p.kr * __ldcg(la.p.slots + pm);
+    // Low-rank steps of a tile, after its num_kb FP8 steps, in loops of their own:
+    // halves * kr per slot; of a 64-wide step's two halves of V (halves 2) the hi
+    // one first.  Each role asks for a tile's number of slots a tile ahead (asked
+    // for at the tile, and with the two kinds of step in one loop, a tile took 2 us
+    // more even without slots).
+    auto lora_slots = [&](const int32_t t) -> int {
+        if constexpr (LORA) {
+            if (t < p.npm * p.npn) {
+                int pm, pn;
+                raster(t, p.npm, p.npn, kRasterG, pm, pn);
+                return __ldcg(la.p.slots + pm);
+            }
+        }
         return 0;
     };
     extern __shared__ uint8_t smem_raw[];
@@ -290,7 +299,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                    : PC::TX - kA / 8 * (uint32_t)p.a_gap8 - kB / 8 * (uint32_t)p.b_gap8;
             const int32_t num_kg = PC::G * p.num_kb;  // K groups of the packed scales
             uint32_t stage = 0, phase = 0;
+            int slots_next = lora_slots(t_first);
             for (int32_t t = t_first; t < T; t += t_step) {
+                const int slots = slots_next;
+                slots_next = lora_slots(t + t_step);
                 const PairTile ti = pair_tile<MODE>(t, p, row_off, tile_off, rt_off);
                 const int32_t row0 = ti.row0 + (int32_t)rank * kBM;
                 const int32_t nb0 = ti.pn * kPairBN + (int32_t)rank * (kPairBN / 2);
@@ -299,28 +311,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         *reinterpret_cast<int4 *>(p.tile_map_out + 4 * (int64_t)t) =
                             make_int4(ti.e, ti.pm, ti.pn, 0);
                 }
-                const int n_steps = p.num_kb + lora_steps(ti.pm);
-                for (int kb = 0; kb < n_steps; ++kb) {
+                int adapter_next = 0;
+                if constexpr (LORA) {
+                    if (slots > 0) adapter_next = __ldcg(la.p.adapters + ti.pm * la.p.cap);
+                }
+                for (int kb = 0; kb < p.num_kb; ++kb) {
                     if (!wait_bar(bar_empty(stage), phase ^ 1u, abort_flag, p, 0 * 256 + stage))
                         goto roles_done;
                     const uint32_t fb = leader ? bar_full(stage) : ptx::map_shared(bar_full(stage), 0);
-                    if constexpr (LORA) {
-                        if (kb >= p.num_kb) {
-                            const int hv = la.p.halves, ls = kb - p.num_kb, sl = ls / (hv * la.p.kr);
-                            const int c = (ls / hv - sl * la.p.kr) * 64;
-                            const int slot = ti.pm * la.p.cap + sl;
-                            if (leader) ptx::mbar_arrive_expect_tx(fb, 2 * (kA + kB));
-                            ptx::tma_load_2d_pair(sbase + PC::OFF_A + stage * kA, &la.p.V, fb, c,
-                                                  (hv * slot + ls % hv) * 256 + (int32_t)rank * kBM);
-                            ptx::tma_load_3d_pair(sbase + PC::OFF_B + stage * kB, &la.p.B, fb, c, nb0,
-                                                  __ldcg(la.p.adapters + slot));
-                            if (++stage == PC::STAGES) {
-                                stage = 0;
-                                phase ^= 1u;
-                            }
-                            continue;
-                        }
-                    }
                     if (leader) ptx::mbar_arrive_expect_tx(fb, 2 * tx_bytes);
                     // first K element of the stage: a 128-byte row holds 128 one-byte
                     // elements, or 32 fp32 ones (TF32)
@@ -362,6 +360,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                         phase ^= 1u;
                     }
                 }
+                if constexpr (LORA) {
+                    for (int sl = 0; sl < slots; ++sl) {
+                        const int slot = ti.pm * la.p.cap + sl, adapter = adapter_next;
+                        if (sl + 1 < slots) adapter_next = __ldcg(la.p.adapters + slot + 1);
+                        for (int c = 0; c < la.p.kr * 64; c += 64)
+                            for (int h = 0; h < la.p.halves; ++h) {
+                                if (!wait_bar(bar_empty(stage), phase ^ 1u, abort_flag, p, 0 * 256 + stage))
+                                    goto roles_done;
+                                const uint32_t fb =
+                                    leader ? bar_full(stage) : ptx::map_shared(bar_full(stage), 0);
+                                if (leader) ptx::mbar_arrive_expect_tx(fb, 2 * (kA + kB));
+                                ptx::tma_load_2d_pair(sbase + PC::OFF_A + stage * kA, &la.p.V, fb, c,
+                                                      (la.p.halves * slot + h) * 256 + (int32_t)rank * kBM);
+                                ptx::tma_load_3d_pair(sbase + PC::OFF_B + stage * kB, &la.p.B, fb, c, nb0,
+                                                      adapter);
+                                if (++stage == PC::STAGES) {
+                                    stage = 0;
+                                    phase ^= 1u;
+                                }
+                            }
+                    }
+                }
             }
         }
     } else if (run && warp == 1 && leader) {
@@ -371,7 +391,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             int32_t lt = 0;
             const uint32_t idesc = F4 == 3 ? ptx::idesc_tf32(2 * kBM, kPairBN)
                                            : ptx::idesc_f8(2 * kBM, kPairBN) | p.ab_fmt;
+            int slots_next = lora_slots(t_first);
             for (int32_t t = t_first; t < T; t += t_step, ++lt) {
+                const int slots = slots_next;
+                slots_next = lora_slots(t + t_step);
                 const int acc = lt % PC::NUM_ACC;
                 const uint32_t acc_par = (uint32_t)((lt / PC::NUM_ACC) & 1);
                 const uint32_t d_tmem = tmem_base + acc * kPairBN;
@@ -379,9 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       1 * 256 + 64))
                     goto roles_done;
                 ptx::tc_fence_after();
-                const int n_steps =
-                    p.num_kb + (LORA ? lora_steps(pair_tile<MODE>(t, p, row_off, tile_off, rt_off).pm) : 0);
-                for (int kb = 0; kb < n_steps; ++kb) {
+                for (int kb = 0; kb < p.num_kb; ++kb) {
                     // block modes: data and scale factors in place (the
                     // scale-copy thread waited for "full" and committed its copies)
                     const uint32_t rb = PC::kBlock ? bar_sfr(stage) : bar_full(stage);
@@ -389,19 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tc_fence_after();
                     const uint32_t a0 = sbase + PC::OFF_A + stage * kA;
                     const uint32_t b0 = sbase + PC::OFF_B + stage * kB;
-                    if (LORA && kb >= p.num_kb) {
-                        if constexpr (LORA) {
-                            const int hv = la.p.halves, c = (kb - p.num_kb) / hv % la.p.kr * 64;
-                            const int nk = (min(64, la.p.rank - c) + 15) / 16;
-                            // both halves in a row: the lo one 64 bytes on, against the same rows
-                            for (int h = hv; h < 3; ++h)
-                                for (int k = 0; k < nk; ++k)
-                                    ptx::mma_bf16_pair(d_tmem,
-                                                       ptx::desc_kmajor_sw128(a0 + (h - hv) * 64 + k * 32),
-                                                       ptx::desc_kmajor_sw128(b0 + k * 32),
-                                                       ptx::idesc_bf16(2 * kBM, kPairBN), 1u);
-                        }
-                    } else if constexpr (F4 == 2) {
+                    if constexpr (F4 == 2) {
                         // MMA k: K elements 64k .. 64k + 63 = K group k's four
                         // 16-wide scale blocks (the whole word, sf_id 0)
                         const uint32_t sf = tmem_base + 256 + stage * PC::SF_COLS;
@@ -453,6 +462,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                         phase ^= 1u;
                     }
                 }
+                if constexpr (LORA) {
+                    for (int sl = 0; sl < slots; ++sl)
+                        for (int c = 0; c < la.p.kr * 64; c += 64)
+                            for (int h = 0; h < la.p.halves; ++h) {
+                                if (!wait_bar(bar_sfr(stage), phase, abort_flag, p, 1 * 256 + stage))
+                                    goto roles_done;
+                                ptx::tc_fence_after();
+                                const uint32_t a0 = sbase + PC::OFF_A + stage * kA;
+                                const uint32_t b0 = sbase + PC::OFF_B + stage * kB;
+                                const int nk = (min(64, la.p.rank - c) + 15) / 16;
+                                // both halves in a row (halves 1): the lo one 64 bytes
+                                // on, against the same rows
+                                for (int o = 0; o < 3 - la.p.halves; ++o)
+                                    for (int k = 0; k < nk; ++k)
+                                        ptx::mma_bf16_pair(d_tmem,
+                                                           ptx::desc_kmajor_sw128(a0 + o * 64 + k * 32),
+                                                           ptx::desc_kmajor_sw128(b0 + k * 32),
+                                                           ptx::idesc_bf16(2 * kBM, kPairBN), 1u);
+                                ptx::tc_commit_pair_mc(bar_empty(stage), 0x3);
+                                if (++stage == PC::STAGES) {
+                                    stage = 0;
+                                    phase ^= 1u;
+                                }
+                            }
+                }
                 ptx::tc_commit_pair_mc(bar_accf(acc), 0x3);
             }
         }
@@ -465,21 +499,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int h = warp - 2;
         if (lane == 0) {
             uint32_t stage = 0, phase = 0;
+            int slots_next = lora_slots(t_first);
             for (int32_t t = t_first; t < T; t += t_step) {
-                const int n_steps =
-                    p.num_kb + (LORA ? lora_steps(pair_tile<MODE>(t, p, row_off, tile_off, rt_off).pm) : 0);
-                for (int kb = 0; kb < n_steps; ++kb) {
+                const int slots = slots_next;
+                slots_next = lora_slots(t + t_step);
+                for (int kb = 0; kb < p.num_kb; ++kb) {
                     if (!wait_bar(bar_full(stage), phase, abort_flag, p, 2 * 256 + stage))
                         goto roles_done;
                     ptx::tc_fence_after();
-                    if (LORA && kb >= p.num_kb) {  // no scales: pass the stage on
-                        ptx::tc_commit_pair_mc(bar_sfr(stage), 0x1);
-                        if (++stage == PC::STAGES) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
-                        continue;
-                    }
                     const uint32_t sf = tmem_base + 256 + stage * PC::SF_COLS;
                     const uint32_t cs = sbase + PC::OFF_SF + stage * PC::CHUNK;
                     constexpr int G = PC::G;
@@ -504,6 +531,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (++stage == PC::STAGES) {
                         stage = 0;
                         phase ^= 1u;
+                    }
+                }
+                if constexpr (LORA) {  // no scales: pass the stages on
+                    for (int ls = slots * la.p.kr * la.p.halves; ls > 0; --ls) {
+                        if (!wait_bar(bar_full(stage), phase, abort_flag, p, 2 * 256 + stage)) goto roles_done;
+                        ptx::tc_fence_after();
+                        ptx::tc_commit_pair_mc(bar_sfr(stage), 0x1);
+                        if (++stage == PC::STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
                 }
             }

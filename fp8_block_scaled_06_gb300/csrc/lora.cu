@@ -2,8 +2,8 @@
 //
 //   C[i] = out( Q(x_i) W^T + bias + alpha_l B_l (A_l x_i) ),  l = adapter[i]
 //
-// Few rows: the streaming kernels (stream.cu).  Many: the rows
-// quantised, V = alpha A x, then the CTA-pair product (gemm_pair.cu).  In both V
+// Few rows: the streaming kernels (stream.cu).  Many: the rows quantised and
+// V = alpha A x, then the CTA-pair product (gemm_pair.cu).  In both V
 // is taken against the adapters' B rows as further K steps into the product's
 // fp32 accumulator, so the sum is rounded once.
 //
@@ -13,6 +13,8 @@
 // other adapters, as two bf16 halves (V = hi + lo to 16 bits): the product
 // then needs no gather, and an adapter costs rank / 128 of a K step's weights.
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "internal.h"
 #include "kernel_common.cuh"
@@ -38,10 +40,10 @@ struct LoraPrep {
     const float *alpha;       // [L] or null
     const int32_t *adapter;   // [M]
     int32_t L, r, r64, wide;  // LoraV: V's row length, halves in rows of their own
-    int32_t tile, cap, tiles;
+    int32_t tile, cap, tiles;  // tiles 0: no adapters
     __nv_bfloat16 *v;         // [tiles][cap][halves][tile][r64]
     int32_t *slot_cnt, *slot_adapter;  // the pair kernel's tables
-    int32_t items;            // blocks per tile and rank block of the low-rank part
+    int32_t items;            // blocks per tile and rank block of V
     unsigned int *status;
 };
 
@@ -50,7 +52,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<uint32_t *>(&b);
 }
 
-__device__ __forceinline__ float bf16_round(float v) { return __bfloat162float(__float2bfloat16_rn(v)); }
+// What rounding to bf16 leaves of v (of an infinity, or a v rounded to one: nothing).
+__device__ __forceinline__ float bf16_rest(float v) {
+    const float h = __bfloat162float(__float2bfloat16_rn(v));
+    return isinf(h) ? 0.0f : v - h;
+}
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -60,30 +66,27 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// 8 consecutive values of x as bf16 pairs; HALF 0: x rounded to bf16, 1: what
-// that leaves, rounded (fp32 x: 16 significant bits in two halves).
-template <bool BF16, int HALF>
-__device__ __forceinline__ uint4 x_pairs(const void *x, int64_t off, bool in) {
-    if (!in) return make_uint4(0u, 0u, 0u, 0u);
+// 8 consecutive values of x as bf16 pairs; of fp32 x the rounded values (hi) and
+// what they leave, rounded (lo): 16 significant bits in two halves.
+template <bool BF16>
+__device__ __forceinline__ void x_pairs(const void *x, int64_t off, uint4 &hi, uint4 &lo) {
     if constexpr (BF16) {
-        return __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(x) + off));
+        hi = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(x) + off));
     } else {
         float4 a, b;
         load8<false>(x, off, a, b);
-        float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        if constexpr (HALF == 1) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] -= bf16_round(v[i]);
-        }
-        return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                          pack_bf16(v[6], v[7]));
+        hi = make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
+        lo = make_uint4(pack_bf16(bf16_rest(a.x), bf16_rest(a.y)), pack_bf16(bf16_rest(a.z), bf16_rest(a.w)),
+                        pack_bf16(bf16_rest(b.x), bf16_rest(b.y)), pack_bf16(bf16_rest(b.z), bf16_rest(b.w)));
     }
 }
 
-// Row blockIdx.x of x: codes, scale bytes.
+// Row blockIdx.x of x: codes, scale bytes.  Behind lora_v_kernel, it starts beside
+// it (that one began only when all before it was complete, and nothing of it is
+// read here) and ends after it, so that the product can rely on both.
 template <bool BF16>
 __global__ void __launch_bounds__(256) lora_quant_kernel(const __grid_constant__ LoraPrep p) {
-    ptx::grid_dep_wait();
+    if (p.tiles == 0) ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     const int tid = threadIdx.x, nt = blockDim.x, blk = blockIdx.x;
     const int rt = blk / 128, in_t = blk - rt * 128;
@@ -103,16 +106,18 @@ __global__ void __launch_bounds__(256) lora_quant_kernel(const __grid_constant__
             p.xsf[((int64_t)(c >> 4) * p.n_rt + rt) * 512 + 16 * (in_t & 31) + 4 * (in_t >> 5) + ((c >> 2) & 3)] =
                 (uint8_t)(__float_as_uint(s) >> 23);
     }
+    if (p.tiles != 0) ptx::grid_dep_wait();
 }
 
-// V.  A block takes an item of a tile and 16 ranks: items are the pairs (slot,
-// 16 of the slot's rows) in order; blocks past the last one leave.  The K range goes over the block's warps (bound by the
-// latency of its loads: 16 warps with their loads of up to 128 K each in
-// flight), each a 16 x 16 product by mma.sync, joined in shared memory in warp
-// order.  A lane's 16-byte load covers 8 consecutive K of a row; the same K
-// permutation on both operands leaves the product unchanged.
+// V.  A block takes an item of a tile and 16 ranks: items are the pairs (slot, 16
+// of the slot's rows) in order; blocks past the last one leave.  The K range goes
+// over the block's 16 warps, each a 16 x 16 product by mma.sync (ranks x rows),
+// joined in shared memory in warp order.  A lane's 16-byte load covers 8
+// consecutive K of a row; the same K permutation on both operands leaves the
+// product unchanged.  Rows and ranks past the item's read others' values, into
+// products that are not stored.
 template <bool BF16>
-__global__ void __launch_bounds__(kLThreads) lora_v_kernel(const __grid_constant__ LoraPrep p) {
+__global__ void __launch_bounds__(kLThreads, 2) lora_v_kernel(const __grid_constant__ LoraPrep p) {
     __shared__ int32_t ad[kMaxTile];
     __shared__ int32_t cnt[FP8G_MAX_ADAPTERS];
     __shared__ int32_t pick[3];  // adapter, slot, first of its rows
@@ -122,7 +127,6 @@ __global__ void __launch_bounds__(kLThreads) lora_v_kernel(const __grid_constant
     const int blk = blockIdx.x;
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    // ------------------------------------------------------- low-rank part
     const int rblocks = (p.r + 15) / 16;
     int w = blk;
     const int item = w % p.items;
@@ -201,56 +205,50 @@ __global__ void __launch_bounds__(kLThreads) lora_v_kernel(const __grid_constant
         }
     // this lane's x rows (g, g + 8) and adapter rows (ranks g, g + 8 of the block)
     const int g = lane >> 2, c8 = 8 * (lane & 3);
-    const int i0 = rows[g], i1 = rows[g + 8];
-    const int64_t x0 = (int64_t)(row0 + max(i0, 0)) * p.K + c8, x1 = (int64_t)(row0 + max(i1, 0)) * p.K + c8;
-    const int r0 = rb * 16 + g, r1 = r0 + 8;
-    const __nv_bfloat16 *a0 = p.a + ((int64_t)l * p.r + min(r0, p.r - 1)) * p.K + c8;
-    const __nv_bfloat16 *a1 = p.a + ((int64_t)l * p.r + min(r1, p.r - 1)) * p.K + c8;
-    float d0[4] = {}, d1[4] = {};
-    const int steps = p.K / 32;  // K is a multiple of 32
-    constexpr int kU = 4;
-    for (int s0 = warp * kU; s0 < steps; s0 += kLWarps * kU) {
-        uint4 xa[kU], xb[kU], wa[kU], wb[kU];
+    const int i0 = rows[g] < 0 ? rows[0] : rows[g], i1 = rows[g + 8] < 0 ? rows[0] : rows[g + 8];
+    const int64_t x0 = (int64_t)(row0 + i0) * p.K + c8, x1 = (int64_t)(row0 + i1) * p.K + c8;
+    const int r0 = min(rb * 16 + g, p.r - 1), r1 = min(rb * 16 + g + 8, p.r - 1);
+    const __nv_bfloat16 *a0 = p.a + ((int64_t)l * p.r + r0) * p.K + c8;
+    const __nv_bfloat16 *a1 = p.a + ((int64_t)l * p.r + r1) * p.K + c8;
+    float d0[4] = {}, d1[4] = {};  // rows 0-7, 8-15
+    constexpr int kU = BF16 ? 2 : 1;
+    auto go = [&](auto count, int s0) {
+        constexpr int U = decltype(count)::value;
+        uint4 xa[U], xb[U], wa[U], wb[U], ya[U], yb[U];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const bool in = s0 + u < steps;
-            const int64_t k = in ? (int64_t)(s0 + u) * 32 : 0;
-            xa[u] = x_pairs<BF16, 0>(p.x, x0 + k, in && i0 >= 0);
-            xb[u] = x_pairs<BF16, 0>(p.x, x1 + k, in && i1 >= 0);
-            wa[u] = in && r0 < p.r ? __ldg(reinterpret_cast<const uint4 *>(a0 + k)) : z;
-            wb[u] = in && r1 < p.r ? __ldg(reinterpret_cast<const uint4 *>(a1 + k)) : z;
+        for (int u = 0; u < U; ++u) {
+            const int k = (s0 + u) * 32;
+            x_pairs<BF16>(p.x, x0 + k, xa[u], ya[u]);
+            x_pairs<BF16>(p.x, x1 + k, xb[u], yb[u]);
+            wa[u] = __ldg(reinterpret_cast<const uint4 *>(a0 + k));
+            wb[u] = __ldg(reinterpret_cast<const uint4 *>(a1 + k));
         }
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const uint32_t f0[4] = {xa[u].x, xb[u].x, xa[u].y, xb[u].y};
-            const uint32_t f1[4] = {xa[u].z, xb[u].z, xa[u].w, xb[u].w};
-            mma_16816(d0, f0, wa[u].x, wa[u].y);
-            mma_16816(d1, f0, wb[u].x, wb[u].y);
-            mma_16816(d0, f1, wa[u].z, wa[u].w);
-            mma_16816(d1, f1, wb[u].z, wb[u].w);
+        for (int u = 0; u < U; ++u) {
+            const uint32_t f0[4] = {wa[u].x, wb[u].x, wa[u].y, wb[u].y};
+            const uint32_t f1[4] = {wa[u].z, wb[u].z, wa[u].w, wb[u].w};
+            mma_16816(d0, f0, xa[u].x, xa[u].y);
+            mma_16816(d1, f0, xb[u].x, xb[u].y);
+            mma_16816(d0, f1, xa[u].z, xa[u].w);
+            mma_16816(d1, f1, xb[u].z, xb[u].w);
             if constexpr (!BF16) {
-                const bool in = s0 + u < steps;
-                const int64_t k = in ? (int64_t)(s0 + u) * 32 : 0;
-                const uint4 ya = x_pairs<false, 1>(p.x, x0 + k, in && i0 >= 0);
-                const uint4 yb = x_pairs<false, 1>(p.x, x1 + k, in && i1 >= 0);
-                const uint32_t h0[4] = {ya.x, yb.x, ya.y, yb.y}, h1[4] = {ya.z, yb.z, ya.w, yb.w};
-                mma_16816(d0, h0, wa[u].x, wa[u].y);
-                mma_16816(d1, h0, wb[u].x, wb[u].y);
-                mma_16816(d0, h1, wa[u].z, wa[u].w);
-                mma_16816(d1, h1, wb[u].z, wb[u].w);
+                mma_16816(d0, f0, ya[u].x, ya[u].y);
+                mma_16816(d1, f0, yb[u].x, yb[u].y);
+                mma_16816(d0, f1, ya[u].z, ya[u].w);
+                mma_16816(d1, f1, yb[u].z, yb[u].w);
             }
         }
-    }
-    {
-        const int c = 2 * (lane & 3);
-        acc[warp][g][c] = d0[0];
-        acc[warp][g][c + 1] = d0[1];
-        acc[warp][g + 8][c] = d0[2];
-        acc[warp][g + 8][c + 1] = d0[3];
-        acc[warp][g][8 + c] = d1[0];
-        acc[warp][g][8 + c + 1] = d1[1];
-        acc[warp][g + 8][8 + c] = d1[2];
-        acc[warp][g + 8][8 + c + 1] = d1[3];
+    };
+    const int steps = p.K / 32;  // K is a multiple of 32
+    int s0 = warp * kU;
+#pragma unroll 1
+    for (; s0 + kU <= steps; s0 += kLWarps * kU) go(std::integral_constant<int, kU>{}, s0);
+    if (kU > 1 && s0 < steps) go(std::integral_constant<int, 1>{}, s0);
+    const int c2 = 2 * (lane & 3);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        acc[warp][c2 + (e & 1)][g + 8 * (e >> 1)] = d0[e];
+        acc[warp][8 + c2 + (e & 1)][g + 8 * (e >> 1)] = d1[e];
     }
     __syncthreads();
     if (tid < 256) {
@@ -261,11 +259,8 @@ __global__ void __launch_bounds__(kLThreads) lora_v_kernel(const __grid_constant
         if (p.alpha != nullptr) v *= __ldg(p.alpha + l);
         if (row >= 0) {
             if (rb * 16 + c >= p.r) v = 0.0f;
-            const __nv_bfloat16 h = __float2bfloat16_rn(v);
-            // (an infinite or NaN V has no second half)
-            const float rest = v - __bfloat162float(h);
-            hi[(int64_t)row * p.r64 + c] = h;
-            hi[half + (int64_t)row * p.r64 + c] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
+            hi[(int64_t)row * p.r64 + c] = __float2bfloat16_rn(v);
+            hi[half + (int64_t)row * p.r64 + c] = __float2bfloat16_rn(bf16_rest(v));
         }
     }
 }
@@ -421,21 +416,22 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
         a.wide = lv.wide;
         a.tile = nb;
         a.cap = cap;
-        a.tiles = tiles;
+        a.tiles = lora ? tiles : 0;
         a.v = reinterpret_cast<__nv_bfloat16 *>(ws + o_v);
         a.slot_cnt = reinterpret_cast<int32_t *>(ws + o_part);
         a.slot_adapter = reinterpret_cast<int32_t *>(ws + o_cnt);
         a.items = nb / 16 + cap;  // at most one partly filled item per slot beside the whole ones
         a.status = d.status;
-        e = bf16 ? launch_programmatic(lora_quant_kernel<true>, dim3((unsigned)M), dim3(256), stream, a)
-                 : launch_programmatic(lora_quant_kernel<false>, dim3((unsigned)M), dim3(256), stream, a);
-        if (e == cudaSuccess && lora) {
+        if (lora) {
             const int64_t blocks = (int64_t)tiles * ((r + 15) / 16) * a.items;
             e = blocks >= INT32_MAX ? cudaErrorInvalidValue
                 : bf16 ? launch_programmatic(lora_v_kernel<true>, dim3((unsigned)blocks), dim3(kLThreads), stream, a)
                        : launch_programmatic(lora_v_kernel<false>, dim3((unsigned)blocks), dim3(kLThreads), stream,
                                              a);
         }
+        if (e == cudaSuccess)
+            e = bf16 ? launch_programmatic(lora_quant_kernel<true>, dim3((unsigned)M), dim3(256), stream, a)
+                     : launch_programmatic(lora_quant_kernel<false>, dim3((unsigned)M), dim3(256), stream, a);
         PairLora pl{};
         if (lora) {
             pl.V = mv;

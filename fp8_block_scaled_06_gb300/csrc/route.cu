@@ -7,7 +7,23 @@
 //               sigmoid | sigmoid / sum of the chosen sigmoids
 //   order     = the pairs (t, j) by expert, then by t k + j
 //
-// HEADER
+// Few tokens, or more than 64 experts: a warp takes a token, its logits in
+// registers as order-preserving integers (lane i: experts i, i + 32, ...).  Each
+// of the k rounds is two warp reductions (redux: the largest key, then the lowest
+// expert that has it).  Many tokens: four lanes take one (route_quad).  Either
+// way a logit is read once, and what bounds the kernel is not memory (32768 x 64
+// fp32 logits, 8 MB, are read in 1.3 us) but the comparisons: about 100 pairs of
+// 64-bit words a lane, 13.7 us for 32768 tokens of 64 experts, k = 8, softmax
+// and order included (inserting into a list of eight, 168 pairs: 18.4 us).  77
+// tokens: 7.1 us, one: 3.4 us, latency.
+//
+// Order: a stable counting sort.  A token chooses an expert at most once, so a
+// warp's choices of an expert are a mask over its eight tokens: a pair's rank
+// is the masks' set bits before it.  A block counts; the second kernel (none when
+// one block holds every token) adds the counts of the blocks before and stores
+// the pairs at base + rank (6.9 us for 262144 pairs; ranking them there by
+// matching in a warp, 10.0 us).  No atomic decides a position, so the order is
+// the same in every run.
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -19,7 +35,9 @@ namespace {
 
 constexpr int kWarps = 32;
 constexpr int kTokensPerBlock = 256;
-constexpr int kQuadTokens = 32;  // more tokens than this: four lanes a token
+// More tokens than this: four lanes a token.  A block has 32 warps, so up to 32
+// tokens a warp each is the shorter way (one token: 3.4 us against 4.1).
+constexpr int kQuadTokens = 32;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float((int)0xFF800000u); }
 
