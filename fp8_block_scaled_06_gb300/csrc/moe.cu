@@ -73,11 +73,11 @@ fp8g_status fp8g_moe_route(const void *logits, int32_t in_dtype, int64_t ld, int
         return FP8G_OK;
     }
     void *hist = nullptr;
-    if (ordered && route_blocks(T) > 1) {
+    if (ordered && route_blocks(T, true) > 1) {
         cudaMemPool_t pool;
         if ((st = host_pool(d.dev, pool)) != FP8G_OK) return st;
         // counts of every block of tokens, then ranks of the pairs
-        const size_t bytes = (size_t)route_blocks(T) * E * 4 + (size_t)T * k;
+        const size_t bytes = (size_t)route_blocks(T, true) * E * 4 + (size_t)T * k;
         if (cudaMallocFromPoolAsync(&hist, bytes, pool, stream) != cudaSuccess)
             return FP8G_ERR_CUDA;
     }

@@ -7,15 +7,14 @@
 //               sigmoid | sigmoid / sum of the chosen sigmoids
 //   order     = the pairs (t, j) by expert, then by t k + j
 //
-// Few tokens, or more than 64 experts: a warp takes a token, its logits in
-// registers as order-preserving integers (lane i: experts i, i + 32, ...).  Each
+// More than 64 experts: a warp takes a token, its logits in registers as order-preserving integers (lane i: experts i, i + 32, ...).  Each
 // of the k rounds is two warp reductions (redux: the largest key, then the lowest
 // expert that has it).  Many tokens: four lanes take one (route_quad).  Either
 // way a logit is read once, and what bounds the kernel is not memory (32768 x 64
 // fp32 logits, 8 MB, are read in 1.3 us) but the comparisons: about 100 pairs of
 // 64-bit words a lane, 13.7 us for 32768 tokens of 64 experts, k = 8, softmax
 // and order included (inserting into a list of eight, 168 pairs: 18.4 us).  77
-// tokens: 7.1 us, one: 3.4 us, latency.
+// tokens: 7.1 us, one: 2.5 us (in a graph), latency.
 //
 // Order: a stable counting sort.  A token chooses an expert at most once, so a
 // warp's choices of an expert are a mask over its eight tokens: a pair's rank
@@ -34,10 +33,8 @@ namespace fp8g {
 namespace {
 
 constexpr int kWarps = 32;
-constexpr int kTokensPerBlock = 256;
-// More tokens than this: four lanes a token.  A block has 32 warps, so up to 32
-// tokens a warp each is the shorter way (one token: 3.4 us against 4.1).
-constexpr int kQuadTokens = 32;
+constexpr int kBlockTokens = 256;  // tokens of a block at most
+constexpr int kFewTokens = 64;     // of a block where that leaves SMs idle
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float((int)0xFF800000u); }
 
@@ -52,6 +49,7 @@ struct RouteArgs {
     int32_t *hist;                   // [blocks][E]: pairs of a block's tokens
     uint8_t *rank;                   // [T k]: of a pair among its block's of its expert
     int32_t vec;                     // four logits of a row at a time
+    int32_t tokens;                  // of a block
 };
 
 // Order-preserving key of a logit, 0 where it cannot be chosen.
@@ -364,7 +362,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a) {
         __syncthreads();
     }
     ptx::grid_dep_wait();  // launched programmatically: global memory from here on
-    const int t0 = blockIdx.x * kTokensPerBlock, n = min(a.T - t0, kTokensPerBlock);
+    const int t0 = blockIdx.x * a.tokens, n = min(a.T - t0, a.tokens);
     const int per = K == 0 ? (n + warps - 1) / warps : 8;  // tokens of a warp
     // this lane's choices: (expert, token of the warp), and the pair's number
     constexpr int kMine = K == 0 ? 8 : K / 4;
@@ -429,7 +427,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_order_kernel(RouteArgs a, i
     __syncthreads();
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    const int t0 = blockIdx.x * kTokensPerBlock, n = min(a.T - t0, kTokensPerBlock) * a.k, i0 = t0 * a.k;
+    const int t0 = blockIdx.x * a.tokens, n = min(a.T - t0, a.tokens) * a.k, i0 = t0 * a.k;
     // this thread's first pairs, on the way while the counts are added
     constexpr int kFirst = 2;
     int e[kFirst], r[kFirst];
@@ -481,22 +479,38 @@ cudaError_t launch_nv(const RouteArgs &a, bool bf16, int blocks, int threads, si
 
 }  // namespace
 
-int route_blocks(int64_t T) { return (int)((T + kTokensPerBlock - 1) / kTokensPerBlock); }
+// Tokens of a block.  A block of 256 keeps one SM busy for 8 us (64 experts, k =
+// 8), one of 64 for 3; 64 where the blocks' counts, which every block of the order
+// adds up, stay few: 2048 tokens with the order 14.7 us with 256, 7.3 with 64,
+// 32768 tokens 15.5 and 23.9.  Up to 256 tokens one block makes the order by itself
+// (256: 11.8 us; a temporary and a second launch cost the host 6 us).
+static int route_tokens(int64_t T, bool ordered) {
+    if (ordered && (T <= kBlockTokens || T > 128 * kFewTokens)) return kBlockTokens;
+    return kFewTokens;
+}
+int route_blocks(int64_t T, bool ordered) {
+    const int n = route_tokens(T, ordered);
+    return (int)((T + n - 1) / n);
+}
 
 cudaError_t launch_moe_route(const void *logits, int bf16, int64_t ld, int32_t T, int32_t E, int32_t k,
                              int32_t score, float scale, int32_t *ids, float *weights,
                              int32_t *counts, int32_t *rows, int32_t *slots, int32_t *hist,
                              cudaStream_t s) {
-    const int blocks = route_blocks(T);
+    const int tokens = route_tokens(T, rows != nullptr), blocks = route_blocks(T, rows != nullptr);
     const uintptr_t unit = bf16 ? 8 : 16;  // bytes of four logits
     const int vec = E % 4 == 0 && ld % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % unit == 0;
     uint8_t *rank = reinterpret_cast<uint8_t *>(hist + (int64_t)blocks * E);
-    const RouteArgs a{logits, ld, T, E, k, score, scale, ids, weights, counts, rows, slots, hist, rank, vec};
+    const RouteArgs a{logits, ld, T, E, k, score, scale, ids, weights, counts, rows, slots, hist, rank, vec,
+                      tokens};
     const size_t smem = rows == nullptr ? 0 : order_smem(E);  // E <= 256: 27 KB
     cudaError_t e;
-    if (T > kQuadTokens && E <= 64) {
-        const int threads = (int)((T < kTokensPerBlock ? T : kTokensPerBlock) * 4 + 31) / 32 * 32;
-        const bool b16 = bf16 != 0;
+    const int most = T < tokens ? T : tokens;  // tokens of a block
+    const bool b16 = bf16 != 0;
+    // a warp a token against four lanes a token, 64 experts, k = 8: 2.5 us both for
+    // one token, 3.6 and 2.5 for 32, 20 and 8 for 256
+    if (E <= 64) {
+        const int threads = (most * 4 + 31) / 32 * 32;
         if (E <= 32)
             e = k <= 4   ? launch_nv<8, 4>(a, b16, blocks, threads, smem, s)
                 : k <= 8 ? launch_nv<8, 8>(a, b16, blocks, threads, smem, s)
@@ -506,15 +520,9 @@ cudaError_t launch_moe_route(const void *logits, int bf16, int64_t ld, int32_t T
                 : k <= 8 ? launch_nv<16, 8>(a, b16, blocks, threads, smem, s)
                          : launch_nv<16, 16>(a, b16, blocks, threads, smem, s);
     } else {
-        const int threads = 32 * (T < kWarps ? T : kWarps);
-        if (E <= 32)
-            e = launch_nv<1, 0>(a, bf16 != 0, blocks, threads, smem, s);
-        else if (E <= 64)
-            e = launch_nv<2, 0>(a, bf16 != 0, blocks, threads, smem, s);
-        else if (E <= 128)
-            e = launch_nv<4, 0>(a, bf16 != 0, blocks, threads, smem, s);
-        else
-            e = launch_nv<8, 0>(a, bf16 != 0, blocks, threads, smem, s);
+        const int threads = 32 * (most < kWarps ? most : kWarps);
+        e = E <= 128 ? launch_nv<4, 0>(a, b16, blocks, threads, smem, s)
+                     : launch_nv<8, 0>(a, b16, blocks, threads, smem, s);
     }
     if (e != cudaSuccess || rows == nullptr || blocks == 1) return e;
     return launch_programmatic_smem(route_order_kernel, dim3(blocks), dim3(kWarps * 32),

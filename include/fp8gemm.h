@@ -529,7 +529,7 @@ typedef enum {
  * t k + j (`c_row_of` of the grouped GEMMs over a C of T k rows); entries past
  * the sum of counts, which is T k unless some id is -1, are -1.  The order is
  * the same in every run.  One kernel; with the order and more than 256 tokens
- * two, and a temporary of 4 E ceil(T / 256) bytes from the library's pool.
+ * two, and a temporary of 4 E ceil(T / 64) + T k bytes from the library's pool.
  * k <= E, else FP8G_ERR_INVALID_ARG; E <= FP8G_MAX_ROUTED_EXPERTS, k <=
  * FP8G_MAX_TOP_K, T <= FP8G_MAX_ROUTED_TOKENS, else FP8G_ERR_UNSUPPORTED_SHAPE;
  * T may be 0.  Pointers aligned to their elements.
