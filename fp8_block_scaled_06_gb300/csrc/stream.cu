@@ -37,6 +37,7 @@
 // 0.08 us to issue a copy, and a step has six.
 #include <cuda_bf16.h>
 
+#include <cstddef>
 #include <type_traits>
 
 #include "kernel_common.cuh"
@@ -62,7 +63,6 @@ constexpr int kCols = 8;           // token columns at a time in an epilogue (fe
 constexpr int kPairs = 256;        // pairs (token, expert) of a table of the weighted sum
 constexpr int kTickets = 4;        // tickets in flight in a CTA
 constexpr int kSmemMax = 232448;
-constexpr int kAdWords = FP8G_MAX_ADAPTERS / 32;
 
 enum Epi : int { kGated, kRows, kOut };
 
@@ -85,14 +85,9 @@ struct LoraTables {
     // a group's rows are taken in the order of their slots (those without an
     // adapter last): a slot's are columns first[s] .. first[s + 1] - 1
     int16_t first[kStreamLoraGroups][kStreamMaxTokens + 1];
-    int16_t row_of[kStreamLoraRows], col_of[kStreamLoraRows];  // column -> row of the call, and back
+    int16_t row_of[kStreamLoraRows];  // column -> row of the call
     union {
-        struct {  // while the tables are made
-            uint32_t bits[kStreamLoraGroups][kAdWords];  // adapters of a group's rows
-            int16_t word0[kStreamLoraGroups][kAdWords];  // slots before a word's
-            int16_t slot_of[kStreamLoraRows];
-            uint8_t count[kStreamLoraRows / 32][kStreamMaxTokens + 1];  // a warp's rows of a slot
-        };
+        alignas(16) uint32_t key[kStreamLoraRows];  // while the tables are made: lora_key
         float acc[4][16][17];  // products to join (V)
     };
 };
@@ -158,134 +153,75 @@ __device__ __forceinline__ void make_tables(const StreamParams &p, MoeTables &t)
     __syncthreads();
 }
 
-// Warp 0, after the columns: windows and items.
-__device__ __forceinline__ void lora_windows(const StreamParams &p, LoraTables &t, int lane) {
-    int items = 0;
-    for (int g = 0; g < (p.T + p.nb - 1) / p.nb; ++g) {
-        int most = 0;
-        for (int s = lane; s < t.n[g]; s += 32) {
-            const int lo = t.first[g][s], hi = t.first[g][s + 1];
-            items += (hi - lo + 15) / 16;
-            most = max(most, ((hi + 15) & ~15) - (lo & ~15));
-        }
-        most = __reduce_max_sync(0xffffffffu, most);
-        if (lane == 0) t.windows[g] = p.halves == 2 && most > p.v_cols ? 2 : 1;
-    }
-    items = __reduce_add_sync(0xffffffffu, items);
-    if (lane == 0) t.items = items * ((p.rank + 15) / 16);
-    __syncwarp();
+// Rows in the order of their columns: by adapter (none: last), then by row.
+__device__ __forceinline__ uint32_t lora_key(const StreamParams &p, int i) {
+    const int l = p.rank > 0 ? __ldg(p.idx + i) : -1;
+    return (uint32_t)(l < 0 || l >= p.n_mat ? FP8G_MAX_ADAPTERS : l) * kStreamLoraRows + i;
 }
 
+// A row's column is the number of smaller keys in its group (128 at most: counted
+// by the row's thread; sorting in several steps with barriers took 3 us longer).
+// Then a warp a group: a slot starts where the adapter changes.
 __device__ __forceinline__ void make_tables(const StreamParams &p, LoraTables &t) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ng = (p.T + p.nb - 1) / p.nb;
-    if (p.T <= 32) {  // one warp, a row a lane
-        if (warp == 0) {
-            int l = lane < p.T && p.kr > 0 ? __ldg(p.idx + lane) : -1;
-            // rows without an adapter after the others, no rows after those
-            int key = l < 0 || l >= p.n_mat ? FP8G_MAX_ADAPTERS : l;
-            if (lane >= p.T) key = FP8G_MAX_ADAPTERS + 1;
-            const uint32_t same = __match_any_sync(0xffffffffu, key);
-            const bool first = lane == __ffs((int)same) - 1;
-            const uint32_t firsts = __ballot_sync(0xffffffffu, first);
-            int col = __popc(same & ((1u << lane) - 1u)), less = 0, slot = 0;
-            for (uint32_t m = firsts; m != 0; m &= m - 1) {
-                const int o = __ffs((int)m) - 1;
-                const int ko = __shfl_sync(0xffffffffu, key, o), c = __popc(__shfl_sync(0xffffffffu, same, o));
-                if (ko < key) {
-                    less += c;
-                    ++slot;
-                }
-            }
-            col += less;
-            const uint32_t slots = __ballot_sync(0xffffffffu, first && key < FP8G_MAX_ADAPTERS);
-            const uint32_t have = __ballot_sync(0xffffffffu, key < FP8G_MAX_ADAPTERS);
-            if (lane < p.T) {
-                t.col_of[lane] = (int16_t)col;
-                t.row_of[col] = (int16_t)lane;
-                if (first && key < FP8G_MAX_ADAPTERS) {
-                    t.adapter[0][slot] = (int16_t)l;
-                    t.first[0][slot] = (int16_t)less;
-                }
-            }
-            if (lane == 0) {
-                t.n[0] = __popc(slots);
-                t.first[0][__popc(slots)] = (int16_t)__popc(have);
-                t.n_groups = 1;
-            }
-            __syncwarp();
-            lora_windows(p, t, lane);
-        }
-        __syncthreads();
-        return;
-    }
-    for (int i = threadIdx.x; i < kStreamLoraGroups * kAdWords; i += (int)blockDim.x) t.bits[0][i] = 0;
-    __syncthreads();
-    if (p.kr > 0) {
-        for (int i = threadIdx.x; i < p.T; i += (int)blockDim.x) {
-            const int l = __ldg(p.idx + i);
-            if (l >= p.n_mat && blockIdx.x == 0) record_error(p, FP8G_ERR_INVALID_ARG, (unsigned)i);
-            if (l >= 0 && l < p.n_mat) atomicOr(&t.bits[i / p.nb][l >> 5], 1u << (l & 31));
-        }
-        __syncthreads();
-    }
-    if (warp < ng) {  // lane i: adapters 32 i .. 32 i + 31
-        const uint32_t w = t.bits[warp][lane];
-        const int c = __popc(w), s = warp_scan(c, lane);
-        int at = s - c;
-        t.word0[warp][lane] = (int16_t)at;
-        for (uint32_t m = w; m != 0; m &= m - 1)
-            t.adapter[warp][at++] = (int16_t)(32 * lane + __ffs((int)m) - 1);
-        if (lane == 31) t.n[warp] = s;
-    }
-    __syncthreads();
-    // column of a row: the rows of smaller slots, then the earlier ones of its
-    // own; a warp's 32 rows by matching, the warps of a group by their counts
-    const int padded = (p.T + 31) & ~31, last = kStreamMaxTokens;  // slot index of no adapter: n <= 128
-    for (int i = threadIdx.x; i < (padded / 32) * (last + 1); i += (int)blockDim.x) t.count[0][i] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < padded; i += (int)blockDim.x) {
-        const int g = i / p.nb;
-        int s = -1;
-        if (i < p.T) {
-            const int l = p.kr > 0 ? __ldg(p.idx + i) : -1;
-            s = l < 0 || l >= p.n_mat
-                    ? t.n[g]
-                    : t.word0[g][l >> 5] + __popc(t.bits[g][l >> 5] & ((1u << (l & 31)) - 1u));
-        }
-        // (rows of two groups in one warp: nb is a multiple of 16)
-        const uint32_t same = __match_any_sync(0xffffffffu, s < 0 ? -1 : s + (g << 8));
-        const int before = __popc(same & ((1u << lane) - 1u));
-        if (s >= 0) {
-            t.slot_of[i] = (int16_t)s;
-            t.col_of[i] = (int16_t)before;
-            if (before == 0) t.count[i / 32][s] += (uint8_t)__popc(same);
-        }
-    }
-    __syncthreads();
-    if (warp < ng) {
-        const int g = warp, w0 = g * p.nb / 32, w1 = (min(p.T, (g + 1) * p.nb) + 31) / 32;
-        int run = 0;
-        for (int s0 = 0; s0 <= t.n[g]; s0 += 32) {
-            const int s = s0 + lane;
-            int c = 0;
-            if (s <= t.n[g])
-                for (int w = w0; w < w1; ++w) c += t.count[w][s];
-            const int incl = warp_scan(c, lane);
-            if (s <= t.n[g]) t.first[g][s] = (int16_t)(run + incl - c);
-            run += __shfl_sync(0xffffffffu, incl, 31);
-        }
+    for (int i = threadIdx.x; i < ((p.T + 3) & ~3); i += (int)blockDim.x)
+        t.key[i] = i < p.T ? lora_key(p, i) : 0xFFFFFFFFu;
+    if (threadIdx.x == 0) {
+        t.n_groups = ng;
+        t.items = 0;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < p.T; i += (int)blockDim.x) {
-        const int g = i / p.nb, s = t.slot_of[i];
-        int col = t.first[g][s] + t.col_of[i];
-        for (int w = g * p.nb / 32; w < i / 32; ++w) col += t.count[w][s];
-        t.col_of[i] = (int16_t)col;
-        t.row_of[g * p.nb + col] = (int16_t)i;
+        const int lo = i / p.nb * p.nb, hi = min(p.T, lo + p.nb);  // nb is a multiple of 16
+        const uint32_t mine = t.key[i];
+        int col = 0;
+#pragma unroll 4
+        for (int j = lo; j < hi; j += 4) {
+            const uint4 k = *reinterpret_cast<const uint4 *>(t.key + j);
+            col += (k.x < mine) + (k.y < mine) + (k.z < mine) + (k.w < mine);
+        }
+        t.row_of[lo + col] = (int16_t)i;
     }
-    if (threadIdx.x == 0) t.n_groups = ng;
-    if (warp == 0) lora_windows(p, t, lane);
+    __syncthreads();
+    if (warp < ng) {
+        const int g = warp, lo = g * p.nb, n = min(p.nb, p.T - lo);
+        int slots = 0, with = 0;  // slots, rows with an adapter
+        uint32_t before = 0xFFFFFFFFu;  // adapter of the last column
+        for (int c0 = 0; c0 < n; c0 += 32) {
+            const int c = c0 + lane;
+            const uint32_t l = c < n ? t.key[t.row_of[lo + c]] / kStreamLoraRows : FP8G_MAX_ADAPTERS;
+            uint32_t prev = __shfl_up_sync(0xffffffffu, l, 1);
+            if (lane == 0) prev = before;
+            before = __shfl_sync(0xffffffffu, l, 31);
+            const bool on = l < FP8G_MAX_ADAPTERS, first = on && l != prev;
+            const uint32_t b = __ballot_sync(0xffffffffu, first);
+            if (first) {
+                const int s = slots + __popc(b & ((1u << lane) - 1u));
+                t.adapter[g][s] = (int16_t)l;
+                t.first[g][s] = (int16_t)c;
+            }
+            slots += __popc(b);
+            with += __popc(__ballot_sync(0xffffffffu, on));
+        }
+        if (lane == 0) {
+            t.n[g] = slots;
+            t.first[g][slots] = (int16_t)with;
+        }
+        __syncwarp();
+        int items = 0, most = 0;
+        for (int s = lane; s < slots; s += 32) {
+            const int from = t.first[g][s], to = t.first[g][s + 1];
+            items += (to - from + 15) / 16;
+            most = max(most, ((to + 15) & ~15) - (from & ~15));
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        items = __reduce_add_sync(0xffffffffu, items);
+        if (lane == 0) {
+            t.windows[g] = p.halves == 2 && most > p.v_cols ? 2 : 1;
+            atomicAdd(&t.items, items * ((p.rank + 15) / 16));
+        }
+    }
     __syncthreads();
 }
 
@@ -392,7 +328,6 @@ __global__ void __launch_bounds__(kPrepThreads) moe_prep_kernel(const __grid_con
 
 // Block (token, segment): the token's codes at its column.
 __global__ void __launch_bounds__(kPrepThreads) lora_prep_kernel(const __grid_constant__ StreamParams p) {
-    __shared__ LoraTables t;
     const int tid = threadIdx.x;
     const int ks = p.ph[0].ks, segs = quant_segments(ks);
     const int tok = blockIdx.x / segs, c = (blockIdx.x - tok * segs) * kPrepThreads + tid;
@@ -404,9 +339,10 @@ __global__ void __launch_bounds__(kPrepThreads) lora_prep_kernel(const __grid_co
     if (blockIdx.x == 0 && p.kr > 0)
         for (int i = tid; i < p.T; i += kPrepThreads)
             if (__ldg(p.idx + i) >= p.n_mat) record_error(p, FP8G_ERR_INVALID_ARG, (unsigned)i);
-    make_tables(p, t);
+    // the row's column: the smaller keys of its group
+    const int g = tok / p.nb, j = g * p.nb + tid;
+    const int col = __syncthreads_count(tid < p.nb && j < p.T && lora_key(p, j) < lora_key(p, tok));
     if (c >= ks * 16) return;
-    const int g = tok / p.nb, col = t.col_of[tok];
     if (q.in) *reinterpret_cast<uint2 *>(p.xq + ((int64_t)g * p.nb + col) * p.K + c * 8) = q.q;
     if ((c & 3) == 0) p.xsf[sf_at(g, ks, col, c)] = q.sf;
 }
@@ -438,6 +374,7 @@ struct Tail {
     typename TablesOf<LORA>::T tab;
 };
 
+static_assert(offsetof(LoraTables, key) % 16 == 0 && alignof(Tail<true>) % 16 == 0, "keys are read in fours");
 static_assert(kSmemMax - 1024 - (int)(sizeof(Tail<false>) > sizeof(Tail<true>) ? sizeof(Tail<false>)
                                                                                : sizeof(Tail<true>)) >=
                   6 * (2 * kWTile + 16 * 128 + 2048),
