@@ -305,10 +305,16 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
     if (M == 0) return FP8G_OK;
 
     const LoraV lv(lora ? r : 1);
-    const bool pair = M > kStreamLoraRows;
+    const int32_t ks = (int32_t)((K + 127) / 128), n_rt = (int32_t)((N + 127) / 128);
+    // CTA pairs from 513 rows on, and from 129 where the low-rank steps of a tile
+    // are few beside its FP8 steps: they make all of a pair's 256 rows wait, where
+    // the streaming kernel covers an adapter's columns.  256 rows at 4096 x 14336:
+    // 8 adapters of rank 16 30.8 us (streamed 37.1), 32 of rank 64 63.9 (55.2); 128
+    // rows: 30.3 (31.4) and 63.1 (43.0).
+    const int most = lora ? (L < kMaxTile ? L : kMaxTile) * lv.kr * lv.halves : 0;
+    const bool pair = M > kStreamLoraRows || (M > kStreamMaxTokens && 2 * most <= ks);
     const int nb = pair ? 256 : stream_columns(M);
     const int tiles = (int)((M + nb - 1) / nb), cap = L < nb ? L : nb;
-    const int32_t ks = (int32_t)((K + 127) / 128), n_rt = (int32_t)((N + 127) / 128);
     const int32_t n_rtA = (int32_t)((M + 127) / 128);
     // rows of V and of the scales: 32-bit TMA coordinates
     if ((int64_t)tiles * cap * lv.halves * nb >= kMaxDim || (int64_t)ks * n_rtA >= kMaxDim)
@@ -316,10 +322,11 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
     StreamParams p{};
     StreamPhase &h = p.ph[0];
     if (!pair) {
-        // one weight tile a unit where pairs of them would be few
+        // one weight tile a ticket where pairs of them would be few: 33 rows at 4096 x
+        // 14336 27.4 us by one, 29.6 by pairs; 4096 x 28672 41.7 and 35.5
         h.sub = tiles * ((N + 255) / 256) * 8 >= d.num_sms * 5 ? 2 : 1;
         h.mt = (int32_t)((N + 128 * h.sub - 1) / (128 * h.sub));
-        stream_sizes(p, nb, h.sub, true, lv.halves, stream_one_ticket(tiles * h.mt, ks, d.num_sms));
+        stream_sizes(p, nb, h.sub, true, lv.halves);
         h.ks = ks;
         h.rows = (int32_t)N;
         h.n_rt = n_rt;

@@ -118,7 +118,7 @@ fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t *ids, co
     // groups: each expert's rows in tiles of nb
     const int max_groups = (int)((E < R ? E : R) + R / nb);
     StreamParams p{};
-    stream_sizes(p, nb, 2, false, 1, false);
+    stream_sizes(p, nb, 2, false, 1);
     StreamPhase &g = p.ph[0], &dn = p.ph[1];
     g.sub = dn.sub = 2;
     g.mt = (int32_t)((F + 127) / 128);

@@ -71,8 +71,8 @@ constexpr int kPrepWarps = kPrepThreads / 32;
 constexpr int kWTile = 128 * 128;  // bytes of a weight tile in shared memory
 constexpr int kMaxStages = 16;
 constexpr int kSfSlot = 16;        // tensor-memory columns of a stage's scales
-constexpr int kLittle = 16;        // steps an SM, in parts_of
-constexpr int kMinSteps = 4;       // steps of a part at least
+// Steps of a part at least (33 rows at 1024 x 2048: 15.3 us, with parts of four 17.8).
+constexpr int kMinSteps = 8;
 constexpr int kCols = 8;           // token columns at a time in an epilogue (few: its code runs cold)
 constexpr int kPairs = 256;        // pairs (token, expert) of a table of the weighted sum
 constexpr int kTickets = 4;        // tickets in flight in a CTA
@@ -394,14 +394,14 @@ static_assert(kSmemMax - 1024 - (int)(sizeof(Tail<false>) > sizeof(Tail<true>) ?
                   6 * (2 * kWTile + 16 * 128 + 2048),
               "six stages with 16 token columns");
 
-// Parts of the tiles of a product, where the tiles alone are fewer than five for
-// eight SMs: as many as give every SM two tickets, or just one where that is
-// little work already (a part costs its sums' way through memory).
+// Parts of the tiles of a product: as many as give every SM a ticket at most.  (One
+// token, two experts, down product of 32 tiles of 112 steps: 4 parts 67.3 us per
+// call, 10 parts, two tickets an SM, 70.7.  64 tiles of 32 steps, adapters, one
+// row at 4096 x 8192: 2 parts 17.3, unsplit 18.9.)
 __host__ __device__ inline int parts_of(int tiles, int ks, int num_sms) {
-    if (tiles * 8 >= num_sms * 5 || tiles >= kStreamSplitTiles || tiles == 0) return 1;
-    const bool little = (int64_t)tiles * ks < (int64_t)kLittle * num_sms;
-    const int want = little ? num_sms / tiles : (2 * num_sms + tiles - 1) / tiles, most = ks / kMinSteps;
-    return want < most ? want : most > 1 ? most : 1;
+    if (tiles == 0 || tiles * 2 > num_sms || tiles > kStreamSplitTiles) return 1;
+    const int most = ks / kMinSteps;
+    return min(num_sms / tiles, most > 1 ? most : 1);
 }
 
 // What a ticket stands for: steps [k0, k1) of the upt of a tile.
@@ -1407,14 +1407,13 @@ cudaError_t launch_one(const StreamParams &p, int grid, cudaStream_t s) {
 
 }  // namespace
 
-void stream_sizes(StreamParams &p, int nb, int sub, bool lora, int v_halves, bool one) {
+void stream_sizes(StreamParams &p, int nb, int sub, bool lora, int v_halves) {
     p.nb = nb;
     // Tensor memory beside the scales (up to eight stages' 128 columns): two
     // accumulators, so that a tile's epilogue overlaps the next tile, then two
     // chains each
     const int room_cols = 512 - 8 * kSfSlot;
     p.nacc = 2 * sub * nb <= room_cols ? 2 : 1;
-    if (lora && one && p.nacc * sub * 2 * nb > room_cols && sub * 2 * nb <= room_cols) p.nacc = 1;
     p.chains = p.nacc * sub * 2 * nb <= room_cols ? 2 : 1;
     p.acc_cols = sub * p.chains * nb;
     p.w_bytes = sub * kWTile;
@@ -1431,13 +1430,8 @@ void stream_sizes(StreamParams &p, int nb, int sub, bool lora, int v_halves, boo
     if (p.stages > kMaxStages) p.stages = kMaxStages;
 }
 
-bool stream_one_ticket(int64_t tiles, int ks, int num_sms) {
-    return tiles <= num_sms && tiles * parts_of((int)tiles, ks, num_sms) <= num_sms;
-}
-
 size_t stream_part_bytes(const StreamParams &p, int num_sms) {
-    // tiles * parts_of(tiles) < tiles + 2 SMs with tiles < 5/8 SMs
-    return (size_t)(num_sms * 21 / 8 + 2) * 2 * p.nb * 128 * sizeof(float);
+    return (size_t)num_sms * 2 * p.nb * 128 * sizeof(float);  // split tiles: at most a part per SM
 }
 
 cudaError_t launch_stream(bool lora, const StreamParams &p, int num_sms, cudaStream_t s) {

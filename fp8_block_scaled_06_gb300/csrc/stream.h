@@ -9,7 +9,7 @@ constexpr int kStreamMaxTokens = 128;    // token rows of a group
 constexpr int kStreamMaxGroups = 320;
 constexpr int kStreamLoraRows = 512;     // token rows of a call with adapters
 constexpr int kStreamLoraGroups = kStreamLoraRows / kStreamMaxTokens;
-constexpr int kStreamSplitTiles = 256;   // a product with as many tiles is not split
+constexpr int kStreamSplitTiles = 128;   // a product with more tiles is not split (128 x 2 > 152 SMs)
 
 // V = alpha A x of a slot (an adapter of a row tile) as two bf16 halves, V = hi
 // + lo to 16 bits.  Rank up to 32: a row of 64 values holds both, hi in
@@ -79,9 +79,7 @@ struct StreamParams {
 // Token columns for groups of up to n rows.
 inline int stream_columns(int64_t n) { return n <= 64 ? (int)((n + 15) / 16 * 16) : kStreamMaxTokens; }
 // Ring and accumulator sizes for nb token columns, sub weight tiles a stage.
-void stream_sizes(StreamParams &p, int nb, int sub, bool lora, int v_halves, bool one);
-// Whether no SM takes more than one ticket of a product of so many tiles.
-bool stream_one_ticket(int64_t tiles, int ks, int num_sms);
+void stream_sizes(StreamParams &p, int nb, int sub, bool lora, int v_halves);
 // Bytes of a product's partial tiles; SMs of the device.
 size_t stream_part_bytes(const StreamParams &p, int num_sms);
 // Prepares the tokens, then runs the products: two launches.

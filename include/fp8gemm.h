@@ -594,9 +594,9 @@ FP8G_API fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t
  * % 16 == 0, else FP8G_ERR_ALIGNMENT.  Results do not vary between runs.
  * lora_b is finite: an infinity or NaN in an adapter's B can reach rows of other
  * adapters as NaN (in W, A, alpha and x they stay with their own column or rows).
- * Two kernels up to 512 rows, three for more (two without adapters), and one
- * temporary from the library's pool: M K bytes, 4 M min(L, 256) max(r, 64) for A x,
- * up to 512 rows also up to 53 MB of partial sums.
+ * Two kernels for few rows (up to 128, with many adapters 512), else three (two
+ * without adapters), and one temporary from the library's pool: M K bytes, 4 M
+ * min(L, 256) max(r, 64) for A x, for few rows also up to 20 MB of partial sums.
  */
 FP8G_API fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void *W, const uint8_t *sfw,
                                    int32_t w_fmt, const void *lora_a, const void *lora_b,

@@ -194,3 +194,10 @@ def test_pack_scales(n, rows, K):
     sf[0, 0, 0] = 3.0
     fp8g.pack_scales(sf.cuda())
     assert fp8g.fp8_gemm_status()[0] == fp8g.FP8G_ERR_SCALE_FORMAT
+
+
+@pytest.mark.parametrize("M,N,K,L,r", [(129, 136, 1024, 1, 8), (200, 264, 1056, 2, 32), (300, 520, 2048, 1, 72),
+                                       (512, 128, 1024, 4, 16)])
+def test_few_adapters_of_many_rows(M, N, K, L, r):
+    """From 129 rows on a call with few adapters beside its K takes the path of the prompts."""
+    Projection(M, N, K, L, r).check_exact()
