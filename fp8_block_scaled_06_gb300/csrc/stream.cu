@@ -474,6 +474,13 @@ struct Step {
 // A role's way through a tile's low-rank steps: windows in rank blocks in slots.
 struct LowRank {
     int slot = 0, c = 0, w = 0;
+    __device__ __forceinline__ void next(const StreamParams &p, int nw) {
+        if (++w < nw) return;
+        w = 0;
+        if (++c < p.kr) return;
+        c = 0;
+        ++slot;
+    }
     template <bool LORA>
     __device__ __forceinline__ void start(const StreamParams &p, const Tail<LORA> &t, const Tile &o) {
         if constexpr (LORA) {
@@ -508,13 +515,7 @@ __device__ __forceinline__ Step step_of(const StreamParams &p, const Tail<LORA> 
                     s.n = s.none ? 16 : min(p.v_cols, hi - from);
                 }
             }
-            if (++q.w == t.tab.windows[o.g]) {
-                q.w = 0;
-                if (++q.c == p.kr) {
-                    q.c = 0;
-                    ++q.slot;
-                }
-            }
+            q.next(p, t.tab.windows[o.g]);
         }
     }
     return s;
@@ -674,8 +675,6 @@ __device__ __forceinline__ void load_tokens(const StreamParams &p, Tail<LORA> &t
                 }
                 t.low[r.stage] = (uint32_t)(st.lo | st.n << 8 |
                                             (st.none ? 0 : (min(64, p.rank - st.c) + 15) / 16) << 16);
-                // the window's rows, from the start of the region: the halves in
-                // one copy, or of a wider window each half's 16 rows in turn
                 const int v0 = (o.g * p.slot_cap + st.slot) * p.halves;
                 ptx::mbar_arrive_expect_tx(fb, p.halves * st.n * 128u);
                 if (st.n == 16)
@@ -761,28 +760,36 @@ __device__ __forceinline__ void issue_mmas(const StreamParams &p, Tail<LORA> &t,
         const bool has1 = uniform(o.has1) != 0;
         const uint32_t d0 = tmem + acc * p.acc_cols, d1 = d0 + tile_cols;
         const uint32_t id8 = ptx::idesc_mxf8(128, 0, 0) | (uint32_t)(n16 >> 3) << 17 | p.w_fmt;
-        for (int k = k0; k < k1; ++k) {
+        for (int k = k0; k < (LORA ? min(k1, fp8) : k1); ++k) {
             if (!wait(&t.sfr[r.stage], r.phase, 256 + r.stage)) return;
             ptx::tc_fence_after();
             const uint32_t at = r.stage * stage16;
             const uint32_t first = k == k0 ? 0u : 1u;
-            if (!LORA || k < fp8) {
-                const uint32_t sf = sf_tmem + r.stage * kSfSlot;
-                if (elect_one()) {
+            const uint32_t sf = sf_tmem + r.stage * kSfSlot;
+            if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t id = id8 | ((uint32_t)j << 4) | ((uint32_t)j << 29);
-                        const uint32_t on = j < p.chains ? first : 1u, c = (j & 1) ? odd : 0;
-                        ptx::mma_mxf8(d0 + c, w_desc + at + 2 * j, x_desc + at + 2 * j, id, sf, sf + 8, on);
-                        if (has1)
-                            ptx::mma_mxf8(d1 + c, w_desc + at + tile16 + 2 * j, x_desc + at + 2 * j, id, sf + 4,
-                                          sf + 8, on);
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t id = id8 | ((uint32_t)j << 4) | ((uint32_t)j << 29);
+                    const uint32_t on = j < p.chains ? first : 1u, c = (j & 1) ? odd : 0;
+                    ptx::mma_mxf8(d0 + c, w_desc + at + 2 * j, x_desc + at + 2 * j, id, sf, sf + 8, on);
+                    if (has1)
+                        ptx::mma_mxf8(d1 + c, w_desc + at + tile16 + 2 * j, x_desc + at + 2 * j, id, sf + 4,
+                                      sf + 8, on);
                 }
-            } else if constexpr (LORA) {
+            }
+            if (elect_one()) ptx::tc_commit(ptx::smem_addr(&t.empty[r.stage]));
+            __syncwarp();
+            r.next(p);
+        }
+        if constexpr (LORA) {
+            for (int k = max(k0, fp8); k < k1; ++k) {
+                if (!wait(&t.sfr[r.stage], r.phase, 256 + r.stage)) return;
+                ptx::tc_fence_after();
                 const int all = uniform((int)t.low[r.stage]);
                 const int lo = all & 255, n = all >> 8 & 255, nk = all >> 16;
+                const uint32_t first = k == k0 ? 0u : 1u;
                 const uint32_t id16 = ptx::idesc_bf16(128, 0) | (uint32_t)(n >> 3) << 17;
+                const uint32_t at = r.stage * stage16;
                 // the lo half: rows of its own after the hi ones, or columns 32-63;
                 // into the second accumulator
                 const uint64_t xh = x_desc + at, xl = xh + (p.halves == 2 ? n * 8 : 4);
@@ -798,10 +805,10 @@ __device__ __forceinline__ void issue_mmas(const StreamParams &p, Tail<LORA> &t,
                         if (has1) ptx::mma_bf16(dl + tile_cols, w1, xl + 2 * j, id16, j == 0 ? e : 1u);
                     }
                 }
+                if (elect_one()) ptx::tc_commit(ptx::smem_addr(&t.empty[r.stage]));
+                __syncwarp();
+                r.next(p);
             }
-            if (elect_one()) ptx::tc_commit(ptx::smem_addr(&t.empty[r.stage]));
-            __syncwarp();
-            r.next(p);
         }
         if (elect_one()) ptx::tc_commit(ptx::smem_addr(&t.accf[acc]));
         __syncwarp();
