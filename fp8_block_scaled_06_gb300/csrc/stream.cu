@@ -36,14 +36,16 @@
 // mma.sync, the same term took 128 rows of 32 adapters of rank 64 from 48 to 66 us.
 //
 // Measured, per call on the device back to back, beside the bytes at 6.78 TB/s:
-// one token, two experts of 4096 x 14336, 72 us (54); 5 tokens over 64 experts of
-// 2080 x 1440, 62 (43); 16 tokens over 32 4-bit experts of 4096 x 2048, 78 (56);
+// one token, two experts of 4096 x 14336, 67 us (54); 5 tokens over 64 experts of
+// 2080 x 1440, 60 (43); 16 tokens over 32 4-bit experts of 4096 x 2048, 72 (56);
 // 64 tokens over 8 experts of 4096 x 14336, 227 (214).  While it streams it reads
 // 6.6 to 7.1 TB/s; what is left is 6 us from the call before to the first weights
 // in shared memory, the wait of the down product's first tokens, and 6 us from the
-// last weights to the end.  Adapters: 33 rows at 4096 x 4096, rank 16, 23 us (3);
-// 128 rows of 32 adapters, rank 64, at 4096 x 14336, 44 (21): V is done 14 us after
-// the tokens, then 32 low-rank steps of 0.5 us, bound by the loading thread.
+// last weights to the end.  Adapters: 33 rows at 4096 x 4096, rank 16, 22 us (3);
+// 128 rows of 32 adapters, rank 64, at 4096 x 14336, 42 (21): 26 the projection (an
+// SM takes in 58 GB/s, of which half are tokens), 3 V, 13 the 32 low-rank steps, of
+// which 9 are the roles' own instructions a step (measured without the loads and
+// MMAs).
 //
 // Roles: warp 0 takes tickets and loads weights, warp 3 the tokens' slices and
 // the scales, warp 2 copies scales to tensor memory, warp 1 issues MMAs, warps
