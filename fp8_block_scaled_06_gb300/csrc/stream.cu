@@ -289,11 +289,12 @@ __global__ void __launch_bounds__(kPrepThreads) moe_prep_kernel(const __grid_con
     __syncthreads();
     ptx::grid_dep_wait();  // launched programmatically: global memory from here on
     ptx::grid_dep_launch();
+    const int first = tid < p.n_idx ? __ldg(p.idx + tid) : -1;  // on the way beside the token
     const Quant8 q = quant_8(p, tok, c);
     for (int i = blockIdx.x * kPrepThreads + tid; i < p.n_counters; i += gridDim.x * kPrepThreads)
         p.counters[i] = 0;
     for (int i = tid; i < p.n_idx; i += kPrepThreads) {
-        const int e = __ldg(p.idx + i);
+        const int e = i == tid ? first : __ldg(p.idx + i);
         if (e >= p.n_mat && blockIdx.x == 0) record_error(p, FP8G_ERR_INVALID_ARG, (unsigned)i);
         if (e >= 0 && e < p.n_mat) {
             atomicAdd(&cnt[e], 1);
@@ -352,9 +353,7 @@ __global__ void __launch_bounds__(kPrepThreads) lora_prep_kernel(const __grid_co
     const Quant8 q = quant_8(p, tok, c);
     for (int i = blockIdx.x * kPrepThreads + tid; i < p.n_counters; i += gridDim.x * kPrepThreads)
         p.counters[i] = 0;
-    if (blockIdx.x == 0 && p.kr > 0)
-        for (int i = tid; i < p.T; i += kPrepThreads)
-            if (__ldg(p.idx + i) >= p.n_mat) record_error(p, FP8G_ERR_INVALID_ARG, (unsigned)i);
+    if (c == 0 && p.kr > 0 && __ldg(p.idx + tok) >= p.n_mat) record_error(p, FP8G_ERR_INVALID_ARG, (unsigned)tok);
     // the row's column: the smaller keys of its group
     const int g = tok / p.nb, j = g * p.nb + tid;
     const int col = __syncthreads_count(tid < p.nb && j < p.T && lora_key(p, j) < lora_key(p, tok));

@@ -201,3 +201,20 @@ def test_pack_scales(n, rows, K):
 def test_few_adapters_of_many_rows(M, N, K, L, r):
     """From 129 rows on a call with few adapters beside its K takes the path of the prompts."""
     Projection(M, N, K, L, r).check_exact()
+
+
+def test_calls_on_several_streams():
+    ps = [Projection(m, 520, 1056, 5, 16, seed=m) for m in (1, 40, 128, 700)]
+    want = [p.run() for p in ps]
+    args = [(p.x.bfloat16().cuda(), p.W, p.pw, p.a.bfloat16().cuda(), p.b.bfloat16().cuda(),
+             p.alpha.float().cuda(), p.adapter.cuda(), p.bias.cuda()) for p in ps]
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    got = [[] for _ in ps]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(fp8g.gemm_lora(*args[i], out="f32"))
+    torch.cuda.synchronize()
+    assert fp8g.fp8_gemm_status()[0] == 0
+    assert all(torch.equal(g, w) for w, gs in zip(want, got) for g in gs)

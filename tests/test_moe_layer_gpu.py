@@ -206,3 +206,25 @@ def test_route_then_layer():
     got = l.run().cpu().double()
     assert ((got - ref).abs() <= (96 + 4) * 2.0 ** -21 * room).all()
     assert (got[4] == 0).all()
+
+
+@pytest.mark.parametrize("T,E,k,H,F", [(512, 16, 16, 64, 64), (33, 256, 16, 64, 32), (127, 20, 7, 96, 160)])
+def test_many_pairs(T, E, k, H, F):
+    Layer(T, E, k, H, F, seed=2).check_exact()
+
+
+def test_calls_on_several_streams():
+    """Calls in flight together: no CTA waits for one that has not started."""
+    layers = [Layer(t, 4, 2, 1056, 1120, seed=t) for t in (1, 20, 64)]
+    want = [l.run() for l in layers]
+    args = [(l.x.bfloat16().cuda(), l.ids.cuda(), l.w.cuda(), l.W13, l.p13, l.W2, l.p2) for l in layers]
+    streams = [torch.cuda.Stream() for _ in layers]
+    torch.cuda.synchronize()
+    got = [[] for _ in layers]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(fp8g.moe_layer(*args[i], gate=layers[i].gate, out="f32"))
+    torch.cuda.synchronize()
+    assert fp8g.fp8_gemm_status()[0] == 0
+    assert all(torch.equal(g, w) for w, gs in zip(want, got) for g in gs)
