@@ -1068,7 +1068,22 @@ __device__ __forceinline__ void store_cols(const StreamParams &p, const StreamPh
 // values a thread.  y: rows in memory, or where the tiles are split the sums of
 // the tiles' parts (in order).  The pairs' rows and weights go through shared
 // memory a table at a time, so that only the loads of y are on the way, several
-// tokens' at once.
+// tokens' at once; a call of one table makes it before its first tile.
+template <bool LORA>
+__device__ __forceinline__ void fill_pairs(const StreamParams &p, Tail<LORA> &t, int tok0, int n) {
+    for (int i = (int)threadIdx.x - kSEpiWarp0 * 32; i < n * p.k; i += kEpiThreads) {
+        const int pos = __ldcg(p.pos + tok0 * p.k + i);
+        int at = pos;
+        if (t.parts[1] > 1 && pos >= 0) {
+            // group and column of the row: its partial tiles' first value
+            int g = 0;
+            while (pos >= t.tab.g[g].row0 + t.tab.g[g].n) ++g;
+            at = g << 8 | (pos - t.tab.g[g].row0);
+        }
+        t.pair_at[i] = at;
+        t.pair_w[i] = __ldg(p.weights + tok0 * p.k + i);
+    }
+}
 template <bool LORA>
 __device__ __forceinline__ void combine(const StreamParams &p, Tail<LORA> &t, const Tile &o) {
     const StreamPhase &h = p.ph[1];
@@ -1079,20 +1094,11 @@ __device__ __forceinline__ void combine(const StreamParams &p, Tail<LORA> &t, co
     const int step = min(p.T, kPairs / p.k);  // tokens of a table
     for (int tok0 = 0; tok0 < p.T; tok0 += step) {
         const int n = min(step, p.T - tok0);
-        (void)epi_all(true);
-        for (int i = tid; i < n * p.k; i += kEpiThreads) {
-            const int pos = __ldcg(p.pos + tok0 * p.k + i);
-            int at = pos;
-            if (parts > 1 && pos >= 0) {
-                // group and column of the row: its partial tiles' first value
-                int g = 0;
-                while (pos >= t.tab.g[g].row0 + t.tab.g[g].n) ++g;
-                at = g << 8 | (pos - t.tab.g[g].row0);
-            }
-            t.pair_at[i] = at;
-            t.pair_w[i] = __ldg(p.weights + tok0 * p.k + i);
+        if (step < p.T) {
+            (void)epi_all(true);
+            fill_pairs(p, t, tok0, n);
+            (void)epi_all(true);
         }
-        (void)epi_all(true);
         if (c >= H) continue;
         constexpr int kTok = 4;
         for (int a = team; a < n; a += teams * kTok) {
@@ -1352,6 +1358,8 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const __grid_constant__ 
                 if (threadIdx.x == kSEpiWarp0 * 32) (void)atom_add_acq_rel(p.counters + 2, 1);
             }
         }
+        if constexpr (!LORA)
+            if (p.T <= kPairs / p.k) fill_pairs(p, t, 0, p.T);  // (read after the barriers below)
         Queue q;
         Tile o;
         for (int lt = 0;; ++lt) {
