@@ -398,7 +398,8 @@ static_assert(kSmemMax - 1024 - (int)(sizeof(Tail<false>) > sizeof(Tail<true>) ?
 // Parts of the tiles of a product: as many as give every SM a ticket at most.  (One
 // token, two experts, down product of 32 tiles of 112 steps: 4 parts 67.3 us per
 // call, 10 parts, two tickets an SM, 70.7.  64 tiles of 32 steps, adapters, one
-// row at 4096 x 8192: 2 parts 17.3, unsplit 18.9.)
+// row at 4096 x 8192: 2 parts 17.3, unsplit 18.9.  64 tokens, 128 down tiles of 112
+// steps: unsplit 227, 2 parts 249.)
 __host__ __device__ inline int parts_of(int tiles, int ks, int num_sms) {
     if (tiles == 0 || tiles * 2 > num_sms || tiles > kStreamSplitTiles) return 1;
     const int most = ks / kMinSteps;
