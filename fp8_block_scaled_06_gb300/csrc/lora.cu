@@ -214,7 +214,8 @@ __global__ void __launch_bounds__(kLThreads, 2) lora_v_kernel(const __grid_const
     constexpr int kU = BF16 ? 2 : 1;
     auto go = [&](auto count, int s0) {
         constexpr int U = decltype(count)::value;
-        uint4 xa[U], xb[U], wa[U], wb[U], ya[U], yb[U];
+        uint4 xa[U], xb[U], wa[U], wb[U];
+        [[maybe_unused]] uint4 ya[U], yb[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int k = (s0 + u) * 32;

@@ -41,7 +41,7 @@
 // 64 tokens over 8 experts of 4096 x 14336, 227 (214).  While it streams it reads
 // 6.6 to 7.1 TB/s; what is left is 6 us from the call before to the first weights
 // in shared memory, the wait of the down product's first tokens, and 6 us from the
-// last weights to the end.  Adapters: 33 rows at 4096 x 4096, rank 16, 22 us (3);
+// last weights to the end.  Adapters: 33 rows at 4096 x 4096, rank 16, 19 us (3);
 // 128 rows of 32 adapters, rank 64, at 4096 x 14336, 42 (21): 26 the projection (an
 // SM takes in 58 GB/s, of which half are tokens), 3 V, 13 the 32 low-rank steps, of
 // which 9 are the roles' own instructions a step (measured without the loads and
@@ -406,13 +406,16 @@ __host__ __device__ inline int parts_of(int tiles, int ks, int num_sms) {
     return min(num_sms / tiles, most > 1 ? most : 1);
 }
 
-// What a ticket stands for: steps [k0, k1) of the upt of a tile.
+// What a ticket stands for: steps [k0, k1) of a tile, then (adapters) its low-rank
+// steps [l0, l1).  Every part has its share of both (the low-rank ones all in the
+// last part: 33 rows of 16 adapters at 4096 x 4096 21.7 us instead of 18.6); the
+// FP8 steps start its accumulators.
 struct Tile {
     int32_t ph, g, mt, part, tile;
     int32_t row0, n, n16;
     int32_t mat0, mat1, w0, w1;  // matrix and first row of the two weight tiles
     bool has1;                   // the second one exists
-    int32_t k0, k1, upt;
+    int32_t k0, k1, l0, l1;
 };
 
 template <bool LORA>
@@ -426,9 +429,13 @@ __device__ __forceinline__ bool decode(const StreamParams &p, const Tail<LORA> &
     o.part = ticket - o.tile * parts;
     o.g = o.tile / h.mt;
     o.mt = o.tile - o.g * h.mt;
-    o.upt = h.ks;
+    o.k0 = h.ks * o.part / parts;
+    o.k1 = h.ks * (o.part + 1) / parts;
+    o.l0 = o.l1 = 0;
     if constexpr (LORA) {
-        o.upt += t.tab.n[o.g] * p.kr * t.tab.windows[o.g];
+        const int low = t.tab.n[o.g] * p.kr * t.tab.windows[o.g];
+        o.l0 = low * o.part / parts;
+        o.l1 = low * (o.part + 1) / parts;
         o.row0 = o.g * p.nb;
         o.n = min(p.nb, p.T - o.row0);
         o.mat0 = 0;
@@ -437,16 +444,6 @@ __device__ __forceinline__ bool decode(const StreamParams &p, const Tail<LORA> &
         o.row0 = gr.row0;
         o.n = gr.n;
         o.mat0 = o.ph ? gr.mat : 2 * gr.mat;
-    }
-    o.k0 = o.upt * o.part / parts;
-    o.k1 = o.upt * (o.part + 1) / parts;
-    if constexpr (LORA) {
-        // a stage without room for V's halves of all columns: the low-rank steps
-        // are the last part's, after an FP8 step at least
-        if (p.halves == 2 && p.v_cols < p.nb) {
-            o.k0 = h.ks * o.part / parts;
-            o.k1 = o.part + 1 == parts ? o.upt : h.ks * (o.part + 1) / parts;
-        }
     }
     o.n16 = (o.n + 15) & ~15;
     if (!LORA && o.ph == 0) {
@@ -462,16 +459,12 @@ __device__ __forceinline__ bool decode(const StreamParams &p, const Tail<LORA> &
     return true;
 }
 
-// Step k of a tile: FP8 steps first, then the low-rank ones.  `lo`, `n`: the
-// token columns it covers, all of them but in low-rank steps: the 16-column
-// windows of the slot's rows (of up to v_cols columns where V's halves take rows
-// of their own; the step that starts an accumulator covers all: V is zero in the
-// others').
+// A low-rank step: a slot's 64 ranks from c on for n token columns from lo on, the
+// 16-column windows of the slot's rows (of up to v_cols columns where V's halves
+// take rows of their own; V is zero in the others' columns).
 struct Step {
-    bool fp8;
-    int slot, c;  // low-rank: slot of the group, first rank
-    int lo, n;
-    bool none;    // low-rank: the slot has no rows in this window
+    int slot, c, lo, n;
+    bool none;  // the slot has no rows in this window
 };
 // A role's way through a tile's low-rank steps: windows in rank blocks in slots.
 struct LowRank {
@@ -486,40 +479,24 @@ struct LowRank {
     template <bool LORA>
     __device__ __forceinline__ void start(const StreamParams &p, const Tail<LORA> &t, const Tile &o) {
         if constexpr (LORA) {
-            const int l = o.k0 - p.ph[0].ks;
-            slot = c = w = 0;
-            if (l > 0) {  // (divisions take longer than a step's MMAs: once a tile)
-                const int nw = t.tab.windows[o.g], per = p.kr * nw;
-                slot = l / per;
-                c = (l - slot * per) / nw;
-                w = l - slot * per - c * nw;
-            }
+            // (divisions take longer than a step's MMAs: once a tile)
+            const int nw = t.tab.windows[o.g], per = p.kr * nw;
+            slot = o.l0 / per;
+            c = (o.l0 - slot * per) / nw;
+            w = o.l0 - slot * per - c * nw;
         }
     }
 };
-template <bool LORA>
-__device__ __forceinline__ Step step_of(const StreamParams &p, const Tail<LORA> &t, const Tile &o, int k,
-                                        LowRank &q) {
-    Step s{true, 0, 0, 0, o.n16, false};
-    if constexpr (LORA) {
-        if (k >= p.ph[0].ks) {
-            s.fp8 = false;
-            s.slot = q.slot;
-            s.c = q.c * 64;
-            if (k != o.k0) {
-                const int lo = t.tab.first[o.g][s.slot] & ~15, hi = (t.tab.first[o.g][s.slot + 1] + 15) & ~15;
-                s.lo = lo;
-                s.n = hi - lo;
-                if (p.halves == 2 && p.v_cols < p.nb) {
-                    const int from = lo + q.w * p.v_cols;
-                    s.none = from >= hi;
-                    s.lo = s.none ? lo : from;
-                    s.n = s.none ? 16 : min(p.v_cols, hi - from);
-                }
-            }
-            q.next(p, t.tab.windows[o.g]);
-        }
+__device__ __forceinline__ Step step_of(const StreamParams &p, const LoraTables &t, const Tile &o, LowRank &q) {
+    const int lo = t.first[o.g][q.slot] & ~15, hi = (t.first[o.g][q.slot + 1] + 15) & ~15;
+    Step s{q.slot, q.c * 64, lo, hi - lo, false};
+    if (p.halves == 2 && p.v_cols < p.nb) {
+        const int from = lo + q.w * p.v_cols;
+        s.none = from >= hi;
+        s.lo = s.none ? lo : from;
+        s.n = s.none ? 16 : min(p.v_cols, hi - from);
     }
+    q.next(p, t.windows[o.g]);
     return s;
 }
 
@@ -602,27 +579,32 @@ __device__ __forceinline__ void load_weights(const StreamParams &p, Tail<LORA> &
         Tile o;
         if (!decode(p, t, ticket, o)) return;
         const StreamPhase &h = p.ph[o.ph];
-        LowRank low;
-        low.start(p, t, o);
-        const int ask = max(o.k0, o.k1 - 2);
+        // the next ticket: late enough that a CTA does not hold a tile others could
+        // start, early enough that the answer is there when this tile's loads are out
+        const int steps = o.k1 - o.k0 + o.l1 - o.l0, ask = max(0, steps - 2);
         for (int k = o.k0; k < o.k1; ++k) {
-            // late enough that a CTA does not hold a tile others could start,
-            // early enough that the answer is there when this tile's loads are out
-            if (k == ask) next = atomicAdd(p.counters, 1);
+            if (k - o.k0 == ask) next = atomicAdd(p.counters, 1);
             if (!wait_bar(ptx::smem_addr(&t.empty[r.stage]), r.phase ^ 1u, abort_flag, p, r.stage)) return;
             const uint32_t fb = ptx::smem_addr(&t.full[r.stage]), s0 = sbase + r.stage * p.stage_bytes;
-            const Step st = step_of(p, t, o, k, low);
-            if (st.fp8) {
-                ptx::mbar_arrive_expect_tx(fb, o.has1 ? 2 * w_tx : w_tx);
-                ptx::tma_load_3d(s0, &h.W, fb, k * kBK, o.w0, o.mat0);
-                if (o.has1) ptx::tma_load_3d(s0 + kWTile, &h.W, fb, k * kBK, o.w1, o.mat1);
-            } else if constexpr (LORA) {
-                const int l = t.tab.adapter[o.g][st.slot];
-                ptx::mbar_arrive_expect_tx(fb, o.has1 ? 2 * kWTile : kWTile);
-                ptx::tma_load_3d(s0, &p.B, fb, st.c, o.w0, l);
-                if (o.has1) ptx::tma_load_3d(s0 + kWTile, &p.B, fb, st.c, o.w1, l);
-            }
+            ptx::mbar_arrive_expect_tx(fb, o.has1 ? 2 * w_tx : w_tx);
+            ptx::tma_load_3d(s0, &h.W, fb, k * kBK, o.w0, o.mat0);
+            if (o.has1) ptx::tma_load_3d(s0 + kWTile, &h.W, fb, k * kBK, o.w1, o.mat1);
             r.next(p);
+        }
+        if constexpr (LORA) {
+            LowRank low;
+            if (o.l0 < o.l1) low.start(p, t, o);
+            for (int l = o.l0; l < o.l1; ++l) {
+                if (o.k1 - o.k0 + l - o.l0 == ask) next = atomicAdd(p.counters, 1);
+                const Step st = step_of(p, t.tab, o, low);
+                const int adapter = t.tab.adapter[o.g][st.slot];
+                if (!wait_bar(ptx::smem_addr(&t.empty[r.stage]), r.phase ^ 1u, abort_flag, p, r.stage)) return;
+                const uint32_t fb = ptx::smem_addr(&t.full[r.stage]), s0 = sbase + r.stage * p.stage_bytes;
+                ptx::mbar_arrive_expect_tx(fb, o.has1 ? 2 * kWTile : kWTile);
+                ptx::tma_load_3d(s0, &p.B, fb, st.c, o.w0, adapter);
+                if (o.has1) ptx::tma_load_3d(s0 + kWTile, &p.B, fb, st.c, o.w1, adapter);
+                r.next(p);
+            }
         }
     }
 }
@@ -645,8 +627,6 @@ __device__ __forceinline__ void load_tokens(const StreamParams &p, Tail<LORA> &t
             fence_proxy_async_all();
             ready = o.g;
         }
-        LowRank low;
-        low.start(p, t, o);
         const int64_t step = (int64_t)h.n_rt * 512;
         const uint8_t *c0 = h.sfw + (int64_t)o.mat0 * h.ks * step + o.w0 / 128 * 512;
         const uint8_t *c1 = h.sfw + (int64_t)o.mat1 * h.ks * step + o.w1 / 128 * 512;
@@ -661,20 +641,30 @@ __device__ __forceinline__ void load_tokens(const StreamParams &p, Tail<LORA> &t
                 return;
             const uint32_t fb = ptx::smem_addr(&t.full[r.stage]);
             const uint32_t x0 = sbase + r.stage * p.stage_bytes + p.w_bytes, sf = x0 + p.x_bytes;
-            const Step st = step_of(p, t, o, k, low);
-            if (st.fp8) {
-                ptx::mbar_arrive_expect_tx(fb, boxes * box * 128u + (o.has1 ? 1536u : 1024u));
-                for (int i = 0; i < boxes; ++i)
-                    ptx::tma_load_2d(x0 + i * box * 128, map, fb, k * kBK, o.row0 + i * box);
-                ptx::bulk_load(sf, cx + (int64_t)k * 512, 512, fb);
-                ptx::bulk_load(sf + 512, c0 + k * step, pair ? 1024 : 512, fb);
-                if (o.has1 && !pair) ptx::bulk_load(sf + 1024, c1 + k * step, 512, fb);
-            } else if constexpr (LORA) {
+            ptx::mbar_arrive_expect_tx(fb, boxes * box * 128u + (o.has1 ? 1536u : 1024u));
+            for (int i = 0; i < boxes; ++i)
+                ptx::tma_load_2d(x0 + i * box * 128, map, fb, k * kBK, o.row0 + i * box);
+            ptx::bulk_load(sf, cx + (int64_t)k * 512, 512, fb);
+            ptx::bulk_load(sf + 512, c0 + k * step, pair ? 1024 : 512, fb);
+            if (o.has1 && !pair) ptx::bulk_load(sf + 1024, c1 + k * step, 512, fb);
+            r.next(p);
+        }
+        if constexpr (LORA) {
+            LowRank low;
+            if (o.l0 < o.l1) {
+                low.start(p, t, o);
                 if (!v_done) {  // every item of V
                     if (!wait_count(p, t, p.counters + 2, t.tab.items)) return;
                     fence_proxy_async_all();
                     v_done = true;
                 }
+            }
+            for (int l = o.l0; l < o.l1; ++l) {
+                const Step st = step_of(p, t.tab, o, low);
+                if (!wait_bar(ptx::smem_addr(&t.empty[r.stage]), r.phase ^ 1u, abort_flag, p, 4 * 256 + r.stage))
+                    return;
+                const uint32_t fb = ptx::smem_addr(&t.full[r.stage]);
+                const uint32_t x0 = sbase + r.stage * p.stage_bytes + p.w_bytes;
                 t.low[r.stage] = (uint32_t)(st.lo | st.n << 8 |
                                             (st.none ? 0 : (min(64, p.rank - st.c) + 15) / 16) << 16);
                 const int v0 = (o.g * p.slot_cap + st.slot) * p.halves;
@@ -685,8 +675,8 @@ __device__ __forceinline__ void load_tokens(const StreamParams &p, Tail<LORA> &t
                     for (int b = 0; b < p.halves; ++b)
                         for (int i = 0; i < st.n; i += 16)
                             ptx::tma_load_3d(x0 + (b * st.n + i) * 128, &p.V1, fb, st.c, st.lo + i, v0 + b);
+                r.next(p);
             }
-            r.next(p);
         }
     }
 }
@@ -701,11 +691,11 @@ __device__ __forceinline__ void copy_scales(const StreamParams &p, Tail<LORA> &t
     Queue q;
     Tile o;
     while (take<LORA, false>(p, t, q, o, 2))
-        for (int k = o.k0; k < o.k1; ++k) {
+        for (int i = o.l0 - o.l1 + o.k0 - o.k1, low = o.l0 - o.l1; i < 0; ++i) {
             if (!wait_bar(ptx::smem_addr(&t.full[r.stage]), r.phase, &t.abort_flag, p, 2 * 256 + r.stage))
                 return;
             ptx::tc_fence_after();
-            if (!LORA || k < p.ph[0].ks) {
+            if (!LORA || i < low) {
                 const uint32_t sf = sf_tmem + r.stage * kSfSlot;
                 const uint32_t cs = sbase + r.stage * p.stage_bytes + p.w_bytes + p.x_bytes;
                 ptx::tc_cp_32x128b_warpx4(sf, ptx::desc_sf_chunk(cs + 512));
@@ -758,11 +748,11 @@ __device__ __forceinline__ void issue_mmas(const StreamParams &p, Tail<LORA> &t,
         const int acc = acc_of(p, lt, par);
         if (!wait(&t.acce[acc], par ^ 1u, 256 + 64 + acc)) return;
         ptx::tc_fence_after();
-        const int k0 = uniform(o.k0), k1 = uniform(o.k1), n16 = uniform(o.n16), fp8 = p.ph[0].ks;
+        const int k0 = uniform(o.k0), k1 = uniform(o.k1), n16 = uniform(o.n16);
         const bool has1 = uniform(o.has1) != 0;
         const uint32_t d0 = tmem + acc * p.acc_cols, d1 = d0 + tile_cols;
         const uint32_t id8 = ptx::idesc_mxf8(128, 0, 0) | (uint32_t)(n16 >> 3) << 17 | p.w_fmt;
-        for (int k = k0; k < (LORA ? min(k1, fp8) : k1); ++k) {
+        for (int k = k0; k < k1; ++k) {
             if (!wait(&t.sfr[r.stage], r.phase, 256 + r.stage)) return;
             ptx::tc_fence_after();
             const uint32_t at = r.stage * stage16;
@@ -784,27 +774,26 @@ __device__ __forceinline__ void issue_mmas(const StreamParams &p, Tail<LORA> &t,
             r.next(p);
         }
         if constexpr (LORA) {
-            for (int k = max(k0, fp8); k < k1; ++k) {
+            for (int l = uniform(o.l1 - o.l0); l > 0; --l) {
                 if (!wait(&t.sfr[r.stage], r.phase, 256 + r.stage)) return;
                 ptx::tc_fence_after();
                 const int all = uniform((int)t.low[r.stage]);
                 const int lo = all & 255, n = all >> 8 & 255, nk = all >> 16;
-                const uint32_t first = k == k0 ? 0u : 1u;
                 const uint32_t id16 = ptx::idesc_bf16(128, 0) | (uint32_t)(n >> 3) << 17;
                 const uint32_t at = r.stage * stage16;
                 // the lo half: rows of its own after the hi ones, or columns 32-63;
                 // into the second accumulator
                 const uint64_t xh = x_desc + at, xl = xh + (p.halves == 2 ? n * 8 : 4);
-                const uint32_t dh = d0 + lo, dl = dh + odd, e = first | (p.chains == 1 ? 1u : 0u);
+                const uint32_t dh = d0 + lo, dl = dh + odd;
                 if (elect_one()) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         if (j >= nk) break;
                         const uint64_t w0 = w_desc + at + 2 * j, w1 = w0 + tile16;
-                        ptx::mma_bf16(dh, w0, xh + 2 * j, id16, j == 0 ? first : 1u);
-                        if (has1) ptx::mma_bf16(dh + tile_cols, w1, xh + 2 * j, id16, j == 0 ? first : 1u);
-                        ptx::mma_bf16(dl, w0, xl + 2 * j, id16, j == 0 ? e : 1u);
-                        if (has1) ptx::mma_bf16(dl + tile_cols, w1, xl + 2 * j, id16, j == 0 ? e : 1u);
+                        ptx::mma_bf16(dh, w0, xh + 2 * j, id16, 1u);
+                        if (has1) ptx::mma_bf16(dh + tile_cols, w1, xh + 2 * j, id16, 1u);
+                        ptx::mma_bf16(dl, w0, xl + 2 * j, id16, 1u);
+                        if (has1) ptx::mma_bf16(dl + tile_cols, w1, xl + 2 * j, id16, 1u);
                     }
                 }
                 if (elect_one()) ptx::tc_commit(ptx::smem_addr(&t.empty[r.stage]));
@@ -919,7 +908,8 @@ __device__ __forceinline__ void low_rank_item(const StreamParams &p, LoraTables 
     constexpr int kU = BF16 ? (FEW ? 6 : 4) : 2;
     auto go = [&](auto count, int s0) {
         constexpr int U = decltype(count)::value;
-        uint4 xa[U], xb[U], wa[U], wb[U], ya[U], yb[U];
+        uint4 xa[U], wa[U], wb[U];
+        [[maybe_unused]] uint4 xb[U], ya[U], yb[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int k = (s0 + u) * 32;
