@@ -218,3 +218,22 @@ def test_calls_on_several_streams():
     torch.cuda.synchronize()
     assert fp8g.fp8_gemm_status()[0] == 0
     assert all(torch.equal(g, w) for w, gs in zip(want, got) for g in gs)
+
+
+@pytest.mark.parametrize("M", [5, 100, 600])
+def test_non_finite_adapter_values_stay_with_its_rows(M):
+    """A and alpha of one adapter, a value of W: NaN in its rows, its column."""
+    p = Projection(M, 136, 160, 3, 8)
+    want = p.run()
+    p.a[1, 2, 7] = float("nan")
+    p.alpha[2] = float("inf")
+    got = p.run()
+    others = ((p.adapter != 1) & (p.adapter != 2)).cuda()
+    assert torch.equal(got[others], want[others])
+    hit = (p.adapter == 1) & (p.x[:, 7] != 0)
+    assert torch.isnan(got[hit.cuda()]).any(1).all()
+    p = Projection(M, 136, 160, 3, 8)
+    p.W[40, 3] = 0x7F  # NaN
+    got = p.run()
+    keep = torch.arange(136) != 40
+    assert torch.equal(got[:, keep.cuda()], want[:, keep.cuda()]) and torch.isnan(got[:, 40]).all()
