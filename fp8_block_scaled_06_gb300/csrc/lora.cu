@@ -382,7 +382,7 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
         p.x_bf16 = bf16;
         p.T = (int32_t)M;
         p.K = (int32_t)K;
-        p.idx = adapter;
+        p.idx = lora ? adapter : nullptr;
         p.n_idx = (int32_t)M;
         p.n_mat = L;
         p.xq = ws + o_xq;
@@ -401,7 +401,7 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
         p.alpha = alpha;
         p.bias = bias;
         p.v = ws + o_v;
-        p.rank = r;
+        p.rank = lora ? r : 0;  // 0: the kernels read no idx
         p.r64 = lv.r64;
         p.halves = lv.halves;
         p.slot_cap = cap;

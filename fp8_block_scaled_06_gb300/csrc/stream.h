@@ -72,7 +72,7 @@ struct StreamParams {
     const float *alpha;    // [L] or null
     const float *bias;     // [N] or null
     void *v;               // bf16 [group][slot_cap][halves * nb][r64]
-    int32_t rank, kr, r64, halves, slot_cap;  // kr 0: no adapters
+    int32_t rank, kr, r64, halves, slot_cap;  // rank and kr 0: no adapters, idx is null
     int32_t v_cols;  // token columns whose halves of V fit a stage
 };
 

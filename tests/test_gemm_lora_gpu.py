@@ -237,3 +237,17 @@ def test_non_finite_adapter_values_stay_with_its_rows(M):
     got = p.run()
     keep = torch.arange(136) != 40
     assert torch.equal(got[:, keep.cuda()], want[:, keep.cuda()]) and torch.isnan(got[:, 40]).all()
+
+
+@pytest.mark.parametrize("r", [0, 8, 16, 256, 300, -1])
+@pytest.mark.parametrize("M", [1, 40, 128, 129, 600])
+def test_no_adapters_null_pointers(M, r):
+    """With L = 0 lora_a, lora_b and adapter may be null, and r says nothing."""
+    p = Projection(M, 136, 160, 0, 8)
+    x, bias = p.x.bfloat16().cuda(), p.bias.cuda()
+    C = torch.full((M, 136), float("nan"), device="cuda")
+    fp8g.fp8_gemm_lora(x, fp8g.FP8G_IN_BF16, p.W, p.pw, p.fmt, None, None, None, None, 0, r, bias, C,
+                       fp8g.FP8G_OUT_F32, M, 136, 160)
+    assert fp8g.fp8_gemm_status()[0] == 0
+    ref, _ = p.reference(True, False)
+    assert torch.equal(C.cpu().double(), ref)
