@@ -552,7 +552,7 @@ _t = None  # torch, its dtypes
 def _names():
     global _t
     import torch
-    _t = (torch.empty, torch.bfloat16, torch.float32, torch.int32)
+    _t = (torch.empty, torch.bfloat16, torch.float32, torch.int32, torch.uint8)
     return _t
 
 
@@ -566,7 +566,7 @@ def moe_route(logits, k: int, score: int = FP8G_SCORE_SOFTMAX_TOPK, scale: float
     """fp32 or bf16 logits [T, E] -> (ids int32 [T, k], weights fp32 [T, k]), and
     with `ordered` also (counts [E], rows [T k], slots [T k]), the row order of the
     grouped GEMM (its counts, rows and c_row_of)."""
-    empty, bf16, f32, i32 = _t or _names()
+    empty, bf16, f32, i32, _ = _t or _names()
     dt, dev = logits.dtype, logits.device
     assert logits.is_cuda and (dt is f32 or dt is bf16)
     T, E = logits.shape
@@ -598,13 +598,16 @@ def moe_route(logits, k: int, score: int = FP8G_SCORE_SOFTMAX_TOPK, scale: float
 def moe_layer(x, ids, weights, W13, sf13, W2, sf2, w_fmt: int = FP8G_E4M3,
               gate: int = FP8G_GATE_SILU, out: str = "bf16", stream=None):
     """Mixture-of-experts layer of a few tokens: x fp32 or bf16 [T, H], ids and
-    weights [T, k] from moe_route, W13 [E, 2F, H] and W2 [E, H, F] codes of w_fmt,
-    sf13 / sf2 from pack_scales (sf13 of W13's scales viewed as [2E, F, H/32]).
-    Allocates the output [T, H]."""
-    empty, bf16, f32, i32 = _t or _names()
-    dt = x.dtype
-    assert x.is_cuda and (dt is bf16 or dt is f32)
-    assert ids.dtype is i32 and weights.dtype is f32
+    weights [T, k] from moe_route, W13 [E, 2F, H] and W2 [E, H, F] codes of w_fmt
+    (one-byte elements), sf13 / sf2 from pack_scales (sf13 of W13's scales viewed
+    as [2E, F, H/32]), all on x's device.  Allocates the output [T, H]."""
+    empty, bf16, f32, i32, u8 = _t or _names()
+    dt, dev = x.dtype, x.get_device()
+    assert dev >= 0 and (dt is bf16 or dt is f32)
+    assert ids.get_device() == dev and weights.get_device() == dev and W13.get_device() == dev
+    assert W2.get_device() == dev and sf13.get_device() == dev and sf2.get_device() == dev
+    assert ids.dtype is i32 and weights.dtype is f32 and W13.itemsize == 1 and W2.itemsize == 1
+    assert sf13.dtype is u8 and sf2.dtype is u8, "scales from pack_scales"
     T, H = x.shape
     t, k = ids.shape
     E, F2, c13 = W13.shape
@@ -629,20 +632,25 @@ def moe_layer(x, ids, weights, W13, sf13, W2, sf2, w_fmt: int = FP8G_E4M3,
 def gemm_lora(x, W, sfw, lora_a, lora_b, alpha, adapter, bias=None, w_fmt: int = FP8G_E4M3,
               out: str = "bf16", stream=None):
     """Projection with low-rank adapters: x fp32 or bf16 [M, K], W codes [N, K] of
-    w_fmt, sfw from pack_scales, lora_a bf16 [L, r, K], lora_b bf16 [L, N, r],
-    alpha fp32 [L] or None, adapter int32 [M] (negative: none), bias fp32 [N] or
-    None.  Allocates C [M, N]."""
-    empty, bf16, f32, i32 = _t or _names()
-    dt = x.dtype
-    assert x.is_cuda and (dt is bf16 or dt is f32)
-    assert lora_a.dtype is bf16 and lora_b.dtype is bf16 and adapter.dtype is i32
+    w_fmt (one-byte elements), sfw from pack_scales, lora_a bf16 [L, r, K], lora_b
+    bf16 [L, N, r], alpha fp32 [L] or None, adapter int32 [M] (negative: none),
+    bias fp32 [N] or None, all on x's device.  Allocates C [M, N]."""
+    empty, bf16, f32, i32, u8 = _t or _names()
+    dt, dev = x.dtype, x.get_device()
+    assert dev >= 0 and (dt is bf16 or dt is f32)
+    assert W.get_device() == dev and sfw.get_device() == dev and adapter.get_device() == dev
+    assert lora_a.get_device() == dev and lora_b.get_device() == dev
+    assert lora_a.dtype is bf16 and lora_b.dtype is bf16 and adapter.dtype is i32 and W.itemsize == 1
+    assert sfw.dtype is u8, "scales from pack_scales"
     M, K = x.shape
     N, cols = W.shape
     L, r, ka = lora_a.shape
     assert cols == packed_cols(K, w_fmt) and ka == K and lora_b.shape == (L, N, r)
     assert adapter.numel() == M and sfw.numel() == _packed_bytes(1, N, K)
-    assert alpha is None or alpha.dtype is f32 and alpha.numel() == L and alpha.is_contiguous()
-    assert bias is None or bias.dtype is f32 and bias.numel() == N and bias.is_contiguous()
+    assert alpha is None or (alpha.get_device() == dev and alpha.dtype is f32 and alpha.numel() == L
+                             and alpha.is_contiguous())
+    assert bias is None or (bias.get_device() == dev and bias.dtype is f32 and bias.numel() == N
+                            and bias.is_contiguous())
     assert W.is_contiguous() and sfw.is_contiguous()
     if not (x.is_contiguous() and adapter.is_contiguous() and lora_a.is_contiguous() and lora_b.is_contiguous()):
         x, adapter = _packed(x, stream), _packed(adapter, stream)
