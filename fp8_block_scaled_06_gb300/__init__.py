@@ -519,6 +519,13 @@ def gemm(A, B, sa, sb, out: str = "bf16", block: bool = True, stream=None):
     return C
 
 
+def _packed(x, stream):
+    """x, packed: a copy is made on the current stream and its memory is that
+    stream's, so a call on a `stream` of its own refuses to make one."""
+    assert stream is None, "with a stream of its own a call takes packed tensors"
+    return x.contiguous()
+
+
 def _packed_bytes(matrices: int, rows: int, K: int) -> int:
     """fp8g_packed_scale_bytes, without the call."""
     return matrices * (-(-rows // 128)) * (-(-K // 128)) * 512
@@ -530,7 +537,8 @@ def pack_scales(sf, stream=None):
     gemm_lora take (once per weight)."""
     import torch
     assert sf.is_cuda and sf.dtype == torch.float32 and sf.dim() in (2, 3)
-    sf = sf.contiguous()
+    if not sf.is_contiguous():
+        sf = _packed(sf, stream)
     rows, kb = sf.shape[-2:]
     lead = tuple(sf.shape[:-2])
     out = torch.empty(lead + (-(-kb // 4), -(-rows // 128), 512), dtype=torch.uint8,
@@ -542,9 +550,8 @@ def pack_scales(sf, stream=None):
 # The three below are called once a layer for a few tokens, where the host's time
 # is what a call costs: torch's names are looked up once, dtypes compared by
 # identity and the library's function called at once (on the GB300 host gemm_lora
-# takes 18.5 us of which the C call 8 to 12, 20.9 before).  A tensor that is not packed is
-# copied on the current stream, so with another `stream` it is refused; the
-# output is the current stream's memory.
+# takes 18.5 us of which the C call 8 to 12, 20.9 before).  The output is the
+# current stream's memory.
 
 _t = None  # torch, its dtypes
 
@@ -554,11 +561,6 @@ def _names():
     import torch
     _t = (torch.empty, torch.bfloat16, torch.float32, torch.int32, torch.uint8)
     return _t
-
-
-def _packed(x, stream):
-    assert stream is None, "with a stream of its own a call takes packed tensors"
-    return x.contiguous()
 
 
 def moe_route(logits, k: int, score: int = FP8G_SCORE_SOFTMAX_TOPK, scale: float = 1.0,

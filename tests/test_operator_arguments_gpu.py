@@ -86,3 +86,25 @@ def test_other_element_types(name, arg):
 def test_router_host_logits():
     with pytest.raises(AssertionError):
         fp8g.moe_route(torch.zeros((4, 8)), 2)
+
+
+def test_tensors_that_are_not_packed():
+    """Copied on the current stream; refused by a call on a stream of its own,
+    which would neither wait for the copy nor keep its memory."""
+    sf = 2.0 ** torch.arange(160 * 8, device="cuda").remainder(9).float().view(160, 8)
+    want = fp8g.pack_scales(sf)
+    turned = sf.t().contiguous().t()
+    assert not turned.is_contiguous() and torch.equal(fp8g.pack_scales(turned), want)
+    x = torch.zeros((128, 3), device="cuda").t()
+    calls = [lambda s: fp8g.pack_scales(turned, stream=s), lambda s: fp8g.moe_route(x[:, ::2], 2, stream=s),
+             lambda s: fp8g.moe_layer(**{**layer_args(), "x": x}, stream=s),
+             lambda s: fp8g.gemm_lora(**{**projection_args(), "x": x}, stream=s)]
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call in calls:
+        call(None)
+        with pytest.raises(AssertionError, match="packed"):
+            call(other)
+    got = fp8g.pack_scales(sf, stream=other)
+    other.synchronize()
+    assert torch.equal(got, want)
