@@ -68,6 +68,17 @@ __device__ __forceinline__ float rel_exp(float l, float top) {
     return l == top ? 1.0f : expf(l - top);
 }
 
+// 1 / (1 + exp(-l)) times exp(-m), m at most 0.  In the normalised sigmoid, with m
+// the largest chosen logit or 0, the factor cancels in the quotient and the largest
+// numerator is at least 1/2 however low the logits (with m = 0 all are 0 from -89
+// down, and so is their sum).  em: exp(m).
+__device__ __forceinline__ float sigmoid_over(float l, float m, float em) {
+    return 1.0f / (em + expf(m - l));
+}
+__device__ __forceinline__ float sigmoid_shift(int score, float top) {
+    return score == FP8G_SCORE_SIGMOID_NORM ? fminf(top, 0.0f) : 0.0f;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -133,8 +144,8 @@ __device__ __forceinline__ int route_token(const RouteArgs &a, int t, int lane) 
     }
     float w = 0.0f;
     if (mine >= 0) {
-        const float l = key_value(mine_key);
-        w = a.score <= FP8G_SCORE_SOFTMAX_TOPK ? rel_exp(l, key_value(all)) : 1.0f / (1.0f + expf(-l));
+        const float l = key_value(mine_key), top = key_value(all), m = sigmoid_shift(a.score, top);
+        w = a.score <= FP8G_SCORE_SOFTMAX_TOPK ? rel_exp(l, top) : sigmoid_over(l, m, m < 0.0f ? expf(m) : 1.0f);
     }
     if (a.score == FP8G_SCORE_SOFTMAX_TOPK || a.score == FP8G_SCORE_SIGMOID_NORM) sum = warp_sum(w);
     if (lane < a.k) {
@@ -259,6 +270,7 @@ __device__ __forceinline__ void route_quad(const RouteArgs &a, int t, int q, uin
         for (int i = 0; i < NE; ++i)
             if (key[i] != 0u) sum += rel_exp(key_value(key[i]), top);
     }
+    const float m = sigmoid_shift(a.score, top), em = m < 0.0f ? expf(m) : 1.0f;
     float w[K / 4];
     uint64_t mine[K / 4];
 #pragma unroll
@@ -269,7 +281,7 @@ __device__ __forceinline__ void route_quad(const RouteArgs &a, int t, int q, uin
         w[j] = 0.0f;
         if (kj != 0u)
             w[j] = a.score <= FP8G_SCORE_SOFTMAX_TOPK ? rel_exp(key_value(kj), top)
-                                                      : 1.0f / (1.0f + expf(-key_value(kj)));
+                                                      : sigmoid_over(key_value(kj), m, em);
         if (a.score == FP8G_SCORE_SOFTMAX_TOPK || a.score == FP8G_SCORE_SIGMOID_NORM) sum += w[j];
     }
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);

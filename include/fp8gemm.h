@@ -506,7 +506,8 @@ FP8G_API fp8g_status fp8g_pack_scales(const float *sf, int64_t matrices, int64_t
 /*
  * Weight of a chosen expert from its logit: softmax over every expert of the
  * token, softmax over the chosen ones, the sigmoid, the sigmoid divided by the
- * sum of the chosen ones' sigmoids.
+ * sum of the chosen ones' sigmoids (for logits so low that fp32 has no sigmoid of
+ * them, too: there the quotient is that of their exponentials).
  */
 typedef enum {
     FP8G_SCORE_SOFTMAX = 0,

@@ -124,3 +124,31 @@ def test_other_stream_and_graph():
     buf.copy_(x)
     graph.replay()
     assert all(torch.equal(p, q) for p, q in zip(want, got))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,k", [(8, 2), (24, 6), (64, 16), (100, 6), (256, 16)])  # both ways of choosing
+def test_normalised_sigmoid_of_low_logits(E, k, dtype):
+    """Logits whose sigmoid is 0 in fp32: the quotient of the sigmoids stays that of
+    the definition, in 64 bits and in logarithms."""
+    gen = torch.Generator().manual_seed(E)
+    spread = torch.rand((10, E), generator=gen) * 6
+    spread[9] *= 15  # some chosen ones have a sigmoid, some none
+    low = torch.tensor([-80.0, -88.7, -89.0, -100.0, -1e4, -1e9, 0.0, 60.0, -3.0, -30.0])[:, None]
+    x = low - spread
+    x = torch.cat([x, torch.full((1, E), torch.finfo(dtype).min), torch.full((1, E), -1e4), x[:1], x[3:4]])
+    x[-2, 1:] = -120.0  # one that has a sigmoid, the others none
+    x[-1, 2] = INF      # and +inf
+    x = x.to(dtype)
+    ids, w = fp8g.moe_route(x.cuda(), k, 3, 1.5)
+    assert fp8g.fp8_gemm_status()[0] == 0
+    v, i = torch.sort(x.double(), dim=1, descending=True, stable=True)
+    v, i = v[:, :k], i[:, :k]
+    want = 1.5 * torch.softmax(torch.nn.functional.logsigmoid(v), 1)
+    assert torch.equal(ids.cpu(), i.int())
+    # two exponentials, a difference of logits (exact where the quotient is not
+    # small; else within 2^-24 of it, which the exponential turns into that much
+    # of itself), two divisions, k additions, a product
+    tol = (k + 16 + 256) * 2.0 ** -23 * want + 2.0 ** -126
+    assert ((w.cpu().double() - want).abs() <= tol).all()
+    assert ((w.sum(1) - 1.5).abs() <= (2 * k + 16) * 2.0 ** -23 * 1.5).all()
