@@ -53,6 +53,7 @@
 
 #include "internal.h"
 #include "kernel_common.cuh"
+#include "lora_value.cuh"
 #include "ptx.cuh"
 
 namespace fp8g {
@@ -172,6 +173,49 @@ __device__ __forceinline__ PairTile pair_tile(int32_t t, const GemmParams &p, co
         ti.rtA0 = 2 * ti.pm;
     }
     return ti;
+}
+
+// The NaN among columns ncol0 .. ncol0 + 63 of C of a warp's rows, lane: row `row`
+// (-1: none), computed again (lora_value.cuh).
+template <bool OUT_F32>
+__device__ __noinline__ void pair_again(const GemmParams &p, const PairLora &l, int64_t row, int64_t ncol0) {
+    const int lane = threadIdx.x & 31;
+    const int64_t tile = __shfl_sync(0xffffffffu, row, 0) / 256;  // (a warp's first row exists where one does)
+    const int slots = __ldcg(l.slots + tile), mine = row < 0 ? -1 : __ldg(l.row_adapter + row);
+    int slot = 0;
+    while (slot < slots && __ldcg(l.adapters + tile * l.cap + slot) != mine) ++slot;
+    LoraValue v;
+    v.K = (int32_t)p.K;
+    v.fmt = l.fmt;
+    v.sfx_step = (int64_t)p.n_rtA * 512;
+    v.sfw_step = (int64_t)p.n_rtB * 512;
+    v.half = l.halves == 2 ? (int64_t)256 * l.r64 : 32;
+    for (int64_t n = ncol0; n < min(ncol0 + kCW, p.N); ++n) {
+        const int64_t at = row * p.N + n;
+        float *out = static_cast<float *>(p.C) + at;
+        __nv_bfloat16 *out16 = static_cast<__nv_bfloat16 *>(p.C) + at;
+        bool bad = false;
+        if (row >= 0) bad = isnan(OUT_F32 ? *out : __bfloat162float(*out16));
+        v.w = l.w + n * (p.K / 8 * (8 - p.b_gap8));
+        v.sfw = p.sfb_pk + n / 128 * 512 + scale_byte(n);
+        for (uint32_t m = __ballot_sync(0xffffffffu, bad); m != 0; m &= m - 1) {
+            const int src = __ffs((int)m) - 1;
+            const int64_t rs = __shfl_sync(0xffffffffu, row, src);
+            const int s = __shfl_sync(0xffffffffu, slot, src), ad = __shfl_sync(0xffffffffu, mine, src);
+            v.rank = s < slots ? l.rank : 0;
+            v.x = l.x + rs * p.K;
+            v.sfx = p.sfa_pk + rs / 128 * 512 + scale_byte(rs);
+            v.v = static_cast<const __nv_bfloat16 *>(l.v) +
+                  ((tile * l.cap + s) * l.halves * 256 + (rs & 255)) * l.r64;
+            v.b = static_cast<const __nv_bfloat16 *>(l.b) + (s < slots ? (ad * p.N + n) * l.rank : 0);
+            const float x = epi1(lora_value(v), p.bias, p.act, n);
+            if (lane != src) continue;
+            if (OUT_F32)
+                *out = x;
+            else
+                *out16 = __float2bfloat16_rn(x);
+        }
+    }
 }
 
 // The low-rank steps of kernels that have them (LORA), nothing for the others.
@@ -598,6 +642,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < kCW / 32; ++c)
                     store_row32<OUT_F32>(p.C, row, p.N, ncol0 + c * 32, r[c], a_t, p.st32 != 0);
+            }
+            if constexpr (LORA) {
+                bool has_nan = false;
+#pragma unroll
+                for (int c = 0; c < kCW / 32; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) has_nan |= isnan(__uint_as_float(r[c][i]));
+                if (__any_sync(0xffffffffu, has_nan && row >= 0) && __ldcg(la.p.slots + ti.pm) > 0)
+                    pair_again<OUT_F32>(p, la.p, row, ncol0);
             }
         }
     }

@@ -113,6 +113,11 @@ struct PairLora {
     const int32_t *slots;     // [row tile]
     const int32_t *adapters;  // [row tile][cap]
     int32_t cap, rank, kr, halves;
+    // what a value next to a B that is not finite is computed again from (lora_value.cuh)
+    int32_t r64, L, fmt;
+    const int32_t *row_adapter;  // [M]
+    const uint8_t *x, *w;        // codes
+    const void *v, *b;           // what V and B map
 };
 
 // gemm_pair.cu (per-tensor and block-scaled, CTA pairs); lora: block-scaled only

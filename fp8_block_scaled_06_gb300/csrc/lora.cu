@@ -397,6 +397,9 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
         p.B = mb;
         p.V = mv;
         p.V1 = mv1;
+        p.w = static_cast<const uint8_t *>(W);
+        p.b = lora_b;
+        p.fmt = w_fmt;
         p.a = lora_a;
         p.alpha = alpha;
         p.bias = bias;
@@ -450,6 +453,14 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
             pl.rank = r;
             pl.kr = lv.kr;
             pl.halves = lv.halves;
+            pl.r64 = lv.r64;
+            pl.L = L;
+            pl.fmt = w_fmt;
+            pl.row_adapter = adapter;
+            pl.x = a.xq;
+            pl.w = static_cast<const uint8_t *>(W);
+            pl.v = a.v;
+            pl.b = lora_b;
         }
         if (e == cudaSuccess)
             st = run_pair_packed(a.xq, a.xsf, W, sfw, w_fmt, bias, C, out, M, N, K, lora ? &pl : nullptr, stream);

@@ -31,9 +31,10 @@
 // adapter among the group's tokens, bf16 steps (kind::f16) of the adapter's B
 // rows against both halves of V, into the same fp32 accumulator; a step covers
 // the 16-column windows that hold the adapter's tokens (V is zero in the others'
-// columns, so B has to be finite).  B comes through the ring as the weights do:
-// read through L1, of which 20 KB are left beside the ring, into registers for
-// mma.sync, the same term took 128 rows of 32 adapters of rank 64 from 48 to 66 us.
+// columns; lora_value.cuh has what follows for a B that is not finite).  B comes
+// through the ring as the weights do: read through L1, of which 20 KB are left
+// beside the ring, into registers for mma.sync, the same term took 128 rows of 32
+// adapters of rank 64 from 48 to 66 us.
 //
 // Measured, per call on the device back to back, beside the bytes at 6.78 TB/s:
 // one token, two experts of 4096 x 14336, 67 us (54); 5 tokens over 64 experts of
@@ -57,6 +58,7 @@
 #include <type_traits>
 
 #include "kernel_common.cuh"
+#include "lora_value.cuh"
 #include "quant_math.cuh"
 #include "stream.h"
 
@@ -1010,11 +1012,13 @@ __device__ __forceinline__ float gate_act(float g, int gate) {
 // kCols columns of a finished tile: v[s][i] is this lane's weight row f of weight
 // tile s, token column c + i.  (Plain stores go on with all columns and leave out
 // those past the group, so that their latencies overlap; the layer's, mostly of
-// a column or two, end at the last one.)
+// a column or two, end at the last one.)  spoilt (kOut): set where an
+// adapter's B is not finite: no value of its windows is then, so the first of the
+// kCols columns tells (a comparison for each took 512 rows from 112.0 to 114.8 us).
 template <bool LORA, int EPI, int SUBS>
 __device__ __forceinline__ void store_cols(const StreamParams &p, const StreamPhase &h, const Tail<LORA> &t,
                                            const Tile &o, int c, int c_hi, int f, int q, int lane, float bias,
-                                           const float (&v)[SUBS][kCols]) {
+                                           const float (&v)[SUBS][kCols], bool &spoilt) {
     if constexpr (EPI != kOut) {
 #pragma unroll
         for (int i = 0; i < kCols; ++i) {
@@ -1039,6 +1043,7 @@ __device__ __forceinline__ void store_cols(const StreamParams &p, const StreamPh
             }
         }
     } else {
+        spoilt |= !isfinite(v[0][0]);
         int row[kCols];
 #pragma unroll
         for (int i = 0; i < kCols; ++i) row[i] = c + i < c_hi ? t.tab.row_of[o.row0 + c + i] : 0;
@@ -1053,6 +1058,53 @@ __device__ __forceinline__ void store_cols(const StreamParams &p, const StreamPh
                 static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(x);
         }
     }
+}
+
+// The NaN among a warp's values of a tile, lane: feature f, computed again
+// (lora_value.cuh); columns as finish_tile takes them.  (Arguments by value: a Tile
+// by reference would live in memory, 0.5 us a call.)
+__device__ __noinline__ void again(const StreamParams &p, Tail<true> &t, int g, int f, int c_first, int c_step) {
+    const StreamPhase &h = p.ph[0];
+    const int lane = threadIdx.x & 31, slots = t.tab.n[g], row0 = g * p.nb, n = min(p.nb, p.T - row0);
+    if (slots == 0) return;
+    // V as other SMs wrote it
+    if (!__all_sync(0xffffffffu, wait_count(p, t, p.counters + 2, t.tab.items))) return;
+    LoraValue v;
+    v.K = p.K;
+    v.fmt = p.fmt;
+    v.sfx_step = 512;
+    v.sfw_step = (int64_t)h.n_rt * 512;
+    v.half = p.halves == 2 ? (int64_t)p.nb * p.r64 : 32;
+    for (int c = c_first; c < n; c += c_step)
+        for (int col = c; col < min(n, c + kCols); ++col) {
+            const int64_t at = (int64_t)t.tab.row_of[row0 + col] * h.rows + f;
+            float *out = static_cast<float *>(p.out) + at;
+            __nv_bfloat16 *out16 = static_cast<__nv_bfloat16 *>(p.out) + at;
+            bool bad = false;
+            if (f < h.rows) bad = isnan(p.out_f32 ? *out : __bfloat162float(*out16));
+            int s = 0;
+            while (s < slots && col >= t.tab.first[g][s + 1]) ++s;
+            v.rank = s < slots ? p.rank : 0;
+            v.x = p.xq + (int64_t)(row0 + col) * p.K;
+            v.sfx = h.sfx + (int64_t)g * h.ks * 512 + scale_byte(col);
+            v.v = static_cast<const __nv_bfloat16 *>(p.v) +
+                  ((int64_t)(g * p.slot_cap + s) * p.halves * p.nb + col) * p.r64;
+            for (uint32_t m = __ballot_sync(0xffffffffu, bad); m != 0; m &= m - 1) {
+                const int src = __ffs((int)m) - 1;
+                const int64_t fs = f - lane + src;
+                v.w = p.w + fs * (p.K / 8 * (8 - p.gap8));
+                v.sfw = h.sfw + fs / 128 * 512 + scale_byte(fs);
+                v.b = static_cast<const __nv_bfloat16 *>(p.b) +
+                      (s < slots ? (t.tab.adapter[g][s] * (int64_t)h.rows + fs) * p.rank : 0);
+                float x = lora_value(v);
+                if (p.bias != nullptr) x = __fadd_rn(x, __ldg(p.bias + fs));
+                if (lane != src) continue;
+                if (p.out_f32)
+                    *out = x;
+                else
+                    *out16 = __float2bfloat16_rn(x);
+            }
+        }
 }
 
 // out[t, h] = sum_j w[t, j] y[pos[t, j], h] of one tile of h, j in order; four
@@ -1182,7 +1234,7 @@ __device__ __forceinline__ void finish_tile(const StreamParams &p, Tail<LORA> &t
     const float bias = EPI == kOut && p.bias != nullptr && f < h.rows ? __ldg(p.bias + f) : 0.0f;
     const int64_t part_size = (int64_t)2 * p.nb * 128;
     float *part0 = h.part + (int64_t)o.tile * parts * part_size;  // the tile's parts
-    bool last = true;
+    bool last = true, spoilt = false;
     if (parts > 1) {
         float *part = part0 + o.part * part_size;
         if (live)
@@ -1236,7 +1288,7 @@ __device__ __forceinline__ void finish_tile(const StreamParams &p, Tail<LORA> &t
                     }
                 }
             }
-            store_cols<LORA, EPI, kSubs>(p, h, t, o, c, o.n, f, q, lane, bias, v);
+            store_cols<LORA, EPI, kSubs>(p, h, t, o, c, o.n, f, q, lane, bias, v, spoilt);
         }
     if (parts == 1) {
         ptx::tc_fence_before();
@@ -1252,6 +1304,8 @@ __device__ __forceinline__ void finish_tile(const StreamParams &p, Tail<LORA> &t
     } else if constexpr (EPI == kRows) {
         // the last group to finish this tile of h sums the tokens' experts
         if (count_in(t, p.done_tile + o.mt, t.tab.n_groups)) combine(p, t, o);
+    } else {
+        if (__any_sync(0xffffffffu, spoilt)) again(p, t, o.g, f, c_first, c_step);
     }
 }
 

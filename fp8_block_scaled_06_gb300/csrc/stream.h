@@ -68,6 +68,9 @@ struct StreamParams {
     float *y;              // [T k][H]
     // adapters
     CUtensorMap B, V, V1;  // V: boxes of 16 rows of all halves, of one
+    const uint8_t *w;      // what B and ph[0].W map
+    const void *b;
+    int32_t fmt;           // of the weights
     const void *a;         // bf16 [L][rank][K]
     const float *alpha;    // [L] or null
     const float *bias;     // [N] or null

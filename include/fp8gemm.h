@@ -593,8 +593,10 @@ FP8G_API fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t
  * (lora_a, lora_b, adapter unused, may be null); M may be 0.  x, W (packed
  * formats 32), sfw, lora_a, lora_b, C 16-byte aligned, N * sizeof(out element)
  * % 16 == 0, else FP8G_ERR_ALIGNMENT.  Results do not vary between runs.
- * lora_b is finite: an infinity or NaN in an adapter's B can reach rows of other
- * adapters as NaN (in W, A, alpha and x they stay with their own column or rows).
+ * Infinities and NaN stay with their own rows (x; an adapter's A, B and alpha) or
+ * column (W, bias): of an adapter's B that is not finite, every other row has the
+ * value that it has without.  Those values are computed one by one, up to some
+ * hundred times the call's time where a whole B is NaN.
  * Two kernels for few rows (up to 128, with many adapters 512), else three (two
  * without adapters), and one temporary from the library's pool: M K bytes, 4 M
  * min(L, 256) max(r, 64) for A x, for few rows also up to 20 MB of partial sums.

@@ -251,3 +251,70 @@ def test_no_adapters_null_pointers(M, r):
     assert fp8g.fp8_gemm_status()[0] == 0
     ref, _ = p.reference(True, False)
     assert torch.equal(C.cpu().double(), ref)
+
+
+def poisoned(M, N, K, L, r, at, fmt=fp8g.FP8G_E4M3, runs=None):
+    p = Projection(M, N, K, L, r, fmt, runs=runs)
+    nan, inf = float("nan"), float("inf")
+    if at == "all":
+        p.b[1] = inf
+    elif at == "some":
+        p.b[1, 3, 0], p.b[1, N - 1, r - 1], p.b[0, 5, 2], p.b[0, N // 2] = nan, -inf, inf, nan
+    else:  # a column of NaN in every adapter but the last
+        p.b[:-1, :, r // 2] = nan
+    return p
+
+
+def check_poisoned(p):
+    ref, _ = p.reference(True, True)
+    clean = torch.isfinite(p.b).all(2)  # [L, N]
+    own = torch.ones_like(ref, dtype=torch.bool)  # outputs whose own row of B is finite
+    for l in range(p.L):
+        own[p.adapter == l] = clean[l]
+    assert torch.isfinite(ref[own]).all()
+    for out, bf16 in (("f32", True), ("bf16", False)):
+        got = p.run(out, bf16=bf16).cpu()
+        assert fp8g.fp8_gemm_status()[0] == 0
+        want = ref if out == "f32" else ref.float().bfloat16()
+        torch.testing.assert_close(got.to(want.dtype), want, rtol=0, atol=0, equal_nan=True)
+
+
+@pytest.mark.parametrize("at", ["all", "some", "column"])
+@pytest.mark.parametrize("M,N,K,L,r,runs", [
+    (5, 136, 160, 3, 8, None), (33, 264, 416, 16, 16, None), (100, 136, 96, 4, 72, None),
+    (128, 520, 160, 32, 64, None), (300, 136, 1056, 2, 8, None), (400, 136, 96, 40, 40, None),
+    (600, 264, 160, 3, 8, None), (700, 136, 96, 5, 136, 9), (1, 128, 6144, 2, 8, None),
+    (20, 136, 5120, 5, 136, None)])
+def test_non_finite_b_stays_with_its_rows(M, N, K, L, r, runs, at):
+    """Every output is that of the definition: other adapters' rows, rows without an
+    adapter and features whose row of B is finite have their values, the others the
+    infinity or NaN that they sum to."""
+    p = poisoned(M, N, K, L, r, at, runs=runs)
+    p.adapter[0] = 1  # some row has a poisoned adapter
+    check_poisoned(p)
+
+
+@pytest.mark.parametrize("M", [20, 600])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_non_finite_b_formats(M, fmt):
+    p = poisoned(M, 264, 256, 3, 16, "all", fmt)
+    p.adapter[:3] = torch.tensor([0, 1, -1], dtype=torch.int32)
+    check_poisoned(p)
+
+
+@pytest.mark.parametrize("M", [24, 600])
+def test_non_finite_b_beside_other_nan(M):
+    """A NaN of x, of W or of its scales is left where it is."""
+    p = poisoned(M, 136, 160, 3, 8, "all")
+    p.adapter[:4] = torch.tensor([1, 0, 2, -1], dtype=torch.int32)
+    ref, _ = p.reference(True, True)
+    p.x[1, 3] = float("nan")
+    p.x[3, 8] = float("nan")
+    p.W[40, 3] = 0x7F
+    p.pw.view(2, 2, 512)[0, 0, 16 * 9] = 255  # the scale of feature 9, first block
+    got = p.run().cpu().double()
+    assert torch.isnan(got[[1, 3]]).all() and torch.isnan(got[:, [9, 40]]).all()
+    rows, cols = torch.ones(M, dtype=torch.bool), torch.ones(136, dtype=torch.bool)
+    rows[[1, 3]] = False
+    cols[[9, 40]] = False
+    torch.testing.assert_close(got[rows][:, cols], ref[rows][:, cols], rtol=0, atol=0, equal_nan=True)
