@@ -13,7 +13,8 @@ OBJ_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(HERE, "libfp8g.so")
 SOURCES = ["gemm.cu", "gemm_pair.cu", "gemm_promote.cu", "scales.cu", "quant.cu", "api.cu",
            "noalloc.cu", "selftest.cu", "route.cu", "stream.cu", "moe.cu", "lora.cu"]
-HEADERS = ["ptx.cuh", "internal.h", "kernel_common.cuh", "quant_math.cuh", "stream.h", "lora_value.cuh"]
+HEADERS = ["ptx.cuh", "internal.h", "kernel_common.cuh", "quant_math.cuh", "stream.h", "lora_value.cuh",
+           "lora_pieces.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -55,6 +55,7 @@
 #include "kernel_common.cuh"
 #include "lora_value.cuh"
 #include "ptx.cuh"
+#include "stream.h"
 
 namespace fp8g {
 
@@ -189,7 +190,9 @@ __device__ __noinline__ void pair_again(const GemmParams &p, const PairLora &l, 
     v.fmt = l.fmt;
     v.sfx_step = (int64_t)p.n_rtA * 512;
     v.sfw_step = (int64_t)p.n_rtB * 512;
-    v.half = l.halves == 2 ? (int64_t)256 * l.r64 : 32;
+    v.pieces = l.pieces;
+    v.per = l.per;
+    v.block = (int64_t)256 * l.r64;
     for (int64_t n = ncol0; n < min(ncol0 + kCW, p.N); ++n) {
         const int64_t at = row * p.N + n;
         float *out = static_cast<float *>(p.C) + at;
@@ -206,7 +209,7 @@ __device__ __noinline__ void pair_again(const GemmParams &p, const PairLora &l, 
             v.x = l.x + rs * p.K;
             v.sfx = p.sfa_pk + rs / 128 * 512 + scale_byte(rs);
             v.v = static_cast<const __nv_bfloat16 *>(l.v) +
-                  ((tile * l.cap + s) * l.halves * 256 + (rs & 255)) * l.r64;
+                  ((tile * l.cap + s) * l.blocks * 256 + (rs & 255)) * l.r64;
             v.b = static_cast<const __nv_bfloat16 *>(l.b) + (s < slots ? (ad * p.N + n) * l.rank : 0);
             const float x = epi1(lora_value(v), p.bias, p.act, n);
             if (lane != src) continue;
@@ -235,8 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     using PC = PairCfg<MODE, F4>;
     static_assert(!LORA || (MODE == kModeBlock && F4 == 0), "low-rank steps: block-scaled FP8-rate");
     // Low-rank steps of a tile, after its num_kb FP8 steps, in loops of their own:
-    // halves * kr per slot; of a 64-wide step's two halves of V (halves 2) the hi
-    // one first.  Each role asks for a tile's number of slots a tile ahead (asked
+    // blocks * kr per slot, the blocks of V's pieces of 64 ranks one after the other.  Each role asks for a tile's number of slots a tile ahead (asked
     // for at the tile, and with the two kinds of step in one loop, a tile took 2 us
     // more even without slots).
     auto lora_slots = [&](const int32_t t) -> int {
@@ -409,14 +411,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int slot = ti.pm * la.p.cap + sl, adapter = adapter_next;
                         if (sl + 1 < slots) adapter_next = __ldcg(la.p.adapters + slot + 1);
                         for (int c = 0; c < la.p.kr * 64; c += 64)
-                            for (int h = 0; h < la.p.halves; ++h) {
+                            for (int h = 0; h < la.p.blocks; ++h) {
                                 if (!wait_bar(bar_empty(stage), phase ^ 1u, abort_flag, p, 0 * 256 + stage))
                                     goto roles_done;
                                 const uint32_t fb =
                                     leader ? bar_full(stage) : ptx::map_shared(bar_full(stage), 0);
                                 if (leader) ptx::mbar_arrive_expect_tx(fb, 2 * (kA + kB));
                                 ptx::tma_load_2d_pair(sbase + PC::OFF_A + stage * kA, &la.p.V, fb, c,
-                                                      (la.p.halves * slot + h) * 256 + (int32_t)rank * kBM);
+                                                      (la.p.blocks * slot + h) * 256 + (int32_t)rank * kBM);
                                 ptx::tma_load_3d_pair(sbase + PC::OFF_B + stage * kB, &la.p.B, fb, c, nb0,
                                                       adapter);
                                 if (++stage == PC::STAGES) {
@@ -509,19 +511,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (LORA) {
                     for (int sl = 0; sl < slots; ++sl)
                         for (int c = 0; c < la.p.kr * 64; c += 64)
-                            for (int h = 0; h < la.p.halves; ++h) {
+                            for (int h = 0; h < la.p.blocks; ++h) {
                                 if (!wait_bar(bar_sfr(stage), phase, abort_flag, p, 1 * 256 + stage))
                                     goto roles_done;
                                 ptx::tc_fence_after();
                                 const uint32_t a0 = sbase + PC::OFF_A + stage * kA;
                                 const uint32_t b0 = sbase + PC::OFF_B + stage * kB;
                                 const int nk = (min(64, la.p.rank - c) + 15) / 16;
-                                // both halves in a row (halves 1): the lo one 64 bytes
-                                // on, against the same rows
-                                for (int o = 0; o < 3 - la.p.halves; ++o)
+                                // the block's pieces side by side, against the same rows
+                                // (two in all for a bf16 output, three for fp32: LoraV)
+                                const int pieces = OUT_F32 ? min(la.p.per, 3 - h * la.p.per) : 3 - la.p.blocks;
+                                const uint32_t apart = OUT_F32 && la.p.per == 3 ? 32 : 64;
+                                for (int o = 0; o < pieces; ++o)
                                     for (int k = 0; k < nk; ++k)
                                         ptx::mma_bf16_pair(d_tmem,
-                                                           ptx::desc_kmajor_sw128(a0 + o * 64 + k * 32),
+                                                           ptx::desc_kmajor_sw128(a0 + o * apart + k * 32),
                                                            ptx::desc_kmajor_sw128(b0 + k * 32),
                                                            ptx::idesc_bf16(2 * kBM, kPairBN), 1u);
                                 ptx::tc_commit_pair_mc(bar_empty(stage), 0x3);
@@ -578,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if constexpr (LORA) {  // no scales: pass the stages on
-                    for (int ls = slots * la.p.kr * la.p.halves; ls > 0; --ls) {
+                    for (int ls = slots * la.p.kr * la.p.blocks; ls > 0; --ls) {
                         if (!wait_bar(bar_full(stage), phase, abort_flag, p, 2 * 256 + stage)) goto roles_done;
                         ptx::tc_fence_after();
                         ptx::tc_commit_pair_mc(bar_sfr(stage), 0x1);

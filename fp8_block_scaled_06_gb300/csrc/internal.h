@@ -105,14 +105,14 @@ cudaError_t launch_gemm_promote(bool out_f32, const GemmMaps &maps, const GemmPa
                                 cudaStream_t stream);
 
 // Low-rank steps of the block-scaled CTA-pair kernel: after a tile's FP8 steps,
-// halves * kr bf16 steps per slot of its 256 rows (V against the adapter's
-// rows; lora.cu).  halves 1: both halves of V in a row (LoraV in stream.h).
+// blocks * kr bf16 steps per slot of its 256 rows (V against the adapter's
+// rows; lora.cu; LoraV in stream.h).
 struct PairLora {
-    CUtensorMap V;  // bf16 rows: block h of row i of slot s of row tile t at ((t cap + s) halves + h) 256 + i
+    CUtensorMap V;  // bf16 rows: block b of row i of slot s of row tile t at ((t cap + s) blocks + b) 256 + i
     CUtensorMap B;  // bf16 [adapter][N][rank]
     const int32_t *slots;     // [row tile]
     const int32_t *adapters;  // [row tile][cap]
-    int32_t cap, rank, kr, halves;
+    int32_t cap, rank, kr, pieces, per, blocks;
     // what a value next to a B that is not finite is computed again from (lora_value.cuh)
     int32_t r64, L, fmt;
     const int32_t *row_adapter;  // [M]

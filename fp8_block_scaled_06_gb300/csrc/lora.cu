@@ -10,7 +10,7 @@
 // V.  Rows are taken in tiles (a group of the streaming kernel, or the 256 rows
 // of a pair).  The adapters among a tile's rows, in rising order,
 // are its slots; a slot holds V of all the tile's rows, zero for those of
-// other adapters, as two bf16 halves (V = hi + lo to 16 bits): the product
+// other adapters, as two or three bf16 pieces (lora_pieces.cuh): the product
 // then needs no gather, and an adapter costs rank / 128 of a K step's weights.
 #include <cuda_bf16.h>
 
@@ -18,6 +18,7 @@
 
 #include "internal.h"
 #include "kernel_common.cuh"
+#include "lora_pieces.cuh"
 #include "quant_math.cuh"
 #include "stream.h"
 
@@ -39,47 +40,13 @@ struct LoraPrep {
     const __nv_bfloat16 *a;   // [L][r][K]
     const float *alpha;       // [L] or null
     const int32_t *adapter;   // [M]
-    int32_t L, r, r64, wide;  // LoraV: V's row length, halves in rows of their own
+    int32_t L, r, r64, per, blocks;  // LoraV
     int32_t tile, cap, tiles;  // tiles 0: no adapters
-    __nv_bfloat16 *v;         // [tiles][cap][halves][tile][r64]
+    __nv_bfloat16 *v;         // [tiles][cap][blocks][tile][r64]
     int32_t *slot_cnt, *slot_adapter;  // the pair kernel's tables
     int32_t items;            // blocks per tile and rank block of V
     unsigned int *status;
 };
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t *>(&b);
-}
-
-// What rounding to bf16 leaves of v (of an infinity, or a v rounded to one: nothing).
-__device__ __forceinline__ float bf16_rest(float v) {
-    const float h = __bfloat162float(__float2bfloat16_rn(v));
-    return isinf(h) ? 0.0f : v - h;
-}
-
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// 8 consecutive values of x as bf16 pairs; of fp32 x the rounded values (hi) and
-// what they leave, rounded (lo): 16 significant bits in two halves.
-template <bool BF16>
-__device__ __forceinline__ void x_pairs(const void *x, int64_t off, uint4 &hi, uint4 &lo) {
-    if constexpr (BF16) {
-        hi = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(x) + off));
-    } else {
-        float4 a, b;
-        load8<false>(x, off, a, b);
-        hi = make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
-        lo = make_uint4(pack_bf16(bf16_rest(a.x), bf16_rest(a.y)), pack_bf16(bf16_rest(a.z), bf16_rest(a.w)),
-                        pack_bf16(bf16_rest(b.x), bf16_rest(b.y)), pack_bf16(bf16_rest(b.z), bf16_rest(b.w)));
-    }
-}
 
 // Row blockIdx.x of x: codes, scale bytes.  Behind lora_v_kernel, it starts beside
 // it (that one began only when all before it was complete, and nothing of it is
@@ -116,7 +83,7 @@ __global__ void __launch_bounds__(256) lora_quant_kernel(const __grid_constant__
 // consecutive K of a row; the same K permutation on both operands leaves the
 // product unchanged.  Rows and ranks past the item's read others' values, into
 // products that are not stored.
-template <bool BF16>
+template <int P, bool BF16>
 __global__ void __launch_bounds__(kLThreads, 2) lora_v_kernel(const __grid_constant__ LoraPrep p) {
     __shared__ int32_t ad[kMaxTile];
     __shared__ int32_t cnt[FP8G_MAX_ADAPTERS];
@@ -190,18 +157,15 @@ __global__ void __launch_bounds__(kLThreads, 2) lora_v_kernel(const __grid_const
     const int l = pick[0];
     if (l < 0) return;
     __nv_bfloat16 *hi =
-        p.v + ((int64_t)(tile * p.cap + pick[1]) * (p.wide ? 2 : 1) * p.tile) * p.r64 + rb * 16;
-    const int64_t half = p.wide ? (int64_t)p.tile * p.r64 : 32;
+        p.v + ((int64_t)(tile * p.cap + pick[1]) * p.blocks * p.tile) * p.r64 + rb * 16;
+    const int64_t block = (int64_t)p.tile * p.r64;
     // zero rows of the other adapters (the slot's first item), and the columns
     // past the rank (its first rank block)
-    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
     if (pick[2] == 0)
         for (int i = tid; i < p.tile; i += kLThreads) {
-            uint4 *d = reinterpret_cast<uint4 *>(hi + (int64_t)i * p.r64);
-            uint4 *e = reinterpret_cast<uint4 *>(hi + half + (int64_t)i * p.r64);
-            if (ad[i] != l) d[0] = d[1] = e[0] = e[1] = z;
-            if (rb == 0)
-                for (int c = 2 * rblocks; c < (p.wide ? p.r64 : 32) / 8; ++c) d[c] = e[c] = z;
+            __nv_bfloat16 *d = hi + (int64_t)i * p.r64;
+            if (ad[i] != l) zero_v<P>(d, 1, p.per, block);
+            if (rb == 0) zero_v<P>(d + 16 * rblocks, (p.per == 1 ? p.r64 / 16 : p.per == 2 ? 2 : 1) - rblocks, p.per, block);
         }
     // this lane's x rows (g, g + 8) and adapter rows (ranks g, g + 8 of the block)
     const int g = lane >> 2, c8 = 8 * (lane & 3);
@@ -214,13 +178,13 @@ __global__ void __launch_bounds__(kLThreads, 2) lora_v_kernel(const __grid_const
     constexpr int kU = BF16 ? 2 : 1;
     auto go = [&](auto count, int s0) {
         constexpr int U = decltype(count)::value;
-        uint4 xa[U], xb[U], wa[U], wb[U];
-        [[maybe_unused]] uint4 ya[U], yb[U];
+        uint4 wa[U], wb[U];
+        X8<BF16> xa[U], xb[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int k = (s0 + u) * 32;
-            x_pairs<BF16>(p.x, x0 + k, xa[u], ya[u]);
-            x_pairs<BF16>(p.x, x1 + k, xb[u], yb[u]);
+            xa[u].load(p.x, x0 + k);
+            xb[u].load(p.x, x1 + k);
             wa[u] = __ldg(reinterpret_cast<const uint4 *>(a0 + k));
             wb[u] = __ldg(reinterpret_cast<const uint4 *>(a1 + k));
         }
@@ -228,15 +192,14 @@ __global__ void __launch_bounds__(kLThreads, 2) lora_v_kernel(const __grid_const
         for (int u = 0; u < U; ++u) {
             const uint32_t f0[4] = {wa[u].x, wb[u].x, wa[u].y, wb[u].y};
             const uint32_t f1[4] = {wa[u].z, wb[u].z, wa[u].w, wb[u].w};
-            mma_16816(d0, f0, xa[u].x, xa[u].y);
-            mma_16816(d1, f0, xb[u].x, xb[u].y);
-            mma_16816(d0, f1, xa[u].z, xa[u].w);
-            mma_16816(d1, f1, xb[u].z, xb[u].w);
-            if constexpr (!BF16) {
-                mma_16816(d0, f0, ya[u].x, ya[u].y);
-                mma_16816(d1, f0, yb[u].x, yb[u].y);
-                mma_16816(d0, f1, ya[u].z, ya[u].w);
-                mma_16816(d1, f1, yb[u].z, yb[u].w);
+#pragma unroll
+            for (int i = 0; i < X8<BF16>::kMost; ++i) {
+                if (i == P) break;
+                const uint4 x = xa[u].template next<P>(), y = xb[u].template next<P>();
+                mma_16816(d0, f0, x.x, x.y);
+                mma_16816(d1, f0, y.x, y.y);
+                mma_16816(d0, f1, x.z, x.w);
+                mma_16816(d1, f1, y.z, y.w);
             }
         }
     };
@@ -260,8 +223,7 @@ __global__ void __launch_bounds__(kLThreads, 2) lora_v_kernel(const __grid_const
         if (p.alpha != nullptr) v *= __ldg(p.alpha + l);
         if (row >= 0) {
             if (rb * 16 + c >= p.r) v = 0.0f;
-            hi[(int64_t)row * p.r64 + c] = __float2bfloat16_rn(v);
-            hi[half + (int64_t)row * p.r64 + c] = __float2bfloat16_rn(bf16_rest(v));
+            store_v<P>(hi + (int64_t)row * p.r64 + c, v, p.per, block);
         }
     }
 }
@@ -305,20 +267,20 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
     if (st != FP8G_OK) return st;
     if (M == 0) return FP8G_OK;
 
-    const LoraV lv(lora ? r : 1);
+    const LoraV lv(lora ? r : 1, out == FP8G_OUT_F32);
     const int32_t ks = (int32_t)((K + 127) / 128), n_rt = (int32_t)((N + 127) / 128);
     // CTA pairs from 513 rows on, and from 129 where the low-rank steps of a tile
     // are few beside its FP8 steps: they make all of a pair's 256 rows wait, where
     // the streaming kernel covers an adapter's columns.  256 rows at 4096 x 14336:
     // 8 adapters of rank 16 30.8 us (streamed 37.1), 32 of rank 64 63.9 (55.2); 128
     // rows: 30.3 (31.4) and 63.1 (43.0).
-    const int most = lora ? (L < kMaxTile ? L : kMaxTile) * lv.kr * lv.halves : 0;
+    const int most = lora ? (L < kMaxTile ? L : kMaxTile) * lv.kr * lv.blocks : 0;
     const bool pair = M > kStreamLoraRows || (M > kStreamMaxTokens && 2 * most <= ks);
     const int nb = pair ? 256 : stream_columns(M);
     const int tiles = (int)((M + nb - 1) / nb), cap = L < nb ? L : nb;
     const int32_t n_rtA = (int32_t)((M + 127) / 128);
     // rows of V and of the scales: 32-bit TMA coordinates
-    if ((int64_t)tiles * cap * lv.halves * nb >= kMaxDim || (int64_t)ks * n_rtA >= kMaxDim)
+    if ((int64_t)tiles * cap * lv.blocks * nb >= kMaxDim || (int64_t)ks * n_rtA >= kMaxDim)
         return FP8G_ERR_UNSUPPORTED_SHAPE;
     StreamParams p{};
     StreamPhase &h = p.ph[0];
@@ -327,7 +289,7 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
         // 14336 27.4 us by one, 29.6 by pairs; 4096 x 28672 41.7 and 35.5
         h.sub = tiles * ((N + 255) / 256) * 8 >= d.num_sms * 5 ? 2 : 1;
         h.mt = (int32_t)((N + 128 * h.sub - 1) / (128 * h.sub));
-        stream_sizes(p, nb, h.sub, true, lv.halves);
+        stream_sizes(p, nb, h.sub, true, lv.blocks);
         h.ks = ks;
         h.rows = (int32_t)N;
         h.n_rt = n_rt;
@@ -341,7 +303,7 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
         return o;
     };
     const size_t o_xq = take((size_t)M * K), o_xsf = take((size_t)(pair ? n_rtA : tiles) * ks * 512);
-    const size_t o_v = take((size_t)tiles * cap * lv.halves * nb * lv.r64 * 2);
+    const size_t o_v = take((size_t)tiles * cap * lv.blocks * nb * lv.r64 * 2);
     const size_t o_part = take(pair ? (size_t)tiles * 4 : stream_part_bytes(p, d.num_sms));
     p.n_counters = 3 + kStreamSplitTiles;
     const size_t o_cnt = take(pair ? (size_t)tiles * cap * 4 : (size_t)p.n_counters * 4);
@@ -350,17 +312,19 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
     void *wsv = nullptr;
     if (cudaMallocFromPoolAsync(&wsv, at, pool, stream) != cudaSuccess) return FP8G_ERR_CUDA;
     uint8_t *ws = static_cast<uint8_t *>(wsv);
-    CUtensorMap mb{}, mv{}, mv1{};
+    CUtensorMap mb{}, mv{}, mv32{}, mv1{};
     if (lora) {
         const uint64_t db[3] = {(uint64_t)r, (uint64_t)N, (uint64_t)L};
         const uint32_t bb[3] = {64u, 128u, 1u};
-        const uint64_t dv[2] = {(uint64_t)lv.r64, (uint64_t)tiles * cap * lv.halves * nb};
+        const uint64_t dv[2] = {(uint64_t)lv.r64, (uint64_t)tiles * cap * lv.blocks * nb};
         const uint32_t bv[2] = {64u, 128u};
-        const uint64_t dv3[3] = {(uint64_t)lv.r64, (uint64_t)nb, (uint64_t)tiles * cap * lv.halves};
-        const uint32_t bv2[3] = {64u, 16u, (uint32_t)lv.halves}, bv1[3] = {64u, 16u, 1u};
+        const uint64_t dv3[3] = {(uint64_t)lv.r64, (uint64_t)nb, (uint64_t)tiles * cap * lv.blocks};
+        const uint32_t bv16[3] = {64u, 16u, (uint32_t)lv.blocks}, bv32[3] = {64u, 32u, (uint32_t)lv.blocks};
+        const uint32_t bv1[3] = {64u, 16u, 1u};
         st = host_bf16_map(lora_b, 3, db, bb, d.dev, mb);
         if (st == FP8G_OK)
-            st = pair ? host_bf16_map(ws + o_v, 2, dv, bv, d.dev, mv) : host_bf16_map(ws + o_v, 3, dv3, bv2, d.dev, mv);
+            st = pair ? host_bf16_map(ws + o_v, 2, dv, bv, d.dev, mv) : host_bf16_map(ws + o_v, 3, dv3, bv16, d.dev, mv);
+        if (st == FP8G_OK && !pair) st = host_bf16_map(ws + o_v, 3, dv3, bv32, d.dev, mv32);
         if (st == FP8G_OK && !pair) st = host_bf16_map(ws + o_v, 3, dv3, bv1, d.dev, mv1);
     }
     const bool bf16 = x_dtype == FP8G_IN_BF16;
@@ -396,6 +360,7 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
         p.timeout_ns = d.timeout_ns;
         p.B = mb;
         p.V = mv;
+        p.V32 = mv32;
         p.V1 = mv1;
         p.w = static_cast<const uint8_t *>(W);
         p.b = lora_b;
@@ -406,7 +371,9 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
         p.v = ws + o_v;
         p.rank = lora ? r : 0;  // 0: the kernels read no idx
         p.r64 = lv.r64;
-        p.halves = lv.halves;
+        p.pieces = lv.pieces;
+        p.per = lv.per;
+        p.blocks = lv.blocks;
         p.slot_cap = cap;
         if (st == FP8G_OK) e = launch_stream(true, p, d.num_sms, stream);
     } else if (st == FP8G_OK) {
@@ -424,7 +391,8 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
         a.L = L;
         a.r = r;
         a.r64 = lv.r64;
-        a.wide = lv.wide;
+        a.per = lv.per;
+        a.blocks = lv.blocks;
         a.tile = nb;
         a.cap = cap;
         a.tiles = lora ? tiles : 0;
@@ -435,10 +403,11 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
         a.status = d.status;
         if (lora) {
             const int64_t blocks = (int64_t)tiles * ((r + 15) / 16) * a.items;
-            e = blocks >= INT32_MAX ? cudaErrorInvalidValue
-                : bf16 ? launch_programmatic(lora_v_kernel<true>, dim3((unsigned)blocks), dim3(kLThreads), stream, a)
-                       : launch_programmatic(lora_v_kernel<false>, dim3((unsigned)blocks), dim3(kLThreads), stream,
-                                             a);
+            auto kern = lv.pieces == 3 ? (bf16 ? lora_v_kernel<3, true> : lora_v_kernel<3, false>)
+                                       : (bf16 ? lora_v_kernel<2, true> : lora_v_kernel<2, false>);
+            e = blocks >= INT32_MAX
+                    ? cudaErrorInvalidValue
+                    : launch_programmatic(kern, dim3((unsigned)blocks), dim3(kLThreads), stream, a);
         }
         if (e == cudaSuccess)
             e = bf16 ? launch_programmatic(lora_quant_kernel<true>, dim3((unsigned)M), dim3(256), stream, a)
@@ -452,7 +421,9 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
             pl.cap = cap;
             pl.rank = r;
             pl.kr = lv.kr;
-            pl.halves = lv.halves;
+            pl.pieces = lv.pieces;
+            pl.per = lv.per;
+            pl.blocks = lv.blocks;
             pl.r64 = lv.r64;
             pl.L = L;
             pl.fmt = w_fmt;

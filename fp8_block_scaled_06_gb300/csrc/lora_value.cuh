@@ -5,7 +5,7 @@
 // of which some are other adapters': V is zero there, and a zero times a finite
 // value adds nothing.  A B that is infinite or NaN adds NaN.  So a NaN that an
 // epilogue has stored is computed here again, as
-//   sum_k (sx x)(sw w) + sum_j (hi_j + lo_j) B_j
+//   sum_k (sx x)(sw w) + sum_j V_j B_j
 // of its own row, adapter and feature, and stays NaN only where that is one.  A
 // finite B costs the epilogues a comparison a value or less.
 #pragma once
@@ -13,6 +13,7 @@
 #include <cuda_fp16.h>
 
 #include "internal.h"
+#include "stream.h"
 
 namespace fp8g {
 
@@ -40,8 +41,9 @@ struct LoraValue {
     const uint8_t *sfx, *sfw;    // their bytes in the first chunk of packed scales
     int64_t sfx_step, sfw_step;  // bytes between chunks
     int32_t K, fmt, rank;        // rank 0: the row has no adapter
-    const __nv_bfloat16 *v;      // the row's hi halves; lo: `half` values on
-    int64_t half;
+    int32_t pieces, per;         // V: LoraV, values of a block of rows, the row's first pieces
+    int64_t block;
+    const __nv_bfloat16 *v;
     const __nv_bfloat16 *b;      // the feature's row of B
 };
 
@@ -61,9 +63,10 @@ static __device__ __noinline__ float lora_value(const LoraValue &o) {
     for (int j = lane; j < o.rank; j += 32) {
         // (V was written by other SMs: not from L1)
         const unsigned short *v = reinterpret_cast<const unsigned short *>(o.v);
-        const float hi = __uint_as_float((uint32_t)__ldcg(v + j) << 16);
-        const float lo = __uint_as_float((uint32_t)__ldcg(v + o.half + j) << 16);
-        low = fmaf(hi + lo, __bfloat162float(o.b[j]), low);
+        float sum = 0.0f;  // of the pieces, exact
+        for (int i = 0; i < o.pieces; ++i)
+            sum += __uint_as_float((uint32_t)__ldcg(v + v_piece(i, o.per, o.block) + j) << 16);
+        low = fmaf(sum, __bfloat162float(o.b[j]), low);
     }
     low = lane_sum(low);
     if (isnan(low)) return low;

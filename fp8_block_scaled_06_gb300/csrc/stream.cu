@@ -27,9 +27,9 @@
 // be scheduled, whatever else the GPU runs.  Waits are bounded all the same.
 //
 // Adapters.  The epilogue warps first compute V = alpha A x (items off a counter,
-// as the tickets), in two bf16 halves.  After its FP8 steps a tile takes, per
+// as the tickets), in two or three bf16 pieces.  After its FP8 steps a tile takes, per
 // adapter among the group's tokens, bf16 steps (kind::f16) of the adapter's B
-// rows against both halves of V, into the same fp32 accumulator; a step covers
+// rows against all pieces of V, into the same fp32 accumulator; a step covers
 // the 16-column windows that hold the adapter's tokens (V is zero in the others'
 // columns; lora_value.cuh has what follows for a B that is not finite).  B comes
 // through the ring as the weights do: read through L1, of which 20 KB are left
@@ -58,6 +58,7 @@
 #include <type_traits>
 
 #include "kernel_common.cuh"
+#include "lora_pieces.cuh"
 #include "lora_value.cuh"
 #include "quant_math.cuh"
 #include "stream.h"
@@ -236,7 +237,7 @@ __device__ __forceinline__ void make_tables(const StreamParams &p, LoraTables &t
         most = __reduce_max_sync(0xffffffffu, most);
         items = __reduce_add_sync(0xffffffffu, items);
         if (lane == 0) {
-            t.windows[g] = p.halves == 2 && most > p.v_cols ? 2 : 1;
+            t.windows[g] = (max(most, 1) + p.v_cols - 1) / p.v_cols;
             atomicAdd(&t.items, items * ((p.rank + 15) / 16));
         }
     }
@@ -387,7 +388,7 @@ struct Tail {
     int32_t pair_at[LORA ? 1 : kPairs];
     float pair_w[LORA ? 1 : kPairs];
     int32_t item, pick[4];  // item of V at hand
-    uint32_t low[LORA ? kMaxStages : 1];  // a stage's low-rank step: first column, columns, MMAs of each half
+    uint32_t low[LORA ? kMaxStages : 1];  // a stage's low-rank step: first column, columns, MMAs of each piece
     typename TablesOf<LORA>::T tab;
 };
 
@@ -462,7 +463,7 @@ __device__ __forceinline__ bool decode(const StreamParams &p, const Tail<LORA> &
 }
 
 // A low-rank step: a slot's 64 ranks from c on for n token columns from lo on, the
-// 16-column windows of the slot's rows (of up to v_cols columns where V's halves
+// 16-column windows of the slot's rows (of up to v_cols columns where V's pieces
 // take rows of their own; V is zero in the others' columns).
 struct Step {
     int slot, c, lo, n;
@@ -492,7 +493,7 @@ struct LowRank {
 __device__ __forceinline__ Step step_of(const StreamParams &p, const LoraTables &t, const Tile &o, LowRank &q) {
     const int lo = t.first[o.g][q.slot] & ~15, hi = (t.first[o.g][q.slot + 1] + 15) & ~15;
     Step s{q.slot, q.c * 64, lo, hi - lo, false};
-    if (p.halves == 2 && p.v_cols < p.nb) {
+    if (p.v_cols < p.nb) {
         const int from = lo + q.w * p.v_cols;
         s.none = from >= hi;
         s.lo = s.none ? lo : from;
@@ -613,8 +614,8 @@ __device__ __forceinline__ void load_weights(const StreamParams &p, Tail<LORA> &
 
 // Warp 3: the tokens' slices (or V's), and all scale chunks (tokens', first
 // weight tile's, second's).  A down product's tokens wait for the gate/up tiles
-// of their group.
-template <bool LORA>
+// of their group.  P: pieces of V.
+template <bool LORA, int P>
 __device__ __forceinline__ void load_tokens(const StreamParams &p, Tail<LORA> &t, uint32_t sbase) {
     volatile int *abort_flag = &t.abort_flag;
     Ring r;
@@ -669,12 +670,14 @@ __device__ __forceinline__ void load_tokens(const StreamParams &p, Tail<LORA> &t
                 const uint32_t x0 = sbase + r.stage * p.stage_bytes + p.w_bytes;
                 t.low[r.stage] = (uint32_t)(st.lo | st.n << 8 |
                                             (st.none ? 0 : (min(64, p.rank - st.c) + 15) / 16) << 16);
-                const int v0 = (o.g * p.slot_cap + st.slot) * p.halves;
-                ptx::mbar_arrive_expect_tx(fb, p.halves * st.n * 128u);
+                const int v0 = (o.g * p.slot_cap + st.slot) * p.blocks;
+                ptx::mbar_arrive_expect_tx(fb, p.blocks * st.n * 128u);
                 if (st.n == 16)
                     ptx::tma_load_3d(x0, &p.V, fb, st.c, st.lo, v0);
+                else if (P == 3 && st.n == 32 && p.blocks > 1)
+                    ptx::tma_load_3d(x0, &p.V32, fb, st.c, st.lo, v0);
                 else
-                    for (int b = 0; b < p.halves; ++b)
+                    for (int b = 0; b < p.blocks; ++b)
                         for (int i = 0; i < st.n; i += 16)
                             ptx::tma_load_3d(x0 + (b * st.n + i) * 128, &p.V1, fb, st.c, st.lo + i, v0 + b);
                 r.next(p);
@@ -729,7 +732,7 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, 
 // issue, more than 4-bit weights take to load).  MMAs into one accumulator follow
 // each other at about 140 cycles however few their columns, so a tile has two
 // where tensor memory allows (chains): MMAs alternate and the epilogue adds them.
-template <bool LORA>
+template <bool LORA, int P>
 __device__ __forceinline__ void issue_mmas(const StreamParams &p, Tail<LORA> &t, uint32_t sbase, uint32_t tmem,
                                            uint32_t sf_tmem) {
     volatile int *abort_flag = &t.abort_flag;
@@ -783,19 +786,23 @@ __device__ __forceinline__ void issue_mmas(const StreamParams &p, Tail<LORA> &t,
                 const int lo = all & 255, n = all >> 8 & 255, nk = all >> 16;
                 const uint32_t id16 = ptx::idesc_bf16(128, 0) | (uint32_t)(n >> 3) << 17;
                 const uint32_t at = r.stage * stage16;
-                // the lo half: rows of its own after the hi ones, or columns 32-63;
-                // into the second accumulator
-                const uint64_t xh = x_desc + at, xl = xh + (p.halves == 2 ? n * 8 : 4);
-                const uint32_t dh = d0 + lo, dl = dh + odd;
+                // pieces (LoraV), the second one into the second accumulator
+                const uint64_t x0 = x_desc + at;
+                const uint64_t x1 = x0 + (P == 3 && p.per == 3 ? 2 : p.per == 2 ? 4 : n * 8);
+                const uint64_t x2 = x0 + (p.per == 3 ? 4 : p.per == 2 ? n * 8 : 2 * n * 8);
+                const uint32_t da = d0 + lo, db = da + odd;
                 if (elect_one()) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         if (j >= nk) break;
                         const uint64_t w0 = w_desc + at + 2 * j, w1 = w0 + tile16;
-                        ptx::mma_bf16(dh, w0, xh + 2 * j, id16, 1u);
-                        if (has1) ptx::mma_bf16(dh + tile_cols, w1, xh + 2 * j, id16, 1u);
-                        ptx::mma_bf16(dl, w0, xl + 2 * j, id16, 1u);
-                        if (has1) ptx::mma_bf16(dl + tile_cols, w1, xl + 2 * j, id16, 1u);
+                        ptx::mma_bf16(da, w0, x0 + 2 * j, id16, 1u);
+                        if (has1) ptx::mma_bf16(da + tile_cols, w1, x0 + 2 * j, id16, 1u);
+                        ptx::mma_bf16(db, w0, x1 + 2 * j, id16, 1u);
+                        if (has1) ptx::mma_bf16(db + tile_cols, w1, x1 + 2 * j, id16, 1u);
+                        if (P == 2) continue;
+                        ptx::mma_bf16(da, w0, x2 + 2 * j, id16, 1u);
+                        if (has1) ptx::mma_bf16(da + tile_cols, w1, x2 + 2 * j, id16, 1u);
                     }
                 }
                 if (elect_one()) ptx::tc_commit(ptx::smem_addr(&t.empty[r.stage]));
@@ -839,35 +846,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&b);
 }
-// What rounding to bf16 leaves of v (of an infinity, or a v rounded to one: nothing).
-__device__ __forceinline__ float bf16_rest(float v) {
-    const float h = __bfloat162float(__float2bfloat16_rn(v));
-    return isinf(h) ? 0.0f : v - h;
-}
-
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Eight values of x as bf16 pairs; of fp32 x the rounded values (hi) and what
-// they leave, rounded (lo).
-template <bool BF16>
-__device__ __forceinline__ void x_pairs(const StreamParams &p, int64_t off, uint4 &hi, uint4 &lo) {
-    if constexpr (BF16) {
-        hi = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.x) + off));
-    } else {
-        float4 a, b;
-        load8<false>(p.x, off, a, b);
-        hi = make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
-        lo = make_uint4(pack_bf16(bf16_rest(a.x), bf16_rest(a.y)), pack_bf16(bf16_rest(a.z), bf16_rest(a.w)),
-                        pack_bf16(bf16_rest(b.x), bf16_rest(b.y)), pack_bf16(bf16_rest(b.z), bf16_rest(b.w)));
-    }
-}
-
 // An item is up to 16 rows of a slot against 16 ranks of its adapter; the K range
 // goes over the eight warps, each a 16 x 16 product by mma.sync (ranks x rows),
 // joined in warp order.  A lane's 16-byte load covers 8 consecutive K of a row;
@@ -877,26 +855,23 @@ __device__ __forceinline__ void x_pairs(const StreamParams &p, int64_t off, uint
 // K = 4096), is the number of instructions: rows and ranks past the end read
 // others' values, into products that are not stored, and no load has a condition.
 // FEW: eight rows at most.
-template <bool BF16, bool FEW>
+template <int P, bool BF16, bool FEW>
 __device__ __forceinline__ void low_rank_item(const StreamParams &p, LoraTables &t, const int32_t *pick) {
     const int tid = threadIdx.x - kSEpiWarp0 * 32, warp = tid >> 5, lane = tid & 31;
     const int g = pick[0], slot = pick[1], l = t.adapter[g][slot], rb = pick[3];
     const int col0 = t.first[g][slot] + pick[2], n = min(16, t.first[g][slot + 1] - col0);  // this item's columns
     __nv_bfloat16 *hi = static_cast<__nv_bfloat16 *>(p.v) +
-                        (int64_t)(g * p.slot_cap + slot) * p.halves * p.nb * p.r64 + rb * 16;
-    const int64_t half = p.halves == 2 ? (int64_t)p.nb * p.r64 : 32;
+                        (int64_t)(g * p.slot_cap + slot) * p.blocks * p.nb * p.r64 + rb * 16;
+    const int64_t block = (int64_t)p.nb * p.r64;
     if (pick[2] == 0) {
         // the slot's first rows: zeros for the tokens of other adapters, and
         // in the columns past the rank
-        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-        const int rblocks = (p.rank + 15) / 16, cols = (p.halves == 2 ? p.r64 : 32) / 8;
+        const int rblocks = (p.rank + 15) / 16, all = p.per == 1 ? p.r64 / 16 : p.per == 2 ? 2 : 1;
         const int s_lo = t.first[g][slot], s_hi = t.first[g][slot + 1];
         for (int i = tid; i < p.nb; i += kEpiThreads) {
-            uint4 *d = reinterpret_cast<uint4 *>(hi + (int64_t)i * p.r64);
-            uint4 *e = reinterpret_cast<uint4 *>(hi + half + (int64_t)i * p.r64);
-            if (i < s_lo || i >= s_hi) d[0] = d[1] = e[0] = e[1] = z;
-            if (rb == 0)
-                for (int c = 2 * rblocks; c < cols; ++c) d[c] = e[c] = z;
+            __nv_bfloat16 *d = hi + (int64_t)i * p.r64;
+            if (i < s_lo || i >= s_hi) zero_v<P>(d, 1, p.per, block);
+            if (rb == 0) zero_v<P>(d + 16 * rblocks, all - rblocks, p.per, block);
         }
     }
     const int gr = lane >> 2, c8 = 8 * (lane & 3);
@@ -910,29 +885,32 @@ __device__ __forceinline__ void low_rank_item(const StreamParams &p, LoraTables 
     constexpr int kU = BF16 ? (FEW ? 6 : 4) : 2;
     auto go = [&](auto count, int s0) {
         constexpr int U = decltype(count)::value;
-        uint4 xa[U], wa[U], wb[U];
-        [[maybe_unused]] uint4 xb[U], ya[U], yb[U];
+        uint4 wa[U], wb[U];
+        X8<BF16> xa[U];
+        [[maybe_unused]] X8<BF16> xb[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int k = (s0 + u) * 32;
             wa[u] = __ldg(reinterpret_cast<const uint4 *>(a0 + k));
             wb[u] = __ldg(reinterpret_cast<const uint4 *>(a1 + k));
-            x_pairs<BF16>(p, x0 + k, xa[u], ya[u]);
-            if constexpr (!FEW) x_pairs<BF16>(p, x1 + k, xb[u], yb[u]);
+            xa[u].load(p.x, x0 + k);
+            if constexpr (!FEW) xb[u].load(p.x, x1 + k);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint32_t f0[4] = {wa[u].x, wb[u].x, wa[u].y, wb[u].y};
             const uint32_t f1[4] = {wa[u].z, wb[u].z, wa[u].w, wb[u].w};
-            mma_16816(d0, f0, xa[u].x, xa[u].y);
-            if constexpr (!FEW) mma_16816(d1, f0, xb[u].x, xb[u].y);
-            mma_16816(d0, f1, xa[u].z, xa[u].w);
-            if constexpr (!FEW) mma_16816(d1, f1, xb[u].z, xb[u].w);
-            if constexpr (!BF16) {
-                mma_16816(d0, f0, ya[u].x, ya[u].y);
-                mma_16816(d1, f0, yb[u].x, yb[u].y);
-                mma_16816(d0, f1, ya[u].z, ya[u].w);
-                mma_16816(d1, f1, yb[u].z, yb[u].w);
+#pragma unroll
+            for (int i = 0; i < X8<BF16>::kMost; ++i) {
+                if (i == P) break;
+                const uint4 x = xa[u].template next<P>();
+                mma_16816(d0, f0, x.x, x.y);
+                mma_16816(d0, f1, x.z, x.w);
+                if constexpr (!FEW) {
+                    const uint4 y = xb[u].template next<P>();
+                    mma_16816(d1, f0, y.x, y.y);
+                    mma_16816(d1, f1, y.z, y.w);
+                }
             }
         }
     };
@@ -966,13 +944,10 @@ __device__ __forceinline__ void low_rank_item(const StreamParams &p, LoraTables 
     for (int q = 0; q < kSEpiWarps / 2; ++q) v += t.acc[q][i][c];
     if (p.alpha != nullptr) v *= __ldg(p.alpha + l);
     if (rb * 16 + c >= p.rank) v = 0.0f;
-    if (i < n) {
-        const int64_t at = (int64_t)(col0 + i) * p.r64 + c;
-        hi[at] = __float2bfloat16_rn(v);
-        hi[half + at] = __float2bfloat16_rn(bf16_rest(v));
-    }
+    if (i < n) store_v<P>(hi + (int64_t)(col0 + i) * p.r64 + c, v, p.per, block);
 }
 
+template <int P>
 __device__ __forceinline__ void low_rank(const StreamParams &p, LoraTables &t, int32_t *pick, int item) {
     const int rblocks = (p.rank + 15) / 16;
     if ((threadIdx.x >> 5) == kSEpiWarp0) {
@@ -996,11 +971,11 @@ __device__ __forceinline__ void low_rank(const StreamParams &p, LoraTables &t, i
     (void)epi_all(true);
     const int left = t.first[pick[0]][pick[1] + 1] - t.first[pick[0]][pick[1]] - pick[2];
     if (!p.x_bf16)
-        low_rank_item<false, false>(p, t, pick);
+        low_rank_item<P, false, false>(p, t, pick);
     else if (left <= 8)
-        low_rank_item<true, true>(p, t, pick);
+        low_rank_item<P, true, true>(p, t, pick);
     else
-        low_rank_item<true, false>(p, t, pick);
+        low_rank_item<P, true, false>(p, t, pick);
 }
 
 __device__ __forceinline__ float gate_act(float g, int gate) {
@@ -1074,7 +1049,9 @@ __device__ __noinline__ void again(const StreamParams &p, Tail<true> &t, int g, 
     v.fmt = p.fmt;
     v.sfx_step = 512;
     v.sfw_step = (int64_t)h.n_rt * 512;
-    v.half = p.halves == 2 ? (int64_t)p.nb * p.r64 : 32;
+    v.pieces = p.pieces;
+    v.per = p.per;
+    v.block = (int64_t)p.nb * p.r64;
     for (int c = c_first; c < n; c += c_step)
         for (int col = c; col < min(n, c + kCols); ++col) {
             const int64_t at = (int64_t)t.tab.row_of[row0 + col] * h.rows + f;
@@ -1088,7 +1065,7 @@ __device__ __noinline__ void again(const StreamParams &p, Tail<true> &t, int g, 
             v.x = p.xq + (int64_t)(row0 + col) * p.K;
             v.sfx = h.sfx + (int64_t)g * h.ks * 512 + scale_byte(col);
             v.v = static_cast<const __nv_bfloat16 *>(p.v) +
-                  ((int64_t)(g * p.slot_cap + s) * p.halves * p.nb + col) * p.r64;
+                  ((int64_t)(g * p.slot_cap + s) * p.blocks * p.nb + col) * p.r64;
             for (uint32_t m = __ballot_sync(0xffffffffu, bad); m != 0; m &= m - 1) {
                 const int src = __ffs((int)m) - 1;
                 const int64_t fs = f - lane + src;
@@ -1309,7 +1286,7 @@ __device__ __forceinline__ void finish_tile(const StreamParams &p, Tail<LORA> &t
     }
 }
 
-template <bool LORA>
+template <bool LORA, int P>
 __global__ void __launch_bounds__(512, 1) stream_kernel(const __grid_constant__ StreamParams p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = ptx::smem_addr(smem_raw);
@@ -1379,13 +1356,13 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const __grid_constant__ 
             load_weights(p, t, sbase);
         }
     } else if (warp == 1) {
-        issue_mmas(p, t, sbase, tmem, sf_tmem);
+        issue_mmas<LORA, P>(p, t, sbase, tmem, sf_tmem);
     } else if (warp == 2) {
         if (lane == 0) copy_scales(p, t, sbase, sf_tmem);
     } else if (warp == 3) {
         if (lane == 0) {
             ptx::grid_dep_wait();
-            load_tokens(p, t, sbase);
+            load_tokens<LORA, P>(p, t, sbase);
         }
     } else if (warp < kSEpiWarp0 + kSEpiWarps) {
         ptx::grid_dep_wait();
@@ -1397,7 +1374,7 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const __grid_constant__ 
                 (void)epi_all(true);
                 const int item = t.item;
                 if (item >= t.tab.items) break;
-                low_rank(p, t.tab, t.pick, item);
+                low_rank<P>(p, t.tab, t.pick, item);
                 fence_proxy_async_all();
                 (void)epi_all(true);
                 if (threadIdx.x == kSEpiWarp0 * 32) (void)atom_add_acq_rel(p.counters + 2, 1);
@@ -1448,9 +1425,9 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const __grid_constant__ 
     }
 }
 
-template <bool LORA>
+template <bool LORA, int P>
 cudaError_t launch_one(const StreamParams &p, int grid, cudaStream_t s) {
-    auto kern = stream_kernel<LORA>;
+    auto kern = stream_kernel<LORA, P>;
     static unsigned long long attr_done = 0ull;  // per device; races benignly
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1468,7 +1445,7 @@ cudaError_t launch_one(const StreamParams &p, int grid, cudaStream_t s) {
 
 }  // namespace
 
-void stream_sizes(StreamParams &p, int nb, int sub, bool lora, int v_halves) {
+void stream_sizes(StreamParams &p, int nb, int sub, bool lora, int v_blocks) {
     p.nb = nb;
     // Tensor memory beside the scales (up to eight stages' 128 columns): two
     // accumulators, so that a tile's epilogue overlaps the next tile, then two
@@ -1478,10 +1455,12 @@ void stream_sizes(StreamParams &p, int nb, int sub, bool lora, int v_halves) {
     p.chains = p.nacc * sub * 2 * nb <= room_cols ? 2 : 1;
     p.acc_cols = sub * p.chains * nb;
     p.w_bytes = sub * kWTile;
-    // V's halves in rows of their own: room for all columns of both, or of
-    // kStreamMaxTokens for half of them (more stages; the rest takes a second step)
-    p.v_cols = v_halves == 2 && nb == kStreamMaxTokens ? nb / 2 : nb;
-    p.x_bytes = (v_halves == 2 ? 2 * p.v_cols : nb) * 128;
+    // V's pieces in rows of their own: room for all columns of two, or of
+    // kStreamMaxTokens for half of them; of three for 32 (more stages; slots of more
+    // columns take further steps)
+    p.v_cols = v_blocks == 3 ? (nb < 32 ? nb : 32) : v_blocks == 2 && nb == kStreamMaxTokens ? nb / 2 : nb;
+    const int x_rows = v_blocks * p.v_cols;
+    p.x_bytes = (x_rows > nb ? x_rows : nb) * 128;
     // the scales' chunks (512 bytes each: tokens, weight tiles), in 1024-byte multiples
     p.stage_bytes = p.w_bytes + p.x_bytes + (sub == 2 ? 2048 : 1024);
     const int room = kSmemMax - 1024 - (int)(lora ? sizeof(Tail<true>) : sizeof(Tail<false>));
@@ -1500,10 +1479,11 @@ cudaError_t launch_stream(bool lora, const StreamParams &p, int num_sms, cudaStr
     cudaError_t e;
     if (lora) {
         e = launch_programmatic(lora_prep_kernel, dim3((unsigned)(p.T * segs)), dim3(kPrepThreads), s, p);
-        if (e == cudaSuccess) e = launch_one<true>(p, num_sms, s);
+        if (e == cudaSuccess)
+            e = p.pieces == 3 ? launch_one<true, 3>(p, num_sms, s) : launch_one<true, 2>(p, num_sms, s);
     } else {
         e = launch_programmatic(moe_prep_kernel, dim3((unsigned)(p.T * segs)), dim3(kPrepThreads), s, p);
-        if (e == cudaSuccess) e = launch_one<false>(p, num_sms, s);
+        if (e == cudaSuccess) e = launch_one<false, 0>(p, num_sms, s);
     }
     return e;
 }

@@ -11,16 +11,24 @@ constexpr int kStreamLoraRows = 512;     // token rows of a call with adapters
 constexpr int kStreamLoraGroups = kStreamLoraRows / kStreamMaxTokens;
 constexpr int kStreamSplitTiles = 128;   // a product with more tiles is not split (128 x 2 > 152 SMs)
 
-// V = alpha A x of a slot (an adapter of a row tile) as two bf16 halves, V = hi
-// + lo to 16 bits.  Rank up to 32: a row of 64 values holds both, hi in
-// columns 0-31 and lo in 32-63: one 64-wide step.  More: rows of r64 = rank
-// rounded up to 64, the tile's hi rows first, then its lo rows: r64 / 64 steps.
+// V = alpha A x of a slot (an adapter of a row tile) as bf16 pieces
+// (lora_pieces.cuh): three where the output is fp32, else two.  In a row of 64
+// values: three from columns 0, 16 and 32 on (rank up to 16), or two from columns
+// 0 and 32 on (up to 32), a third one then in a row of its own: one 64-wide step a
+// row.  Higher ranks: each piece in rows of its own, of r64 = rank rounded up to 64,
+// r64 / 64 steps.  The first block of the tile's rows first, then the second, the third.
 struct LoraV {
-    bool wide;            // halves in rows of their own
-    int r64, kr, halves;  // row length, steps per slot, blocks of rows
-    explicit LoraV(int rank)
-        : wide(rank > 32), r64(wide ? (rank + 63) / 64 * 64 : 64), kr(r64 / 64), halves(wide ? 2 : 1) {}
+    int pieces, per, blocks, r64, kr;  // pieces in a row, blocks of rows, row length, steps per slot
+    LoraV(int rank, bool out_f32)
+        : pieces(out_f32 ? 3 : 2), per(rank > 32 ? 1 : rank > 16 ? 2 : pieces), blocks((pieces + per - 1) / per),
+          r64(per > 1 ? 64 : (rank + 63) / 64 * 64), kr(r64 / 64) {}
 };
+// Where piece i of a value is from its first one on; block: values of a block of rows.
+__host__ __device__ inline int64_t v_piece(int i, int per, int64_t block) {
+    if (i == 0) return 0;
+    if (i == 1) return per == 1 ? block : per == 2 ? 32 : 16;
+    return per == 1 ? 2 * block : per == 2 ? block : 32;
+}
 
 // One product: weights [n_mat][rows][K] against a group's token rows.
 struct StreamPhase {
@@ -67,22 +75,22 @@ struct StreamParams {
     uint8_t *hq, *hsf;     // h: codes [T k][F] and packed scales
     float *y;              // [T k][H]
     // adapters
-    CUtensorMap B, V, V1;  // V: boxes of 16 rows of all halves, of one
+    CUtensorMap B, V, V32, V1;  // V: boxes of 16 and 32 rows of all blocks, of 16 rows of one
     const uint8_t *w;      // what B and ph[0].W map
     const void *b;
     int32_t fmt;           // of the weights
     const void *a;         // bf16 [L][rank][K]
     const float *alpha;    // [L] or null
     const float *bias;     // [N] or null
-    void *v;               // bf16 [group][slot_cap][halves * nb][r64]
-    int32_t rank, kr, r64, halves, slot_cap;  // rank and kr 0: no adapters, idx is null
-    int32_t v_cols;  // token columns whose halves of V fit a stage
+    void *v;               // bf16 [group][slot_cap][blocks][nb][r64]
+    int32_t rank, kr, r64, pieces, per, blocks, slot_cap;  // LoraV; rank and kr 0: no adapters, idx is null
+    int32_t v_cols;  // token columns whose pieces of V a stage takes
 };
 
 // Token columns for groups of up to n rows.
 inline int stream_columns(int64_t n) { return n <= 64 ? (int)((n + 15) / 16 * 16) : kStreamMaxTokens; }
 // Ring and accumulator sizes for nb token columns, sub weight tiles a stage.
-void stream_sizes(StreamParams &p, int nb, int sub, bool lora, int v_halves);
+void stream_sizes(StreamParams &p, int nb, int sub, bool lora, int v_blocks);
 // Bytes of a product's partial tiles; SMs of the device.
 size_t stream_part_bytes(const StreamParams &p, int num_sms);
 // Prepares the tokens, then runs the products: two launches.

@@ -586,8 +586,9 @@ FP8G_API fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t
  * matrix); lora_a: bf16 [L, r, K]; lora_b: bf16 [L, N, r]; alpha: fp32 [L] or
  * null (1); adapter: device int32 [M]; bias: fp32 [N] or null; C: [M, N] bf16
  * or fp32 per `out`.  Adapters of smaller rank are padded with zeros to r.
- * alpha A x is held to 16 significant bits (two bf16 halves) for the product
- * with B, an fp32 x to as many for the product with A; sums are fp32.
+ * Sums are fp32.  alpha A x, for the product with B, and an fp32 x, for the
+ * product with A, keep all 24 significant bits where C is fp32, 16 where it is
+ * bf16.
  * K % 32 == 0 (packed formats 128), r % 8 == 0, L <= FP8G_MAX_ADAPTERS, r <=
  * FP8G_MAX_LORA_RANK, else FP8G_ERR_UNSUPPORTED_SHAPE; L = 0: no adapters
  * (lora_a, lora_b, adapter unused, may be null); M may be 0.  x, W (packed

@@ -318,3 +318,60 @@ def test_non_finite_b_beside_other_nan(M):
     rows[[1, 3]] = False
     cols[[9, 40]] = False
     torch.testing.assert_close(got[rows][:, cols], ref[rows][:, cols], rtol=0, atol=0, equal_nan=True)
+
+
+class LowRank(Projection):
+    """Only the low-rank term: W is zero, alpha 1, a row's V the sums of `terms`
+    products, B one rank in each feature, so that the fp32 output is V itself."""
+
+    def __init__(self, M, N, K, L, r, top_x, top_a, terms, runs=None):
+        super().__init__(M, N, K, L, r, runs=runs)
+        gen = torch.Generator().manual_seed(M + r)
+        self.W.zero_()
+        self.pw = fp8g.pack_scales(torch.ones((N, K // 32), device="cuda"))
+        self.w.zero_()
+        self.alpha[:] = 1
+        self.adapter[0] = 0  # one row at least has an adapter
+        where = torch.rand((M, K), generator=gen).argsort(1) < terms
+        self.x = torch.randint(-top_x, top_x + 1, (M, K), generator=gen).double() * where
+        self.a = torch.randint(-top_a, top_a + 1, (L, r, K), generator=gen).double()
+        self.b = torch.zeros((L, N, r), dtype=torch.double)
+        at = torch.randint(0, r, (L, N), generator=gen)
+        self.b.scatter_(2, at[..., None], torch.randint(0, 2, (L, N, 1), generator=gen).double() * 2 - 1)
+
+
+SHAPES = [(1, 128, 512, 1, 8), (20, 264, 96, 3, 16), (33, 136, 160, 2, 24), (40, 136, 2080, 5, 32), (64, 136, 96, 2, 40),
+          (128, 264, 160, 9, 64), (100, 136, 96, 2, 72), (300, 136, 1056, 2, 16), (300, 136, 96, 50, 24),
+          (600, 136, 160, 3, 8), (600, 264, 96, 4, 24), (700, 136, 160, 5, 136)]
+
+
+@pytest.mark.parametrize("runs", [None, 2])
+@pytest.mark.parametrize("M,N,K,L,r", SHAPES)
+def test_v_keeps_24_bits(M, N, K, L, r, runs):
+    """bf16 x and A of eight bits, V of up to 23."""
+    p = LowRank(M, N, K, L, r, 255, 255, 64, runs)
+    ref, room = p.reference(False, False)
+    assert float(room.max()) < 2 ** 24 and float(room.max()) > 2 ** 17
+    got = p.run(bias=False)
+    assert fp8g.fp8_gemm_status()[0] == 0
+    assert torch.equal(got.cpu().double(), ref)
+
+
+@pytest.mark.parametrize("M,N,K,L,r", SHAPES)
+def test_fp32_x_keeps_24_bits(M, N, K, L, r):
+    """One product a sum, of an x of 24 bits and an A of one."""
+    p = LowRank(M, N, K, L, r, 2 ** 24 - 1, 1, 1)
+    ref, room = p.reference(False, False)
+    got = p.run(bf16=False, bias=False)
+    assert fp8g.fp8_gemm_status()[0] == 0
+    assert torch.equal(got.cpu().double(), ref)
+
+
+@pytest.mark.parametrize("M", [3, 600])
+def test_largest_finite_x_and_v(M):
+    """Finite values stay finite: the pieces of the largest floats are."""
+    p = LowRank(M, 136, 96, 2, 8, 1, 1, 1)
+    p.x *= torch.finfo(torch.float32).max
+    ref, _ = p.reference(False, False)
+    got = p.run(bf16=False, bias=False)
+    assert torch.equal(got.cpu().double(), ref)
