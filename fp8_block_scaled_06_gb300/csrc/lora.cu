@@ -45,6 +45,7 @@ struct LoraPrep {
     __nv_bfloat16 *v;         // [tiles][cap][blocks][tile][r64]
     int32_t *slot_cnt, *slot_adapter;  // the pair kernel's tables
     int32_t items;            // blocks per tile and rank block of V
+    int32_t row0;             // of the call: the first of these rows
     unsigned int *status;
 };
 
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(kLThreads, 2) lora_v_kernel(const __grid_const
         int l = i < n ? __ldg(p.adapter + row0 + i) : -1;
         if (l >= p.L) {
             if (item == 0 && rb == 0 && atomicCAS(&p.status[0], 0u, (unsigned)FP8G_ERR_INVALID_ARG) == 0u)
-                atomicExch(&p.status[1], (unsigned)(row0 + i));
+                atomicExch(&p.status[1], (unsigned)(p.row0 + row0 + i));
             l = -1;
         }
         ad[i] = l < 0 ? -1 : l;
@@ -231,6 +232,7 @@ __global__ void __launch_bounds__(kLThreads, 2) lora_v_kernel(const __grid_const
 bool is_aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool packed(int f) { return f == FP8G_E2M1 || f == FP8G_E2M3 || f == FP8G_E3M2; }
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
+constexpr int64_t kMaxVBytes = (int64_t)1 << 30;
 
 }  // namespace
 
@@ -238,35 +240,13 @@ constexpr int64_t kMaxDim = (int64_t)1 << 31;
 
 using namespace fp8g;
 
-extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void *W, const uint8_t *sfw,
-                                     int32_t w_fmt, const void *lora_a, const void *lora_b,
-                                     const float *alpha, const int32_t *adapter, int32_t L, int32_t r,
-                                     const float *bias, void *C, int out, int64_t M, int64_t N, int64_t K,
-                                     cudaStream_t stream) {
-    if (x_dtype != FP8G_IN_F32 && x_dtype != FP8G_IN_BF16) return FP8G_ERR_INVALID_ARG;
-    if (out != FP8G_OUT_BF16 && out != FP8G_OUT_F32) return FP8G_ERR_INVALID_ARG;
-    if (w_fmt < FP8G_E4M3 || w_fmt > FP8G_E3M2) return FP8G_ERR_INVALID_ARG;
-    if (M < 0 || N < 1 || K < 1 || L < 0 || (L > 0 && r < 1)) return FP8G_ERR_INVALID_ARG;
-    if (W == nullptr || sfw == nullptr) return FP8G_ERR_INVALID_ARG;
-    if (M > 0 && (x == nullptr || C == nullptr)) return FP8G_ERR_INVALID_ARG;
+// Rows row0 .. row0 + M - 1 of a call whose arguments hold, x, adapter and C theirs.
+static fp8g_status lora_rows(const HostDevice &d, int64_t row0, const void *x, int32_t x_dtype, const void *W,
+                             const uint8_t *sfw, int32_t w_fmt, const void *lora_a, const void *lora_b,
+                             const float *alpha, const int32_t *adapter, int32_t L, int32_t r, const float *bias,
+                             void *C, int out, int64_t M, int64_t N, int64_t K, cudaStream_t stream) {
     const bool lora = L > 0;
-    if (lora && (lora_a == nullptr || lora_b == nullptr || (M > 0 && adapter == nullptr)))
-        return FP8G_ERR_INVALID_ARG;
-    if (K % (packed(w_fmt) ? 128 : 32) != 0 || (lora && r % 8 != 0)) return FP8G_ERR_UNSUPPORTED_SHAPE;
-    if (L > FP8G_MAX_ADAPTERS || (lora && r > FP8G_MAX_LORA_RANK) || M >= (1 << 24) || N >= (1 << 24) ||
-        K >= (1 << 24))
-        return FP8G_ERR_UNSUPPORTED_SHAPE;
-    if (!is_aligned(x, 16) || !is_aligned(C, 16) || !is_aligned(W, packed(w_fmt) ? 32 : 16) ||
-        !is_aligned(sfw, 16) || !is_aligned(bias, 4) || (N * (out == FP8G_OUT_F32 ? 4 : 2)) % 16 != 0)
-        return FP8G_ERR_ALIGNMENT;
-    if (lora && (!is_aligned(lora_a, 16) || !is_aligned(lora_b, 16) || !is_aligned(alpha, 4) ||
-                 !is_aligned(adapter, 4)))
-        return FP8G_ERR_ALIGNMENT;
-    HostDevice d;
-    fp8g_status st = host_device(d);
-    if (st != FP8G_OK) return st;
-    if (M == 0) return FP8G_OK;
-
+    fp8g_status st = FP8G_OK;
     const LoraV lv(lora ? r : 1, out == FP8G_OUT_F32);
     const int32_t ks = (int32_t)((K + 127) / 128), n_rt = (int32_t)((N + 127) / 128);
     // CTA pairs from 513 rows on, and from 129 where the low-rank steps of a tile
@@ -345,6 +325,7 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
         p.x = x;
         p.x_bf16 = bf16;
         p.T = (int32_t)M;
+        p.first_row = (int32_t)row0;
         p.K = (int32_t)K;
         p.idx = lora ? adapter : nullptr;
         p.n_idx = (int32_t)M;
@@ -399,6 +380,7 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
         a.v = reinterpret_cast<__nv_bfloat16 *>(ws + o_v);
         a.slot_cnt = reinterpret_cast<int32_t *>(ws + o_part);
         a.slot_adapter = reinterpret_cast<int32_t *>(ws + o_cnt);
+        a.row0 = (int32_t)row0;
         a.items = nb / 16 + cap;  // at most one partly filled item per slot beside the whole ones
         a.status = d.status;
         if (lora) {
@@ -439,4 +421,54 @@ extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void 
     const cudaError_t ef = cudaFreeAsync(wsv, stream);
     if (st != FP8G_OK) return st;
     return e == cudaSuccess && ef == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+}
+
+extern "C" fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void *W, const uint8_t *sfw,
+                                     int32_t w_fmt, const void *lora_a, const void *lora_b,
+                                     const float *alpha, const int32_t *adapter, int32_t L, int32_t r,
+                                     const float *bias, void *C, int out, int64_t M, int64_t N, int64_t K,
+                                     cudaStream_t stream) {
+    if (x_dtype != FP8G_IN_F32 && x_dtype != FP8G_IN_BF16) return FP8G_ERR_INVALID_ARG;
+    if (out != FP8G_OUT_BF16 && out != FP8G_OUT_F32) return FP8G_ERR_INVALID_ARG;
+    if (w_fmt < FP8G_E4M3 || w_fmt > FP8G_E3M2) return FP8G_ERR_INVALID_ARG;
+    if (M < 0 || N < 1 || K < 1 || L < 0 || (L > 0 && r < 1)) return FP8G_ERR_INVALID_ARG;
+    if (W == nullptr || sfw == nullptr) return FP8G_ERR_INVALID_ARG;
+    if (M > 0 && (x == nullptr || C == nullptr)) return FP8G_ERR_INVALID_ARG;
+    const bool lora = L > 0;
+    if (lora && (lora_a == nullptr || lora_b == nullptr || (M > 0 && adapter == nullptr)))
+        return FP8G_ERR_INVALID_ARG;
+    if (K % (packed(w_fmt) ? 128 : 32) != 0 || (lora && r % 8 != 0)) return FP8G_ERR_UNSUPPORTED_SHAPE;
+    if (L > FP8G_MAX_ADAPTERS || (lora && r > FP8G_MAX_LORA_RANK) || M >= (1 << 24) || N >= (1 << 24) ||
+        K >= (1 << 24))
+        return FP8G_ERR_UNSUPPORTED_SHAPE;
+    if (!is_aligned(x, 16) || !is_aligned(C, 16) || !is_aligned(W, packed(w_fmt) ? 32 : 16) ||
+        !is_aligned(sfw, 16) || !is_aligned(bias, 4) || (N * (out == FP8G_OUT_F32 ? 4 : 2)) % 16 != 0)
+        return FP8G_ERR_ALIGNMENT;
+    if (lora && (!is_aligned(lora_a, 16) || !is_aligned(lora_b, 16) || !is_aligned(alpha, 4) ||
+                 !is_aligned(adapter, 4)))
+        return FP8G_ERR_ALIGNMENT;
+    HostDevice d;
+    const fp8g_status st = host_device(d);
+    if (st != FP8G_OK) return st;
+    // V's temporary has a slot for every adapter in every 256 rows, as many as a tile
+    // might use (8192 rows, rank 64, 256 adapters loaded: 537 MB): rows in even shares
+    // of at most kMaxVBytes of it, so that it does not grow with them (262144 rows of
+    // rank 256 would take 69 GB; from 2^22 on V's rows would pass 31 bits)
+    int64_t step = M;
+    if (lora && M > kStreamLoraRows) {
+        const LoraV lv(r, out == FP8G_OUT_F32);
+        const int64_t tile = (int64_t)(L < kMaxTile ? L : kMaxTile) * lv.blocks * kMaxTile * lv.r64 * 2;
+        const int64_t tiles = (M + kMaxTile - 1) / kMaxTile, most = kMaxVBytes / tile;
+        const int64_t shares = (tiles + most - 1) / most;
+        step = (tiles + shares - 1) / shares * kMaxTile;
+    }
+    for (int64_t i = 0; i < M; i += step) {
+        const fp8g_status si =
+            lora_rows(d, i, static_cast<const uint8_t *>(x) + i * K * (x_dtype == FP8G_IN_BF16 ? 2 : 4), x_dtype,
+                      W, sfw, w_fmt, lora_a, lora_b, alpha, lora ? adapter + i : nullptr, L, r, bias,
+                      static_cast<uint8_t *>(C) + i * N * (out == FP8G_OUT_F32 ? 4 : 2), out,
+                      M - i < step ? M - i : step, N, K, stream);
+        if (si != FP8G_OK) return si;
+    }
+    return FP8G_OK;
 }

@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kPrepThreads) lora_prep_kernel(const __grid_co
     const Quant8 q = quant_8(p, tok, c);
     for (int i = blockIdx.x * kPrepThreads + tid; i < p.n_counters; i += gridDim.x * kPrepThreads)
         p.counters[i] = 0;
-    if (c == 0 && p.kr > 0 && __ldg(p.idx + tok) >= p.n_mat) record_error(p, FP8G_ERR_INVALID_ARG, (unsigned)tok);
+    if (c == 0 && p.kr > 0 && __ldg(p.idx + tok) >= p.n_mat) record_error(p, FP8G_ERR_INVALID_ARG, (unsigned)(p.first_row + tok));
     // the row's column: the smaller keys of its group
     const int g = tok / p.nb, j = g * p.nb + tid;
     const int col = __syncthreads_count(tid < p.nb && j < p.T && lora_key(p, j) < lora_key(p, tok));

@@ -54,6 +54,7 @@ struct StreamParams {
     const void *x;         // tokens, fp32 or bf16
     int32_t x_bf16;
     int32_t T, K;          // token rows, their length
+    int32_t first_row;     // of the call (adapters: it may be taken in shares)
     const int32_t *idx;    // MoE: expert of each pair [T][k]; adapters: adapter of each row [T]
     int32_t n_idx, n_mat;  // their number; experts / adapters
     uint8_t *xq, *xsf;     // token codes (MoE: expert order) and packed scales

@@ -599,8 +599,13 @@ FP8G_API fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t
  * value that it has without.  Those values are computed one by one, up to some
  * hundred times the call's time where a whole B is NaN.
  * Two kernels for few rows (up to 128, with many adapters 512), else three (two
- * without adapters), and one temporary from the library's pool: M K bytes, 4 M
- * min(L, 256) max(r, 64) for A x, for few rows also up to 20 MB of partial sums.
+ * without adapters), and one temporary from the library's pool, of M K bytes for
+ * the codes, ceil(M / 128) ceil(K / 128) 512 for their scales, for V tiles of nb
+ * rows (256, or for few M rounded up to 16, from 65 on to 128) with min(L, nb)
+ * slots of 2 p nb r64 bytes each (r64: r rounded up to 64; p = 2 pieces, 3 for
+ * fp32 C; 1 for r <= 32, for fp32 C for r <= 16 and 2 up to 32), for few rows up
+ * to 20 MB of partial sums, and tables.  Rows whose V would take more than 1 GB
+ * are taken in shares, one call after the other.
  */
 FP8G_API fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void *W, const uint8_t *sfw,
                                    int32_t w_fmt, const void *lora_a, const void *lora_b,

@@ -375,3 +375,15 @@ def test_largest_finite_x_and_v(M):
     ref, _ = p.reference(False, False)
     got = p.run(bf16=False, bias=False)
     assert torch.equal(got.cpu().double(), ref)
+
+
+@pytest.mark.parametrize("M,r,L", [(3000, 256, 1024), (4200, 200, 256), (5300, 136, 300)])
+def test_rows_in_shares(M, r, L):
+    """Many rows of many adapters are taken in shares, which bounds V's temporary."""
+    p = Projection(M, 136, 96, L, r)
+    p.check_exact()
+    p.adapter[M - 100] = L
+    ref, _ = p.reference(True, True)
+    got = p.run()
+    assert fp8g.fp8_gemm_status() == (fp8g.FP8G_ERR_INVALID_ARG, M - 100)
+    assert torch.equal(got.cpu().double(), ref)
