@@ -647,8 +647,8 @@ def gemm_lora(x, W, sfw, lora_a, lora_b, alpha, adapter, bias=None, w_fmt: int =
     M, K = x.shape
     N, cols = W.shape
     L, r, ka = lora_a.shape
-    assert cols == packed_cols(K, w_fmt) and ka == K and lora_b.shape == (L, N, r)
-    assert adapter.numel() == M and sfw.numel() == _packed_bytes(1, N, K)
+    assert cols == (K if w_fmt < FP8G_E2M1 else packed_cols(K, w_fmt)) and ka == K and lora_b.shape == (L, N, r)
+    assert adapter.numel() == M and sfw.numel() == (N + 127) // 128 * ((K + 127) // 128) * 512
     assert alpha is None or (alpha.get_device() == dev and alpha.dtype is f32 and alpha.numel() == L
                              and alpha.is_contiguous())
     assert bias is None or (bias.get_device() == dev and bias.dtype is f32 and bias.numel() == N

@@ -296,16 +296,22 @@ static fp8g_status lora_rows(const HostDevice &d, int64_t row0, const void *x, i
     if (lora) {
         const uint64_t db[3] = {(uint64_t)r, (uint64_t)N, (uint64_t)L};
         const uint32_t bb[3] = {64u, 128u, 1u};
-        const uint64_t dv[2] = {(uint64_t)lv.r64, (uint64_t)tiles * cap * lv.blocks * nb};
-        const uint32_t bv[2] = {64u, 128u};
-        const uint64_t dv3[3] = {(uint64_t)lv.r64, (uint64_t)nb, (uint64_t)tiles * cap * lv.blocks};
-        const uint32_t bv16[3] = {64u, 16u, (uint32_t)lv.blocks}, bv32[3] = {64u, 32u, (uint32_t)lv.blocks};
-        const uint32_t bv1[3] = {64u, 16u, 1u};
         st = host_bf16_map(lora_b, 3, db, bb, d.dev, mb);
-        if (st == FP8G_OK)
-            st = pair ? host_bf16_map(ws + o_v, 2, dv, bv, d.dev, mv) : host_bf16_map(ws + o_v, 3, dv3, bv16, d.dev, mv);
-        if (st == FP8G_OK && !pair) st = host_bf16_map(ws + o_v, 3, dv3, bv32, d.dev, mv32);
-        if (st == FP8G_OK && !pair) st = host_bf16_map(ws + o_v, 3, dv3, bv1, d.dev, mv1);
+        if (pair) {
+            const uint64_t dv[2] = {(uint64_t)lv.r64, (uint64_t)tiles * cap * lv.blocks * nb};
+            const uint32_t bv[2] = {64u, 128u};
+            if (st == FP8G_OK) st = host_bf16_map(ws + o_v, 2, dv, bv, d.dev, mv);
+        } else {
+            // boxes of 16 and 32 rows of all blocks, of 16 rows of one (LoraV), as far as used
+            const uint64_t dv[3] = {(uint64_t)lv.r64, (uint64_t)nb, (uint64_t)tiles * cap * lv.blocks};
+            const uint32_t b16[3] = {64u, 16u, (uint32_t)lv.blocks}, b32[3] = {64u, 32u, (uint32_t)lv.blocks};
+            const uint32_t b1[3] = {64u, 16u, 1u};
+            if (st == FP8G_OK) st = host_bf16_map(ws + o_v, 3, dv, b16, d.dev, mv);
+            mv1 = mv;
+            if (st == FP8G_OK && lv.blocks > 1) st = host_bf16_map(ws + o_v, 3, dv, b1, d.dev, mv1);
+            if (st == FP8G_OK && lv.blocks > 1 && lv.pieces == 3)
+                st = host_bf16_map(ws + o_v, 3, dv, b32, d.dev, mv32);
+        }
     }
     const bool bf16 = x_dtype == FP8G_IN_BF16;
     cudaError_t e = cudaSuccess;
