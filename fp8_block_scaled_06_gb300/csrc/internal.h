@@ -252,7 +252,8 @@ int32_t host_gap8(int fmt);       // eighths of a tile that a packed load does n
 
 // route.cu: logits [T, E] (rows ld elements apart) -> ids, weights [T, k];
 // rows != null: counts [E], rows, slots [T k] too, with hist a temporary of
-// route_blocks(T) * E int32 (unused when route_blocks(T) is 1).
+// route_blocks(T, true) * E int32 and T * k bytes behind them (unused when
+// route_blocks(T, true) is 1).
 int route_blocks(int64_t T, bool ordered);
 cudaError_t launch_moe_route(const void *logits, int bf16, int64_t ld, int32_t T, int32_t E, int32_t k,
                              int32_t score, float scale, int32_t *ids, float *weights,

@@ -144,7 +144,7 @@ fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t *ids, co
     const size_t o_hq = take((size_t)R * F), o_hsf = take((size_t)max_groups * g.mt * 512);
     const size_t o_y = take((size_t)R * H * 4), o_pos = take((size_t)R * 4);
     const size_t o_part0 = take(stream_part_bytes(p, d.num_sms)), o_part1 = take(stream_part_bytes(p, d.num_sms));
-    p.n_counters = 3 + max_groups + dn.mt + 2 * kStreamSplitTiles;
+    p.n_counters = 3 + max_groups + dn.mt + kStreamSplitTiles;
     const size_t o_cnt = take((size_t)p.n_counters * 4);
     cudaMemPool_t pool;
     if ((st = host_pool(d.dev, pool)) != FP8G_OK) return st;
@@ -187,7 +187,6 @@ fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t *ids, co
     g.part = reinterpret_cast<float *>(ws + o_part0);
     g.part_cnt = p.done_tile + dn.mt;
     dn.part = reinterpret_cast<float *>(ws + o_part1);
-    dn.part_cnt = g.part_cnt + kStreamSplitTiles;
     p.out = out;
     p.out_f32 = out_dtype == FP8G_OUT_F32;
     p.status = d.status;

@@ -41,7 +41,7 @@ struct StreamPhase {
     int32_t rows;          // rows of a weight matrix (gated: of each half)
     int32_t n_rt;          // 128-row tiles of packed scales per matrix
     float *part;           // partial tiles [tile][part][2][nb][128]
-    int32_t *part_cnt;     // [kStreamSplitTiles] parts done of a tile
+    int32_t *part_cnt;     // [kStreamSplitTiles] parts done of a tile (not of the down product: done_tile)
 };
 
 struct StreamParams {
@@ -61,7 +61,7 @@ struct StreamParams {
     // counters, zeroed by the preparing kernel: [0] the next ticket, [1] the
     // next item of V, [2] items of V done, then (MoE) gated tiles done per group,
     // groups (of split tiles: parts) done per tile of the down product, and the
-    // products' part counters
+    // part counters of the first product
     int32_t *counters;
     int32_t n_counters;
     int32_t *done_group, *done_tile;
