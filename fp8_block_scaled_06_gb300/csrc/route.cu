@@ -7,21 +7,27 @@
 //               sigmoid | sigmoid / sum of the chosen sigmoids
 //   order     = the pairs (t, j) by expert, then by t k + j
 //
-// More than 64 experts: a warp takes a token, its logits in registers as order-preserving integers (lane i: experts i, i + 32, ...).  Each
-// of the k rounds is two warp reductions (redux: the largest key, then the lowest
-// expert that has it).  Many tokens: four lanes take one (route_quad).  Either
-// way a logit is read once, and what bounds the kernel is not memory (32768 x 64
-// fp32 logits, 8 MB, are read in 1.3 us) but the comparisons: about 100 pairs of
-// 64-bit words a lane, 13.7 us for 32768 tokens of 64 experts, k = 8, softmax
-// and order included (inserting into a list of eight, 168 pairs: 18.4 us).  77
-// tokens: 7.1 us, one: 2.5 us (in a graph), latency.
+// Up to 64 experts four lanes take a token (route_quad), more: a warp takes one, its
+// logits in registers as order-preserving integers (lane i: experts i, i + 32, ...),
+// with two warp reductions in each of the k rounds (redux: the largest key, then the
+// lowest expert that has it).  Either way a logit is read once, and what bounds the
+// kernel is not memory (32768 x 64 fp32 logits, 8 MB, are read in 1.3 us) but issuing
+// instructions: of four lanes' comparisons, about 100 pairs of 64-bit words a lane,
+// softmax, ranks and stores, 1800 a warp; a block of 32 warps an SM issues in 57 % of
+// its slots (DRAM 7 %), and 24 of 152 SMs have no block.
+//
+// Device times per call, back to back in a graph (k = 8, softmax over all): one token
+// of 8 experts 2.1 us, of 64 3.9, 77 with the order 6.6: latency; 2048 with it 8.6,
+// 32768 10.5 without and 17.0 with it, 262144 130; 77, 2048 and 32768 tokens of 256
+// experts 20.5, 22.1 and 69.  (Inserting into a list of eight instead of merging, 168
+// pairs: the first kernel alone 18.4 us in place of 13.7.)
 //
 // Order: a stable counting sort.  A token chooses an expert at most once, so a
 // warp's choices of an expert are a mask over its eight tokens: a pair's rank
 // is the masks' set bits before it.  A block counts; the second kernel (none when
 // one block holds every token) adds the counts of the blocks before and stores
-// the pairs at base + rank (6.9 us for 262144 pairs; ranking them there by
-// matching in a warp, 10.0 us).  No atomic decides a position, so the order is
+// the pairs at base + rank (6.5 us more for 262144 pairs; ranking them there by
+// matching in a warp, 3 us more still).  No atomic decides a position, so the order is
 // the same in every run.
 #include <cuda_bf16.h>
 
@@ -491,11 +497,11 @@ cudaError_t launch_nv(const RouteArgs &a, bool bf16, int blocks, int threads, si
 
 }  // namespace
 
-// Tokens of a block.  A block of 256 keeps one SM busy for 8 us (64 experts, k =
-// 8), one of 64 for 3; 64 where the blocks' counts, which every block of the order
-// adds up, stay few: 2048 tokens with the order 14.7 us with 256, 7.3 with 64,
-// 32768 tokens 15.5 and 23.9.  Up to 256 tokens one block makes the order by itself
-// (256: 11.8 us; a temporary and a second launch cost the host 6 us).
+// Tokens of a block.  64 where the blocks' counts, which every block of the order
+// adds up, stay few: with the order (64 experts, k = 8) 2048 tokens take 8.6 us, with
+// 256 16.4; 8192 9.0 and 16.6; 32768 25.9, with 256 17.0.  Up to 256 tokens one block
+// makes the order by itself (256: 13.6 us; a temporary and a second launch cost the
+// host 6 us).
 static int route_tokens(int64_t T, bool ordered) {
     if (ordered && (T <= kBlockTokens || T > 128 * kFewTokens)) return kBlockTokens;
     return kFewTokens;
@@ -519,8 +525,8 @@ cudaError_t launch_moe_route(const void *logits, int bf16, int64_t ld, int32_t T
     cudaError_t e;
     const int most = T < tokens ? T : tokens;  // tokens of a block
     const bool b16 = bf16 != 0;
-    // a warp a token against four lanes a token, 64 experts, k = 8: 2.5 us both for
-    // one token, 3.6 and 2.5 for 32, 20 and 8 for 256
+    // a warp a token against four lanes a token, 64 experts, k = 8: 2.8 and 3.9 us for
+    // one token, 4.0 and 3.8 for 32, 6.8 and 4.3 for 256, 25.4 and 10.5 for 32768
     if (E <= 64) {
         const int threads = (most * 4 + 31) / 32 * 32;
         if (E <= 32)

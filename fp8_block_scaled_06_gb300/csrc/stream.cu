@@ -42,11 +42,11 @@
 // 64 tokens over 8 experts of 4096 x 14336, 227 (214).  While it streams it reads
 // 6.6 to 7.1 TB/s; what is left is 6 us from the call before to the first weights
 // in shared memory, the wait of the down product's first tokens, and 6 us from the
-// last weights to the end.  Adapters: 33 rows at 4096 x 4096, rank 16, 19 us (3);
-// 128 rows of 32 adapters, rank 64, at 4096 x 14336, 42 (21): 26 the projection (an
-// SM takes in 58 GB/s, of which half are tokens), 3 V, 13 the 32 low-rank steps, of
-// which 9 are the roles' own instructions a step (measured without the loads and
-// MMAs).
+// last weights to the end.  Adapters: 33 rows at 4096 x 4096, rank 16, 18.5 us (3)
+// with the weights in L2, 22.6 from memory; 128 rows of 32 adapters, rank 64, at 4096
+// x 14336, 42 (21): 26 the projection (112 tiles, so 40 of 152 SMs have none; an SM
+// takes in 58 GB/s, of which half are tokens), 3 V, 13 the 32 low-rank steps, of which
+// 9 are the roles' own instructions a step (measured without the loads and MMAs).
 //
 // Roles: warp 0 takes tickets and loads weights, warp 3 the tokens' slices and
 // the scales, warp 2 copies scales to tensor memory, warp 1 issues MMAs, warps
@@ -1286,6 +1286,10 @@ __device__ __forceinline__ void finish_tile(const StreamParams &p, Tail<LORA> &t
     }
 }
 
+// (512: 128 registers a thread, which leaves room on the SM for the next call's
+// preparing blocks while this one ends.  With its own 384 threads' worth, 140 to 158,
+// device times are the same and calls back to back slower: 5 tokens over 64 experts 60.7
+// -> 62.6 us, 16 over 32 4-bit ones 77.2 -> 78.2.)
 template <bool LORA, int P>
 __global__ void __launch_bounds__(512, 1) stream_kernel(const __grid_constant__ StreamParams p) {
     extern __shared__ uint8_t smem_raw[];

@@ -560,7 +560,8 @@ typedef enum { FP8G_GATE_SILU = 0, FP8G_GATE_GELU = 1, FP8G_GATE_RELU = 2 } fp8g
  * formats 128), T <= FP8G_MOE_MAX_TOKENS, k <= FP8G_MAX_TOP_K, E <=
  * FP8G_MAX_ROUTED_EXPERTS, else FP8G_ERR_UNSUPPORTED_SHAPE; T may be 0.  The
  * weights of experts without tokens are not read.  For more tokens route with
- * fp8g_moe_route and use the grouped GEMMs.  Results do not vary between runs.
+ * fp8g_moe_route and use the grouped GEMMs (up to FP8G_MAX_EXPERTS experts), or call
+ * this for shares of them.  Results do not vary between runs.
  * Two kernels and one temporary from the library's pool.
  */
 FP8G_API fp8g_status fp8_moe_layer(const void *x, int32_t x_dtype, const int32_t *ids,
