@@ -238,9 +238,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     using PC = PairCfg<MODE, F4>;
     static_assert(!LORA || (MODE == kModeBlock && F4 == 0), "low-rank steps: block-scaled FP8-rate");
     // Low-rank steps of a tile, after its num_kb FP8 steps, in loops of their own:
-    // blocks * kr per slot, the blocks of V's pieces of 64 ranks one after the other.  Each role asks for a tile's number of slots a tile ahead (asked
-    // for at the tile, and with the two kinds of step in one loop, a tile took 2 us
-    // more even without slots).
+    // blocks * kr per slot, the blocks of V's pieces of 64 ranks one after the other.
+    // Each role asks for a tile's number of slots a tile ahead (asked for at the tile,
+    // and with the two kinds of step in one loop, a tile took 2 us more even without
+    // slots).
     auto lora_slots = [&](const int32_t t) -> int {
         if constexpr (LORA) {
             if (t < p.npm * p.npn) {
