@@ -55,6 +55,9 @@ FP8G_SCORE_SIGMOID_NORM = 3
 FP8G_GATE_SILU = 0
 FP8G_GATE_GELU = 1
 FP8G_GATE_RELU = 2
+FP8G_NT = 0
+FP8G_NN = 1
+FP8G_TN = 2
 
 # Every symbol include/fp8gemm.h declares.
 EXPORTS = (
@@ -70,6 +73,8 @@ EXPORTS = (
     "fp8g_set_wait_timeout_ms", "fp8g_shutdown", "fp8g_version",
     "fp8g_packed_scale_bytes", "fp8g_pack_scales", "fp8g_moe_route", "fp8_moe_layer",
     "fp8_gemm_lora",
+    "fp8g_quantize_block128", "fp8g_quantize_tile128", "fp8g_requantize_block128",
+    "fp8_gemm_block128", "fp8_gated_block128", "fp8g_gated_block128_backward",
 )
 
 
@@ -176,6 +181,15 @@ def load():
         lib.fp8_gemm_lora.restype = st
         lib.fp8_gemm_lora.argtypes = [P, i32, P, P, i32, P, P, P, P, i32, i32, P, P, ctypes.c_int,
                                       i64, i64, i64, P]
+        for name, args in (
+                ("fp8g_quantize_block128", [P, i32, i64, i64, i64, i32, P, P, P, P, P]),
+                ("fp8g_quantize_tile128", [P, i32, i64, i64, i64, i32, P, P, P]),
+                ("fp8g_requantize_block128", [P, i32, P, i64, i64, i32, P, P, P]),
+                ("fp8_gemm_block128", [i32, P, P, i32, P, P, i32, P, ctypes.c_int, i32, i64, i64, i64, P]),
+                ("fp8_gated_block128", [P, P, i32, P, P, i32, i32, P, P, P, P, i64, i64, i64, P]),
+                ("fp8g_gated_block128_backward", [P, i32, P, P, i32, i32, i64, i64, P, P, P, P, P, P, P])):
+            getattr(lib, name).restype = st
+            getattr(lib, name).argtypes = args
         lib.fp8_gemm_status.restype = st
         lib.fp8_gemm_status.argtypes = [P, P]
         lib.fp8g_status_string.restype = ctypes.c_char_p
@@ -438,6 +452,48 @@ def fp8_gemm_lora(x, x_dtype: int, W, sfw, w_fmt: int, lora_a, lora_b, alpha, ad
            "fp8_gemm_lora")
 
 
+def fp8g_quantize_block128(x, in_dtype: int, ld: int, rows: int, cols: int, fmt: int, q_row=None,
+                           s_row=None, q_col=None, s_col=None, stream=None):
+    _check(load().fp8g_quantize_block128(_ptr(x), int(in_dtype), ld, rows, cols, int(fmt), _ptr(q_row),
+                                         _ptr(s_row), _ptr(q_col), _ptr(s_col), _stream(stream)),
+           "fp8g_quantize_block128")
+
+
+def fp8g_quantize_tile128(x, in_dtype: int, ld: int, rows: int, cols: int, fmt: int, q, s,
+                          stream=None):
+    _check(load().fp8g_quantize_tile128(_ptr(x), int(in_dtype), ld, rows, cols, int(fmt), _ptr(q),
+                                        _ptr(s), _stream(stream)), "fp8g_quantize_tile128")
+
+
+def fp8g_requantize_block128(q, q_fmt: int, s, rows: int, cols: int, fmt: int, q_col, s_col,
+                             stream=None):
+    _check(load().fp8g_requantize_block128(_ptr(q), int(q_fmt), _ptr(s), rows, cols, int(fmt),
+                                           _ptr(q_col), _ptr(s_col), _stream(stream)),
+           "fp8g_requantize_block128")
+
+
+def fp8_gemm_block128(form: int, A, sfa, a_fmt: int, B, sfb, b_fmt: int, C, out: int, add: int,
+                      M: int, N: int, K: int, stream=None):
+    _check(load().fp8_gemm_block128(int(form), _ptr(A), _ptr(sfa), int(a_fmt), _ptr(B), _ptr(sfb),
+                                    int(b_fmt), _ptr(C), int(out), int(add), M, N, K,
+                                    _stream(stream)), "fp8_gemm_block128")
+
+
+def fp8_gated_block128(x, sfx, x_fmt: int, W13, sf13, w_fmt: int, gate: int, h, sh, gu, sgu, M: int,
+                       F: int, K: int, stream=None):
+    _check(load().fp8_gated_block128(_ptr(x), _ptr(sfx), int(x_fmt), _ptr(W13), _ptr(sf13), int(w_fmt),
+                                     int(gate), _ptr(h), _ptr(sh), _ptr(gu), _ptr(sgu), M, F, K,
+                                     _stream(stream)), "fp8_gated_block128")
+
+
+def fp8g_gated_block128_backward(dh, dh_dtype: int, gu, sgu, gate: int, fmt: int, M: int, F: int, dgu_row,
+                                 s_row, dgu_col, s_col, h_col, sh_col, stream=None):
+    _check(load().fp8g_gated_block128_backward(_ptr(dh), int(dh_dtype), _ptr(gu), _ptr(sgu), int(gate),
+                                               int(fmt), M, F, _ptr(dgu_row), _ptr(s_row), _ptr(dgu_col),
+                                               _ptr(s_col), _ptr(h_col), _ptr(sh_col), _stream(stream)),
+           "fp8g_gated_block128_backward")
+
+
 def fp8g_kernel_timing_begin(n: int):
     _check(load().fp8g_kernel_timing_begin(int(n)), "fp8g_kernel_timing_begin")
 
@@ -667,3 +723,176 @@ def gemm_lora(x, W, sfw, lora_a, lora_b, alpha, adapter, bias=None, w_fmt: int =
     if st:
         raise Fp8gError(st, "fp8_gemm_lora")
     return C
+
+
+# Scales for blocks of 128 (fp8_gemm_block128 and the calls around it).  Codes are
+# uint8 (or torch's float8) [R, C]; scales fp32 [ceil(C/128), R] along rows,
+# [ceil(R/128), C] along columns, [ceil(R/128), ceil(C/128)] of tiles.
+
+_here = None  # the current device's index
+
+
+def _on(dev: int, *tensors):
+    """The tensors lie on device `dev`, the current one, and are packed."""
+    global _here
+    if _here is None:
+        import torch
+        _here = torch.cuda.current_device
+    assert dev >= 0 and dev == _here(), "tensors of the current CUDA device"
+    for t in tensors:
+        assert t.get_device() == dev and t.is_contiguous()
+
+
+def _source(x, stream):
+    """x [R, C] fp32 or bf16 -> (x, rows apart), its columns packed and rows 16-byte aligned."""
+    _, bf16, f32, _, _ = _t or _names()
+    dt = x.dtype
+    assert dt is bf16 or dt is f32
+    R, C = x.shape
+    ld, step = x.stride()
+    if R <= 1:
+        ld = C
+    if (C > 1 and step != 1) or ld < C or ld * x.itemsize % 16 or x.data_ptr() % 16:
+        x, ld = _packed(x, stream), C
+        if x.data_ptr() % 16:
+            x = x.clone()
+    return x, ld
+
+
+def quantize_block128(x, row: bool = True, col: bool = False, fmt: int = FP8G_E4M3, stream=None):
+    """fp32 or bf16 [R, C] -> ((codes, scales) along rows or None, (codes, scales)
+    along columns or None), one reading of x."""
+    empty, bf16, f32, _, u8 = _t or _names()
+    dev = x.device
+    _on(x.get_device())
+    assert row or col
+    x, ld = _source(x, stream)
+    R, C = x.shape
+    qr = empty((R, C), dtype=u8, device=dev) if row else None
+    sr = empty((-(-C // 128), R), dtype=f32, device=dev) if row else None
+    qc = empty((R, C), dtype=u8, device=dev) if col else None
+    sc = empty((-(-R // 128), C), dtype=f32, device=dev) if col else None
+    st = (_lib or load()).fp8g_quantize_block128(
+        x.data_ptr(), FP8G_IN_BF16 if x.dtype is bf16 else FP8G_IN_F32, ld, R, C, fmt,
+        _ptr(qr), _ptr(sr), _ptr(qc), _ptr(sc), _stream(stream))
+    if st:
+        raise Fp8gError(st, "fp8g_quantize_block128")
+    return (qr, sr) if row else None, (qc, sc) if col else None
+
+
+def quantize_tile128(x, fmt: int = FP8G_E4M3, stream=None):
+    """fp32 or bf16 [R, C] (weights) -> (codes, scales of 128 x 128 tiles)."""
+    empty, bf16, f32, _, u8 = _t or _names()
+    _on(x.get_device())
+    x, ld = _source(x, stream)
+    R, C = x.shape
+    q = empty((R, C), dtype=u8, device=x.device)
+    s = empty((-(-R // 128), -(-C // 128)), dtype=f32, device=x.device)
+    fp8g_quantize_tile128(x, FP8G_IN_BF16 if x.dtype is bf16 else FP8G_IN_F32, ld, R, C, fmt, q, s, stream)
+    return q, s
+
+
+def requantize_block128(q, s, fmt: int = FP8G_E4M3, q_fmt: int = FP8G_E4M3, stream=None):
+    """Codes [R, C] of q_fmt with scales along rows -> (codes, scales) along columns."""
+    empty, _, f32, _, u8 = _t or _names()
+    _on(q.get_device(), q, s)
+    R, C = q.shape
+    assert q.itemsize == 1 and s.dtype is f32 and s.shape == (-(-C // 128), R)
+    qc = empty((R, C), dtype=u8, device=q.device)
+    sc = empty((-(-R // 128), C), dtype=f32, device=q.device)
+    st = (_lib or load()).fp8g_requantize_block128(q.data_ptr(), q_fmt, s.data_ptr(), R, C, fmt,
+                                                   qc.data_ptr(), sc.data_ptr(), _stream(stream))
+    if st:
+        raise Fp8gError(st, "fp8g_requantize_block128")
+    return qc, sc
+
+
+_FORMS = {"nt": FP8G_NT, "nn": FP8G_NN, "tn": FP8G_TN}
+
+
+def gemm_block128(A, sfa, B, sfb, form: str = "nt", a_fmt: int = FP8G_E4M3, b_fmt: int = FP8G_E4M3,
+                  out: str = "bf16", add_to=None, stream=None):
+    """Product of codes with block-128 scales: "nt" A [M, K] B [N, K]^T (forward), "nn"
+    A [M, K] B [K, N] (input gradient), A along rows and B in tiles; "tn" A [K, M]^T
+    B [K, N] (weight gradient), both along columns.  Allocates C [M, N], or adds to
+    add_to (fp32 [M, N]) and returns it."""
+    empty, bf16, f32, _, _ = _t or _names()
+    dev = A.get_device()
+    _on(dev, A, sfa, B, sfb)
+    assert A.itemsize == 1 and B.itemsize == 1 and sfa.dtype is f32 and sfb.dtype is f32
+    a0, a1 = A.shape
+    b0, b1 = B.shape
+    if form == "tn":
+        K, M, N = a0, a1, b1
+        kb = -(-K // 128)
+        assert b0 == K and sfa.shape == (kb, M) and sfb.shape == (kb, N)
+    else:
+        M, K = a0, a1
+        N, k = (b0, b1) if form == "nt" else (b1, b0)
+        assert k == K and sfa.shape == (-(-K // 128), M) and sfb.shape == (-(-b0 // 128), -(-b1 // 128))
+    if add_to is not None:
+        _on(dev, add_to)
+        C, wide = add_to, True
+        assert C.dtype is f32 and C.shape == (M, N)
+    else:
+        wide = out != "bf16"
+        C = empty((M, N), dtype=f32 if wide else bf16, device=A.device)
+    st = (_lib or load()).fp8_gemm_block128(
+        _FORMS[form], A.data_ptr(), sfa.data_ptr(), a_fmt, B.data_ptr(), sfb.data_ptr(), b_fmt, C.data_ptr(),
+        FP8G_OUT_F32 if wide else FP8G_OUT_BF16, 0 if add_to is None else 1, M, N, K, _stream(stream))
+    if st:
+        raise Fp8gError(st, "fp8_gemm_block128")
+    return C
+
+
+def gated_block128(x, sfx, W13, sf13, gate: int = FP8G_GATE_SILU, keep: bool = False,
+                   x_fmt: int = FP8G_E4M3, w_fmt: int = FP8G_E4M3, stream=None):
+    """h = act(x W13[:F]^T) (x W13[F:]^T): x [M, K] codes with scales along rows, W13
+    [2F, K] in tiles -> ((codes, scales) of h along rows, with `keep` (codes, scales)
+    of gate and up [M, 2F] along rows, the checkpoint of the backward pass, or None)."""
+    empty, _, f32, _, u8 = _t or _names()
+    dev = x.device
+    _on(x.get_device(), x, sfx, W13, sf13)
+    assert x.itemsize == 1 and W13.itemsize == 1 and sfx.dtype is f32 and sf13.dtype is f32
+    M, K = x.shape
+    F2, k = W13.shape
+    F = F2 // 2
+    kb = -(-K // 128)
+    assert k == K and F2 == 2 * F and sfx.shape == (kb, M) and sf13.shape == (-(-F2 // 128), kb)
+    h = empty((M, F), dtype=u8, device=dev)
+    sh = empty((-(-F // 128), M), dtype=f32, device=dev)
+    gu = empty((M, F2), dtype=u8, device=dev) if keep else None
+    sgu = empty((-(-F2 // 128), M), dtype=f32, device=dev) if keep else None
+    st = (_lib or load()).fp8_gated_block128(
+        x.data_ptr(), sfx.data_ptr(), x_fmt, W13.data_ptr(), sf13.data_ptr(), w_fmt, gate, h.data_ptr(),
+        sh.data_ptr(), _ptr(gu), _ptr(sgu), M, F, K, _stream(stream))
+    if st:
+        raise Fp8gError(st, "fp8_gated_block128")
+    return (h, sh), (gu, sgu) if keep else None
+
+
+def gated_block128_backward(dh, gu, sgu, gate: int = FP8G_GATE_SILU, fmt: int = FP8G_E4M3, stream=None):
+    """dh [M, F] fp32 or bf16 and gated_block128's checkpoint -> (codes, scales) of the
+    gradient of gate and up [M, 2F] along rows, the same along columns, and h [M, F]
+    along columns (E4M3)."""
+    empty, bf16, f32, _, u8 = _t or _names()
+    dev = dh.device
+    if not dh.is_contiguous():
+        dh = _packed(dh, stream)
+    _on(dh.get_device(), dh, gu, sgu)
+    dt = dh.dtype
+    M, F = dh.shape
+    assert (dt is bf16 or dt is f32) and gu.itemsize == 1 and gu.shape == (M, 2 * F)
+    assert sgu.dtype is f32 and sgu.shape == (-(-2 * F // 128), M)
+    mb = -(-M // 128)
+    row, col = empty((M, 2 * F), dtype=u8, device=dev), empty((M, 2 * F), dtype=u8, device=dev)
+    h = empty((M, F), dtype=u8, device=dev)
+    s_row, s_col = empty((-(-2 * F // 128), M), dtype=f32, device=dev), empty((mb, 2 * F), dtype=f32, device=dev)
+    s_h = empty((mb, F), dtype=f32, device=dev)
+    st = (_lib or load()).fp8g_gated_block128_backward(
+        dh.data_ptr(), FP8G_IN_BF16 if dt is bf16 else FP8G_IN_F32, gu.data_ptr(), sgu.data_ptr(), gate, fmt,
+        M, F, row.data_ptr(), s_row.data_ptr(), col.data_ptr(), s_col.data_ptr(), h.data_ptr(),
+        s_h.data_ptr(), _stream(stream))
+    if st:
+        raise Fp8gError(st, "fp8g_gated_block128_backward")
+    return (row, s_row), (col, s_col), (h, s_h)

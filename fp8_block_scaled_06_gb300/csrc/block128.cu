@@ -1,0 +1,254 @@
+// Entry points of the operators with fp32 scales for blocks of 128: argument
+// checks, tensor maps, the choice between the kernel for few rows
+// (block128_few.cu) and the one on CTA pairs (block128_gemm.cu).
+#include "block128.h"
+
+namespace fp8g {
+
+namespace {
+
+bool is_aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+bool fp8_fmt(int f) { return f == FP8G_E4M3 || f == FP8G_E5M2; }
+int64_t blocks(int64_t n) { return (n + kBlk - 1) / kBlk; }
+constexpr int64_t kMaxDim = (int64_t)1 << 31;
+constexpr int64_t kMaxQuantRows = (int64_t)65535 * kBlk;  // tiles of 128 rows: a grid's second axis
+
+// Rows of C that take the kernel for few rows, and its rows per tile.
+constexpr int64_t kFewRows = 128;
+int few_tile(int64_t M, bool gated) { return M <= 16 ? 16 : M <= 32 || gated ? 32 : 64; }
+
+// CTAs that share a tile's K blocks: the fewest rounds of K blocks over two CTAs
+// an SM, where each further CTA costs a tile about two K blocks of joining.
+int few_split(int64_t tiles, int num_kb, int num_sms) {
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int s = 1; s <= 8; s *= 2) {
+        if (s > num_kb) break;
+        const int64_t rounds = (tiles * s + 2 * num_sms - 1) / (2 * num_sms);
+        const int64_t cost = rounds * ((num_kb + s - 1) / s + 2) + s;
+        if (cost < least) {
+            least = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
+fp8g_status map2(const void *ptr, int64_t inner, int64_t outer, int rows, int dev, CUtensorMap &m) {
+    const uint64_t d[2] = {(uint64_t)inner, (uint64_t)outer};
+    const uint32_t b[2] = {(uint32_t)kBlk, (uint32_t)rows};
+    return host_operand_map(ptr, FP8G_E4M3, 2, d, b, dev, m);  // (one-byte elements)
+}
+
+fp8g_status check_quant(const void *x, int64_t rows, int64_t cols, int64_t ld, int esz, int fmt) {
+    if (!fp8_fmt(fmt) || rows < 0 || cols < 1 || ld < cols) return FP8G_ERR_INVALID_ARG;
+    if (rows > 0 && x == nullptr) return FP8G_ERR_INVALID_ARG;
+    if (cols % 16 != 0 || rows > kMaxQuantRows || cols >= kMaxDim || ld >= ((int64_t)1 << 40))
+        return FP8G_ERR_UNSUPPORTED_SHAPE;
+    if (!is_aligned(x, 16) || ld * esz % 16 != 0) return FP8G_ERR_ALIGNMENT;
+    return FP8G_OK;
+}
+
+fp8g_status run_quant(const B128Quant &a, int fmt, cudaStream_t stream) {
+    HostDevice d;
+    const fp8g_status st = host_device(d);
+    if (st != FP8G_OK || a.R == 0) return st;
+    return launch_b128_quant(a, fmt, stream) == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+}
+
+}  // namespace
+
+}  // namespace fp8g
+
+using namespace fp8g;
+
+extern "C" {
+
+fp8g_status fp8g_quantize_block128(const void *x, int32_t in_dtype, int64_t ld, int64_t rows, int64_t cols,
+                                   int32_t fmt, uint8_t *q_row, float *s_row, uint8_t *q_col, float *s_col,
+                                   cudaStream_t stream) {
+    if (in_dtype != FP8G_IN_F32 && in_dtype != FP8G_IN_BF16) return FP8G_ERR_INVALID_ARG;
+    if ((q_row == nullptr) != (s_row == nullptr) || (q_col == nullptr) != (s_col == nullptr))
+        return FP8G_ERR_INVALID_ARG;
+    if (q_row == nullptr && q_col == nullptr && rows != 0) return FP8G_ERR_INVALID_ARG;
+    const fp8g_status st = check_quant(x, rows, cols, ld, in_dtype == FP8G_IN_BF16 ? 2 : 4, fmt);
+    if (st != FP8G_OK) return st;
+    if (!is_aligned(q_row, 16) || !is_aligned(s_row, 16) || !is_aligned(q_col, 16) || !is_aligned(s_col, 16))
+        return FP8G_ERR_ALIGNMENT;
+    const B128Quant a{x, ld, rows, cols, in_dtype, 0, nullptr, q_row, q_col, nullptr, s_row, s_col, nullptr};
+    return run_quant(a, fmt, stream);
+}
+
+fp8g_status fp8g_quantize_tile128(const void *x, int32_t in_dtype, int64_t ld, int64_t rows, int64_t cols,
+                                  int32_t fmt, uint8_t *q, float *s, cudaStream_t stream) {
+    if (in_dtype != FP8G_IN_F32 && in_dtype != FP8G_IN_BF16) return FP8G_ERR_INVALID_ARG;
+    if (rows != 0 && (q == nullptr || s == nullptr)) return FP8G_ERR_INVALID_ARG;
+    const fp8g_status st = check_quant(x, rows, cols, ld, in_dtype == FP8G_IN_BF16 ? 2 : 4, fmt);
+    if (st != FP8G_OK) return st;
+    if (!is_aligned(q, 16) || !is_aligned(s, 16)) return FP8G_ERR_ALIGNMENT;
+    const B128Quant a{x, ld, rows, cols, in_dtype, 0, nullptr, nullptr, nullptr, q, nullptr, nullptr, s};
+    return run_quant(a, fmt, stream);
+}
+
+fp8g_status fp8g_requantize_block128(const uint8_t *q, int32_t q_fmt, const float *s, int64_t rows, int64_t cols,
+                                     int32_t fmt, uint8_t *q_col, float *s_col, cudaStream_t stream) {
+    if (!fp8_fmt(q_fmt)) return FP8G_ERR_INVALID_ARG;
+    if (rows != 0 && (s == nullptr || q_col == nullptr || s_col == nullptr || q_col == q)) return FP8G_ERR_INVALID_ARG;
+    const fp8g_status st = check_quant(q, rows, cols, cols, 1, fmt);
+    if (st != FP8G_OK) return st;
+    if (!is_aligned(s, 16) || !is_aligned(q_col, 16) || !is_aligned(s_col, 16)) return FP8G_ERR_ALIGNMENT;
+    const B128Quant a{q, cols, rows, cols, kB128Codes, q_fmt, s, nullptr, q_col, nullptr, nullptr, s_col, nullptr};
+    return run_quant(a, fmt, stream);
+}
+
+fp8g_status fp8_gemm_block128(int32_t form, const void *A, const float *sfa, int32_t a_fmt, const void *B,
+                              const float *sfb, int32_t b_fmt, void *C, int out, int32_t add, int64_t M, int64_t N,
+                              int64_t K, cudaStream_t stream) {
+    if (form != FP8G_NT && form != FP8G_NN && form != FP8G_TN) return FP8G_ERR_INVALID_ARG;
+    if (!fp8_fmt(a_fmt) || !fp8_fmt(b_fmt)) return FP8G_ERR_INVALID_ARG;
+    if (out != FP8G_OUT_BF16 && out != FP8G_OUT_F32) return FP8G_ERR_INVALID_ARG;
+    if (add != 0 && (add != 1 || out != FP8G_OUT_F32)) return FP8G_ERR_INVALID_ARG;
+    const bool tn = form == FP8G_TN;
+    if (M < 0 || N < 1 || K < 0 || (tn ? M < 1 : K < 1)) return FP8G_ERR_INVALID_ARG;
+    if (M > 0 && C == nullptr) return FP8G_ERR_INVALID_ARG;
+    if (M > 0 && K > 0 && (A == nullptr || sfa == nullptr || B == nullptr || sfb == nullptr))
+        return FP8G_ERR_INVALID_ARG;
+    if (M >= kMaxDim || N >= kMaxDim || K >= kMaxDim) return FP8G_ERR_UNSUPPORTED_SHAPE;
+    const int64_t esz = out == FP8G_OUT_F32 ? 4 : 2;
+    if ((!tn && K % 16 != 0) || (tn && M % 16 != 0) || (form != FP8G_NT && N % 16 != 0) || N * esz % 16 != 0)
+        return FP8G_ERR_ALIGNMENT;
+    if (!is_aligned(A, 16) || !is_aligned(B, 16) || !is_aligned(C, 16) || !is_aligned(sfa, 16) || !is_aligned(sfb, 16))
+        return FP8G_ERR_ALIGNMENT;
+    HostDevice d;
+    fp8g_status st = host_device(d);
+    if (st != FP8G_OK || M == 0) return st;
+    if (K == 0) {  // no rows to sum over
+        if (add) return FP8G_OK;
+        return cudaMemsetAsync(C, 0, (size_t)(M * N * esz), stream) == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+    }
+    B128Params p{};
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.num_kb = (int32_t)blocks(K);
+    p.sa = sfa;
+    p.sb = sfb;
+    p.n_blocks = (int32_t)blocks(N);
+    p.sb_n = form == FP8G_NT ? p.num_kb : 1;
+    p.sb_k = form == FP8G_NT ? 1 : p.n_blocks;
+    p.a_mn = tn;
+    p.b_mn = form != FP8G_NT;
+    p.C = C;
+    p.st32 = is_aligned(C, 32) && N * esz % 32 == 0;
+    p.status = d.status;
+    p.timeout_ns = d.timeout_ns;
+    const int o = add ? kB128Add : out == FP8G_OUT_F32 ? kB128F32 : kB128Bf16;
+    const uint32_t ta = host_mma_type(a_fmt), tb = host_mma_type(b_fmt);
+    const bool few = !tn && M <= kFewRows;
+    const int nt = few ? few_tile(M, false) : kBlk;
+    CUtensorMap mA, mB;
+    st = tn ? map2(A, M, K, kBlk, d.dev, mA) : map2(A, K, M, nt, d.dev, mA);
+    if (st == FP8G_OK)
+        st = p.b_mn ? map2(B, N, K, kBlk, d.dev, mB) : map2(B, K, N, kBlk, d.dev, mB);
+    if (st != FP8G_OK) return st;
+    cudaError_t e;
+    if (few) {
+        p.types = (tb << 7) | (ta << 10) | ((uint32_t)p.b_mn << 15);
+        const int split = few_split((int64_t)p.n_blocks * ((M + nt - 1) / nt), p.num_kb, d.num_sms);
+        e = launch_b128_few(mA, mB, p, o, nt, split, stream);
+    } else {
+        const int64_t npm = (M + 2 * kBlk - 1) / (2 * kBlk), npn = (N + 2 * kBlk - 1) / (2 * kBlk);
+        if (npm * npn >= kMaxDim) return FP8G_ERR_UNSUPPORTED_SHAPE;
+        p.types = (ta << 7) | (tb << 10) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16);
+        p.npm = (int32_t)npm;
+        p.npn = (int32_t)npn;
+        p.T = (int32_t)(npm * npn);
+        e = launch_b128_pair(mA, mB, p, o, tn, d.num_sms, stream);
+    }
+    return e == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+}
+
+fp8g_status fp8_gated_block128(const void *x, const float *sfx, int32_t x_fmt, const void *W13, const float *sf13,
+                               int32_t w_fmt, int32_t gate, uint8_t *h, float *sh, uint8_t *gu, float *sgu,
+                               int64_t M, int64_t F, int64_t K, cudaStream_t stream) {
+    if (!fp8_fmt(x_fmt) || !fp8_fmt(w_fmt)) return FP8G_ERR_INVALID_ARG;
+    if (gate < FP8G_GATE_SILU || gate > FP8G_GATE_RELU) return FP8G_ERR_INVALID_ARG;
+    if (M < 0 || F < 1 || K < 1) return FP8G_ERR_INVALID_ARG;
+    if ((gu == nullptr) != (sgu == nullptr)) return FP8G_ERR_INVALID_ARG;
+    if (M > 0 && (x == nullptr || sfx == nullptr || W13 == nullptr || sf13 == nullptr || h == nullptr || sh == nullptr))
+        return FP8G_ERR_INVALID_ARG;
+    if (F % kBlk != 0 || M >= kMaxDim || 2 * F >= kMaxDim || K >= kMaxDim) return FP8G_ERR_UNSUPPORTED_SHAPE;
+    if (K % 16 != 0 || !is_aligned(x, 16) || !is_aligned(W13, 16) || !is_aligned(h, 16) || !is_aligned(gu, 16) ||
+        !is_aligned(sfx, 16) || !is_aligned(sf13, 16) || !is_aligned(sh, 16) || !is_aligned(sgu, 16))
+        return FP8G_ERR_ALIGNMENT;
+    HostDevice d;
+    fp8g_status st = host_device(d);
+    if (st != FP8G_OK || M == 0) return st;
+    B128Params p{};
+    p.M = M;
+    p.N = F;
+    p.K = K;
+    p.num_kb = (int32_t)blocks(K);
+    p.sa = sfx;
+    p.sb = sf13;
+    p.n_blocks = (int32_t)(F / kBlk);
+    p.sb_n = p.num_kb;
+    p.sb_k = 1;
+    p.gate = gate;
+    p.h = h;
+    p.sh = sh;
+    p.gu = gu;
+    p.sgu = sgu;
+    p.status = d.status;
+    p.timeout_ns = d.timeout_ns;
+    const uint32_t tx = host_mma_type(x_fmt), tw = host_mma_type(w_fmt);
+    const bool few = M <= kFewRows;
+    const int nt = few ? few_tile(M, true) : kBlk;
+    CUtensorMap mX, mW;
+    st = map2(x, K, M, nt, d.dev, mX);
+    if (st == FP8G_OK) {
+        const uint64_t dw[3] = {(uint64_t)K, (uint64_t)F, 2};
+        const uint32_t bw[3] = {(uint32_t)kBlk, (uint32_t)kBlk, 1};
+        st = host_operand_map(W13, FP8G_E4M3, 3, dw, bw, d.dev, mW);
+    }
+    if (st != FP8G_OK) return st;
+    cudaError_t e;
+    if (few) {
+        p.types = (tw << 7) | (tx << 10);
+        const int split = few_split((int64_t)p.n_blocks * ((M + nt - 1) / nt), p.num_kb, d.num_sms);
+        e = launch_b128_few(mX, mW, p, kB128Gated, nt, split, stream);
+    } else {
+        const int64_t npm = (M + 2 * kBlk - 1) / (2 * kBlk);
+        if (npm * p.n_blocks >= kMaxDim) return FP8G_ERR_UNSUPPORTED_SHAPE;
+        p.types = (tx << 7) | (tw << 10);
+        p.npm = (int32_t)npm;
+        p.npn = p.n_blocks;
+        p.T = p.npm * p.npn;
+        e = launch_b128_pair(mX, mW, p, kB128Gated, false, d.num_sms, stream);
+    }
+    return e == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+}
+
+fp8g_status fp8g_gated_block128_backward(const void *dh, int32_t dh_dtype, const uint8_t *gu, const float *sgu,
+                                         int32_t gate, int32_t fmt, int64_t M, int64_t F, uint8_t *dgu_row,
+                                         float *s_row, uint8_t *dgu_col, float *s_col, uint8_t *h_col, float *sh_col,
+                                         cudaStream_t stream) {
+    if (dh_dtype != FP8G_IN_F32 && dh_dtype != FP8G_IN_BF16) return FP8G_ERR_INVALID_ARG;
+    if (gate < FP8G_GATE_SILU || gate > FP8G_GATE_RELU || !fp8_fmt(fmt)) return FP8G_ERR_INVALID_ARG;
+    if (M < 0 || F < 1) return FP8G_ERR_INVALID_ARG;
+    if (M > 0 && (dh == nullptr || gu == nullptr || sgu == nullptr || dgu_row == nullptr || s_row == nullptr ||
+                  dgu_col == nullptr || s_col == nullptr || h_col == nullptr || sh_col == nullptr))
+        return FP8G_ERR_INVALID_ARG;
+    if (F % kBlk != 0 || M > kMaxQuantRows || 2 * F >= kMaxDim) return FP8G_ERR_UNSUPPORTED_SHAPE;
+    const void *all[] = {dh, gu, sgu, dgu_row, s_row, dgu_col, s_col, h_col, sh_col};
+    for (const void *ptr : all)
+        if (!is_aligned(ptr, 16)) return FP8G_ERR_ALIGNMENT;
+    HostDevice d;
+    const fp8g_status st = host_device(d);
+    if (st != FP8G_OK || M == 0) return st;
+    const B128Backward a{dh, gu, sgu, M, F, dgu_row, dgu_col, h_col, s_row, s_col, sh_col};
+    return launch_b128_backward(a, dh_dtype == FP8G_IN_BF16, gate, fmt, stream) == cudaSuccess ? FP8G_OK
+                                                                                               : FP8G_ERR_CUDA;
+}
+
+}  // extern "C"

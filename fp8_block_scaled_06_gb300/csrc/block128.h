@@ -1,0 +1,79 @@
+// Declarations of the operators with scales for blocks of 128 (block128*.cu).
+//
+// Scales are fp32 and lie by block of the contraction first: one per 128
+// consecutive values of a row at [block of the row][row], one per 128 values of
+// a column at [block of the column][column].  So both operands' scales of one
+// K block are contiguous over the rows (columns) of C, whichever way the
+// operand lies.
+#pragma once
+#include "internal.h"
+
+namespace fp8g {
+
+constexpr int kBlk = 128;
+
+// A product C[M, N] = sum over K blocks, or the gated projection pair.
+struct B128Params {
+    int64_t M, N, K;
+    int32_t num_kb;         // ceil(K / 128)
+    int32_t npm, npn;       // tiles of C
+    int32_t T;              // npm npn
+    const float *sa;        // [num_kb][M]
+    const float *sb;        // vectors [num_kb][N]; tiles: block (n, k) at n sb_n + k sb_k
+    int64_t sb_n, sb_k;
+    int32_t n_blocks;       // tiles of 128 along N (gated: along F)
+    uint32_t types;         // operand types and majors as instruction descriptor bits
+    int32_t a_mn, b_mn;     // operand lies with M (N) contiguous
+    void *C;
+    int32_t st32;           // 32-byte stores (C 32-byte aligned, rows multiples of 32 B)
+    // gated: columns of C are the F columns of h
+    int32_t gate;
+    uint8_t *h, *gu;        // codes [M, F], [M, 2F] (gu may be null)
+    float *sh, *sgu;        // [F / 128][M], [2 F / 128][M]
+    unsigned int *status;
+    uint64_t timeout_ns;
+};
+
+enum B128Out : int { kB128Bf16 = 0, kB128F32 = 1, kB128Add = 2, kB128Gated = 3 };
+
+// block128_gemm.cu: CTA pairs over 256 x 256 tiles (gated: 256 rows, 128 columns
+// of gate and of up).  vec_b: B's scales are vectors.
+cudaError_t launch_b128_pair(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p,
+                             int out, bool vec_b, int num_sms, cudaStream_t stream);
+
+// block128_few.cu: few rows of C.  The weights (B) are the MMA's 128-row operand,
+// nt rows of A its columns; K split over clusters of `split` CTAs.
+cudaError_t launch_b128_few(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p,
+                            int out, int nt, int split, cudaStream_t stream);
+
+// block128_quant.cu.  src: FP8G_IN_F32 / FP8G_IN_BF16 values, rows ld apart, or
+// codes of src_fmt with row scales (kB128Codes).  Outputs that are null are left out.
+constexpr int kB128Codes = 2;
+struct B128Quant {
+    const void *x;
+    int64_t ld, R, C;
+    int32_t src, src_fmt;
+    const float *s_src;
+    uint8_t *q_row, *q_col, *q_tile;
+    float *s_row, *s_col, *s_tile;
+};
+cudaError_t launch_b128_quant(const B128Quant &a, int fmt, cudaStream_t stream);
+
+struct B128Backward {
+    const void *dh;
+    const uint8_t *gu;
+    const float *sgu;
+    int64_t M, F;
+    uint8_t *row, *col, *h;      // [M, 2F], [M, 2F], [M, F]
+    float *s_row, *s_col, *s_h;
+};
+cudaError_t launch_b128_backward(const B128Backward &a, bool bf16, int gate, int fmt,
+                                 cudaStream_t stream);
+
+// Lets `kernel` have `bytes` of dynamic shared memory on the current device (an idempotent
+// call of half a microsecond).
+inline cudaError_t b128_allow_smem(const void *kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+}  // namespace fp8g

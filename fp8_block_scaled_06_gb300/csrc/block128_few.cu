@@ -1,0 +1,349 @@
+// Products and gated projections with scales for blocks of 128, for few rows of
+// A: bound by the weights' bytes.
+//
+// The weights are the MMA's operand of 128 rows, NT rows of A its columns, so a
+// tile of C is 128 weight rows by NT.  A CTA holds a ring of 16 KB weight tiles (32
+// KB for gate and up); two CTAs share an SM, about 200 KB in flight.  The K blocks
+// of a tile are split over a cluster of up to eight CTAs, so that a narrow C
+// still uses every SM; each CTA's share of the sum stays in its shared memory,
+// and the CTAs add each other's (distributed shared memory) in rank order, each for
+// its own rows of A, so results do not vary.
+//
+// As in block128_gemm.cu each K block's product goes to a tensor-memory buffer of
+// its own and is added, scaled, to registers: thread = weight row, its values the NT
+// rows, whose scales (times the weight block's) go through shared memory, read as
+// broadcasts.
+//
+// Roles (256 threads): warp 0 TMA, warp 1 MMA issue, warps 4-7 promotion; all eight
+// add and store.
+#include <cuda_bf16.h>
+
+#include "block128.h"
+#include "block128_math.cuh"
+#include "kernel_common.cuh"
+#include "ptx.cuh"
+
+namespace fp8g {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTile = kBlk * kBlk;
+
+template <int NT, bool GATED>
+struct Few {
+    static constexpr int G = GATED ? 2 : 1;              // weight tiles of a stage
+    static constexpr int STAGE = G * kTile + NT * kBlk;
+    static constexpr int STAGES = 106496 / STAGE;        // two CTAs to an SM
+    static constexpr int COLS = G * NT;                  // tensor-memory columns of a buffer
+    static constexpr int BUFS = COLS >= 64 ? 2 : 4;
+    static constexpr int TMEM = COLS * BUFS < 32 ? 32 : COLS * BUFS;
+    static constexpr int RING = STAGES * STAGE;
+    static constexpr int SUMS = COLS * kBlk * 4;         // this CTA's sums, in the ring's place
+    static_assert(SUMS <= RING && (TMEM & (TMEM - 1)) == 0 && TMEM <= 256, "");
+    static constexpr int OFF_S = RING;                   // per promotion warp: [2][G][NT] scales
+    static constexpr int OFF_BAR = OFF_S + 4 * 2 * COLS * 4;
+    static constexpr int NUM_BARS = 2 * STAGES + 2 * BUFS + 1;
+    static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+    static constexpr int BYTES = OFF_MISC + 16 + 1024;
+    static_assert(2 * (BYTES + 1024) <= 233472, "two CTAs to an SM");
+};
+
+template <int NT, int OUT>
+__global__ void __launch_bounds__(kThreads, 2)
+    b128_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const B128Params p) {
+    constexpr bool GATED = OUT == kB128Gated;
+    using L = Few<NT, GATED>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_base = ptx::smem_addr(smem_raw);
+    uint8_t *smem = smem_raw + ((1024u - (raw_base & 1023u)) & 1023u);
+    const uint32_t sbase = ptx::smem_addr(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = (int)gridDim.z, rank = (int)blockIdx.z;  // the cluster is (1, 1, split)
+    const int pn = (int)blockIdx.x;
+    const int64_t m0 = (int64_t)blockIdx.y * NT;
+    const int kb0 = (int)((int64_t)p.num_kb * rank / split), kb1 = (int)((int64_t)p.num_kb * (rank + 1) / split);
+
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
+    auto bar_full = [&](int s) { return ptx::smem_addr(&bars[s]); };
+    auto bar_empty = [&](int s) { return ptx::smem_addr(&bars[L::STAGES + s]); };
+    auto bar_pfull = [&](int b) { return ptx::smem_addr(&bars[2 * L::STAGES + b]); };
+    auto bar_pempty = [&](int b) { return ptx::smem_addr(&bars[2 * L::STAGES + L::BUFS + b]); };
+    const uint32_t bar_drain = ptx::smem_addr(&bars[L::NUM_BARS - 1]);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < L::STAGES; ++s) {
+            ptx::mbar_init(bar_full(s), 1);
+            ptx::mbar_init(bar_empty(s), 1);
+        }
+        for (int b = 0; b < L::BUFS; ++b) {
+            ptx::mbar_init(bar_pfull(b), 1);
+            ptx::mbar_init(bar_pempty(b), 4);
+        }
+        ptx::mbar_init(bar_drain, 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&tmA);
+        ptx::prefetch_tmap(&tmB);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_addr(tmem_slot), L::TMEM);
+        ptx::tmem_relinquish();
+    }
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!wait_bar(bar_empty(stage), phase ^ 1u, abort_flag, p, 0 * 256 + stage)) break;
+                const uint32_t fb = bar_full(stage), st = sbase + stage * L::STAGE;
+                const int32_t k0 = kb * kBlk, n0 = pn * kBlk;
+                ptx::mbar_arrive_expect_tx(fb, L::STAGE);
+                if constexpr (GATED) {
+                    ptx::tma_load_3d(st, &tmB, fb, k0, n0, 0);
+                    ptx::tma_load_3d(st + kTile, &tmB, fb, k0, n0, 1);
+                } else {
+                    ptx::tma_load_2d(st, &tmB, fb, p.b_mn ? n0 : k0, p.b_mn ? k0 : n0);
+                }
+                ptx::tma_load_2d(st + L::G * kTile, &tmA, fb, k0, (int32_t)m0);
+                if (++stage == L::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = ptx::idesc_f8(kBlk, NT) | p.types;
+            const uint32_t w_step = p.b_mn ? 32 * kBlk : 32;
+            uint32_t stage = 0, phase = 0, buf = 0, bphase = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!wait_bar(bar_pempty(buf), bphase ^ 1u, abort_flag, p, 1 * 256 + 64 + buf)) break;
+                if (!wait_bar(bar_full(stage), phase, abort_flag, p, 1 * 256 + stage)) break;
+                ptx::tc_fence_after();
+                const uint32_t w0 = sbase + stage * L::STAGE, x0 = w0 + L::G * kTile;
+#pragma unroll
+                for (int g = 0; g < L::G; ++g)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        ptx::mma_f8(tmem_base + buf * L::COLS + g * NT,
+                                    ptx::smem_desc(w0 + g * kTile + k * w_step, 1024, 1024, 2),
+                                    ptx::smem_desc(x0 + k * 32, 1024, 1024, 2), idesc, k != 0 ? 1u : 0u);
+                ptx::tc_commit(bar_pfull(buf));
+                ptx::tc_commit(bar_empty(stage));
+                if (++stage == L::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+                if (++buf == L::BUFS) {
+                    buf = 0;
+                    bphase ^= 1u;
+                }
+            }
+        }
+    } else if (warp >= 4) {
+        const int q = warp - 4;
+        const uint32_t lane_base = (uint32_t)(q * 32) << 16;
+        float *sc = reinterpret_cast<float *>(smem + L::OFF_S) + q * 2 * L::COLS;
+        constexpr int SPL = (NT + 31) / 32;  // rows of A whose scales a lane fetches
+        const float *sa[SPL];
+        bool mine[SPL];
+#pragma unroll
+        for (int j = 0; j < SPL; ++j) {
+            mine[j] = lane + 32 * j < NT;
+            sa[j] = p.sa + min(m0 + lane + 32 * j, p.M - 1);
+        }
+        const float *sb[L::G];
+#pragma unroll
+        for (int g = 0; g < L::G; ++g) sb[g] = p.sb + (pn + (int64_t)g * p.n_blocks) * p.sb_n;
+        float na[SPL], nb[L::G];  // the next K block's
+        auto fetch = [&](int kb) {
+            if (kb >= kb1) return;
+#pragma unroll
+            for (int j = 0; j < SPL; ++j) na[j] = __ldg(sa[j] + kb * p.M);
+#pragma unroll
+            for (int g = 0; g < L::G; ++g) nb[g] = __ldg(sb[g] + kb * p.sb_k);
+        };
+        fetch(kb0);
+        uint64_t acc[L::COLS / 2];
+#pragma unroll
+        for (int i = 0; i < L::COLS / 2; ++i) acc[i] = 0ull;
+        uint32_t buf = 0, bphase = 0;
+        bool ok = true;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            float *s = sc + ((kb - kb0) & 1) * L::COLS;
+#pragma unroll
+            for (int g = 0; g < L::G; ++g)
+#pragma unroll
+                for (int j = 0; j < SPL; ++j)
+                    if (mine[j]) s[g * NT + lane + 32 * j] = __fmul_rn(na[j], nb[g]);
+            fetch(kb + 1);
+            __syncwarp();
+            if (!wait_bar_warp(bar_pfull(buf), bphase, abort_flag, p, 3 * 256 + 64 + buf)) {
+                ok = false;
+                break;
+            }
+            ptx::tc_fence_after();
+            constexpr int STEP = L::COLS < 32 ? L::COLS : 32;
+#pragma unroll
+            for (int c = 0; c < L::COLS; c += STEP) {
+                uint32_t r[STEP];
+                if constexpr (STEP == 32) {
+                    ptx::tmem_ld_32x32b_x32(lane_base + tmem_base + buf * L::COLS + c, r);
+                } else {
+                    uint32_t a[8], b[8];
+                    ptx::tmem_ld_32x32b_x8(lane_base + tmem_base + buf * L::COLS + c, a);
+                    ptx::tmem_ld_32x32b_x8(lane_base + tmem_base + buf * L::COLS + c + 8, b);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) r[i] = a[i], r[8 + i] = b[i];
+                }
+                ptx::tmem_ld_wait();
+                const ulonglong2 *s2 = reinterpret_cast<const ulonglong2 *>(s + c);
+#pragma unroll
+                for (int i = 0; i < STEP / 4; ++i) {
+                    const ulonglong2 f = s2[i];
+                    b128_fma2(acc[c / 2 + 2 * i], b128_pair(r[4 * i], r[4 * i + 1]), f.x);
+                    b128_fma2(acc[c / 2 + 2 * i + 1], b128_pair(r[4 * i + 2], r[4 * i + 3]), f.y);
+                }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar_pempty(buf));
+            if (++buf == L::BUFS) {
+                buf = 0;
+                bphase ^= 1u;
+            }
+        }
+        // every MMA and every copy of this CTA is done: its sums take the ring's place,
+        // [column][weight row]
+        if (ok) {
+            float *sums = reinterpret_cast<float *>(smem);
+#pragma unroll
+            for (int i = 0; i < L::COLS / 2; ++i) {
+                sums[(2 * i) * kBlk + q * 32 + lane] = b128_lo(acc[i]);
+                sums[(2 * i + 1) * kBlk + q * 32 + lane] = b128_hi(acc[i]);
+            }
+        }
+    }
+    __syncwarp();
+    __syncthreads();
+    if (*abort_flag) {
+        if (warp == 1 && lane == 0) {
+            ptx::tc_commit(bar_drain);
+            const uint64_t t0 = ptx::globaltimer();
+            while (!ptx::mbar_try_wait(bar_drain, 0) && ptx::globaltimer() - t0 < p.timeout_ns) {
+            }
+        }
+        const uint64_t t0 = ptx::globaltimer();
+        while (ptx::globaltimer() - t0 < 200000ull) {
+        }
+        __syncthreads();
+    }
+    ptx::cluster_sync();  // the cluster's sums are in place
+    // Row i of the tile's rows of A is added and stored by CTA i % split; a warp takes
+    // a row at a time, four weight rows a lane.
+    auto total = [&](int col) {
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const uint32_t at = sbase + (col * kBlk + 4 * lane) * 4;
+        for (int j = 0; j < split; ++j) {
+            const float4 o = ptx::ld_cluster_f4(ptx::map_shared(at, j));
+            v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+        }
+        return v;
+    };
+    for (int i = rank + split * warp; i < NT && m0 + i < p.M; i += split * (kThreads / 32)) {
+        const int64_t m = m0 + i, n = (int64_t)pn * kBlk + 4 * lane;
+        if constexpr (!GATED) {
+            float4 v = total(i);
+            if (n < p.N) {
+                if constexpr (OUT == kB128Bf16) {
+                    __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+                    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.C) + m * p.N + n) =
+                        make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
+                } else {
+                    float4 *c = reinterpret_cast<float4 *>(static_cast<float *>(p.C) + m * p.N + n);
+                    if constexpr (OUT == kB128Add) {
+                        const float4 o = *c;
+                        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+                    }
+                    *c = v;
+                }
+            }
+        } else {
+            const float4 g = total(i), u = total(NT + i);
+            const float4 h = make_float4(__fmul_rn(b128_gate(g.x, p.gate), u.x), __fmul_rn(b128_gate(g.y, p.gate), u.y),
+                                         __fmul_rn(b128_gate(g.z, p.gate), u.z), __fmul_rn(b128_gate(g.w, p.gate), u.w));
+            auto code = [&](const float4 v, uint8_t *q, float *s) {
+                const float sv = b128_scale<FP8G_E4M3>(b128_warp_max(b128_amax4(v.x, v.y, v.z, v.w)));
+                *reinterpret_cast<uint32_t *>(q) = b128_codes<FP8G_E4M3>(v.x, v.y, v.z, v.w, __frcp_rn(sv));
+                if (lane == 0) *s = sv;
+            };
+            code(h, p.h + m * p.N + n, p.sh + pn * p.M + m);
+            if (p.gu != nullptr) {
+                code(g, p.gu + m * 2 * p.N + n, p.sgu + pn * p.M + m);
+                code(u, p.gu + m * 2 * p.N + p.N + n, p.sgu + ((int64_t)p.n_blocks + pn) * p.M + m);
+            }
+        }
+    }
+    ptx::cluster_sync();  // no CTA leaves while another reads its sums
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem_base, L::TMEM);
+    }
+}
+
+template <int NT, int OUT>
+cudaError_t launch_few(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p, int split,
+                       cudaStream_t stream) {
+    using L = Few<NT, OUT == kB128Gated>;
+    auto kern = b128_few_kernel<NT, OUT>;
+    const cudaError_t e = b128_allow_smem(reinterpret_cast<const void *>(kern), L::BYTES);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.n_blocks, (unsigned)((p.M + NT - 1) / NT), (unsigned)split);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = L::BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = (unsigned)split;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, A, B, p);
+}
+
+template <int NT>
+cudaError_t few_out(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p, int out, int split,
+                    cudaStream_t stream) {
+    if (out == kB128Bf16) return launch_few<NT, kB128Bf16>(A, B, p, split, stream);
+    if (out == kB128F32) return launch_few<NT, kB128F32>(A, B, p, split, stream);
+    return launch_few<NT, kB128Add>(A, B, p, split, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_b128_few(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p, int out,
+                            int nt, int split, cudaStream_t stream) {
+    if (out == kB128Gated)
+        return nt == 16 ? launch_few<16, kB128Gated>(A, B, p, split, stream)
+                        : launch_few<32, kB128Gated>(A, B, p, split, stream);
+    return nt == 16   ? few_out<16>(A, B, p, out, split, stream)
+           : nt == 32 ? few_out<32>(A, B, p, out, split, stream)
+                      : few_out<64>(A, B, p, out, split, stream);
+}
+
+}  // namespace fp8g

@@ -1,0 +1,527 @@
+// Products with fp32 scales for blocks of 128 on CTA pairs, sm_103a:
+//
+//   C[i, j] = sum_kb sa[kb][i] sb(kb, j) P_kb[i, j],  P_kb = sum_{k in kb} a_ik b_kj
+//
+// and the gated projection pair that ends in 8 bits,
+//   g = x Wg^T, u = x Wu^T, h = act(g) u  ->  codes and scales of h (and of g, u).
+//
+// The tensor core takes no fp32 scales, so each K block's unscaled product P_kb
+// goes to one of two 256-column tensor-memory buffers (kind::f8f6f4, the first of
+// its four MMAs overwrites) and eight promotion warps per CTA add it, scaled, to
+// fp32 registers while the MMAs of the next K block fill the other buffer.  One K
+// block of a pair's 256 x 256 tile takes the tensor cores 512 cycles; a promotion
+// warp's 32 x 128 share is 4 tensor-memory loads of 32 columns and 64 packed FMAs
+// where one scale serves its 128 columns (128 x 128 tiles of B), with the FMA pipe
+// half busy.  With a scale per column (weight gradients) each pair of values costs
+// a multiplication too, and the pipe is as busy as the tensor core.
+//
+// Operands lie either way.  Contraction contiguous: 128 B rows of the 128-byte
+// swizzle, an MMA's 32 values 32 B apart.  M (N) contiguous: the tile's 128 rows are
+// the K values, an MMA's 32 of them 4 KB apart, and the instruction descriptor's
+// major bit is set.  In both the eight-row swizzle atoms follow each other (1 KB),
+// so the weights serve the forward product and the input gradient as they lie, and
+// activations the forward product and the weight gradient.
+//
+// Roles (384 threads): warp 0 TMA producer (both CTAs, their own halves), warp 1 of
+// the even CTA MMA issue, warp 2 copies B's scale vectors where there are any, warps
+// 4-11 promotion and epilogue: lane quarter warp & 3, half of the columns.  They
+// hold 128 accumulators a thread, so registers move to them (setmaxnreg: 256 x 216
+// + 128 x 72 = 384 x 168).  Scales are read three K blocks ahead, straight to
+// registers.  Every wait is bounded.
+#include <cuda_bf16.h>
+
+#include "block128.h"
+#include "block128_math.cuh"
+#include "kernel_common.cuh"
+#include "ptx.cuh"
+
+namespace fp8g {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kProm0 = 4;              // first promotion warp
+constexpr int kPromWarps = 8;
+constexpr int kRegsLaunch = 168, kRegsProm = 216, kRegsRest = 72;
+static_assert(32 * kPromWarps * kRegsProm + 128 * kRegsRest <= kThreads * kRegsLaunch,
+              "setmaxnreg draws on the block's own registers");
+constexpr int kTile = kBlk * kBlk;     // bytes of an operand tile of one CTA
+constexpr int kVecStages = 4;          // K blocks of B's scale vectors in flight
+constexpr int kVecBytes = 2 * kBlk * 4;
+
+template <bool VECB>
+struct Lay {
+    static constexpr int STAGES = 6;
+    static constexpr int OFF_B = STAGES * kTile;
+    static constexpr int OFF_VEC = 2 * STAGES * kTile;
+    static constexpr int OFF_X = OFF_VEC + (VECB ? kVecStages * kVecBytes : 0);  // row maxima: [2][2][128] float4
+    static constexpr int OFF_BAR = OFF_X + 2 * 2 * kBlk * 16;
+    // full, empty [STAGES]; product full, product empty [2]; vector full, empty
+    // [kVecStages]; row maxima [lane quarter][half]; drain
+    static constexpr int NUM_BARS = 2 * STAGES + 4 + 2 * kVecStages + 8 + 1;
+    static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+    static constexpr int BYTES = OFF_MISC + 16 + 1024;
+    static_assert(BYTES <= 232448, "shared memory over the per-CTA limit");
+};
+
+__device__ __forceinline__ bool wait_bar_cluster(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                                 const B128Params &p, unsigned detail) {
+    if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
+    const uint64_t t0 = ptx::globaltimer();
+    while (true) {
+        if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (ptx::globaltimer() - t0 > p.timeout_ns) {
+            *abort_flag = 1;
+            record_error(p, FP8G_ERR_TIMEOUT, detail);
+            return false;
+        }
+    }
+}
+
+// Scales of a K block for one lane: its row of A, its warp's one or two 128-column
+// blocks of B (1 for vectors, which go through shared memory).
+struct Scales {
+    float a, b0, b1;
+};
+
+template <bool VECB, int OUT>
+struct ScaleSource {
+    const float *a, *b0, *b1;
+    __device__ __forceinline__ void tile(const B128Params &p, int64_t row, int pn, int half) {
+        a = p.sa + min(row, p.M - 1);
+        if constexpr (!VECB) {
+            const int64_t n = OUT == kB128Gated ? pn : min(2 * pn + half, p.n_blocks - 1);
+            b0 = p.sb + n * p.sb_n;
+            b1 = p.sb + (n + p.n_blocks) * p.sb_n;
+        }
+    }
+    __device__ __forceinline__ Scales at(const B128Params &p, int kb) const {
+        Scales s{0.0f, 1.0f, 1.0f};
+        if (kb < p.num_kb) {
+            s.a = __ldg(a + kb * p.M);
+            if constexpr (!VECB) {
+                s.b0 = __ldg(b0 + kb * p.sb_k);
+                if constexpr (OUT == kB128Gated) s.b1 = __ldg(b1 + kb * p.sb_k);
+            }
+        }
+        return s;
+    }
+};
+
+// 64 codes of one row from 64 values times r, 16-byte stores (dst 16-byte aligned).
+__device__ __forceinline__ void store_codes64(uint8_t *dst, const float (&v)[64], float r) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        uint4 o;
+        o.x = b128_codes<FP8G_E4M3>(v[16 * w], v[16 * w + 1], v[16 * w + 2], v[16 * w + 3], r);
+        o.y = b128_codes<FP8G_E4M3>(v[16 * w + 4], v[16 * w + 5], v[16 * w + 6], v[16 * w + 7], r);
+        o.z = b128_codes<FP8G_E4M3>(v[16 * w + 8], v[16 * w + 9], v[16 * w + 10], v[16 * w + 11], r);
+        o.w = b128_codes<FP8G_E4M3>(v[16 * w + 12], v[16 * w + 13], v[16 * w + 14], v[16 * w + 15], r);
+        reinterpret_cast<uint4 *>(dst)[w] = o;
+    }
+}
+
+__device__ __forceinline__ float amax64(const float (&v)[64]) {
+    float m[4] = {};
+#pragma unroll
+    for (int i = 0; i < 64; ++i) m[i & 3] = fmaxf(m[i & 3], fabsf(v[i]));
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+template <bool VECB, int OUT>
+__global__ void __launch_bounds__(kThreads, 1)
+    b128_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                     const B128Params p) {
+    using L = Lay<VECB>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_base = ptx::smem_addr(smem_raw);
+    uint8_t *smem = smem_raw + ((1024u - (raw_base & 1023u)) & 1023u);
+    const uint32_t sbase = ptx::smem_addr(smem);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = ptx::cluster_rank();
+    const bool leader = rank == 0;
+
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
+    auto bar_full = [&](int s) { return ptx::smem_addr(&bars[s]); };
+    auto bar_empty = [&](int s) { return ptx::smem_addr(&bars[L::STAGES + s]); };
+    auto bar_pfull = [&](int b) { return ptx::smem_addr(&bars[2 * L::STAGES + b]); };
+    auto bar_pempty = [&](int b) { return ptx::smem_addr(&bars[2 * L::STAGES + 2 + b]); };
+    auto bar_vfull = [&](int s) { return ptx::smem_addr(&bars[2 * L::STAGES + 4 + s]); };
+    auto bar_vempty = [&](int s) { return ptx::smem_addr(&bars[2 * L::STAGES + 4 + kVecStages + s]); };
+    auto bar_max = [&](int q, int h) {
+        return ptx::smem_addr(&bars[2 * L::STAGES + 4 + 2 * kVecStages + 2 * q + h]);
+    };
+    const uint32_t bar_drain = ptx::smem_addr(&bars[L::NUM_BARS - 1]);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
+
+    // ------------------------------------------------------------ setup
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < L::STAGES; ++s) {
+            ptx::mbar_init(bar_full(s), 1);
+            ptx::mbar_init(bar_empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(bar_pfull(b), 1);
+            ptx::mbar_init(bar_pempty(b), 2 * kPromWarps);
+        }
+        for (int s = 0; s < kVecStages; ++s) {
+            ptx::mbar_init(bar_vfull(s), 1);
+            ptx::mbar_init(bar_vempty(s), kPromWarps);
+        }
+        for (int i = 0; i < 8; ++i) ptx::mbar_init(bar_max(i >> 1, i & 1), 1);
+        ptx::mbar_init(bar_drain, 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        ptx::prefetch_tmap(&tmA);
+        ptx::prefetch_tmap(&tmB);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(ptx::smem_addr(tmem_slot), 512);
+        ptx::tmem_relinquish_pair();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_sync();  // both CTAs' barriers and tensor memory exist
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    if (tmem_base != 0u && threadIdx.x == 0) {  // all 512 columns: they begin at 0 in both CTAs
+        record_error(p, FP8G_ERR_DEVICE, 0xA11Cu);
+        *abort_flag = 1;
+    }
+    ptx::grid_dep_wait();  // global memory only after the previous kernel
+    ptx::grid_dep_launch();
+    __syncthreads();
+    const int32_t t_first = *abort_flag ? p.T : (int32_t)ptx::cluster_id_x();
+    const int32_t t_step = (int32_t)ptx::num_clusters_x();
+
+    // (each in its own branch: the compiler allots a branch's registers by it)
+    if (warp < kProm0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+        if (warp == 0) {
+            // ===== TMA producer: both CTAs' copies complete on the even CTA's barrier =====
+            if (lane == 0) {
+                uint32_t stage = 0, phase = 0;
+                for (int32_t t = t_first; t < p.T; t += t_step) {
+                    int32_t pm, pn;
+                    raster(t, p.npm, p.npn, kRasterG, pm, pn);
+                    const int32_t m0 = (2 * pm + (int32_t)rank) * kBlk, n0 = (2 * pn + (int32_t)rank) * kBlk;
+                    for (int kb = 0; kb < p.num_kb; ++kb) {
+                        if (!wait_bar(bar_empty(stage), phase ^ 1u, abort_flag, p, 0 * 256 + stage)) goto roles_done;
+                        const uint32_t fb = leader ? bar_full(stage) : ptx::map_shared(bar_full(stage), 0);
+                        if (leader) ptx::mbar_arrive_expect_tx(fb, 4 * kTile);
+                        const int32_t k0 = kb * kBlk;
+                        ptx::tma_load_2d_pair(sbase + stage * kTile, &tmA, fb, p.a_mn ? m0 : k0, p.a_mn ? k0 : m0);
+                        if constexpr (OUT == kB128Gated)  // gate rows to the even CTA, up rows to the odd one
+                            ptx::tma_load_3d_pair(sbase + L::OFF_B + stage * kTile, &tmB, fb, k0, pn * kBlk, (int32_t)rank);
+                        else
+                            ptx::tma_load_2d_pair(sbase + L::OFF_B + stage * kTile, &tmB, fb, p.b_mn ? n0 : k0,
+                                                  p.b_mn ? k0 : n0);
+                        if (++stage == L::STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+            }
+        } else if (warp == 1 && leader) {
+            // ===== MMA issue (even CTA): 256 x 256 x 32 per instruction =====
+            if (lane == 0) {
+                const uint32_t idesc = ptx::idesc_f8(2 * kBlk, 2 * kBlk) | p.types;
+                const uint32_t a_step = p.a_mn ? 32 * kBlk : 32, b_step = p.b_mn ? 32 * kBlk : 32;
+                uint32_t stage = 0, phase = 0, g = 0;
+                for (int32_t t = t_first; t < p.T; t += t_step) {
+                    for (int kb = 0; kb < p.num_kb; ++kb, ++g) {
+                        const uint32_t buf = g & 1u;
+                        if (!wait_bar_cluster(bar_pempty(buf), ((g >> 1) & 1u) ^ 1u, abort_flag, p, 1 * 256 + 64 + buf))
+                            goto roles_done;
+                        if (!wait_bar(bar_full(stage), phase, abort_flag, p, 1 * 256 + stage)) goto roles_done;
+                        ptx::tc_fence_after();
+                        const uint32_t a0 = sbase + stage * kTile, b0 = sbase + L::OFF_B + stage * kTile;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            ptx::mma_f8_pair(buf * 2 * kBlk, ptx::smem_desc(a0 + k * a_step, 1024, 1024, 2),
+                                             ptx::smem_desc(b0 + k * b_step, 1024, 1024, 2), idesc, k != 0 ? 1u : 0u);
+                        ptx::tc_commit_pair_mc(bar_pfull(buf), 0x3);
+                        ptx::tc_commit_pair_mc(bar_empty(stage), 0x3);
+                        if (++stage == L::STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+            }
+        } else if (VECB && warp == 2) {
+            // ===== B's scale vectors: 256 columns of each K block =====
+            if (lane == 0) {
+                uint32_t s = 0, phase = 0;
+                for (int32_t t = t_first; t < p.T; t += t_step) {
+                    int32_t pm, pn;
+                    raster(t, p.npm, p.npn, kRasterG, pm, pn);
+                    const int64_t n0 = (int64_t)pn * 2 * kBlk;
+                    const uint32_t bytes = (uint32_t)min((int64_t)2 * kBlk, p.N - n0) * 4u;  // (N a multiple of 16)
+                    for (int kb = 0; kb < p.num_kb; ++kb) {
+                        if (!wait_bar(bar_vempty(s), phase ^ 1u, abort_flag, p, 2 * 256 + s)) goto roles_done;
+                        ptx::mbar_arrive_expect_tx(bar_vfull(s), bytes);
+                        ptx::bulk_load(sbase + L::OFF_VEC + s * kVecBytes, p.sb + kb * p.N + n0, bytes, bar_vfull(s));
+                        if (++s == kVecStages) {
+                            s = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+            }
+        }
+    } else {
+        // ===== promotion and epilogue: this CTA's 128 rows =====
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsProm));
+        const int q = warp & 3, half = (warp - kProm0) >> 2;
+        // first tensor-memory column of this warp's 32-column chunk c: half of the 256;
+        // gated: the same 64 columns of gate (chunks 0, 1) and of up (2, 3)
+        auto chunk = [&](int c) {
+            return OUT == kB128Gated ? (c >> 1) * kBlk + half * 64 + (c & 1) * 32 : half * kBlk + c * 32;
+        };
+        const uint32_t lane_base = (uint32_t)(q * 32) << 16;
+        const int row_in = (int)rank * kBlk + q * 32 + lane;
+        uint32_t g = 0, vs = 0, vphase = 0, lt = 0;
+        int32_t pm = 0, pn = 0;
+        ScaleSource<VECB, OUT> src;
+        Scales s0{}, s1{}, s2{};
+        auto begin = [&](int32_t t) {
+            raster(t, p.npm, p.npn, kRasterG, pm, pn);
+            src.tile(p, (int64_t)pm * 2 * kBlk + row_in, pn, half);
+            s0 = src.at(p, 0);
+            s1 = src.at(p, 1);
+            s2 = src.at(p, 2);
+        };
+        if (t_first < p.T) begin(t_first);
+        for (int32_t t = t_first; t < p.T; t += t_step, ++lt) {
+            uint64_t acc[4][16];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[c][i] = 0ull;
+            bool ok = true;
+            for (int kb = 0; kb < p.num_kb; ++kb, ++g) {
+                const Scales s = s0;
+                s0 = s1;
+                s1 = s2;
+                s2 = src.at(p, kb + 3);
+                const uint32_t buf = g & 1u;
+                if constexpr (VECB) {
+                    if (!wait_bar_warp(bar_vfull(vs), vphase, abort_flag, p, 3 * 256 + 32 + vs)) {
+                        ok = false;
+                        break;
+                    }
+                }
+                if (!wait_bar_warp(bar_pfull(buf), (g >> 1) & 1u, abort_flag, p, 3 * 256 + 64 + buf)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t tm = lane_base + buf * 2 * kBlk;
+                auto add = [&](int c, const uint32_t(&r)[32]) {
+                    if constexpr (VECB) {
+                        const ulonglong2 *sb = reinterpret_cast<const ulonglong2 *>(
+                            smem + L::OFF_VEC + vs * kVecBytes + chunk(c) * 4);
+                        const uint64_t sa = b128_pair(s.a, s.a);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const ulonglong2 b = sb[i];  // the same address in every lane
+                            b128_fma2(acc[c][2 * i], b128_pair(r[4 * i], r[4 * i + 1]), b128_mul2(sa, b.x));
+                            b128_fma2(acc[c][2 * i + 1], b128_pair(r[4 * i + 2], r[4 * i + 3]), b128_mul2(sa, b.y));
+                        }
+                    } else {
+                        const float f = __fmul_rn(s.a, OUT == kB128Gated && c >= 2 ? s.b1 : s.b0);
+                        const uint64_t ff = b128_pair(f, f);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) b128_fma2(acc[c][i], b128_pair(r[2 * i], r[2 * i + 1]), ff);
+                    }
+                };
+                // a chunk's load runs beside the FMAs of the one before
+                uint32_t r0[32], r1[32];
+                ptx::tmem_ld_32x32b_x32(tm + chunk(0), r0);
+                ptx::tmem_ld_wait();
+                ptx::tmem_ld_32x32b_x32(tm + chunk(1), r1);
+                add(0, r0);
+                ptx::tmem_ld_wait();
+                ptx::tmem_ld_32x32b_x32(tm + chunk(2), r0);
+                add(1, r1);
+                ptx::tmem_ld_wait();
+                ptx::tmem_ld_32x32b_x32(tm + chunk(3), r1);
+                add(2, r0);
+                ptx::tmem_ld_wait();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_shared(bar_pempty(buf), 0));
+                add(3, r1);
+                if constexpr (VECB) {
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar_vempty(vs));
+                    if (++vs == kVecStages) {
+                        vs = 0;
+                        vphase ^= 1u;
+                    }
+                }
+            }
+            if (!ok) break;
+            const int64_t row = (int64_t)pm * 2 * kBlk + row_in;
+            const int32_t tn = pn;
+            if (t + t_step < p.T) begin(t + t_step);  // the next tile's first scales
+
+            if constexpr (OUT != kB128Gated) {
+                const int64_t n0 = (int64_t)tn * 2 * kBlk + half * kBlk;
+                if (row < p.M) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t r[32];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            r[2 * i] = (uint32_t)acc[c][i];
+                            r[2 * i + 1] = (uint32_t)(acc[c][i] >> 32);
+                        }
+                        const int64_t n = n0 + c * 32;
+                        if constexpr (OUT == kB128Add) {
+                            const float4 *old = reinterpret_cast<const float4 *>(static_cast<float *>(p.C) + row * p.N + n);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (n + 4 * i < p.N) {
+                                    const float4 v = __ldcs(old + i);
+                                    r[4 * i] = __float_as_uint(__uint_as_float(r[4 * i]) + v.x);
+                                    r[4 * i + 1] = __float_as_uint(__uint_as_float(r[4 * i + 1]) + v.y);
+                                    r[4 * i + 2] = __float_as_uint(__uint_as_float(r[4 * i + 2]) + v.z);
+                                    r[4 * i + 3] = __float_as_uint(__uint_as_float(r[4 * i + 3]) + v.w);
+                                }
+                        }
+                        store_row32<OUT != kB128Bf16>(p.C, row, p.N, n, r, 1.0f, p.st32 != 0);
+                    }
+                }
+            } else {
+                // h in the gate's place; a row's maxima from the two warps that share it
+                float gv[64], uv[64], h[64];
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        gv[c * 32 + 2 * i] = b128_lo(acc[c][i]);
+                        gv[c * 32 + 2 * i + 1] = b128_hi(acc[c][i]);
+                        uv[c * 32 + 2 * i] = b128_lo(acc[c + 2][i]);
+                        uv[c * 32 + 2 * i + 1] = b128_hi(acc[c + 2][i]);
+                    }
+                const bool keep = p.gu != nullptr;
+                float4 top = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int i = 0; i < 64; ++i) h[i] = __fmul_rn(b128_gate(gv[i], p.gate), uv[i]);
+                top.x = amax64(h);
+                if (keep) {
+                    top.y = amax64(gv);
+                    top.z = amax64(uv);
+                }
+                // [tile parity][half][row]: a slot is written again two tiles later, after
+                // its reader's next arrival
+                float4 *x = reinterpret_cast<float4 *>(smem + L::OFF_X) + (lt & 1) * 2 * kBlk;
+                x[half * kBlk + q * 32 + lane] = top;
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar_max(q, half));
+                if (!wait_bar_warp(bar_max(q, half ^ 1), lt & 1u, abort_flag, p, 3 * 256 + 96 + q)) break;
+                const float4 o = x[(half ^ 1) * kBlk + q * 32 + lane];
+                if (row < p.M) {
+                    const int64_t F = p.N, f = (int64_t)tn * kBlk + half * 64;
+                    const float sh = b128_scale<FP8G_E4M3>(fmaxf(top.x, o.x));
+                    store_codes64(p.h + row * F + f, h, __frcp_rn(sh));
+                    if (half == 0) p.sh[tn * p.M + row] = sh;
+                    if (keep) {
+                        const float sg = b128_scale<FP8G_E4M3>(fmaxf(top.y, o.y));
+                        const float su = b128_scale<FP8G_E4M3>(fmaxf(top.z, o.z));
+                        store_codes64(p.gu + row * 2 * F + f, gv, __frcp_rn(sg));
+                        store_codes64(p.gu + row * 2 * F + F + f, uv, __frcp_rn(su));
+                        if (half == 0) {
+                            p.sgu[tn * p.M + row] = sg;
+                            p.sgu[(p.n_blocks + tn) * p.M + row] = su;
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+roles_done:
+    __syncwarp();
+    __syncthreads();
+    if (*abort_flag) {
+        // drain the MMAs that are in flight, give copies a bounded time to land
+        if (leader && warp == 1 && lane == 0) {
+            ptx::tc_commit_pair(bar_drain);
+            const uint64_t t0 = ptx::globaltimer();
+            while (!ptx::mbar_try_wait(bar_drain, 0) && ptx::globaltimer() - t0 < p.timeout_ns) {
+            }
+        }
+        const uint64_t t0 = ptx::globaltimer();
+        while (ptx::globaltimer() - t0 < 200000ull) {
+        }
+        __syncthreads();
+    }
+    // neither CTA leaves while the other may still arrive on its barriers
+    ptx::cluster_sync();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+template <bool VECB, int OUT>
+cudaError_t launch_pair(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p, int grid,
+                        cudaStream_t stream) {
+    auto kern = b128_pair_kernel<VECB, OUT>;
+    static unsigned long long done = 0ull;  // devices on which the kernel was set up
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if ((done & bit) == 0ull) {
+        // setmaxnreg.inc takes from what the block was launched with
+        cudaFuncAttributes fa;
+        if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+        if (fa.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
+        e = b128_allow_smem(reinterpret_cast<const void *>(kern), Lay<VECB>::BYTES);
+        if (e != cudaSuccess) return e;
+        done |= bit;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Lay<VECB>::BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, A, B, p);
+}
+
+}  // namespace
+
+cudaError_t launch_b128_pair(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p,
+                             int out, bool vec_b, int num_sms, cudaStream_t stream) {
+    const int grid = 2 * (int)min((int64_t)p.T, (int64_t)num_sms / 2);
+    if (out == kB128Gated) return launch_pair<false, kB128Gated>(A, B, p, grid, stream);
+    if (vec_b) {
+        if (out == kB128Bf16) return launch_pair<true, kB128Bf16>(A, B, p, grid, stream);
+        return out == kB128F32 ? launch_pair<true, kB128F32>(A, B, p, grid, stream)
+                               : launch_pair<true, kB128Add>(A, B, p, grid, stream);
+    }
+    if (out == kB128Bf16) return launch_pair<false, kB128Bf16>(A, B, p, grid, stream);
+    return out == kB128F32 ? launch_pair<false, kB128F32>(A, B, p, grid, stream)
+                           : launch_pair<false, kB128Add>(A, B, p, grid, stream);
+}
+
+}  // namespace fp8g

@@ -1,0 +1,125 @@
+// Arithmetic shared by the block-128 kernels: the scale rule, code conversion
+// of four values, gate activations, packed fp32 pairs.
+#pragma once
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "fp8gemm.h"
+#include "quant_math.cuh"
+
+namespace fp8g {
+
+// Scale of a block from its largest magnitude (not NaN): amax / largest value of
+// the format, at least 2^-126 so that its reciprocal is finite, 1 for zeros.  A
+// block with an infinity has an infinite scale and NaN products.
+template <int FMT>
+__device__ __forceinline__ float b128_scale(float amax) {
+    const float s = __fdiv_rn(amax, Fp8Fmt<FMT>::kMax);
+    return s == 0.0f && amax == 0.0f ? 1.0f : fmaxf(s, 1.17549435e-38f);
+}
+
+// Codes of four values, first value lowest; NaN gives the code 0x7F.
+template <int FMT>
+__device__ __forceinline__ uint32_t b128_cvt4(float a, float b, float c, float d) {
+    uint16_t lo, hi;
+    if constexpr (FMT == 0) {
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    } else {
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    }
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+template <int FMT>
+__device__ __forceinline__ uint32_t b128_codes(float a, float b, float c, float d, float r) {
+    return b128_cvt4<FMT>(__fmul_rn(a, r), __fmul_rn(b, r), __fmul_rn(c, r), __fmul_rn(d, r));
+}
+template <int FMT>
+__device__ __forceinline__ uint32_t b128_codes4(const float (&v)[4], const float (&r)[4]) {
+    return b128_cvt4<FMT>(__fmul_rn(v[0], r[0]), __fmul_rn(v[1], r[1]), __fmul_rn(v[2], r[2]), __fmul_rn(v[3], r[3]));
+}
+
+// Four codes -> fp32 (exact).
+__device__ __forceinline__ void b128_decode(uint32_t q, int fmt, float (&v)[4]) {
+    uint32_t lo, hi;
+    if (fmt == FP8G_E4M3) {
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"((uint16_t)q));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(q >> 16)));
+    } else {
+        asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(lo) : "h"((uint16_t)q));
+        asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(q >> 16)));
+    }
+    const uint32_t w[2] = {lo, hi};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+            : "=f"(v[2 * i]), "=f"(v[2 * i + 1])
+            : "r"(w[i]));
+    }
+}
+
+// Largest magnitude of four values; NaN counts as 0.
+__device__ __forceinline__ float b128_amax4(float a, float b, float c, float d) {
+    return fmaxf(fmaxf(fmaxf(fabsf(a), fabsf(b)), fmaxf(fabsf(c), fabsf(d))), 0.0f);
+}
+
+// Largest of the warp's values (>= 0, not NaN: their bits are in order).
+__device__ __forceinline__ float b128_warp_max(float v) {
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+}
+
+// 1 / (1 + e^-g), from the hardware's base-2 exponential and reciprocal (relative
+// error about 2^-22 (1 + |g| / 4), beside the 2^-4 of the codes that it ends in; the
+// exact division took the gated epilogue twice the instructions).
+__device__ __forceinline__ float b128_sigmoid(float g) {
+    float e, y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(1.0f + e));
+    return y;
+}
+
+__device__ __forceinline__ float b128_gate(float g, int gate) {
+    if (gate == FP8G_GATE_SILU) return g * b128_sigmoid(g);
+    if (gate == FP8G_GATE_GELU) return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
+    return g < 0.0f ? 0.0f : g;
+}
+
+// The activation's value and its derivative.
+__device__ __forceinline__ void b128_gate_grad(float g, int gate, float &y, float &d) {
+    if (gate == FP8G_GATE_SILU) {
+        const float s = b128_sigmoid(g);
+        y = g * s;
+        d = s * (1.0f + g * (1.0f - s));
+    } else if (gate == FP8G_GATE_GELU) {
+        const float c = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
+        float e;
+        asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(g * g * -0.72134752044448170f));
+        y = g * c;
+        d = c + g * e * 0.39894228040143268f;
+    } else {
+        y = g < 0.0f ? 0.0f : g;
+        d = g > 0.0f ? 1.0f : (isnan(g) ? g : 0.0f);
+    }
+}
+
+// Packed pairs of fp32 (lo first).
+__device__ __forceinline__ uint64_t b128_pair(float lo, float hi) {
+    return (uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32);
+}
+__device__ __forceinline__ uint64_t b128_pair(uint32_t lo, uint32_t hi) {
+    return (uint64_t)lo | ((uint64_t)hi << 32);
+}
+__device__ __forceinline__ float b128_lo(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float b128_hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+// d += a b.  Volatile: it stays behind the wait for the tensor-memory load of a.
+__device__ __forceinline__ void b128_fma2(uint64_t &d, uint64_t a, uint64_t b) {
+    asm volatile("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ uint64_t b128_mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+}  // namespace fp8g

@@ -615,6 +615,98 @@ FP8G_API fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void *W
                                    int64_t K, cudaStream_t stream);
 
 /*
+ * Operators with fp32 scales for blocks of 128 (the source pages' block scaling
+ * with coarser blocks and no power-of-two rule; they print no such kernel).
+ * Codes are E4M3 or E5M2, one byte each, top = 448 or 57344.  A scale is
+ *   along rows     s[j * R + r]  of the 128 values x[r][128 j ..]
+ *   along columns  s[i * C + c]  of the 128 values x[128 i ..][c]
+ *   of a tile      s[i * ceil(C/128) + j] of the 128 x 128 values
+ * of a matrix [R, C]: fp32, amax / top of the block (blocks at an edge are cut
+ * short), at least 2^-126, 1 for a block of zeros; code = FP8(fl32(x fl32(1 / s))),
+ * nearest even, saturating.  NaN has the code 0x7F and does not count for amax; a
+ * block with an infinity has an infinite scale, and its products are NaN.
+ */
+
+/*
+ * x (fp32 or bf16 per in_dtype) [rows, cols], rows ld elements apart -> codes
+ * [rows, cols] with scales along rows (q_row, s_row) and / or along columns
+ * (q_col, s_col), from one reading; a pair may be null, not both.  rows may be 0.
+ * cols % 16 == 0, rows <= 65535 * 128, else FP8G_ERR_UNSUPPORTED_SHAPE; pointers
+ * and rows of x 16-byte aligned.  One kernel.
+ * fp8g_quantize_tile128: the same with a scale per tile (weights).
+ */
+FP8G_API fp8g_status fp8g_quantize_block128(const void *x, int32_t in_dtype, int64_t ld, int64_t rows,
+                                            int64_t cols, int32_t fmt, uint8_t *q_row, float *s_row,
+                                            uint8_t *q_col, float *s_col, cudaStream_t stream);
+FP8G_API fp8g_status fp8g_quantize_tile128(const void *x, int32_t in_dtype, int64_t ld, int64_t rows,
+                                           int64_t cols, int32_t fmt, uint8_t *q, float *s,
+                                           cudaStream_t stream);
+
+/*
+ * 8-bit checkpoint of an activation for the weight gradient: codes q [rows, cols]
+ * of q_fmt with scales along rows -> codes of fmt with scales along columns, of
+ * the values fl32(dec(q) s).  q_col does not overlap q.  Rules as above.
+ */
+FP8G_API fp8g_status fp8g_requantize_block128(const uint8_t *q, int32_t q_fmt, const float *s, int64_t rows,
+                                              int64_t cols, int32_t fmt, uint8_t *q_col, float *s_col,
+                                              cudaStream_t stream);
+
+/*
+ * Which axis of the stored operands is summed over.
+ *   FP8G_NT  C[M, N] = A[M, K] B[N, K]^T   forward: A along rows, B in tiles
+ *   FP8G_NN  C[M, N] = A[M, K] B[K, N]     input gradient: A along rows, B in tiles (the
+ *                                          forward product's weights as they lie)
+ *   FP8G_TN  C[M, N] = A[K, M]^T B[K, N]   weight gradient: both along columns
+ */
+typedef enum { FP8G_NT = 0, FP8G_NN = 1, FP8G_TN = 2 } fp8g_form;
+
+/*
+ * Product of operands with block-128 scales sfa, sfb (laid out as the quantisers
+ * above give them for the operands as they are stored):
+ *   C = out( sum over K blocks of  sa sb (sum of 128 products) )
+ * fp32 sums.  a_fmt, b_fmt: FP8G_E4M3 or FP8G_E5M2.  C bf16 or fp32 per `out`; add
+ * = 1 (fp32 only) adds the product to what C holds.  M may be 0 (NT, NN), and K
+ * with FP8G_TN (C is zeroed, or kept with add).
+ * K % 16 == 0 (NT, NN), M % 16 == 0 (TN), N % 16 == 0 (NN, TN), N * sizeof(out
+ * element) % 16 == 0, pointers 16-byte aligned, else FP8G_ERR_ALIGNMENT.  Results
+ * do not vary between runs.  One kernel, no workspace; fp8g_kernel_timing_begin
+ * does not record it.
+ */
+FP8G_API fp8g_status fp8_gemm_block128(int32_t form, const void *A, const float *sfa, int32_t a_fmt,
+                                       const void *B, const float *sfb, int32_t b_fmt, void *C, int out,
+                                       int32_t add, int64_t M, int64_t N, int64_t K, cudaStream_t stream);
+
+/*
+ * Gated projection pair of a feed-forward layer, in one kernel:
+ *   g = x . W13[0..F)^T,  u = x . W13[F..2F)^T,  h = act(g) u     (fp32)
+ * x [M, K] with scales along rows, W13 [2F, K] in tiles, gate as for
+ * fp8_moe_layer.  h [M, F]: E4M3 codes with scales sh along rows, what
+ * fp8_gemm_block128 takes for the down projection.  gu [M, 2F] and sgu (both or
+ * neither): g and u in E4M3 with scales along rows, the checkpoint for
+ * fp8g_gated_block128_backward.  F % 128 == 0, else FP8G_ERR_UNSUPPORTED_SHAPE;
+ * K % 16 == 0, pointers 16-byte aligned, else FP8G_ERR_ALIGNMENT.  M may be 0.
+ */
+FP8G_API fp8g_status fp8_gated_block128(const void *x, const float *sfx, int32_t x_fmt, const void *W13,
+                                        const float *sf13, int32_t w_fmt, int32_t gate, uint8_t *h,
+                                        float *sh, uint8_t *gu, float *sgu, int64_t M, int64_t F,
+                                        int64_t K, cudaStream_t stream);
+
+/*
+ * Backward of h = act(g) u from the checkpoint and dh [M, F] (fp32 or bf16):
+ *   dg = dh u act'(g),  du = dh act(g)
+ * dgu [M, 2F] in fmt along rows (dgu_row, s_row: for the input gradient) and along
+ * columns (dgu_col, s_col: for W13's gradient), and h [M, F] in E4M3 along columns
+ * (h_col, sh_col: for the down weights' gradient), the forward pass's h need not be
+ * kept.  ReLU's derivative at 0 is 0.  F % 128 == 0, M <= 65535 * 128, else
+ * FP8G_ERR_UNSUPPORTED_SHAPE; pointers 16-byte aligned.  M may be 0.  One kernel.
+ */
+FP8G_API fp8g_status fp8g_gated_block128_backward(const void *dh, int32_t dh_dtype, const uint8_t *gu,
+                                                  const float *sgu, int32_t gate, int32_t fmt, int64_t M,
+                                                  int64_t F, uint8_t *dgu_row, float *s_row,
+                                                  uint8_t *dgu_col, float *s_col, uint8_t *h_col,
+                                                  float *sh_col, cudaStream_t stream);
+
+/*
  * Synchronises `stream`, then returns and clears the current device's status
  * word (FP8G_OK if no kernel recorded an error since the last call).
  * `detail` (nullable) receives a kernel-specific code for the first error
