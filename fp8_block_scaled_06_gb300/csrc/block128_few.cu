@@ -199,15 +199,15 @@ __global__ void __launch_bounds__(kThreads, 2)
                 uint32_t r[STEP];
                 if constexpr (STEP == 32) {
                     ptx::tmem_ld_32x32b_x32(lane_base + tmem_base + buf * L::COLS + c, r);
+                    ptx::tmem_ld_wait(r);
                 } else {
                     uint32_t a[8], b[8];
                     ptx::tmem_ld_32x32b_x8(lane_base + tmem_base + buf * L::COLS + c, a);
                     ptx::tmem_ld_32x32b_x8(lane_base + tmem_base + buf * L::COLS + c + 8, b);
-                    ptx::tmem_ld_wait();
+                    ptx::tmem_ld_wait(a, b);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) r[i] = a[i], r[8 + i] = b[i];
                 }
-                ptx::tmem_ld_wait();
                 const ulonglong2 *s2 = reinterpret_cast<const ulonglong2 *>(s + c);
 #pragma unroll
                 for (int i = 0; i < STEP / 4; ++i) {

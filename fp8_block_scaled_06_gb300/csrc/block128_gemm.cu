@@ -23,11 +23,14 @@
 // activations the forward product and the weight gradient.
 //
 // Roles (384 threads): warp 0 TMA producer (both CTAs, their own halves), warp 1 of
-// the even CTA MMA issue, warp 2 copies B's scale vectors where there are any, warps
-// 4-11 promotion and epilogue: lane quarter warp & 3, half of the columns.  They
+// the even CTA MMA issue, warps 4-11 promotion and epilogue: lane quarter warp & 3,
+// half of the columns.  They
 // hold 128 accumulators a thread, so registers move to them (setmaxnreg: 256 x 216
-// + 128 x 72 = 384 x 168).  Scales are read three K blocks ahead, straight to
-// registers.  Every wait is bounded.
+// + 128 x 72 = 384 x 168).  Scales are read up to three K blocks ahead, straight to
+// registers; column vectors then pass through shared memory of the warp's own, to be
+// read as broadcasts.  A warp's arrival that frees a buffer is relaxed: with release
+// semantics it waited for the scale loads in flight too (2500 instead of  cycles a K
+// block).  Every wait is bounded.
 #include <cuda_bf16.h>
 
 #include "block128.h"
@@ -46,19 +49,18 @@ constexpr int kRegsLaunch = 168, kRegsProm = 216, kRegsRest = 72;
 static_assert(32 * kPromWarps * kRegsProm + 128 * kRegsRest <= kThreads * kRegsLaunch,
               "setmaxnreg draws on the block's own registers");
 constexpr int kTile = kBlk * kBlk;     // bytes of an operand tile of one CTA
-constexpr int kVecStages = 4;          // K blocks of B's scale vectors in flight
-constexpr int kVecBytes = 2 * kBlk * 4;
+constexpr int kVecBytes = 2 * kBlk * 4;  // two K blocks of a warp's 128 column scales
 
 template <bool VECB>
 struct Lay {
     static constexpr int STAGES = 6;
     static constexpr int OFF_B = STAGES * kTile;
     static constexpr int OFF_VEC = 2 * STAGES * kTile;
-    static constexpr int OFF_X = OFF_VEC + (VECB ? kVecStages * kVecBytes : 0);  // row maxima: [2][2][128] float4
+    static constexpr int OFF_X = OFF_VEC + (VECB ? kPromWarps * kVecBytes : 0);  // row maxima: [2][2][128] float4
     static constexpr int OFF_BAR = OFF_X + 2 * 2 * kBlk * 16;
-    // full, empty [STAGES]; product full, product empty [2]; vector full, empty
-    // [kVecStages]; row maxima [lane quarter][half]; drain
-    static constexpr int NUM_BARS = 2 * STAGES + 4 + 2 * kVecStages + 8 + 1;
+    // full, empty [STAGES]; product full, product empty [2]; row maxima [lane
+    // quarter][half]; drain
+    static constexpr int NUM_BARS = 2 * STAGES + 4 + 8 + 1;
     static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
     static constexpr int BYTES = OFF_MISC + 16 + 1024;
     static_assert(BYTES <= 232448, "shared memory over the per-CTA limit");
@@ -90,7 +92,9 @@ struct ScaleSource {
     const float *a, *b0, *b1;
     __device__ __forceinline__ void tile(const B128Params &p, int64_t row, int pn, int half) {
         a = p.sa + min(row, p.M - 1);
-        if constexpr (!VECB) {
+        if constexpr (VECB) {  // four columns a lane (N is a multiple of 16)
+            b0 = p.sb + min(((int64_t)2 * pn + half) * kBlk + 4 * (threadIdx.x & 31), p.N - 4);
+        } else {
             const int64_t n = OUT == kB128Gated ? pn : min(2 * pn + half, p.n_blocks - 1);
             b0 = p.sb + n * p.sb_n;
             b1 = p.sb + (n + p.n_blocks) * p.sb_n;
@@ -106,6 +110,9 @@ struct ScaleSource {
             }
         }
         return s;
+    }
+    __device__ __forceinline__ float4 vector(const B128Params &p, int kb) const {
+        return kb < p.num_kb ? __ldg(reinterpret_cast<const float4 *>(b0 + kb * p.N)) : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
     }
 };
 
@@ -148,11 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto bar_empty = [&](int s) { return ptx::smem_addr(&bars[L::STAGES + s]); };
     auto bar_pfull = [&](int b) { return ptx::smem_addr(&bars[2 * L::STAGES + b]); };
     auto bar_pempty = [&](int b) { return ptx::smem_addr(&bars[2 * L::STAGES + 2 + b]); };
-    auto bar_vfull = [&](int s) { return ptx::smem_addr(&bars[2 * L::STAGES + 4 + s]); };
-    auto bar_vempty = [&](int s) { return ptx::smem_addr(&bars[2 * L::STAGES + 4 + kVecStages + s]); };
-    auto bar_max = [&](int q, int h) {
-        return ptx::smem_addr(&bars[2 * L::STAGES + 4 + 2 * kVecStages + 2 * q + h]);
-    };
+    auto bar_max = [&](int q, int h) { return ptx::smem_addr(&bars[2 * L::STAGES + 4 + 2 * q + h]); };
     const uint32_t bar_drain = ptx::smem_addr(&bars[L::NUM_BARS - 1]);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
@@ -166,10 +169,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(bar_pfull(b), 1);
             ptx::mbar_init(bar_pempty(b), 2 * kPromWarps);
-        }
-        for (int s = 0; s < kVecStages; ++s) {
-            ptx::mbar_init(bar_vfull(s), 1);
-            ptx::mbar_init(bar_vempty(s), kPromWarps);
         }
         for (int i = 0; i < 8; ++i) ptx::mbar_init(bar_max(i >> 1, i & 1), 1);
         ptx::mbar_init(bar_drain, 1);
@@ -255,26 +254,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-        } else if (VECB && warp == 2) {
-            // ===== B's scale vectors: 256 columns of each K block =====
-            if (lane == 0) {
-                uint32_t s = 0, phase = 0;
-                for (int32_t t = t_first; t < p.T; t += t_step) {
-                    int32_t pm, pn;
-                    raster(t, p.npm, p.npn, kRasterG, pm, pn);
-                    const int64_t n0 = (int64_t)pn * 2 * kBlk;
-                    const uint32_t bytes = (uint32_t)min((int64_t)2 * kBlk, p.N - n0) * 4u;  // (N a multiple of 16)
-                    for (int kb = 0; kb < p.num_kb; ++kb) {
-                        if (!wait_bar(bar_vempty(s), phase ^ 1u, abort_flag, p, 2 * 256 + s)) goto roles_done;
-                        ptx::mbar_arrive_expect_tx(bar_vfull(s), bytes);
-                        ptx::bulk_load(sbase + L::OFF_VEC + s * kVecBytes, p.sb + kb * p.N + n0, bytes, bar_vfull(s));
-                        if (++s == kVecStages) {
-                            s = 0;
-                            phase ^= 1u;
-                        }
-                    }
-                }
-            }
         }
     } else {
         // ===== promotion and epilogue: this CTA's 128 rows =====
@@ -287,16 +266,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         const uint32_t lane_base = (uint32_t)(q * 32) << 16;
         const int row_in = (int)rank * kBlk + q * 32 + lane;
-        uint32_t g = 0, vs = 0, vphase = 0, lt = 0;
+        uint32_t g = 0, lt = 0;
         int32_t pm = 0, pn = 0;
         ScaleSource<VECB, OUT> src;
         Scales s0{}, s1{}, s2{};
+        float *cols = reinterpret_cast<float *>(smem + L::OFF_VEC) + (warp - kProm0) * 2 * kBlk;  // VECB: this warp's
+        float4 vec{}, vec0{};
         auto begin = [&](int32_t t) {
             raster(t, p.npm, p.npn, kRasterG, pm, pn);
             src.tile(p, (int64_t)pm * 2 * kBlk + row_in, pn, half);
             s0 = src.at(p, 0);
             s1 = src.at(p, 1);
             s2 = src.at(p, 2);
+            if constexpr (VECB) {
+                vec0 = src.vector(p, 0);
+                vec = src.vector(p, 1);
+            }
         };
         if (t_first < p.T) begin(t_first);
         for (int32_t t = t_first; t < p.T; t += t_step, ++lt) {
@@ -305,6 +290,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 4; ++c)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[c][i] = 0ull;
+            if constexpr (VECB) {
+                reinterpret_cast<float4 *>(cols)[lane] = vec0;
+                __syncwarp();
+            }
             bool ok = true;
             for (int kb = 0; kb < p.num_kb; ++kb, ++g) {
                 const Scales s = s0;
@@ -312,12 +301,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s1 = s2;
                 s2 = src.at(p, kb + 3);
                 const uint32_t buf = g & 1u;
-                if constexpr (VECB) {
-                    if (!wait_bar_warp(bar_vfull(vs), vphase, abort_flag, p, 3 * 256 + 32 + vs)) {
-                        ok = false;
-                        break;
-                    }
-                }
+                // scale vectors: the next K block's are in registers since the last one, the
+                // one's after it are asked for now
+                const float4 v = vec;
+                if constexpr (VECB) vec = src.vector(p, kb + 2);
                 if (!wait_bar_warp(bar_pfull(buf), (g >> 1) & 1u, abort_flag, p, 3 * 256 + 64 + buf)) {
                     ok = false;
                     break;
@@ -326,8 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t tm = lane_base + buf * 2 * kBlk;
                 auto add = [&](int c, const uint32_t(&r)[32]) {
                     if constexpr (VECB) {
-                        const ulonglong2 *sb = reinterpret_cast<const ulonglong2 *>(
-                            smem + L::OFF_VEC + vs * kVecBytes + chunk(c) * 4);
+                        const ulonglong2 *sb = reinterpret_cast<const ulonglong2 *>(cols + (kb & 1) * kBlk + 32 * c);
                         const uint64_t sa = b128_pair(s.a, s.a);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
@@ -345,27 +331,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // a chunk's load runs beside the FMAs of the one before
                 uint32_t r0[32], r1[32];
                 ptx::tmem_ld_32x32b_x32(tm + chunk(0), r0);
-                ptx::tmem_ld_wait();
+                ptx::tmem_ld_wait(r0);
                 ptx::tmem_ld_32x32b_x32(tm + chunk(1), r1);
                 add(0, r0);
-                ptx::tmem_ld_wait();
+                ptx::tmem_ld_wait(r1);
                 ptx::tmem_ld_32x32b_x32(tm + chunk(2), r0);
                 add(1, r1);
-                ptx::tmem_ld_wait();
+                ptx::tmem_ld_wait(r0);
                 ptx::tmem_ld_32x32b_x32(tm + chunk(3), r1);
                 add(2, r0);
-                ptx::tmem_ld_wait();
+                ptx::tmem_ld_wait(r1);
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_shared(bar_pempty(buf), 0));
+                if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::map_shared(bar_pempty(buf), 0));
                 add(3, r1);
                 if constexpr (VECB) {
+                    reinterpret_cast<float4 *>(cols + (~kb & 1) * kBlk)[lane] = v;
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(bar_vempty(vs));
-                    if (++vs == kVecStages) {
-                        vs = 0;
-                        vphase ^= 1u;
-                    }
                 }
             }
             if (!ok) break;

@@ -112,9 +112,9 @@ __device__ __forceinline__ uint64_t b128_pair(uint32_t lo, uint32_t hi) {
 }
 __device__ __forceinline__ float b128_lo(uint64_t v) { return __uint_as_float((uint32_t)v); }
 __device__ __forceinline__ float b128_hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
-// d += a b.  Volatile: it stays behind the wait for the tensor-memory load of a.
+// d += a b
 __device__ __forceinline__ void b128_fma2(uint64_t &d, uint64_t a, uint64_t b) {
-    asm volatile("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
 }
 __device__ __forceinline__ uint64_t b128_mul2(uint64_t a, uint64_t b) {
     uint64_t d;
