@@ -25,8 +25,8 @@
 // Roles (384 threads): warp 0 TMA producer (both CTAs, their own halves), warp 1 of
 // the even CTA MMA issue, warps 4-11 promotion and epilogue: lane quarter warp & 3,
 // half of the columns.  They
-// hold 128 accumulators a thread, so registers move to them (setmaxnreg: 256 x 216
-// + 128 x 72 = 384 x 168).  Scales are read up to three K blocks ahead, straight to
+// hold 128 accumulators a thread, so registers move to them (setmaxnreg: 256 x 232
+// + 128 x 40 = 384 x 168).  Scales are read up to three K blocks ahead, straight to
 // registers; column vectors then pass through shared memory of the warp's own, to be
 // read as broadcasts.  A warp's arrival that frees a buffer is relaxed: with release
 // semantics it waited for the scale loads in flight too (2500 instead of  cycles a K
@@ -45,22 +45,26 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kProm0 = 4;              // first promotion warp
 constexpr int kPromWarps = 8;
-constexpr int kRegsLaunch = 168, kRegsProm = 216, kRegsRest = 72;
+constexpr int kRegsLaunch = 168, kRegsProm = 232, kRegsRest = 40;
 static_assert(32 * kPromWarps * kRegsProm + 128 * kRegsRest <= kThreads * kRegsLaunch,
               "setmaxnreg draws on the block's own registers");
 constexpr int kTile = kBlk * kBlk;     // bytes of an operand tile of one CTA
-constexpr int kVecBytes = 2 * kBlk * 4;  // two K blocks of a warp's 128 column scales
+constexpr int kBufs = 2;               // product buffers of 256 columns
 
 template <bool VECB>
 struct Lay {
-    static constexpr int STAGES = 6;
+    static constexpr int STAGES = VECB ? 5 : 6;
     static constexpr int OFF_B = STAGES * kTile;
-    static constexpr int OFF_VEC = 2 * STAGES * kTile;
-    static constexpr int OFF_X = OFF_VEC + (VECB ? kPromWarps * kVecBytes : 0);  // row maxima: [2][2][128] float4
-    static constexpr int OFF_BAR = OFF_X + 2 * 2 * kBlk * 16;
-    // full, empty [STAGES]; product full, product empty [2]; row maxima [lane
+    // a promotion warp's scales of CH K blocks: A's [CH][32 lanes], then B's [CH][128
+    // columns] or [CH][two tiles]; two such buffers a warp
+    static constexpr int CH = VECB ? 4 : 8;
+    static constexpr int SCALES = CH * (32 + (VECB ? kBlk : 2));
+    static constexpr int OFF_S = 2 * STAGES * kTile;
+    static constexpr int OFF_X = OFF_S + kPromWarps * 2 * SCALES * 4;  // row maxima: [2][2][128] float4
+    static constexpr int OFF_BAR = OFF_X + (VECB ? 0 : 2 * 2 * kBlk * 16);
+    // full, empty [STAGES]; product full, product empty [kBufs]; row maxima [lane
     // quarter][half]; drain
-    static constexpr int NUM_BARS = 2 * STAGES + 4 + 8 + 1;
+    static constexpr int NUM_BARS = 2 * STAGES + 2 * kBufs + 8 + 1;
     static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
     static constexpr int BYTES = OFF_MISC + 16 + 1024;
     static_assert(BYTES <= 232448, "shared memory over the per-CTA limit");
@@ -68,10 +72,10 @@ struct Lay {
 
 __device__ __forceinline__ bool wait_bar_cluster(uint32_t bar, uint32_t parity, volatile int *abort_flag,
                                                  const B128Params &p, unsigned detail) {
-    if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
+    if (ptx::mbar_try_wait_cluster_relaxed(bar, parity)) return true;
     const uint64_t t0 = ptx::globaltimer();
     while (true) {
-        if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
+        if (ptx::mbar_try_wait_cluster_relaxed(bar, parity)) return true;
         if (*abort_flag) return false;
         if (ptx::globaltimer() - t0 > p.timeout_ns) {
             *abort_flag = 1;
@@ -81,38 +85,42 @@ __device__ __forceinline__ bool wait_bar_cluster(uint32_t bar, uint32_t parity, 
     }
 }
 
-// Scales of a K block for one lane: its row of A, its warp's one or two 128-column
-// blocks of B (1 for vectors, which go through shared memory).
-struct Scales {
-    float a, b0, b1;
-};
-
+// The scales of a promotion warp, copied (cp.async) to shared memory of its own, CH K
+// blocks at a time and one such chunk ahead: waiting for a copy and asking for the next
+// cost a K block 230 cycles where each had its own.  (In registers, handed on from one
+// K block to the next, each handing on waited for the newest load.)
 template <bool VECB, int OUT>
-struct ScaleSource {
-    const float *a, *b0, *b1;
+struct ScaleChunks {
+    using L = Lay<VECB>;
+    float *buf;          // [2][SCALES]
+    const float *a, *b;  // this lane's row of A; columns of B, or one of its two tiles
     __device__ __forceinline__ void tile(const B128Params &p, int64_t row, int pn, int half) {
+        const int lane = threadIdx.x & 31;
         a = p.sa + min(row, p.M - 1);
         if constexpr (VECB) {  // four columns a lane (N is a multiple of 16)
-            b0 = p.sb + min(((int64_t)2 * pn + half) * kBlk + 4 * (threadIdx.x & 31), p.N - 4);
+            b = p.sb + min((int64_t)pn * 2 * kBlk + half * 64 + 4 * lane + (lane >= 16 ? 64 : 0), p.N - 4);
         } else {
-            const int64_t n = OUT == kB128Gated ? pn : min(2 * pn + half, p.n_blocks - 1);
-            b0 = p.sb + n * p.sb_n;
-            b1 = p.sb + (n + p.n_blocks) * p.sb_n;
+            const int64_t n0 = OUT == kB128Gated ? pn : 2 * pn;
+            const int64_t n1 = OUT == kB128Gated ? n0 + p.n_blocks : min(n0 + 1, (int64_t)p.n_blocks - 1);
+            b = p.sb + ((lane & 1) == 0 ? n0 : n1) * p.sb_n;
         }
     }
-    __device__ __forceinline__ Scales at(const B128Params &p, int kb) const {
-        Scales s{0.0f, 1.0f, 1.0f};
-        if (kb < p.num_kb) {
-            s.a = __ldg(a + kb * p.M);
-            if constexpr (!VECB) {
-                s.b0 = __ldg(b0 + kb * p.sb_k);
-                if constexpr (OUT == kB128Gated) s.b1 = __ldg(b1 + kb * p.sb_k);
+    // K blocks kb .. kb + CH - 1 of the tile to buffer i
+    __device__ __forceinline__ void ask(const B128Params &p, int kb, uint32_t i) const {
+        const int lane = threadIdx.x & 31;
+        const uint32_t at = ptx::smem_addr(buf + (i & 1u) * L::SCALES);
+#pragma unroll
+        for (int j = 0; j < L::CH; ++j)
+            if (kb + j < p.num_kb) {
+                ptx::cp_async_4(at + (j * 32 + lane) * 4, a + (kb + j) * p.M, 4);
+                if constexpr (VECB)
+                    ptx::cp_async_16(at + (L::CH * 32 + j * kBlk + 4 * lane) * 4, b + (kb + j) * p.N, 16);
             }
+        if constexpr (!VECB) {
+            if (lane < 2 * L::CH && kb + (lane >> 1) < p.num_kb)
+                ptx::cp_async_4(at + (L::CH * 32 + lane) * 4, b + (kb + (lane >> 1)) * p.sb_k, 4);
         }
-        return s;
-    }
-    __device__ __forceinline__ float4 vector(const B128Params &p, int kb) const {
-        return kb < p.num_kb ? __ldg(reinterpret_cast<const float4 *>(b0 + kb * p.N)) : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+        ptx::cp_async_commit();
     }
 };
 
@@ -154,8 +162,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto bar_full = [&](int s) { return ptx::smem_addr(&bars[s]); };
     auto bar_empty = [&](int s) { return ptx::smem_addr(&bars[L::STAGES + s]); };
     auto bar_pfull = [&](int b) { return ptx::smem_addr(&bars[2 * L::STAGES + b]); };
-    auto bar_pempty = [&](int b) { return ptx::smem_addr(&bars[2 * L::STAGES + 2 + b]); };
-    auto bar_max = [&](int q, int h) { return ptx::smem_addr(&bars[2 * L::STAGES + 4 + 2 * q + h]); };
+    auto bar_pempty = [&](int b) { return ptx::smem_addr(&bars[2 * L::STAGES + kBufs + b]); };
+    auto bar_max = [&](int q, int h) { return ptx::smem_addr(&bars[2 * L::STAGES + 2 * kBufs + 2 * q + h]); };
     const uint32_t bar_drain = ptx::smem_addr(&bars[L::NUM_BARS - 1]);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
@@ -166,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(bar_full(s), 1);
             ptx::mbar_init(bar_empty(s), 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kBufs; ++b) {
             ptx::mbar_init(bar_pfull(b), 1);
             ptx::mbar_init(bar_pempty(b), 2 * kPromWarps);
         }
@@ -236,11 +244,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int32_t t = t_first; t < p.T; t += t_step) {
                     for (int kb = 0; kb < p.num_kb; ++kb, ++g) {
                         const uint32_t buf = g & 1u;
+                        if (!wait_bar(bar_full(stage), phase, abort_flag, p, 1 * 256 + stage)) goto roles_done;
+                        const uint32_t a0 = sbase + stage * kTile, b0 = sbase + L::OFF_B + stage * kTile;
                         if (!wait_bar_cluster(bar_pempty(buf), ((g >> 1) & 1u) ^ 1u, abort_flag, p, 1 * 256 + 64 + buf))
                             goto roles_done;
-                        if (!wait_bar(bar_full(stage), phase, abort_flag, p, 1 * 256 + stage)) goto roles_done;
                         ptx::tc_fence_after();
-                        const uint32_t a0 = sbase + stage * kTile, b0 = sbase + L::OFF_B + stage * kTile;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             ptx::mma_f8_pair(buf * 2 * kBlk, ptx::smem_desc(a0 + k * a_step, 1024, 1024, 2),
@@ -259,96 +267,84 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ===== promotion and epilogue: this CTA's 128 rows =====
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsProm));
         const int q = warp & 3, half = (warp - kProm0) >> 2;
-        // first tensor-memory column of this warp's 32-column chunk c: half of the 256;
-        // gated: the same 64 columns of gate (chunks 0, 1) and of up (2, 3)
-        auto chunk = [&](int c) {
-            return OUT == kB128Gated ? (c >> 1) * kBlk + half * 64 + (c & 1) * 32 : half * kBlk + c * 32;
-        };
-        const uint32_t lane_base = (uint32_t)(q * 32) << 16;
+        // tensor-memory column of this warp's chunk c: 64 columns of the tile's first
+        // block of B (gated: of gate) and the same 64 of its second (of up)
+        const uint32_t lane_base = ((uint32_t)(q * 32) << 16) + half * 64;
+        auto chunk = [&](uint32_t i, int c) { return lane_base + (i & 1u) * 2 * kBlk + (c >> 1) * kBlk + (c & 1) * 32; };
+        const uint32_t free0 = ptx::map_shared(bar_pempty(0), 0), free1 = ptx::map_shared(bar_pempty(1), 0);
         const int row_in = (int)rank * kBlk + q * 32 + lane;
         uint32_t g = 0, lt = 0;
         int32_t pm = 0, pn = 0;
-        ScaleSource<VECB, OUT> src;
-        Scales s0{}, s1{}, s2{};
-        float *cols = reinterpret_cast<float *>(smem + L::OFF_VEC) + (warp - kProm0) * 2 * kBlk;  // VECB: this warp's
-        float4 vec{}, vec0{};
+        uint32_t chunks = 0;  // of scales, over all tiles
+        ScaleChunks<VECB, OUT> scales;
+        scales.buf = reinterpret_cast<float *>(smem + L::OFF_S) + (warp - kProm0) * 2 * L::SCALES;
         auto begin = [&](int32_t t) {
             raster(t, p.npm, p.npn, kRasterG, pm, pn);
-            src.tile(p, (int64_t)pm * 2 * kBlk + row_in, pn, half);
-            s0 = src.at(p, 0);
-            s1 = src.at(p, 1);
-            s2 = src.at(p, 2);
-            if constexpr (VECB) {
-                vec0 = src.vector(p, 0);
-                vec = src.vector(p, 1);
-            }
+            scales.tile(p, (int64_t)pm * 2 * kBlk + row_in, pn, half);
+            scales.ask(p, 0, chunks);
         };
         if (t_first < p.T) begin(t_first);
         for (int32_t t = t_first; t < p.T; t += t_step, ++lt) {
-            uint64_t acc[4][16];
+            float acc[4][32];
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) acc[c][i] = 0ull;
-            if constexpr (VECB) {
-                reinterpret_cast<float4 *>(cols)[lane] = vec0;
-                __syncwarp();
-            }
+                for (int i = 0; i < 32; ++i) acc[c][i] = 0.0f;
+            uint32_t r0[32], r1[32];
             bool ok = true;
             for (int kb = 0; kb < p.num_kb; ++kb, ++g) {
-                const Scales s = s0;
-                s0 = s1;
-                s1 = s2;
-                s2 = src.at(p, kb + 3);
                 const uint32_t buf = g & 1u;
-                // scale vectors: the next K block's are in registers since the last one, the
-                // one's after it are asked for now
-                const float4 v = vec;
-                if constexpr (VECB) vec = src.vector(p, kb + 2);
-                if (!wait_bar_warp(bar_pfull(buf), (g >> 1) & 1u, abort_flag, p, 3 * 256 + 64 + buf)) {
+                if (kb % L::CH == 0) {
+                    ptx::cp_async_wait<0>();
+                    __syncwarp();  // this chunk is there for every lane, and the one before it read by all
+                    ++chunks;
+                    if (kb + L::CH < p.num_kb) scales.ask(p, kb + L::CH, chunks);
+                }
+                const float *sc = scales.buf + (~chunks & 1u) * L::SCALES;
+                const float sa = sc[kb % L::CH * 32 + lane];
+                float2 sb{};
+                if constexpr (!VECB) sb = *reinterpret_cast<const float2 *>(sc + L::CH * 32 + kb % L::CH * 2);
+                auto add = [&](int c, const uint32_t(&r)[32]) {
+                    if constexpr (VECB) {
+                        const float4 *col = reinterpret_cast<const float4 *>(sc + L::CH * 32 + kb % L::CH * kBlk + 32 * c);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 b = col[i];  // the same address in every lane
+                            acc[c][4 * i] = __fmaf_rn(__uint_as_float(r[4 * i]), __fmul_rn(sa, b.x), acc[c][4 * i]);
+                            acc[c][4 * i + 1] = __fmaf_rn(__uint_as_float(r[4 * i + 1]), __fmul_rn(sa, b.y), acc[c][4 * i + 1]);
+                            acc[c][4 * i + 2] = __fmaf_rn(__uint_as_float(r[4 * i + 2]), __fmul_rn(sa, b.z), acc[c][4 * i + 2]);
+                            acc[c][4 * i + 3] = __fmaf_rn(__uint_as_float(r[4 * i + 3]), __fmul_rn(sa, b.w), acc[c][4 * i + 3]);
+                        }
+                    } else {
+                        const float f = __fmul_rn(sa, c >= 2 ? sb.y : sb.x);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) acc[c][i] = __fmaf_rn(__uint_as_float(r[i]), f, acc[c][i]);
+                    }
+                };
+                // From here to the arrival the buffer is kept from the MMAs of the K block after
+                // next: two chunks are loaded at a time (64 registers), the next two as soon as
+                // theirs are free, and everything else comes before or behind.
+                if (!__all_sync(0xffffffffu, ptx::mbar_try_wait(bar_pfull(buf), (g >> 1) & 1u)) &&
+                    !wait_bar_warp(bar_pfull(buf), (g >> 1) & 1u, abort_flag, p, 3 * 256 + 64 + buf)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
-                const uint32_t tm = lane_base + buf * 2 * kBlk;
-                auto add = [&](int c, const uint32_t(&r)[32]) {
-                    if constexpr (VECB) {
-                        const ulonglong2 *sb = reinterpret_cast<const ulonglong2 *>(cols + (kb & 1) * kBlk + 32 * c);
-                        const uint64_t sa = b128_pair(s.a, s.a);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const ulonglong2 b = sb[i];  // the same address in every lane
-                            b128_fma2(acc[c][2 * i], b128_pair(r[4 * i], r[4 * i + 1]), b128_mul2(sa, b.x));
-                            b128_fma2(acc[c][2 * i + 1], b128_pair(r[4 * i + 2], r[4 * i + 3]), b128_mul2(sa, b.y));
-                        }
-                    } else {
-                        const float f = __fmul_rn(s.a, OUT == kB128Gated && c >= 2 ? s.b1 : s.b0);
-                        const uint64_t ff = b128_pair(f, f);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) b128_fma2(acc[c][i], b128_pair(r[2 * i], r[2 * i + 1]), ff);
-                    }
-                };
-                // a chunk's load runs beside the FMAs of the one before
-                uint32_t r0[32], r1[32];
-                ptx::tmem_ld_32x32b_x32(tm + chunk(0), r0);
+                ptx::tmem_ld_32x32b_x32(chunk(g, 0), r0);
+                ptx::tmem_ld_32x32b_x32(chunk(g, 1), r1);
                 ptx::tmem_ld_wait(r0);
-                ptx::tmem_ld_32x32b_x32(tm + chunk(1), r1);
-                add(0, r0);
                 ptx::tmem_ld_wait(r1);
-                ptx::tmem_ld_32x32b_x32(tm + chunk(2), r0);
+                add(0, r0);
+                ptx::tmem_ld_32x32b_x32(chunk(g, 2), r0);
                 add(1, r1);
+                ptx::tmem_ld_32x32b_x32(chunk(g, 3), r1);
                 ptx::tmem_ld_wait(r0);
-                ptx::tmem_ld_32x32b_x32(tm + chunk(3), r1);
-                add(2, r0);
                 ptx::tmem_ld_wait(r1);
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::map_shared(bar_pempty(buf), 0));
+                ptx::mbar_arrive_cluster_relaxed(buf ? free1 : free0, lane == 0);
+                add(2, r0);
                 add(3, r1);
-                if constexpr (VECB) {
-                    reinterpret_cast<float4 *>(cols + (~kb & 1) * kBlk)[lane] = v;
-                    __syncwarp();
-                }
             }
             if (!ok) break;
             const int64_t row = (int64_t)pm * 2 * kBlk + row_in;
@@ -356,17 +352,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (t + t_step < p.T) begin(t + t_step);  // the next tile's first scales
 
             if constexpr (OUT != kB128Gated) {
-                const int64_t n0 = (int64_t)tn * 2 * kBlk + half * kBlk;
+                const int64_t n0 = (int64_t)tn * 2 * kBlk + half * 64;
                 if (row < p.M) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t r[32];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            r[2 * i] = (uint32_t)acc[c][i];
-                            r[2 * i + 1] = (uint32_t)(acc[c][i] >> 32);
-                        }
-                        const int64_t n = n0 + c * 32;
+                        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(acc[c][i]);
+                        const int64_t n = n0 + (c >> 1) * kBlk + (c & 1) * 32;
                         if constexpr (OUT == kB128Add) {
                             const float4 *old = reinterpret_cast<const float4 *>(static_cast<float *>(p.C) + row * p.N + n);
 #pragma unroll
@@ -388,11 +381,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        gv[c * 32 + 2 * i] = b128_lo(acc[c][i]);
-                        gv[c * 32 + 2 * i + 1] = b128_hi(acc[c][i]);
-                        uv[c * 32 + 2 * i] = b128_lo(acc[c + 2][i]);
-                        uv[c * 32 + 2 * i + 1] = b128_hi(acc[c + 2][i]);
+                    for (int i = 0; i < 32; ++i) {
+                        gv[c * 32 + i] = acc[c][i];
+                        uv[c * 32 + i] = acc[c + 2][i];
                     }
                 const bool keep = p.gu != nullptr;
                 float4 top = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
