@@ -70,19 +70,14 @@ struct Lay {
     static_assert(BYTES <= 232448, "shared memory over the per-CTA limit");
 };
 
-__device__ __forceinline__ bool wait_bar_cluster(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                                 const B128Params &p, unsigned detail) {
-    if (ptx::mbar_try_wait_cluster_relaxed(bar, parity)) return true;
-    const uint64_t t0 = ptx::globaltimer();
-    while (true) {
-        if (ptx::mbar_try_wait_cluster_relaxed(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (ptx::globaltimer() - t0 > p.timeout_ns) {
-            *abort_flag = 1;
-            record_error(p, FP8G_ERR_TIMEOUT, detail);
-            return false;
-        }
-    }
+// Bounded wait of a whole warp, for a phase that orders no memory of this proxy by
+// itself (tcgen05.commit, TMA, the relaxed arrivals): every lane asks, which is
+// quicker than one lane's answer handed round; a wait that runs long goes on in
+// wait_bar_warp.
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int *abort_flag, const B128Params &p,
+                                         unsigned detail) {
+    return __all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity)) ||
+           wait_bar_warp(bar, parity, abort_flag, p, detail);
 }
 
 // The scales of a promotion warp, copied (cp.async) to shared memory of its own, CH K
@@ -237,28 +232,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == 1 && leader) {
             // ===== MMA issue (even CTA): 256 x 256 x 32 per instruction =====
-            if (lane == 0) {
-                const uint32_t idesc = ptx::idesc_f8(2 * kBlk, 2 * kBlk) | p.types;
-                const uint32_t a_step = p.a_mn ? 32 * kBlk : 32, b_step = p.b_mn ? 32 * kBlk : 32;
-                uint32_t stage = 0, phase = 0, g = 0;
-                for (int32_t t = t_first; t < p.T; t += t_step) {
-                    for (int kb = 0; kb < p.num_kb; ++kb, ++g) {
-                        const uint32_t buf = g & 1u;
-                        if (!wait_bar(bar_full(stage), phase, abort_flag, p, 1 * 256 + stage)) goto roles_done;
-                        const uint32_t a0 = sbase + stage * kTile, b0 = sbase + L::OFF_B + stage * kTile;
-                        if (!wait_bar_cluster(bar_pempty(buf), ((g >> 1) & 1u) ^ 1u, abort_flag, p, 1 * 256 + 64 + buf))
-                            goto roles_done;
-                        ptx::tc_fence_after();
+            // The whole warp runs the loop and one elected lane issues: from a branch of one
+            // lane's own the four MMAs took 500 cycles to issue, in the chain from a buffer's
+            // release to its next product.
+            const uint32_t idesc = ptx::idesc_f8(2 * kBlk, 2 * kBlk) | p.types;
+            const uint32_t a_step = (p.a_mn ? 32 * kBlk : 32) >> 4, b_step = (p.b_mn ? 32 * kBlk : 32) >> 4;
+            const uint64_t a_desc = ptx::smem_desc(sbase, 1024, 1024, 2);
+            const uint64_t b_desc = ptx::smem_desc(sbase + L::OFF_B, 1024, 1024, 2);
+            uint32_t stage = 0, phase = 0, g = 0;
+            for (int32_t t = t_first; t < p.T; t += t_step) {
+                for (int kb = 0; kb < p.num_kb; ++kb, ++g) {
+                    const uint32_t buf = g & 1u;
+                    if (!wait_all(bar_full(stage), phase, abort_flag, p, 1 * 256 + stage)) goto roles_done;
+                    if (!wait_all(bar_pempty(buf), ((g >> 1) & 1u) ^ 1u, abort_flag, p, 1 * 256 + 64 + buf))
+                        goto roles_done;
+                    ptx::tc_fence_after();
+                    const uint64_t a0 = a_desc + stage * (kTile >> 4), b0 = b_desc + stage * (kTile >> 4);
+                    if (ptx::elect_one()) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            ptx::mma_f8_pair(buf * 2 * kBlk, ptx::smem_desc(a0 + k * a_step, 1024, 1024, 2),
-                                             ptx::smem_desc(b0 + k * b_step, 1024, 1024, 2), idesc, k != 0 ? 1u : 0u);
+                            ptx::mma_f8_pair(buf * 2 * kBlk, a0 + k * a_step, b0 + k * b_step, idesc, k != 0 ? 1u : 0u);
                         ptx::tc_commit_pair_mc(bar_pfull(buf), 0x3);
                         ptx::tc_commit_pair_mc(bar_empty(stage), 0x3);
-                        if (++stage == L::STAGES) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
+                    }
+                    __syncwarp();
+                    if (++stage == L::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
                     }
                 }
             }
@@ -324,8 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // From here to the arrival the buffer is kept from the MMAs of the K block after
                 // next: two chunks are loaded at a time (64 registers), the next two as soon as
                 // theirs are free, and everything else comes before or behind.
-                if (!__all_sync(0xffffffffu, ptx::mbar_try_wait(bar_pfull(buf), (g >> 1) & 1u)) &&
-                    !wait_bar_warp(bar_pfull(buf), (g >> 1) & 1u, abort_flag, p, 3 * 256 + 64 + buf)) {
+                if (!wait_all(bar_pfull(buf), (g >> 1) & 1u, abort_flag, p, 3 * 256 + 64 + buf)) {
                     ok = false;
                     break;
                 }
