@@ -15,7 +15,8 @@ SOURCES = ["gemm.cu", "gemm_pair.cu", "gemm_promote.cu", "scales.cu", "quant.cu"
            "noalloc.cu", "selftest.cu", "route.cu", "stream.cu", "moe.cu", "lora.cu",
            "block128.cu", "block128_quant.cu", "block128_gemm.cu", "block128_few.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "kernel_common.cuh", "quant_math.cuh", "stream.h", "lora_value.cuh",
-           "lora_pieces.cuh", "block128.h", "block128_math.cuh"]
+           "lora_pieces.cuh", "block128.h", "block128_math.cuh",
+           "block128_wait.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -20,7 +20,7 @@
 
 #include "block128.h"
 #include "block128_math.cuh"
-#include "kernel_common.cuh"
+#include "block128_wait.cuh"
 #include "ptx.cuh"
 
 namespace fp8g {
@@ -122,32 +122,34 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = ptx::idesc_f8(kBlk, NT) | p.types;
-            const uint32_t w_step = p.b_mn ? 32 * kBlk : 32;
-            uint32_t stage = 0, phase = 0, buf = 0, bphase = 0;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!wait_bar(bar_pempty(buf), bphase ^ 1u, abort_flag, p, 1 * 256 + 64 + buf)) break;
-                if (!wait_bar(bar_full(stage), phase, abort_flag, p, 1 * 256 + stage)) break;
-                ptx::tc_fence_after();
-                const uint32_t w0 = sbase + stage * L::STAGE, x0 = w0 + L::G * kTile;
+        // (whole warp, one elected lane: block128_gemm.cu)
+        const uint32_t idesc = ptx::idesc_f8(kBlk, NT) | p.types;
+        const uint32_t w_step = (p.b_mn ? 32 * kBlk : 32) >> 4;
+        const uint64_t w_desc = ptx::smem_desc(sbase, 1024, 1024, 2);
+        uint32_t stage = 0, phase = 0, buf = 0, bphase = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!b128_wait_all(bar_full(stage), phase, abort_flag, p, 1 * 256 + stage)) break;
+            if (!b128_wait_all(bar_pempty(buf), bphase ^ 1u, abort_flag, p, 1 * 256 + 64 + buf)) break;
+            ptx::tc_fence_after();
+            const uint64_t w0 = w_desc + stage * (L::STAGE >> 4), x0 = w0 + (L::G * kTile >> 4);
+            if (ptx::elect_one()) {
 #pragma unroll
                 for (int g = 0; g < L::G; ++g)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        ptx::mma_f8(tmem_base + buf * L::COLS + g * NT,
-                                    ptx::smem_desc(w0 + g * kTile + k * w_step, 1024, 1024, 2),
-                                    ptx::smem_desc(x0 + k * 32, 1024, 1024, 2), idesc, k != 0 ? 1u : 0u);
+                        ptx::mma_f8(tmem_base + buf * L::COLS + g * NT, w0 + (g * kTile >> 4) + k * w_step, x0 + k * 2,
+                                    idesc, k != 0 ? 1u : 0u);
                 ptx::tc_commit(bar_pfull(buf));
                 ptx::tc_commit(bar_empty(stage));
-                if (++stage == L::STAGES) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-                if (++buf == L::BUFS) {
-                    buf = 0;
-                    bphase ^= 1u;
-                }
+            }
+            __syncwarp();
+            if (++stage == L::STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+            if (++buf == L::BUFS) {
+                buf = 0;
+                bphase ^= 1u;
             }
         }
     } else if (warp >= 4) {
@@ -188,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (mine[j]) s[g * NT + lane + 32 * j] = __fmul_rn(na[j], nb[g]);
             fetch(kb + 1);
             __syncwarp();
-            if (!wait_bar_warp(bar_pfull(buf), bphase, abort_flag, p, 3 * 256 + 64 + buf)) {
+            if (!b128_wait_all(bar_pfull(buf), bphase, abort_flag, p, 3 * 256 + 64 + buf)) {
                 ok = false;
                 break;
             }

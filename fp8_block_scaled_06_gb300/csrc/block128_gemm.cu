@@ -35,7 +35,7 @@
 
 #include "block128.h"
 #include "block128_math.cuh"
-#include "kernel_common.cuh"
+#include "block128_wait.cuh"
 #include "ptx.cuh"
 
 namespace fp8g {
@@ -69,16 +69,6 @@ struct Lay {
     static constexpr int BYTES = OFF_MISC + 16 + 1024;
     static_assert(BYTES <= 232448, "shared memory over the per-CTA limit");
 };
-
-// Bounded wait of a whole warp, for a phase that orders no memory of this proxy by
-// itself (tcgen05.commit, TMA, the relaxed arrivals): every lane asks, which is
-// quicker than one lane's answer handed round; a wait that runs long goes on in
-// wait_bar_warp.
-__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int *abort_flag, const B128Params &p,
-                                         unsigned detail) {
-    return __all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity)) ||
-           wait_bar_warp(bar, parity, abort_flag, p, detail);
-}
 
 // The scales of a promotion warp, copied (cp.async) to shared memory of its own, CH K
 // blocks at a time and one such chunk ahead: waiting for a copy and asking for the next
@@ -243,8 +233,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int32_t t = t_first; t < p.T; t += t_step) {
                 for (int kb = 0; kb < p.num_kb; ++kb, ++g) {
                     const uint32_t buf = g & 1u;
-                    if (!wait_all(bar_full(stage), phase, abort_flag, p, 1 * 256 + stage)) goto roles_done;
-                    if (!wait_all(bar_pempty(buf), ((g >> 1) & 1u) ^ 1u, abort_flag, p, 1 * 256 + 64 + buf))
+                    if (!b128_wait_all(bar_full(stage), phase, abort_flag, p, 1 * 256 + stage)) goto roles_done;
+                    if (!b128_wait_all(bar_pempty(buf), ((g >> 1) & 1u) ^ 1u, abort_flag, p, 1 * 256 + 64 + buf))
                         goto roles_done;
                     ptx::tc_fence_after();
                     const uint64_t a0 = a_desc + stage * (kTile >> 4), b0 = b_desc + stage * (kTile >> 4);
@@ -270,7 +260,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         // tensor-memory column of this warp's chunk c: 64 columns of the tile's first
         // block of B (gated: of gate) and the same 64 of its second (of up)
         const uint32_t lane_base = ((uint32_t)(q * 32) << 16) + half * 64;
-        auto chunk = [&](uint32_t i, int c) { return lane_base + (i & 1u) * 2 * kBlk + (c >> 1) * kBlk + (c & 1) * 32; };
+        // scale vectors: the chunk is 16 rows of 64 columns, in fragments of 8 columns of which
+        // a lane holds two of two rows, so that it reads a quarter of the columns' scales (a
+        // whole row a lane, shared memory took 1024 cycles a K block to hand them out)
+        auto chunk = [&](uint32_t i, int c) {
+            const uint32_t at = lane_base + (i & 1u) * 2 * kBlk + (c >> 1) * kBlk;
+            return VECB ? at + ((c & 1) << 20) : at + (c & 1) * 32;
+        };
+        auto load = [&](uint32_t i, int c, uint32_t(&r)[32]) {
+            if constexpr (VECB)
+                ptx::tmem_ld_16x256b_x8(chunk(i, c), r);
+            else
+                ptx::tmem_ld_32x32b_x32(chunk(i, c), r);
+        };
         const uint32_t free0 = ptx::map_shared(bar_pempty(0), 0), free1 = ptx::map_shared(bar_pempty(1), 0);
         const int row_in = (int)rank * kBlk + q * 32 + lane;
         uint32_t g = 0, lt = 0;
@@ -301,19 +303,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (kb + L::CH < p.num_kb) scales.ask(p, kb + L::CH, chunks);
                 }
                 const float *sc = scales.buf + (~chunks & 1u) * L::SCALES;
-                const float sa = sc[kb % L::CH * 32 + lane];
+                const float sa = VECB ? 0.0f : sc[kb % L::CH * 32 + lane];
                 float2 sb{};
                 if constexpr (!VECB) sb = *reinterpret_cast<const float2 *>(sc + L::CH * 32 + kb % L::CH * 2);
+                // VECB: the lane's rows' and its columns' scales, the latter of one block of 64 at a
+                // time, read before what they are for arrives
+                float2 ra[2], cb[8];
+                auto columns = [&](int block) {
+                    const float2 *col = reinterpret_cast<const float2 *>(sc + L::CH * 32 + kb % L::CH * kBlk + block * 64);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) cb[j] = col[4 * j + (lane & 3)];
+                };
+                if constexpr (VECB) {
+                    const float *r = sc + kb % L::CH * 32 + (lane >> 2);
+                    ra[0] = make_float2(r[0], r[8]);
+                    ra[1] = make_float2(r[16], r[24]);
+                    columns(0);
+                }
                 auto add = [&](int c, const uint32_t(&r)[32]) {
                     if constexpr (VECB) {
-                        const float4 *col = reinterpret_cast<const float4 *>(sc + L::CH * 32 + kb % L::CH * kBlk + 32 * c);
+                        const float a0 = ra[c & 1].x, a1 = ra[c & 1].y;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float4 b = col[i];  // the same address in every lane
-                            acc[c][4 * i] = __fmaf_rn(__uint_as_float(r[4 * i]), __fmul_rn(sa, b.x), acc[c][4 * i]);
-                            acc[c][4 * i + 1] = __fmaf_rn(__uint_as_float(r[4 * i + 1]), __fmul_rn(sa, b.y), acc[c][4 * i + 1]);
-                            acc[c][4 * i + 2] = __fmaf_rn(__uint_as_float(r[4 * i + 2]), __fmul_rn(sa, b.z), acc[c][4 * i + 2]);
-                            acc[c][4 * i + 3] = __fmaf_rn(__uint_as_float(r[4 * i + 3]), __fmul_rn(sa, b.w), acc[c][4 * i + 3]);
+                        for (int j = 0; j < 8; ++j) {
+                            const float2 b = cb[j];
+                            acc[c][4 * j] = __fmaf_rn(__uint_as_float(r[4 * j]), __fmul_rn(a0, b.x), acc[c][4 * j]);
+                            acc[c][4 * j + 1] = __fmaf_rn(__uint_as_float(r[4 * j + 1]), __fmul_rn(a0, b.y), acc[c][4 * j + 1]);
+                            acc[c][4 * j + 2] = __fmaf_rn(__uint_as_float(r[4 * j + 2]), __fmul_rn(a1, b.x), acc[c][4 * j + 2]);
+                            acc[c][4 * j + 3] = __fmaf_rn(__uint_as_float(r[4 * j + 3]), __fmul_rn(a1, b.y), acc[c][4 * j + 3]);
                         }
                     } else {
                         const float f = __fmul_rn(sa, c >= 2 ? sb.y : sb.x);
@@ -324,19 +340,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // From here to the arrival the buffer is kept from the MMAs of the K block after
                 // next: two chunks are loaded at a time (64 registers), the next two as soon as
                 // theirs are free, and everything else comes before or behind.
-                if (!wait_all(bar_pfull(buf), (g >> 1) & 1u, abort_flag, p, 3 * 256 + 64 + buf)) {
+                if (!b128_wait_all(bar_pfull(buf), (g >> 1) & 1u, abort_flag, p, 3 * 256 + 64 + buf)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
-                ptx::tmem_ld_32x32b_x32(chunk(g, 0), r0);
-                ptx::tmem_ld_32x32b_x32(chunk(g, 1), r1);
+                load(g, 0, r0);
+                load(g, 1, r1);
                 ptx::tmem_ld_wait(r0);
                 ptx::tmem_ld_wait(r1);
                 add(0, r0);
-                ptx::tmem_ld_32x32b_x32(chunk(g, 2), r0);
+                load(g, 2, r0);
                 add(1, r1);
-                ptx::tmem_ld_32x32b_x32(chunk(g, 3), r1);
+                load(g, 3, r1);
+                if constexpr (VECB) columns(1);
                 ptx::tmem_ld_wait(r0);
                 ptx::tmem_ld_wait(r1);
                 ptx::tc_fence_before();
@@ -350,7 +367,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t tn = pn;
             if (t + t_step < p.T) begin(t + t_step);  // the next tile's first scales
 
-            if constexpr (OUT != kB128Gated) {
+            if constexpr (VECB) {
+                // eight columns of a row from four lanes: whole sectors of an fp32 C
+                const int64_t row0 = row - lane + (lane >> 2), n0 = (int64_t)tn * 2 * kBlk + half * 64 + 2 * (lane & 3);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int64_t m = row0 + (c & 1) * 16 + (i & 1) * 8, n = n0 + (c >> 1) * kBlk + (i >> 1) * 8;
+                        if (m < p.M && n < p.N) {
+                            float2 v = make_float2(acc[c][4 * (i >> 1) + 2 * (i & 1)], acc[c][4 * (i >> 1) + 2 * (i & 1) + 1]);
+                            if constexpr (OUT == kB128Bf16) {
+                                *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.C) + m * p.N + n) =
+                                    __floats2bfloat162_rn(v.x, v.y);
+                            } else {
+                                float2 *at = reinterpret_cast<float2 *>(static_cast<float *>(p.C) + m * p.N + n);
+                                if constexpr (OUT == kB128Add)
+                                    ptx::red_add_v2(at, v);
+                                else
+                                    *at = v;
+                            }
+                        }
+                    }
+            } else if constexpr (OUT != kB128Gated) {
                 const int64_t n0 = (int64_t)tn * 2 * kBlk + half * 64;
                 if (row < p.M) {
 #pragma unroll
@@ -360,16 +399,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(acc[c][i]);
                         const int64_t n = n0 + (c >> 1) * kBlk + (c & 1) * 32;
                         if constexpr (OUT == kB128Add) {
-                            const float4 *old = reinterpret_cast<const float4 *>(static_cast<float *>(p.C) + row * p.N + n);
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
-                                if (n + 4 * i < p.N) {
-                                    const float4 v = __ldcs(old + i);
-                                    r[4 * i] = __float_as_uint(__uint_as_float(r[4 * i]) + v.x);
-                                    r[4 * i + 1] = __float_as_uint(__uint_as_float(r[4 * i + 1]) + v.y);
-                                    r[4 * i + 2] = __float_as_uint(__uint_as_float(r[4 * i + 2]) + v.z);
-                                    r[4 * i + 3] = __float_as_uint(__uint_as_float(r[4 * i + 3]) + v.w);
-                                }
+                                if (n + 4 * i < p.N)
+                                    ptx::red_add_v4(static_cast<float *>(p.C) + row * p.N + n + 4 * i,
+                                                    make_float4(acc[c][4 * i], acc[c][4 * i + 1], acc[c][4 * i + 2], acc[c][4 * i + 3]));
+                            continue;
                         }
                         store_row32<OUT != kB128Bf16>(p.C, row, p.N, n, r, 1.0f, p.st32 != 0);
                     }
