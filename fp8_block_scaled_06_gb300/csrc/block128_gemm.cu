@@ -338,28 +338,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 };
                 // From here to the arrival the buffer is kept from the MMAs of the K block after
-                // next: two chunks are loaded at a time (64 registers), the next two as soon as
-                // theirs are free, and everything else comes before or behind.
+                // next; everything else comes before or behind.
                 if (!b128_wait_all(bar_pfull(buf), (g >> 1) & 1u, abort_flag, p, 3 * 256 + 64 + buf)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
                 load(g, 0, r0);
-                load(g, 1, r1);
-                ptx::tmem_ld_wait(r0);
-                ptx::tmem_ld_wait(r1);
-                add(0, r0);
-                load(g, 2, r0);
-                add(1, r1);
-                load(g, 3, r1);
-                if constexpr (VECB) columns(1);
-                ptx::tmem_ld_wait(r0);
-                ptx::tmem_ld_wait(r1);
+                if constexpr (VECB) {
+                    // loads of 16 rows take twice the tensor memory's time, and the FMAs twice
+                    // the others': each load runs beside the chunk before it
+                    ptx::tmem_ld_wait(r0);
+                    load(g, 1, r1);
+                    add(0, r0);
+                    ptx::tmem_ld_wait(r1);
+                    load(g, 2, r0);
+                    add(1, r1);
+                    columns(1);
+                    ptx::tmem_ld_wait(r0);
+                    load(g, 3, r1);
+                    add(2, r0);
+                    ptx::tmem_ld_wait(r1);
+                } else {
+                    // two chunks at a time (64 registers), the next two as soon as theirs are free
+                    load(g, 1, r1);
+                    ptx::tmem_ld_wait(r0);
+                    ptx::tmem_ld_wait(r1);
+                    add(0, r0);
+                    load(g, 2, r0);
+                    add(1, r1);
+                    load(g, 3, r1);
+                    ptx::tmem_ld_wait(r0);
+                    ptx::tmem_ld_wait(r1);
+                }
                 ptx::tc_fence_before();
                 __syncwarp();
                 ptx::mbar_arrive_cluster_relaxed(buf ? free1 : free0, lane == 0);
-                add(2, r0);
+                if constexpr (!VECB) add(2, r0);
                 add(3, r1);
             }
             if (!ok) break;
