@@ -287,11 +287,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         if (t_first < p.T) begin(t_first);
         for (int32_t t = t_first; t < p.T; t += t_step, ++lt) {
-            float acc[4][32];
+            // VECB: pairs of columns, in packed arithmetic (issue slots, not the pipe, ran short)
+            float acc[VECB ? 1 : 4][32];
+            uint64_t acc2[VECB ? 4 : 1][16];
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
-                for (int i = 0; i < 32; ++i) acc[c][i] = 0.0f;
+                for (int i = 0; i < 32; ++i) {
+                    if constexpr (VECB)
+                        acc2[c][i / 2] = 0ull;
+                    else
+                        acc[c][i] = 0.0f;
+                }
             uint32_t r0[32], r1[32];
             bool ok = true;
             for (int kb = 0; kb < p.num_kb; ++kb, ++g) {
@@ -308,9 +315,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (!VECB) sb = *reinterpret_cast<const float2 *>(sc + L::CH * 32 + kb % L::CH * 2);
                 // VECB: the lane's rows' and its columns' scales, the latter of one block of 64 at a
                 // time, read before what they are for arrives
-                float2 ra[2], cb[8];
+                float2 ra[2];
+                uint64_t cb[8];
                 auto columns = [&](int block) {
-                    const float2 *col = reinterpret_cast<const float2 *>(sc + L::CH * 32 + kb % L::CH * kBlk + block * 64);
+                    const uint64_t *col = reinterpret_cast<const uint64_t *>(sc + L::CH * 32 + kb % L::CH * kBlk + block * 64);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) cb[j] = col[4 * j + (lane & 3)];
                 };
@@ -322,14 +330,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 auto add = [&](int c, const uint32_t(&r)[32]) {
                     if constexpr (VECB) {
-                        const float a0 = ra[c & 1].x, a1 = ra[c & 1].y;
+                        const uint64_t a0 = b128_pair(ra[c & 1].x, ra[c & 1].x), a1 = b128_pair(ra[c & 1].y, ra[c & 1].y);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            const float2 b = cb[j];
-                            acc[c][4 * j] = __fmaf_rn(__uint_as_float(r[4 * j]), __fmul_rn(a0, b.x), acc[c][4 * j]);
-                            acc[c][4 * j + 1] = __fmaf_rn(__uint_as_float(r[4 * j + 1]), __fmul_rn(a0, b.y), acc[c][4 * j + 1]);
-                            acc[c][4 * j + 2] = __fmaf_rn(__uint_as_float(r[4 * j + 2]), __fmul_rn(a1, b.x), acc[c][4 * j + 2]);
-                            acc[c][4 * j + 3] = __fmaf_rn(__uint_as_float(r[4 * j + 3]), __fmul_rn(a1, b.y), acc[c][4 * j + 3]);
+                            b128_fma2(acc2[c][2 * j], b128_pair(r[4 * j], r[4 * j + 1]), b128_mul2(a0, cb[j]));
+                            b128_fma2(acc2[c][2 * j + 1], b128_pair(r[4 * j + 2], r[4 * j + 3]), b128_mul2(a1, cb[j]));
                         }
                     } else {
                         const float f = __fmul_rn(sa, c >= 2 ? sb.y : sb.x);
@@ -338,43 +343,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 };
                 // From here to the arrival the buffer is kept from the MMAs of the K block after
-                // next; everything else comes before or behind.
+                // next: two chunks are loaded at a time (64 registers), the next two as soon as
+                // theirs are free, and everything else comes before or behind.
                 if (!b128_wait_all(bar_pfull(buf), (g >> 1) & 1u, abort_flag, p, 3 * 256 + 64 + buf)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
                 load(g, 0, r0);
-                if constexpr (VECB) {
-                    // loads of 16 rows take twice the tensor memory's time, and the FMAs twice
-                    // the others': each load runs beside the chunk before it
-                    ptx::tmem_ld_wait(r0);
-                    load(g, 1, r1);
-                    add(0, r0);
-                    ptx::tmem_ld_wait(r1);
-                    load(g, 2, r0);
-                    add(1, r1);
-                    columns(1);
-                    ptx::tmem_ld_wait(r0);
-                    load(g, 3, r1);
-                    add(2, r0);
-                    ptx::tmem_ld_wait(r1);
-                } else {
-                    // two chunks at a time (64 registers), the next two as soon as theirs are free
-                    load(g, 1, r1);
-                    ptx::tmem_ld_wait(r0);
-                    ptx::tmem_ld_wait(r1);
-                    add(0, r0);
-                    load(g, 2, r0);
-                    add(1, r1);
-                    load(g, 3, r1);
-                    ptx::tmem_ld_wait(r0);
-                    ptx::tmem_ld_wait(r1);
-                }
+                load(g, 1, r1);
+                ptx::tmem_ld_wait(r0);
+                ptx::tmem_ld_wait(r1);
+                add(0, r0);
+                load(g, 2, r0);
+                add(1, r1);
+                load(g, 3, r1);
+                if constexpr (VECB) columns(1);
+                ptx::tmem_ld_wait(r0);
+                ptx::tmem_ld_wait(r1);
                 ptx::tc_fence_before();
                 __syncwarp();
                 ptx::mbar_arrive_cluster_relaxed(buf ? free1 : free0, lane == 0);
-                if constexpr (!VECB) add(2, r0);
+                add(2, r0);
                 add(3, r1);
             }
             if (!ok) break;
@@ -391,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 16; ++i) {
                         const int64_t m = row0 + (c & 1) * 16 + (i & 1) * 8, n = n0 + (c >> 1) * kBlk + (i >> 1) * 8;
                         if (m < p.M && n < p.N) {
-                            float2 v = make_float2(acc[c][4 * (i >> 1) + 2 * (i & 1)], acc[c][4 * (i >> 1) + 2 * (i & 1) + 1]);
+                            const float2 v = make_float2(b128_lo(acc2[c][i]), b128_hi(acc2[c][i]));
                             if constexpr (OUT == kB128Bf16) {
                                 *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.C) + m * p.N + n) =
                                     __floats2bfloat162_rn(v.x, v.y);
