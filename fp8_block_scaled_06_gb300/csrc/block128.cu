@@ -11,7 +11,7 @@ bool is_aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t
 bool fp8_fmt(int f) { return f == FP8G_E4M3 || f == FP8G_E5M2; }
 int64_t blocks(int64_t n) { return (n + kBlk - 1) / kBlk; }
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
-constexpr int64_t kMaxQuantRows = (int64_t)65535 * kBlk;  // tiles of 128 rows: a grid's second axis
+constexpr int64_t kMaxQuantRows = (int64_t)65535 * 16;  // 16 rows at least a block: a grid's second axis
 
 // Rows of C that take the kernel for few rows, and its rows per tile.
 constexpr int64_t kFewRows = 128;

@@ -14,10 +14,14 @@
 //   dg = dh u act'(g),  du = dh act(g)   along rows and along columns
 //   h  = act(g) u                         along columns (for the down weights)
 //
-// Bound by memory: a CTA takes a 128 x 128 tile, each warp 16 rows, each lane four
-// columns, so that a row of a warp is a whole line of the source and of the codes.
-// A row's largest magnitude is one warp reduction, a column's goes through 4 KB
-// of shared memory.
+// Bound by memory.  Along columns (and in tiles) a CTA takes a 128 x 128 tile, copied
+// to shared memory as it was read (cp.async; several CTAs share an SM, one's copies run
+// beside another's arithmetic).  A first pass over it finds the rows' and the columns'
+// largest magnitudes, a second writes all codes: each warp has 16 rows, each lane four
+// columns, so that a row of a warp is a whole line of the codes.  A warp's 16 row
+// scales are divided out side by side in 16 lanes (a division a row by every lane was a
+// third of the instructions).  Along rows alone a lane takes 16 values of a row and
+// eight lanes a block, with no second pass.
 #include "block128.h"
 #include "block128_math.cuh"
 #include "ptx.cuh"
@@ -30,99 +34,192 @@ constexpr int kTileThreads = 256;
 constexpr int kTileWarps = kTileThreads / 32;
 constexpr int kRowsPerWarp = kBlk / kTileWarps;
 
-// Column maxima of the tile: this thread's of its warp's rows -> the tile's, in place.
-// red: [kTileWarps][128] floats.
-__device__ __forceinline__ void tile_col_max(float (&m)[4], float *red, int warp, int lane) {
-    reinterpret_cast<float4 *>(red + warp * kBlk)[lane] = make_float4(m[0], m[1], m[2], m[3]);
-    __syncthreads();
+__device__ __forceinline__ void widen4(const uint2 u, float (&v)[4]) {
+    v[0] = __uint_as_float(u.x << 16), v[1] = __uint_as_float(u.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(u.y << 16), v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+}
+
+// rows x (16 * PIECES) bytes, `pitch` bytes apart in memory, to dst, packed; of a row
+// the first `bytes` exist; rows past `rows` and bytes past `bytes` are filled with
+// zeros and read nothing.
+template <int PIECES>
+__device__ __forceinline__ void copy_tile(uint32_t dst, const void *src, int64_t pitch, int rows, int bytes) {
 #pragma unroll
-    for (int w = 0; w < kTileWarps; ++w) {
-        const float4 v = reinterpret_cast<const float4 *>(red + w * kBlk)[lane];
-        m[0] = fmaxf(m[0], v.x);
-        m[1] = fmaxf(m[1], v.y);
-        m[2] = fmaxf(m[2], v.z);
-        m[3] = fmaxf(m[3], v.w);
+    for (int k = 0; k < kBlk * PIECES / kTileThreads; ++k) {
+        const int j = threadIdx.x + k * kTileThreads, r = j / PIECES, b = j % PIECES * 16;
+        const bool in = r < rows && b < bytes;
+        ptx::cp_async_16(dst + j * 16, static_cast<const uint8_t *>(src) + (in ? r * pitch + b : 0), in ? 16 : 0);
     }
 }
 
-template <int SRC, int FMT, bool ROW, bool COL, bool TILE>
-__global__ void __launch_bounds__(kTileThreads) b128_quant_kernel(const B128Quant a) {
-    __shared__ float red[(COL || TILE) ? kTileWarps * kBlk : 1];
+// ---------------------------------------------------------------- along rows
+
+constexpr int kRowTile = 16;   // rows of a CTA, two a warp
+constexpr int kColSpan = 512;  // columns of a CTA, 16 a lane
+
+template <bool BF16, int FMT>
+__global__ void __launch_bounds__(kTileThreads) b128_quant_rows_kernel(const B128Quant a) {
+    __shared__ float scales[kColSpan / kBlk][kRowTile];
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t r0 = (int64_t)blockIdx.y * kBlk, c = (int64_t)blockIdx.x * kBlk + 4 * lane;
-    const int64_t row0 = r0 + warp * kRowsPerWarp;
-    const bool in = c < a.C;  // (C is a multiple of 16: four columns are in or out together)
-    float v[kRowsPerWarp][4];
+    const int64_t c = (int64_t)blockIdx.x * kColSpan + 16 * lane, row0 = (int64_t)blockIdx.y * kRowTile;
+    float v[2][16];
 #pragma unroll
-    for (int i = 0; i < kRowsPerWarp; ++i) {
-        const int64_t r = row0 + i;
-        v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.0f;
-        if (in && r < a.R) {
-            if constexpr (SRC == FP8G_IN_F32) {
-                const float4 f = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(a.x) + r * a.ld + c));
-                v[i][0] = f.x, v[i][1] = f.y, v[i][2] = f.z, v[i][3] = f.w;
-            } else if constexpr (SRC == FP8G_IN_BF16) {
-                const uint2 u = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.x) + r * a.ld + c));
-                v[i][0] = __uint_as_float(u.x << 16), v[i][1] = __uint_as_float(u.x & 0xFFFF0000u);
-                v[i][2] = __uint_as_float(u.y << 16), v[i][3] = __uint_as_float(u.y & 0xFFFF0000u);
+    for (int i = 0; i < 2; ++i) {
+        const int64_t r = row0 + 2 * warp + i;
+        const bool in = c < a.C && r < a.R;  // (C is a multiple of 16)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[i][k] = 0.0f;
+        if (in) {
+            if constexpr (BF16) {
+                const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + r * a.ld + c);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint4 u = __ldg(x + k);
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[i][8 * k + 2 * j] = __uint_as_float(w[j] << 16);
+                        v[i][8 * k + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+                    }
+                }
             } else {
-                const uint32_t q = __ldg(reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(a.x) + r * a.ld + c));
-                const float s = __ldg(a.s_src + (int64_t)blockIdx.x * a.R + r);
-                b128_decode(q, a.src_fmt, v[i]);
+                const float4 *x = reinterpret_cast<const float4 *>(static_cast<const float *>(a.x) + r * a.ld + c);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[i][k] = __fmul_rn(v[i][k], s);
+                for (int k = 0; k < 4; ++k) {
+                    const float4 u = __ldg(x + k);
+                    v[i][4 * k] = u.x, v[i][4 * k + 1] = u.y, v[i][4 * k + 2] = u.z, v[i][4 * k + 3] = u.w;
+                }
             }
         }
     }
-    float cm[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    float own = 0.0f;  // lane i: the scale of row i of the warp
 #pragma unroll
-    for (int i = 0; i < kRowsPerWarp; ++i) {
-        if constexpr (ROW) {
-            const float s = b128_scale<FMT>(b128_warp_max(b128_amax4(v[i][0], v[i][1], v[i][2], v[i][3])));
-            if (lane == i) own = s;
-            const uint32_t q = b128_codes<FMT>(v[i][0], v[i][1], v[i][2], v[i][3], __frcp_rn(s));
-            if (in && row0 + i < a.R) *reinterpret_cast<uint32_t *>(a.q_row + (row0 + i) * a.C + c) = q;
-        }
-        if constexpr (COL || TILE) {
+    for (int i = 0; i < 2; ++i) {
+        float m[4] = {};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) cm[k] = fmaxf(cm[k], fabsf(v[i][k]));
-        }
+        for (int k = 0; k < 16; ++k) m[k & 3] = fmaxf(m[k & 3], fabsf(v[i][k]));
+        float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+#pragma unroll
+        for (int o = 1; o < 8; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float s = b128_scale<FMT>(top), r = __frcp_rn(s);
+        if ((lane & 7) == 0) scales[lane >> 3][2 * warp + i] = s;
+        uint4 q;
+        q.x = b128_codes<FMT>(v[i][0], v[i][1], v[i][2], v[i][3], r);
+        q.y = b128_codes<FMT>(v[i][4], v[i][5], v[i][6], v[i][7], r);
+        q.z = b128_codes<FMT>(v[i][8], v[i][9], v[i][10], v[i][11], r);
+        q.w = b128_codes<FMT>(v[i][12], v[i][13], v[i][14], v[i][15], r);
+        const int64_t row = row0 + 2 * warp + i;
+        if (c < a.C && row < a.R) *reinterpret_cast<uint4 *>(a.q_row + row * a.C + c) = q;
     }
-    if constexpr (ROW) {
-        if (lane < kRowsPerWarp && row0 + lane < a.R) a.s_row[(int64_t)blockIdx.x * a.R + row0 + lane] = own;
+    __syncthreads();
+    // the rows of a block side by side
+    const int i = threadIdx.x % kRowTile, b = threadIdx.x / kRowTile;
+    if (b < kColSpan / kBlk && row0 + i < a.R && (int64_t)blockIdx.x * kColSpan + b * kBlk < a.C)
+        a.s_row[((int64_t)blockIdx.x * (kColSpan / kBlk) + b) * a.R + row0 + i] = scales[b][i];
+}
+
+// ------------------------------------------------------ along columns, in tiles
+
+template <int SRC>
+constexpr int kSrcBytes = SRC == FP8G_IN_F32 ? 4 : SRC == FP8G_IN_BF16 ? 2 : 1;
+
+template <int SRC, int FMT, bool ROW, bool TILE>
+__global__ void __launch_bounds__(kTileThreads) b128_quant_tile_kernel(const B128Quant a) {
+    constexpr int E = kSrcBytes<SRC>;
+    extern __shared__ __align__(16) uint8_t sm[];
+    uint32_t *top = reinterpret_cast<uint32_t *>(sm + kBlk * kBlk * E);  // column maxima [128]
+    float *src_s = reinterpret_cast<float *>(top + kBlk);                // row scales of codes [128]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row0 = (int64_t)blockIdx.y * kBlk, c0 = (int64_t)blockIdx.x * kBlk, c = c0 + 4 * lane;
+    const int rows = (int)min((int64_t)kBlk, a.R - row0);
+    const bool in = c < a.C;  // (C is a multiple of 16: four columns are in or out together)
+    if (threadIdx.x < kBlk) top[threadIdx.x] = 0u;
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    copy_tile<8 * E>(ptx::smem_addr(sm), static_cast<const uint8_t *>(a.x) + (row0 * a.ld + c0) * E, a.ld * E, rows,
+                     (int)min((int64_t)kBlk, a.C - c0) * E);
+    if constexpr (SRC == kB128Codes) {
+        if (threadIdx.x < kBlk)
+            ptx::cp_async_4(ptx::smem_addr(src_s + threadIdx.x),
+                            a.s_src + (int64_t)blockIdx.x * a.R + row0 + min((int)threadIdx.x, rows - 1), 4);
     }
-    if constexpr (COL || TILE) {
-        tile_col_max(cm, red, warp, lane);
-        float s[4], r[4];
-        if constexpr (TILE) {
-            const float one = b128_scale<FMT>(b128_warp_max(fmaxf(fmaxf(cm[0], cm[1]), fmaxf(cm[2], cm[3]))));
-#pragma unroll
-            for (int k = 0; k < 4; ++k) s[k] = one;
-            if (threadIdx.x == 0) a.s_tile[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = one;
+    ptx::cp_async_commit();
+    ptx::cp_async_wait<0>();
+    __syncthreads();
+    auto values = [&](int r, float (&v)[4]) {
+        if constexpr (SRC == FP8G_IN_F32) {
+            const float4 f = reinterpret_cast<const float4 *>(sm)[r * 32 + lane];
+            v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+        } else if constexpr (SRC == FP8G_IN_BF16) {
+            widen4(reinterpret_cast<const uint2 *>(sm)[r * 32 + lane], v);
         } else {
+            b128_decode(reinterpret_cast<const uint32_t *>(sm)[r * 32 + lane], a.src_fmt, v);
+            const float s = src_s[r];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[k] = b128_scale<FMT>(cm[k]);
-            if (warp == 0 && in)
-                *reinterpret_cast<float4 *>(a.s_col + (int64_t)blockIdx.y * a.C + c) = make_float4(s[0], s[1], s[2], s[3]);
+            for (int k = 0; k < 4; ++k) v[k] = __fmul_rn(v[k], s);
+        }
+    };
+    // (rows and columns past the matrix are zeros: they change no maximum)
+    const int first = warp * kRowsPerWarp;
+    float cm[4] = {}, own = 0.0f;  // own: lane i has row first + i's
+#pragma unroll 4
+    for (int i = 0; i < kRowsPerWarp; ++i) {
+        float v[4];
+        values(first + i, v);
+        if constexpr (ROW) {
+            const float m = b128_warp_max(b128_amax4(v[0], v[1], v[2], v[3]));
+            own = lane == i ? m : own;
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) r[k] = __frcp_rn(s[k]);
-        uint8_t *q = TILE ? a.q_tile : a.q_col;
+        for (int k = 0; k < 4; ++k) cm[k] = fmaxf(cm[k], fabsf(v[k]));
+    }
+    // (magnitudes that are not NaN: their bits are in order)
 #pragma unroll
-        for (int i = 0; i < kRowsPerWarp; ++i)
-            if (in && row0 + i < a.R)
-                *reinterpret_cast<uint32_t *>(q + (row0 + i) * a.C + c) =
-                    b128_codes4<FMT>(v[i], r);
+    for (int k = 0; k < 4; ++k) atomicMax(top + 4 * lane + k, __float_as_uint(cm[k]));
+    float rr = 0.0f;
+    if constexpr (ROW) {
+        const float s = b128_scale<FMT>(own);
+        rr = __frcp_rn(s);
+        if (lane < kRowsPerWarp && first + lane < rows) a.s_row[(int64_t)blockIdx.x * a.R + row0 + first + lane] = s;
+    }
+    __syncthreads();
+    const uint4 t = reinterpret_cast<const uint4 *>(top)[lane];
+    float s[4] = {__uint_as_float(t.x), __uint_as_float(t.y), __uint_as_float(t.z), __uint_as_float(t.w)};
+    if constexpr (TILE) {
+        const float one = b128_scale<FMT>(b128_warp_max(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]))));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[k] = one;
+        if (threadIdx.x == 0) a.s_tile[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = one;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[k] = b128_scale<FMT>(s[k]);
+        if (warp == 0 && in)
+            *reinterpret_cast<float4 *>(a.s_col + (int64_t)blockIdx.y * a.C + c) = make_float4(s[0], s[1], s[2], s[3]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s[k] = __frcp_rn(s[k]);
+    const int64_t at = (row0 + first) * a.C + c;
+    uint8_t *q = (TILE ? a.q_tile : a.q_col) + at, *q_row = ROW ? a.q_row + at : nullptr;
+    const int live = in ? min(kRowsPerWarp, rows - first) : 0;
+#pragma unroll 4
+    for (int i = 0; i < kRowsPerWarp; ++i) {
+        float v[4];
+        values(first + i, v);
+        const float r = ROW ? __shfl_sync(0xffffffffu, rr, i) : 0.0f;
+        if (i < live) {
+            if constexpr (ROW) *reinterpret_cast<uint32_t *>(q_row) = b128_codes<FMT>(v[0], v[1], v[2], v[3], r);
+            *reinterpret_cast<uint32_t *>(q) = b128_codes4<FMT>(v, s);
+        }
+        q += a.C;
+        q_row += a.C;
     }
 }
 
-// The tile's sources lie in shared memory as they were read (64 KB for a bf16 dh,
-// so that three CTAs share an SM and one's loads run beside another's arithmetic);
-// dg, du and h are computed from them twice, for the rows and then for the columns,
-// once the columns' maxima are known (kept in fp32 they would take 192 registers).
+// ------------------------------------------------------------ gated backward
+
+// dg, du and h are computed twice from the tile, for the maxima and for the codes (kept
+// in fp32 they would take 192 registers).
 template <bool BF16>
 struct BackTile {
     static constexpr int D = BF16 ? 2 : 4;  // bytes of a value of dh
@@ -144,26 +241,14 @@ __global__ void __launch_bounds__(kTileThreads, BF16 ? 3 : 2) b128_backward_kern
     for (int i = threadIdx.x; i < 3 * kBlk; i += kTileThreads) top[i] = 0u;
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    // (rows past the last are filled with zeros, and read nothing)
     const uint32_t base = ptx::smem_addr(sm);
-#pragma unroll
-    for (int k = 0; k < kBlk * 8 / kTileThreads; ++k) {
-        const int j = threadIdx.x + k * kTileThreads, r = j >> 3, b = (j & 7) * 16;
-        const int64_t at = (row0 + min(r, rows - 1)) * F2 + c0 + b;
-        ptx::cp_async_16(base + j * 16, a.gu + at, r < rows ? 16 : 0);
-        ptx::cp_async_16(base + L::OFF_U + j * 16, a.gu + at + F, r < rows ? 16 : 0);
-    }
-    constexpr int kPer = 8 * L::D;  // 16-byte pieces of a row of dh
-#pragma unroll
-    for (int k = 0; k < kBlk * kPer / kTileThreads; ++k) {
-        const int j = threadIdx.x + k * kTileThreads, r = j / kPer, b = j % kPer * 16;
-        const uint8_t *src = static_cast<const uint8_t *>(a.dh) + ((row0 + min(r, rows - 1)) * F + c0) * L::D + b;
-        ptx::cp_async_16(base + L::OFF_D + j * 16, src, r < rows ? 16 : 0);
-    }
+    copy_tile<8>(base, a.gu + row0 * F2 + c0, F2, rows, kBlk);
+    copy_tile<8>(base + L::OFF_U, a.gu + row0 * F2 + F + c0, F2, rows, kBlk);
+    copy_tile<8 * L::D>(base + L::OFF_D, static_cast<const uint8_t *>(a.dh) + (row0 * F + c0) * L::D, F * L::D, rows,
+                        kBlk * L::D);
     {
         const int r = threadIdx.x & (kBlk - 1), up = threadIdx.x / kBlk;
-        const float *src = a.sgu + (up * fb + blockIdx.x) * a.M + row0 + min(r, rows - 1);
-        ptx::cp_async_4(base + L::OFF_S + threadIdx.x * 4, src, r < rows ? 4 : 0);
+        ptx::cp_async_4(base + L::OFF_S + threadIdx.x * 4, a.sgu + (up * fb + blockIdx.x) * a.M + row0 + min(r, rows - 1), 4);
     }
     ptx::cp_async_commit();
     ptx::cp_async_wait<0>();
@@ -175,9 +260,7 @@ __global__ void __launch_bounds__(kTileThreads, BF16 ? 3 : 2) b128_backward_kern
         b128_decode(gq[r * 32 + lane], FP8G_E4M3, g);
         b128_decode(uq[r * 32 + lane], FP8G_E4M3, u);
         if constexpr (BF16) {
-            const uint2 w = reinterpret_cast<const uint2 *>(sm + L::OFF_D)[r * 32 + lane];
-            x[0] = __uint_as_float(w.x << 16), x[1] = __uint_as_float(w.x & 0xFFFF0000u);
-            x[2] = __uint_as_float(w.y << 16), x[3] = __uint_as_float(w.y & 0xFFFF0000u);
+            widen4(reinterpret_cast<const uint2 *>(sm + L::OFF_D)[r * 32 + lane], x);
         } else {
             const float4 w = reinterpret_cast<const float4 *>(sm + L::OFF_D)[r * 32 + lane];
             x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
@@ -193,19 +276,18 @@ __global__ void __launch_bounds__(kTileThreads, BF16 ? 3 : 2) b128_backward_kern
             h[k] = y * uu;
         }
     };
-    const int first = warp * kRowsPerWarp, last = min(first + kRowsPerWarp, rows);
+    // (rows past the last are zeros)
+    const int first = warp * kRowsPerWarp;
     float mg[4] = {}, mu[4] = {}, mh[4] = {};
     float own_g = 0.0f, own_u = 0.0f;
 #pragma unroll 2
-    for (int r = first; r < last; ++r) {
+    for (int i = 0; i < kRowsPerWarp; ++i) {
         float dg[4], du[4], h[4];
-        values(r, dg, du, h);
-        const float s0 = b128_scale<FMT>(b128_warp_max(b128_amax4(dg[0], dg[1], dg[2], dg[3])));
-        const float s1 = b128_scale<FMT>(b128_warp_max(b128_amax4(du[0], du[1], du[2], du[3])));
-        if (lane == r - first) own_g = s0, own_u = s1;
-        uint8_t *q = a.row + (row0 + r) * F2 + c0 + 4 * lane;
-        *reinterpret_cast<uint32_t *>(q) = b128_codes<FMT>(dg[0], dg[1], dg[2], dg[3], __frcp_rn(s0));
-        *reinterpret_cast<uint32_t *>(q + F) = b128_codes<FMT>(du[0], du[1], du[2], du[3], __frcp_rn(s1));
+        values(first + i, dg, du, h);
+        const float a0 = b128_warp_max(b128_amax4(dg[0], dg[1], dg[2], dg[3]));
+        const float a1 = b128_warp_max(b128_amax4(du[0], du[1], du[2], du[3]));
+        own_g = lane == i ? a0 : own_g;
+        own_u = lane == i ? a1 : own_u;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             mg[k] = fmaxf(mg[k], fabsf(dg[k]));
@@ -213,17 +295,20 @@ __global__ void __launch_bounds__(kTileThreads, BF16 ? 3 : 2) b128_backward_kern
             mh[k] = fmaxf(mh[k], fabsf(h[k]));
         }
     }
-    if (first + lane < last) {
-        a.s_row[blockIdx.x * a.M + row0 + first + lane] = own_g;
-        a.s_row[(fb + blockIdx.x) * a.M + row0 + first + lane] = own_u;
-    }
-    // (magnitudes that are not NaN: their bits are in order)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         atomicMax(top + 4 * lane + k, __float_as_uint(mg[k]));
         atomicMax(top + kBlk + 4 * lane + k, __float_as_uint(mu[k]));
         atomicMax(top + 2 * kBlk + 4 * lane + k, __float_as_uint(mh[k]));
     }
+    own_g = b128_scale<FMT>(own_g);
+    own_u = b128_scale<FMT>(own_u);
+    if (lane < kRowsPerWarp && first + lane < rows) {
+        a.s_row[blockIdx.x * a.M + row0 + first + lane] = own_g;
+        a.s_row[(fb + blockIdx.x) * a.M + row0 + first + lane] = own_u;
+    }
+    own_g = __frcp_rn(own_g);
+    own_u = __frcp_rn(own_u);
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -241,26 +326,40 @@ __global__ void __launch_bounds__(kTileThreads, BF16 ? 3 : 2) b128_backward_kern
 #pragma unroll
     for (int k = 0; k < 4; ++k) mg[k] = __frcp_rn(mg[k]), mu[k] = __frcp_rn(mu[k]), mh[k] = __frcp_rn(mh[k]);
 #pragma unroll 2
-    for (int r = first; r < last; ++r) {
+    for (int i = 0; i < kRowsPerWarp; ++i) {
         float dg[4], du[4], h[4];
-        values(r, dg, du, h);
-        uint8_t *q = a.col + (row0 + r) * F2 + c0 + 4 * lane;
-        *reinterpret_cast<uint32_t *>(q) = b128_codes4<FMT>(dg, mg);
-        *reinterpret_cast<uint32_t *>(q + F) = b128_codes4<FMT>(du, mu);
-        *reinterpret_cast<uint32_t *>(a.h + (row0 + r) * F + c0 + 4 * lane) = b128_codes4<FP8G_E4M3>(h, mh);
+        values(first + i, dg, du, h);
+        const float r0 = __shfl_sync(0xffffffffu, own_g, i), r1 = __shfl_sync(0xffffffffu, own_u, i);
+        if (first + i < rows) {
+            const int64_t at = (row0 + first + i) * F2 + c0 + 4 * lane;
+            *reinterpret_cast<uint32_t *>(a.row + at) = b128_codes<FMT>(dg[0], dg[1], dg[2], dg[3], r0);
+            *reinterpret_cast<uint32_t *>(a.row + at + F) = b128_codes<FMT>(du[0], du[1], du[2], du[3], r1);
+            *reinterpret_cast<uint32_t *>(a.col + at) = b128_codes4<FMT>(dg, mg);
+            *reinterpret_cast<uint32_t *>(a.col + at + F) = b128_codes4<FMT>(du, mu);
+            *reinterpret_cast<uint32_t *>(a.h + (row0 + first + i) * F + c0 + 4 * lane) = b128_codes4<FP8G_E4M3>(h, mh);
+        }
     }
+}
+
+template <int SRC, int FMT, bool ROW, bool TILE>
+cudaError_t quant_tile(const B128Quant &a, cudaStream_t s) {
+    auto kern = b128_quant_tile_kernel<SRC, FMT, ROW, TILE>;
+    constexpr int kBytes = kBlk * kBlk * kSrcBytes<SRC> + 2 * kBlk * 4;
+    if constexpr (kBytes > 48 * 1024) {
+        const cudaError_t e = b128_allow_smem(reinterpret_cast<const void *>(kern), kBytes);
+        if (e != cudaSuccess) return e;
+    }
+    const dim3 grid((unsigned)((a.C + kBlk - 1) / kBlk), (unsigned)((a.R + kBlk - 1) / kBlk));
+    return launch_programmatic_smem(kern, grid, dim3(kTileThreads), kBytes, s, a);
 }
 
 template <int SRC, int FMT>
 cudaError_t quant_src(const B128Quant &a, cudaStream_t s) {
-    const dim3 grid((unsigned)((a.C + kBlk - 1) / kBlk), (unsigned)((a.R + kBlk - 1) / kBlk));
-    if (a.q_tile != nullptr)
-        return launch_programmatic(b128_quant_kernel<SRC, FMT, false, false, true>, grid, dim3(kTileThreads), s, a);
-    if (a.q_row != nullptr && a.q_col != nullptr)
-        return launch_programmatic(b128_quant_kernel<SRC, FMT, true, true, false>, grid, dim3(kTileThreads), s, a);
-    if (a.q_row != nullptr)
-        return launch_programmatic(b128_quant_kernel<SRC, FMT, true, false, false>, grid, dim3(kTileThreads), s, a);
-    return launch_programmatic(b128_quant_kernel<SRC, FMT, false, true, false>, grid, dim3(kTileThreads), s, a);
+    if (a.q_tile != nullptr) return quant_tile<SRC, FMT, false, true>(a, s);
+    if (a.q_col != nullptr)
+        return a.q_row != nullptr ? quant_tile<SRC, FMT, true, false>(a, s) : quant_tile<SRC, FMT, false, false>(a, s);
+    const dim3 grid((unsigned)((a.C + kColSpan - 1) / kColSpan), (unsigned)((a.R + kRowTile - 1) / kRowTile));
+    return launch_programmatic(b128_quant_rows_kernel<SRC == FP8G_IN_BF16, FMT>, grid, dim3(kTileThreads), s, a);
 }
 
 template <bool BF16, int GATE, int FMT>
@@ -280,14 +379,9 @@ cudaError_t backward_gate(const B128Backward &a, int fmt, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_b128_quant(const B128Quant &a, int fmt, cudaStream_t s) {
-    if (a.src == kB128Codes) {  // codes are turned: along columns only
-        const dim3 grid((unsigned)((a.C + kBlk - 1) / kBlk), (unsigned)((a.R + kBlk - 1) / kBlk));
-        return fmt == FP8G_E4M3
-                   ? launch_programmatic(b128_quant_kernel<kB128Codes, FP8G_E4M3, false, true, false>, grid,
-                                         dim3(kTileThreads), s, a)
-                   : launch_programmatic(b128_quant_kernel<kB128Codes, FP8G_E5M2, false, true, false>, grid,
-                                         dim3(kTileThreads), s, a);
-    }
+    if (a.src == kB128Codes)  // codes are turned: along columns only
+        return fmt == FP8G_E4M3 ? quant_tile<kB128Codes, FP8G_E4M3, false, false>(a, s)
+                                : quant_tile<kB128Codes, FP8G_E5M2, false, false>(a, s);
     if (a.src == FP8G_IN_F32)
         return fmt == FP8G_E4M3 ? quant_src<FP8G_IN_F32, FP8G_E4M3>(a, s) : quant_src<FP8G_IN_F32, FP8G_E5M2>(a, s);
     return fmt == FP8G_E4M3 ? quant_src<FP8G_IN_BF16, FP8G_E4M3>(a, s) : quant_src<FP8G_IN_BF16, FP8G_E5M2>(a, s);

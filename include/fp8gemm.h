@@ -631,7 +631,7 @@ FP8G_API fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void *W
  * x (fp32 or bf16 per in_dtype) [rows, cols], rows ld elements apart -> codes
  * [rows, cols] with scales along rows (q_row, s_row) and / or along columns
  * (q_col, s_col), from one reading; a pair may be null, not both.  rows may be 0.
- * cols % 16 == 0, rows <= 65535 * 128, else FP8G_ERR_UNSUPPORTED_SHAPE; pointers
+ * cols % 16 == 0, rows <= 65535 * 16, else FP8G_ERR_UNSUPPORTED_SHAPE; pointers
  * and rows of x 16-byte aligned.  One kernel.
  * fp8g_quantize_tile128: the same with a scale per tile (weights).
  */
@@ -697,7 +697,7 @@ FP8G_API fp8g_status fp8_gated_block128(const void *x, const float *sfx, int32_t
  * dgu [M, 2F] in fmt along rows (dgu_row, s_row: for the input gradient) and along
  * columns (dgu_col, s_col: for W13's gradient), and h [M, F] in E4M3 along columns
  * (h_col, sh_col: for the down weights' gradient), the forward pass's h need not be
- * kept.  ReLU's derivative at 0 is 0.  F % 128 == 0, M <= 65535 * 128, else
+ * kept.  ReLU's derivative at 0 is 0.  F % 128 == 0, M <= 65535 * 16, else
  * FP8G_ERR_UNSUPPORTED_SHAPE; pointers 16-byte aligned.  M may be 0.  One kernel.
  */
 FP8G_API fp8g_status fp8g_gated_block128_backward(const void *dh, int32_t dh_dtype, const uint8_t *gu,
