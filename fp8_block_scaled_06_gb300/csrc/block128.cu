@@ -13,22 +13,36 @@ int64_t blocks(int64_t n) { return (n + kBlk - 1) / kBlk; }
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
 constexpr int64_t kMaxQuantRows = (int64_t)65535 * 16;  // 16 rows at least a block: a grid's second axis
 
-// Rows of C that take the kernel for few rows, and its rows per tile.
-constexpr int64_t kFewRows = 128;
-int few_tile(int64_t M, bool gated) { return M <= 16 ? 16 : M <= 32 || gated ? 32 : 64; }
+// Which kernel, and its shape.
+struct Plan {
+    bool few;
+    int nt, split;  // few: rows of A of a tile, CTAs that share its K blocks
+};
 
-// CTAs that share a tile's K blocks: the fewest rounds of K blocks over two CTAs
-// an SM, where each further CTA costs a tile about two K blocks of joining.
-int few_split(int64_t tiles, int num_kb, int num_sms) {
-    int best = 1;
-    int64_t least = INT64_MAX;
-    for (int s = 1; s <= 8; s *= 2) {
-        if (s > num_kb) break;
-        const int64_t rounds = (tiles * s + 2 * num_sms - 1) / (2 * num_sms);
-        const int64_t cost = rounds * ((num_kb + s - 1) / s + 2) + s;
-        if (cost < least) {
+// The kernel for few rows against the one on CTA pairs, by estimates of their time.
+// A round of pairs takes 76 hundredths of a 10^4-cycle unit a K block (every tile 256 x
+// 256, however few of its rows exist), the call eight more at its ends.  Few rows: a
+// tile of 128 weight rows; a round begins and ends with the time of five K blocks
+// (first loads, joining), each further CTA of a tile joins about one more; a K block
+// takes 110 where a CTA has its SM alone, 130 where two share it (loads bound both).
+// Measured, us, few rows / pairs: 64 x 14336 x 4096 14.5 / 19.5, 77 of them 24 / 19.5,
+// 77 x 4096 x 14336 21 / 54, 256 of them 34 / 46; gated, 64 rows of F 14336, K 4096 27 /
+// 40, 128 rows 48 / 40.
+Plan plan(int64_t M, int64_t n_blocks, int64_t pair_tiles, int num_kb, bool gated, int num_sms) {
+    const int64_t rounds = (pair_tiles + num_sms / 2 - 1) / (num_sms / 2);
+    int64_t least = (rounds * num_kb + 8) * 76;
+    Plan best{false, kBlk, 1};
+    const int most = gated ? 64 : 128;
+    int nt = 16;
+    while (nt < most && nt < M) nt *= 2;
+    const int64_t tiles = n_blocks * ((M + nt - 1) / nt);
+    const int per_sm = nt < most ? 2 : 1;
+    for (int s = 1; s <= 8 && s <= num_kb; s *= 2) {
+        const int64_t r = (tiles * s + per_sm * num_sms - 1) / (per_sm * num_sms);
+        const int64_t cost = (r * ((num_kb + s - 1) / s + 5) + s) * (per_sm == 1 ? 110 : 130);
+        if (cost < least && M <= 65535 * 16) {  // (a grid's second axis)
             least = cost;
-            best = s;
+            best = Plan{true, nt, s};
         }
     }
     return best;
@@ -144,21 +158,19 @@ fp8g_status fp8_gemm_block128(int32_t form, const void *A, const float *sfa, int
     p.timeout_ns = d.timeout_ns;
     const int o = add ? kB128Add : out == FP8G_OUT_F32 ? kB128F32 : kB128Bf16;
     const uint32_t ta = host_mma_type(a_fmt), tb = host_mma_type(b_fmt);
-    const bool few = !tn && M <= kFewRows;
-    const int nt = few ? few_tile(M, false) : kBlk;
+    const int64_t npm = (M + 2 * kBlk - 1) / (2 * kBlk), npn = (N + 2 * kBlk - 1) / (2 * kBlk);
+    if (npm * npn >= kMaxDim) return FP8G_ERR_UNSUPPORTED_SHAPE;
+    const Plan pl = tn ? Plan{false, kBlk, 1} : plan(M, p.n_blocks, npm * npn, p.num_kb, false, d.num_sms);
     CUtensorMap mA, mB;
-    st = tn ? map2(A, M, K, kBlk, d.dev, mA) : map2(A, K, M, nt, d.dev, mA);
+    st = tn ? map2(A, M, K, kBlk, d.dev, mA) : map2(A, K, M, pl.nt, d.dev, mA);
     if (st == FP8G_OK)
         st = p.b_mn ? map2(B, N, K, kBlk, d.dev, mB) : map2(B, K, N, kBlk, d.dev, mB);
     if (st != FP8G_OK) return st;
     cudaError_t e;
-    if (few) {
+    if (pl.few) {
         p.types = (tb << 7) | (ta << 10) | ((uint32_t)p.b_mn << 15);
-        const int split = few_split((int64_t)p.n_blocks * ((M + nt - 1) / nt), p.num_kb, d.num_sms);
-        e = launch_b128_few(mA, mB, p, o, nt, split, stream);
+        e = launch_b128_few(mA, mB, p, o, pl.nt, pl.split, stream);
     } else {
-        const int64_t npm = (M + 2 * kBlk - 1) / (2 * kBlk), npn = (N + 2 * kBlk - 1) / (2 * kBlk);
-        if (npm * npn >= kMaxDim) return FP8G_ERR_UNSUPPORTED_SHAPE;
         p.types = (ta << 7) | (tb << 10) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16);
         p.npm = (int32_t)npm;
         p.npn = (int32_t)npn;
@@ -202,10 +214,11 @@ fp8g_status fp8_gated_block128(const void *x, const float *sfx, int32_t x_fmt, c
     p.status = d.status;
     p.timeout_ns = d.timeout_ns;
     const uint32_t tx = host_mma_type(x_fmt), tw = host_mma_type(w_fmt);
-    const bool few = M <= kFewRows;
-    const int nt = few ? few_tile(M, true) : kBlk;
+    const int64_t npm = (M + 2 * kBlk - 1) / (2 * kBlk);
+    if (npm * p.n_blocks >= kMaxDim) return FP8G_ERR_UNSUPPORTED_SHAPE;
+    const Plan pl = plan(M, p.n_blocks, npm * p.n_blocks, p.num_kb, true, d.num_sms);
     CUtensorMap mX, mW;
-    st = map2(x, K, M, nt, d.dev, mX);
+    st = map2(x, K, M, pl.nt, d.dev, mX);
     if (st == FP8G_OK) {
         const uint64_t dw[3] = {(uint64_t)K, (uint64_t)F, 2};
         const uint32_t bw[3] = {(uint32_t)kBlk, (uint32_t)kBlk, 1};
@@ -213,13 +226,10 @@ fp8g_status fp8_gated_block128(const void *x, const float *sfx, int32_t x_fmt, c
     }
     if (st != FP8G_OK) return st;
     cudaError_t e;
-    if (few) {
+    if (pl.few) {
         p.types = (tw << 7) | (tx << 10);
-        const int split = few_split((int64_t)p.n_blocks * ((M + nt - 1) / nt), p.num_kb, d.num_sms);
-        e = launch_b128_few(mX, mW, p, kB128Gated, nt, split, stream);
+        e = launch_b128_few(mX, mW, p, kB128Gated, pl.nt, pl.split, stream);
     } else {
-        const int64_t npm = (M + 2 * kBlk - 1) / (2 * kBlk);
-        if (npm * p.n_blocks >= kMaxDim) return FP8G_ERR_UNSUPPORTED_SHAPE;
         p.types = (tx << 7) | (tw << 10);
         p.npm = (int32_t)npm;
         p.npn = p.n_blocks;
@@ -239,14 +249,16 @@ fp8g_status fp8g_gated_block128_backward(const void *dh, int32_t dh_dtype, const
     if (M > 0 && (dh == nullptr || gu == nullptr || sgu == nullptr || dgu_row == nullptr || s_row == nullptr ||
                   dgu_col == nullptr || s_col == nullptr || h_col == nullptr || sh_col == nullptr))
         return FP8G_ERR_INVALID_ARG;
-    if (F % kBlk != 0 || M > kMaxQuantRows || 2 * F >= kMaxDim) return FP8G_ERR_UNSUPPORTED_SHAPE;
+    if (F % kBlk != 0 || M > kMaxQuantRows || 2 * F >= kMaxDim ||
+        (M + kBlk - 1) / kBlk * (F / kBlk) >= kMaxDim / 2)
+        return FP8G_ERR_UNSUPPORTED_SHAPE;
     const void *all[] = {dh, gu, sgu, dgu_row, s_row, dgu_col, s_col, h_col, sh_col};
     for (const void *ptr : all)
         if (!is_aligned(ptr, 16)) return FP8G_ERR_ALIGNMENT;
     HostDevice d;
     const fp8g_status st = host_device(d);
     if (st != FP8G_OK || M == 0) return st;
-    const B128Backward a{dh, gu, sgu, M, F, dgu_row, dgu_col, h_col, s_row, s_col, sh_col};
+    const B128Backward a{dh, gu, sgu, M, F, dgu_row, dgu_col, h_col, s_row, s_col, sh_col, d.num_sms};
     return launch_b128_backward(a, dh_dtype == FP8G_IN_BF16, gate, fmt, stream) == cudaSuccess ? FP8G_OK
                                                                                                : FP8G_ERR_CUDA;
 }

@@ -66,6 +66,7 @@ struct B128Backward {
     int64_t M, F;
     uint8_t *row, *col, *h;      // [M, 2F], [M, 2F], [M, F]
     float *s_row, *s_col, *s_h;
+    int32_t num_sms;
 };
 cudaError_t launch_b128_backward(const B128Backward &a, bool bf16, int gate, int fmt,
                                  cudaStream_t stream);

@@ -3,7 +3,7 @@
 //
 // The weights are the MMA's operand of 128 rows, NT rows of A its columns, so a
 // tile of C is 128 weight rows by NT.  A CTA holds a ring of 16 KB weight tiles (32
-// KB for gate and up); two CTAs share an SM, about 200 KB in flight.  The K blocks
+// KB for gate and up), with two CTAs on an SM about 200 KB in flight.  The K blocks
 // of a tile are split over a cluster of up to eight CTAs, so that a narrow C
 // still uses every SM; each CTA's share of the sum stays in its shared memory,
 // and the CTAs add each other's (distributed shared memory) in rank order, each for
@@ -11,11 +11,11 @@
 //
 // As in block128_gemm.cu each K block's product goes to a tensor-memory buffer of
 // its own and is added, scaled, to registers: thread = weight row, its values the NT
-// rows, whose scales (times the weight block's) go through shared memory, read as
-// broadcasts.
+// rows, whose scales go through shared memory, read as broadcasts.  Beyond 64 sums a thread (128 rows of A, or 64 of gate and up) four more
+// warps take half of the rows, and a CTA has its SM alone.
 //
-// Roles (256 threads): warp 0 TMA, warp 1 MMA issue, warps 4-7 promotion; all eight
-// add and store.
+// Roles (256 or 384 threads): warp 0 TMA, warp 1 MMA issue, warps 4 and up promotion; all
+// warps add and store.
 #include <cuda_bf16.h>
 
 #include "block128.h"
@@ -27,30 +27,39 @@ namespace fp8g {
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kTile = kBlk * kBlk;
 
 template <int NT, bool GATED>
 struct Few {
     static constexpr int G = GATED ? 2 : 1;              // weight tiles of a stage
-    static constexpr int STAGE = G * kTile + NT * kBlk;
-    static constexpr int STAGES = 106496 / STAGE;        // two CTAs to an SM
     static constexpr int COLS = G * NT;                  // tensor-memory columns of a buffer
-    static constexpr int BUFS = COLS >= 64 ? 2 : 4;
-    static constexpr int TMEM = COLS * BUFS < 32 ? 32 : COLS * BUFS;
+    // up to 64 sums a thread; more take a second set of promotion warps and an SM alone
+    static constexpr int HALVES = COLS > 64 ? 2 : 1;
+    static constexpr int WT = NT / HALVES;               // rows of A of a promotion warp
+    static constexpr int PROM = 4 * HALVES;
+    static constexpr int WARPS = 4 + PROM;
+    static constexpr int PER_SM = HALVES == 1 ? 2 : 1;
+    static constexpr int STAGE = G * kTile + NT * kBlk;
+    static constexpr int STAGES = (PER_SM == 2 ? 110592 : 212992) / STAGE;
+    static constexpr int BUFS = 4;
+    static constexpr int TMEM = COLS * BUFS;
     static constexpr int RING = STAGES * STAGE;
     static constexpr int SUMS = COLS * kBlk * 4;         // this CTA's sums, in the ring's place
-    static_assert(SUMS <= RING && (TMEM & (TMEM - 1)) == 0 && TMEM <= 256, "");
-    static constexpr int OFF_S = RING;                   // per promotion warp: [2][G][NT] scales
-    static constexpr int OFF_BAR = OFF_S + 4 * 2 * COLS * 4;
+    static_assert(SUMS <= RING && (TMEM & (TMEM - 1)) == 0 && TMEM * PER_SM <= 512, "");
+    // a promotion warp's scales of CH K blocks, A's [CH][WT] then B's [CH][G]; two such
+    // chunks, one ahead
+    static constexpr int CH = GATED ? 2 : 4;
+    static constexpr int SCALES = CH * (WT + G) < 4 ? 4 : (CH * (WT + G) + 3) / 4 * 4;
+    static constexpr int OFF_S = RING;
+    static constexpr int OFF_BAR = OFF_S + PROM * 2 * SCALES * 4;
     static constexpr int NUM_BARS = 2 * STAGES + 2 * BUFS + 1;
     static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
     static constexpr int BYTES = OFF_MISC + 16 + 1024;
-    static_assert(2 * (BYTES + 1024) <= 233472, "two CTAs to an SM");
+    static_assert(PER_SM * (BYTES + 1024) <= 233472, "CTAs to an SM");
 };
 
 template <int NT, int OUT>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(32 * Few<NT, OUT == kB128Gated>::WARPS, Few<NT, OUT == kB128Gated>::PER_SM)
     b128_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const B128Params p) {
     constexpr bool GATED = OUT == kB128Gated;
@@ -81,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         for (int b = 0; b < L::BUFS; ++b) {
             ptx::mbar_init(bar_pfull(b), 1);
-            ptx::mbar_init(bar_pempty(b), 4);
+            ptx::mbar_init(bar_pempty(b), L::PROM);
         }
         ptx::mbar_init(bar_drain, 1);
         *abort_flag = 0;
@@ -153,69 +162,76 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         }
     } else if (warp >= 4) {
-        const int q = warp - 4;
-        const uint32_t lane_base = (uint32_t)(q * 32) << 16;
-        float *sc = reinterpret_cast<float *>(smem + L::OFF_S) + q * 2 * L::COLS;
-        constexpr int SPL = (NT + 31) / 32;  // rows of A whose scales a lane fetches
-        const float *sa[SPL];
-        bool mine[SPL];
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        constexpr int WC = L::G * L::WT;     // this warp's sums a thread
+        const uint32_t taddr = ((uint32_t)(q * 32) << 16) + tmem_base + half * L::WT;
+        float *sc = reinterpret_cast<float *>(smem + L::OFF_S) + (warp - 4) * 2 * L::SCALES;
+        const float *sb = p.sb + (pn + (int64_t)(lane & (L::G - 1)) * p.n_blocks) * p.sb_n;
+        // Scales of K blocks kb .. to chunk i (cp.async; fetched a K block ahead in registers,
+        // each K block waited for its fetch: 1700 cycles)
+        auto ask = [&](int kb, int i) {
+            const uint32_t at = ptx::smem_addr(sc + (i & 1) * L::SCALES);
 #pragma unroll
-        for (int j = 0; j < SPL; ++j) {
-            mine[j] = lane + 32 * j < NT;
-            sa[j] = p.sa + min(m0 + lane + 32 * j, p.M - 1);
-        }
-        const float *sb[L::G];
+            for (int j = 0; j < L::CH; ++j)
+                if (kb + j < kb1) {
 #pragma unroll
-        for (int g = 0; g < L::G; ++g) sb[g] = p.sb + (pn + (int64_t)g * p.n_blocks) * p.sb_n;
-        float na[SPL], nb[L::G];  // the next K block's
-        auto fetch = [&](int kb) {
-            if (kb >= kb1) return;
-#pragma unroll
-            for (int j = 0; j < SPL; ++j) na[j] = __ldg(sa[j] + kb * p.M);
-#pragma unroll
-            for (int g = 0; g < L::G; ++g) nb[g] = __ldg(sb[g] + kb * p.sb_k);
+                    for (int r = 0; r < L::WT; r += 32)
+                        if (lane + r < L::WT)
+                            ptx::cp_async_4(at + (j * L::WT + lane + r) * 4,
+                                            p.sa + (kb + j) * p.M + min(m0 + half * L::WT + lane + r, p.M - 1), 4);
+                    if (lane < L::G) ptx::cp_async_4(at + (L::CH * L::WT + j * L::G + lane) * 4, sb + (kb + j) * p.sb_k, 4);
+                }
+            ptx::cp_async_commit();
         };
-        fetch(kb0);
-        uint64_t acc[L::COLS / 2];
+        ask(kb0, 0);
+        uint64_t acc[WC / 2];
 #pragma unroll
-        for (int i = 0; i < L::COLS / 2; ++i) acc[i] = 0ull;
+        for (int i = 0; i < WC / 2; ++i) acc[i] = 0ull;
         uint32_t buf = 0, bphase = 0;
         bool ok = true;
         for (int kb = kb0; kb < kb1; ++kb) {
-            float *s = sc + ((kb - kb0) & 1) * L::COLS;
+            const int at_k = (kb - kb0) % L::CH, chunk = (kb - kb0) / L::CH;
+            if (at_k == 0) {
+                ptx::cp_async_wait<0>();
+                __syncwarp();  // the chunk is there for every lane, and the one before it read by all
+                ask(kb + L::CH, chunk + 1);
+            }
+            const float *s = sc + (chunk & 1) * L::SCALES;
+            uint64_t fb[L::G];
 #pragma unroll
-            for (int g = 0; g < L::G; ++g)
-#pragma unroll
-                for (int j = 0; j < SPL; ++j)
-                    if (mine[j]) s[g * NT + lane + 32 * j] = __fmul_rn(na[j], nb[g]);
-            fetch(kb + 1);
-            __syncwarp();
+            for (int g = 0; g < L::G; ++g) {
+                const float f = s[L::CH * L::WT + at_k * L::G + g];
+                fb[g] = b128_pair(f, f);
+            }
+            s += at_k * L::WT;
             if (!b128_wait_all(bar_pfull(buf), bphase, abort_flag, p, 3 * 256 + 64 + buf)) {
                 ok = false;
                 break;
             }
             ptx::tc_fence_after();
-            constexpr int STEP = L::COLS < 32 ? L::COLS : 32;
+            constexpr int STEP = L::WT < 32 ? 16 : 32;
 #pragma unroll
-            for (int c = 0; c < L::COLS; c += STEP) {
+            for (int c = 0; c < WC; c += STEP) {
                 uint32_t r[STEP];
+                const uint32_t at = taddr + buf * L::COLS + c / L::WT * NT + c % L::WT;
                 if constexpr (STEP == 32) {
-                    ptx::tmem_ld_32x32b_x32(lane_base + tmem_base + buf * L::COLS + c, r);
+                    ptx::tmem_ld_32x32b_x32(at, r);
                     ptx::tmem_ld_wait(r);
                 } else {
                     uint32_t a[8], b[8];
-                    ptx::tmem_ld_32x32b_x8(lane_base + tmem_base + buf * L::COLS + c, a);
-                    ptx::tmem_ld_32x32b_x8(lane_base + tmem_base + buf * L::COLS + c + 8, b);
+                    ptx::tmem_ld_32x32b_x8(at, a);
+                    ptx::tmem_ld_32x32b_x8(at + 8, b);
                     ptx::tmem_ld_wait(a, b);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) r[i] = a[i], r[8 + i] = b[i];
                 }
-                const ulonglong2 *s2 = reinterpret_cast<const ulonglong2 *>(s + c);
+                const ulonglong2 *s2 = reinterpret_cast<const ulonglong2 *>(s + c % L::WT);
 #pragma unroll
                 for (int i = 0; i < STEP / 4; ++i) {
-                    const ulonglong2 f = s2[i];
-                    b128_fma2(acc[c / 2 + 2 * i], b128_pair(r[4 * i], r[4 * i + 1]), f.x);
-                    b128_fma2(acc[c / 2 + 2 * i + 1], b128_pair(r[4 * i + 2], r[4 * i + 3]), f.y);
+                    const ulonglong2 f = s2[i];  // the same address in every lane
+                    const uint64_t w = fb[c / L::WT];
+                    b128_fma2(acc[c / 2 + 2 * i], b128_pair(r[4 * i], r[4 * i + 1]), b128_mul2(f.x, w));
+                    b128_fma2(acc[c / 2 + 2 * i + 1], b128_pair(r[4 * i + 2], r[4 * i + 3]), b128_mul2(f.y, w));
                 }
             }
             ptx::tc_fence_before();
@@ -229,11 +245,12 @@ __global__ void __launch_bounds__(kThreads, 2)
         // every MMA and every copy of this CTA is done: its sums take the ring's place,
         // [column][weight row]
         if (ok) {
-            float *sums = reinterpret_cast<float *>(smem);
+            float *sums = reinterpret_cast<float *>(smem) + half * L::WT * kBlk + q * 32 + lane;
 #pragma unroll
-            for (int i = 0; i < L::COLS / 2; ++i) {
-                sums[(2 * i) * kBlk + q * 32 + lane] = b128_lo(acc[i]);
-                sums[(2 * i + 1) * kBlk + q * 32 + lane] = b128_hi(acc[i]);
+            for (int i = 0; i < WC / 2; ++i) {
+                const int col = 2 * i / L::WT * NT + 2 * i % L::WT;
+                sums[col * kBlk] = b128_lo(acc[i]);
+                sums[(col + 1) * kBlk] = b128_hi(acc[i]);
             }
         }
     }
@@ -263,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         return v;
     };
-    for (int i = rank + split * warp; i < NT && m0 + i < p.M; i += split * (kThreads / 32)) {
+    for (int i = rank + split * warp; i < NT && m0 + i < p.M; i += split * L::WARPS) {
         const int64_t m = m0 + i, n = (int64_t)pn * kBlk + 4 * lane;
         if constexpr (!GATED) {
             float4 v = total(i);
@@ -313,7 +330,7 @@ cudaError_t launch_few(const CUtensorMap &A, const CUtensorMap &B, const B128Par
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.n_blocks, (unsigned)((p.M + NT - 1) / NT), (unsigned)split);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(32 * L::WARPS, 1, 1);
     cfg.dynamicSmemBytes = L::BYTES;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -341,11 +358,13 @@ cudaError_t few_out(const CUtensorMap &A, const CUtensorMap &B, const B128Params
 cudaError_t launch_b128_few(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p, int out,
                             int nt, int split, cudaStream_t stream) {
     if (out == kB128Gated)
-        return nt == 16 ? launch_few<16, kB128Gated>(A, B, p, split, stream)
-                        : launch_few<32, kB128Gated>(A, B, p, split, stream);
-    return nt == 16   ? few_out<16>(A, B, p, out, split, stream)
-           : nt == 32 ? few_out<32>(A, B, p, out, split, stream)
-                      : few_out<64>(A, B, p, out, split, stream);
+        return nt == 16   ? launch_few<16, kB128Gated>(A, B, p, split, stream)
+               : nt == 32 ? launch_few<32, kB128Gated>(A, B, p, split, stream)
+                          : launch_few<64, kB128Gated>(A, B, p, split, stream);
+    return nt == 16    ? few_out<16>(A, B, p, out, split, stream)
+           : nt == 32  ? few_out<32>(A, B, p, out, split, stream)
+           : nt == 64  ? few_out<64>(A, B, p, out, split, stream)
+                       : few_out<128>(A, B, p, out, split, stream);
 }
 
 }  // namespace fp8g

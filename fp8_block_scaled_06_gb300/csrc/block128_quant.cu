@@ -42,11 +42,11 @@ __device__ __forceinline__ void widen4(const uint2 u, float (&v)[4]) {
 // rows x (16 * PIECES) bytes, `pitch` bytes apart in memory, to dst, packed; of a row
 // the first `bytes` exist; rows past `rows` and bytes past `bytes` are filled with
 // zeros and read nothing.
-template <int PIECES>
+template <int PIECES, int THREADS = kTileThreads>
 __device__ __forceinline__ void copy_tile(uint32_t dst, const void *src, int64_t pitch, int rows, int bytes) {
 #pragma unroll
-    for (int k = 0; k < kBlk * PIECES / kTileThreads; ++k) {
-        const int j = threadIdx.x + k * kTileThreads, r = j / PIECES, b = j % PIECES * 16;
+    for (int k = 0; k < kBlk * PIECES / THREADS; ++k) {
+        const int j = threadIdx.x + k * THREADS, r = j / PIECES, b = j % PIECES * 16;
         const bool in = r < rows && b < bytes;
         ptx::cp_async_16(dst + j * 16, static_cast<const uint8_t *>(src) + (in ? r * pitch + b : 0), in ? 16 : 0);
     }
@@ -218,125 +218,145 @@ __global__ void __launch_bounds__(kTileThreads) b128_quant_tile_kernel(const B12
 
 // ------------------------------------------------------------ gated backward
 
-// dg, du and h are computed twice from the tile, for the maxima and for the codes (kept
-// in fp32 they would take 192 registers).
+// One CTA an SM takes tile after tile, the next one's copies running beside this one's
+// arithmetic.  dg, du and h of a tile stay in registers (8 rows of four columns a
+// thread, 96 values) between the maxima and the codes: computed for both (and four
+// such CTAs an SM, none with a tile ahead) the arithmetic bound it, 162 us at
+// 4099 x 14336 for  now.
+constexpr int kBackThreads = 512;
+constexpr int kBackRows = kBlk / (kBackThreads / 32);
+
 template <bool BF16>
 struct BackTile {
     static constexpr int D = BF16 ? 2 : 4;  // bytes of a value of dh
     static constexpr int OFF_U = kBlk * kBlk, OFF_D = 2 * kBlk * kBlk;
     static constexpr int OFF_S = OFF_D + D * kBlk * kBlk;  // scales of g, u: [2][128]
-    static constexpr int OFF_M = OFF_S + 2 * kBlk * 4;     // column maxima of dg, du, h: [3][128]
-    static constexpr int BYTES = OFF_M + 3 * kBlk * 4;
+    static constexpr int TILE = OFF_S + 2 * kBlk * 4;
+    static constexpr int OFF_M = 2 * TILE;                 // column maxima of dg, du, h: [2][3][128]
+    static constexpr int BYTES = OFF_M + 2 * 3 * kBlk * 4;
 };
 
 template <bool BF16, int GATE, int FMT>
-__global__ void __launch_bounds__(kTileThreads, BF16 ? 3 : 2) b128_backward_kernel(const B128Backward a) {
+__global__ void __launch_bounds__(kBackThreads, 1) b128_backward_kernel(const B128Backward a) {
     using L = BackTile<BF16>;
     extern __shared__ __align__(16) uint8_t sm[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t row0 = (int64_t)blockIdx.y * kBlk, c0 = (int64_t)blockIdx.x * kBlk;
-    const int64_t F = a.F, F2 = 2 * F, fb = gridDim.x;
-    const int rows = (int)min((int64_t)kBlk, a.M - row0);
-    uint32_t *top = reinterpret_cast<uint32_t *>(sm + L::OFF_M);
-    for (int i = threadIdx.x; i < 3 * kBlk; i += kTileThreads) top[i] = 0u;
+    const int64_t F = a.F, F2 = 2 * F;
+    const int32_t fb = (int32_t)(F / kBlk), tiles = fb * (int32_t)((a.M + kBlk - 1) / kBlk);
+    uint32_t *tops = reinterpret_cast<uint32_t *>(sm + L::OFF_M);
+    for (int i = threadIdx.x; i < 2 * 3 * kBlk; i += kBackThreads) tops[i] = 0u;
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    const uint32_t base = ptx::smem_addr(sm);
-    copy_tile<8>(base, a.gu + row0 * F2 + c0, F2, rows, kBlk);
-    copy_tile<8>(base + L::OFF_U, a.gu + row0 * F2 + F + c0, F2, rows, kBlk);
-    copy_tile<8 * L::D>(base + L::OFF_D, static_cast<const uint8_t *>(a.dh) + (row0 * F + c0) * L::D, F * L::D, rows,
-                        kBlk * L::D);
-    {
-        const int r = threadIdx.x & (kBlk - 1), up = threadIdx.x / kBlk;
-        ptx::cp_async_4(base + L::OFF_S + threadIdx.x * 4, a.sgu + (up * fb + blockIdx.x) * a.M + row0 + min(r, rows - 1), 4);
-    }
-    ptx::cp_async_commit();
-    ptx::cp_async_wait<0>();
-    __syncthreads();
-    const uint32_t *gq = reinterpret_cast<const uint32_t *>(sm), *uq = gq + L::OFF_U / 4;
-    const float *sg = reinterpret_cast<const float *>(sm + L::OFF_S), *su = sg + kBlk;
-    auto values = [&](int r, float (&dg)[4], float (&du)[4], float (&h)[4]) {
-        float g[4], u[4], x[4];
-        b128_decode(gq[r * 32 + lane], FP8G_E4M3, g);
-        b128_decode(uq[r * 32 + lane], FP8G_E4M3, u);
-        if constexpr (BF16) {
-            widen4(reinterpret_cast<const uint2 *>(sm + L::OFF_D)[r * 32 + lane], x);
-        } else {
-            const float4 w = reinterpret_cast<const float4 *>(sm + L::OFF_D)[r * 32 + lane];
-            x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+    // Tile t to buffer i: a group of copies (rows past the last read nothing and become zeros)
+    auto ask = [&](int32_t t, int i) {
+        if (t < tiles) {
+            const int64_t row0 = (int64_t)(t / fb) * kBlk, c0 = (int64_t)(t % fb) * kBlk;
+            const int rows = (int)min((int64_t)kBlk, a.M - row0);
+            const uint32_t base = ptx::smem_addr(sm) + i * L::TILE;
+            copy_tile<8, kBackThreads>(base, a.gu + row0 * F2 + c0, F2, rows, kBlk);
+            copy_tile<8, kBackThreads>(base + L::OFF_U, a.gu + row0 * F2 + F + c0, F2, rows, kBlk);
+            copy_tile<8 * L::D, kBackThreads>(base + L::OFF_D, static_cast<const uint8_t *>(a.dh) + (row0 * F + c0) * L::D,
+                                              F * L::D, rows, kBlk * L::D);
+            if (threadIdx.x < 2 * kBlk) {
+                const int r = threadIdx.x & (kBlk - 1), up = threadIdx.x / kBlk;
+                ptx::cp_async_4(base + L::OFF_S + threadIdx.x * 4,
+                                a.sgu + ((int64_t)up * fb + t % fb) * a.M + row0 + min(r, rows - 1), 4);
+            }
         }
-        const float s0 = sg[r], s1 = su[r];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float y, dy;
-            const float uu = __fmul_rn(u[k], s1);
-            b128_gate_grad(__fmul_rn(g[k], s0), GATE, y, dy);
-            dg[k] = x[k] * uu * dy;
-            du[k] = x[k] * y;
-            h[k] = y * uu;
-        }
+        ptx::cp_async_commit();
     };
-    // (rows past the last are zeros)
-    const int first = warp * kRowsPerWarp;
-    float mg[4] = {}, mu[4] = {}, mh[4] = {};
-    float own_g = 0.0f, own_u = 0.0f;
-#pragma unroll 2
-    for (int i = 0; i < kRowsPerWarp; ++i) {
-        float dg[4], du[4], h[4];
-        values(first + i, dg, du, h);
-        const float a0 = b128_warp_max(b128_amax4(dg[0], dg[1], dg[2], dg[3]));
-        const float a1 = b128_warp_max(b128_amax4(du[0], du[1], du[2], du[3]));
-        own_g = lane == i ? a0 : own_g;
-        own_u = lane == i ? a1 : own_u;
+    ask((int32_t)blockIdx.x, 0);
+    const int first = warp * kBackRows;
+    int i = 0;
+    for (int32_t t = (int32_t)blockIdx.x; t < tiles; t += (int32_t)gridDim.x, i ^= 1) {
+        ptx::cp_async_wait<0>();
+        __syncthreads();  // this tile is there, and the other buffer read by all
+        ask(t + (int32_t)gridDim.x, i ^ 1);
+        const int64_t row0 = (int64_t)(t / fb) * kBlk, c0 = (int64_t)(t % fb) * kBlk;
+        const int rows = (int)min((int64_t)kBlk, a.M - row0);
+        const uint8_t *tile = sm + i * L::TILE;
+        const uint32_t *gq = reinterpret_cast<const uint32_t *>(tile), *uq = gq + L::OFF_U / 4;
+        const float *sg = reinterpret_cast<const float *>(tile + L::OFF_S), *su = sg + kBlk;
+        uint32_t *top = tops + i * 3 * kBlk;
+        float dg[kBackRows][4], du[kBackRows][4], h[kBackRows][4];
+        float mg[4] = {}, mu[4] = {}, mh[4] = {};
+        float own_g = 0.0f, own_u = 0.0f;  // lane j: row first + j's
+#pragma unroll
+        for (int j = 0; j < kBackRows; ++j) {
+            const int r = first + j;
+            float g[4], u[4], x[4];
+            b128_decode(gq[r * 32 + lane], FP8G_E4M3, g);
+            b128_decode(uq[r * 32 + lane], FP8G_E4M3, u);
+            if constexpr (BF16) {
+                widen4(reinterpret_cast<const uint2 *>(tile + L::OFF_D)[r * 32 + lane], x);
+            } else {
+                const float4 w = reinterpret_cast<const float4 *>(tile + L::OFF_D)[r * 32 + lane];
+                x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+            }
+            const float s0 = sg[r], s1 = su[r];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float y, dy;
+                const float uu = __fmul_rn(u[k], s1);
+                b128_gate_grad(__fmul_rn(g[k], s0), GATE, y, dy);
+                dg[j][k] = x[k] * uu * dy;
+                du[j][k] = x[k] * y;
+                h[j][k] = y * uu;
+                mg[k] = fmaxf(mg[k], fabsf(dg[j][k]));
+                mu[k] = fmaxf(mu[k], fabsf(du[j][k]));
+                mh[k] = fmaxf(mh[k], fabsf(h[j][k]));
+            }
+            const float a0 = b128_warp_max(b128_amax4(dg[j][0], dg[j][1], dg[j][2], dg[j][3]));
+            const float a1 = b128_warp_max(b128_amax4(du[j][0], du[j][1], du[j][2], du[j][3]));
+            own_g = lane == j ? a0 : own_g;
+            own_u = lane == j ? a1 : own_u;
+        }
+        // (magnitudes that are not NaN: their bits are in order)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            mg[k] = fmaxf(mg[k], fabsf(dg[k]));
-            mu[k] = fmaxf(mu[k], fabsf(du[k]));
-            mh[k] = fmaxf(mh[k], fabsf(h[k]));
+            atomicMax(top + 4 * lane + k, __float_as_uint(mg[k]));
+            atomicMax(top + kBlk + 4 * lane + k, __float_as_uint(mu[k]));
+            atomicMax(top + 2 * kBlk + 4 * lane + k, __float_as_uint(mh[k]));
         }
-    }
+        own_g = b128_scale<FMT>(own_g);
+        own_u = b128_scale<FMT>(own_u);
+        if (lane < kBackRows && first + lane < rows) {
+            a.s_row[(int64_t)(t % fb) * a.M + row0 + first + lane] = own_g;
+            a.s_row[((int64_t)fb + t % fb) * a.M + row0 + first + lane] = own_u;
+        }
+        own_g = __frcp_rn(own_g);
+        own_u = __frcp_rn(own_u);
+        __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        atomicMax(top + 4 * lane + k, __float_as_uint(mg[k]));
-        atomicMax(top + kBlk + 4 * lane + k, __float_as_uint(mu[k]));
-        atomicMax(top + 2 * kBlk + 4 * lane + k, __float_as_uint(mh[k]));
-    }
-    own_g = b128_scale<FMT>(own_g);
-    own_u = b128_scale<FMT>(own_u);
-    if (lane < kRowsPerWarp && first + lane < rows) {
-        a.s_row[blockIdx.x * a.M + row0 + first + lane] = own_g;
-        a.s_row[(fb + blockIdx.x) * a.M + row0 + first + lane] = own_u;
-    }
-    own_g = __frcp_rn(own_g);
-    own_u = __frcp_rn(own_u);
-    __syncthreads();
+        for (int k = 0; k < 4; ++k) {
+            mg[k] = b128_scale<FMT>(__uint_as_float(top[4 * lane + k]));
+            mu[k] = b128_scale<FMT>(__uint_as_float(top[kBlk + 4 * lane + k]));
+            mh[k] = b128_scale<FP8G_E4M3>(__uint_as_float(top[2 * kBlk + 4 * lane + k]));
+        }
+        if (warp == 0) {
+            float *s = a.s_col + (int64_t)(t / fb) * F2 + c0 + 4 * lane;
+            *reinterpret_cast<float4 *>(s) = make_float4(mg[0], mg[1], mg[2], mg[3]);
+            *reinterpret_cast<float4 *>(s + F) = make_float4(mu[0], mu[1], mu[2], mu[3]);
+            *reinterpret_cast<float4 *>(a.s_h + (int64_t)(t / fb) * F + c0 + 4 * lane) =
+                make_float4(mh[0], mh[1], mh[2], mh[3]);
+        }
+        // the other buffer's maxima were read before this tile's first barrier: zeros for
+        // the next tile
+        for (int k = threadIdx.x; k < 3 * kBlk; k += kBackThreads) tops[(i ^ 1) * 3 * kBlk + k] = 0u;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        mg[k] = b128_scale<FMT>(__uint_as_float(top[4 * lane + k]));
-        mu[k] = b128_scale<FMT>(__uint_as_float(top[kBlk + 4 * lane + k]));
-        mh[k] = b128_scale<FP8G_E4M3>(__uint_as_float(top[2 * kBlk + 4 * lane + k]));
-    }
-    if (warp == 0) {
-        float *s = a.s_col + (int64_t)blockIdx.y * F2 + c0 + 4 * lane;
-        *reinterpret_cast<float4 *>(s) = make_float4(mg[0], mg[1], mg[2], mg[3]);
-        *reinterpret_cast<float4 *>(s + F) = make_float4(mu[0], mu[1], mu[2], mu[3]);
-        *reinterpret_cast<float4 *>(a.s_h + (int64_t)blockIdx.y * F + c0 + 4 * lane) =
-            make_float4(mh[0], mh[1], mh[2], mh[3]);
-    }
+        for (int k = 0; k < 4; ++k) mg[k] = __frcp_rn(mg[k]), mu[k] = __frcp_rn(mu[k]), mh[k] = __frcp_rn(mh[k]);
+        const int64_t at = (row0 + first) * F2 + c0 + 4 * lane;
+        uint8_t *row = a.row + at, *col = a.col + at, *hq = a.h + (row0 + first) * F + c0 + 4 * lane;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) mg[k] = __frcp_rn(mg[k]), mu[k] = __frcp_rn(mu[k]), mh[k] = __frcp_rn(mh[k]);
-#pragma unroll 2
-    for (int i = 0; i < kRowsPerWarp; ++i) {
-        float dg[4], du[4], h[4];
-        values(first + i, dg, du, h);
-        const float r0 = __shfl_sync(0xffffffffu, own_g, i), r1 = __shfl_sync(0xffffffffu, own_u, i);
-        if (first + i < rows) {
-            const int64_t at = (row0 + first + i) * F2 + c0 + 4 * lane;
-            *reinterpret_cast<uint32_t *>(a.row + at) = b128_codes<FMT>(dg[0], dg[1], dg[2], dg[3], r0);
-            *reinterpret_cast<uint32_t *>(a.row + at + F) = b128_codes<FMT>(du[0], du[1], du[2], du[3], r1);
-            *reinterpret_cast<uint32_t *>(a.col + at) = b128_codes4<FMT>(dg, mg);
-            *reinterpret_cast<uint32_t *>(a.col + at + F) = b128_codes4<FMT>(du, mu);
-            *reinterpret_cast<uint32_t *>(a.h + (row0 + first + i) * F + c0 + 4 * lane) = b128_codes4<FP8G_E4M3>(h, mh);
+        for (int j = 0; j < kBackRows; ++j) {
+            const float r0 = __shfl_sync(0xffffffffu, own_g, j), r1 = __shfl_sync(0xffffffffu, own_u, j);
+            if (first + j < rows) {
+                *reinterpret_cast<uint32_t *>(row + j * F2) = b128_codes<FMT>(dg[j][0], dg[j][1], dg[j][2], dg[j][3], r0);
+                *reinterpret_cast<uint32_t *>(row + j * F2 + F) = b128_codes<FMT>(du[j][0], du[j][1], du[j][2], du[j][3], r1);
+                *reinterpret_cast<uint32_t *>(col + j * F2) = b128_codes4<FMT>(dg[j], mg);
+                *reinterpret_cast<uint32_t *>(col + j * F2 + F) = b128_codes4<FMT>(du[j], mu);
+                *reinterpret_cast<uint32_t *>(hq + j * F) = b128_codes4<FP8G_E4M3>(h[j], mh);
+            }
         }
     }
 }
@@ -364,11 +384,12 @@ cudaError_t quant_src(const B128Quant &a, cudaStream_t s) {
 
 template <bool BF16, int GATE, int FMT>
 cudaError_t backward_fmt(const B128Backward &a, cudaStream_t s) {
-    const dim3 grid((unsigned)(a.F / kBlk), (unsigned)((a.M + kBlk - 1) / kBlk));
     auto kern = b128_backward_kernel<BF16, GATE, FMT>;
     constexpr int kBytes = BackTile<BF16>::BYTES;
     const cudaError_t e = b128_allow_smem(reinterpret_cast<const void *>(kern), kBytes);
-    return e != cudaSuccess ? e : launch_programmatic_smem(kern, grid, dim3(kTileThreads), kBytes, s, a);
+    const int64_t tiles = (a.M + kBlk - 1) / kBlk * (a.F / kBlk);
+    const dim3 grid((unsigned)min(tiles, (int64_t)a.num_sms));
+    return e != cudaSuccess ? e : launch_programmatic_smem(kern, grid, dim3(kBackThreads), kBytes, s, a);
 }
 
 template <bool BF16, int GATE>
