@@ -18,6 +18,36 @@ __device__ __forceinline__ float b128_scale(float amax) {
     return s == 0.0f && amax == 0.0f ? 1.0f : fmaxf(s, 1.17549435e-38f);
 }
 
+// Packed pairs of fp32 (lo first).
+__device__ __forceinline__ uint64_t b128_pair(float lo, float hi) {
+    return (uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32);
+}
+__device__ __forceinline__ uint64_t b128_pair(uint32_t lo, uint32_t hi) {
+    return (uint64_t)lo | ((uint64_t)hi << 32);
+}
+__device__ __forceinline__ float b128_lo(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float b128_hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+// d += a b
+__device__ __forceinline__ void b128_fma2(uint64_t &d, uint64_t a, uint64_t b) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ uint64_t b128_mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t b128_add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t b128_madd2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 // Codes of four values, first value lowest; NaN gives the code 0x7F.
 template <int FMT>
 __device__ __forceinline__ uint32_t b128_cvt4(float a, float b, float c, float d) {
@@ -33,11 +63,14 @@ __device__ __forceinline__ uint32_t b128_cvt4(float a, float b, float c, float d
 }
 template <int FMT>
 __device__ __forceinline__ uint32_t b128_codes(float a, float b, float c, float d, float r) {
-    return b128_cvt4<FMT>(__fmul_rn(a, r), __fmul_rn(b, r), __fmul_rn(c, r), __fmul_rn(d, r));
+    const uint64_t rr = b128_pair(r, r), x = b128_mul2(b128_pair(a, b), rr), y = b128_mul2(b128_pair(c, d), rr);
+    return b128_cvt4<FMT>(b128_lo(x), b128_hi(x), b128_lo(y), b128_hi(y));
 }
 template <int FMT>
 __device__ __forceinline__ uint32_t b128_codes4(const float (&v)[4], const float (&r)[4]) {
-    return b128_cvt4<FMT>(__fmul_rn(v[0], r[0]), __fmul_rn(v[1], r[1]), __fmul_rn(v[2], r[2]), __fmul_rn(v[3], r[3]));
+    const uint64_t x = b128_mul2(b128_pair(v[0], v[1]), b128_pair(r[0], r[1]));
+    const uint64_t y = b128_mul2(b128_pair(v[2], v[3]), b128_pair(r[2], r[3]));
+    return b128_cvt4<FMT>(b128_lo(x), b128_hi(x), b128_lo(y), b128_hi(y));
 }
 
 // Four codes -> fp32 (exact).
@@ -71,11 +104,12 @@ __device__ __forceinline__ float b128_warp_max(float v) {
 
 // 1 / (1 + e^-g), from the hardware's base-2 exponential and reciprocal (relative
 // error about 2^-22 (1 + |g| / 4), beside the 2^-4 of the codes that it ends in; the
-// exact division took the gated epilogue twice the instructions).
+// exact division took the gated epilogue twice the instructions, and subnormal numbers
+// of the two, flushed here, change no sum with 1 and no fp32 product of note).
 __device__ __forceinline__ float b128_sigmoid(float g) {
     float e, y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(1.0f + e));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + e));
     return y;
 }
 
@@ -94,7 +128,7 @@ __device__ __forceinline__ void b128_gate_grad(float g, int gate, float &y, floa
     } else if (gate == FP8G_GATE_GELU) {
         const float c = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
         float e;
-        asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(g * g * -0.72134752044448170f));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * g * -0.72134752044448170f));
         y = g * c;
         d = c + g * e * 0.39894228040143268f;
     } else {
@@ -103,23 +137,29 @@ __device__ __forceinline__ void b128_gate_grad(float g, int gate, float &y, floa
     }
 }
 
-// Packed pairs of fp32 (lo first).
-__device__ __forceinline__ uint64_t b128_pair(float lo, float hi) {
-    return (uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32);
-}
-__device__ __forceinline__ uint64_t b128_pair(uint32_t lo, uint32_t hi) {
-    return (uint64_t)lo | ((uint64_t)hi << 32);
-}
-__device__ __forceinline__ float b128_lo(uint64_t v) { return __uint_as_float((uint32_t)v); }
-__device__ __forceinline__ float b128_hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
-// d += a b
-__device__ __forceinline__ void b128_fma2(uint64_t &d, uint64_t a, uint64_t b) {
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
-}
-__device__ __forceinline__ uint64_t b128_mul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
+// The same of two values in packed arithmetic.
+template <int GATE>
+__device__ __forceinline__ void b128_gate_grad2(uint64_t g, uint64_t &y, uint64_t &d) {
+    if constexpr (GATE == FP8G_GATE_SILU) {
+        const uint64_t one = b128_pair(1.0f, 1.0f);
+        const uint64_t t = b128_mul2(g, b128_pair(-1.4426950408889634f, -1.4426950408889634f));
+        float e0, e1, s0, s1;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(b128_lo(t)));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(b128_hi(t)));
+        const uint64_t u = b128_add2(b128_pair(e0, e1), one);
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s0) : "f"(b128_lo(u)));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s1) : "f"(b128_hi(u)));
+        const uint64_t s = b128_pair(s0, s1);
+        y = b128_mul2(g, s);
+        const uint64_t rest = b128_madd2(s, b128_pair(-1.0f, -1.0f), one);  // 1 - s, exactly rounded
+        d = b128_mul2(s, b128_madd2(g, rest, one));
+    } else {
+        float y0, y1, d0, d1;
+        b128_gate_grad(b128_lo(g), GATE, y0, d0);
+        b128_gate_grad(b128_hi(g), GATE, y1, d1);
+        y = b128_pair(y0, y1);
+        d = b128_pair(d0, d1);
+    }
 }
 
 }  // namespace fp8g

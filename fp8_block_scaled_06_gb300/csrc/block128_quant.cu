@@ -293,15 +293,20 @@ __global__ void __launch_bounds__(kBackThreads, 1) b128_backward_kernel(const B1
                 const float4 w = reinterpret_cast<const float4 *>(tile + L::OFF_D)[r * 32 + lane];
                 x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
             }
-            const float s0 = sg[r], s1 = su[r];
+            const uint64_t s0 = b128_pair(sg[r], sg[r]), s1 = b128_pair(su[r], su[r]);
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {  // (packed: the instructions bound this kernel)
+                const uint64_t gg = b128_mul2(b128_pair(g[k], g[k + 1]), s0), uu = b128_mul2(b128_pair(u[k], u[k + 1]), s1);
+                const uint64_t xx = b128_pair(x[k], x[k + 1]);
+                uint64_t y, dy;
+                b128_gate_grad2<GATE>(gg, y, dy);
+                const uint64_t vg = b128_mul2(b128_mul2(xx, uu), dy), vu = b128_mul2(xx, y), vh = b128_mul2(y, uu);
+                dg[j][k] = b128_lo(vg), dg[j][k + 1] = b128_hi(vg);
+                du[j][k] = b128_lo(vu), du[j][k + 1] = b128_hi(vu);
+                h[j][k] = b128_lo(vh), h[j][k + 1] = b128_hi(vh);
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                float y, dy;
-                const float uu = __fmul_rn(u[k], s1);
-                b128_gate_grad(__fmul_rn(g[k], s0), GATE, y, dy);
-                dg[j][k] = x[k] * uu * dy;
-                du[j][k] = x[k] * y;
-                h[j][k] = y * uu;
                 mg[k] = fmaxf(mg[k], fabsf(dg[j][k]));
                 mu[k] = fmaxf(mu[k], fabsf(du[j][k]));
                 mh[k] = fmaxf(mh[k], fabsf(h[j][k]));
