@@ -123,10 +123,10 @@ __device__ __forceinline__ void store_codes64(uint8_t *dst, const float (&v)[64]
 }
 
 __device__ __forceinline__ float amax64(const float (&v)[64]) {
-    float m[4] = {};
+    float m[2] = {};
 #pragma unroll
-    for (int i = 0; i < 64; ++i) m[i & 3] = fmaxf(m[i & 3], fabsf(v[i]));
-    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    for (int i = 0; i < 64; i += 2) m[(i >> 1) & 1] = b128_max3(m[(i >> 1) & 1], v[i], v[i + 1]);
+    return fmaxf(m[0], m[1]);
 }
 
 template <bool VECB, int OUT>

@@ -92,9 +92,15 @@ __device__ __forceinline__ void b128_decode(uint32_t q, int fmt, float (&v)[4]) 
     }
 }
 
+// Larger of m (not NaN) and two magnitudes; NaN does not count.
+__device__ __forceinline__ float b128_max3(float m, float a, float b) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
+    return r;
+}
 // Largest magnitude of four values; NaN counts as 0.
 __device__ __forceinline__ float b128_amax4(float a, float b, float c, float d) {
-    return fmaxf(fmaxf(fmaxf(fabsf(a), fabsf(b)), fmaxf(fabsf(c), fabsf(d))), 0.0f);
+    return b128_max3(b128_max3(0.0f, a, b), c, d);
 }
 
 // Largest of the warp's values (>= 0, not NaN: their bits are in order).

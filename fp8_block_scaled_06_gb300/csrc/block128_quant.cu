@@ -96,10 +96,10 @@ __global__ void __launch_bounds__(kTileThreads) b128_quant_rows_kernel(const B12
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        float m[4] = {};
+        float m[2] = {};
 #pragma unroll
-        for (int k = 0; k < 16; ++k) m[k & 3] = fmaxf(m[k & 3], fabsf(v[i][k]));
-        float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+        for (int k = 0; k < 16; k += 2) m[(k >> 1) & 1] = b128_max3(m[(k >> 1) & 1], v[i][k], v[i][k + 1]);
+        float top = fmaxf(m[0], m[1]);
 #pragma unroll
         for (int o = 1; o < 8; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float s = b128_scale<FMT>(top), r = __frcp_rn(s);
@@ -164,15 +164,17 @@ __global__ void __launch_bounds__(kTileThreads) b128_quant_tile_kernel(const B12
     const int first = warp * kRowsPerWarp;
     float cm[4] = {}, own = 0.0f;  // own: lane i has row first + i's
 #pragma unroll 4
-    for (int i = 0; i < kRowsPerWarp; ++i) {
-        float v[4];
+    for (int i = 0; i < kRowsPerWarp; i += 2) {
+        float v[4], w[4];
         values(first + i, v);
+        values(first + i + 1, w);
         if constexpr (ROW) {
-            const float m = b128_warp_max(b128_amax4(v[0], v[1], v[2], v[3]));
-            own = lane == i ? m : own;
+            const float m0 = b128_warp_max(b128_amax4(v[0], v[1], v[2], v[3]));
+            const float m1 = b128_warp_max(b128_amax4(w[0], w[1], w[2], w[3]));
+            own = lane == i ? m0 : lane == i + 1 ? m1 : own;
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) cm[k] = fmaxf(cm[k], fabsf(v[k]));
+        for (int k = 0; k < 4; ++k) cm[k] = b128_max3(cm[k], v[k], w[k]);
     }
     // (magnitudes that are not NaN: their bits are in order)
 #pragma unroll
@@ -305,11 +307,13 @@ __global__ void __launch_bounds__(kBackThreads, 1) b128_backward_kernel(const B1
                 du[j][k] = b128_lo(vu), du[j][k + 1] = b128_hi(vu);
                 h[j][k] = b128_lo(vh), h[j][k + 1] = b128_hi(vh);
             }
+            if (j & 1) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                mg[k] = fmaxf(mg[k], fabsf(dg[j][k]));
-                mu[k] = fmaxf(mu[k], fabsf(du[j][k]));
-                mh[k] = fmaxf(mh[k], fabsf(h[j][k]));
+                for (int k = 0; k < 4; ++k) {
+                    mg[k] = b128_max3(mg[k], dg[j - 1][k], dg[j][k]);
+                    mu[k] = b128_max3(mu[k], du[j - 1][k], du[j][k]);
+                    mh[k] = b128_max3(mh[k], h[j - 1][k], h[j][k]);
+                }
             }
             const float a0 = b128_warp_max(b128_amax4(dg[j][0], dg[j][1], dg[j][2], dg[j][3]));
             const float a1 = b128_warp_max(b128_amax4(du[j][0], du[j][1], du[j][2], du[j][3]));
