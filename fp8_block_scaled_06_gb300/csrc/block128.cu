@@ -206,7 +206,7 @@ fp8g_status fp8_gated_block128(const void *x, const float *sfx, int32_t x_fmt, c
     p.n_blocks = (int32_t)(F / kBlk);
     p.sb_n = p.num_kb;
     p.sb_k = 1;
-    p.gate = gate;
+    p.st32 = is_aligned(h, 32) && is_aligned(gu, 32);
     p.h = h;
     p.sh = sh;
     p.gu = gu;
@@ -228,13 +228,13 @@ fp8g_status fp8_gated_block128(const void *x, const float *sfx, int32_t x_fmt, c
     cudaError_t e;
     if (pl.few) {
         p.types = (tw << 7) | (tx << 10);
-        e = launch_b128_few(mX, mW, p, kB128Gated, pl.nt, pl.split, stream);
+        e = launch_b128_few(mX, mW, p, kB128Gated + gate, pl.nt, pl.split, stream);
     } else {
         p.types = (tx << 7) | (tw << 10);
         p.npm = (int32_t)npm;
         p.npn = p.n_blocks;
         p.T = p.npm * p.npn;
-        e = launch_b128_pair(mX, mW, p, kB128Gated, false, d.num_sms, stream);
+        e = launch_b128_pair(mX, mW, p, kB128Gated + gate, false, d.num_sms, stream);
     }
     return e == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
 }

@@ -27,13 +27,13 @@ struct B128Params {
     void *C;
     int32_t st32;           // 32-byte stores (C 32-byte aligned, rows multiples of 32 B)
     // gated: columns of C are the F columns of h
-    int32_t gate;
     uint8_t *h, *gu;        // codes [M, F], [M, 2F] (gu may be null)
     float *sh, *sgu;        // [F / 128][M], [2 F / 128][M]
     unsigned int *status;
     uint64_t timeout_ns;
 };
 
+// What a product kernel ends in (kB128Gated + FP8G_GATE_*: h = act(g) u in 8 bits).
 enum B128Out : int { kB128Bf16 = 0, kB128F32 = 1, kB128Add = 2, kB128Gated = 3 };
 
 // block128_gemm.cu: CTA pairs over 256 x 256 tiles (gated: 256 rows, 128 columns

@@ -59,10 +59,10 @@ struct Few {
 };
 
 template <int NT, int OUT>
-__global__ void __launch_bounds__(32 * Few<NT, OUT == kB128Gated>::WARPS, Few<NT, OUT == kB128Gated>::PER_SM)
+__global__ void __launch_bounds__(32 * Few<NT, (OUT >= kB128Gated)>::WARPS, Few<NT, (OUT >= kB128Gated)>::PER_SM)
     b128_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const B128Params p) {
-    constexpr bool GATED = OUT == kB128Gated;
+    constexpr bool GATED = (OUT >= kB128Gated);
     using L = Few<NT, GATED>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = ptx::smem_addr(smem_raw);
@@ -300,8 +300,9 @@ __global__ void __launch_bounds__(32 * Few<NT, OUT == kB128Gated>::WARPS, Few<NT
             }
         } else {
             const float4 g = total(i), u = total(NT + i);
-            const float4 h = make_float4(__fmul_rn(b128_gate(g.x, p.gate), u.x), __fmul_rn(b128_gate(g.y, p.gate), u.y),
-                                         __fmul_rn(b128_gate(g.z, p.gate), u.z), __fmul_rn(b128_gate(g.w, p.gate), u.w));
+            constexpr int GATE = GATED ? OUT - kB128Gated : 0;
+            const float4 h = make_float4(__fmul_rn(b128_gate<GATE>(g.x), u.x), __fmul_rn(b128_gate<GATE>(g.y), u.y),
+                                         __fmul_rn(b128_gate<GATE>(g.z), u.z), __fmul_rn(b128_gate<GATE>(g.w), u.w));
             auto code = [&](const float4 v, uint8_t *q, float *s) {
                 const float sv = b128_scale<FP8G_E4M3>(b128_warp_max(b128_amax4(v.x, v.y, v.z, v.w)));
                 *reinterpret_cast<uint32_t *>(q) = b128_codes<FP8G_E4M3>(v.x, v.y, v.z, v.w, __frcp_rn(sv));
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(32 * Few<NT, OUT == kB128Gated>::WARPS, Few<NT
 template <int NT, int OUT>
 cudaError_t launch_few(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p, int split,
                        cudaStream_t stream) {
-    using L = Few<NT, OUT == kB128Gated>;
+    using L = Few<NT, (OUT >= kB128Gated)>;
     auto kern = b128_few_kernel<NT, OUT>;
     const cudaError_t e = b128_allow_smem(reinterpret_cast<const void *>(kern), L::BYTES);
     if (e != cudaSuccess) return e;
@@ -353,14 +354,21 @@ cudaError_t few_out(const CUtensorMap &A, const CUtensorMap &B, const B128Params
     return launch_few<NT, kB128Add>(A, B, p, split, stream);
 }
 
+template <int OUT>
+cudaError_t few_gated(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p, int nt, int split,
+                      cudaStream_t stream) {
+    return nt == 16   ? launch_few<16, OUT>(A, B, p, split, stream)
+           : nt == 32 ? launch_few<32, OUT>(A, B, p, split, stream)
+                      : launch_few<64, OUT>(A, B, p, split, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_b128_few(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p, int out,
                             int nt, int split, cudaStream_t stream) {
-    if (out == kB128Gated)
-        return nt == 16   ? launch_few<16, kB128Gated>(A, B, p, split, stream)
-               : nt == 32 ? launch_few<32, kB128Gated>(A, B, p, split, stream)
-                          : launch_few<64, kB128Gated>(A, B, p, split, stream);
+    if (out == kB128Gated + FP8G_GATE_SILU) return few_gated<kB128Gated + FP8G_GATE_SILU>(A, B, p, nt, split, stream);
+    if (out == kB128Gated + FP8G_GATE_GELU) return few_gated<kB128Gated + FP8G_GATE_GELU>(A, B, p, nt, split, stream);
+    if (out == kB128Gated + FP8G_GATE_RELU) return few_gated<kB128Gated + FP8G_GATE_RELU>(A, B, p, nt, split, stream);
     return nt == 16    ? few_out<16>(A, B, p, out, split, stream)
            : nt == 32  ? few_out<32>(A, B, p, out, split, stream)
            : nt == 64  ? few_out<64>(A, B, p, out, split, stream)

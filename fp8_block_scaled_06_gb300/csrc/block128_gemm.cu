@@ -85,8 +85,8 @@ struct ScaleChunks {
         if constexpr (VECB) {  // four columns a lane (N is a multiple of 16)
             b = p.sb + min((int64_t)pn * 2 * kBlk + half * 64 + 4 * lane + (lane >= 16 ? 64 : 0), p.N - 4);
         } else {
-            const int64_t n0 = OUT == kB128Gated ? pn : 2 * pn;
-            const int64_t n1 = OUT == kB128Gated ? n0 + p.n_blocks : min(n0 + 1, (int64_t)p.n_blocks - 1);
+            const int64_t n0 = OUT >= kB128Gated ? pn : 2 * pn;
+            const int64_t n1 = OUT >= kB128Gated ? n0 + p.n_blocks : min(n0 + 1, (int64_t)p.n_blocks - 1);
             b = p.sb + ((lane & 1) == 0 ? n0 : n1) * p.sb_n;
         }
     }
@@ -109,16 +109,20 @@ struct ScaleChunks {
     }
 };
 
-// 64 codes of one row from 64 values times r, 16-byte stores (dst 16-byte aligned).
-__device__ __forceinline__ void store_codes64(uint8_t *dst, const float (&v)[64], float r) {
+// 64 codes of one row from 64 values times r, in 32-byte stores (wide; each a whole
+// sector) or 16-byte ones.
+__device__ __forceinline__ void store_codes64(uint8_t *dst, const float (&v)[64], float r, bool wide) {
+    uint32_t o[16];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        uint4 o;
-        o.x = b128_codes<FP8G_E4M3>(v[16 * w], v[16 * w + 1], v[16 * w + 2], v[16 * w + 3], r);
-        o.y = b128_codes<FP8G_E4M3>(v[16 * w + 4], v[16 * w + 5], v[16 * w + 6], v[16 * w + 7], r);
-        o.z = b128_codes<FP8G_E4M3>(v[16 * w + 8], v[16 * w + 9], v[16 * w + 10], v[16 * w + 11], r);
-        o.w = b128_codes<FP8G_E4M3>(v[16 * w + 12], v[16 * w + 13], v[16 * w + 14], v[16 * w + 15], r);
-        reinterpret_cast<uint4 *>(dst)[w] = o;
+    for (int w = 0; w < 16; ++w)
+        o[w] = b128_codes<FP8G_E4M3>(v[4 * w], v[4 * w + 1], v[4 * w + 2], v[4 * w + 3], r);
+    if (wide) {
+        ptx::st_global_v8(dst, o);
+        ptx::st_global_v8(dst + 32, o + 8);
+    } else {
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            reinterpret_cast<uint4 *>(dst)[w] = make_uint4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
     }
 }
 
@@ -208,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (leader) ptx::mbar_arrive_expect_tx(fb, 4 * kTile);
                         const int32_t k0 = kb * kBlk;
                         ptx::tma_load_2d_pair(sbase + stage * kTile, &tmA, fb, p.a_mn ? m0 : k0, p.a_mn ? k0 : m0);
-                        if constexpr (OUT == kB128Gated)  // gate rows to the even CTA, up rows to the odd one
+                        if constexpr (OUT >= kB128Gated)  // gate rows to the even CTA, up rows to the odd one
                             ptx::tma_load_3d_pair(sbase + L::OFF_B + stage * kTile, &tmB, fb, k0, pn * kBlk, (int32_t)rank);
                         else
                             ptx::tma_load_2d_pair(sbase + L::OFF_B + stage * kTile, &tmB, fb, p.b_mn ? n0 : k0,
@@ -394,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-            } else if constexpr (OUT != kB128Gated) {
+            } else if constexpr (OUT < kB128Gated) {
                 const int64_t n0 = (int64_t)tn * 2 * kBlk + half * 64;
                 if (row < p.M) {
 #pragma unroll
@@ -427,7 +431,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool keep = p.gu != nullptr;
                 float4 top = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-                for (int i = 0; i < 64; ++i) h[i] = __fmul_rn(b128_gate(gv[i], p.gate), uv[i]);
+                for (int i = 0; i < 64; i += 2) {
+                    const uint64_t y = b128_gate2<OUT - kB128Gated>(b128_pair(gv[i], gv[i + 1]));
+                    const uint64_t v = b128_mul2(y, b128_pair(uv[i], uv[i + 1]));
+                    h[i] = b128_lo(v), h[i + 1] = b128_hi(v);
+                }
                 top.x = amax64(h);
                 if (keep) {
                     top.y = amax64(gv);
@@ -444,13 +452,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (row < p.M) {
                     const int64_t F = p.N, f = (int64_t)tn * kBlk + half * 64;
                     const float sh = b128_scale<FP8G_E4M3>(fmaxf(top.x, o.x));
-                    store_codes64(p.h + row * F + f, h, __frcp_rn(sh));
+                    store_codes64(p.h + row * F + f, h, __frcp_rn(sh), p.st32 != 0);
                     if (half == 0) p.sh[tn * p.M + row] = sh;
                     if (keep) {
                         const float sg = b128_scale<FP8G_E4M3>(fmaxf(top.y, o.y));
                         const float su = b128_scale<FP8G_E4M3>(fmaxf(top.z, o.z));
-                        store_codes64(p.gu + row * 2 * F + f, gv, __frcp_rn(sg));
-                        store_codes64(p.gu + row * 2 * F + F + f, uv, __frcp_rn(su));
+                        store_codes64(p.gu + row * 2 * F + f, gv, __frcp_rn(sg), p.st32 != 0);
+                        store_codes64(p.gu + row * 2 * F + F + f, uv, __frcp_rn(su), p.st32 != 0);
                         if (half == 0) {
                             p.sgu[tn * p.M + row] = sg;
                             p.sgu[(p.n_blocks + tn) * p.M + row] = su;
@@ -525,7 +533,9 @@ cudaError_t launch_pair(const CUtensorMap &A, const CUtensorMap &B, const B128Pa
 cudaError_t launch_b128_pair(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p,
                              int out, bool vec_b, int num_sms, cudaStream_t stream) {
     const int grid = 2 * (int)min((int64_t)p.T, (int64_t)num_sms / 2);
-    if (out == kB128Gated) return launch_pair<false, kB128Gated>(A, B, p, grid, stream);
+    if (out == kB128Gated + FP8G_GATE_SILU) return launch_pair<false, kB128Gated + FP8G_GATE_SILU>(A, B, p, grid, stream);
+    if (out == kB128Gated + FP8G_GATE_GELU) return launch_pair<false, kB128Gated + FP8G_GATE_GELU>(A, B, p, grid, stream);
+    if (out == kB128Gated + FP8G_GATE_RELU) return launch_pair<false, kB128Gated + FP8G_GATE_RELU>(A, B, p, grid, stream);
     if (vec_b) {
         if (out == kB128Bf16) return launch_pair<true, kB128Bf16>(A, B, p, grid, stream);
         return out == kB128F32 ? launch_pair<true, kB128F32>(A, B, p, grid, stream)

@@ -119,9 +119,10 @@ __device__ __forceinline__ float b128_sigmoid(float g) {
     return y;
 }
 
-__device__ __forceinline__ float b128_gate(float g, int gate) {
-    if (gate == FP8G_GATE_SILU) return g * b128_sigmoid(g);
-    if (gate == FP8G_GATE_GELU) return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
+template <int GATE>
+__device__ __forceinline__ float b128_gate(float g) {
+    if (GATE == FP8G_GATE_SILU) return g * b128_sigmoid(g);
+    if (GATE == FP8G_GATE_GELU) return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
     return g < 0.0f ? 0.0f : g;
 }
 
@@ -143,21 +144,30 @@ __device__ __forceinline__ void b128_gate_grad(float g, int gate, float &y, floa
     }
 }
 
-// The same of two values in packed arithmetic.
+// 1 / (1 + e^-g) of two values.
+__device__ __forceinline__ uint64_t b128_sigmoid2(uint64_t g) {
+    const uint64_t t = b128_mul2(g, b128_pair(-1.4426950408889634f, -1.4426950408889634f));
+    float e0, e1, s0, s1;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(b128_lo(t)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(b128_hi(t)));
+    const uint64_t u = b128_add2(b128_pair(e0, e1), b128_pair(1.0f, 1.0f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s0) : "f"(b128_lo(u)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s1) : "f"(b128_hi(u)));
+    return b128_pair(s0, s1);
+}
+
+// The activation of two values; its value and derivative.
+template <int GATE>
+__device__ __forceinline__ uint64_t b128_gate2(uint64_t g) {
+    if constexpr (GATE == FP8G_GATE_SILU) return b128_mul2(g, b128_sigmoid2(g));
+    return b128_pair(b128_gate<GATE>(b128_lo(g)), b128_gate<GATE>(b128_hi(g)));
+}
 template <int GATE>
 __device__ __forceinline__ void b128_gate_grad2(uint64_t g, uint64_t &y, uint64_t &d) {
     if constexpr (GATE == FP8G_GATE_SILU) {
-        const uint64_t one = b128_pair(1.0f, 1.0f);
-        const uint64_t t = b128_mul2(g, b128_pair(-1.4426950408889634f, -1.4426950408889634f));
-        float e0, e1, s0, s1;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(b128_lo(t)));
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(b128_hi(t)));
-        const uint64_t u = b128_add2(b128_pair(e0, e1), one);
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s0) : "f"(b128_lo(u)));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s1) : "f"(b128_hi(u)));
-        const uint64_t s = b128_pair(s0, s1);
+        const uint64_t one = b128_pair(1.0f, 1.0f), s = b128_sigmoid2(g);
         y = b128_mul2(g, s);
-        const uint64_t rest = b128_madd2(s, b128_pair(-1.0f, -1.0f), one);  // 1 - s, exactly rounded
+        const uint64_t rest = b128_madd2(s, b128_pair(-1.0f, -1.0f), one);  // 1 - s, rounded once
         d = b128_mul2(s, b128_madd2(g, rest, one));
     } else {
         float y0, y1, d0, d1;
