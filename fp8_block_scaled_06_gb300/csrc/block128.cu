@@ -128,6 +128,8 @@ fp8g_status fp8_gemm_block128(int32_t form, const void *A, const float *sfa, int
     if (M > 0 && K > 0 && (A == nullptr || sfa == nullptr || B == nullptr || sfb == nullptr))
         return FP8G_ERR_INVALID_ARG;
     if (M >= kMaxDim || N >= kMaxDim || K >= kMaxDim) return FP8G_ERR_UNSUPPORTED_SHAPE;
+    const int64_t npm = (M + 2 * kBlk - 1) / (2 * kBlk), npn = (N + 2 * kBlk - 1) / (2 * kBlk);
+    if (npm * npn >= kMaxDim) return FP8G_ERR_UNSUPPORTED_SHAPE;
     const int64_t esz = out == FP8G_OUT_F32 ? 4 : 2;
     if ((!tn && K % 16 != 0) || (tn && M % 16 != 0) || (form != FP8G_NT && N % 16 != 0) || N * esz % 16 != 0)
         return FP8G_ERR_ALIGNMENT;
@@ -158,8 +160,6 @@ fp8g_status fp8_gemm_block128(int32_t form, const void *A, const float *sfa, int
     p.timeout_ns = d.timeout_ns;
     const int o = add ? kB128Add : out == FP8G_OUT_F32 ? kB128F32 : kB128Bf16;
     const uint32_t ta = host_mma_type(a_fmt), tb = host_mma_type(b_fmt);
-    const int64_t npm = (M + 2 * kBlk - 1) / (2 * kBlk), npn = (N + 2 * kBlk - 1) / (2 * kBlk);
-    if (npm * npn >= kMaxDim) return FP8G_ERR_UNSUPPORTED_SHAPE;
     const Plan pl = tn ? Plan{false, kBlk, 1} : plan(M, p.n_blocks, npm * npn, p.num_kb, false, d.num_sms);
     CUtensorMap mA, mB;
     st = tn ? map2(A, M, K, kBlk, d.dev, mA) : map2(A, K, M, pl.nt, d.dev, mA);
@@ -190,6 +190,8 @@ fp8g_status fp8_gated_block128(const void *x, const float *sfx, int32_t x_fmt, c
     if (M > 0 && (x == nullptr || sfx == nullptr || W13 == nullptr || sf13 == nullptr || h == nullptr || sh == nullptr))
         return FP8G_ERR_INVALID_ARG;
     if (F % kBlk != 0 || M >= kMaxDim || 2 * F >= kMaxDim || K >= kMaxDim) return FP8G_ERR_UNSUPPORTED_SHAPE;
+    const int64_t npm = (M + 2 * kBlk - 1) / (2 * kBlk);
+    if (npm * (F / kBlk) >= kMaxDim) return FP8G_ERR_UNSUPPORTED_SHAPE;
     if (K % 16 != 0 || !is_aligned(x, 16) || !is_aligned(W13, 16) || !is_aligned(h, 16) || !is_aligned(gu, 16) ||
         !is_aligned(sfx, 16) || !is_aligned(sf13, 16) || !is_aligned(sh, 16) || !is_aligned(sgu, 16))
         return FP8G_ERR_ALIGNMENT;
@@ -214,8 +216,6 @@ fp8g_status fp8_gated_block128(const void *x, const float *sfx, int32_t x_fmt, c
     p.status = d.status;
     p.timeout_ns = d.timeout_ns;
     const uint32_t tx = host_mma_type(x_fmt), tw = host_mma_type(w_fmt);
-    const int64_t npm = (M + 2 * kBlk - 1) / (2 * kBlk);
-    if (npm * p.n_blocks >= kMaxDim) return FP8G_ERR_UNSUPPORTED_SHAPE;
     const Plan pl = plan(M, p.n_blocks, npm * p.n_blocks, p.num_kb, true, d.num_sms);
     CUtensorMap mX, mW;
     st = map2(x, K, M, pl.nt, d.dev, mX);

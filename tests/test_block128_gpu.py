@@ -369,3 +369,88 @@ def test_backward_rows_behind_stay(fp8g):
     fp8g.fp8g_gated_block128_backward(dh, fp8g.FP8G_IN_F32, gu.cuda(), sgu.cuda(), 0, 0, M, F, a, s[0], b, s[1], c, s[2])
     settled(fp8g)
     assert all((t[M:] == 0x55).all() for t in (a, b, c))
+
+
+# --------------------------------------- more tiles than the kernels' grids: several a CTA
+
+@pytest.mark.parametrize("form,M,N,K", [("nt", 2100, 2600, 144), ("nn", 2100, 2592, 400), ("tn", 2064, 2832, 260),
+                                        ("nt", 130, 5000, 1040), ("tn", 4096, 4096, 128)])
+@pytest.mark.parametrize("out", ["bf16", "add"])
+def test_many_tiles(fp8g, form, M, N, K, out):
+    r = torch.Generator(device="cuda").manual_seed(19)
+
+    def coded(R, C, kind, x):
+        if kind == "tile":
+            return fp8g.quantize_tile128(x)
+        return fp8g.quantize_block128(x, row=kind == "row", col=kind == "col")[kind == "col"]
+    rand = lambda *s: torch.randn(s, device="cuda", generator=r)
+    if form == "tn":
+        A, B, ka, kb = coded(K, M, "col", rand(K, M)), coded(K, N, "col", rand(K, N)), "col", "col"
+    else:
+        b = rand(N, K) if form == "nt" else rand(K, N)
+        A, B, ka, kb = coded(M, K, "row", rand(M, K)), coded(*b.shape, "tile", b), "row", "tile"
+    C = rand(M, N) if out == "add" else None
+    start = C.clone() if out == "add" else None
+    got = fp8g.gemm_block128(*A, *B, form=form, add_to=C)
+    settled(fp8g)
+    want, mags = ref.product(ref.decode(*A, ka, E4M3), ref.decode(*B, kb, E4M3), form)
+    tol = ref.sum_tol(K) * mags
+    if out == "add":
+        want = want + start.double()
+        tol = tol + 2.0 ** -24 * want.abs()
+    else:
+        tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs()
+    assert ((got.double() - want).abs() <= tol).all()
+    again = fp8g.gemm_block128(*A, *B, form=form, add_to=start)
+    assert torch.equal(again, got)
+
+
+def test_many_tiles_gated_and_back(fp8g):
+    M, F, K = 1500, 2048, 272
+    r = torch.Generator(device="cuda").manual_seed(20)
+    x, _ = fp8g.quantize_block128(torch.randn((M, K), device="cuda", generator=r))
+    W = fp8g.quantize_tile128(torch.randn((2 * F, K), device="cuda", generator=r) * K ** -0.5)
+    h, gu = fp8g.gated_block128(*x, *W, keep=True)
+    settled(fp8g)
+    both, mags = ref.product(ref.decode(*x, "row", E4M3), ref.decode(*W, "tile", E4M3), "nt")
+    err = ref.sum_tol(K) * mags
+    g, u = both[:, :F], both[:, F:]
+    y, _ = ref.act(g, 0)
+    ref.assert_coded(*gu, "row", E4M3, both, err)
+    eh = (1.13 * err[:, :F] + 2.0 ** -20 * (2 + g.abs()) * g.abs()) * (u.abs() + err[:, F:]) + y.abs() * err[:, F:] \
+        + 2.0 ** -23 * (y * u).abs()
+    ref.assert_coded(*h, "row", E4M3, y * u, eh)
+    dh = torch.randn((M, F), device="cuda", generator=r).bfloat16()
+    row, col, hc = fp8g.gated_block128_backward(dh, *gu)
+    both = ref.decode(*gu, "row", E4M3)
+    g, u, xx = both[:, :F], both[:, F:], dh.double()
+    y, d = ref.act(g, 0)
+    e = 2.0 ** -19 * (2 + g.abs())
+    want = torch.cat((xx * u * d, xx * y), 1)
+    err = torch.cat((xx.abs() * u.abs() * e, xx.abs() * (g.abs() * e)), 1)
+    ref.assert_coded(*row, "row", E4M3, want, err)
+    ref.assert_coded(*col, "col", E4M3, want, err)
+    ref.assert_coded(*hc, "col", E4M3, y * u, g.abs() * u.abs() * e)
+
+
+def test_quantise_bits_many_tiles(fp8g):
+    x = ref.values(2500, 1200, gen(21))
+    row, col = fp8g.quantize_block128(x.bfloat16().cuda(), row=True, col=True)
+    same(row, ref.quant(x.bfloat16(), "row", E4M3))
+    same(col, ref.quant(x.bfloat16(), "col", E4M3))
+    same(fp8g.quantize_block128(x.cuda())[0], ref.quant(x, "row", E4M3))
+
+
+@pytest.mark.parametrize("arg", ["A", "sfa", "B", "sfb", "add_to"])
+def test_the_product_refuses_what_does_not_fit(fp8g, arg):
+    u = lambda *s: torch.zeros(s, dtype=torch.uint8, device="cuda")
+    f = lambda *s: torch.ones(s, device="cuda")
+    good = dict(A=u(32, 256), sfa=f(2, 32), B=u(64, 256), sfb=f(1, 2), add_to=f(32, 64))
+    fp8g.gemm_block128(**good)
+    bad = {"A": [u(32, 240), u(256, 32).t(), torch.zeros((32, 256), device="cuda"), u(32, 256).cpu()],
+           "sfa": [f(32, 2), f(2, 32).double(), f(4, 32)[::2]], "B": [u(64, 128), u(256, 64).t()],
+           "sfb": [f(2, 1), f(1, 2).bfloat16()], "add_to": [f(64, 32), f(32, 64).bfloat16(), f(64, 32).t()]}[arg]
+    for t in bad:
+        with pytest.raises((AssertionError, fp8g.Fp8gError)):
+            fp8g.gemm_block128(**dict(good, **{arg: t}))
+    settled(fp8g)
