@@ -13,10 +13,11 @@ OBJ_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(HERE, "libfp8g.so")
 SOURCES = ["gemm.cu", "gemm_pair.cu", "gemm_promote.cu", "scales.cu", "quant.cu", "api.cu",
            "noalloc.cu", "selftest.cu", "route.cu", "stream.cu", "moe.cu", "lora.cu",
-           "block128.cu", "block128_quant.cu", "block128_gemm.cu", "block128_few.cu"]
+           "block128.cu", "block128_quant.cu", "block128_gemm.cu",
+           "block128_share.cu", "block128_few.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "kernel_common.cuh", "quant_math.cuh", "stream.h", "lora_value.cuh",
            "lora_pieces.cuh", "block128.h", "block128_math.cuh",
-           "block128_wait.cuh"]
+           "block128_wait.cuh", "block128_pair.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

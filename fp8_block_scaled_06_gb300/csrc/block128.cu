@@ -13,6 +13,30 @@ int64_t blocks(int64_t n) { return (n + kBlk - 1) / kBlk; }
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
 constexpr int64_t kMaxQuantRows = (int64_t)65535 * 16;  // 16 rows at least a block: a grid's second axis
 
+// How T tiles of num_kb K blocks go to `most` CTA pairs: rounds of whole tiles and, where
+// the last would leave pairs idle, its K blocks in shares, a tile's to four pairs at
+// most (the one with its end adds the others' sums, 256 KB each).  Shares cost the time
+// of about 50 K blocks (writing and adding sums, zeroing flags, the gap between kernels;
+// 4096 x 4096 x 4096, where they save 20, took 76 us in place of 64): taken where they
+// save 60.
+struct Deal {
+    int32_t pairs, full, share;
+    int64_t units;  // K blocks one after the other
+};
+Deal deal(int64_t T, int num_kb, int most, bool can_share) {
+    Deal d{(int32_t)(T < most ? T : most), 0, 0, (T + most - 1) / most * num_kb};
+    const int64_t full = T / most, rest = T - full * most;
+    if (rest == 0 || !can_share) return d;
+    int64_t share = (rest * num_kb + most - 1) / most;
+    if (share < (num_kb + 3) / 4) share = (num_kb + 3) / 4;
+    if (num_kb - share < 60) return d;
+    d.full = (int32_t)full;
+    d.share = (int32_t)share;
+    d.pairs = (int32_t)(full > 0 ? most : (rest * num_kb + share - 1) / share);
+    d.units = full * num_kb + share + 50;
+    return d;
+}
+
 // Which kernel, and its shape.
 struct Plan {
     bool few;
@@ -20,17 +44,16 @@ struct Plan {
 };
 
 // The kernel for few rows against the one on CTA pairs, by estimates of their time.
-// A round of pairs takes 76 hundredths of a 10^4-cycle unit a K block (every tile 256 x
+// Pairs take 76 hundredths of a 10^4-cycle unit a K block (every tile 256 x
 // 256, however few of its rows exist), the call eight more at its ends.  Few rows: a
 // tile of 128 weight rows; a round begins and ends with the time of five K blocks
 // (first loads, joining), each further CTA of a tile joins about one more; a K block
 // takes 110 where a CTA has its SM alone, 130 where two share it (loads bound both).
-// Measured, us, few rows / pairs: 64 x 14336 x 4096 14.5 / 19.5, 77 of them 24 / 19.5,
-// 77 x 4096 x 14336 21 / 54, 256 of them 34 / 46; gated, 64 rows of F 14336, K 4096 27 /
-// 40, 128 rows 48 / 40.
-Plan plan(int64_t M, int64_t n_blocks, int64_t pair_tiles, int num_kb, bool gated, int num_sms) {
-    const int64_t rounds = (pair_tiles + num_sms / 2 - 1) / (num_sms / 2);
-    int64_t least = (rounds * num_kb + 8) * 76;
+// Measured, us, few rows / pairs in whole tiles: 64 x 14336 x 4096 14.5 / 19.5, 77 of
+// them 24 / 19.5, 77 x 4096 x 14336 21 / 54, 256 of them 34 / 46; gated, 64 rows of F
+// 14336, K 4096 27 / 40, 128 rows 48 / 40.
+Plan plan(int64_t M, int64_t n_blocks, const Deal &d, int num_kb, bool gated, int num_sms) {
+    int64_t least = (d.units + 8) * 76;
     Plan best{false, kBlk, 1};
     const int most = gated ? 64 : 128;
     int nt = 16;
@@ -46,6 +69,27 @@ Plan plan(int64_t M, int64_t n_blocks, int64_t pair_tiles, int num_kb, bool gate
         }
     }
     return best;
+}
+
+// The kernel on CTA pairs, with a temporary for sums where tiles are shared.
+fp8g_status run_pairs(const CUtensorMap &A, const CUtensorMap &B, B128Params &p, const Deal &dl, int out, bool vec_b,
+                      int dev, cudaStream_t stream) {
+    p.pairs = dl.pairs;
+    p.full = dl.full;
+    p.share = dl.share;
+    if (dl.share == 0) return launch_b128_pair(A, B, p, out, vec_b, stream) == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+    cudaMemPool_t pool;
+    const fp8g_status st = host_pool(dev, pool);
+    if (st != FP8G_OK) return st;
+    void *ws = nullptr;
+    const size_t sums = (size_t)dl.pairs * kB128PartBytes, flags = (size_t)dl.pairs * kB128ThereBytes;
+    if (cudaMallocFromPoolAsync(&ws, sums + flags, pool, stream) != cudaSuccess) return FP8G_ERR_CUDA;
+    p.part = static_cast<float *>(ws);
+    p.there = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + sums);
+    cudaError_t e = cudaMemsetAsync(p.there, 0, flags, stream);
+    if (e == cudaSuccess) e = launch_b128_share(A, B, p, out, vec_b, stream);
+    const cudaError_t ef = cudaFreeAsync(ws, stream);
+    return e == cudaSuccess && ef == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
 }
 
 fp8g_status map2(const void *ptr, int64_t inner, int64_t outer, int rows, int dev, CUtensorMap &m) {
@@ -129,7 +173,7 @@ fp8g_status fp8_gemm_block128(int32_t form, const void *A, const float *sfa, int
         return FP8G_ERR_INVALID_ARG;
     if (M >= kMaxDim || N >= kMaxDim || K >= kMaxDim) return FP8G_ERR_UNSUPPORTED_SHAPE;
     const int64_t npm = (M + 2 * kBlk - 1) / (2 * kBlk), npn = (N + 2 * kBlk - 1) / (2 * kBlk);
-    if (npm * npn >= kMaxDim) return FP8G_ERR_UNSUPPORTED_SHAPE;
+    if (npm * npn >= kMaxDim / 2) return FP8G_ERR_UNSUPPORTED_SHAPE;
     const int64_t esz = out == FP8G_OUT_F32 ? 4 : 2;
     if ((!tn && K % 16 != 0) || (tn && M % 16 != 0) || (form != FP8G_NT && N % 16 != 0) || N * esz % 16 != 0)
         return FP8G_ERR_ALIGNMENT;
@@ -160,24 +204,23 @@ fp8g_status fp8_gemm_block128(int32_t form, const void *A, const float *sfa, int
     p.timeout_ns = d.timeout_ns;
     const int o = add ? kB128Add : out == FP8G_OUT_F32 ? kB128F32 : kB128Bf16;
     const uint32_t ta = host_mma_type(a_fmt), tb = host_mma_type(b_fmt);
-    const Plan pl = tn ? Plan{false, kBlk, 1} : plan(M, p.n_blocks, npm * npn, p.num_kb, false, d.num_sms);
+    const Deal dl = deal(npm * npn, p.num_kb, d.num_sms / 2, true);
+    const Plan pl = tn ? Plan{false, kBlk, 1} : plan(M, p.n_blocks, dl, p.num_kb, false, d.num_sms);
     CUtensorMap mA, mB;
     st = tn ? map2(A, M, K, kBlk, d.dev, mA) : map2(A, K, M, pl.nt, d.dev, mA);
     if (st == FP8G_OK)
         st = p.b_mn ? map2(B, N, K, kBlk, d.dev, mB) : map2(B, K, N, kBlk, d.dev, mB);
     if (st != FP8G_OK) return st;
-    cudaError_t e;
     if (pl.few) {
         p.types = (tb << 7) | (ta << 10) | ((uint32_t)p.b_mn << 15);
-        e = launch_b128_few(mA, mB, p, o, pl.nt, pl.split, stream);
+        return launch_b128_few(mA, mB, p, o, pl.nt, pl.split, stream) == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
     } else {
         p.types = (ta << 7) | (tb << 10) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16);
         p.npm = (int32_t)npm;
         p.npn = (int32_t)npn;
         p.T = (int32_t)(npm * npn);
-        e = launch_b128_pair(mA, mB, p, o, tn, d.num_sms, stream);
+        return run_pairs(mA, mB, p, dl, o, tn, d.dev, stream);
     }
-    return e == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
 }
 
 fp8g_status fp8_gated_block128(const void *x, const float *sfx, int32_t x_fmt, const void *W13, const float *sf13,
@@ -191,7 +234,7 @@ fp8g_status fp8_gated_block128(const void *x, const float *sfx, int32_t x_fmt, c
         return FP8G_ERR_INVALID_ARG;
     if (F % kBlk != 0 || M >= kMaxDim || 2 * F >= kMaxDim || K >= kMaxDim) return FP8G_ERR_UNSUPPORTED_SHAPE;
     const int64_t npm = (M + 2 * kBlk - 1) / (2 * kBlk);
-    if (npm * (F / kBlk) >= kMaxDim) return FP8G_ERR_UNSUPPORTED_SHAPE;
+    if (npm * (F / kBlk) >= kMaxDim / 2) return FP8G_ERR_UNSUPPORTED_SHAPE;
     if (K % 16 != 0 || !is_aligned(x, 16) || !is_aligned(W13, 16) || !is_aligned(h, 16) || !is_aligned(gu, 16) ||
         !is_aligned(sfx, 16) || !is_aligned(sf13, 16) || !is_aligned(sh, 16) || !is_aligned(sgu, 16))
         return FP8G_ERR_ALIGNMENT;
@@ -216,7 +259,8 @@ fp8g_status fp8_gated_block128(const void *x, const float *sfx, int32_t x_fmt, c
     p.status = d.status;
     p.timeout_ns = d.timeout_ns;
     const uint32_t tx = host_mma_type(x_fmt), tw = host_mma_type(w_fmt);
-    const Plan pl = plan(M, p.n_blocks, npm * p.n_blocks, p.num_kb, true, d.num_sms);
+    const Deal dl = deal(npm * p.n_blocks, p.num_kb, d.num_sms / 2, false);
+    const Plan pl = plan(M, p.n_blocks, dl, p.num_kb, true, d.num_sms);
     CUtensorMap mX, mW;
     st = map2(x, K, M, pl.nt, d.dev, mX);
     if (st == FP8G_OK) {
@@ -225,18 +269,17 @@ fp8g_status fp8_gated_block128(const void *x, const float *sfx, int32_t x_fmt, c
         st = host_operand_map(W13, FP8G_E4M3, 3, dw, bw, d.dev, mW);
     }
     if (st != FP8G_OK) return st;
-    cudaError_t e;
     if (pl.few) {
         p.types = (tw << 7) | (tx << 10);
-        e = launch_b128_few(mX, mW, p, kB128Gated + gate, pl.nt, pl.split, stream);
+        return launch_b128_few(mX, mW, p, kB128Gated + gate, pl.nt, pl.split, stream) == cudaSuccess ? FP8G_OK
+                                                                                                    : FP8G_ERR_CUDA;
     } else {
         p.types = (tx << 7) | (tw << 10);
         p.npm = (int32_t)npm;
         p.npn = p.n_blocks;
         p.T = p.npm * p.npn;
-        e = launch_b128_pair(mX, mW, p, kB128Gated + gate, false, d.num_sms, stream);
+        return run_pairs(mX, mW, p, dl, kB128Gated + gate, false, d.dev, stream);
     }
-    return e == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
 }
 
 fp8g_status fp8g_gated_block128_backward(const void *dh, int32_t dh_dtype, const uint8_t *gu, const float *sgu,

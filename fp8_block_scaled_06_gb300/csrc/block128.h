@@ -18,6 +18,12 @@ struct B128Params {
     int32_t num_kb;         // ceil(K / 128)
     int32_t npm, npn;       // tiles of C
     int32_t T;              // npm npn
+    // CTA pairs: pair c takes tiles c, c + pairs, .. of the first `full` rounds; the K blocks
+    // of the tiles behind them are dealt out in shares of `share` (0: whole tiles, as a
+    // last round)
+    int32_t pairs, full, share;
+    float *part;            // [pairs][256 x 256] sums of a share that ends inside its tile
+    int32_t *there;         // [pairs][16] by warp: part is written (zeros at the start)
     const float *sa;        // [num_kb][M]
     const float *sb;        // vectors [num_kb][N]; tiles: block (n, k) at n sb_n + k sb_k
     int64_t sb_n, sb_k;
@@ -36,10 +42,13 @@ struct B128Params {
 // What a product kernel ends in (kB128Gated + FP8G_GATE_*: h = act(g) u in 8 bits).
 enum B128Out : int { kB128Bf16 = 0, kB128F32 = 1, kB128Add = 2, kB128Gated = 3 };
 
-// block128_gemm.cu: CTA pairs over 256 x 256 tiles (gated: 256 rows, 128 columns
+// block128_gemm.cu, block128_share.cu (p.share > 0; no gated outputs): CTA pairs over 256 x 256 tiles (gated: 256 rows, 128 columns
 // of gate and of up).  vec_b: B's scales are vectors.
 cudaError_t launch_b128_pair(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p,
-                             int out, bool vec_b, int num_sms, cudaStream_t stream);
+                             int out, bool vec_b, cudaStream_t stream);
+cudaError_t launch_b128_share(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p,
+                              int out, bool vec_b, cudaStream_t stream);
+constexpr int64_t kB128PartBytes = (int64_t)4 * kBlk * kBlk * 4, kB128ThereBytes = 16 * 4;  // of a pair
 
 // block128_few.cu: few rows of C.  The weights (B) are the MMA's 128-row operand,
 // nt rows of A its columns; K split over clusters of `split` CTAs.

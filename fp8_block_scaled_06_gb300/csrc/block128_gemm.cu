@@ -1,549 +1,19 @@
-// Products with fp32 scales for blocks of 128 on CTA pairs, sm_103a:
-//
-//   C[i, j] = sum_kb sa[kb][i] sb(kb, j) P_kb[i, j],  P_kb = sum_{k in kb} a_ik b_kj
-//
-// and the gated projection pair that ends in 8 bits,
-//   g = x Wg^T, u = x Wu^T, h = act(g) u  ->  codes and scales of h (and of g, u).
-//
-// The tensor core takes no fp32 scales, so each K block's unscaled product P_kb
-// goes to one of two 256-column tensor-memory buffers (kind::f8f6f4, the first of
-// its four MMAs overwrites) and eight promotion warps per CTA add it, scaled, to
-// fp32 registers while the MMAs of the next K block fill the other buffer.  One K
-// block of a pair's 256 x 256 tile takes the tensor cores 512 cycles; a promotion
-// warp's 32 x 128 share is 4 tensor-memory loads of 32 columns and 64 packed FMAs
-// where one scale serves its 128 columns (128 x 128 tiles of B), with the FMA pipe
-// half busy.  With a scale per column (weight gradients) each pair of values costs
-// a multiplication too, and the pipe is as busy as the tensor core.
-//
-// Operands lie either way.  Contraction contiguous: 128 B rows of the 128-byte
-// swizzle, an MMA's 32 values 32 B apart.  M (N) contiguous: the tile's 128 rows are
-// the K values, an MMA's 32 of them 4 KB apart, and the instruction descriptor's
-// major bit is set.  In both the eight-row swizzle atoms follow each other (1 KB),
-// so the weights serve the forward product and the input gradient as they lie, and
-// activations the forward product and the weight gradient.
-//
-// Roles (384 threads): warp 0 TMA producer (both CTAs, their own halves), warp 1 of
-// the even CTA MMA issue, warps 4-11 promotion and epilogue: lane quarter warp & 3,
-// half of the columns.  They
-// hold 128 accumulators a thread, so registers move to them (setmaxnreg: 256 x 232
-// + 128 x 40 = 384 x 168).  Scales are read up to three K blocks ahead, straight to
-// registers; column vectors then pass through shared memory of the warp's own, to be
-// read as broadcasts.  A warp's arrival that frees a buffer is relaxed: with release
-// semantics it waited for the scale loads in flight too (2500 instead of  cycles a K
-// block).  Every wait is bounded.
-#include <cuda_bf16.h>
-
-#include "block128.h"
-#include "block128_math.cuh"
-#include "block128_wait.cuh"
-#include "ptx.cuh"
+// The product on CTA pairs in whole tiles (block128_pair.cuh).
+#include "block128_pair.cuh"
 
 namespace fp8g {
 
-namespace {
-
-constexpr int kThreads = 384;
-constexpr int kProm0 = 4;              // first promotion warp
-constexpr int kPromWarps = 8;
-constexpr int kRegsLaunch = 168, kRegsProm = 232, kRegsRest = 40;
-static_assert(32 * kPromWarps * kRegsProm + 128 * kRegsRest <= kThreads * kRegsLaunch,
-              "setmaxnreg draws on the block's own registers");
-constexpr int kTile = kBlk * kBlk;     // bytes of an operand tile of one CTA
-constexpr int kBufs = 2;               // product buffers of 256 columns
-
-template <bool VECB>
-struct Lay {
-    static constexpr int STAGES = VECB ? 5 : 6;
-    static constexpr int OFF_B = STAGES * kTile;
-    // a promotion warp's scales of CH K blocks: A's [CH][32 lanes], then B's [CH][128
-    // columns] or [CH][two tiles]; two such buffers a warp
-    static constexpr int CH = VECB ? 4 : 8;
-    static constexpr int SCALES = CH * (32 + (VECB ? kBlk : 2));
-    static constexpr int OFF_S = 2 * STAGES * kTile;
-    static constexpr int OFF_X = OFF_S + kPromWarps * 2 * SCALES * 4;  // row maxima: [2][2][128] float4
-    static constexpr int OFF_BAR = OFF_X + (VECB ? 0 : 2 * 2 * kBlk * 16);
-    // full, empty [STAGES]; product full, product empty [kBufs]; row maxima [lane
-    // quarter][half]; drain
-    static constexpr int NUM_BARS = 2 * STAGES + 2 * kBufs + 8 + 1;
-    static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
-    static constexpr int BYTES = OFF_MISC + 16 + 1024;
-    static_assert(BYTES <= 232448, "shared memory over the per-CTA limit");
-};
-
-// The scales of a promotion warp, copied (cp.async) to shared memory of its own, CH K
-// blocks at a time and one such chunk ahead: waiting for a copy and asking for the next
-// cost a K block 230 cycles where each had its own.  (In registers, handed on from one
-// K block to the next, each handing on waited for the newest load.)
-template <bool VECB, int OUT>
-struct ScaleChunks {
-    using L = Lay<VECB>;
-    float *buf;          // [2][SCALES]
-    const float *a, *b;  // this lane's row of A; columns of B, or one of its two tiles
-    __device__ __forceinline__ void tile(const B128Params &p, int64_t row, int pn, int half) {
-        const int lane = threadIdx.x & 31;
-        a = p.sa + min(row, p.M - 1);
-        if constexpr (VECB) {  // four columns a lane (N is a multiple of 16)
-            b = p.sb + min((int64_t)pn * 2 * kBlk + half * 64 + 4 * lane + (lane >= 16 ? 64 : 0), p.N - 4);
-        } else {
-            const int64_t n0 = OUT >= kB128Gated ? pn : 2 * pn;
-            const int64_t n1 = OUT >= kB128Gated ? n0 + p.n_blocks : min(n0 + 1, (int64_t)p.n_blocks - 1);
-            b = p.sb + ((lane & 1) == 0 ? n0 : n1) * p.sb_n;
-        }
-    }
-    // K blocks kb .. kb + CH - 1 of the tile to buffer i
-    __device__ __forceinline__ void ask(const B128Params &p, int kb, uint32_t i) const {
-        const int lane = threadIdx.x & 31;
-        const uint32_t at = ptx::smem_addr(buf + (i & 1u) * L::SCALES);
-#pragma unroll
-        for (int j = 0; j < L::CH; ++j)
-            if (kb + j < p.num_kb) {
-                ptx::cp_async_4(at + (j * 32 + lane) * 4, a + (kb + j) * p.M, 4);
-                if constexpr (VECB)
-                    ptx::cp_async_16(at + (L::CH * 32 + j * kBlk + 4 * lane) * 4, b + (kb + j) * p.N, 16);
-            }
-        if constexpr (!VECB) {
-            if (lane < 2 * L::CH && kb + (lane >> 1) < p.num_kb)
-                ptx::cp_async_4(at + (L::CH * 32 + lane) * 4, b + (kb + (lane >> 1)) * p.sb_k, 4);
-        }
-        ptx::cp_async_commit();
-    }
-};
-
-// 64 codes of one row from 64 values times r, in 32-byte stores (wide; each a whole
-// sector) or 16-byte ones.
-__device__ __forceinline__ void store_codes64(uint8_t *dst, const float (&v)[64], float r, bool wide) {
-    uint32_t o[16];
-#pragma unroll
-    for (int w = 0; w < 16; ++w)
-        o[w] = b128_codes<FP8G_E4M3>(v[4 * w], v[4 * w + 1], v[4 * w + 2], v[4 * w + 3], r);
-    if (wide) {
-        ptx::st_global_v8(dst, o);
-        ptx::st_global_v8(dst + 32, o + 8);
-    } else {
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-            reinterpret_cast<uint4 *>(dst)[w] = make_uint4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
-    }
-}
-
-__device__ __forceinline__ float amax64(const float (&v)[64]) {
-    float m[2] = {};
-#pragma unroll
-    for (int i = 0; i < 64; i += 2) m[(i >> 1) & 1] = b128_max3(m[(i >> 1) & 1], v[i], v[i + 1]);
-    return fmaxf(m[0], m[1]);
-}
-
-template <bool VECB, int OUT>
-__global__ void __launch_bounds__(kThreads, 1)
-    b128_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                     const B128Params p) {
-    using L = Lay<VECB>;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw_base = ptx::smem_addr(smem_raw);
-    uint8_t *smem = smem_raw + ((1024u - (raw_base & 1023u)) & 1023u);
-    const uint32_t sbase = ptx::smem_addr(smem);
-    const int warp = threadIdx.x >> 5;
-    const int lane = threadIdx.x & 31;
-    const uint32_t rank = ptx::cluster_rank();
-    const bool leader = rank == 0;
-
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
-    auto bar_full = [&](int s) { return ptx::smem_addr(&bars[s]); };
-    auto bar_empty = [&](int s) { return ptx::smem_addr(&bars[L::STAGES + s]); };
-    auto bar_pfull = [&](int b) { return ptx::smem_addr(&bars[2 * L::STAGES + b]); };
-    auto bar_pempty = [&](int b) { return ptx::smem_addr(&bars[2 * L::STAGES + kBufs + b]); };
-    auto bar_max = [&](int q, int h) { return ptx::smem_addr(&bars[2 * L::STAGES + 2 * kBufs + 2 * q + h]); };
-    const uint32_t bar_drain = ptx::smem_addr(&bars[L::NUM_BARS - 1]);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
-
-    // ------------------------------------------------------------ setup
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < L::STAGES; ++s) {
-            ptx::mbar_init(bar_full(s), 1);
-            ptx::mbar_init(bar_empty(s), 1);
-        }
-        for (int b = 0; b < kBufs; ++b) {
-            ptx::mbar_init(bar_pfull(b), 1);
-            ptx::mbar_init(bar_pempty(b), 2 * kPromWarps);
-        }
-        for (int i = 0; i < 8; ++i) ptx::mbar_init(bar_max(i >> 1, i & 1), 1);
-        ptx::mbar_init(bar_drain, 1);
-        *abort_flag = 0;
-        ptx::fence_mbar_init();
-    }
-    if (warp == 0 && lane == 0) {
-        ptx::prefetch_tmap(&tmA);
-        ptx::prefetch_tmap(&tmB);
-    }
-    if (warp == 1) {
-        ptx::tmem_alloc_pair(ptx::smem_addr(tmem_slot), 512);
-        ptx::tmem_relinquish_pair();
-    }
-    ptx::tc_fence_before();
-    __syncthreads();
-    ptx::cluster_sync();  // both CTAs' barriers and tensor memory exist
-    ptx::tc_fence_after();
-    const uint32_t tmem_base = *tmem_slot;
-    if (tmem_base != 0u && threadIdx.x == 0) {  // all 512 columns: they begin at 0 in both CTAs
-        record_error(p, FP8G_ERR_DEVICE, 0xA11Cu);
-        *abort_flag = 1;
-    }
-    ptx::grid_dep_wait();  // global memory only after the previous kernel
-    ptx::grid_dep_launch();
-    __syncthreads();
-    const int32_t t_first = *abort_flag ? p.T : (int32_t)ptx::cluster_id_x();
-    const int32_t t_step = (int32_t)ptx::num_clusters_x();
-
-    // (each in its own branch: the compiler allots a branch's registers by it)
-    if (warp < kProm0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-        if (warp == 0) {
-            // ===== TMA producer: both CTAs' copies complete on the even CTA's barrier =====
-            if (lane == 0) {
-                uint32_t stage = 0, phase = 0;
-                for (int32_t t = t_first; t < p.T; t += t_step) {
-                    int32_t pm, pn;
-                    raster(t, p.npm, p.npn, kRasterG, pm, pn);
-                    const int32_t m0 = (2 * pm + (int32_t)rank) * kBlk, n0 = (2 * pn + (int32_t)rank) * kBlk;
-                    for (int kb = 0; kb < p.num_kb; ++kb) {
-                        if (!wait_bar(bar_empty(stage), phase ^ 1u, abort_flag, p, 0 * 256 + stage)) goto roles_done;
-                        const uint32_t fb = leader ? bar_full(stage) : ptx::map_shared(bar_full(stage), 0);
-                        if (leader) ptx::mbar_arrive_expect_tx(fb, 4 * kTile);
-                        const int32_t k0 = kb * kBlk;
-                        ptx::tma_load_2d_pair(sbase + stage * kTile, &tmA, fb, p.a_mn ? m0 : k0, p.a_mn ? k0 : m0);
-                        if constexpr (OUT >= kB128Gated)  // gate rows to the even CTA, up rows to the odd one
-                            ptx::tma_load_3d_pair(sbase + L::OFF_B + stage * kTile, &tmB, fb, k0, pn * kBlk, (int32_t)rank);
-                        else
-                            ptx::tma_load_2d_pair(sbase + L::OFF_B + stage * kTile, &tmB, fb, p.b_mn ? n0 : k0,
-                                                  p.b_mn ? k0 : n0);
-                        if (++stage == L::STAGES) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
-                    }
-                }
-            }
-        } else if (warp == 1 && leader) {
-            // ===== MMA issue (even CTA): 256 x 256 x 32 per instruction =====
-            // The whole warp runs the loop and one elected lane issues: from a branch of one
-            // lane's own the four MMAs took 500 cycles to issue, in the chain from a buffer's
-            // release to its next product.
-            const uint32_t idesc = ptx::idesc_f8(2 * kBlk, 2 * kBlk) | p.types;
-            const uint32_t a_step = (p.a_mn ? 32 * kBlk : 32) >> 4, b_step = (p.b_mn ? 32 * kBlk : 32) >> 4;
-            const uint64_t a_desc = ptx::smem_desc(sbase, 1024, 1024, 2);
-            const uint64_t b_desc = ptx::smem_desc(sbase + L::OFF_B, 1024, 1024, 2);
-            uint32_t stage = 0, phase = 0, g = 0;
-            for (int32_t t = t_first; t < p.T; t += t_step) {
-                for (int kb = 0; kb < p.num_kb; ++kb, ++g) {
-                    const uint32_t buf = g & 1u;
-                    if (!b128_wait_all(bar_full(stage), phase, abort_flag, p, 1 * 256 + stage)) goto roles_done;
-                    if (!b128_wait_all(bar_pempty(buf), ((g >> 1) & 1u) ^ 1u, abort_flag, p, 1 * 256 + 64 + buf))
-                        goto roles_done;
-                    ptx::tc_fence_after();
-                    const uint64_t a0 = a_desc + stage * (kTile >> 4), b0 = b_desc + stage * (kTile >> 4);
-                    if (ptx::elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            ptx::mma_f8_pair(buf * 2 * kBlk, a0 + k * a_step, b0 + k * b_step, idesc, k != 0 ? 1u : 0u);
-                        ptx::tc_commit_pair_mc(bar_pfull(buf), 0x3);
-                        ptx::tc_commit_pair_mc(bar_empty(stage), 0x3);
-                    }
-                    __syncwarp();
-                    if (++stage == L::STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
-            }
-        }
-    } else {
-        // ===== promotion and epilogue: this CTA's 128 rows =====
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsProm));
-        const int q = warp & 3, half = (warp - kProm0) >> 2;
-        // tensor-memory column of this warp's chunk c: 64 columns of the tile's first
-        // block of B (gated: of gate) and the same 64 of its second (of up)
-        const uint32_t lane_base = ((uint32_t)(q * 32) << 16) + half * 64;
-        // scale vectors: the chunk is 16 rows of 64 columns, in fragments of 8 columns of which
-        // a lane holds two of two rows, so that it reads a quarter of the columns' scales (a
-        // whole row a lane, shared memory took 1024 cycles a K block to hand them out)
-        auto chunk = [&](uint32_t i, int c) {
-            const uint32_t at = lane_base + (i & 1u) * 2 * kBlk + (c >> 1) * kBlk;
-            return VECB ? at + ((c & 1) << 20) : at + (c & 1) * 32;
-        };
-        auto load = [&](uint32_t i, int c, uint32_t(&r)[32]) {
-            if constexpr (VECB)
-                ptx::tmem_ld_16x256b_x8(chunk(i, c), r);
-            else
-                ptx::tmem_ld_32x32b_x32(chunk(i, c), r);
-        };
-        const uint32_t free0 = ptx::map_shared(bar_pempty(0), 0), free1 = ptx::map_shared(bar_pempty(1), 0);
-        const int row_in = (int)rank * kBlk + q * 32 + lane;
-        uint32_t g = 0, lt = 0;
-        int32_t pm = 0, pn = 0;
-        uint32_t chunks = 0;  // of scales, over all tiles
-        ScaleChunks<VECB, OUT> scales;
-        scales.buf = reinterpret_cast<float *>(smem + L::OFF_S) + (warp - kProm0) * 2 * L::SCALES;
-        auto begin = [&](int32_t t) {
-            raster(t, p.npm, p.npn, kRasterG, pm, pn);
-            scales.tile(p, (int64_t)pm * 2 * kBlk + row_in, pn, half);
-            scales.ask(p, 0, chunks);
-        };
-        if (t_first < p.T) begin(t_first);
-        for (int32_t t = t_first; t < p.T; t += t_step, ++lt) {
-            // VECB: pairs of columns, in packed arithmetic (issue slots, not the pipe, ran short)
-            float acc[VECB ? 1 : 4][32];
-            uint64_t acc2[VECB ? 4 : 1][16];
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    if constexpr (VECB)
-                        acc2[c][i / 2] = 0ull;
-                    else
-                        acc[c][i] = 0.0f;
-                }
-            uint32_t r0[32], r1[32];
-            bool ok = true;
-            for (int kb = 0; kb < p.num_kb; ++kb, ++g) {
-                const uint32_t buf = g & 1u;
-                if (kb % L::CH == 0) {
-                    ptx::cp_async_wait<0>();
-                    __syncwarp();  // this chunk is there for every lane, and the one before it read by all
-                    ++chunks;
-                    if (kb + L::CH < p.num_kb) scales.ask(p, kb + L::CH, chunks);
-                }
-                const float *sc = scales.buf + (~chunks & 1u) * L::SCALES;
-                const float sa = VECB ? 0.0f : sc[kb % L::CH * 32 + lane];
-                float2 sb{};
-                if constexpr (!VECB) sb = *reinterpret_cast<const float2 *>(sc + L::CH * 32 + kb % L::CH * 2);
-                // VECB: the lane's rows' and its columns' scales, the latter of one block of 64 at a
-                // time, read before what they are for arrives
-                float2 ra[2];
-                uint64_t cb[8];
-                auto columns = [&](int block) {
-                    const uint64_t *col = reinterpret_cast<const uint64_t *>(sc + L::CH * 32 + kb % L::CH * kBlk + block * 64);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) cb[j] = col[4 * j + (lane & 3)];
-                };
-                if constexpr (VECB) {
-                    const float *r = sc + kb % L::CH * 32 + (lane >> 2);
-                    ra[0] = make_float2(r[0], r[8]);
-                    ra[1] = make_float2(r[16], r[24]);
-                    columns(0);
-                }
-                auto add = [&](int c, const uint32_t(&r)[32]) {
-                    if constexpr (VECB) {
-                        const uint64_t a0 = b128_pair(ra[c & 1].x, ra[c & 1].x), a1 = b128_pair(ra[c & 1].y, ra[c & 1].y);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            b128_fma2(acc2[c][2 * j], b128_pair(r[4 * j], r[4 * j + 1]), b128_mul2(a0, cb[j]));
-                            b128_fma2(acc2[c][2 * j + 1], b128_pair(r[4 * j + 2], r[4 * j + 3]), b128_mul2(a1, cb[j]));
-                        }
-                    } else {
-                        const float f = __fmul_rn(sa, c >= 2 ? sb.y : sb.x);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) acc[c][i] = __fmaf_rn(__uint_as_float(r[i]), f, acc[c][i]);
-                    }
-                };
-                // From here to the arrival the buffer is kept from the MMAs of the K block after
-                // next: two chunks are loaded at a time (64 registers), the next two as soon as
-                // theirs are free, and everything else comes before or behind.
-                if (!b128_wait_all(bar_pfull(buf), (g >> 1) & 1u, abort_flag, p, 3 * 256 + 64 + buf)) {
-                    ok = false;
-                    break;
-                }
-                ptx::tc_fence_after();
-                load(g, 0, r0);
-                load(g, 1, r1);
-                ptx::tmem_ld_wait(r0);
-                ptx::tmem_ld_wait(r1);
-                add(0, r0);
-                load(g, 2, r0);
-                add(1, r1);
-                load(g, 3, r1);
-                if constexpr (VECB) columns(1);
-                ptx::tmem_ld_wait(r0);
-                ptx::tmem_ld_wait(r1);
-                ptx::tc_fence_before();
-                __syncwarp();
-                ptx::mbar_arrive_cluster_relaxed(buf ? free1 : free0, lane == 0);
-                add(2, r0);
-                add(3, r1);
-            }
-            if (!ok) break;
-            const int64_t row = (int64_t)pm * 2 * kBlk + row_in;
-            const int32_t tn = pn;
-            if (t + t_step < p.T) begin(t + t_step);  // the next tile's first scales
-
-            if constexpr (VECB) {
-                // eight columns of a row from four lanes: whole sectors of an fp32 C
-                const int64_t row0 = row - lane + (lane >> 2), n0 = (int64_t)tn * 2 * kBlk + half * 64 + 2 * (lane & 3);
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int64_t m = row0 + (c & 1) * 16 + (i & 1) * 8, n = n0 + (c >> 1) * kBlk + (i >> 1) * 8;
-                        if (m < p.M && n < p.N) {
-                            const float2 v = make_float2(b128_lo(acc2[c][i]), b128_hi(acc2[c][i]));
-                            if constexpr (OUT == kB128Bf16) {
-                                *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.C) + m * p.N + n) =
-                                    __floats2bfloat162_rn(v.x, v.y);
-                            } else {
-                                float2 *at = reinterpret_cast<float2 *>(static_cast<float *>(p.C) + m * p.N + n);
-                                if constexpr (OUT == kB128Add)
-                                    ptx::red_add_v2(at, v);
-                                else
-                                    *at = v;
-                            }
-                        }
-                    }
-            } else if constexpr (OUT < kB128Gated) {
-                const int64_t n0 = (int64_t)tn * 2 * kBlk + half * 64;
-                if (row < p.M) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t r[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(acc[c][i]);
-                        const int64_t n = n0 + (c >> 1) * kBlk + (c & 1) * 32;
-                        if constexpr (OUT == kB128Add) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (n + 4 * i < p.N)
-                                    ptx::red_add_v4(static_cast<float *>(p.C) + row * p.N + n + 4 * i,
-                                                    make_float4(acc[c][4 * i], acc[c][4 * i + 1], acc[c][4 * i + 2], acc[c][4 * i + 3]));
-                            continue;
-                        }
-                        store_row32<OUT != kB128Bf16>(p.C, row, p.N, n, r, 1.0f, p.st32 != 0);
-                    }
-                }
-            } else {
-                // h in the gate's place; a row's maxima from the two warps that share it
-                float gv[64], uv[64], h[64];
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        gv[c * 32 + i] = acc[c][i];
-                        uv[c * 32 + i] = acc[c + 2][i];
-                    }
-                const bool keep = p.gu != nullptr;
-                float4 top = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                for (int i = 0; i < 64; i += 2) {
-                    const uint64_t y = b128_gate2<OUT - kB128Gated>(b128_pair(gv[i], gv[i + 1]));
-                    const uint64_t v = b128_mul2(y, b128_pair(uv[i], uv[i + 1]));
-                    h[i] = b128_lo(v), h[i + 1] = b128_hi(v);
-                }
-                top.x = amax64(h);
-                if (keep) {
-                    top.y = amax64(gv);
-                    top.z = amax64(uv);
-                }
-                // [tile parity][half][row]: a slot is written again two tiles later, after
-                // its reader's next arrival
-                float4 *x = reinterpret_cast<float4 *>(smem + L::OFF_X) + (lt & 1) * 2 * kBlk;
-                x[half * kBlk + q * 32 + lane] = top;
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar_max(q, half));
-                if (!wait_bar_warp(bar_max(q, half ^ 1), lt & 1u, abort_flag, p, 3 * 256 + 96 + q)) break;
-                const float4 o = x[(half ^ 1) * kBlk + q * 32 + lane];
-                if (row < p.M) {
-                    const int64_t F = p.N, f = (int64_t)tn * kBlk + half * 64;
-                    const float sh = b128_scale<FP8G_E4M3>(fmaxf(top.x, o.x));
-                    store_codes64(p.h + row * F + f, h, __frcp_rn(sh), p.st32 != 0);
-                    if (half == 0) p.sh[tn * p.M + row] = sh;
-                    if (keep) {
-                        const float sg = b128_scale<FP8G_E4M3>(fmaxf(top.y, o.y));
-                        const float su = b128_scale<FP8G_E4M3>(fmaxf(top.z, o.z));
-                        store_codes64(p.gu + row * 2 * F + f, gv, __frcp_rn(sg), p.st32 != 0);
-                        store_codes64(p.gu + row * 2 * F + F + f, uv, __frcp_rn(su), p.st32 != 0);
-                        if (half == 0) {
-                            p.sgu[tn * p.M + row] = sg;
-                            p.sgu[(p.n_blocks + tn) * p.M + row] = su;
-                        }
-                    }
-                }
-            }
-        }
-    }
-
-roles_done:
-    __syncwarp();
-    __syncthreads();
-    if (*abort_flag) {
-        // drain the MMAs that are in flight, give copies a bounded time to land
-        if (leader && warp == 1 && lane == 0) {
-            ptx::tc_commit_pair(bar_drain);
-            const uint64_t t0 = ptx::globaltimer();
-            while (!ptx::mbar_try_wait(bar_drain, 0) && ptx::globaltimer() - t0 < p.timeout_ns) {
-            }
-        }
-        const uint64_t t0 = ptx::globaltimer();
-        while (ptx::globaltimer() - t0 < 200000ull) {
-        }
-        __syncthreads();
-    }
-    // neither CTA leaves while the other may still arrive on its barriers
-    ptx::cluster_sync();
-    if (warp == 1) {
-        ptx::tc_fence_after();
-        ptx::tmem_dealloc_pair(tmem_base, 512);
-    }
-}
-
-template <bool VECB, int OUT>
-cudaError_t launch_pair(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p, int grid,
-                        cudaStream_t stream) {
-    auto kern = b128_pair_kernel<VECB, OUT>;
-    static unsigned long long done = 0ull;  // devices on which the kernel was set up
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const unsigned long long bit = 1ull << (dev & 63);
-    if ((done & bit) == 0ull) {
-        // setmaxnreg.inc takes from what the block was launched with
-        cudaFuncAttributes fa;
-        if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
-        if (fa.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
-        e = b128_allow_smem(reinterpret_cast<const void *>(kern), Lay<VECB>::BYTES);
-        if (e != cudaSuccess) return e;
-        done |= bit;
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = Lay<VECB>::BYTES;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, A, B, p);
-}
-
-}  // namespace
-
 cudaError_t launch_b128_pair(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p,
-                             int out, bool vec_b, int num_sms, cudaStream_t stream) {
-    const int grid = 2 * (int)min((int64_t)p.T, (int64_t)num_sms / 2);
-    if (out == kB128Gated + FP8G_GATE_SILU) return launch_pair<false, kB128Gated + FP8G_GATE_SILU>(A, B, p, grid, stream);
-    if (out == kB128Gated + FP8G_GATE_GELU) return launch_pair<false, kB128Gated + FP8G_GATE_GELU>(A, B, p, grid, stream);
-    if (out == kB128Gated + FP8G_GATE_RELU) return launch_pair<false, kB128Gated + FP8G_GATE_RELU>(A, B, p, grid, stream);
-    if (vec_b) {
-        if (out == kB128Bf16) return launch_pair<true, kB128Bf16>(A, B, p, grid, stream);
-        return out == kB128F32 ? launch_pair<true, kB128F32>(A, B, p, grid, stream)
-                               : launch_pair<true, kB128Add>(A, B, p, grid, stream);
-    }
-    if (out == kB128Bf16) return launch_pair<false, kB128Bf16>(A, B, p, grid, stream);
-    return out == kB128F32 ? launch_pair<false, kB128F32>(A, B, p, grid, stream)
-                           : launch_pair<false, kB128Add>(A, B, p, grid, stream);
+                             int out, bool vec_b, cudaStream_t stream) {
+    const int grid = 2 * p.pairs;
+    if (out == kB128Gated + FP8G_GATE_SILU)
+        return launch_pair<false, kB128Gated + FP8G_GATE_SILU, false>(A, B, p, grid, stream);
+    if (out == kB128Gated + FP8G_GATE_GELU)
+        return launch_pair<false, kB128Gated + FP8G_GATE_GELU, false>(A, B, p, grid, stream);
+    if (out == kB128Gated + FP8G_GATE_RELU)
+        return launch_pair<false, kB128Gated + FP8G_GATE_RELU, false>(A, B, p, grid, stream);
+    return vec_b ? launch_product<true, false>(A, B, p, out, grid, stream)
+                 : launch_product<false, false>(A, B, p, out, grid, stream);
 }
 
 }  // namespace fp8g

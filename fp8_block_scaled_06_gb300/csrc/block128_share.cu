@@ -1,0 +1,14 @@
+// The product on CTA pairs where pairs share the K blocks of tiles (block128_pair.cuh).
+// Kernels of their own: the bookkeeping in registers cost the whole-tile loop 5%.
+#include "block128_pair.cuh"
+
+namespace fp8g {
+
+cudaError_t launch_b128_share(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p,
+                              int out, bool vec_b, cudaStream_t stream) {
+    const int grid = 2 * p.pairs;
+    return vec_b ? launch_product<true, true>(A, B, p, out, grid, stream)
+                 : launch_product<false, true>(A, B, p, out, grid, stream);
+}
+
+}  // namespace fp8g

@@ -374,7 +374,10 @@ def test_backward_rows_behind_stay(fp8g):
 # --------------------------------------- more tiles than the kernels' grids: several a CTA
 
 @pytest.mark.parametrize("form,M,N,K", [("nt", 2100, 2600, 144), ("nn", 2100, 2592, 400), ("tn", 2064, 2832, 260),
-                                        ("nt", 130, 5000, 1040), ("tn", 4096, 4096, 128)])
+                                        ("nt", 130, 5000, 1040), ("tn", 4096, 4096, 128),
+                                        # K blocks of tiles shared between pairs: all tiles, the last ones
+                                        ("nn", 1500, 1040, 16000), ("tn", 272, 400, 12000), ("tn", 16, 16, 12001),
+                                        ("nt", 4100, 1288, 16384), ("tn", 2304, 2304, 16400)])
 @pytest.mark.parametrize("out", ["bf16", "add"])
 def test_many_tiles(fp8g, form, M, N, K, out):
     r = torch.Generator(device="cuda").manual_seed(19)
@@ -405,8 +408,8 @@ def test_many_tiles(fp8g, form, M, N, K, out):
     assert torch.equal(again, got)
 
 
-def test_many_tiles_gated_and_back(fp8g):
-    M, F, K = 1500, 2048, 272
+@pytest.mark.parametrize("M,F,K", [(1500, 2048, 272), (1030, 384, 4112), (3000, 1024, 4096)])
+def test_many_tiles_gated_and_back(fp8g, M, F, K):
     r = torch.Generator(device="cuda").manual_seed(20)
     x, _ = fp8g.quantize_block128(torch.randn((M, K), device="cuda", generator=r))
     W = fp8g.quantize_tile128(torch.randn((2 * F, K), device="cuda", generator=r) * K ** -0.5)
