@@ -737,7 +737,7 @@ def _on(dev: int, *tensors):
     global _here
     if _here is None:
         import torch
-        _here = torch.cuda.current_device
+        _here = torch._C._cuda_getDevice  # (torch.cuda.current_device without its check for a first use)
     assert dev >= 0 and dev == _here(), "tensors of the current CUDA device"
     for t in tensors:
         assert t.get_device() == dev and t.is_contiguous()

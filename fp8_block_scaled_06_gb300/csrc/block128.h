@@ -80,10 +80,16 @@ struct B128Backward {
 cudaError_t launch_b128_backward(const B128Backward &a, bool bf16, int gate, int fmt,
                                  cudaStream_t stream);
 
-// Lets `kernel` have `bytes` of dynamic shared memory on the current device (an idempotent
-// call of half a microsecond).
-inline cudaError_t b128_allow_smem(const void *kernel, int bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+// Lets `kernel` have `bytes` of dynamic shared memory on the current device, once (`done`:
+// the devices that it has it on).
+inline cudaError_t b128_allow_smem(const void *kernel, int bytes, unsigned long long &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (e != cudaSuccess || (done & bit) != 0ull) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done |= bit;
+    return e;
 }
 
 }  // namespace fp8g

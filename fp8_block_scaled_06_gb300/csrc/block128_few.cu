@@ -9,9 +9,10 @@
 // and the CTAs add each other's (distributed shared memory) in rank order, each for
 // its own rows of A, so results do not vary.
 //
-// As in block128_gemm.cu each K block's product goes to a tensor-memory buffer of
-// its own and is added, scaled, to registers: thread = weight row, its values the NT
-// rows, whose scales go through shared memory, read as broadcasts.  Beyond 64 sums a thread (128 rows of A, or 64 of gate and up) four more
+// As in block128_pair.cuh each K block's product goes to a tensor-memory buffer of
+// its own and is added, scaled, to registers, in fragments of which a lane holds two rows
+// of A of four weight rows: it reads a quarter of the rows' scales (a weight row a lane,
+// shared memory took 512 cycles a K block of 128 rows to hand them out).  Beyond 64 sums a thread (128 rows of A, or 64 of gate and up) four more
 // warps take half of the rows, and a CTA has its SM alone.
 //
 // Roles (256 or 384 threads): warp 0 TMA, warp 1 MMA issue, warps 4 and up promotion; all
@@ -44,7 +45,8 @@ struct Few {
     static constexpr int BUFS = 4;
     static constexpr int TMEM = COLS * BUFS;
     static constexpr int RING = STAGES * STAGE;
-    static constexpr int SUMS = COLS * kBlk * 4;         // this CTA's sums, in the ring's place
+    static constexpr int PITCH = kBlk + 4;               // of a column's sums: a warp's stores in 32 banks
+    static constexpr int SUMS = COLS * PITCH * 4;        // this CTA's sums, in the ring's place
     static_assert(SUMS <= RING && (TMEM & (TMEM - 1)) == 0 && TMEM * PER_SM <= 512, "");
     // a promotion warp's scales of CH K blocks, A's [CH][WT] then B's [CH][G]; two such
     // chunks, one ahead
@@ -131,7 +133,7 @@ __global__ void __launch_bounds__(32 * Few<NT, (OUT >= kB128Gated)>::WARPS, Few<
             }
         }
     } else if (warp == 1) {
-        // (whole warp, one elected lane: block128_gemm.cu)
+        // (whole warp, one elected lane: block128_pair.cuh)
         const uint32_t idesc = ptx::idesc_f8(kBlk, NT) | p.types;
         const uint32_t w_step = (p.b_mn ? 32 * kBlk : 32) >> 4;
         const uint64_t w_desc = ptx::smem_desc(sbase, 1024, 1024, 2);
@@ -163,7 +165,6 @@ __global__ void __launch_bounds__(32 * Few<NT, (OUT >= kB128Gated)>::WARPS, Few<
         }
     } else if (warp >= 4) {
         const int q = warp & 3, half = (warp - 4) >> 2;
-        constexpr int WC = L::G * L::WT;     // this warp's sums a thread
         const uint32_t taddr = ((uint32_t)(q * 32) << 16) + tmem_base + half * L::WT;
         float *sc = reinterpret_cast<float *>(smem + L::OFF_S) + (warp - 4) * 2 * L::SCALES;
         const float *sb = p.sb + (pn + (int64_t)(lane & (L::G - 1)) * p.n_blocks) * p.sb_n;
@@ -184,9 +185,14 @@ __global__ void __launch_bounds__(32 * Few<NT, (OUT >= kB128Gated)>::WARPS, Few<
             ptx::cp_async_commit();
         };
         ask(kb0, 0);
-        uint64_t acc[WC / 2];
+        // pairs of rows of A: fragment j / 2's of weight row 16 h + lane / 4, + 8 for odd j
+        uint64_t acc[L::G][2][L::WT / 4];
 #pragma unroll
-        for (int i = 0; i < WC / 2; ++i) acc[i] = 0ull;
+        for (int g = 0; g < L::G; ++g)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < L::WT / 4; ++j) acc[g][h][j] = 0ull;
         uint32_t buf = 0, bphase = 0;
         bool ok = true;
         for (int kb = kb0; kb < kb1; ++kb) {
@@ -209,29 +215,22 @@ __global__ void __launch_bounds__(32 * Few<NT, (OUT >= kB128Gated)>::WARPS, Few<
                 break;
             }
             ptx::tc_fence_after();
-            constexpr int STEP = L::WT < 32 ? 16 : 32;
 #pragma unroll
-            for (int c = 0; c < WC; c += STEP) {
-                uint32_t r[STEP];
-                const uint32_t at = taddr + buf * L::COLS + c / L::WT * NT + c % L::WT;
-                if constexpr (STEP == 32) {
-                    ptx::tmem_ld_32x32b_x32(at, r);
+            for (int g = 0; g < L::G; ++g) {
+                uint64_t f[L::WT / 8];
+#pragma unroll
+                for (int j = 0; j < L::WT / 8; ++j)
+                    f[j] = b128_mul2(reinterpret_cast<const uint64_t *>(s)[4 * j + (lane & 3)], fb[g]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t r[L::WT / 2];
+                    ptx::tmem_ld_16x256b(taddr + buf * L::COLS + g * NT + ((uint32_t)h << 20), r);
                     ptx::tmem_ld_wait(r);
-                } else {
-                    uint32_t a[8], b[8];
-                    ptx::tmem_ld_32x32b_x8(at, a);
-                    ptx::tmem_ld_32x32b_x8(at + 8, b);
-                    ptx::tmem_ld_wait(a, b);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) r[i] = a[i], r[8 + i] = b[i];
-                }
-                const ulonglong2 *s2 = reinterpret_cast<const ulonglong2 *>(s + c % L::WT);
-#pragma unroll
-                for (int i = 0; i < STEP / 4; ++i) {
-                    const ulonglong2 f = s2[i];  // the same address in every lane
-                    const uint64_t w = fb[c / L::WT];
-                    b128_fma2(acc[c / 2 + 2 * i], b128_pair(r[4 * i], r[4 * i + 1]), b128_mul2(f.x, w));
-                    b128_fma2(acc[c / 2 + 2 * i + 1], b128_pair(r[4 * i + 2], r[4 * i + 3]), b128_mul2(f.y, w));
+                    for (int j = 0; j < L::WT / 8; ++j) {
+                        b128_fma2(acc[g][h][2 * j], b128_pair(r[4 * j], r[4 * j + 1]), f[j]);
+                        b128_fma2(acc[g][h][2 * j + 1], b128_pair(r[4 * j + 2], r[4 * j + 3]), f[j]);
+                    }
                 }
             }
             ptx::tc_fence_before();
@@ -245,13 +244,17 @@ __global__ void __launch_bounds__(32 * Few<NT, (OUT >= kB128Gated)>::WARPS, Few<
         // every MMA and every copy of this CTA is done: its sums take the ring's place,
         // [column][weight row]
         if (ok) {
-            float *sums = reinterpret_cast<float *>(smem) + half * L::WT * kBlk + q * 32 + lane;
+            float *sums = reinterpret_cast<float *>(smem) + q * 32 + (lane >> 2);
 #pragma unroll
-            for (int i = 0; i < WC / 2; ++i) {
-                const int col = 2 * i / L::WT * NT + 2 * i % L::WT;
-                sums[col * kBlk] = b128_lo(acc[i]);
-                sums[(col + 1) * kBlk] = b128_hi(acc[i]);
-            }
+            for (int g = 0; g < L::G; ++g)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < L::WT / 4; ++j) {
+                        float *at = sums + (g * NT + half * L::WT + 8 * (j >> 1) + 2 * (lane & 3)) * L::PITCH + 16 * h + 8 * (j & 1);
+                        at[0] = b128_lo(acc[g][h][j]);
+                        at[L::PITCH] = b128_hi(acc[g][h][j]);
+                    }
         }
     }
     __syncwarp();
@@ -273,7 +276,7 @@ __global__ void __launch_bounds__(32 * Few<NT, (OUT >= kB128Gated)>::WARPS, Few<
     // a row at a time, four weight rows a lane.
     auto total = [&](int col) {
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const uint32_t at = sbase + (col * kBlk + 4 * lane) * 4;
+        const uint32_t at = sbase + (col * L::PITCH + 4 * lane) * 4;
         for (int j = 0; j < split; ++j) {
             const float4 o = ptx::ld_cluster_f4(ptx::map_shared(at, j));
             v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
@@ -327,7 +330,8 @@ cudaError_t launch_few(const CUtensorMap &A, const CUtensorMap &B, const B128Par
                        cudaStream_t stream) {
     using L = Few<NT, (OUT >= kB128Gated)>;
     auto kern = b128_few_kernel<NT, OUT>;
-    const cudaError_t e = b128_allow_smem(reinterpret_cast<const void *>(kern), L::BYTES);
+    static unsigned long long done = 0ull;
+    const cudaError_t e = b128_allow_smem(reinterpret_cast<const void *>(kern), L::BYTES, done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.n_blocks, (unsigned)((p.M + NT - 1) / NT), (unsigned)split);

@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto load = [&](uint32_t i, int c, uint32_t(&r)[32]) {
             if constexpr (VECB)
-                ptx::tmem_ld_16x256b_x8(chunk(i, c), r);
+                ptx::tmem_ld_16x256b(chunk(i, c), r);
             else
                 ptx::tmem_ld_32x32b_x32(chunk(i, c), r);
         };
@@ -638,20 +638,16 @@ template <bool VECB, int OUT, bool SHARE>
 cudaError_t launch_pair(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p, int grid,
                         cudaStream_t stream) {
     auto kern = b128_pair_kernel<VECB, OUT, SHARE>;
-    static unsigned long long done = 0ull;  // devices on which the kernel was set up
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const unsigned long long bit = 1ull << (dev & 63);
-    if ((done & bit) == 0ull) {
+    static unsigned long long done = 0ull;
+    if (done == 0ull) {
         // setmaxnreg.inc takes from what the block was launched with
         cudaFuncAttributes fa;
-        if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
-        if (fa.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
-        e = b128_allow_smem(reinterpret_cast<const void *>(kern), Lay<VECB>::BYTES);
+        const cudaError_t e = cudaFuncGetAttributes(&fa, kern);
         if (e != cudaSuccess) return e;
-        done |= bit;
+        if (fa.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
     }
+    const cudaError_t e = b128_allow_smem(reinterpret_cast<const void *>(kern), Lay<VECB>::BYTES, done);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);

@@ -125,7 +125,7 @@ template <int SRC>
 constexpr int kSrcBytes = SRC == FP8G_IN_F32 ? 4 : SRC == FP8G_IN_BF16 ? 2 : 1;
 
 template <int SRC, int FMT, bool ROW, bool TILE>
-__global__ void __launch_bounds__(kTileThreads) b128_quant_tile_kernel(const B128Quant a) {
+__global__ void __launch_bounds__(kTileThreads, 4) b128_quant_tile_kernel(const B128Quant a) {
     constexpr int E = kSrcBytes<SRC>;
     extern __shared__ __align__(16) uint8_t sm[];
     uint32_t *top = reinterpret_cast<uint32_t *>(sm + kBlk * kBlk * E);  // column maxima [128]
@@ -155,15 +155,15 @@ __global__ void __launch_bounds__(kTileThreads) b128_quant_tile_kernel(const B12
             widen4(reinterpret_cast<const uint2 *>(sm)[r * 32 + lane], v);
         } else {
             b128_decode(reinterpret_cast<const uint32_t *>(sm)[r * 32 + lane], a.src_fmt, v);
-            const float s = src_s[r];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = __fmul_rn(v[k], s);
+            const uint64_t s = b128_pair(src_s[r], src_s[r]);
+            const uint64_t lo = b128_mul2(b128_pair(v[0], v[1]), s), hi = b128_mul2(b128_pair(v[2], v[3]), s);
+            v[0] = b128_lo(lo), v[1] = b128_hi(lo), v[2] = b128_lo(hi), v[3] = b128_hi(hi);
         }
     };
     // (rows and columns past the matrix are zeros: they change no maximum)
     const int first = warp * kRowsPerWarp;
     float cm[4] = {}, own = 0.0f;  // own: lane i has row first + i's
-#pragma unroll 4
+#pragma unroll
     for (int i = 0; i < kRowsPerWarp; i += 2) {
         float v[4], w[4];
         values(first + i, v);
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kTileThreads) b128_quant_tile_kernel(const B12
     const int64_t at = (row0 + first) * a.C + c;
     uint8_t *q = (TILE ? a.q_tile : a.q_col) + at, *q_row = ROW ? a.q_row + at : nullptr;
     const int live = in ? min(kRowsPerWarp, rows - first) : 0;
-#pragma unroll 4
+#pragma unroll
     for (int i = 0; i < kRowsPerWarp; ++i) {
         float v[4];
         values(first + i, v);
@@ -375,7 +375,8 @@ cudaError_t quant_tile(const B128Quant &a, cudaStream_t s) {
     auto kern = b128_quant_tile_kernel<SRC, FMT, ROW, TILE>;
     constexpr int kBytes = kBlk * kBlk * kSrcBytes<SRC> + 2 * kBlk * 4;
     if constexpr (kBytes > 48 * 1024) {
-        const cudaError_t e = b128_allow_smem(reinterpret_cast<const void *>(kern), kBytes);
+        static unsigned long long done = 0ull;
+        const cudaError_t e = b128_allow_smem(reinterpret_cast<const void *>(kern), kBytes, done);
         if (e != cudaSuccess) return e;
     }
     const dim3 grid((unsigned)((a.C + kBlk - 1) / kBlk), (unsigned)((a.R + kBlk - 1) / kBlk));
@@ -395,7 +396,8 @@ template <bool BF16, int GATE, int FMT>
 cudaError_t backward_fmt(const B128Backward &a, cudaStream_t s) {
     auto kern = b128_backward_kernel<BF16, GATE, FMT>;
     constexpr int kBytes = BackTile<BF16>::BYTES;
-    const cudaError_t e = b128_allow_smem(reinterpret_cast<const void *>(kern), kBytes);
+    static unsigned long long done = 0ull;
+    const cudaError_t e = b128_allow_smem(reinterpret_cast<const void *>(kern), kBytes, done);
     const int64_t tiles = (a.M + kBlk - 1) / kBlk * (a.F / kBlk);
     const dim3 grid((unsigned)min(tiles, (int64_t)a.num_sms));
     return e != cudaSuccess ? e : launch_programmatic_smem(kern, grid, dim3(kBackThreads), kBytes, s, a);
