@@ -182,7 +182,8 @@ struct ScaleChunks {
 #pragma unroll
         for (int j = 0; j < L::CH; ++j)
             if (kb + j < n(p)) {
-                ptx::cp_async_4(at + (j * 32 + lane) * 4, a + (kb + j) * p.M, 4);
+                // (VECB: the scales of a fragment's four rows side by side)
+                ptx::cp_async_4(at + (j * 32 + (VECB ? lane % 8 * 4 + lane / 8 : lane)) * 4, a + (kb + j) * p.M, 4);
                 if constexpr (VECB)
                     ptx::cp_async_16(at + (L::CH * 32 + j * kBlk + 4 * lane) * 4, b + (kb + j) * p.N, 16);
             }
@@ -418,9 +419,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 8; ++j) cb[j] = col[4 * j + (lane & 3)];
                 };
                 if constexpr (VECB) {
-                    const float *r = sc + at_k * 32 + (lane >> 2);
-                    ra[0] = make_float2(r[0], r[8]);
-                    ra[1] = make_float2(r[16], r[24]);
+                    const float4 r = reinterpret_cast<const float4 *>(sc + at_k * 32)[lane >> 2];
+                    ra[0] = make_float2(r.x, r.y);
+                    ra[1] = make_float2(r.z, r.w);
                     columns(0);
                 }
                 auto add = [&](int c, const uint32_t(&r)[32]) {
