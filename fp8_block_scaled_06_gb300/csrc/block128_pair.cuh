@@ -54,18 +54,18 @@ constexpr int kBufs = 2;               // product buffers of 256 columns
 
 template <bool VECB>
 struct Lay {
-    static constexpr int STAGES = VECB ? 5 : 6;
+    static constexpr int STAGES = 6;
     static constexpr int OFF_B = STAGES * kTile;
-    // a promotion warp's scales of CH K blocks: A's [CH][32 lanes], then B's [CH][128
-    // columns] or [CH][two tiles]; two such buffers a warp
-    static constexpr int CH = VECB ? 4 : 8;
-    static constexpr int SCALES = CH * (32 + (VECB ? kBlk : 2));
+    // scales of CH K blocks: A's [CH][128 rows], then B's [CH][256 columns] or [CH][two
+    // tiles]; two such chunks
+    static constexpr int CH = 8;
+    static constexpr int SCALES = CH * (kBlk + (VECB ? 2 * kBlk : 2));
     static constexpr int OFF_S = 2 * STAGES * kTile;
-    static constexpr int OFF_X = OFF_S + kPromWarps * 2 * SCALES * 4;  // row maxima: [2][2][128] float4
+    static constexpr int OFF_X = OFF_S + 2 * SCALES * 4;  // row maxima: [2][2][128] float4
     static constexpr int OFF_BAR = OFF_X + (VECB ? 0 : 2 * 2 * kBlk * 16);
     // full, empty [STAGES]; product full, product empty [kBufs]; row maxima [lane
-    // quarter][half]; drain
-    static constexpr int NUM_BARS = 2 * STAGES + 2 * kBufs + 8 + 1;
+    // quarter][half]; scales full, empty [2]; drain
+    static constexpr int NUM_BARS = 2 * STAGES + 2 * kBufs + 8 + 4 + 1;
     static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
     static constexpr int BYTES = OFF_MISC + 16 + 1024;
     static_assert(BYTES <= 232448, "shared memory over the per-CTA limit");
@@ -149,49 +149,22 @@ __device__ __forceinline__ bool wait_flag(const int32_t *flag, volatile int *abo
     return ok != 0;
 }
 
-// The scales of a promotion warp, copied (cp.async) to shared memory of its own, CH K
-// blocks at a time and one such chunk ahead: waiting for a copy and asking for the next
-// cost a K block 230 cycles where each had its own.  (In registers, handed on from one
-// K block to the next, each handing on waited for the newest load.)
-template <bool VECB, int OUT, bool SHARE>
-struct ScaleChunks {
-    using L = Lay<VECB>;
-    float *buf;          // [2][SCALES]
-    const float *a, *b;  // this lane's row of A; columns of B, or one of its two tiles
-    int32_t own;         // K blocks of the item, where tiles are shared
-    __device__ __forceinline__ int32_t n(const B128Params &p) const { return SHARE ? own : p.num_kb; }
-    __device__ __forceinline__ void tile(const B128Params &p, int64_t row, int pn, int half, int32_t k0, int32_t k1) {
-        if constexpr (SHARE)
-            own = k1 - k0;
-        else
-            k0 = 0;
-        const int lane = threadIdx.x & 31;
-        a = p.sa + k0 * p.M + min(row, p.M - 1);
-        if constexpr (VECB) {  // four columns a lane (N is a multiple of 16)
-            b = p.sb + k0 * p.N + min((int64_t)pn * 2 * kBlk + half * 64 + 4 * lane + (lane >= 16 ? 64 : 0), p.N - 4);
+// One K block's scales of the two warps that copy them: lane l of 64 has rows l and l + 64
+// of the CTA's 128, and four columns of the tile's 256 (VECB) or, of the first 2 CH
+// lanes, one of its two tiles of B in K block l / 2 of the chunk.
+template <bool VECB, int OUT>
+struct ScaleSource {
+    const float *a0, *a1, *b;
+    __device__ __forceinline__ void tile(const B128Params &p, int l, int64_t row0, int pn, int32_t k0) {
+        a0 = p.sa + k0 * p.M + min(row0 + l, p.M - 1);
+        a1 = p.sa + k0 * p.M + min(row0 + l + 64, p.M - 1);
+        if constexpr (VECB) {  // (N is a multiple of 16)
+            b = p.sb + k0 * p.N + min((int64_t)pn * 2 * kBlk + 4 * l, p.N - 4);
         } else {
             const int64_t n0 = OUT >= kB128Gated ? pn : 2 * pn;
             const int64_t n1 = OUT >= kB128Gated ? n0 + p.n_blocks : min(n0 + 1, (int64_t)p.n_blocks - 1);
-            b = p.sb + ((lane & 1) == 0 ? n0 : n1) * p.sb_n + k0 * p.sb_k;
+            b = p.sb + ((l & 1) == 0 ? n0 : n1) * p.sb_n + (k0 + (l >> 1)) * p.sb_k;
         }
-    }
-    // K blocks kb .. kb + CH - 1 of the item to buffer i
-    __device__ __forceinline__ void ask(const B128Params &p, int32_t kb, uint32_t i) const {
-        const int lane = threadIdx.x & 31;
-        const uint32_t at = ptx::smem_addr(buf + (i & 1u) * L::SCALES);
-#pragma unroll
-        for (int j = 0; j < L::CH; ++j)
-            if (kb + j < n(p)) {
-                // (VECB: the scales of a fragment's four rows side by side)
-                ptx::cp_async_4(at + (j * 32 + (VECB ? lane % 8 * 4 + lane / 8 : lane)) * 4, a + (kb + j) * p.M, 4);
-                if constexpr (VECB)
-                    ptx::cp_async_16(at + (L::CH * 32 + j * kBlk + 4 * lane) * 4, b + (kb + j) * p.N, 16);
-            }
-        if constexpr (!VECB) {
-            if (lane < 2 * L::CH && kb + (lane >> 1) < n(p))
-                ptx::cp_async_4(at + (L::CH * 32 + lane) * 4, b + (kb + (lane >> 1)) * p.sb_k, 4);
-        }
-        ptx::cp_async_commit();
     }
 };
 
@@ -239,6 +212,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto bar_pfull = [&](int b) { return ptx::smem_addr(&bars[2 * L::STAGES + b]); };
     auto bar_pempty = [&](int b) { return ptx::smem_addr(&bars[2 * L::STAGES + kBufs + b]); };
     auto bar_max = [&](int q, int h) { return ptx::smem_addr(&bars[2 * L::STAGES + 2 * kBufs + 2 * q + h]); };
+    auto bar_sfull = [&](int i) { return ptx::smem_addr(&bars[2 * L::STAGES + 2 * kBufs + 8 + i]); };
+    auto bar_sempty = [&](int i) { return ptx::smem_addr(&bars[2 * L::STAGES + 2 * kBufs + 10 + i]); };
     const uint32_t bar_drain = ptx::smem_addr(&bars[L::NUM_BARS - 1]);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
@@ -254,6 +229,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(bar_pempty(b), 2 * kPromWarps);
         }
         for (int i = 0; i < 8; ++i) ptx::mbar_init(bar_max(i >> 1, i & 1), 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar_sfull(i), 64);
+            ptx::mbar_init(bar_sempty(i), kPromWarps);
+        }
         ptx::mbar_init(bar_drain, 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
@@ -344,6 +323,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
+        } else if (warp >= 2) {
+            // ===== scales: chunks of CH K blocks, two of them ahead, over all items =====
+            const int l = (int)threadIdx.x - 64;
+            uint32_t c = 0;
+            Item it;
+            for (int32_t i = 0; run && item<SHARE>(p, pair, i, it); ++i) {
+                int32_t pm, pn;
+                raster(it.t, p.npm, p.npn, kRasterG, pm, pn);
+                ScaleSource<VECB, OUT> src;
+                src.tile(p, l, (2 * (int64_t)pm + rank) * kBlk, pn, it.k0);
+                const int32_t n = it.k1 - it.k0;
+                for (int32_t kb = 0; kb < n; kb += L::CH, ++c) {
+                    if (!b128_wait_all(bar_sempty(c & 1u), ((c >> 1) & 1u) ^ 1u, abort_flag, p, 2 * 256 + (c & 1u)))
+                        goto roles_done;
+                    const uint32_t at = sbase + L::OFF_S + (c & 1u) * L::SCALES * 4;
+                    // (VECB: a fragment's four rows side by side)
+                    const uint32_t to = at + (VECB ? l / 32 * 32 + l % 8 * 4 + l % 32 / 8 : l) * 4;
+                    for (int j = 0; j < L::CH && kb + j < n; ++j) {
+                        ptx::cp_async_4(to + j * kBlk * 4, src.a0, 4);
+                        ptx::cp_async_4(to + j * kBlk * 4 + 256, src.a1, 4);
+                        src.a0 += p.M;
+                        src.a1 += p.M;
+                        if constexpr (VECB) {
+                            ptx::cp_async_16(at + (L::CH * kBlk + j * 2 * kBlk + 4 * l) * 4, src.b, 16);
+                            src.b += p.N;
+                        }
+                    }
+                    if constexpr (!VECB) {
+                        if (l < 2 * L::CH && kb + (l >> 1) < n) ptx::cp_async_4(at + (L::CH * kBlk + l) * 4, src.b, 4);
+                        src.b += L::CH * p.sb_k;
+                    }
+                    ptx::cp_async_arrive(bar_sfull(c & 1u));
+                }
+            }
         }
     } else {
         // ===== promotion and epilogue: this CTA's 128 rows =====
@@ -368,20 +381,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t free0 = ptx::map_shared(bar_pempty(0), 0), free1 = ptx::map_shared(bar_pempty(1), 0);
         const int row_in = (int)rank * kBlk + q * 32 + lane;
         uint32_t g = 0, lt = 0;
-        int32_t pm = 0, pn = 0;
-        uint32_t chunks = 0;  // of scales, over all tiles
-        ScaleChunks<VECB, OUT, SHARE> scales;
-        scales.buf = reinterpret_cast<float *>(smem + L::OFF_S) + (warp - kProm0) * 2 * L::SCALES;
-        auto begin = [&](int32_t i) {  // the i-th item's first scales
-            Item o;
-            if (!item<SHARE>(p, pair, i, o)) return false;
-            raster(o.t, p.npm, p.npn, kRasterG, pm, pn);
-            scales.tile(p, (int64_t)pm * 2 * kBlk + row_in, pn, half, o.k0, o.k1);
-            scales.ask(p, 0, chunks);
-            return true;
-        };
-        int32_t i = 0;
-        for (bool more = run && begin(0); more;) {
+        uint32_t chunks = 0;  // of scales, over all items
+        Item it;
+        for (int32_t i = 0; run && item<SHARE>(p, pair, i, it); ++i) {
             // VECB: pairs of columns, in packed arithmetic (issue slots, not the pipe, ran short)
             float acc[VECB ? 1 : 4][32];
             uint64_t acc2[VECB ? 4 : 1][16];
@@ -396,30 +398,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             uint32_t r0[32], r1[32];
             bool ok = true;
-            for (int32_t kb = 0; kb < scales.n(p); ++kb, ++g) {
+            const int32_t n = SHARE ? it.k1 - it.k0 : p.num_kb;
+            for (int32_t kb = 0; kb < n; ++kb, ++g) {
                 const uint32_t buf = g & 1u;
                 const int32_t at_k = kb % L::CH;
-                if (at_k == 0) {
-                    ptx::cp_async_wait<0>();
-                    __syncwarp();  // this chunk is there for every lane, and the one before it read by all
-                    ++chunks;
-                    if (kb + L::CH < scales.n(p)) scales.ask(p, kb + L::CH, chunks);
+                if (at_k == 0 && !b128_wait_all(bar_sfull(chunks & 1u), (chunks >> 1) & 1u, abort_flag, p, 3 * 256 + chunks % 2)) {
+                    ok = false;
+                    break;
                 }
-                const float *sc = scales.buf + (~chunks & 1u) * L::SCALES;
-                const float sa = VECB ? 0.0f : sc[at_k * 32 + lane];
+                const float *sc = reinterpret_cast<const float *>(smem + L::OFF_S) + (chunks & 1u) * L::SCALES;
+                const float sa = VECB ? 0.0f : sc[at_k * kBlk + q * 32 + lane];
                 float2 sb{};
-                if constexpr (!VECB) sb = *reinterpret_cast<const float2 *>(sc + L::CH * 32 + at_k * 2);
+                if constexpr (!VECB) sb = *reinterpret_cast<const float2 *>(sc + L::CH * kBlk + at_k * 2);
                 // VECB: the lane's rows' and its columns' scales, the latter of one block of 64 at a
                 // time, read before what they are for arrives
                 float2 ra[2];
                 uint64_t cb[8];
                 auto columns = [&](int block) {
-                    const uint64_t *col = reinterpret_cast<const uint64_t *>(sc + L::CH * 32 + at_k * kBlk + block * 64);
+                    const uint64_t *col = reinterpret_cast<const uint64_t *>(sc + L::CH * kBlk + at_k * 2 * kBlk + block * kBlk +
+                                                                             half * 64);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) cb[j] = col[4 * j + (lane & 3)];
                 };
                 if constexpr (VECB) {
-                    const float4 r = reinterpret_cast<const float4 *>(sc + at_k * 32)[lane >> 2];
+                    const float4 r = reinterpret_cast<const float4 *>(sc + at_k * kBlk + q * 32)[lane >> 2];
                     ra[0] = make_float2(r.x, r.y);
                     ra[1] = make_float2(r.z, r.w);
                     columns(0);
@@ -462,13 +464,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::mbar_arrive_cluster_relaxed(buf ? free1 : free0, lane == 0);
                 add(2, r0);
                 add(3, r1);
+                if (at_k == L::CH - 1 || kb + 1 == n) {  // this chunk is read
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar_sempty(chunks & 1u));
+                    ++chunks;
+                }
             }
             if (!ok) break;
+            int32_t pm, tn;
+            raster(it.t, p.npm, p.npn, kRasterG, pm, tn);
             const int64_t row = (int64_t)pm * 2 * kBlk + row_in;
-            const int32_t tn = pn;
-            Item it{};
-            if constexpr (SHARE) item<SHARE>(p, pair, i, it);
-            more = begin(++i);  // (beside what follows)
             if (SHARE && (it.publish || it.from < pair)) {
                 // sums as the warp holds them, 16 bytes a lane
                 auto at = [&](int32_t c) {
