@@ -726,7 +726,7 @@ def gemm_lora(x, W, sfw, lora_a, lora_b, alpha, adapter, bias=None, w_fmt: int =
 
 
 # Scales for blocks of 128 (fp8_gemm_block128 and the calls around it).  Codes are
-# uint8 (or torch's float8) [R, C]; scales fp32 [ceil(C/128), R] along rows,
+# uint8 (or torch's float8 of the format that is named) [R, C]; scales fp32 [ceil(C/128), R] along rows,
 # [ceil(R/128), C] along columns, [ceil(R/128), ceil(C/128)] of tiles.
 
 _here = None  # the current device's index
@@ -741,6 +741,21 @@ def _on(dev: int, *tensors):
     assert dev >= 0 and dev == _here(), "tensors of the current CUDA device"
     for t in tensors:
         assert t.get_device() == dev and t.is_contiguous()
+
+
+_f8 = None
+
+
+def _coded(t, fmt: int) -> bool:
+    """t holds codes of fmt: bytes, or torch's type of that format."""
+    global _f8
+    dt = t.dtype
+    if dt is (_t or _names())[4]:
+        return True
+    if _f8 is None:
+        import torch
+        _f8 = (torch.float8_e4m3fn, torch.float8_e5m2)
+    return fmt in (FP8G_E4M3, FP8G_E5M2) and dt is _f8[fmt]
 
 
 def _source(x, stream):
@@ -797,7 +812,7 @@ def requantize_block128(q, s, fmt: int = FP8G_E4M3, q_fmt: int = FP8G_E4M3, stre
     empty, _, f32, _, u8 = _t or _names()
     _on(q.get_device(), q, s)
     R, C = q.shape
-    assert q.itemsize == 1 and s.dtype is f32 and s.shape == (-(-C // 128), R)
+    assert _coded(q, q_fmt) and s.dtype is f32 and s.shape == (-(-C // 128), R)
     qc = empty((R, C), dtype=u8, device=q.device)
     sc = empty((-(-R // 128), C), dtype=f32, device=q.device)
     st = (_lib or load()).fp8g_requantize_block128(q.data_ptr(), q_fmt, s.data_ptr(), R, C, fmt,
@@ -819,7 +834,7 @@ def gemm_block128(A, sfa, B, sfb, form: str = "nt", a_fmt: int = FP8G_E4M3, b_fm
     empty, bf16, f32, _, _ = _t or _names()
     dev = A.get_device()
     _on(dev, A, sfa, B, sfb)
-    assert A.itemsize == 1 and B.itemsize == 1 and sfa.dtype is f32 and sfb.dtype is f32
+    assert _coded(A, a_fmt) and _coded(B, b_fmt) and sfa.dtype is f32 and sfb.dtype is f32
     a0, a1 = A.shape
     b0, b1 = B.shape
     if form == "tn":
@@ -853,7 +868,7 @@ def gated_block128(x, sfx, W13, sf13, gate: int = FP8G_GATE_SILU, keep: bool = F
     empty, _, f32, _, u8 = _t or _names()
     dev = x.device
     _on(x.get_device(), x, sfx, W13, sf13)
-    assert x.itemsize == 1 and W13.itemsize == 1 and sfx.dtype is f32 and sf13.dtype is f32
+    assert _coded(x, x_fmt) and _coded(W13, w_fmt) and sfx.dtype is f32 and sf13.dtype is f32
     M, K = x.shape
     F2, k = W13.shape
     F = F2 // 2
@@ -882,7 +897,7 @@ def gated_block128_backward(dh, gu, sgu, gate: int = FP8G_GATE_SILU, fmt: int = 
     _on(dh.get_device(), dh, gu, sgu)
     dt = dh.dtype
     M, F = dh.shape
-    assert (dt is bf16 or dt is f32) and gu.itemsize == 1 and gu.shape == (M, 2 * F)
+    assert (dt is bf16 or dt is f32) and _coded(gu, FP8G_E4M3) and gu.shape == (M, 2 * F)
     assert sgu.dtype is f32 and sgu.shape == (-(-2 * F // 128), M)
     mb = -(-M // 128)
     row, col = empty((M, 2 * F), dtype=u8, device=dev), empty((M, 2 * F), dtype=u8, device=dev)

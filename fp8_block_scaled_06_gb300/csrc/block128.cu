@@ -17,8 +17,8 @@ constexpr int64_t kMaxQuantRows = (int64_t)65535 * 16;  // 16 rows at least a bl
 // the last would leave pairs idle, its K blocks in shares, a tile's to four pairs at
 // most (the one with its end adds the others' sums, 256 KB each).  Shares cost the time
 // of about 50 K blocks (writing and adding sums, zeroing flags, the gap between kernels;
-// 4096 x 4096 x 4096, where they save 20, took 76 us in place of 64): taken where they
-// save 60.
+// 4096 x 4096 x 4096, where they save 20, took 74 us in place of 58): taken where they
+// save 60 (1024 x 1024 x 16384 weight gradient 45 us, in whole tiles 108).
 struct Deal {
     int32_t pairs, full, share;
     int64_t units;  // K blocks one after the other
@@ -49,9 +49,9 @@ struct Plan {
 // tile of 128 weight rows; a round begins and ends with the time of five K blocks
 // (first loads, joining), each further CTA of a tile joins about one more; a K block
 // takes 110 where a CTA has its SM alone, 130 where two share it (loads bound both).
-// Measured, us, few rows / pairs in whole tiles: 64 x 14336 x 4096 14.5 / 19.5, 77 of
-// them 24 / 19.5, 77 x 4096 x 14336 21 / 54, 256 of them 34 / 46; gated, 64 rows of F
-// 14336, K 4096 27 / 40, 128 rows 48 / 40.
+// Measured, us, few rows / pairs: 64 x 14336 x 4096 15 / 18, 77 of them 21 / 17.5, 77 x
+// 4096 x 14336 19 / 50, 256 of them 30 / 43; gated, 64 rows of F 14336, K 4096 25 / 35,
+// 128 rows 44 / 35.
 Plan plan(int64_t M, int64_t n_blocks, const Deal &d, int num_kb, bool gated, int num_sms) {
     int64_t least = (d.units + 8) * 76;
     Plan best{false, kBlk, 1};
@@ -82,7 +82,7 @@ fp8g_status run_pairs(const CUtensorMap &A, const CUtensorMap &B, B128Params &p,
     const fp8g_status st = host_pool(dev, pool);
     if (st != FP8G_OK) return st;
     void *ws = nullptr;
-    const size_t sums = (size_t)dl.pairs * kB128PartBytes, flags = (size_t)dl.pairs * kB128ThereBytes;
+    const size_t sums = (size_t)dl.pairs * kB128PartBytes, flags = ((size_t)dl.pairs * 16 + 1) * 4;
     if (cudaMallocFromPoolAsync(&ws, sums + flags, pool, stream) != cudaSuccess) return FP8G_ERR_CUDA;
     p.part = static_cast<float *>(ws);
     p.there = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + sums);

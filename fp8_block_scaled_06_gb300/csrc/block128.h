@@ -23,7 +23,8 @@ struct B128Params {
     // last round)
     int32_t pairs, full, share;
     float *part;            // [pairs][256 x 256] sums of a share that ends inside its tile
-    int32_t *there;         // [pairs][16] by warp: part is written (zeros at the start)
+    int32_t *there;         // zeros at the start. [pairs][16] by warp: part is written; then
+                            // the pairs that have begun
     const float *sa;        // [num_kb][M]
     const float *sb;        // vectors [num_kb][N]; tiles: block (n, k) at n sb_n + k sb_k
     int64_t sb_n, sb_k;
@@ -42,13 +43,14 @@ struct B128Params {
 // What a product kernel ends in (kB128Gated + FP8G_GATE_*: h = act(g) u in 8 bits).
 enum B128Out : int { kB128Bf16 = 0, kB128F32 = 1, kB128Add = 2, kB128Gated = 3 };
 
-// block128_gemm.cu, block128_share.cu (p.share > 0; no gated outputs): CTA pairs over 256 x 256 tiles (gated: 256 rows, 128 columns
-// of gate and of up).  vec_b: B's scales are vectors.
+// block128_gemm.cu, block128_share.cu (p.share > 0; no gated outputs): CTA pairs over
+// 256 x 256 tiles (gated: 256 rows, 128 columns of gate and of up).  vec_b: B's scales are
+// vectors.
 cudaError_t launch_b128_pair(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p,
                              int out, bool vec_b, cudaStream_t stream);
 cudaError_t launch_b128_share(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p,
                               int out, bool vec_b, cudaStream_t stream);
-constexpr int64_t kB128PartBytes = (int64_t)4 * kBlk * kBlk * 4, kB128ThereBytes = 16 * 4;  // of a pair
+constexpr int64_t kB128PartBytes = (int64_t)4 * kBlk * kBlk * 4;  // a pair's sums
 
 // block128_few.cu: few rows of C.  The weights (B) are the MMA's 128-row operand,
 // nt rows of A its columns; K split over clusters of `split` CTAs.
@@ -81,7 +83,7 @@ cudaError_t launch_b128_backward(const B128Backward &a, bool bf16, int gate, int
                                  cudaStream_t stream);
 
 // Lets `kernel` have `bytes` of dynamic shared memory on the current device, once (`done`:
-// the devices that it has it on).
+// the devices that it has it on; calls that race on it set it twice).
 inline cudaError_t b128_allow_smem(const void *kernel, int bytes, unsigned long long &done) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

@@ -12,8 +12,10 @@
 // As in block128_pair.cuh each K block's product goes to a tensor-memory buffer of
 // its own and is added, scaled, to registers, in fragments of which a lane holds two rows
 // of A of four weight rows: it reads a quarter of the rows' scales (a weight row a lane,
-// shared memory took 512 cycles a K block of 128 rows to hand them out).  Beyond 64 sums a thread (128 rows of A, or 64 of gate and up) four more
-// warps take half of the rows, and a CTA has its SM alone.
+// shared memory took 512 cycles a K block of 128 rows to hand them out).  Beyond 64 sums
+// a thread (128 rows of A, or 64 of gate and up) four more warps take half of the rows,
+// and a CTA has its SM alone.  Measured (58.7 MB of weights, back to back): 1 x 4096 x 14336
+// 12.4 us, 128 x 14336 x 4096 21 us; gate and up, 1 row of F 14336, K 4096 21 us, 5.6 TB/s.
 //
 // Roles (256 or 384 threads): warp 0 TMA, warp 1 MMA issue, warps 4 and up promotion; all
 // warps add and store.
@@ -168,8 +170,7 @@ __global__ void __launch_bounds__(32 * Few<NT, (OUT >= kB128Gated)>::WARPS, Few<
         const uint32_t taddr = ((uint32_t)(q * 32) << 16) + tmem_base + half * L::WT;
         float *sc = reinterpret_cast<float *>(smem + L::OFF_S) + (warp - 4) * 2 * L::SCALES;
         const float *sb = p.sb + (pn + (int64_t)(lane & (L::G - 1)) * p.n_blocks) * p.sb_n;
-        // Scales of K blocks kb .. to chunk i (cp.async; fetched a K block ahead in registers,
-        // each K block waited for its fetch: 1700 cycles)
+        // Scales of K blocks kb .. to chunk i
         auto ask = [&](int kb, int i) {
             const uint32_t at = ptx::smem_addr(sc + (i & 1) * L::SCALES);
 #pragma unroll

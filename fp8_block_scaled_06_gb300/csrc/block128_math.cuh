@@ -126,13 +126,10 @@ __device__ __forceinline__ float b128_gate(float g) {
     return g < 0.0f ? 0.0f : g;
 }
 
-// The activation's value and its derivative.
-__device__ __forceinline__ void b128_gate_grad(float g, int gate, float &y, float &d) {
-    if (gate == FP8G_GATE_SILU) {
-        const float s = b128_sigmoid(g);
-        y = g * s;
-        d = s * (1.0f + g * (1.0f - s));
-    } else if (gate == FP8G_GATE_GELU) {
+// The activation's value and its derivative (GELU, ReLU).
+template <int GATE>
+__device__ __forceinline__ void b128_gate_grad(float g, float &y, float &d) {
+    if constexpr (GATE == FP8G_GATE_GELU) {
         const float c = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
         float e;
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * g * -0.72134752044448170f));
@@ -171,8 +168,8 @@ __device__ __forceinline__ void b128_gate_grad2(uint64_t g, uint64_t &y, uint64_
         d = b128_mul2(s, b128_madd2(g, rest, one));
     } else {
         float y0, y1, d0, d1;
-        b128_gate_grad(b128_lo(g), GATE, y0, d0);
-        b128_gate_grad(b128_hi(g), GATE, y1, d1);
+        b128_gate_grad<GATE>(b128_lo(g), y0, d0);
+        b128_gate_grad<GATE>(b128_hi(g), y1, d1);
         y = b128_pair(y0, y1);
         d = b128_pair(d0, d1);
     }

@@ -8,12 +8,23 @@
 // The tensor core takes no fp32 scales, so each K block's unscaled product P_kb
 // goes to one of two 256-column tensor-memory buffers (kind::f8f6f4, the first of
 // its four MMAs overwrites) and eight promotion warps per CTA add it, scaled, to
-// fp32 registers while the MMAs of the next K block fill the other buffer.  One K
-// block of a pair's 256 x 256 tile takes the tensor cores 512 cycles; a promotion
-// warp's 32 x 128 share is 4 tensor-memory loads of 32 columns and 64 packed FMAs
-// where one scale serves its 128 columns (128 x 128 tiles of B), with the FMA pipe
-// half busy.  With a scale per column (weight gradients) each pair of values costs
-// a multiplication too, and the pipe is as busy as the tensor core.
+// fp32 registers while the MMAs of the next K block fill the other buffer.  The four
+// MMAs of a pair's 256 x 256 tile take 725 cycles a K block; a buffer that is filled has to
+// be read and released within that time, latencies included, or the MMAs wait.  So between
+// a product's arrival and the release the promotion warps do nothing else, the release is
+// a relaxed arrival (with release semantics it waited for copies in flight: 2500 cycles a
+// K block), the MMA warp stays whole and one elected lane issues (one lane's own branch:
+// 1020), and two other warps copy all scales (a ring of each promotion warp's own: 5% of
+// 8192 cubed).  Measured 8192 x 8192 x 8192: 353 us, 3110 TFLOP/s, as the kernel whose
+// scales the tensor core applies (gemm_pair.cu, powers of two for blocks of 32).
+//
+// A promotion warp has 32 rows and 128 columns.  Where one scale serves 128 columns (tiles
+// of B), a lane has a row: 4 loads of 32 columns, 128 FMAs.  With a scale per column
+// (weight gradients) it has two columns of four rows in each fragment of 8 x 16, so that it
+// reads a quarter of the columns' scales (a row a lane, shared memory took 1024 cycles a K
+// block to hand them out), in packed pairs; those loads take three times as long, and
+// loads, arithmetic and scales come one after the other: 1250 cycles a K block, 1680
+// TFLOP/s at 4096 x 14336 x 4096.
 //
 // Operands lie either way.  Contraction contiguous: 128 B rows of the 128-byte
 // swizzle, an MMA's 32 values 32 B apart.  M (N) contiguous: the tile's 128 rows are
@@ -23,14 +34,10 @@
 // activations the forward product and the weight gradient.
 //
 // Roles (384 threads): warp 0 TMA producer (both CTAs, their own halves), warp 1 of
-// the even CTA MMA issue, warps 4-11 promotion and epilogue: lane quarter warp & 3,
-// half of the columns.  They
-// hold 128 accumulators a thread, so registers move to them (setmaxnreg: 256 x 232
-// + 128 x 40 = 384 x 168).  Scales are read up to three K blocks ahead, straight to
-// registers; column vectors then pass through shared memory of the warp's own, to be
-// read as broadcasts.  A warp's arrival that frees a buffer is relaxed: with release
-// semantics it waited for the scale loads in flight too (2500 instead of  cycles a K
-// block).  Every wait is bounded.
+// the even CTA MMA issue, warps 2 and 3 scales (chunks of eight K blocks, two ahead), warps
+// 4-11 promotion and epilogue: lane quarter warp & 3, 64 columns of either half of the
+// tile.  These hold 128 accumulators a thread, so registers move to them (setmaxnreg: 256
+// x 232 + 128 x 40 = 384 x 168).  Every wait is bounded.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -74,8 +81,8 @@ struct Lay {
 // What pair c computes i-th: K blocks [k0, k1) of tile t.  A share of a tile's K blocks
 // that does not reach its end comes first (`publish`: its sums go to memory), the one
 // that does comes last and adds those of pairs [from, c) in their order: by then they are
-// there, and a pair waits only for pairs before it, which wait for nothing before they
-// publish.
+// there, and a pair waits only for pairs before it, which run (they are numbered as they
+// begin) and wait for nothing before they publish.
 struct Item {
     int32_t t, k0, k1, from;
     bool publish;
@@ -257,7 +264,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::grid_dep_wait();  // global memory only after the previous kernel
     ptx::grid_dep_launch();
     __syncthreads();
-    const int32_t pair = (int32_t)ptx::cluster_id_x();
+    int32_t pair = (int32_t)ptx::cluster_id_x();
+    if constexpr (SHARE) {
+        // pairs count in the order in which they begin: one waits only for pairs that run
+        int32_t *ticket = reinterpret_cast<int32_t *>(smem + L::OFF_MISC + 8);
+        if (leader && threadIdx.x == 0) *ticket = atomicAdd(p.there + p.pairs * 16, 1);
+        ptx::cluster_sync();
+        pair = ptx::ld_cluster_s32(ptx::map_shared(ptx::smem_addr(ticket), 0));
+    }
     const bool run = !*abort_flag;
 
     // (each in its own branch: the compiler allots a branch's registers by it)

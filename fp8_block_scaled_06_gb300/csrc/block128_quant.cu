@@ -21,7 +21,9 @@
 // columns, so that a row of a warp is a whole line of the codes.  A warp's 16 row
 // scales are divided out side by side in 16 lanes (a division a row by every lane was a
 // third of the instructions).  Along rows alone a lane takes 16 values of a row and
-// eight lanes a block, with no second pass.
+// eight lanes a block, with no second pass.  Measured: 4099 x 14336 bf16 both ways 39 us,
+// 6.1 TB/s (in one pass from registers, two CTAs an SM, 104 us); 8192 x 4096 codes turned
+// 15 us, 4.6 TB/s, three quarters of the issue slots.
 #include "block128.h"
 #include "block128_math.cuh"
 #include "ptx.cuh"
@@ -222,9 +224,9 @@ __global__ void __launch_bounds__(kTileThreads, 4) b128_quant_tile_kernel(const 
 
 // One CTA an SM takes tile after tile, the next one's copies running beside this one's
 // arithmetic.  dg, du and h of a tile stay in registers (8 rows of four columns a
-// thread, 96 values) between the maxima and the codes: computed for both (and four
-// such CTAs an SM, none with a tile ahead) the arithmetic bound it, 162 us at
-// 4099 x 14336 for  now.
+// thread, 96 values) between the maxima and the codes, and its arithmetic is packed where
+// it can be: the instructions bound it (two thirds of the issue slots at 4099 x 14336, 129 us,
+// 4.2 TB/s; with everything computed twice, for the maxima and for the codes, 162 us).
 constexpr int kBackThreads = 512;
 constexpr int kBackRows = kBlk / (kBackThreads / 32);
 

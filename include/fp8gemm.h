@@ -625,6 +625,7 @@ FP8G_API fp8g_status fp8_gemm_lora(const void *x, int32_t x_dtype, const void *W
  * short), at least 2^-126, 1 for a block of zeros; code = FP8(fl32(x fl32(1 / s))),
  * nearest even, saturating.  NaN has the code 0x7F and does not count for amax; a
  * block with an infinity has an infinite scale, and its products are NaN.
+ * Outputs overlap neither inputs nor each other.
  */
 
 /*
@@ -664,13 +665,16 @@ typedef enum { FP8G_NT = 0, FP8G_NN = 1, FP8G_TN = 2 } fp8g_form;
  * Product of operands with block-128 scales sfa, sfb (laid out as the quantisers
  * above give them for the operands as they are stored):
  *   C = out( sum over K blocks of  sa sb (sum of 128 products) )
- * fp32 sums.  a_fmt, b_fmt: FP8G_E4M3 or FP8G_E5M2.  C bf16 or fp32 per `out`; add
- * = 1 (fp32 only) adds the product to what C holds.  M may be 0 (NT, NN), and K
+ * fp32 sums; sa sb is one fp32 factor (below 2^-126 it loses bits, from
+ * 2^128 on it is infinite).  a_fmt, b_fmt: FP8G_E4M3 or FP8G_E5M2.  C bf16 or fp32 per `out`; add
+ * = 1 (fp32 only) adds the product to what C holds (results below 2^-126 may become
+ * 0, as with global atomics).  M may be 0 (NT, NN), and K
  * with FP8G_TN (C is zeroed, or kept with add).
  * K % 16 == 0 (NT, NN), M % 16 == 0 (TN), N % 16 == 0 (NN, TN), N * sizeof(out
  * element) % 16 == 0, pointers 16-byte aligned, else FP8G_ERR_ALIGNMENT.  Results
- * do not vary between runs.  One kernel, no workspace; fp8g_kernel_timing_begin
- * does not record it.
+ * do not vary between runs.  One kernel; where few tiles of C have long sums, it has a
+ * temporary (256 KB for two SMs, 20 MB at most) and zeroes its flags first.
+ * fp8g_kernel_timing_begin does not record it.
  */
 FP8G_API fp8g_status fp8_gemm_block128(int32_t form, const void *A, const float *sfa, int32_t a_fmt,
                                        const void *B, const float *sfb, int32_t b_fmt, void *C, int out,

@@ -457,3 +457,63 @@ def test_the_product_refuses_what_does_not_fit(fp8g, arg):
         with pytest.raises((AssertionError, fp8g.Fp8gError)):
             fp8g.gemm_block128(**dict(good, **{arg: t}))
     settled(fp8g)
+
+
+def test_shared_tiles_at_once_and_replayed(fp8g):
+    r = torch.Generator(device="cuda").manual_seed(22)
+    rand = lambda *s: torch.randn(s, device="cuda", generator=r)
+    cases = []
+    for M, N in ((272, 400), (1040, 784), (16, 16)):
+        A, B = (fp8g.quantize_block128(rand(12000, n), row=False, col=True)[1] for n in (M, N))
+        cases.append((*A, *B))
+    call = lambda t: fp8g.gemm_block128(*t, form="tn", out="f32")
+    want = [call(t) for t in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for s, t in zip(streams, cases):
+            with torch.cuda.stream(s):
+                got.append(call(t))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graphs, got = [], []
+    for t in cases:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(call(t))
+        graphs.append(g)
+    [c.zero_() for c in got]
+    torch.cuda.synchronize()
+    for _ in range(3):  # two graphs at once, an eager call beside them
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = call(cases[1])
+        torch.cuda.synchronize()
+        assert torch.equal(eager, want[1])
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        [c.zero_() for c in got]
+        torch.cuda.synchronize()
+    settled(fp8g)
+
+
+def test_codes_of_another_type_are_refused(fp8g):
+    x = torch.randn((32, 256), device="cuda")
+    W, sw = fp8g.quantize_tile128(torch.randn((256, 256), device="cuda"))
+    q = {f: fp8g.quantize_block128(x, fmt=f)[0] for f in (E4M3, E5M2)}
+    for f, typed in ((E4M3, torch.float8_e4m3fn), (E5M2, torch.float8_e5m2)):
+        (a, s), other = q[f], 1 - f
+        want = fp8g.gemm_block128(a, s, W, sw, a_fmt=f)
+        assert torch.equal(fp8g.gemm_block128(a.view(typed), s, W, sw, a_fmt=f), want)
+        for bad in (lambda: fp8g.gemm_block128(a.view(typed), s, W, sw, a_fmt=other),
+                    lambda: fp8g.gemm_block128(a.view(torch.int8), s, W, sw, a_fmt=f),
+                    lambda: fp8g.gated_block128(a.view(typed), s, W, sw, x_fmt=other),
+                    lambda: fp8g.requantize_block128(a.view(typed), s, q_fmt=other)):
+            with pytest.raises(AssertionError):
+                bad()
+    h, gu = fp8g.gated_block128(*q[E4M3], W, sw, keep=True)
+    dh = torch.randn((32, 128), device="cuda")
+    with pytest.raises(AssertionError):
+        fp8g.gated_block128_backward(dh, gu[0].view(torch.float8_e5m2), gu[1])
+    settled(fp8g)
