@@ -1,6 +1,8 @@
 // Entry points of the operators with fp32 scales for blocks of 128: argument
 // checks, tensor maps, the choice between the kernel for few rows
 // (block128_few.cu) and the one on CTA pairs (block128_gemm.cu).
+#include <algorithm>
+
 #include "block128.h"
 
 namespace fp8g {
@@ -47,12 +49,16 @@ struct Plan {
 // Pairs take 76 hundredths of a 10^4-cycle unit a K block (every tile 256 x
 // 256, however few of its rows exist), the call eight more at its ends.  Few rows: a
 // tile of 128 weight rows; a round begins and ends with the time of five K blocks
-// (first loads, joining), each further CTA of a tile joins about one more; a K block
-// takes 110 where a CTA has its SM alone, 130 where two share it (loads bound both).
-// Measured, us, few rows / pairs: 64 x 14336 x 4096 15 / 18, 77 of them 21 / 17.5, 77 x
-// 4096 x 14336 19 / 50, 256 of them 30 / 43; gated, 64 rows of F 14336, K 4096 25 / 35,
-// 128 rows 44 / 35.
-Plan plan(int64_t M, int64_t n_blocks, const Deal &d, int num_kb, bool gated, int num_sms) {
+// (first loads, joining), of fifteen if another comes before it, each further CTA of a tile
+// joins about one more; a K block takes 110 where a CTA has its SM alone, 130 where two
+// share it (loads bound both).  A cluster stays in one GPC, so fewer run at once than its
+// SMs would give (1, 2, .. 8 CTAs, an SM each: 152, 76, 46, 36, 28, 23, 15, 15); with two
+// CTAs an SM it has half the SMs, or twice as many run.
+// Measured, us, few rows / pairs: 64 x 14336 x 4096 15 / 18, 77 of them 20 / 17.5, 77 x
+// 4096 x 14336 19 / 29, 256 of them 30 / 43; gated, 64 rows of F 14336, K 4096 24 / 33,
+// 128 rows 44 / 35.  By CTAs of a tile: 77 x 5120 x 5120 2, 3, 4: 14.6, 12.0, 18.6; 64 x 28672
+// x 8192 1, 2, 4: 43, 51, 56.
+Plan plan(int64_t M, int64_t n_blocks, const Deal &d, int num_kb, bool gated, int dev) {
     int64_t least = (d.units + 8) * 76;
     Plan best{false, kBlk, 1};
     const int most = gated ? 64 : 128;
@@ -60,10 +66,14 @@ Plan plan(int64_t M, int64_t n_blocks, const Deal &d, int num_kb, bool gated, in
     while (nt < most && nt < M) nt *= 2;
     const int64_t tiles = n_blocks * ((M + nt - 1) / nt);
     const int per_sm = nt < most ? 2 : 1;
-    for (int s = 1; s <= 8 && s <= num_kb; s *= 2) {
-        const int64_t r = (tiles * s + per_sm * num_sms - 1) / (per_sm * num_sms);
-        const int64_t cost = (r * ((num_kb + s - 1) / s + 5) + s) * (per_sm == 1 ? 110 : 130);
-        if (cost < least && M <= 65535 * 16) {  // (a grid's second axis)
+    if (M > 65535 * 16) return best;  // (a grid's second axis)
+    for (int s = 1; s <= 8 && s <= num_kb; ++s) {
+        int64_t fit = per_sm * b128_few_clusters(s, dev);
+        if (per_sm == 2) fit = std::max<int64_t>(fit, b128_few_clusters((s + 1) / 2, dev));
+        if (fit == 0) continue;
+        const int64_t r = (tiles + fit - 1) / fit;
+        const int64_t cost = (r * ((num_kb + s - 1) / s + 10) - 5 + s) * (per_sm == 1 ? 110 : 130);
+        if (cost < least) {
             least = cost;
             best = Plan{true, nt, s};
         }
@@ -205,7 +215,7 @@ fp8g_status fp8_gemm_block128(int32_t form, const void *A, const float *sfa, int
     const int o = add ? kB128Add : out == FP8G_OUT_F32 ? kB128F32 : kB128Bf16;
     const uint32_t ta = host_mma_type(a_fmt), tb = host_mma_type(b_fmt);
     const Deal dl = deal(npm * npn, p.num_kb, d.num_sms / 2, true);
-    const Plan pl = tn ? Plan{false, kBlk, 1} : plan(M, p.n_blocks, dl, p.num_kb, false, d.num_sms);
+    const Plan pl = tn ? Plan{false, kBlk, 1} : plan(M, p.n_blocks, dl, p.num_kb, false, d.dev);
     CUtensorMap mA, mB;
     st = tn ? map2(A, M, K, kBlk, d.dev, mA) : map2(A, K, M, pl.nt, d.dev, mA);
     if (st == FP8G_OK)
@@ -260,7 +270,7 @@ fp8g_status fp8_gated_block128(const void *x, const float *sfx, int32_t x_fmt, c
     p.timeout_ns = d.timeout_ns;
     const uint32_t tx = host_mma_type(x_fmt), tw = host_mma_type(w_fmt);
     const Deal dl = deal(npm * p.n_blocks, p.num_kb, d.num_sms / 2, false);
-    const Plan pl = plan(M, p.n_blocks, dl, p.num_kb, true, d.num_sms);
+    const Plan pl = plan(M, p.n_blocks, dl, p.num_kb, true, d.dev);
     CUtensorMap mX, mW;
     st = map2(x, K, M, pl.nt, d.dev, mX);
     if (st == FP8G_OK) {

@@ -56,6 +56,8 @@ constexpr int64_t kB128PartBytes = (int64_t)4 * kBlk * kBlk * 4;  // a pair's su
 // nt rows of A its columns; K split over clusters of `split` CTAs.
 cudaError_t launch_b128_few(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p,
                             int out, int nt, int split, cudaStream_t stream);
+// Clusters of `split` CTAs with an SM each that run at once on device `dev`, the current one.
+int b128_few_clusters(int split, int dev);
 
 // block128_quant.cu.  src: FP8G_IN_F32 / FP8G_IN_BF16 values, rows ld apart, or
 // codes of src_fmt with row scales (kB128Codes).  Outputs that are null are left out.

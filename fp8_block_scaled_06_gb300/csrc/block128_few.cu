@@ -21,6 +21,8 @@
 // warps add and store.
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "block128.h"
 #include "block128_math.cuh"
 #include "block128_wait.cuh"
@@ -326,16 +328,16 @@ __global__ void __launch_bounds__(32 * Few<NT, (OUT >= kB128Gated)>::WARPS, Few<
     }
 }
 
-template <int NT, int OUT>
-cudaError_t launch_few(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p, int split,
-                       cudaStream_t stream) {
+// The launch of n_blocks x rows clusters of `split`; to(kernel, configuration) uses it.
+template <int NT, int OUT, typename F>
+cudaError_t few_config(int64_t n_blocks, int64_t rows, int split, cudaStream_t stream, F to) {
     using L = Few<NT, (OUT >= kB128Gated)>;
     auto kern = b128_few_kernel<NT, OUT>;
     static unsigned long long done = 0ull;
     const cudaError_t e = b128_allow_smem(reinterpret_cast<const void *>(kern), L::BYTES, done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.n_blocks, (unsigned)((p.M + NT - 1) / NT), (unsigned)split);
+    cfg.gridDim = dim3((unsigned)n_blocks, (unsigned)rows, (unsigned)split);
     cfg.blockDim = dim3(32 * L::WARPS, 1, 1);
     cfg.dynamicSmemBytes = L::BYTES;
     cfg.stream = stream;
@@ -348,7 +350,15 @@ cudaError_t launch_few(const CUtensorMap &A, const CUtensorMap &B, const B128Par
     attr[1].val.clusterDim.z = (unsigned)split;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, A, B, p);
+    return to(kern, cfg);
+}
+
+template <int NT, int OUT>
+cudaError_t launch_few(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p, int split,
+                       cudaStream_t stream) {
+    return few_config<NT, OUT>(p.n_blocks, (p.M + NT - 1) / NT, split, stream, [&](auto kern, cudaLaunchConfig_t &cfg) {
+        return cudaLaunchKernelEx(&cfg, kern, A, B, p);
+    });
 }
 
 template <int NT>
@@ -368,6 +378,23 @@ cudaError_t few_gated(const CUtensorMap &A, const CUtensorMap &B, const B128Para
 }
 
 }  // namespace
+
+int b128_few_clusters(int split, int dev) {
+    static std::atomic<int> cache[64][9];
+    std::atomic<int> &c = cache[dev & 63][split];
+    int n = c.load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    const cudaError_t e =
+        few_config<128, kB128Bf16>(64, 1, split, nullptr, [&](auto kern, cudaLaunchConfig_t &cfg) {
+            return cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+        });
+    if (e != cudaSuccess || n < 1) {
+        cudaGetLastError();  // clear
+        return 0;
+    }
+    c.store(n, std::memory_order_relaxed);
+    return n;
+}
 
 cudaError_t launch_b128_few(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p, int out,
                             int nt, int split, cudaStream_t stream) {
