@@ -188,21 +188,24 @@ __global__ void __launch_bounds__(kTileThreads, 4) b128_quant_tile_kernel(const 
         if (lane < kRowsPerWarp && first + lane < rows) a.s_row[(int64_t)blockIdx.x * a.R + row0 + first + lane] = s;
     }
     __syncthreads();
-    const uint4 t = reinterpret_cast<const uint4 *>(top)[lane];
-    float s[4] = {__uint_as_float(t.x), __uint_as_float(t.y), __uint_as_float(t.z), __uint_as_float(t.w)};
+    float s[4];  // 1 / scale of the lane's columns
     if constexpr (TILE) {
-        const float one = b128_scale<FMT>(b128_warp_max(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]))));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s[k] = one;
+        const uint4 t = reinterpret_cast<const uint4 *>(top)[lane];
+        const uint32_t most = max(max(t.x, t.y), max(t.z, t.w));
+        const float one = b128_scale<FMT>(b128_warp_max(__uint_as_float(most)));
         if (threadIdx.x == 0) a.s_tile[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = one;
+        s[0] = s[1] = s[2] = s[3] = __frcp_rn(one);
     } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s[k] = b128_scale<FMT>(s[k]);
-        if (warp == 0 && in)
-            *reinterpret_cast<float4 *>(a.s_col + (int64_t)blockIdx.y * a.C + c) = make_float4(s[0], s[1], s[2], s[3]);
+        // (a column's divisions once, not by every warp: a tenth of the instructions)
+        if (threadIdx.x < kBlk) {
+            const float one = b128_scale<FMT>(__uint_as_float(top[threadIdx.x]));
+            if (c0 + threadIdx.x < a.C) a.s_col[(int64_t)blockIdx.y * a.C + c0 + threadIdx.x] = one;
+            top[threadIdx.x] = __float_as_uint(__frcp_rn(one));
+        }
+        __syncthreads();
+        const float4 t = reinterpret_cast<const float4 *>(top)[lane];
+        s[0] = t.x, s[1] = t.y, s[2] = t.z, s[3] = t.w;
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) s[k] = __frcp_rn(s[k]);
     const int64_t at = (row0 + first) * a.C + c;
     uint8_t *q = (TILE ? a.q_tile : a.q_col) + at, *q_row = ROW ? a.q_row + at : nullptr;
     const int live = in ? min(kRowsPerWarp, rows - first) : 0;
@@ -338,24 +341,23 @@ __global__ void __launch_bounds__(kBackThreads, 1) b128_backward_kernel(const B1
         own_g = __frcp_rn(own_g);
         own_u = __frcp_rn(own_u);
         __syncthreads();
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            mg[k] = b128_scale<FMT>(__uint_as_float(top[4 * lane + k]));
-            mu[k] = b128_scale<FMT>(__uint_as_float(top[kBlk + 4 * lane + k]));
-            mh[k] = b128_scale<FP8G_E4M3>(__uint_as_float(top[2 * kBlk + 4 * lane + k]));
+        // (a column's divisions once, not by every warp: an eighth of the instructions)
+        if (threadIdx.x < 3 * kBlk) {
+            const int col = threadIdx.x & (kBlk - 1), which = threadIdx.x / kBlk;
+            const float m = __uint_as_float(top[threadIdx.x]);
+            const float s = which == 2 ? b128_scale<FP8G_E4M3>(m) : b128_scale<FMT>(m);
+            (which == 2 ? a.s_h + (int64_t)(t / fb) * F : a.s_col + (int64_t)(t / fb) * F2 + which * F)[c0 + col] = s;
+            top[threadIdx.x] = __float_as_uint(__frcp_rn(s));
         }
-        if (warp == 0) {
-            float *s = a.s_col + (int64_t)(t / fb) * F2 + c0 + 4 * lane;
-            *reinterpret_cast<float4 *>(s) = make_float4(mg[0], mg[1], mg[2], mg[3]);
-            *reinterpret_cast<float4 *>(s + F) = make_float4(mu[0], mu[1], mu[2], mu[3]);
-            *reinterpret_cast<float4 *>(a.s_h + (int64_t)(t / fb) * F + c0 + 4 * lane) =
-                make_float4(mh[0], mh[1], mh[2], mh[3]);
-        }
+        __syncthreads();
+        auto columns = [&](int which, float(&r)[4]) {
+            const float4 v = reinterpret_cast<const float4 *>(top + which * kBlk)[lane];
+            r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+        };
+        columns(0, mg), columns(1, mu), columns(2, mh);
         // the other buffer's maxima were read before this tile's first barrier: zeros for
         // the next tile
         for (int k = threadIdx.x; k < 3 * kBlk; k += kBackThreads) tops[(i ^ 1) * 3 * kBlk + k] = 0u;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mg[k] = __frcp_rn(mg[k]), mu[k] = __frcp_rn(mu[k]), mh[k] = __frcp_rn(mh[k]);
         const int64_t at = (row0 + first) * F2 + c0 + 4 * lane;
         uint8_t *row = a.row + at, *col = a.col + at, *hq = a.h + (row0 + first) * F + c0 + 4 * lane;
 #pragma unroll
