@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kTileThreads, 4) b128_quant_tile_kernel(const 
     ptx::cp_async_commit();
     ptx::cp_async_wait<0>();
     __syncthreads();
-    auto values = [&](int r, float (&v)[4]) {
+    auto values = [&](int r, float s, float (&v)[4]) {
         if constexpr (SRC == FP8G_IN_F32) {
             const float4 f = reinterpret_cast<const float4 *>(sm)[r * 32 + lane];
             v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
@@ -157,19 +157,21 @@ __global__ void __launch_bounds__(kTileThreads, 4) b128_quant_tile_kernel(const 
             widen4(reinterpret_cast<const uint2 *>(sm)[r * 32 + lane], v);
         } else {
             b128_decode(reinterpret_cast<const uint32_t *>(sm)[r * 32 + lane], a.src_fmt, v);
-            const uint64_t s = b128_pair(src_s[r], src_s[r]);
-            const uint64_t lo = b128_mul2(b128_pair(v[0], v[1]), s), hi = b128_mul2(b128_pair(v[2], v[3]), s);
+            const uint64_t ss = b128_pair(s, s);
+            const uint64_t lo = b128_mul2(b128_pair(v[0], v[1]), ss), hi = b128_mul2(b128_pair(v[2], v[3]), ss);
             v[0] = b128_lo(lo), v[1] = b128_hi(lo), v[2] = b128_lo(hi), v[3] = b128_hi(hi);
         }
     };
     // (rows and columns past the matrix are zeros: they change no maximum)
     const int first = warp * kRowsPerWarp;
+    float4 s4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // four rows' scales
     float cm[4] = {}, own = 0.0f;  // own: lane i has row first + i's
 #pragma unroll
     for (int i = 0; i < kRowsPerWarp; i += 2) {
         float v[4], w[4];
-        values(first + i, v);
-        values(first + i + 1, w);
+        if (SRC == kB128Codes && i % 4 == 0) s4 = *reinterpret_cast<const float4 *>(src_s + first + i);
+        values(first + i, i % 4 == 0 ? s4.x : s4.z, v);
+        values(first + i + 1, i % 4 == 0 ? s4.y : s4.w, w);
         if constexpr (ROW) {
             const float m0 = b128_warp_max(b128_amax4(v[0], v[1], v[2], v[3]));
             const float m1 = b128_warp_max(b128_amax4(w[0], w[1], w[2], w[3]));
@@ -212,7 +214,8 @@ __global__ void __launch_bounds__(kTileThreads, 4) b128_quant_tile_kernel(const 
 #pragma unroll
     for (int i = 0; i < kRowsPerWarp; ++i) {
         float v[4];
-        values(first + i, v);
+        if (SRC == kB128Codes && i % 4 == 0) s4 = *reinterpret_cast<const float4 *>(src_s + first + i);
+        values(first + i, i % 4 == 0 ? s4.x : i % 4 == 1 ? s4.y : i % 4 == 2 ? s4.z : s4.w, v);
         const float r = ROW ? __shfl_sync(0xffffffffu, rr, i) : 0.0f;
         if (i < live) {
             if constexpr (ROW) *reinterpret_cast<uint32_t *>(q_row) = b128_codes<FMT>(v[0], v[1], v[2], v[3], r);
@@ -287,7 +290,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) b128_backward_kernel(const B1
         uint32_t *top = tops + i * 3 * kBlk;
         float dg[kBackRows][4], du[kBackRows][4], h[kBackRows][4];
         float mg[4] = {}, mu[4] = {}, mh[4] = {};
-        float own_g = 0.0f, own_u = 0.0f;  // lane j: row first + j's
+        float own = 0.0f;  // lane j: dg's of row first + j, lane kBackRows + j: du's
 #pragma unroll
         for (int j = 0; j < kBackRows; ++j) {
             const int r = first + j;
@@ -322,8 +325,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) b128_backward_kernel(const B1
             }
             const float a0 = b128_warp_max(b128_amax4(dg[j][0], dg[j][1], dg[j][2], dg[j][3]));
             const float a1 = b128_warp_max(b128_amax4(du[j][0], du[j][1], du[j][2], du[j][3]));
-            own_g = lane == j ? a0 : own_g;
-            own_u = lane == j ? a1 : own_u;
+            own = lane == j ? a0 : lane == kBackRows + j ? a1 : own;
         }
         // (magnitudes that are not NaN: their bits are in order)
 #pragma unroll
@@ -332,14 +334,11 @@ __global__ void __launch_bounds__(kBackThreads, 1) b128_backward_kernel(const B1
             atomicMax(top + kBlk + 4 * lane + k, __float_as_uint(mu[k]));
             atomicMax(top + 2 * kBlk + 4 * lane + k, __float_as_uint(mh[k]));
         }
-        own_g = b128_scale<FMT>(own_g);
-        own_u = b128_scale<FMT>(own_u);
-        if (lane < kBackRows && first + lane < rows) {
-            a.s_row[(int64_t)(t % fb) * a.M + row0 + first + lane] = own_g;
-            a.s_row[((int64_t)fb + t % fb) * a.M + row0 + first + lane] = own_u;
-        }
-        own_g = __frcp_rn(own_g);
-        own_u = __frcp_rn(own_u);
+        own = b128_scale<FMT>(own);
+        const int own_row = first + (lane & (kBackRows - 1));
+        if (lane < 2 * kBackRows && own_row < rows)
+            a.s_row[((int64_t)(lane / kBackRows) * fb + t % fb) * a.M + row0 + own_row] = own;
+        own = __frcp_rn(own);
         __syncthreads();
         // (a column's divisions once, not by every warp: an eighth of the instructions)
         if (threadIdx.x < 3 * kBlk) {
@@ -362,7 +361,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) b128_backward_kernel(const B1
         uint8_t *row = a.row + at, *col = a.col + at, *hq = a.h + (row0 + first) * F + c0 + 4 * lane;
 #pragma unroll
         for (int j = 0; j < kBackRows; ++j) {
-            const float r0 = __shfl_sync(0xffffffffu, own_g, j), r1 = __shfl_sync(0xffffffffu, own_u, j);
+            const float r0 = __shfl_sync(0xffffffffu, own, j), r1 = __shfl_sync(0xffffffffu, own, kBackRows + j);
             if (first + j < rows) {
                 *reinterpret_cast<uint32_t *>(row + j * F2) = b128_codes<FMT>(dg[j][0], dg[j][1], dg[j][2], dg[j][3], r0);
                 *reinterpret_cast<uint32_t *>(row + j * F2 + F) = b128_codes<FMT>(du[j][0], du[j][1], du[j][2], du[j][3], r1);
