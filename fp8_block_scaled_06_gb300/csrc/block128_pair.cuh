@@ -15,7 +15,7 @@
 // a relaxed arrival (with release semantics it waited for copies in flight: 2500 cycles a
 // K block), the MMA warp stays whole and one elected lane issues (one lane's own branch:
 // 1020), and two other warps copy all scales (a ring of each promotion warp's own: 5% of
-// 8192 cubed).  Measured 8192 x 8192 x 8192: 353 us, 3110 TFLOP/s, as the kernel whose
+// 8192 cubed).  Measured 8192 x 8192 x 8192: 350 us, 3140 TFLOP/s, as the kernel whose
 // scales the tensor core applies (gemm_pair.cu, powers of two for blocks of 32).
 //
 // A promotion warp has 32 rows and 128 columns.  Where one scale serves 128 columns (tiles

@@ -23,7 +23,8 @@
 // third of the instructions).  Along rows alone a lane takes 16 values of a row and
 // eight lanes a block, with no second pass.  Measured: 4099 x 14336 bf16 both ways 39 us,
 // 6.1 TB/s (in one pass from registers, two CTAs an SM, 104 us); 8192 x 4096 codes turned
-// 15 us, 4.6 TB/s, three quarters of the issue slots.
+// 13 us, 5.2 TB/s, the ALU pipe two thirds of the time (with decoded values kept in
+// registers from the first pass, so fewer warps, 15.5).
 #include "block128.h"
 #include "block128_math.cuh"
 #include "ptx.cuh"
@@ -231,8 +232,8 @@ __global__ void __launch_bounds__(kTileThreads, 4) b128_quant_tile_kernel(const 
 // One CTA an SM takes tile after tile, the next one's copies running beside this one's
 // arithmetic.  dg, du and h of a tile stay in registers (8 rows of four columns a
 // thread, 96 values) between the maxima and the codes, and its arithmetic is packed where
-// it can be: the instructions bound it (two thirds of the issue slots at 4099 x 14336, 129 us,
-// 4.2 TB/s; with everything computed twice, for the maxima and for the codes, 162 us).
+// it can be: the instructions bound it (two thirds of the issue slots at 4099 x 14336, 107 us,
+// 5.1 TB/s; with everything computed twice, for the maxima and for the codes, 162 us).
 constexpr int kBackThreads = 512;
 constexpr int kBackRows = kBlk / (kBackThreads / 32);
 
