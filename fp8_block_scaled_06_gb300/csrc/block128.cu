@@ -17,26 +17,26 @@ constexpr int64_t kMaxQuantRows = (int64_t)65535 * 16;  // 16 rows at least a bl
 
 // How T tiles of num_kb K blocks go to `most` CTA pairs: rounds of whole tiles and, where
 // the last would leave pairs idle, its K blocks in shares, a tile's to four pairs at
-// most (the one with its end adds the others' sums, 256 KB each).  Shares cost the time
-// of about 50 K blocks (writing and adding sums, zeroing flags, the gap between kernels;
-// 4096 x 4096 x 4096, where they save 20, took 74 us in place of 58): taken where they
-// save 60 (1024 x 1024 x 16384 weight gradient 45 us, in whole tiles 108).
+// most (the one with its end adds the others' sums, 256 KB each), by a kernel of their own:
+// in one kernel, pairs whose shares differ read the rounds' operands at different times,
+// and L2 served fewer (4099 x 4096 x 28672 372 us in place of 330).
+// Shares cost the time of about 50 K blocks (writing and adding sums, zeroing flags, the gap
+// between kernels): taken where they save 60.  Measured, us, with / without: saving 20 (4096 x
+// 4096 x 4096) 69 / 58, 47 (4099 x 4096 x 14336) 178 / 175, 94 (4099 x 4096 x 28672) 330 / 346;
+// weight gradient of 1024 x 1024 x 16384 43 / 75.
 struct Deal {
-    int32_t pairs, full, share;
+    int64_t whole;  // tiles
+    int32_t share;  // K blocks of a pair of the others (0: there are none)
     int64_t units;  // K blocks one after the other
 };
 Deal deal(int64_t T, int num_kb, int most, bool can_share) {
-    Deal d{(int32_t)(T < most ? T : most), 0, 0, (T + most - 1) / most * num_kb};
     const int64_t full = T / most, rest = T - full * most;
+    Deal d{T, 0, (T + most - 1) / most * num_kb};
     if (rest == 0 || !can_share) return d;
     int64_t share = (rest * num_kb + most - 1) / most;
     if (share < (num_kb + 3) / 4) share = (num_kb + 3) / 4;
     if (num_kb - share < 60) return d;
-    d.full = (int32_t)full;
-    d.share = (int32_t)share;
-    d.pairs = (int32_t)(full > 0 ? most : (rest * num_kb + share - 1) / share);
-    d.units = full * num_kb + share + 50;
-    return d;
+    return Deal{full * most, (int32_t)share, full * num_kb + share + 50};
 }
 
 // Which kernel, and its shape.
@@ -81,23 +81,30 @@ Plan plan(int64_t M, int64_t n_blocks, const Deal &d, int num_kb, bool gated, in
     return best;
 }
 
-// The kernel on CTA pairs, with a temporary for sums where tiles are shared.
+// The kernels on CTA pairs: whole tiles, then the others in shares with a temporary for sums
+// (its flags are zeroed before both, so that nothing is between them).
 fp8g_status run_pairs(const CUtensorMap &A, const CUtensorMap &B, B128Params &p, const Deal &dl, int out, bool vec_b,
-                      int dev, cudaStream_t stream) {
-    p.pairs = dl.pairs;
-    p.full = dl.full;
-    p.share = dl.share;
+                      const HostDevice &d, cudaStream_t stream) {
+    const int32_t T = p.T, most = d.num_sms / 2;
+    p.T = (int32_t)dl.whole;
+    p.pairs = std::min(p.T, most);
     if (dl.share == 0) return launch_b128_pair(A, B, p, out, vec_b, stream) == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+    B128Params q = p;
+    q.first = p.T;
+    q.T = T;
+    q.share = dl.share;
+    q.pairs = ((q.T - q.first) * q.num_kb + q.share - 1) / q.share;
     cudaMemPool_t pool;
-    const fp8g_status st = host_pool(dev, pool);
+    const fp8g_status st = host_pool(d.dev, pool);
     if (st != FP8G_OK) return st;
     void *ws = nullptr;
-    const size_t sums = (size_t)dl.pairs * kB128PartBytes, flags = ((size_t)dl.pairs * 16 + 1) * 4;
+    const size_t sums = (size_t)q.pairs * kB128PartBytes, flags = ((size_t)q.pairs * 16 + 1) * 4;
     if (cudaMallocFromPoolAsync(&ws, sums + flags, pool, stream) != cudaSuccess) return FP8G_ERR_CUDA;
-    p.part = static_cast<float *>(ws);
-    p.there = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + sums);
-    cudaError_t e = cudaMemsetAsync(p.there, 0, flags, stream);
-    if (e == cudaSuccess) e = launch_b128_share(A, B, p, out, vec_b, stream);
+    q.part = static_cast<float *>(ws);
+    q.there = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + sums);
+    cudaError_t e = cudaMemsetAsync(q.there, 0, flags, stream);
+    if (e == cudaSuccess && p.T > 0) e = launch_b128_pair(A, B, p, out, vec_b, stream);
+    if (e == cudaSuccess) e = launch_b128_share(A, B, q, out, vec_b, stream);
     const cudaError_t ef = cudaFreeAsync(ws, stream);
     return e == cudaSuccess && ef == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
 }
@@ -229,7 +236,7 @@ fp8g_status fp8_gemm_block128(int32_t form, const void *A, const float *sfa, int
         p.npm = (int32_t)npm;
         p.npn = (int32_t)npn;
         p.T = (int32_t)(npm * npn);
-        return run_pairs(mA, mB, p, dl, o, tn, d.dev, stream);
+        return run_pairs(mA, mB, p, dl, o, tn, d, stream);
     }
 }
 
@@ -288,7 +295,7 @@ fp8g_status fp8_gated_block128(const void *x, const float *sfx, int32_t x_fmt, c
         p.npm = (int32_t)npm;
         p.npn = p.n_blocks;
         p.T = p.npm * p.npn;
-        return run_pairs(mX, mW, p, dl, kB128Gated + gate, false, d.dev, stream);
+        return run_pairs(mX, mW, p, dl, kB128Gated + gate, false, d, stream);
     }
 }
 

@@ -17,11 +17,10 @@ struct B128Params {
     int64_t M, N, K;
     int32_t num_kb;         // ceil(K / 128)
     int32_t npm, npn;       // tiles of C
-    int32_t T;              // npm npn
-    // CTA pairs: pair c takes tiles c, c + pairs, .. of the first `full` rounds; the K blocks
-    // of the tiles behind them are dealt out in shares of `share` (0: whole tiles, as a
-    // last round)
-    int32_t pairs, full, share;
+    int32_t first, T;       // tiles [first, T) of the npm npn
+    // CTA pairs: pair c takes tiles first + c, first + c + pairs, ..; or with `share` > 0 the
+    // tiles' K blocks c share .. one after the other
+    int32_t pairs, share;
     float *part;            // [pairs][256 x 256] sums of a share that ends inside its tile
     int32_t *there;         // zeros at the start. [pairs][16] by warp: part is written; then
                             // the pairs that have begun

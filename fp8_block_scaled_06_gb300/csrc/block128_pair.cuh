@@ -95,19 +95,16 @@ __device__ __forceinline__ bool item(const B128Params &p, int32_t c, int32_t i, 
     o.k0 = 0;
     o.k1 = p.num_kb;
     if constexpr (!SHARE) {
-        o.t = c + i * p.pairs;
+        o.t = p.first + c + i * p.pairs;
         return o.t < p.T;
     }
-    const int32_t base = p.full * p.pairs, kb = p.num_kb, all = (p.T - base) * kb;
+    const int32_t kb = p.num_kb, all = (p.T - p.first) * kb;
     const int32_t u0 = min(c * p.share, all), u1 = min(u0 + p.share, all);
-    int32_t r1 = 0, end = kb;
-    if (u0 < u1) {
-        r1 = (u1 - 1) / kb;
-        end = u1 - r1 * kb;
-    }
+    if (u0 >= u1) return false;
+    const int32_t r1 = (u1 - 1) / kb, end = u1 - r1 * kb;
     if (end < kb) {
         if (i == 0) {
-            o.t = base + r1;
+            o.t = p.first + r1;
             o.k0 = max(u0 - r1 * kb, 0);
             o.k1 = end;
             o.publish = true;
@@ -115,13 +112,9 @@ __device__ __forceinline__ bool item(const B128Params &p, int32_t c, int32_t i, 
         }
         --i;
     }
-    if (i < p.full) {
-        o.t = c + i * p.pairs;
-        return true;
-    }
     const int32_t r0 = u0 / kb;
-    if (i > p.full || u0 >= u1 || u1 < (r0 + 1) * kb) return false;
-    o.t = base + r0;
+    if (i > 0 || u1 < (r0 + 1) * kb) return false;
+    o.t = p.first + r0;
     o.k0 = u0 - r0 * kb;
     if (o.k0 > 0) o.from = r0 * kb / p.share;
     return true;

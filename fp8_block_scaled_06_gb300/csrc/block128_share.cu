@@ -1,5 +1,5 @@
 // The product on CTA pairs where pairs share the K blocks of tiles (block128_pair.cuh).
-// Kernels of their own: the bookkeeping in registers cost the whole-tile loop 5%.
+// Variants of their own: the bookkeeping in registers cost the whole-tile loop 5%.
 #include "block128_pair.cuh"
 
 namespace fp8g {

@@ -672,8 +672,8 @@ typedef enum { FP8G_NT = 0, FP8G_NN = 1, FP8G_TN = 2 } fp8g_form;
  * with FP8G_TN (C is zeroed, or kept with add).
  * K % 16 == 0 (NT, NN), M % 16 == 0 (TN), N % 16 == 0 (NN, TN), N * sizeof(out
  * element) % 16 == 0, pointers 16-byte aligned, else FP8G_ERR_ALIGNMENT.  Results
- * do not vary between runs.  One kernel; where few tiles of C have long sums, it has a
- * temporary (256 KB for two SMs, 20 MB at most) and zeroes its flags first.
+ * do not vary between runs.  One kernel; where tiles of C with long sums leave SMs idle,
+ * they go to a second one with a temporary (20 MB at most), whose flags are zeroed first.
  * fp8g_kernel_timing_begin does not record it.
  */
 FP8G_API fp8g_status fp8_gemm_block128(int32_t form, const void *A, const float *sfa, int32_t a_fmt,
