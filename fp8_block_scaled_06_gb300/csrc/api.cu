@@ -723,6 +723,15 @@ fp8g_status host_bf16_map(const void *ptr, int rank, const uint64_t *dims, const
                        CU_TENSOR_MAP_SWIZZLE_128B, dev, out);
 }
 
+fp8g_status host_store_map(const void *ptr, int esz, int64_t rows, int64_t cols, int dev, CUtensorMap &out) {
+    const CUtensorMapDataType t = esz == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                  : esz == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                             : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};
+    const uint32_t box[2] = {(uint32_t)(64 / esz), 32};
+    return tmap_encode(ptr, t, 8 * esz, 2, dims, box, CU_TENSOR_MAP_SWIZZLE_64B, dev, out);
+}
+
 uint32_t host_mma_type(int fmt) { return mma_type(fmt); }
 
 int32_t host_gap8(int fmt) { return gap8(fmt); }

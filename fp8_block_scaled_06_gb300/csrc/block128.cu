@@ -83,12 +83,12 @@ Plan plan(int64_t M, int64_t n_blocks, const Deal &d, int num_kb, bool gated, in
 
 // The kernels on CTA pairs: whole tiles, then the others in shares with a temporary for sums
 // (its flags are zeroed before both, so that nothing is between them).
-fp8g_status run_pairs(const CUtensorMap &A, const CUtensorMap &B, B128Params &p, const Deal &dl, int out, bool vec_b,
-                      const HostDevice &d, cudaStream_t stream) {
+fp8g_status run_pairs(const B128Maps &m, B128Params &p, const Deal &dl, int out, bool vec_b, const HostDevice &d,
+                      cudaStream_t stream) {
     const int32_t T = p.T, most = d.num_sms / 2;
     p.T = (int32_t)dl.whole;
     p.pairs = std::min(p.T, most);
-    if (dl.share == 0) return launch_b128_pair(A, B, p, out, vec_b, stream) == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+    if (dl.share == 0) return launch_b128_pair(m, p, out, vec_b, stream) == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
     B128Params q = p;
     q.first = p.T;
     q.T = T;
@@ -103,8 +103,8 @@ fp8g_status run_pairs(const CUtensorMap &A, const CUtensorMap &B, B128Params &p,
     q.part = static_cast<float *>(ws);
     q.there = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + sums);
     cudaError_t e = cudaMemsetAsync(q.there, 0, flags, stream);
-    if (e == cudaSuccess && p.T > 0) e = launch_b128_pair(A, B, p, out, vec_b, stream);
-    if (e == cudaSuccess) e = launch_b128_share(A, B, q, out, vec_b, stream);
+    if (e == cudaSuccess && p.T > 0) e = launch_b128_pair(m, p, out, vec_b, stream);
+    if (e == cudaSuccess) e = launch_b128_share(m, q, out, vec_b, stream);
     const cudaError_t ef = cudaFreeAsync(ws, stream);
     return e == cudaSuccess && ef == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
 }
@@ -216,27 +216,27 @@ fp8g_status fp8_gemm_block128(int32_t form, const void *A, const float *sfa, int
     p.a_mn = tn;
     p.b_mn = form != FP8G_NT;
     p.C = C;
-    p.st32 = is_aligned(C, 32) && N * esz % 32 == 0;
     p.status = d.status;
     p.timeout_ns = d.timeout_ns;
     const int o = add ? kB128Add : out == FP8G_OUT_F32 ? kB128F32 : kB128Bf16;
     const uint32_t ta = host_mma_type(a_fmt), tb = host_mma_type(b_fmt);
     const Deal dl = deal(npm * npn, p.num_kb, d.num_sms / 2, true);
     const Plan pl = tn ? Plan{false, kBlk, 1} : plan(M, p.n_blocks, dl, p.num_kb, false, d.dev);
-    CUtensorMap mA, mB;
-    st = tn ? map2(A, M, K, kBlk, d.dev, mA) : map2(A, K, M, pl.nt, d.dev, mA);
+    B128Maps m{};
+    st = tn ? map2(A, M, K, kBlk, d.dev, m.A) : map2(A, K, M, pl.nt, d.dev, m.A);
     if (st == FP8G_OK)
-        st = p.b_mn ? map2(B, N, K, kBlk, d.dev, mB) : map2(B, K, N, kBlk, d.dev, mB);
+        st = p.b_mn ? map2(B, N, K, kBlk, d.dev, m.B) : map2(B, K, N, kBlk, d.dev, m.B);
+    if (st == FP8G_OK && !pl.few) st = host_store_map(C, (int)esz, M, N, d.dev, m.C);
     if (st != FP8G_OK) return st;
     if (pl.few) {
         p.types = (tb << 7) | (ta << 10) | ((uint32_t)p.b_mn << 15);
-        return launch_b128_few(mA, mB, p, o, pl.nt, pl.split, stream) == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+        return launch_b128_few(m.A, m.B, p, o, pl.nt, pl.split, stream) == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
     } else {
         p.types = (ta << 7) | (tb << 10) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16);
         p.npm = (int32_t)npm;
         p.npn = (int32_t)npn;
         p.T = (int32_t)(npm * npn);
-        return run_pairs(mA, mB, p, dl, o, tn, d, stream);
+        return run_pairs(m, p, dl, o, tn, d, stream);
     }
 }
 
@@ -268,7 +268,6 @@ fp8g_status fp8_gated_block128(const void *x, const float *sfx, int32_t x_fmt, c
     p.n_blocks = (int32_t)(F / kBlk);
     p.sb_n = p.num_kb;
     p.sb_k = 1;
-    p.st32 = is_aligned(h, 32) && is_aligned(gu, 32);
     p.h = h;
     p.sh = sh;
     p.gu = gu;
@@ -278,24 +277,26 @@ fp8g_status fp8_gated_block128(const void *x, const float *sfx, int32_t x_fmt, c
     const uint32_t tx = host_mma_type(x_fmt), tw = host_mma_type(w_fmt);
     const Deal dl = deal(npm * p.n_blocks, p.num_kb, d.num_sms / 2, false);
     const Plan pl = plan(M, p.n_blocks, dl, p.num_kb, true, d.dev);
-    CUtensorMap mX, mW;
-    st = map2(x, K, M, pl.nt, d.dev, mX);
+    B128Maps m{};
+    st = map2(x, K, M, pl.nt, d.dev, m.A);
     if (st == FP8G_OK) {
         const uint64_t dw[3] = {(uint64_t)K, (uint64_t)F, 2};
         const uint32_t bw[3] = {(uint32_t)kBlk, (uint32_t)kBlk, 1};
-        st = host_operand_map(W13, FP8G_E4M3, 3, dw, bw, d.dev, mW);
+        st = host_operand_map(W13, FP8G_E4M3, 3, dw, bw, d.dev, m.B);
     }
+    if (st == FP8G_OK && !pl.few) st = host_store_map(h, 1, M, F, d.dev, m.C);
+    if (st == FP8G_OK && !pl.few && gu != nullptr) st = host_store_map(gu, 1, M, 2 * F, d.dev, m.gu);
     if (st != FP8G_OK) return st;
     if (pl.few) {
         p.types = (tw << 7) | (tx << 10);
-        return launch_b128_few(mX, mW, p, kB128Gated + gate, pl.nt, pl.split, stream) == cudaSuccess ? FP8G_OK
+        return launch_b128_few(m.A, m.B, p, kB128Gated + gate, pl.nt, pl.split, stream) == cudaSuccess ? FP8G_OK
                                                                                                     : FP8G_ERR_CUDA;
     } else {
         p.types = (tx << 7) | (tw << 10);
         p.npm = (int32_t)npm;
         p.npn = p.n_blocks;
         p.T = p.npm * p.npn;
-        return run_pairs(mX, mW, p, dl, kB128Gated + gate, false, d, stream);
+        return run_pairs(m, p, dl, kB128Gated + gate, false, d, stream);
     }
 }
 

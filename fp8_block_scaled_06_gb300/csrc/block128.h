@@ -31,7 +31,6 @@ struct B128Params {
     uint32_t types;         // operand types and majors as instruction descriptor bits
     int32_t a_mn, b_mn;     // operand lies with M (N) contiguous
     void *C;
-    int32_t st32;           // 32-byte stores (C 32-byte aligned, rows multiples of 32 B)
     // gated: columns of C are the F columns of h
     uint8_t *h, *gu;        // codes [M, F], [M, 2F] (gu may be null)
     float *sh, *sgu;        // [F / 128][M], [2 F / 128][M]
@@ -45,10 +44,11 @@ enum B128Out : int { kB128Bf16 = 0, kB128F32 = 1, kB128Add = 2, kB128Gated = 3 }
 // block128_gemm.cu, block128_share.cu (p.share > 0; no gated outputs): CTA pairs over
 // 256 x 256 tiles (gated: 256 rows, 128 columns of gate and of up).  vec_b: B's scales are
 // vectors.
-cudaError_t launch_b128_pair(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p,
-                             int out, bool vec_b, cudaStream_t stream);
-cudaError_t launch_b128_share(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p,
-                              int out, bool vec_b, cudaStream_t stream);
+struct B128Maps {
+    CUtensorMap A, B, C, gu;  // C (gated: h) and gu are written (host_store_map)
+};
+cudaError_t launch_b128_pair(const B128Maps &m, const B128Params &p, int out, bool vec_b, cudaStream_t stream);
+cudaError_t launch_b128_share(const B128Maps &m, const B128Params &p, int out, bool vec_b, cudaStream_t stream);
 constexpr int64_t kB128PartBytes = (int64_t)4 * kBlk * kBlk * 4;  // a pair's sums
 
 // block128_few.cu: few rows of C.  The weights (B) are the MMA's 128-row operand,

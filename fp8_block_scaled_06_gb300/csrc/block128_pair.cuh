@@ -58,16 +58,19 @@ static_assert(32 * kPromWarps * kRegsProm + 128 * kRegsRest <= kThreads * kRegsL
               "setmaxnreg draws on the block's own registers");
 constexpr int kTile = kBlk * kBlk;     // bytes of an operand tile of one CTA
 constexpr int kBufs = 2;               // product buffers of 256 columns
+constexpr int kUnit = 32 * 64;
 
 template <bool VECB>
 struct Lay {
-    static constexpr int STAGES = 6;
+    static constexpr int STAGES = 5;
     static constexpr int OFF_B = STAGES * kTile;
+    // output on its way: two units of 32 rows of 64 bytes a promotion warp
+    static constexpr int OFF_C = 2 * STAGES * kTile;
     // scales of CH K blocks: A's [CH][128 rows], then B's [CH][256 columns] or [CH][two
     // tiles]; two such chunks
     static constexpr int CH = 8;
     static constexpr int SCALES = CH * (kBlk + (VECB ? 2 * kBlk : 2));
-    static constexpr int OFF_S = 2 * STAGES * kTile;
+    static constexpr int OFF_S = OFF_C + kPromWarps * 2 * kUnit;
     static constexpr int OFF_X = OFF_S + 2 * SCALES * 4;  // row maxima: [2][2][128] float4
     static constexpr int OFF_BAR = OFF_X + (VECB ? 0 : 2 * 2 * kBlk * 16);
     // full, empty [STAGES]; product full, product empty [kBufs]; row maxima [lane
@@ -168,21 +171,67 @@ struct ScaleSource {
     }
 };
 
-// 64 codes of one row from 64 values times r, in 32-byte stores (wide; each a whole
-// sector) or 16-byte ones.
-__device__ __forceinline__ void store_codes64(uint8_t *dst, const float (&v)[64], float r, bool wide) {
-    uint32_t o[16];
+// A promotion warp's output: units of 32 rows of 64 bytes, in the 64-byte swizzle, that TMA
+// writes while the next one is made.  (Stored from registers, a row a lane, 32 lines an
+// instruction: the stores took 3000 cycles a tile and the MMAs waited; 4096 x 14336 x 4096 bf16
+// 166 us.)
+struct Output {
+    uint32_t base;  // two units of shared memory
+    int lane;
+    uint32_t n;     // units of this tile so far
+    // (made for each tile: nothing of it is kept in registers over the K blocks)
+    __device__ __forceinline__ Output(uint32_t base_, int lane_) : base(base_), lane(lane_), n(0u) {
+        if (lane == 0) ptx::bulk_wait_read<0>();
+        __syncwarp();
+    }
+    __device__ __forceinline__ uint32_t begin() {
+        if (n >= 2u) {
+            if (lane == 0) ptx::bulk_wait_read<1>();
+            __syncwarp();
+        }
+        return base + (n++ & 1u) * kUnit;
+    }
+    // where 16-byte piece `piece` of row r lies in the unit at `at`
+    static __device__ __forceinline__ uint32_t piece(uint32_t at, int r, int piece) {
+        return at + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4);
+    }
+    // in: some of it lies in the matrix.  (The one lane asks; a branch of the warp around the
+    // unit made the K blocks' loop slower, 8192 cubed 343 -> 363 us.)
+    template <bool ADD>
+    __device__ __forceinline__ void end(const CUtensorMap &map, uint32_t at, int64_t x, int64_t y, bool in) {
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (in) {
+                if constexpr (ADD)
+                    ptx::tma_add_2d(&map, at, (int32_t)x, (int32_t)y);
+                else
+                    ptx::tma_store_2d(&map, at, (int32_t)x, (int32_t)y);
+            }
+            ptx::bulk_commit();
+        }
+    }
+    // one unit of which this lane has row `lane`
+    template <bool ADD>
+    __device__ __forceinline__ void row(const CUtensorMap &map, const uint32_t (&w)[16], int64_t x, int64_t y, bool in) {
+        const uint32_t at = begin();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ptx::st_shared_v4(piece(at, lane, j), w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        end<ADD>(map, at, x, y, in);
+    }
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t v;
+    asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
+    return v;
+}
+
+// 64 codes of one row from 64 values times r.
+__device__ __forceinline__ void codes64(uint32_t (&o)[16], const float (&v)[64], float r) {
 #pragma unroll
     for (int w = 0; w < 16; ++w)
         o[w] = b128_codes<FP8G_E4M3>(v[4 * w], v[4 * w + 1], v[4 * w + 2], v[4 * w + 3], r);
-    if (wide) {
-        ptx::st_global_v8(dst, o);
-        ptx::st_global_v8(dst + 32, o + 8);
-    } else {
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-            reinterpret_cast<uint4 *>(dst)[w] = make_uint4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
-    }
 }
 
 __device__ __forceinline__ float amax64(const float (&v)[64]) {
@@ -194,8 +243,8 @@ __device__ __forceinline__ float amax64(const float (&v)[64]) {
 
 template <bool VECB, int OUT, bool SHARE>
 __global__ void __launch_bounds__(kThreads, 1)
-    b128_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                     const B128Params p) {
+    b128_pair_kernel(const __grid_constant__ B128Maps m, const B128Params p) {
+    const CUtensorMap &tmA = m.A, &tmB = m.B;
     using L = Lay<VECB>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = ptx::smem_addr(smem_raw);
@@ -529,46 +578,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
             }
 
+            // (lane and base read anew: what follows from them is not worked out before the K blocks
+            // and kept; the gated kernel had 3% from it)
+            uint32_t lane_again, base_again;
+            asm volatile("mov.u32 %0, %%laneid;" : "=r"(lane_again));
+            asm volatile("mov.u32 %0, %1;" : "=r"(base_again) : "r"(sbase));
+            Output to(base_again + L::OFF_C + (warp - kProm0) * 2 * kUnit, (int)lane_again);
+            const int64_t y = row - lane;  // the warp's first row (whole units past the matrix are left out)
             if constexpr (VECB) {
-                // eight columns of a row from four lanes: whole sectors of an fp32 C
-                const int64_t row0 = row - lane + (lane >> 2), n0 = (int64_t)tn * 2 * kBlk + half * 64 + 2 * (lane & 3);
+                // pairs of columns of 16 rows' halves: units of 64 bytes a row
+                constexpr int COLS = OUT == kB128Bf16 ? 32 : 16, F = COLS / 8;  // columns, fragments of a unit
+                const int64_t n0 = (int64_t)tn * 2 * kBlk + half * 64;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int u = 0; u < 128 / COLS; ++u) {
+                    const int block = u * COLS / 64, f0 = u * COLS % 64 / 8;
+                    const int64_t x = n0 + block * kBlk + f0 * 8;
+                    const uint32_t at = to.begin();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int64_t m = row0 + (c & 1) * 16 + (i & 1) * 8, n = n0 + (c >> 1) * kBlk + (i >> 1) * 8;
-                        if (m < p.M && n < p.N) {
-                            const float2 v = make_float2(b128_lo(acc2[c][i]), b128_hi(acc2[c][i]));
-                            if constexpr (OUT == kB128Bf16) {
-                                *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.C) + m * p.N + n) =
-                                    __floats2bfloat162_rn(v.x, v.y);
-                            } else {
-                                float2 *at = reinterpret_cast<float2 *>(static_cast<float *>(p.C) + m * p.N + n);
-                                if constexpr (OUT == kB128Add)
-                                    ptx::red_add_v2(at, v);
-                                else
-                                    *at = v;
-                            }
-                        }
+                    for (int i = 0; i < 4 * F; ++i) {
+                        const int c = 2 * block + i / (2 * F), k = 2 * (f0 + i / 2 % F) + (i & 1);
+                        const int r = (c & 1) * 16 + (i & 1) * 8 + (lane >> 2), f = i / 2 % F;
+                        const float lo = b128_lo(acc2[c][k]), hi = b128_hi(acc2[c][k]);
+                        if constexpr (OUT == kB128Bf16)
+                            ptx::st_shared(Output::piece(at, r, f) + (lane & 3) * 4, pack_bf16(lo, hi));
+                        else
+                            ptx::st_shared_v2(Output::piece(at, r, 2 * f + ((lane >> 1) & 1)) + (lane & 1) * 8,
+                                              __float_as_uint(lo), __float_as_uint(hi));
                     }
+                    to.end<OUT == kB128Add>(m.C, at, x, y, y < p.M && x < p.N);
+                }
             } else if constexpr (OUT < kB128Gated) {
                 const int64_t n0 = (int64_t)tn * 2 * kBlk + half * 64;
-                if (row < p.M) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t r[32];
+                for (int c = 0; c < 4; ++c) {
+                    const int64_t x = n0 + (c >> 1) * kBlk + (c & 1) * 32;
+                    uint32_t w[16];
+                    if constexpr (OUT == kB128Bf16) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(acc[c][i]);
-                        const int64_t n = n0 + (c >> 1) * kBlk + (c & 1) * 32;
-                        if constexpr (OUT == kB128Add) {
+                        for (int i = 0; i < 16; ++i) w[i] = pack_bf16(acc[c][2 * i], acc[c][2 * i + 1]);
+                        to.row<false>(m.C, w, x, y, y < p.M && x < p.N);
+                    } else {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (n + 4 * i < p.N)
-                                    ptx::red_add_v4(static_cast<float *>(p.C) + row * p.N + n + 4 * i,
-                                                    make_float4(acc[c][4 * i], acc[c][4 * i + 1], acc[c][4 * i + 2], acc[c][4 * i + 3]));
-                            continue;
+                        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(acc[c][16 * h + i]);
+                            to.row<OUT == kB128Add>(m.C, w, x + 16 * h, y, y < p.M && x + 16 * h < p.N);
                         }
-                        store_row32<OUT != kB128Bf16>(p.C, row, p.N, n, r, 1.0f, p.st32 != 0);
                     }
                 }
             } else {
@@ -590,10 +645,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     h[i] = b128_lo(v), h[i + 1] = b128_hi(v);
                 }
                 top.x = amax64(h);
-                if (keep) {
-                    top.y = amax64(gv);
-                    top.z = amax64(uv);
-                }
+                top.y = amax64(gv);
+                top.z = amax64(uv);
                 // [tile parity][half][row]: a slot is written again two tiles later, after
                 // its reader's next arrival
                 const uint32_t par = lt++ & 1u;
@@ -603,24 +656,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) ptx::mbar_arrive(bar_max(q, half));
                 if (!wait_bar_warp(bar_max(q, half ^ 1), par, abort_flag, p, 3 * 256 + 96 + q)) break;
                 const float4 o = x[(half ^ 1) * kBlk + q * 32 + lane];
-                if (row < p.M) {
-                    const int64_t F = p.N, f = (int64_t)tn * kBlk + half * 64;
-                    const float sh = b128_scale<FP8G_E4M3>(fmaxf(top.x, o.x));
-                    store_codes64(p.h + row * F + f, h, __frcp_rn(sh), p.st32 != 0);
-                    if (half == 0) p.sh[tn * p.M + row] = sh;
-                    if (keep) {
-                        const float sg = b128_scale<FP8G_E4M3>(fmaxf(top.y, o.y));
-                        const float su = b128_scale<FP8G_E4M3>(fmaxf(top.z, o.z));
-                        store_codes64(p.gu + row * 2 * F + f, gv, __frcp_rn(sg), p.st32 != 0);
-                        store_codes64(p.gu + row * 2 * F + F + f, uv, __frcp_rn(su), p.st32 != 0);
-                        if (half == 0) {
-                            p.sgu[tn * p.M + row] = sg;
-                            p.sgu[(p.n_blocks + tn) * p.M + row] = su;
-                        }
+                const int64_t F = p.N, f = (int64_t)tn * kBlk + half * 64;
+                const bool in = row < p.M, any = y < p.M;
+                uint32_t w[16];
+                const float sh = b128_scale<FP8G_E4M3>(fmaxf(top.x, o.x));
+                codes64(w, h, __frcp_rn(sh));
+                to.row<false>(m.C, w, f, y, any);
+                if (half == 0 && in) p.sh[tn * p.M + row] = sh;
+                if (keep) {
+                    const float sg = b128_scale<FP8G_E4M3>(fmaxf(top.y, o.y));
+                    const float su = b128_scale<FP8G_E4M3>(fmaxf(top.z, o.z));
+                    codes64(w, gv, __frcp_rn(sg));
+                    to.row<false>(m.gu, w, f, y, any);
+                    codes64(w, uv, __frcp_rn(su));
+                    to.row<false>(m.gu, w, F + f, y, any);
+                    if (half == 0 && in) {
+                        p.sgu[tn * p.M + row] = sg;
+                        p.sgu[(p.n_blocks + tn) * p.M + row] = su;
                     }
                 }
             }
         }
+        if (lane == 0) ptx::bulk_wait_all();
     }
 
 roles_done:
@@ -648,8 +705,7 @@ roles_done:
 }
 
 template <bool VECB, int OUT, bool SHARE>
-cudaError_t launch_pair(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p, int grid,
-                        cudaStream_t stream) {
+cudaError_t launch_pair(const B128Maps &m, const B128Params &p, int grid, cudaStream_t stream) {
     auto kern = b128_pair_kernel<VECB, OUT, SHARE>;
     static unsigned long long done = 0ull;
     if (done == 0ull) {
@@ -675,15 +731,14 @@ cudaError_t launch_pair(const CUtensorMap &A, const CUtensorMap &B, const B128Pa
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, A, B, p);
+    return cudaLaunchKernelEx(&cfg, kern, m, p);
 }
 
 template <bool VECB, bool SHARE>
-cudaError_t launch_product(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p, int out, int grid,
-                           cudaStream_t stream) {
-    if (out == kB128Bf16) return launch_pair<VECB, kB128Bf16, SHARE>(A, B, p, grid, stream);
-    if (out == kB128F32) return launch_pair<VECB, kB128F32, SHARE>(A, B, p, grid, stream);
-    return launch_pair<VECB, kB128Add, SHARE>(A, B, p, grid, stream);
+cudaError_t launch_product(const B128Maps &m, const B128Params &p, int out, int grid, cudaStream_t stream) {
+    if (out == kB128Bf16) return launch_pair<VECB, kB128Bf16, SHARE>(m, p, grid, stream);
+    if (out == kB128F32) return launch_pair<VECB, kB128F32, SHARE>(m, p, grid, stream);
+    return launch_pair<VECB, kB128Add, SHARE>(m, p, grid, stream);
 }
 
 }  // namespace

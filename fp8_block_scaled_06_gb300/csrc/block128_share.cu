@@ -4,11 +4,10 @@
 
 namespace fp8g {
 
-cudaError_t launch_b128_share(const CUtensorMap &A, const CUtensorMap &B, const B128Params &p,
-                              int out, bool vec_b, cudaStream_t stream) {
+cudaError_t launch_b128_share(const B128Maps &m, const B128Params &p, int out, bool vec_b, cudaStream_t stream) {
     const int grid = 2 * p.pairs;
-    return vec_b ? launch_product<true, true>(A, B, p, out, grid, stream)
-                 : launch_product<false, true>(A, B, p, out, grid, stream);
+    return vec_b ? launch_product<true, true>(m, p, out, grid, stream)
+                 : launch_product<false, true>(m, p, out, grid, stream);
 }
 
 }  // namespace fp8g

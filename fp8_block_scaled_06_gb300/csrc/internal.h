@@ -247,6 +247,9 @@ fp8g_status host_operand_map(const void *ptr, int fmt, int rank, const uint64_t 
 // The same for bf16 elements (64 of them are one swizzle span).
 fp8g_status host_bf16_map(const void *ptr, int rank, const uint64_t *dims, const uint32_t *box,
                           int dev, CUtensorMap &out);
+// Map of a matrix [rows, cols] that is written in boxes of 64 bytes x 32 rows, 64-byte swizzle:
+// elements of 1 (bytes), 2 (bf16) or 4 (fp32) bytes.
+fp8g_status host_store_map(const void *ptr, int esz, int64_t rows, int64_t cols, int dev, CUtensorMap &out);
 uint32_t host_mma_type(int fmt);  // the MMA instruction descriptor's type field
 int32_t host_gap8(int fmt);       // eighths of a tile that a packed load does not deliver
 
