@@ -15,7 +15,7 @@
 // a relaxed arrival (with release semantics it waited for copies in flight: 2500 cycles a
 // K block), the MMA warp stays whole and one elected lane issues (one lane's own branch:
 // 1020), and two other warps copy all scales (a ring of each promotion warp's own: 5% of
-// 8192 cubed).  Measured 8192 x 8192 x 8192: 350 us, 3140 TFLOP/s, as the kernel whose
+// 8192 cubed).  Measured 8192 x 8192 x 8192: 345 us, 3190 TFLOP/s, as the kernel whose
 // scales the tensor core applies (gemm_pair.cu, powers of two for blocks of 32).
 //
 // A promotion warp has 32 rows and 128 columns.  Where one scale serves 128 columns (tiles
@@ -23,7 +23,7 @@
 // (weight gradients) it has two columns of four rows in each fragment of 8 x 16, so that it
 // reads a quarter of the columns' scales (a row a lane, shared memory took 1024 cycles a K
 // block to hand them out), in packed pairs; those loads take three times as long, and
-// loads, arithmetic and scales come one after the other: 1250 cycles a K block, 1680
+// loads, arithmetic and scales come one after the other: 1250 cycles a K block, 1730
 // TFLOP/s at 4096 x 14336 x 4096.
 //
 // Operands lie either way.  Contraction contiguous: 128 B rows of the 128-byte
@@ -173,8 +173,9 @@ struct ScaleSource {
 
 // A promotion warp's output: units of 32 rows of 64 bytes, in the 64-byte swizzle, that TMA
 // writes while the next one is made.  (Stored from registers, a row a lane, 32 lines an
-// instruction: the stores took 3000 cycles a tile and the MMAs waited; 4096 x 14336 x 4096 bf16
-// 166 us.)
+// instruction: 3000 cycles a tile, and the MMAs waited.  Measured 4096 x 14336 x 4096: bf16 166 ->
+// 160 us, fp32 188 -> 178, weight gradient added 285 -> 277; gated, with the checkpoint,
+// 380 -> 367.  Five stages of operands make room for it and cost nothing.)
 struct Output {
     uint32_t base;  // two units of shared memory
     int lane;
