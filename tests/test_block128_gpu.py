@@ -517,3 +517,19 @@ def test_codes_of_another_type_are_refused(fp8g):
     with pytest.raises(AssertionError):
         fp8g.gated_block128_backward(dh, gu[0].view(torch.float8_e5m2), gu[1])
     settled(fp8g)
+
+
+@pytest.mark.parametrize("M", [5, 130, 300])
+def test_gated_rows_behind_stay(fp8g, M):
+    F, K = 256, 272
+    x, _ = fp8g.quantize_block128(torch.randn((M, K), device="cuda"))
+    W = fp8g.quantize_tile128(torch.randn((2 * F, K), device="cuda"))
+    h = torch.full((M + 200, F), 0x55, dtype=torch.uint8, device="cuda")
+    gu = torch.full((M + 200, 2 * F), 0x55, dtype=torch.uint8, device="cuda")
+    sh, sgu = torch.zeros((F // 128, M), device="cuda"), torch.zeros((2 * F // 128, M), device="cuda")
+    fp8g.fp8_gated_block128(x[0], x[1], E4M3, W[0], W[1], E4M3, 0, h, sh, gu, sgu, M, F, K)
+    settled(fp8g)
+    assert (h[M:] == 0x55).all() and (gu[M:] == 0x55).all()
+    want = fp8g.gated_block128(*x, *W, keep=True)
+    assert torch.equal(h[:M], want[0][0]) and torch.equal(sh, want[0][1])
+    assert torch.equal(gu[:M], want[1][0]) and torch.equal(sgu, want[1][1])
