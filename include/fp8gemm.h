@@ -665,8 +665,8 @@ typedef enum { FP8G_NT = 0, FP8G_NN = 1, FP8G_TN = 2 } fp8g_form;
  * Product of operands with block-128 scales sfa, sfb (laid out as the quantisers
  * above give them for the operands as they are stored):
  *   C = out( sum over K blocks of  sa sb (sum of 128 products) )
- * fp32 sums; sa sb is one fp32 factor (below 2^-126 it loses bits, from
- * 2^128 on it is infinite).  a_fmt, b_fmt: FP8G_E4M3 or FP8G_E5M2.  C bf16 or fp32 per `out`; add
+ * fp32 sums; both scales are applied in fp32 (sa sb, or sa times a block's sum, loses bits
+ * below 2^-126 and is infinite from 2^128 on).  a_fmt, b_fmt: FP8G_E4M3 or FP8G_E5M2.  C bf16 or fp32 per `out`; add
  * = 1 (fp32 only) adds the product to what C holds (results below 2^-126 may become
  * 0, as with global atomics).  M may be 0 (NT, NN), and K
  * with FP8G_TN (C is zeroed, or kept with add).
