@@ -23,7 +23,7 @@
 // (weight gradients) it has two columns of four rows in each fragment of 8 x 16, so that it
 // reads a quarter of the columns' scales (a row a lane, shared memory took 1024 cycles a K
 // block to hand them out), in packed pairs; those loads take three times as long, and
-// loads, arithmetic and scales come one after the other: 1250 cycles a K block, 1730
+// loads, arithmetic and scales come one after the other: 1200 cycles a K block, 1860
 // TFLOP/s at 4096 x 14336 x 4096.
 //
 // Operands lie either way.  Contraction contiguous: 128 B rows of the 128-byte
