@@ -50,13 +50,13 @@ struct Plan {
 // 256, however few of its rows exist), the call eight more at its ends.  Few rows: a
 // tile of 128 weight rows; a round begins and ends with the time of five K blocks
 // (first loads, joining), of fifteen if another comes before it, each further CTA of a tile
-// joins about one more; a K block takes 110 where a CTA has its SM alone, 130 where two
+// joins about one more; a K block takes 100 where a CTA has its SM alone, 130 where two
 // share it (loads bound both).  A cluster stays in one GPC, so fewer run at once than its
 // SMs would give (1, 2, .. 8 CTAs, an SM each: 152, 76, 46, 36, 28, 23, 15, 15); with two
 // CTAs an SM it has half the SMs, or twice as many run.
-// Measured, us, few rows / pairs: 64 x 14336 x 4096 15 / 18, 77 of them 20 / 17.5, 77 x
-// 4096 x 14336 19 / 29, 256 of them 30 / 43; gated, 64 rows of F 14336, K 4096 24 / 33,
-// 128 rows 44 / 35.  By CTAs of a tile: 77 x 5120 x 5120 2, 3, 4: 14.6, 12.0, 18.6; 64 x 28672
+// Measured, us, few rows / pairs: 64 x 14336 x 4096 14.5 / 17, 77 of them 20 / 17, 77 x
+// 4096 x 14336 18 / 29, 256 of them 28 / 30; gated, 64 rows of F 14336, K 4096 24 / 33,
+// 128 rows 47 / 34.  By CTAs of a tile: 77 x 5120 x 5120 2, 3, 4: 14.6, 12.0, 18.6; 64 x 28672
 // x 8192 1, 2, 4: 43, 51, 56.
 Plan plan(int64_t M, int64_t n_blocks, const Deal &d, int num_kb, bool gated, int dev) {
     int64_t least = (d.units + 8) * 76;
@@ -72,7 +72,7 @@ Plan plan(int64_t M, int64_t n_blocks, const Deal &d, int num_kb, bool gated, in
         if (per_sm == 2) fit = std::max<int64_t>(fit, b128_few_clusters((s + 1) / 2, dev));
         if (fit == 0) continue;
         const int64_t r = (tiles + fit - 1) / fit;
-        const int64_t cost = (r * ((num_kb + s - 1) / s + 10) - 5 + s) * (per_sm == 1 ? 110 : 130);
+        const int64_t cost = (r * ((num_kb + s - 1) / s + 10) - 5 + s) * (per_sm == 1 ? 100 : 130);
         if (cost < least) {
             least = cost;
             best = Plan{true, nt, s};

@@ -234,19 +234,27 @@ __global__ void __launch_bounds__(32 * Few<NT, (OUT >= kB128Gated)>::WARPS, Few<
             ptx::tc_fence_after();
 #pragma unroll
             for (int g = 0; g < L::G; ++g) {
+                // both halves at once where registers allow; the scales are read meanwhile
+                constexpr bool BOTH = L::PER_SM == 1 || L::WT < 64;
+                uint32_t r[BOTH ? 2 : 1][L::WT / 2];
+                auto load = [&](int h) {
+                    ptx::tmem_ld_16x256b(taddr + buf * L::COLS + g * NT + ((uint32_t)h << 20), r[BOTH ? h : 0]);
+                };
+                load(0);
+                if (BOTH) load(1);
                 uint64_t f[L::WT / 8];
 #pragma unroll
                 for (int j = 0; j < L::WT / 8; ++j)
                     f[j] = b128_mul2(reinterpret_cast<const uint64_t *>(s)[4 * j + (lane & 3)], fb[g]);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    uint32_t r[L::WT / 2];
-                    ptx::tmem_ld_16x256b(taddr + buf * L::COLS + g * NT + ((uint32_t)h << 20), r);
-                    ptx::tmem_ld_wait(r);
+                    if (!BOTH && h == 1) load(1);
+                    auto &v = r[BOTH ? h : 0];
+                    ptx::tmem_ld_wait(v);
 #pragma unroll
                     for (int j = 0; j < L::WT / 8; ++j) {
-                        b128_fma2(acc[g][h][2 * j], b128_pair(r[4 * j], r[4 * j + 1]), f[j]);
-                        b128_fma2(acc[g][h][2 * j + 1], b128_pair(r[4 * j + 2], r[4 * j + 3]), f[j]);
+                        b128_fma2(acc[g][h][2 * j], b128_pair(v[4 * j], v[4 * j + 1]), f[j]);
+                        b128_fma2(acc[g][h][2 * j + 1], b128_pair(v[4 * j + 2], v[4 * j + 3]), f[j]);
                     }
                 }
             }
