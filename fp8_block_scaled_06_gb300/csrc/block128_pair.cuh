@@ -74,8 +74,8 @@ struct Lay {
     static constexpr int OFF_X = OFF_S + 2 * SCALES * 4;  // row maxima: [2][2][128] float4
     static constexpr int OFF_BAR = OFF_X + (VECB ? 0 : 2 * 2 * kBlk * 16);
     // full, empty [STAGES]; product full, product empty [kBufs]; row maxima [lane
-    // quarter][half]; scales full, empty [2]; drain
-    static constexpr int NUM_BARS = 2 * STAGES + 2 * kBufs + 8 + 4 + 1;
+    // quarter]; scales full, empty [2]; drain
+    static constexpr int NUM_BARS = 2 * STAGES + 2 * kBufs + 4 + 4 + 1;
     static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
     static constexpr int BYTES = OFF_MISC + 16 + 1024;
     static_assert(BYTES <= 232448, "shared memory over the per-CTA limit");
@@ -261,9 +261,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto bar_empty = [&](int s) { return ptx::smem_addr(&bars[L::STAGES + s]); };
     auto bar_pfull = [&](int b) { return ptx::smem_addr(&bars[2 * L::STAGES + b]); };
     auto bar_pempty = [&](int b) { return ptx::smem_addr(&bars[2 * L::STAGES + kBufs + b]); };
-    auto bar_max = [&](int q, int h) { return ptx::smem_addr(&bars[2 * L::STAGES + 2 * kBufs + 2 * q + h]); };
-    auto bar_sfull = [&](int i) { return ptx::smem_addr(&bars[2 * L::STAGES + 2 * kBufs + 8 + i]); };
-    auto bar_sempty = [&](int i) { return ptx::smem_addr(&bars[2 * L::STAGES + 2 * kBufs + 10 + i]); };
+    auto bar_max = [&](int q) { return ptx::smem_addr(&bars[2 * L::STAGES + 2 * kBufs + q]); };
+    auto bar_sfull = [&](int i) { return ptx::smem_addr(&bars[2 * L::STAGES + 2 * kBufs + 4 + i]); };
+    auto bar_sempty = [&](int i) { return ptx::smem_addr(&bars[2 * L::STAGES + 2 * kBufs + 6 + i]); };
     const uint32_t bar_drain = ptx::smem_addr(&bars[L::NUM_BARS - 1]);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(bar_pfull(b), 1);
             ptx::mbar_init(bar_pempty(b), 2 * kPromWarps);
         }
-        for (int i = 0; i < 8; ++i) ptx::mbar_init(bar_max(i >> 1, i & 1), 1);
+        for (int i = 0; i < 4; ++i) ptx::mbar_init(bar_max(i), 2);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar_sfull(i), 64);
             ptx::mbar_init(bar_sempty(i), kPromWarps);
@@ -651,14 +651,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 top.x = amax64(h);
                 top.y = amax64(gv);
                 top.z = amax64(uv);
+                // One barrier that both warps arrive on: its next phase ends with the slower warp's
+                // next arrival, so neither gets a phase ahead of the other's wait. (With a barrier
+                // of each warp's own, one that had at most two K blocks a tile, which both product
+                // buffers hold, could pass two phases, and the other's parity never came.)
                 // [tile parity][half][row]: a slot is written again two tiles later, after
                 // its reader's next arrival
                 const uint32_t par = lt++ & 1u;
                 float4 *x = reinterpret_cast<float4 *>(smem + L::OFF_X) + par * 2 * kBlk;
                 x[half * kBlk + q * 32 + lane] = top;
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar_max(q, half));
-                if (!wait_bar_warp(bar_max(q, half ^ 1), par, abort_flag, p, 3 * 256 + 96 + q)) break;
+                if (lane == 0) ptx::mbar_arrive(bar_max(q));
+                if (!wait_bar_warp(bar_max(q), par, abort_flag, p, 3 * 256 + 96 + q)) break;
                 const float4 o = x[(half ^ 1) * kBlk + q * 32 + lane];
                 const int64_t F = p.N, f = (int64_t)tn * kBlk + half * 64;
                 const bool in = row < p.M, any = y < p.M;
