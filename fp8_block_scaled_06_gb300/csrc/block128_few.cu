@@ -329,8 +329,9 @@ __global__ void __launch_bounds__(32 * Few<NT, (OUT >= kB128Gated)>::WARPS, Few<
         } else {
             const float4 g = total(i), u = total(NT + i);
             constexpr int GATE = GATED ? OUT - kB128Gated : 0;
-            const float4 h = make_float4(__fmul_rn(b128_gate<GATE>(g.x), u.x), __fmul_rn(b128_gate<GATE>(g.y), u.y),
-                                         __fmul_rn(b128_gate<GATE>(g.z), u.z), __fmul_rn(b128_gate<GATE>(g.w), u.w));
+            const uint64_t h0 = b128_mul2(b128_gate2<GATE>(b128_pair(g.x, g.y)), b128_pair(u.x, u.y));
+            const uint64_t h1 = b128_mul2(b128_gate2<GATE>(b128_pair(g.z, g.w)), b128_pair(u.z, u.w));
+            const float4 h = make_float4(b128_lo(h0), b128_hi(h0), b128_lo(h1), b128_hi(h1));
             auto code = [&](const float4 v, uint8_t *q, float *s) {
                 const float sv = b128_scale<FP8G_E4M3>(b128_warp_max(b128_amax4(v.x, v.y, v.z, v.w)));
                 *reinterpret_cast<uint32_t *>(q) = b128_codes<FP8G_E4M3>(v.x, v.y, v.z, v.w, __frcp_rn(sv));

@@ -684,7 +684,10 @@ FP8G_API fp8g_status fp8_gemm_block128(int32_t form, const void *A, const float 
  * Gated projection pair of a feed-forward layer, in one kernel:
  *   g = x . W13[0..F)^T,  u = x . W13[F..2F)^T,  h = act(g) u     (fp32)
  * x [M, K] with scales along rows, W13 [2F, K] in tiles, gate as for
- * fp8_moe_layer.  h [M, F]: E4M3 codes with scales sh along rows, what
+ * fp8_moe_layer, though not its arithmetic: act is within (20 + 4 |g| + 4 g^2) 2^-24 of its own
+ * value (SiLU without g^2, GELU without |g|) in the tails too, since a block is coded relative to its
+ * own largest value; a sigmoid, Phi(g) or e^(-g^2/2) below 2^-126 is 0.
+ * h [M, F]: E4M3 codes with scales sh along rows, what
  * fp8_gemm_block128 takes for the down projection.  gu [M, 2F] and sgu (both or
  * neither): g and u in E4M3 with scales along rows, the checkpoint for
  * fp8g_gated_block128_backward.  F % 128 == 0, else FP8G_ERR_UNSUPPORTED_SHAPE;
