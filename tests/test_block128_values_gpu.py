@@ -130,3 +130,122 @@ def test_gated_in_the_tails(fp8g, M, gate, kind):
     g, u = both[:, :F], both[:, F:]
     y, _, ey, _ = act_errors(g, gate)
     ref.assert_coded(h[0].cpu(), h[1].cpu(), "row", E4M3, y * u, ey * u.abs())
+
+
+# ------------------------------------------------------------- sums that are exact in any order
+
+def small(r, shape, fmt, most=2):
+    """Codes of whole numbers -most .. most."""
+    t = torch.randint(-most, most + 1, shape, device="cuda", generator=r)
+    return t.float().to(ref.DT[fmt]).view(torch.uint8)
+
+
+def halves(r, *shape):
+    """Scales 1/2, 1 or 2."""
+    return torch.exp2(torch.randint(-1, 2, shape, device="cuda", generator=r).float())
+
+
+def exact_product(r, form, M, N, K, a_fmt=E4M3, b_fmt=E4M3):
+    """Operands of whole numbers and powers of two: a sum is a multiple of 1/4 of at most 16 K, exact in
+    fp32 in any order up to K = 2^18.  And the product in 64 bits."""
+    mk, nk, kk = ref.up(M), ref.up(N), ref.up(K)
+    A = small(r, (K, M) if form == "tn" else (M, K), a_fmt), halves(r, kk, M)
+    B = small(r, (N, K) if form == "nt" else (K, N), b_fmt), halves(r, *((kk, N) if form == "tn" else (nk, kk) if form == "nt"
+                                                                       else (kk, nk)))
+    ka, kb = ("col", "col") if form == "tn" else ("row", "tile")
+    return A, B, ref.product(ref.decode(*A, ka, a_fmt), ref.decode(*B, kb, b_fmt), form)[0]
+
+
+SUMS = [
+    # K blocks of tiles shared between CTA pairs: all tiles, the last ones behind whole ones
+    ("tn", 272, 400, 12000), ("nn", 1500, 1040, 16000), ("tn", 16, 16, 12001), ("nt", 4100, 1288, 16384),
+    ("tn", 2304, 2304, 16400), ("nt", 300, 264, 12304), ("nn", 4099, 4096, 12304),
+    # several whole tiles to a pair
+    ("nt", 4099, 5000, 2064), ("nn", 2100, 2592, 2000), ("tn", 4096, 2832, 2051),
+    # few rows: K split over clusters of up to eight CTAs, one and two of them to an SM
+    ("nt", 1, 4096, 14336), ("nt", 1, 128, 16384), ("nn", 16, 144, 16384), ("nt", 33, 520, 12304), ("nt", 64, 5120, 5120),
+    ("nt", 77, 5120, 5120), ("nn", 128, 272, 16000), ("nt", 128, 2048, 4096), ("nt", 250, 256, 16384),
+]
+
+
+@pytest.mark.parametrize("form,M,N,K", SUMS)
+def test_long_sums_exact(fp8g, form, M, N, K):
+    r = torch.Generator(device="cuda").manual_seed(K + M)
+    A, B, want = exact_product(r, form, M, N, K)
+    start = torch.randint(-9, 10, (M, N), device="cuda", generator=r).float()
+    assert torch.equal(fp8g.gemm_block128(*A, *B, form=form, out="f32").double(), want)
+    assert torch.equal(fp8g.gemm_block128(*A, *B, form=form), want.float().bfloat16())
+    assert torch.equal(fp8g.gemm_block128(*A, *B, form=form, add_to=start.clone()).double(), want + start)
+    settled(fp8g)
+
+
+@pytest.mark.parametrize("a_fmt,b_fmt", [(E4M3, E5M2), (E5M2, E4M3), (E5M2, E5M2)])
+@pytest.mark.parametrize("form,M,N,K", [("nt", 5, 264, 12304), ("nt", 128, 1040, 4096), ("nn", 300, 272, 12304), ("tn", 272, 400, 12000),
+                                        ("nt", 2100, 2600, 1040)])
+def test_long_sums_exact_of_each_type(fp8g, form, M, N, K, a_fmt, b_fmt):
+    r = torch.Generator(device="cuda").manual_seed(K + M + 2 * a_fmt + b_fmt)
+    A, B, want = exact_product(r, form, M, N, K, a_fmt, b_fmt)
+    C = fp8g.gemm_block128(*A, *B, form=form, a_fmt=a_fmt, b_fmt=b_fmt, out="f32")
+    settled(fp8g)
+    assert torch.equal(C.double(), want)
+
+
+@pytest.mark.parametrize("x_fmt,w_fmt", [(E4M3, E4M3), (E5M2, E4M3), (E4M3, E5M2), (E5M2, E5M2)])
+@pytest.mark.parametrize("M,F,K", [(1, 1408, 4112), (16, 256, 2064), (64, 384, 12304), (100, 256, 4096), (300, 384, 1040),
+                                   (1500, 2048, 2064)])
+def test_gated_bits(fp8g, M, F, K, x_fmt, w_fmt):
+    # gate and up are exact, relu(g) u one rounding (of 32 bits here as there): codes and scales bit for bit
+    r = torch.Generator(device="cuda").manual_seed(K + M)
+    x, sx = small(r, (M, K), x_fmt), halves(r, ref.up(K), M)
+    W, sw = small(r, (2 * F, K), w_fmt), halves(r, ref.up(2 * F), ref.up(K))
+    h, gu = fp8g.gated_block128(x, sx, W, sw, gate=fp8g.FP8G_GATE_RELU, keep=True, x_fmt=x_fmt, w_fmt=w_fmt)
+    only, none = fp8g.gated_block128(x, sx, W, sw, gate=fp8g.FP8G_GATE_RELU, x_fmt=x_fmt, w_fmt=w_fmt)
+    settled(fp8g)
+    both = ref.product(ref.decode(x, sx, "row", x_fmt), ref.decode(W, sw, "tile", w_fmt), "nt")[0].float().cpu()
+    for got, v in ((h, both[:, :F].clamp(min=0) * both[:, F:]), (gu, both)):
+        q, s = ref.quant(v, "row", E4M3)
+        # (a zero that came from -0 keeps its sign in one and not in the other)
+        assert torch.equal(got[1].cpu(), s) and torch.equal(got[0].cpu().view(ref.DT[0]).float(), q.view(ref.DT[0]).float())
+    assert none is None and torch.equal(only[0], h[0]) and torch.equal(only[1], h[1])
+
+
+# --------------------------------------- weights that the kernel in front writes
+
+@pytest.mark.parametrize("M", [1, 40, 100, 300])
+def test_weights_written_just_before(fp8g, M):
+    # kernels for few rows fetch weights to L2 while the one in front still runs
+    N, K = 2048, 4096
+    r = torch.Generator(device="cuda").manual_seed(M)
+    x, _ = fp8g.quantize_block128(torch.randn((M, K), device="cuda", generator=r))
+    ws = [torch.randn((N, K), device="cuda", generator=r) for _ in range(3)]
+    want = []
+    for w in ws:
+        t = fp8g.quantize_tile128(w)
+        torch.cuda.synchronize()
+        want.append((fp8g.gemm_block128(*x, *t), fp8g.gated_block128(*x, *t)[0]))
+        torch.cuda.synchronize()
+    q, s = (torch.empty_like(v) for v in fp8g.quantize_tile128(ws[0]))
+
+    def turn():
+        got = []
+        for w in ws:
+            fp8g.fp8g_quantize_tile128(w, fp8g.FP8G_IN_F32, K, N, K, E4M3, q, s)
+            got.append(fp8g.gemm_block128(*x, q, s))
+        for w in ws:
+            fp8g.fp8g_quantize_tile128(w, fp8g.FP8G_IN_F32, K, N, K, E4M3, q, s)
+            got.append(fp8g.gated_block128(*x, q, s)[0])
+        return got
+
+    def check(got):
+        torch.cuda.synchronize()
+        for i, (c, h) in enumerate(want):
+            assert torch.equal(got[i], c) and all(torch.equal(a, b) for a, b in zip(got[3 + i], h))
+    for _ in range(5):
+        check(turn())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = turn()
+    for _ in range(20):
+        g.replay()
+        check(got)
+    settled(fp8g)
