@@ -61,9 +61,14 @@ fp8g_status scale_pool(int dev, cudaMemPool_t &pool) {
         props.allocType = cudaMemAllocationTypePinned;
         props.location.type = cudaMemLocationTypeDevice;
         props.location.id = dev;
-        if (cudaMemPoolCreate(&g_pool[dev], &props) != cudaSuccess) return FP8G_ERR_CUDA;
+        // (Without the relaxed mode a capture under way would be invalidated.)
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return FP8G_ERR_CUDA;
+        const cudaError_t e = cudaMemPoolCreate(&g_pool[dev], &props);
         uint64_t thr = ~0ull;
-        cudaMemPoolSetAttribute(g_pool[dev], cudaMemPoolAttrReleaseThreshold, &thr);
+        if (e == cudaSuccess) cudaMemPoolSetAttribute(g_pool[dev], cudaMemPoolAttrReleaseThreshold, &thr);
+        cudaThreadExchangeStreamCaptureMode(&mode);
+        if (e != cudaSuccess) return FP8G_ERR_CUDA;
         g_pool_ok[dev] = true;
     }
     pool = g_pool[dev];
