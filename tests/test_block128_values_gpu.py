@@ -1,6 +1,9 @@
 """Values of the operators with scales for blocks of 128 where a loose bound would hide a fault:
 short sums on many tiles, blocks in an activation's tail, long sums that are exact, each code
 type."""
+import importlib.util
+import os
+
 import pytest
 import torch
 
@@ -8,6 +11,7 @@ import block128_ref as ref
 
 pytestmark = pytest.mark.gpu
 E4M3, E5M2 = 0, 1
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def settled(fp8g):
@@ -249,3 +253,40 @@ def test_weights_written_just_before(fp8g, M):
         g.replay()
         check(got)
     settled(fp8g)
+
+
+# ------------------------------------------------- the training step, its roundings in quadrature
+
+@pytest.mark.parametrize("tokens", [1, 33, 1100])
+@pytest.mark.parametrize("gate", [0, 1, 2])
+def test_training_step_in_quadrature(fp8g, tokens, gate):
+    spec = importlib.util.spec_from_file_location("ffn_step", os.path.join(ROOT, "examples", "ffn_step.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    layer = example.Layer(384, 256, gate, seed=tokens)
+    r = torch.Generator(device="cuda").manual_seed(tokens)
+    x, dy = (torch.randn((tokens, 384), device="cuda", generator=r).bfloat16() for _ in range(2))
+    y, dx = layer.forward(x), layer.backward(dy)
+    settled(fp8g)
+    v = [t.detach().double().requires_grad_() for t in (x, layer.w13, layer.w2)]
+    gu = v[0] @ v[1].t()
+    h = ref.act(gu[:, :256], gate)[0] * gu[:, 256:]
+    out = h @ v[2].t()
+    wants = [out.detach()] + list(torch.autograd.grad(out, v, dy.double()))
+    # roundings on the way, each independent of the others and of root mean square at most half a step
+    # over sqrt 3: x, W13 (both in g and in u), h, W2; dy, W2, x and W13 in g and in u, the checkpoint, dgu,
+    # W13; the same without the last weights and with x; dy, x and W13 in g and in u, the checkpoint, h
+    for name, got, want, n in (("y", y, wants[0], 6), ("dx", dx, wants[1], 10), ("dw13", layer.dw13, wants[2], 10),
+                               ("dw2", layer.dw2, wants[3], 8)):
+        square = n / 3 * ref.HALF[E4M3] ** 2
+        if gate == 2 and name in ("dx", "dw13"):
+            # ReLU's derivative steps: a gate of unit variance, off by 0.051 (two roundings), changes sign in
+            # 0.051 sqrt(2 / pi) phi(0) = 0.0163 of all places, 0.0325 of those that count, in the half of
+            # the gradient's square that comes through the gate
+            square += 0.0163
+        got, most = got.double(), square ** 0.5
+        assert (got - want).norm() <= most * want.norm(), name
+        # along the wanted gradient: four standard deviations of what 256 independent values leave, and
+        # the second order
+        along = ((got * want).sum() / want.square().sum()).item() - 1
+        assert abs(along) <= most / 4 + most ** 2, (name, along)
