@@ -46,11 +46,11 @@ struct Plan {
 };
 
 // The kernel for few rows against the one on CTA pairs, by estimates of their time.
-// Pairs take 76 hundredths of a 10^4-cycle unit a K block (every tile 256 x
-// 256, however few of its rows exist), the call eight more at its ends.  Few rows: a
-// tile of 128 weight rows; a round begins and ends with the time of five K blocks
-// (first loads, joining), of fifteen if another comes before it, each further CTA of a tile
-// joins about one more; a K block takes 100 where a CTA has its SM alone, 130 where two
+// In units of about 10 cycles: pairs take 76 a K block (every tile 256 x 256, however few of
+// its rows exist; 725 cycles when nothing else holds them up), the call eight K blocks more at
+// its ends.  Few rows: a tile of 128 weight rows; a round begins and ends with the time of five
+// K blocks (first loads, joining), of fifteen if another comes before it, each further CTA of a
+// tile joins about one more; a K block takes 100 where a CTA has its SM alone, 130 where two
 // share it (loads bound both).  A cluster stays in one GPC, so fewer run at once than its
 // SMs would give (1, 2, .. 8 CTAs, an SM each: 152, 76, 46, 36, 28, 23, 15, 15); with two
 // CTAs an SM it has half the SMs, or twice as many run.

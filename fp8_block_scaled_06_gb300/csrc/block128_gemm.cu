@@ -1,4 +1,5 @@
-// The product on CTA pairs in whole tiles (block128_pair.cuh).
+// The product on CTA pairs in whole tiles (block128_pair.cuh).  Where tiles scale B, ptxas spills one
+// register (4 bytes out, 4 in), and the K blocks still take the MMAs' 725 cycles.
 #include "block128_pair.cuh"
 
 namespace fp8g {

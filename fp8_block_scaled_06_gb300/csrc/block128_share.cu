@@ -1,5 +1,6 @@
 // The product on CTA pairs where pairs share the K blocks of tiles (block128_pair.cuh).
-// Variants of their own: the bookkeeping in registers cost the whole-tile loop 5%.
+// Variants of their own: the bookkeeping in registers cost the whole-tile loop 5%.  ptxas spills two to
+// four of these variants' registers (16 bytes out, 84 in at most).
 #include "block128_pair.cuh"
 
 namespace fp8g {

@@ -674,7 +674,7 @@ typedef enum { FP8G_NT = 0, FP8G_NN = 1, FP8G_TN = 2 } fp8g_form;
  * element) % 16 == 0, pointers 16-byte aligned, else FP8G_ERR_ALIGNMENT.  Results
  * do not vary between runs.  One kernel; where tiles of C with long sums leave SMs idle,
  * they go to a second one with a temporary (20 MB at most), whose flags are zeroed first.
- * fp8g_kernel_timing_begin does not record it.
+ * fp8g_kernel_timing_begin records none of the block-128 calls.
  */
 FP8G_API fp8g_status fp8_gemm_block128(int32_t form, const void *A, const float *sfa, int32_t a_fmt,
                                        const void *B, const float *sfb, int32_t b_fmt, void *C, int out,
